@@ -2,7 +2,8 @@
 
 The compute path is a C-ABI shared library of hand-written HIP kernels
 (``libaqlm.so``, declared in ``include/aqlm.h``).  ``binding`` is the thin
-ctypes layer over it; ``synth`` draws seeded synthetic layers.  The library
+ctypes layer over it, ``fused`` that of the products with an epilogue, the gated
+product and their backward passes; ``synth`` draws seeded synthetic layers.  The library
 is loaded on first use and its absence is an error: there is no fallback.
 """
 from .binding import (  # noqa: F401
@@ -31,4 +32,17 @@ from .binding import (  # noqa: F401
     lists_workspace_bytes,
     load_library,
     status_str,
+)
+from .fused import (  # noqa: F401
+    ACTIVATIONS,
+    aqlm_gated,
+    aqlm_gated_backward,
+    aqlm_gated_lists,
+    aqlm_linear_act,
+    aqlm_linear_act_backward,
+    aqlm_linear_act_lists,
+    gated_backward_workspace_bytes,
+    gated_workspace_bytes,
+    linear_act_backward_workspace_bytes,
+    linear_act_workspace_bytes,
 )

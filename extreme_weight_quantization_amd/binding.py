@@ -17,6 +17,7 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libaqlm.so")
 
 AQLM_OK, AQLM_ERR_NULL, AQLM_ERR_SHAPE, AQLM_ERR_SCHEME, AQLM_ERR_ALIGN, AQLM_ERR_HIP, AQLM_ERR_SCRATCH = range(7)
+AQLM_ERR_ACT = 7
 EXPORTED = ("aqlm_linear_gemv", "aqlm_linear_gemv_fused", "aqlm_linear_gemm", "aqlm_linear_decode",
             "aqlm_encode_greedy", "aqlm_kmeans_workspace_bytes", "aqlm_kmeans_init",
             "aqlm_lists_table_bytes", "aqlm_lists_workspace_bytes", "aqlm_lists_plan", "aqlm_lists_fill",
@@ -24,6 +25,9 @@ EXPORTED = ("aqlm_linear_gemv", "aqlm_linear_gemv_fused", "aqlm_linear_gemm", "a
             "aqlm_linear_gemm_dequant", "aqlm_gemm_dequant_workspace_bytes", "aqlm_linear_gemv_lists_noalloc",
             "aqlm_packed_codes_bytes", "aqlm_pack_codes", "aqlm_linear_gemv_packed", "aqlm_linear_gemm_packed",
             "aqlm_linear_decode_packed",
+            "aqlm_linear_act", "aqlm_linear_act_workspace_bytes", "aqlm_gated", "aqlm_gated_workspace_bytes",
+            "aqlm_linear_act_backward", "aqlm_linear_act_backward_workspace_bytes", "aqlm_gated_backward",
+            "aqlm_gated_backward_workspace_bytes", "aqlm_linear_act_lists", "aqlm_gated_lists",
             "aqlm_status_str", "aqlm_last_hip_error", "aqlm_version")
 FUSED_MAX_LAYERS = 8   # AQLM_FUSED_MAX_LAYERS
 
@@ -88,6 +92,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.aqlm_packed_codes_bytes.restype = ci
         lib.aqlm_pack_codes.argtypes = [vp, vp, ci, ci, ci, i64, i64, vp]
         lib.aqlm_pack_codes.restype = ci
+        shape = [ci, ci, ci, i64, i64, i64]   # M, B, g, out, in, batch
+        tail = [vp, i64, ci, *shape, vp]      # workspace, its bytes, act, the shape, stream
+        for name in ("aqlm_linear_act", "aqlm_gated", "aqlm_linear_act_backward", "aqlm_gated_backward"):
+            fn = getattr(lib, name + "_workspace_bytes")
+            fn.argtypes, fn.restype = [*shape, ctypes.POINTER(i64)], ci
+        lib.aqlm_linear_act.argtypes = [vp] * 8 + tail
+        lib.aqlm_gated.argtypes = [pp, pp, pp, vp, pp, pp, vp] + tail
+        lib.aqlm_linear_act_backward.argtypes = [vp] * 7 + tail
+        lib.aqlm_gated_backward.argtypes = [pp, pp, pp, vp, pp, vp, pp] + tail
+        lib.aqlm_linear_act_lists.argtypes = [vp, vp, i64] + [vp] * 7 + tail
+        lib.aqlm_gated_lists.argtypes = [pp, pp, ctypes.POINTER(i64), pp, pp, vp, pp, pp, vp] + tail
+        for name in ("aqlm_linear_act", "aqlm_gated", "aqlm_linear_act_backward", "aqlm_gated_backward",
+                     "aqlm_linear_act_lists", "aqlm_gated_lists"):
+            getattr(lib, name).restype = ci
         lib.aqlm_status_str.argtypes = [ci]
         lib.aqlm_status_str.restype = ctypes.c_char_p
         lib.aqlm_last_hip_error.argtypes = []

@@ -1,0 +1,66 @@
+// Host-side launchers of the fused products (epilogue, gated) and their backward passes.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "aqlm_launch.h"
+
+namespace aqlm {
+
+// What follows the product of one or two layers that share x.  One layer:
+// z = W x + bias, y = act(z) + residual.  Two layers (gate, up): zg, zu likewise,
+// y = act(zg) zu.  Absent pointers are NULL.  residual may be y itself.
+struct Epilogue {
+    const void* bias[2];       // fp16 [out]
+    const void* residual;      // fp16 [batch][out]
+    void* z[2];                // fp16 [batch][out]: where the pre-activations are kept
+    void* y;                   // fp16 [batch][out]
+    int act;
+};
+
+// One or two layers (n) of the same scheme, out and in.
+struct ActLayers {
+    const void* codes[2];
+    const void* codebooks[2];
+    const void* scales[2];
+    int n;
+};
+
+// How a decoded weight enters the fp16 workspace: the codewords' fp32 sum times the row
+// scale; the sum alone (M = 1: exact, the scale then goes into the epilogue); the sum
+// times the scale's power of two (M = 1: exact but for subnormals).
+enum class WeightScale : int { kFull = 0, kNone = 1, kPow2 = 2 };
+
+// w[l][row][0 .. kp) for l < n: the layers' fp16 weights, inputs past `in` zero (kp % 8 == 0).
+hipError_t launch_decode_rows(const GenericScheme& sc, const ActLayers& L, WeightScale ws, void* const* w,
+                              int64_t out, int64_t in, int64_t kp, hipStream_t stream);
+// wt[k][l * op + row] for k < in, l < n, row < op: the transposed weights, rows past `out`
+// zero (op % 64 == 0).
+hipError_t launch_decode_transposed(const GenericScheme& sc, const ActLayers& L, WeightScale ws, void* wt,
+                                    int64_t out, int64_t in, int64_t op, hipStream_t stream);
+// xp[t][0 .. kp): x [batch][in], inputs past `in` zero.
+hipError_t launch_pad_rows(const void* x, void* xp, int64_t batch, int64_t in, int64_t kp, hipStream_t stream);
+
+// Zeros in n 16-bit elements at p (a kernel: a memset may not be recorded into a graph).
+hipError_t launch_zero16(void* p, int64_t n, hipStream_t stream);
+
+// The dense product of gemm_dense.hip on fp16 weights w[l] [out][kp] with an epilogue:
+// z_l = scales[l] (x w_l^T) + bias_l (scales NULL: 1).
+hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void* const* scales, int n,
+                                 const Epilogue& epi, int64_t out, int64_t kp, int64_t batch, hipStream_t stream);
+
+// Gradients of the pre-activations, fp16, as the dense product's x: dz[t][l * op + i] for
+// i < op (rows past `out` zero).  One layer: dy act'(z); two: dy zu act'(zg) and dy act(zg).
+// mant: scales whose mantissas (scale_mantissa) multiply the fp16 result (NULL: none).
+// partial: fp32 [grad_chunks(batch)][n][out], dbias[l] fp16 [out]: sums over the tokens of
+// the unscaled fp32 gradients (both NULL: not wanted).
+int64_t grad_chunks(int64_t batch);
+hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* mant, int n, int act, void* dz,
+                           float* partial, void* const* dbias, int64_t out, int64_t op, int64_t batch,
+                           hipStream_t stream);
+
+// The slice-list product of one layer, or of gate and up, batch 1, with the epilogue in its
+// reduction (gemv_lists.hip).  L as for launch_gemv_lists_fused; its y is not used.
+hipError_t launch_lists_act(ListsLayers L, const void* x, const Epilogue& epi, int64_t in, hipStream_t stream);
+
+}  // namespace aqlm

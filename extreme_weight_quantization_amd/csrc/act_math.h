@@ -1,0 +1,65 @@
+// Activations of the fused products and their slopes, in fp32 (device helpers).
+//
+//   relu       max(z, 0)                             slope 1 for z > 0, else 0
+//   silu       z p,           p = 1 / (1 + e^-z)     slope p (1 + z (1 - p))
+//   gelu       z erfc(-z / sqrt 2) / 2               slope erfc(-z / sqrt 2) / 2 + z e^(-z^2 / 2) / sqrt(2 pi)
+//   gelu_tanh  z (1 + tanh v) / 2 = z p(2v),         slope p + z p (1 - p) 2 v',
+//              v = sqrt(2 / pi) (z + 0.044715 z^3)   v' = sqrt(2 / pi) (1 + 0.134145 z^2)
+//
+// gelu is written with erfc and gelu_tanh with the logistic function of 2v, so that neither
+// takes a difference of two numbers near one where z is far below zero.  NaN stays NaN.
+#pragma once
+#include "aqlm_device.h"
+
+namespace aqlm {
+
+// Values of aqlm_act (include/aqlm.h).
+enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+// __expf is exact to about |z| 2^-24 relative (the rounding of z log2 e): far inside the one
+// fp16 rounding that every result here takes next.
+__device__ __forceinline__ float logistic(float z) { return 1.f / (1.f + __expf(-z)); }
+
+constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kGeluCubic = 0.044715f;
+
+__device__ __forceinline__ float act_value(int act, float z) {
+    switch (act) {
+        case kActRelu: return z < 0.f ? 0.f : z;
+        case kActSilu: return z / (1.f + __expf(-z));
+        case kActGelu: return 0.5f * z * erfcf(z * -0.70710678118654752f);
+        case kActGeluTanh: return z / (1.f + __expf(-kTwoSqrt2OverPi * (z + kGeluCubic * z * z * z)));
+        default: return z;
+    }
+}
+
+__device__ __forceinline__ float act_slope(int act, float z) {
+    switch (act) {
+        case kActRelu: return z <= 0.f ? 0.f : 1.f;
+        case kActSilu: {
+            const float p = logistic(z);
+            return p * (1.f + z * (1.f - p));
+        }
+        case kActGelu:
+            return 0.5f * erfcf(z * -0.70710678118654752f) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+        case kActGeluTanh: {
+            const float p = logistic(kTwoSqrt2OverPi * (z + kGeluCubic * z * z * z));
+            return p + z * p * (1.f - p) * kTwoSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
+        }
+        default: return 1.f;
+    }
+}
+
+// A row scale s as m 2^e with 1 <= |m| < 2: the exact power of two can go into the fp16
+// weights and m into the other factor, so that only one of the two is rounded.  Zero and
+// values that are not finite keep e = 0.
+__device__ __forceinline__ float scale_mantissa(float s, int* e) {
+    *e = 0;
+    if (!(fabsf(s) > 0.f && fabsf(s) < 1e30f)) return s;
+    int k;
+    const float m = frexpf(s, &k);
+    *e = k - 1;
+    return 2.f * m;
+}
+
+}  // namespace aqlm

@@ -8,6 +8,7 @@
 #include "../../include/aqlm.h"
 #include "aqlm_device.h"
 #include "aqlm_launch.h"
+#include "aqlm_validate.h"
 
 static_assert(AQLM_FUSED_MAX_LAYERS == aqlm::kGemvMaxLayers, "fused layer limit");
 
@@ -31,11 +32,7 @@ int device_cu_count() {
     return n;
 }
 
-enum class Op { kGemv, kGemm, kDecode };
-
-static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-static bool generic_scheme_ok(int M, int B, int g) {
+bool generic_scheme_ok(int M, int B, int g) {
     return M >= 1 && M <= AQLM_MAX_CODEBOOKS && B >= 1 && B <= 16 &&
            (g == 1 || g == 2 || g == 4 || g == 8 || g == 16 || g == 32);
 }
@@ -45,7 +42,7 @@ static bool generic_scheme_ok(int M, int B, int g) {
 // at every batch, 8x8 g32 above batch 8 (below, where its eight lookups per 8 inputs
 // and single codebook copy dominate, the general kernel was faster).  -1: the
 // general kernel.
-static int gemv_b8_scheme(int M, int B, int g, int64_t in, int64_t batch) {
+int gemv_b8_scheme(int M, int B, int g, int64_t in, int64_t batch) {
     if (B != 8 || g != 4 * M || in % 8 != 0) return -1;
     if (M == 1) return kSchemeB8M1;
     if (M == 4) return kSchemeB8M4;
@@ -55,9 +52,9 @@ static int gemv_b8_scheme(int M, int B, int g, int64_t in, int64_t batch) {
 
 // Host-side validation shared by the entry points.  Returns AQLM_OK and the
 // scheme id, or an error status; touches no HIP state.
-static int validate(Op op, const void* codes, const void* codebooks, const void* scales,
-                    const void* x, const void* y, int M, int B, int g, int64_t out, int64_t in,
-                    int64_t batch, int* scheme, bool* empty, uintptr_t codes_align = 16) {
+int validate(Op op, const void* codes, const void* codebooks, const void* scales, const void* x, const void* y,
+             int M, int B, int g, int64_t out, int64_t in, int64_t batch, int* scheme, bool* empty,
+             uintptr_t codes_align) {
     if (op == Op::kDecode && x != nullptr) return AQLM_ERR_NULL;
     if (M == 1 && B == 16 && g == 8) *scheme = kScheme1x16;
     else if (M == 2 && B == 8 && g == 8) *scheme = kScheme2x8;
@@ -83,11 +80,18 @@ static int validate(Op op, const void* codes, const void* codebooks, const void*
     return AQLM_OK;
 }
 
-static int finish(hipError_t e) {
+int finish(hipError_t e) {
     if (e != hipSuccess) {
         g_last_hip_error = (int)e;
         return AQLM_ERR_HIP;
     }
+    return AQLM_OK;
+}
+
+int validate_lists(int M, int B, int g, int64_t out, int64_t in) {
+    if (!(M == 1 && B == 16 && g == 8)) return AQLM_ERR_SCHEME;
+    if (out < 0 || out > AQLM_LISTS_MAX_OUT || in < 8 || in > AQLM_MAX_IN || (in % 8) != 0) return AQLM_ERR_SHAPE;
+    if ((uint64_t)out * (uint64_t)(in / 8) > (uint64_t)UINT32_MAX) return AQLM_ERR_SHAPE;
     return AQLM_OK;
 }
 
@@ -305,12 +309,6 @@ int aqlm_kmeans_init(const void* w, const void* scales, const int64_t* seeds, vo
 }
 
 // ---- 1x16 slice lists
-static int validate_lists(int M, int B, int g, int64_t out, int64_t in) {
-    if (!(M == 1 && B == 16 && g == 8)) return AQLM_ERR_SCHEME;
-    if (out < 0 || out > AQLM_LISTS_MAX_OUT || in < 8 || in > AQLM_MAX_IN || (in % 8) != 0) return AQLM_ERR_SHAPE;
-    if ((uint64_t)out * (uint64_t)(in / 8) > (uint64_t)UINT32_MAX) return AQLM_ERR_SHAPE;
-    return AQLM_OK;
-}
 
 int aqlm_lists_table_bytes(int M, int B, int g, int64_t out, int64_t in, int64_t* bytes) {
     if (!bytes) return AQLM_ERR_NULL;
@@ -448,6 +446,7 @@ const char* aqlm_status_str(int status) {
         case AQLM_ERR_SCRATCH:
             return "AQLM_ERR_SCRATCH: the problem needs more scratch than the allocation-free entry point's "
                    "static buffer holds (AQLM_LISTS_NOALLOC_SCRATCH_BYTES)";
+        case AQLM_ERR_ACT: return "AQLM_ERR_ACT: the activation is none of aqlm_act";
         default: return "unknown aqlm status";
     }
 }

@@ -46,6 +46,18 @@
 // takes tile (b % 8) * per + b / 8 of the token-fastest tile order.  Each XCD
 // then holds a contiguous run of row tiles with all their token tiles: its L2
 // keeps its own W tiles, and the X tiles that its concurrent workgroups share.
+//
+// The same kernel with an epilogue (MODE kDenseAct, kDenseGated; see act_launch.h):
+//   one layer    z = s (x w^T) + bias, y = act(z) + residual;
+//   gated        the 128 rows of a tile are 64 outputs of two layers, 16 rows of the gate
+//                and 16 of the up projection in turn, so one wave holds both products of
+//                an output: y = act(zg) zu.
+// A wave passes its fp32 tile through LDS (64 rows of 64 + 4 floats: the writes of the four
+// lane quarters, 4 rows apart, then hit distinct banks) and finishes 8 outputs a lane,
+// with 16-byte accesses to y, z and the residual; everything up to the one rounding
+// of y (and of z where it is kept) is fp32.
+#include "act_launch.h"
+#include "act_math.h"
 #include "aqlm_device.h"
 #include "aqlm_launch.h"
 
@@ -81,10 +93,112 @@ __device__ __forceinline__ void step_barrier() {
     asm volatile("" ::: "memory");
 }
 
+enum DenseMode : int { kDensePlain = 0, kDenseAct = 1, kDenseGated = 2 };
+
+// What the modes with an epilogue take next to the product's arguments.
+struct DenseEpi {
+    const f16* w1;          // gated: the up projection's weights (w: the gate's)
+    const f16* scales[2];   // row factors applied to the product, or NULL
+    const f16* bias[2];
+    const f16* residual;
+    f16* z[2];
+    int act;
+};
+constexpr int kEpiRow = 68;   // floats per row of a wave's fp32 tile in LDS
+static_assert((size_t)kDenseWaves * 64 * kEpiRow * sizeof(float) <= kDenseLds, "epilogue tiles");
+
+// 8 consecutive fp16 values at p, of which `left` are inside the matrix.
+__device__ __forceinline__ void epi_load8(const f16* p, int left, bool vec, float (&v)[8]) {
+    if (vec) {
+        const f16x8 c = *reinterpret_cast<const f16x8*>(p);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = (float)c[q];
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < left ? (float)p[q] : 0.f;
+    }
+}
+
+__device__ __forceinline__ void epi_store8(f16* p, int left, bool vec, const float (&v)[8]) {
+    f16x8 c;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) c[q] = (f16)v[q];
+    if (vec) {
+        *reinterpret_cast<u32x4*>(p) = as_u32x4(c);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < left) p[q] = c[q];
+    }
+}
+
+// The epilogue of one wave: acc[i][j] holds D[4 (l / 16) + r][l % 16] of the 16x16 block (i, j)
+// of its 64x64 piece.  tok0: its first token; col0: its first output.
+template <int MODE>
+__device__ __forceinline__ void dense_epilogue(const f32x4 (&acc)[4][4], float* tile, int lane, int tok0, int col0,
+                                               f16* y, int out, int T, const DenseEpi& e) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                tile[(i * 16 + 4 * (lane >> 4) + r) * kEpiRow + j * 16 + (lane & 15)] = acc[i][j][r];
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    const bool vec = out % 8 == 0;
+    // one layer: 8 lanes of 8 outputs a row; gated: 4 lanes of 8 outputs a row, the gate's in
+    // columns 32 (c / 2) + 8 (c % 2) .. of the tile, the up projection's 16 further
+    constexpr int kLanes = MODE == kDenseGated ? 4 : 8;
+    const int c = lane % kLanes;
+    const int at = MODE == kDenseGated ? 32 * (c >> 1) + 8 * (c & 1) : 8 * c;
+    const int col = col0 + 8 * c, left = out - col;
+    if (left <= 0) return;
+    constexpr int kN = MODE == kDenseGated ? 2 : 1;
+    float s[kN][8], b[kN][8];
+#pragma unroll
+    for (int l = 0; l < kN; ++l)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int k = min(col + q, out - 1);
+            s[l][q] = e.scales[l] != nullptr ? (float)e.scales[l][k] : 1.f;
+            b[l][q] = e.bias[l] != nullptr ? (float)e.bias[l][k] : 0.f;
+        }
+#pragma unroll
+    for (int it = 0; it < kLanes; ++it) {
+        const int rr = it * (64 / kLanes) + lane / kLanes, tok = tok0 + rr;
+        if (tok >= T) continue;
+        const size_t o = (size_t)tok * out + col;
+        float v[8];
+#pragma unroll
+        for (int l = 0; l < kN; ++l) {
+            const float* src = tile + rr * kEpiRow + at + 16 * l;
+            float z[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) z[q] = src[q] * s[l][q] + b[l][q];
+            if (e.z[l] != nullptr) epi_store8(e.z[l] + o, left, vec, z);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = l == 0 ? act_value(e.act, z[q]) : v[q] * z[q];
+        }
+        if constexpr (MODE == kDenseAct) {
+            if (e.residual != nullptr) {
+                float res[8];
+                epi_load8(e.residual + o, left, vec, res);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] += res[q];
+            }
+        }
+        epi_store8(y + o, left, vec, v);
+    }
+}
+
+// y carries no __restrict__: the residual may be y itself, each element read by the lane
+// that then writes it.
+template <int MODE>
 __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __restrict__ x,
-                                                                   const f16* __restrict__ w, f16* __restrict__ y,
+                                                                   const f16* __restrict__ w, f16* y,
                                                                    int out, int in, int T, int n_tt, int n_tiles,
-                                                                   int per_xcd) {
+                                                                   int per_xcd, DenseEpi epi) {
+    constexpr int kCols = MODE == kDenseGated ? kDenseBN / 2 : kDenseBN;   // outputs per tile
     extern __shared__ u32x4 smem[];
     u32x4* Xs = smem;                 // [stage 3][kDenseXStage]
     u32x4* Ws = smem + kDenseWOff;    // [stage 3][kDenseWStage]
@@ -92,7 +206,7 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
     if (tile >= n_tiles) return;      // the whole workgroup: the grid is rounded up to kXcds * per_xcd
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int lw = wave - kDenseWaves;   // loader index (loader waves only)
-    const int n0 = (tile / n_tt) * kDenseBN;
+    const int n0 = (tile / n_tt) * kCols;
     const int t0 = (tile % n_tt) * kDenseBM;
     const int n_k = in / 64;          // the launcher guarantees in % 64 == 0
 
@@ -118,8 +232,13 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
             const int q = 4 * lw + i;
             const int r = 8 * q + rsub;
             const int c = (lane & 7) ^ ((r >> 1) & 7);
-            const int row = min(n0 + r, out - 1);
-            __builtin_amdgcn_global_load_lds((const void*)(w + (size_t)row * in + (size_t)(8 * jc + c) * kGroup),
+            const f16* wl = w;
+            int row = min(n0 + r, out - 1);
+            if constexpr (MODE == kDenseGated) {   // rows 32 m .. + 15: the gate's outputs 16 m ..; + 16: the up's
+                wl = ((r >> 4) & 1) ? epi.w1 : w;
+                row = min(n0 + 16 * (r >> 5) + (r & 15), out - 1);
+            }
+            __builtin_amdgcn_global_load_lds((const void*)(wl + (size_t)row * in + (size_t)(8 * jc + c) * kGroup),
                                              lds_ptr(dw + 64 * q), 16, 0, 0);
         }
     };
@@ -170,7 +289,7 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
         }
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));   // no load in flight into the epilogue's LDS
-        if (out % 8 == 0) {
+        if (MODE != kDensePlain || out % 8 == 0) {
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
         }
@@ -197,6 +316,16 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
     }
     mma16(a1, b1);              // half 1 of the last step
 
+    if constexpr (MODE != kDensePlain) {
+        // every load has landed and every fragment read is done: the stages are free
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        dense_epilogue<MODE>(acc, reinterpret_cast<float*>(smem) + wave * 64 * kEpiRow, lane, t0 + wm * 64,
+                             n0 + wn * (kCols / 2), y, out, T, epi);
+        return;
+    }
     if (out % 8 == 0) {
         // Every load of every wave has landed and every fragment read is done, so the
         // stages are free: each wave's 64x64 tile goes through LDS (fp16, rows of 64 + 8
@@ -247,22 +376,46 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
     }
 }
 
+// Tiles of `cols` outputs x kDenseBM tokens, dealt to the XCDs in contiguous runs.
+template <int MODE>
+hipError_t launch_dense(const void* x, const void* w16, void* y, int64_t out, int64_t in, int64_t batch,
+                        const DenseEpi& epi, hipStream_t stream) {
+    if (in % 64 != 0) return hipErrorInvalidValue;
+    if (out == 0 || batch == 0) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute((const void*)gemm_dense_kernel<MODE>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)kDenseLds);
+    if (e != hipSuccess) return e;
+    constexpr int kCols = MODE == kDenseGated ? kDenseBN / 2 : kDenseBN;
+    const int64_t n_tt = (batch + kDenseBM - 1) / kDenseBM;
+    const int64_t n_tiles = ((out + kCols - 1) / kCols) * n_tt;
+    const int64_t per = (n_tiles + kXcds - 1) / kXcds;
+    if (per * kXcds > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(gemm_dense_kernel<MODE>, dim3((unsigned)(per * kXcds)), dim3(kDenseThreads), kDenseLds, stream,
+                       (const f16*)x, (const f16*)w16, (f16*)y, (int)out, (int)in, (int)batch, (int)n_tt,
+                       (int)n_tiles, (int)per, epi);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_gemm_dense(const void* x, const void* w16, void* y, int64_t out, int64_t in, int64_t batch,
                              hipStream_t stream) {
-    if (in % 64 != 0) return hipErrorInvalidValue;
-    if (out == 0 || batch == 0) return hipSuccess;
-    const hipError_t e = hipFuncSetAttribute((const void*)gemm_dense_kernel,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)kDenseLds);
-    if (e != hipSuccess) return e;
-    const int64_t n_tt = (batch + kDenseBM - 1) / kDenseBM;
-    const int64_t n_tiles = ((out + kDenseBN - 1) / kDenseBN) * n_tt;
-    const int64_t per = (n_tiles + kXcds - 1) / kXcds;
-    hipLaunchKernelGGL(gemm_dense_kernel, dim3((unsigned)(per * kXcds)), dim3(kDenseThreads), kDenseLds, stream,
-                       (const f16*)x, (const f16*)w16, (f16*)y, (int)out, (int)in, (int)batch, (int)n_tt,
-                       (int)n_tiles, (int)per);
-    return hipGetLastError();
+    return launch_dense<kDensePlain>(x, w16, y, out, in, batch, DenseEpi{}, stream);
+}
+
+hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void* const* scales, int n,
+                                 const Epilogue& epi, int64_t out, int64_t kp, int64_t batch, hipStream_t stream) {
+    DenseEpi e = {};
+    for (int l = 0; l < n; ++l) {
+        e.scales[l] = scales ? static_cast<const f16*>(scales[l]) : nullptr;
+        e.bias[l] = static_cast<const f16*>(epi.bias[l]);
+        e.z[l] = static_cast<f16*>(epi.z[l]);
+    }
+    e.residual = static_cast<const f16*>(epi.residual);
+    e.act = epi.act;
+    if (n == 1) return launch_dense<kDenseAct>(x, w[0], epi.y, out, kp, batch, e, stream);
+    e.w1 = static_cast<const f16*>(w[1]);
+    return launch_dense<kDenseGated>(x, w[0], epi.y, out, kp, batch, e, stream);
 }
 
 }  // namespace aqlm

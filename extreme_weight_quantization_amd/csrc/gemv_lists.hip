@@ -39,6 +39,8 @@
 #include <atomic>
 #include <mutex>
 
+#include "act_launch.h"
+#include "act_math.h"
 #include "aqlm_device.h"
 #include "aqlm_launch.h"
 
@@ -382,13 +384,9 @@ __global__ __launch_bounds__(kListThreads) void gemv_lists_fused_kernel(const Li
                   L.geo[l], blockIdx.x - first);
 }
 
-// y[r] = fp16(s[r] * sum of the row's partials), the slots split into kReduceParts
-// contiguous runs added in slot order, then the runs in order.
-__device__ __forceinline__ void lists_reduce(const float* __restrict__ partial, const f16* __restrict__ scales,
-                                             f16* __restrict__ y, int out, int out_pad, int slots, int blk) {
-    __shared__ float red[kReduceParts][64];
-    const int rl = threadIdx.x & 63, part = threadIdx.x >> 6;
-    const int r = blk * 64 + rl;
+// A row's partials: run `part` of kReduceParts contiguous runs of the slots, added in slot order.
+__device__ __forceinline__ float lists_run_sum(const float* __restrict__ partial, int r, int out, int out_pad, int slots,
+                                               int part) {
     const int per = (slots + kReduceParts - 1) / kReduceParts;
     const int q0 = min(slots, part * per), q1 = min(slots, q0 + per);
     float sum = 0.f;
@@ -401,14 +399,60 @@ __device__ __forceinline__ void lists_reduce(const float* __restrict__ partial, 
             for (int i = 0; i < 16; ++i) sum += v[i];
         }
     }
-    red[part][rl] = sum;
-    __syncthreads();
-    if (part == 0 && r < out) {
-        float t = red[0][rl];
+    return sum;
+}
+
+// The runs of row rl, added in order.
+__device__ __forceinline__ float lists_add_runs(const float (&red)[kReduceParts][64], int rl) {
+    float t = red[0][rl];
 #pragma unroll
-        for (int q = 1; q < kReduceParts; ++q) t += red[q][rl];
-        y[r] = (f16)(t * (float)scales[r]);
+    for (int q = 1; q < kReduceParts; ++q) t += red[q][rl];
+    return t;
+}
+
+// y[r] = fp16(s[r] * sum of the row's partials), the slots split into kReduceParts
+// contiguous runs added in slot order, then the runs in order.
+__device__ __forceinline__ void lists_reduce(const float* __restrict__ partial, const f16* __restrict__ scales,
+                                             f16* __restrict__ y, int out, int out_pad, int slots, int blk) {
+    __shared__ float red[kReduceParts][64];
+    const int rl = threadIdx.x & 63, part = threadIdx.x >> 6;
+    const int r = blk * 64 + rl;
+    red[part][rl] = lists_run_sum(partial, r, out, out_pad, slots, part);
+    __syncthreads();
+    if (part == 0 && r < out) y[r] = (f16)(lists_add_runs(red, rl) * (float)scales[r]);
+}
+
+// The same sums for one layer or for the gate and up projections, then the epilogue of
+// act_launch.h in fp32, rounded once.  Layer l of a block is served by 4 waves of its own.
+struct ListsEpi {
+    const float* partial[2];
+    const f16* scales[2];
+    const f16* bias[2];
+    const f16* residual;   // may be y
+    f16* z[2];
+    f16* y;
+    int out, out_pad, slots, act;
+};
+
+template <int N>
+__global__ __launch_bounds__(64 * kReduceParts * N) void lists_reduce_act_kernel(const ListsEpi e) {
+    __shared__ float red[N][kReduceParts][64];
+    const int rl = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), l = wave / kReduceParts, part = wave % kReduceParts;
+    const int r = blockIdx.x * 64 + rl;
+    red[l][part][rl] = lists_run_sum(e.partial[l], r, e.out, e.out_pad, e.slots, part);
+    __syncthreads();
+    if (wave != 0 || r >= e.out) return;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float z = lists_add_runs(red[k], rl) * (float)e.scales[k][r];
+        if (e.bias[k] != nullptr) z += (float)e.bias[k][r];
+        if (e.z[k] != nullptr) e.z[k][r] = (f16)z;
+        v = k == 0 ? act_value(e.act, z) : v * z;
     }
+    if (e.residual != nullptr) v += (float)e.residual[r];
+    e.y[r] = (f16)v;
 }
 
 __global__ __launch_bounds__(64 * kReduceParts) void lists_reduce_kernel(const float* __restrict__ partial,
@@ -475,8 +519,9 @@ int64_t lists_workspace_bytes_aligned(int64_t out, int64_t in) {
     return (lists_workspace_bytes(out, in) + 255) / 256 * 256;
 }
 
-// The caller has filled every per-layer field but geo, wg_end and blk_end (out > 0 for every layer).
-hipError_t launch_gemv_lists_fused(ListsLayers L, const void* x, int64_t in, hipStream_t stream) {
+// The product of layers whose caller has filled every field but geo, wg_end and blk_end
+// (out > 0 for every layer): fills these and writes the partial sums.
+static hipError_t launch_lists_product(ListsLayers& L, const void* x, int64_t in, hipStream_t stream) {
     size_t lds = 0;
     int64_t wgs = 0, blks = 0;
     for (int l = 0; l < L.n; ++l) {
@@ -505,18 +550,49 @@ hipError_t launch_gemv_lists_fused(ListsLayers L, const void* x, int64_t in, hip
     const void* kern = multi ? (const void*)fk : (const void*)sk;
     const hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    if (multi) {
+    if (multi)
         hipLaunchKernelGGL(fk, dim3((unsigned)wgs), dim3(kListThreads), lds, stream, L, static_cast<const f16*>(x));
-        hipLaunchKernelGGL(lists_reduce_fused_kernel, dim3((unsigned)blks), dim3(64 * kReduceParts), 0, stream, L);
-    } else {   // one layer: the compact argument lists
-        const ListsGeo& g = L.geo[0];
+    else   // one layer: the compact argument list
         hipLaunchKernelGGL(sk, dim3((unsigned)wgs), dim3(kListThreads), lds, stream, L.table[0],
                            L.entries[0], L.cap[0], static_cast<const f16*>(L.codebook[0]),
-                           static_cast<const f16*>(x), L.partial[0], g);
-        hipLaunchKernelGGL(lists_reduce_kernel, dim3((unsigned)blks), dim3(64 * kReduceParts), 0, stream,
+                           static_cast<const f16*>(x), L.partial[0], L.geo[0]);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemv_lists_fused(ListsLayers L, const void* x, int64_t in, hipStream_t stream) {
+    const hipError_t e = launch_lists_product(L, x, in, stream);
+    if (e != hipSuccess) return e;
+    const unsigned blks = (unsigned)L.blk_end[L.n - 1];
+    if (L.n > 1)
+        hipLaunchKernelGGL(lists_reduce_fused_kernel, dim3(blks), dim3(64 * kReduceParts), 0, stream, L);
+    else
+        hipLaunchKernelGGL(lists_reduce_kernel, dim3(blks), dim3(64 * kReduceParts), 0, stream,
                            static_cast<const float*>(L.partial[0]), static_cast<const f16*>(L.scales[0]),
-                           static_cast<f16*>(L.y[0]), L.out[0], g.n_rt * 64, g.slots());
+                           static_cast<f16*>(L.y[0]), L.out[0], L.geo[0].n_rt * 64, L.geo[0].slots());
+    return hipGetLastError();
+}
+
+hipError_t launch_lists_act(ListsLayers L, const void* x, const Epilogue& epi, int64_t in, hipStream_t stream) {
+    const hipError_t e = launch_lists_product(L, x, in, stream);
+    if (e != hipSuccess) return e;
+    ListsEpi a = {};
+    for (int l = 0; l < L.n; ++l) {
+        a.partial[l] = L.partial[l];
+        a.scales[l] = static_cast<const f16*>(L.scales[l]);
+        a.bias[l] = static_cast<const f16*>(epi.bias[l]);
+        a.z[l] = static_cast<f16*>(epi.z[l]);
     }
+    a.residual = static_cast<const f16*>(epi.residual);
+    a.y = static_cast<f16*>(epi.y);
+    a.out = L.out[0];
+    a.out_pad = L.geo[0].n_rt * 64;
+    a.slots = L.geo[0].slots();
+    a.act = epi.act;
+    const unsigned blks = (unsigned)((L.out[0] + 63) / 64);
+    if (L.n > 1)
+        hipLaunchKernelGGL(lists_reduce_act_kernel<2>, dim3(blks), dim3(64 * kReduceParts * 2), 0, stream, a);
+    else
+        hipLaunchKernelGGL(lists_reduce_act_kernel<1>, dim3(blks), dim3(64 * kReduceParts), 0, stream, a);
     return hipGetLastError();
 }
 

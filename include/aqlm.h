@@ -65,7 +65,8 @@ typedef enum {
     AQLM_ERR_SCHEME = 3, /* (M, B, g) outside 1..AQLM_MAX_CODEBOOKS x 1..16 x {1,2,4,8,16,32} */
     AQLM_ERR_ALIGN = 4,  /* codes, codebooks, x or y not 16-byte aligned, scales not 2-byte aligned */
     AQLM_ERR_HIP = 5,    /* the HIP runtime reported an error at launch */
-    AQLM_ERR_SCRATCH = 6 /* more scratch needed than an allocation-free entry point holds */
+    AQLM_ERR_SCRATCH = 6, /* more scratch needed than an allocation-free entry point holds */
+    AQLM_ERR_ACT = 7     /* an activation that is none of aqlm_act */
 } aqlm_status;
 
 /* Largest `in` accepted (inputs per row). */
@@ -329,6 +330,104 @@ int aqlm_lists_fused_workspace_bytes(int n_layers, const int64_t* outs, int M, i
 int aqlm_linear_gemv_lists_noalloc(const void* table, const void* entries, int64_t entries_bytes,
                                    const void* codebooks, const void* scales, const void* x, void* y, int M, int B,
                                    int g, int64_t out, int64_t in, int64_t batch, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Fused products: what a feed-forward block does right after its quantized
+ * projections, done before their results leave the kernel, and the gradients
+ * of both with respect to their inputs and biases (the quantized weights are
+ * frozen: codes, codebooks and scales get no gradient).
+ *
+ *   aqlm_linear_act           z = W x + bias;  y = act(z) + residual
+ *   aqlm_gated                zg = Wg x + bg;  zu = Wu x + bu;  y = act(zg) * zu
+ *   aqlm_linear_act_backward  dz = dy * act'(z);  dx = dz W;  dbias = sum_b dz[b]
+ *   aqlm_gated_backward       dzg = dy * zu * act'(zg);  dzu = dy * act(zg);
+ *                             dx = dzg Wg + dzu Wu;  dbias likewise
+ *
+ * act is one of aqlm_act; gelu is z (1 + erf(z / sqrt 2)) / 2, gelu_tanh its
+ * tanh form z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2, silu is
+ * z / (1 + exp(-z)).  relu's slope at 0 is 0.
+ *
+ * Arrays: codes, codebooks, scales, x as above, every scheme with codes in
+ * whole bytes; bias [out] fp16; residual, z, y, dy [batch][out] fp16; x, dx
+ * [batch][in] fp16; dbias [out] fp16.  bias, residual and z (forward) may be
+ * NULL: no bias, no residual, the pre-activations not kept.  residual may be y
+ * itself (the residual stream updated in place); no other arrays may overlap.
+ * The gated calls take host arrays of two entries, gate then up, of one
+ * scheme, out and in; their bias and z arrays may be NULL as a whole or per
+ * entry.  bias and dbias need 2-byte alignment, everything else 16 bytes.
+ *
+ * Backward: z holds the pre-activations that the forward call kept; NULL for
+ * aqlm_linear_act_backward with AQLM_ACT_NONE.  dbias NULL: not wanted (gated:
+ * both or neither).  dx, dbias are overwritten, not added to.  out == 0 gives
+ * dx = 0, batch == 0 gives dbias = 0 (sums over nothing).
+ *
+ * Sizes: 0 <= out <= AQLM_ACT_MAX_OUT, 1 <= in <= AQLM_MAX_IN, in % g == 0,
+ * 0 <= batch <= 2^31 - 257, out * ceil(in / 64) * 8 < 2^32 and
+ * out * (in / g) < 2^32 (else AQLM_ERR_SHAPE).  An activation outside aqlm_act
+ * gives AQLM_ERR_ACT.
+ *
+ * Workspace: caller-owned device memory, 16-byte aligned, of at least the
+ * bytes that the _workspace_bytes call of the same shape gives (0 for some
+ * shapes: NULL is then accepted; an undersized one gives AQLM_ERR_SHAPE).  Its
+ * contents on entry do not matter; calls that share it, captured graphs
+ * included, must not run concurrently.
+ *
+ * Numerics: products are accumulated in fp32; bias, activation, gate and
+ * residual are applied in fp32; y, and z where it is kept, are rounded to fp16
+ * once, y from the unrounded z.  The products run on fp16 weights: exact
+ * codewords for M = 1 (the row scale applied in fp32), otherwise the decoded
+ * weights that aqlm_linear_decode gives.  Backward, dz is rounded to fp16
+ * before dx = dz W; dbias sums the fp32 values in a fixed order.  Results are
+ * deterministic.
+ */
+typedef enum {
+    AQLM_ACT_NONE = 0,
+    AQLM_ACT_RELU = 1,
+    AQLM_ACT_SILU = 2,
+    AQLM_ACT_GELU = 3,
+    AQLM_ACT_GELU_TANH = 4
+} aqlm_act;
+
+/* Largest out of the fused products. */
+#define AQLM_ACT_MAX_OUT (1 << 24)
+
+int aqlm_linear_act_workspace_bytes(int M, int B, int g, int64_t out, int64_t in, int64_t batch, int64_t* bytes);
+int aqlm_linear_act(const void* codes, const void* codebooks, const void* scales, const void* x, const void* bias,
+                    const void* residual, void* z, void* y, void* workspace, int64_t workspace_bytes, int act, int M,
+                    int B, int g, int64_t out, int64_t in, int64_t batch, void* stream);
+
+int aqlm_gated_workspace_bytes(int M, int B, int g, int64_t out, int64_t in, int64_t batch, int64_t* bytes);
+int aqlm_gated(const void* const* codes, const void* const* codebooks, const void* const* scales, const void* x,
+               const void* const* bias, void* const* z, void* y, void* workspace, int64_t workspace_bytes, int act,
+               int M, int B, int g, int64_t out, int64_t in, int64_t batch, void* stream);
+
+int aqlm_linear_act_backward_workspace_bytes(int M, int B, int g, int64_t out, int64_t in, int64_t batch,
+                                             int64_t* bytes);
+int aqlm_linear_act_backward(const void* codes, const void* codebooks, const void* scales, const void* dy,
+                             const void* z, void* dx, void* dbias, void* workspace, int64_t workspace_bytes, int act,
+                             int M, int B, int g, int64_t out, int64_t in, int64_t batch, void* stream);
+
+int aqlm_gated_backward_workspace_bytes(int M, int B, int g, int64_t out, int64_t in, int64_t batch, int64_t* bytes);
+int aqlm_gated_backward(const void* const* codes, const void* const* codebooks, const void* const* scales,
+                        const void* dy, const void* const* z, void* dx, void* const* dbias, void* workspace,
+                        int64_t workspace_bytes, int act, int M, int B, int g, int64_t out, int64_t in, int64_t batch,
+                        void* stream);
+
+/*
+ * The forward calls over slice lists (1x16, batch 0 or 1): table, entries and
+ * entries_bytes as for aqlm_linear_gemv_lists, workspace of
+ * aqlm_lists_fused_workspace_bytes for one layer, or for two of the same out.
+ * The epilogue runs in the reduction of the partial sums; numerics otherwise
+ * as aqlm_linear_gemv_lists.
+ */
+int aqlm_linear_act_lists(const void* table, const void* entries, int64_t entries_bytes, const void* codebooks,
+                          const void* scales, const void* x, const void* bias, const void* residual, void* z, void* y,
+                          void* workspace, int64_t workspace_bytes, int act, int M, int B, int g, int64_t out,
+                          int64_t in, int64_t batch, void* stream);
+int aqlm_gated_lists(const void* const* tables, const void* const* entries, const int64_t* entries_bytes,
+                     const void* const* codebooks, const void* const* scales, const void* x, const void* const* bias,
+                     void* const* z, void* y, void* workspace, int64_t workspace_bytes, int act, int M, int B, int g,
+                     int64_t out, int64_t in, int64_t batch, void* stream);
 
 /* Static, human-readable name of a status code. */
 const char* aqlm_status_str(int status);
