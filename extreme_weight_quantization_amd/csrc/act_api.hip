@@ -1,7 +1,8 @@
 // C ABI of the fused products and their backward passes (declared in include/aqlm.h):
 // argument checks on the host, then the launches on the caller's stream.
 //
-// The products run in passes: the weights decoded once into the workspace as fp16, then a
+// Forward at batch 1..16 the codes are multiplied as they are decoded, in one launch.
+// Otherwise the products run in passes: the weights decoded once into the workspace as fp16, then a
 // dense matrix-core product over them.  Forward, the decoded rows are padded to whole
 // steps of 64 inputs; backward, they are written transposed (dx = dz W sums over the rows
 // of W).  With one codebook (M = 1) a codeword is exactly an fp16 weight: forward, the row
@@ -50,6 +51,7 @@ ForwardPlan forward_plan(int n, int64_t out, int64_t in, int64_t batch) {
     Parts parts;
     p.kp = round_up(in, 64);
     p.pad = p.kp != in;
+    if (batch <= AQLM_GEMV_MAX_BATCH) return p;   // one launch straight from the codes
     for (int l = 0; l < n; ++l) p.w[l] = parts.add(out, p.kp, 2);
     if (p.pad) p.xp = parts.add(batch, p.kp, 2);
     p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
@@ -126,6 +128,8 @@ int forward(const ActLayers& L, const void* x, const Epilogue& epi, void* worksp
     const int wt = check_workspace(workspace, workspace_bytes, p.bytes);
     if (wt != AQLM_OK) return wt;
     const hipStream_t s = (hipStream_t)stream;
+    if (batch <= AQLM_GEMV_MAX_BATCH)
+        return finish(launch_gemv_act(GenericScheme{M, B, g}, L, x, epi, out, in, batch, s));
     char* base = static_cast<char*>(workspace);
     void* w[2] = {base + p.w[0], base + p.w[1]};
     const WeightScale ws = M == 1 ? WeightScale::kNone : WeightScale::kFull;

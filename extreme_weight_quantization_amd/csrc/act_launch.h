@@ -59,6 +59,15 @@ hipError_t launch_act_grad(const void* dy, const void* const* z, const void* con
                            float* partial, void* const* dbias, int64_t out, int64_t op, int64_t batch,
                            hipStream_t stream);
 
+// The products of batch 1..16 (gemv_act.hip): any scheme, no workspace.
+hipError_t launch_gemv_act(const GenericScheme& sc, const ActLayers& L, const void* x, const Epilogue& epi, int64_t out,
+                           int64_t in, int64_t batch, hipStream_t stream);
+// Their streaming form (gemv_stream.hip): false where it does not serve the call (as
+// gemv_stream_lds), else true with the launch's result.
+struct GemvEpi;
+bool launch_gemv_stream_act(const ActLayers& L, const GemvEpi& epi, const void* x, void* y, int64_t out, int64_t in,
+                            int64_t batch, hipStream_t stream, hipError_t* result);
+
 // The slice-list product of one layer, or of gate and up, batch 1, with the epilogue in its
 // reduction (gemv_lists.hip).  L as for launch_gemv_lists_fused; its y is not used.
 hipError_t launch_lists_act(ListsLayers L, const void* x, const Epilogue& epi, int64_t in, hipStream_t stream);

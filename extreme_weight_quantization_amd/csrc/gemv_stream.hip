@@ -37,10 +37,15 @@
 // 16 lanes served together (lane l reads codebook (l / 8) % 2 first), and an
 // address is one v_perm_b32.  Results are deterministic, and a launch over
 // several layers gives bit for bit what one launch per layer gives.
+//
+// The kinds with an epilogue (gemv_body.h) run the same body: gated tiles are 8 rows of
+// the gate and 8 of the up projection, which share the 8 replicas of the LDS codebook.
 #include <algorithm>
 
+#include "act_launch.h"
 #include "aqlm_device.h"
 #include "aqlm_launch.h"
+#include "gemv_body.h"
 
 namespace aqlm {
 
@@ -97,11 +102,12 @@ struct StreamGeo {
     int G, n_slab, n_rt, R, SP, TP;
 };
 
+template <int TILE_ROWS>
 __device__ __forceinline__ StreamGeo stream_geo(int out, int in, int bid, int nwg) {
     StreamGeo g;
     g.G = in / kGroup;
     g.n_slab = (g.G + kSSlab - 1) / kSSlab;
-    g.n_rt = (out + 15) / 16;
+    g.n_rt = (out + TILE_ROWS - 1) / TILE_ROWS;
     g.R = (g.n_rt - bid + nwg - 1) / nwg;
     g.SP = min(kSWaves, g.n_slab);
     g.TP = kSWaves / g.SP;
@@ -110,13 +116,15 @@ __device__ __forceinline__ StreamGeo stream_geo(int out, int in, int bid, int nw
 
 // The product for one layer, run by workgroup bid of the nwg that serve it.
 // D: steps of codes in flight per wave.
-template <int D>
+template <int D, int KIND = kGemvPlain>
 __device__ __forceinline__ void stream_body(const uint8_t* __restrict__ codes, const f16* __restrict__ codebooks,
-                                            const f16* __restrict__ scales, f16* __restrict__ y, const int out,
+                                            const f16* __restrict__ scales, f16* y, const int out,
                                             const int bid, const int nwg, const f16* __restrict__ x, const int in,
-                                            const int T) {
+                                            const int T, const GemvEpi epi = {}) {
+    constexpr bool GATED = KIND == kGemvGated;
+    constexpr int kTileRows = GATED ? 8 : 16;       // output rows of a tile
     extern __shared__ u32x4 smem[];
-    const StreamGeo geo = stream_geo(out, in, bid, nwg);
+    const StreamGeo geo = stream_geo<kTileRows>(out, in, bid, nwg);
     const int G = geo.G;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -133,14 +141,16 @@ __device__ __forceinline__ void stream_body(const uint8_t* __restrict__ codes, c
     const int xslots = (T * XS + 63) & ~63;
     const int nred = geo.SP + 1;                    // partials per tile: the slab parts, then the ragged slab
     float* red = reinterpret_cast<float*>(smem + kSCbBytes / 16 + xslots);
-    const uint16_t* c16 = reinterpret_cast<const uint16_t*>(codes);
+    const bool up = GATED && lrow >= 8;             // gated: this lane's layer
+    const int trow = GATED ? lrow & 7 : lrow;
+    const uint16_t* c16 = reinterpret_cast<const uint16_t*>(up ? epi.codes1 : codes);
 
-    auto tile_row0 = [&](int j) { return (bid + (tp + geo.TP * j) * nwg) * 16; };
+    auto tile_row0 = [&](int j) { return (bid + (tp + geo.TP * j) * nwg) * kTileRows; };
     // Codes of slab s of local tile j for this lane: rows past the layer are clamped
     // into it (their outputs are never written), and a chunk of 8 groups past the
     // row (G % 8 == 0) to the row's last chunk (its products are masked).
     auto load_codes = [&](int j, int s) -> u32x4 {
-        const int row = min(tile_row0(j) + lrow, out - 1);
+        const int row = min(tile_row0(j) + trow, out - 1);
         return load16(c16 + (size_t)row * G + min(s * kSSlab + 8 * kq, G - 8));
     };
 
@@ -158,12 +168,14 @@ __device__ __forceinline__ void stream_body(const uint8_t* __restrict__ codes, c
         }
     }
 
-    // Codebooks: 16-byte slot (2 k + m) 8 + r holds codeword k of codebook m.
+    // Codebooks: 16-byte slot (2 k + m) 8 + r holds codeword k of codebook m (gated: of the
+    // gate's for r < 4, of the up projection's above).
 #pragma unroll
     for (int it = 0; it < kSCbBytes / 16 / kSThreads; ++it) {
         const int km = (it * kSThreads + tid) / kSRepl;
+        const f16* cbl = GATED && (tid & 4) != 0 ? epi.codebooks1 : codebooks;
         __builtin_amdgcn_global_load_lds(
-            (const void*)(codebooks + (size_t)((km & 1) * kCodewords2x8 + (km >> 1)) * kGroup),
+            (const void*)(cbl + (size_t)((km & 1) * kCodewords2x8 + (km >> 1)) * kGroup),
             lds_ptr(smem + it * kSThreads + wave * kWave), 16, 0, 0);
     }
     // x: entry b XS + j (batch row b, group j) after the codebooks; entries past
@@ -183,7 +195,8 @@ __device__ __forceinline__ void stream_body(const uint8_t* __restrict__ codes, c
     __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
     __syncthreads();
 
-    const uint32_t mA = (lane >> 3) & 1u, r16 = (lane & 7u) * 16u;
+    const uint32_t mA = GATED ? (lane >> 2) & 1u : (lane >> 3) & 1u;
+    const uint32_t r16 = (GATED ? (lane & 3u) + 4u * (uint32_t)up : lane & 7u) * 16u;
     const uint32_t base = (r16 + 128u * mA) | ((r16 + 128u * (mA ^ 1u)) << 8);
     const int xrow = min(lrow, T - 1);   // batch columns past the batch repeat the last row (discarded)
     const uint32_t xlane = (uint32_t)kSCbBytes + 16u * (uint32_t)(xrow * XS + 8 * kq);
@@ -236,13 +249,20 @@ __device__ __forceinline__ void stream_body(const uint8_t* __restrict__ codes, c
         }
     }
     __syncthreads();
-    for (int e = tid; e < geo.R * 16 * T; e += kSThreads) {
-        const int i = e / (16 * T), rr = (e / T) % 16, col = e % T;
-        const int row = (bid + i * nwg) * 16 + rr;
+    for (int e = tid; e < geo.R * kTileRows * T; e += kSThreads) {
+        const int i = e / (kTileRows * T), rr = (e / T) % kTileRows, col = e % T;
+        const int row = (bid + i * nwg) * kTileRows + rr;
         if (row < out) {
             float sum = 0.f;
             for (int q = 0; q < nred; ++q) sum += red[((i * nred + q) * 16 + rr) * T + col];
-            y[(size_t)col * out + row] = (f16)(sum * (float)scales[row]);
+            if constexpr (KIND == kGemvPlain) {
+                y[(size_t)col * out + row] = (f16)(sum * (float)scales[row]);
+            } else {
+                float sum1 = 0.f;
+                if constexpr (GATED)
+                    for (int q = 0; q < nred; ++q) sum1 += red[((i * nred + q) * 16 + 8 + rr) * T + col];
+                gemv_finish<KIND>(sum, sum1, scales, y, col, row, out, epi);
+            }
         }
     }
 }
@@ -272,6 +292,14 @@ __global__ __launch_bounds__(kSThreads) __attribute__((amdgpu_waves_per_eu(1, 4)
     stream_body<D>(static_cast<const uint8_t*>(L.codes[li]), static_cast<const f16*>(L.codebooks[li]),
                     static_cast<const f16*>(L.scales[li]), static_cast<f16*>(L.y[li]), L.out[li],
                     (int)blockIdx.x - wg0, wg1 - wg0, x, in, T);
+}
+
+// With an epilogue: one layer, or the gate and up projections (epi's second layer).
+template <int D, int KIND>
+__global__ __launch_bounds__(kSThreads) __attribute__((amdgpu_waves_per_eu(1, 4))) void gemv_stream_act_kernel(
+    const uint8_t* __restrict__ codes, const f16* __restrict__ codebooks, const f16* __restrict__ scales, f16* y, int out,
+    const f16* __restrict__ x, int in, int T, GemvEpi epi) {
+    stream_body<D, KIND>(codes, codebooks, scales, y, out, (int)blockIdx.x, (int)gridDim.x, x, in, T, epi);
 }
 
 template <int D>
@@ -304,25 +332,45 @@ hipError_t launch_d(const GemvLayers& layers, const void* x, int in, int T, size
 // twice as long to stage, it needs four steps a wave: 11008x4096 (three) takes
 // 9.1 us against 9.0, 8192x8192 (four) 10.0 against 10.2, 28672x8192 21.5
 // against 28.3.
-size_t gemv_stream_lds(const GemvLayers& layers, int64_t in, int64_t batch) {
+static size_t stream_lds(int rmax, int64_t in, int64_t batch) {
     if (batch < 1 || batch > kSMaxT || in % 64 != 0 || in <= 0) return 0;
     const int G = (int)(in / kGroup), n_slab = (G + kSSlab - 1) / kSSlab;
     const int SP = std::min(kSWaves, n_slab);
-    int rmax = 0, wg0 = 0;
-    for (int l = 0; l < layers.n; ++l) {
-        const int n_rt = (layers.out[l] + 15) / 16, w = layers.wg_end[l] - wg0;
-        wg0 = layers.wg_end[l];
-        rmax = std::max(rmax, (n_rt + w - 1) / w);
-    }
     if ((int64_t)rmax * n_slab < (batch > 2 ? kSMinSteps34 : kSMinSteps) * kSWaves) return 0;
     const size_t xslots = (size_t)((batch * (((G + 63) & ~63) + 1) + 63) & ~63);
     const size_t lds = (size_t)kSCbBytes + xslots * 16 + (size_t)rmax * (SP + 1) * 16 * batch * sizeof(float);
     return lds <= (size_t)160 * 1024 ? lds : 0;
 }
 
+size_t gemv_stream_lds(const GemvLayers& layers, int64_t in, int64_t batch) {
+    int rmax = 0, wg0 = 0;
+    for (int l = 0; l < layers.n; ++l) {
+        const int n_rt = (layers.out[l] + 15) / 16, w = layers.wg_end[l] - wg0;
+        wg0 = layers.wg_end[l];
+        rmax = std::max(rmax, (n_rt + w - 1) / w);
+    }
+    return stream_lds(rmax, in, batch);
+}
+
 hipError_t launch_gemv_stream(const GemvLayers& layers, const void* x, int64_t in, int64_t batch, size_t lds,
                               hipStream_t stream) {
     return launch_d<kSRing>(layers, x, (int)in, (int)batch, lds, stream);
+}
+
+bool launch_gemv_stream_act(const ActLayers& L, const GemvEpi& epi, const void* x, void* y, int64_t out, int64_t in,
+                            int64_t batch, hipStream_t stream, hipError_t* result) {
+    const int tile = L.n == 2 ? 8 : 16;
+    const int n_rt = (int)((out + tile - 1) / tile), grid = std::min(n_rt, device_cu_count());
+    const size_t lds = stream_lds((n_rt + grid - 1) / grid, in, batch);
+    if (lds == 0) return false;
+    auto kern = L.n == 2 ? gemv_stream_act_kernel<kSRing, kGemvGated> : gemv_stream_act_kernel<kSRing, kGemvAct>;
+    *result = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (*result != hipSuccess) return true;
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(kSThreads), lds, stream, static_cast<const uint8_t*>(L.codes[0]),
+                       static_cast<const f16*>(L.codebooks[0]), static_cast<const f16*>(L.scales[0]),
+                       static_cast<f16*>(y), (int)out, static_cast<const f16*>(x), (int)in, (int)batch, epi);
+    *result = hipGetLastError();
+    return true;
 }
 
 }  // namespace aqlm
