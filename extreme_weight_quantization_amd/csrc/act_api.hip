@@ -1,7 +1,8 @@
 // C ABI of the fused products and their backward passes (declared in include/aqlm.h):
 // argument checks on the host, then the launches on the caller's stream.
 //
-// Forward at batch 1..16 the codes are multiplied as they are decoded, in one launch.
+// Forward at batch 1..16 the codes are multiplied as they are decoded, in one launch; 2x8 and
+// 1x16 at some tens of tokens likewise, with partial sums in the workspace (skinny.hip).
 // Otherwise the products run in passes: the weights decoded once into the workspace as fp16, then a
 // dense matrix-core product over them.  Forward, the decoded rows are padded to whole
 // steps of 64 inputs; backward, they are written transposed (dx = dz W sums over the rows
@@ -42,19 +43,24 @@ struct Parts {
 
 struct ForwardPlan {
     int64_t kp = 0, w[2] = {0, 0}, xp = 0, bytes = 0;
-    bool pad = false;
+    bool pad = false, skinny = false;
 };
 
 // n layers: their weights as rows of kp inputs, then x padded to them.
-ForwardPlan forward_plan(int n, int64_t out, int64_t in, int64_t batch) {
+ForwardPlan forward_plan(int n, const GenericScheme& sc, int64_t out, int64_t in, int64_t batch) {
     ForwardPlan p;
     Parts parts;
     p.kp = round_up(in, 64);
     p.pad = p.kp != in;
-    if (batch <= AQLM_GEMV_MAX_BATCH) return p;   // one launch straight from the codes
+    if (out == 0 || batch <= AQLM_GEMV_MAX_BATCH) return p;   // one launch straight from the codes
+    if (skinny_serves(sc, out, in, batch)) {
+        p.skinny = true;
+        p.bytes = skinny_partial_bytes(n, out, in, batch);
+        return p;
+    }
     for (int l = 0; l < n; ++l) p.w[l] = parts.add(out, p.kp, 2);
     if (p.pad) p.xp = parts.add(batch, p.kp, 2);
-    p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
+    p.bytes = parts.total;
     return p;
 }
 
@@ -89,7 +95,7 @@ int check_sizes(int n, int act, int M, int B, int g, int64_t out, int64_t in, in
         return AQLM_ERR_SHAPE;
     const int64_t bt = (batch + 255) / 256, wide = op > kp ? op : kp;
     if ((wide / 64 + 8) * bt > INT32_MAX / 2 || grad_chunks(batch) * (op / 512 + 1) > INT32_MAX) return AQLM_ERR_SHAPE;
-    if (forward_plan(n, out, in, batch).bytes < 0 || backward_plan(n, act, out, in, batch).bytes < 0)
+    if (forward_plan(n, GenericScheme{M, B, g}, out, in, batch).bytes < 0 || backward_plan(n, act, out, in, batch).bytes < 0)
         return AQLM_ERR_SHAPE;
     return AQLM_OK;
 }
@@ -124,12 +130,14 @@ int forward(const ActLayers& L, const void* x, const Epilogue& epi, void* worksp
     if (!aligned(x, 16) || !aligned(epi.y, 16) || !aligned(epi.residual, 16)) return AQLM_ERR_ALIGN;
     for (int l = 0; l < L.n; ++l)
         if (!aligned(epi.z[l], 16) || !aligned(epi.bias[l], 2)) return AQLM_ERR_ALIGN;
-    const ForwardPlan p = forward_plan(L.n, out, in, batch);
+    const ForwardPlan p = forward_plan(L.n, GenericScheme{M, B, g}, out, in, batch);
     const int wt = check_workspace(workspace, workspace_bytes, p.bytes);
     if (wt != AQLM_OK) return wt;
     const hipStream_t s = (hipStream_t)stream;
     if (batch <= AQLM_GEMV_MAX_BATCH)
         return finish(launch_gemv_act(GenericScheme{M, B, g}, L, x, epi, out, in, batch, s));
+    if (p.skinny)
+        return finish(launch_skinny(GenericScheme{M, B, g}, L, x, workspace, epi, out, in, batch, s));
     char* base = static_cast<char*>(workspace);
     void* w[2] = {base + p.w[0], base + p.w[1]};
     const WeightScale ws = M == 1 ? WeightScale::kNone : WeightScale::kFull;
@@ -227,7 +235,7 @@ int workspace_bytes_of(int n, bool back, int M, int B, int g, int64_t out, int64
     if (!bytes) return AQLM_ERR_NULL;
     const int st = check_sizes(n, AQLM_ACT_RELU, M, B, g, out, in, batch);
     if (st != AQLM_OK) return st;
-    *bytes = back ? backward_plan(n, AQLM_ACT_RELU, out, in, batch).bytes : forward_plan(n, out, in, batch).bytes;
+    *bytes = back ? backward_plan(n, AQLM_ACT_RELU, out, in, batch).bytes : forward_plan(n, GenericScheme{M, B, g}, out, in, batch).bytes;
     return AQLM_OK;
 }
 

@@ -68,6 +68,17 @@ struct GemvEpi;
 bool launch_gemv_stream_act(const ActLayers& L, const GemvEpi& epi, const void* x, void* y, int64_t out, int64_t in,
                             int64_t batch, hipStream_t stream, hipError_t* result);
 
+// The products of tens of tokens (skinny.hip), 2x8 and 1x16: straight from the codes, with
+// fp32 partial sums in the workspace.  The work is dealt to at most kSkinnyWorkgroups
+// workgroups, a fixed number so that the sums' order does not depend on the device.
+constexpr int kSkinnyWorkgroups = 256;
+constexpr int kSkinnyMaxBatch2x8 = 256;
+constexpr int kSkinnyMaxBatch1x16 = 64;
+bool skinny_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch);
+int64_t skinny_partial_bytes(int n, int64_t out, int64_t in, int64_t batch);
+hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void* x, void* partial, const Epilogue& epi,
+                         int64_t out, int64_t in, int64_t batch, hipStream_t stream);
+
 // The slice-list product of one layer, or of gate and up, batch 1, with the epilogue in its
 // reduction (gemv_lists.hip).  L as for launch_gemv_lists_fused; its y is not used.
 hipError_t launch_lists_act(ListsLayers L, const void* x, const Epilogue& epi, int64_t in, hipStream_t stream);

@@ -1,0 +1,395 @@
+// Products of a small batch (tens of tokens) straight from the codes, 2x8 and 1x16:
+//   P_l[t][i] = sum_k Wc_l[i][k] x[t][k]  for one layer, or the gate and up projections,
+// then the epilogue of act_launch.h.
+//
+// "The AQLM Quantization Algorithm, Explained", Figure 2 of the MCQ section (a group's
+// weights are the sum of one codeword per codebook, times the row's scale) and section
+// "Key AQLM quantization parameters" (2x8 and 1x16 at g = 8).
+//
+// Between the decode-phase product (one 16-column matrix-core tile of tokens) and prefill (where decoding
+// the weights once into memory pays) a call is bound by its codeword lookups, the matrix
+// cores and fixed latencies.  So the weights never leave the registers they are looked up into:
+//
+//  * the matrix-core operand of W wants lane l to hold 8 consecutive inputs of row l % 16,
+//    which is one group of 8: a lane looks its groups up (2x8: two codewords from the LDS
+//    copy of the codebooks, 8 replicas, conflict-free as in gemv.hip; 1x16: one 16-byte
+//    gather from L2, a step ahead) and multiplies them at once.  2x8 multiplies its two
+//    codewords one by one, so their sum is never rounded to fp16;
+//  * a workgroup of 16 waves covers 256 rows (gated: 8 gate and 8 up rows a wave) and
+//    walks slabs of 32 groups (256 inputs); the x tile of a slab, BM tokens, sits in LDS
+//    for all waves, three stages of direct-to-LDS loads, one barrier a slab;
+//  * the (token tile, row block, slab) units are dealt to one workgroup per CU in equal
+//    contiguous runs, so every CU has the same work whatever the shape; each run's part of
+//    a row block is written as fp32 partial sums, and skinny_finish_kernel adds a
+//    block's parts in order, applies the row scale and the epilogue, and rounds once.
+//
+// LDS layout of an x stage: token b, group c in 16-byte slot 32 b + (c ^ (b % 16)), so the
+// 16 lanes that read one group of 16 tokens hit 16 distinct bank groups.
+#include <algorithm>
+
+#include "act_launch.h"
+#include "act_math.h"
+#include "aqlm_device.h"
+
+namespace aqlm {
+
+namespace {
+
+constexpr int kKWaves = 16;
+constexpr int kKThreads = kKWaves * kWave;
+constexpr int kKSlab = 32;                                  // groups per step
+constexpr int kKStages = 3;
+constexpr int kKRepl = 8;                                   // 2x8 codebook replicas in LDS
+constexpr int kKCbBytes = 2 * kCodewords2x8 * kKRepl * 16;   // 64 KB
+
+struct SkinnyArgs {
+    const uint8_t* codes[2];
+    const f16* codebooks[2];
+    const f16* x;
+    float* partial;   // [slot][t][l][op]
+    int out, op, G, T;
+    int n_slab, n_blk;   // slabs of a row; row blocks
+    int units;           // token tiles x row blocks x slabs
+};
+
+// First unit of workgroup w, and the workgroup of unit u, of W equal contiguous runs.
+__host__ __device__ __forceinline__ int run_begin(int w, int W, int units) { return (int)((int64_t)w * units / W); }
+__host__ __device__ __forceinline__ int run_of(int u, int W, int units) {
+    return (int)((((int64_t)u + 1) * W - 1) / units);
+}
+
+// 16 bytes of the workgroup's LDS (dynamic only, so it starts at address 0).
+__device__ __forceinline__ u32x4 lds16(uint32_t byte) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)byte);
+}
+
+template <int SCHEME, int BM, bool GATED>
+__global__ __launch_bounds__(kKThreads) __attribute__((amdgpu_waves_per_eu(4, 4))) void skinny_kernel(const SkinnyArgs a) {
+    extern __shared__ u32x4 smem[];
+    constexpr int kCT = BM / 16;                              // column tiles of tokens
+    constexpr int kXStage = BM * kKSlab;                      // 16-byte slots of a stage
+    constexpr int kNX = kXStage / kKThreads;                  // x loads a wave issues a step
+    constexpr uint32_t kXOff = SCHEME == kScheme2x8 ? kKCbBytes : 0;
+    constexpr int kTileRows = GATED ? 8 : 16;
+    constexpr int kN = GATED ? 2 : 1;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lrow = lane & 15, kq = lane >> 4;
+    const bool up = GATED && lrow >= 8;
+    const int trow = GATED ? lrow & 7 : lrow;
+    const uint16_t* codes = reinterpret_cast<const uint16_t*>(up ? a.codes[1] : a.codes[0]);
+    const f16* codebooks = up ? a.codebooks[1] : a.codebooks[0];
+    const int G = a.G, n_slab = a.n_slab;
+    const int W = gridDim.x, wid = blockIdx.x;
+    const int u0 = run_begin(wid, W, a.units), n = run_begin(wid + 1, W, a.units) - u0;   // n >= 1: W <= units
+
+    // a unit is (token tile t, row block b, slab s), s fastest
+    struct Unit { int t, b, s; };
+    auto unit_of = [&](int u) -> Unit {
+        const int blk = u / n_slab;
+        return Unit{blk / a.n_blk, blk % a.n_blk, u - blk * n_slab};
+    };
+    auto next = [&](Unit& v) {
+        if (++v.s == n_slab) {
+            v.s = 0;
+            if (++v.b == a.n_blk) { v.b = 0; ++v.t; }
+        }
+    };
+    // the 8 codes of this lane in a unit: rows past the layer repeat its last row (their
+    // outputs are not used), groups past the row its last 8 (masked when used)
+    auto load_codes = [&](const Unit& v) -> u32x4 {
+        const int row = min((v.b * kKWaves + wave) * kTileRows + trow, a.out - 1);
+        const uint16_t* r = codes + (size_t)row * G;
+        const int g0 = v.s * kKSlab + 8 * kq;
+        if (G % 8 == 0) return load_nt16(r + min(g0, G - 8));
+        u32x4 c;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            c[q] = (uint32_t)r[min(g0 + 2 * q, G - 1)] | ((uint32_t)r[min(g0 + 2 * q + 1, G - 1)] << 16);
+        return c;
+    };
+    // x of a unit into a stage: load i of a wave fills slots 64 (wave kNX + i) .. + 63, two tokens;
+    // tokens past the batch repeat its last one, groups past the row its last group
+    auto load_x = [&](const Unit& v, int stage) {
+        u32x4* dst = smem + kXOff / 16 + stage * kXStage;
+#pragma unroll
+        for (int i = 0; i < kNX; ++i) {
+            const int slot = 64 * (wave * kNX + i) + lane;
+            const int b = slot / kKSlab, c = (slot % kKSlab) ^ (b & 15);
+            const int tok = min(v.t * BM + b, a.T - 1), grp = min(v.s * kKSlab + c, G - 1);
+            __builtin_amdgcn_global_load_lds((const void*)(a.x + ((size_t)tok * G + grp) * kGroup),
+                                             lds_ptr(dst + 64 * (wave * kNX + i)), 16, 0, 0);
+        }
+    };
+    auto gather = [&](const u32x4 cv, u32x4 (&e)[8]) {   // 1x16
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            e[q] = load16(codebooks + (size_t)((cv[q >> 1] >> (16 * (q & 1))) & 0xffffu) * kGroup);
+    };
+
+    Unit cur = unit_of(u0), pre = cur;   // the unit multiplied, and the next one to load
+    u32x4 c0 = load_codes(pre);          // codes of step k
+    load_x(pre, 0);
+    if (n > 1) next(pre);
+    u32x4 c1 = load_codes(pre);          // codes of step k + 1
+    load_x(pre, 1);
+    if (n > 2) next(pre);
+    int loaded = min(n - 1, 2);          // pre is step `loaded`: the last step is loaded again past the end
+    if constexpr (SCHEME == kScheme2x8) {
+        // slot (2 k + m) 8 + r: codeword k of codebook m (gated: the gate's for r < 4)
+#pragma unroll
+        for (int it = 0; it < kKCbBytes / 16 / kKThreads; ++it) {
+            const int km = (it * kKThreads + tid) / kKRepl;
+            const f16* cbl = GATED && (tid & 4) != 0 ? a.codebooks[1] : a.codebooks[0];
+            __builtin_amdgcn_global_load_lds(
+                (const void*)(cbl + (size_t)((km & 1) * kCodewords2x8 + (km >> 1)) * kGroup),
+                lds_ptr(smem + it * kKThreads + wave * kWave), 16, 0, 0);
+        }
+    }
+    u32x4 e[8] = {};
+    if constexpr (SCHEME == kScheme1x16) gather(c0, e);
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+    __syncthreads();
+
+    const uint32_t mA = GATED ? (lane >> 2) & 1u : (lane >> 3) & 1u;
+    const uint32_t r16 = (GATED ? (lane & 3u) + 4u * (uint32_t)up : lane & 7u) * 16u;
+    const uint32_t base = (r16 + 128u * mA) | ((r16 + 128u * (mA ^ 1u)) << 8);
+    const uint32_t xlane = kXOff + 16u * (uint32_t)(kKSlab * lrow + ((8 * kq) ^ lrow));
+    f32x4 acc[kCT];
+#pragma unroll
+    for (int j = 0; j < kCT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // the products of one unit; RAGGED: its last groups are past the row and count as zero
+    auto multiply = [&](const u32x4 cv, const u32x4 (&ev)[8], int s, int stage, auto ragged) {
+        constexpr bool RAGGED = decltype(ragged)::value;
+        const uint32_t xs = xlane + (uint32_t)(stage * kXStage * 16);
+        const int left = G - s * kKSlab - 8 * kq;   // groups of this lane inside the row
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f16x8 w[4], w2[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (SCHEME == kScheme2x8) {
+                    const uint32_t d = cv[2 * h + (q >> 1)], hw = 2u * (q & 1);
+                    w[q] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0004u | ((hw + mA) << 8))));
+                    w2[q] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0005u | ((hw + (mA ^ 1u)) << 8))));
+                } else {
+                    w[q] = as_f16x8(ev[4 * h + q]);
+                }
+                if constexpr (RAGGED) {
+                    w[q] = 4 * h + q < left ? w[q] : f16x8{};
+                    if constexpr (SCHEME == kScheme2x8) w2[q] = 4 * h + q < left ? w2[q] : f16x8{};
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t xa = xs ^ (uint32_t)((4 * h + q) << 4);
+                f16x8 xv[kCT];
+#pragma unroll
+                for (int j = 0; j < kCT; ++j) {
+                    xv[j] = as_f16x8(lds16(xa + (uint32_t)(j * 16 * kKSlab * 16)));
+                    if constexpr (RAGGED) xv[j] = 4 * h + q < left ? xv[j] : f16x8{};
+                }
+#pragma unroll
+                for (int j = 0; j < kCT; ++j) acc[j] = mfma16x16x32(w[q], xv[j], acc[j]);
+                if constexpr (SCHEME == kScheme2x8) {
+#pragma unroll
+                    for (int j = 0; j < kCT; ++j) acc[j] = mfma16x16x32(w2[q], xv[j], acc[j]);
+                }
+            }
+        }
+    };
+    // the run's part of a row block: lane holds rows 4 kq + r of token l % 16 of each column tile
+    auto flush = [&](const Unit& v) {
+        const int first = run_of((v.t * a.n_blk + v.b) * n_slab, W, a.units);
+        const int tile0 = (v.b * kKWaves + wave) * kTileRows;
+        const int l = GATED ? kq >> 1 : 0, r0 = tile0 + (GATED ? 4 * (kq & 1) : 4 * kq);
+        if (tile0 < a.op) {
+#pragma unroll
+            for (int j = 0; j < kCT; ++j) {
+                const int tok = v.t * BM + 16 * j + lrow;
+                if (tok < a.T)
+                    *reinterpret_cast<f32x4*>(a.partial + (((size_t)(wid - first) * a.T + tok) * kN + l) * a.op + r0) =
+                        acc[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kCT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+
+    for (int k = 0, stage = 0; k < n; ++k) {
+        // what later steps need, the x loads last: the wait at the end leaves only those in flight
+        u32x4 en[8];
+        if constexpr (SCHEME == kScheme1x16) gather(c1, en);
+        const u32x4 c2 = load_codes(pre);
+        __builtin_amdgcn_sched_barrier(0);
+        load_x(pre, stage == 0 ? 2 : stage - 1);   // stage (k + 2) % 3: read last in step k - 1
+        if (loaded < n - 1) { next(pre); ++loaded; }
+        __builtin_amdgcn_sched_barrier(0);
+        if ((cur.s + 1) * kKSlab <= G) multiply(c0, e, cur.s, stage, std::false_type{});
+        else multiply(c0, e, cur.s, stage, std::true_type{});
+        const Unit done = cur;
+        next(cur);
+        if (cur.s == 0 || k == n - 1) flush(done);
+        c0 = c1;
+        c1 = c2;
+        if constexpr (SCHEME == kScheme1x16) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) e[q] = en[q];
+        }
+        stage = stage == 2 ? 0 : stage + 1;
+        // x of step k + 1 has landed (issued a step ago); at most this step's x loads are in flight
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kNX));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));   // no LDS load in flight at exit
+}
+
+struct FinishArgs {
+    const float* partial;
+    const f16* scales[2];
+    const f16* bias[2];
+    const f16* residual;   // may be y
+    f16* z[2];
+    f16* y;
+    int out, op, T, act;
+    int bm, blk_rows, n_slab, n_blk, units, W;
+};
+
+// Thread: 4 outputs of a token.  The parts of its row block are the runs from the one that
+// holds the block's first unit to the one that holds its last, added in that order.
+template <int N>
+__global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) {
+    const int per = a.op / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)a.T * per) return;
+    const int t = (int)(i / per), r0 = 4 * (int)(i - (int64_t)t * per);
+    const int blk = (t / a.bm) * a.n_blk + r0 / a.blk_rows;
+    const int parts = run_of((blk + 1) * a.n_slab - 1, a.W, a.units) - run_of(blk * a.n_slab, a.W, a.units) + 1;
+    f32x4 sum[N];
+#pragma unroll
+    for (int l = 0; l < N; ++l) sum[l] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const size_t step = (size_t)a.T * N * a.op;
+    const float* p = a.partial + ((size_t)t * N) * a.op + r0;
+    for (int s = 0; s < parts; ++s, p += step)
+#pragma unroll
+        for (int l = 0; l < N; ++l) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(p + (size_t)l * a.op);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[l][r] += v[r];
+        }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int row = r0 + r;
+        if (row >= a.out) break;
+        const size_t at = (size_t)t * a.out + row;
+        float v = 0.f;
+#pragma unroll
+        for (int l = 0; l < N; ++l) {
+            float z = sum[l][r] * (float)a.scales[l][row];
+            if (a.bias[l] != nullptr) z += (float)a.bias[l][row];
+            if (a.z[l] != nullptr) a.z[l][at] = (f16)z;
+            v = l == 0 ? act_value(a.act, z) : v * z;
+        }
+        if (a.residual != nullptr) v += (float)a.residual[at];
+        a.y[at] = (f16)v;
+    }
+}
+
+// Geometry of one call.
+struct SkinnyPlan {
+    int bm = 0, blk_rows = 0, op = 0, n_slab = 0, n_blk = 0, units = 0, W = 0, slots = 0;
+};
+
+// Token tiles of up to 64 tokens for 2x8 (its codebooks leave room for three x stages of
+// them); 1x16 is bound by its gathers, one per code and token tile.
+SkinnyPlan skinny_plan(int n, int64_t out, int64_t in, int64_t batch) {
+    SkinnyPlan p;
+    const int64_t bm = batch <= 32 ? 32 : 64, tile = n == 2 ? 8 : 16;
+    const int64_t n_slab = (in / kGroup + kKSlab - 1) / kKSlab, n_blk = (out + kKWaves * tile - 1) / (kKWaves * tile);
+    const int64_t units = (batch + bm - 1) / bm * n_blk * n_slab;
+    p.bm = (int)bm;
+    p.blk_rows = (int)(kKWaves * tile);
+    p.op = (int)((out + tile - 1) / tile * tile);
+    p.n_slab = (int)n_slab;
+    p.n_blk = (int)n_blk;
+    p.units = (int)units;
+    p.W = (int)std::min<int64_t>(kSkinnyWorkgroups, units);
+    // the runs that share a row block: those that its slabs fill, and one cut at each end
+    p.slots = (int)((n_slab * p.W + units - 1) / units + 1);
+    return p;
+}
+
+template <int SCHEME, int BM, bool GATED>
+hipError_t launch_main(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t stream) {
+    auto kern = skinny_kernel<SCHEME, BM, GATED>;
+    const size_t lds = (SCHEME == kScheme2x8 ? kKCbBytes : 0) + (size_t)kKStages * BM * kKSlab * 16;
+    static_assert((SCHEME == kScheme2x8 ? kKCbBytes : 0) + kKStages * BM * kKSlab * 16 <= 163840, "LDS budget");
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3(p.W), dim3(kKThreads), lds, stream, a);
+    return hipGetLastError();
+}
+
+template <int SCHEME>
+hipError_t launch_scheme(int n, const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t stream) {
+    if (p.bm == 32) return n == 2 ? launch_main<SCHEME, 32, true>(p, a, stream) : launch_main<SCHEME, 32, false>(p, a, stream);
+    return n == 2 ? launch_main<SCHEME, 64, true>(p, a, stream) : launch_main<SCHEME, 64, false>(p, a, stream);
+}
+
+}  // namespace
+
+bool skinny_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch) {
+    const bool two = sc.M == 2 && sc.B == 8 && sc.g == 8, one = sc.M == 1 && sc.B == 16 && sc.g == 8;
+    if (!two && !one) return false;
+    if (batch > (two ? kSkinnyMaxBatch2x8 : kSkinnyMaxBatch1x16)) return false;
+    // units are counted in 32 bits
+    return ((batch + 31) / 32) * ((out + 127) / 128) * (in / 256 + 1) < (1 << 30);
+}
+
+int64_t skinny_partial_bytes(int n, int64_t out, int64_t in, int64_t batch) {
+    const SkinnyPlan p = skinny_plan(n, out, in, batch);
+    return (int64_t)p.slots * batch * n * p.op * 4;
+}
+
+hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void* x, void* partial, const Epilogue& epi,
+                         int64_t out, int64_t in, int64_t batch, hipStream_t stream) {
+    const SkinnyPlan p = skinny_plan(L.n, out, in, batch);
+    SkinnyArgs a = {};
+    FinishArgs f = {};
+    for (int l = 0; l < L.n; ++l) {
+        a.codes[l] = static_cast<const uint8_t*>(L.codes[l]);
+        a.codebooks[l] = static_cast<const f16*>(L.codebooks[l]);
+        f.scales[l] = static_cast<const f16*>(L.scales[l]);
+        f.bias[l] = static_cast<const f16*>(epi.bias[l]);
+        f.z[l] = static_cast<f16*>(epi.z[l]);
+    }
+    a.x = static_cast<const f16*>(x);
+    f.partial = a.partial = static_cast<float*>(partial);
+    f.out = a.out = (int)out;
+    f.op = a.op = p.op;
+    a.G = (int)(in / kGroup);
+    f.T = a.T = (int)batch;
+    f.n_slab = a.n_slab = p.n_slab;
+    f.n_blk = a.n_blk = p.n_blk;
+    f.units = a.units = p.units;
+    f.residual = static_cast<const f16*>(epi.residual);
+    f.y = static_cast<f16*>(epi.y);
+    f.act = epi.act;
+    f.bm = p.bm;
+    f.blk_rows = p.blk_rows;
+    f.W = p.W;
+    const hipError_t e = sc.B == 8 ? launch_scheme<kScheme2x8>(L.n, p, a, stream)
+                                   : launch_scheme<kScheme1x16>(L.n, p, a, stream);
+    if (e != hipSuccess) return e;
+    const int64_t threads = batch * (p.op / 4);
+    const dim3 grid((unsigned)((threads + 255) / 256));
+    if (L.n == 2) hipLaunchKernelGGL(skinny_finish_kernel<2>, grid, dim3(256), 0, stream, f);
+    else hipLaunchKernelGGL(skinny_finish_kernel<1>, grid, dim3(256), 0, stream, f);
+    return hipGetLastError();
+}
+
+}  // namespace aqlm
