@@ -13,7 +13,7 @@
 //  * the matrix-core operand of W wants lane l to hold 8 consecutive inputs of row l % 16,
 //    which is one group of 8: a lane looks its groups up (2x8: two codewords from the LDS
 //    copy of the codebooks, 8 replicas, conflict-free as in gemv.hip; 1x16: one 16-byte
-//    gather from L2, a step ahead) and multiplies them at once.  2x8 multiplies its two
+//    gather from L2, half a step ahead) and multiplies them at once.  2x8 multiplies its two
 //    codewords one by one, so their sum is never rounded to fp16;
 //  * a workgroup of 16 waves covers 256 rows (gated: 8 gate and 8 up rows a wave) and
 //    walks slabs of 32 groups (256 inputs); the x tile of a slab, BM tokens, sits in LDS
@@ -35,10 +35,9 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kKWaves = 16;
-constexpr int kKThreads = kKWaves * kWave;
+constexpr int kKTiles = 16;                                  // matrix-core row tiles of a workgroup (256 rows)
 constexpr int kKSlab = 32;                                  // groups per step
-constexpr int kKStages = 3;
+constexpr int kKStages = 3;                                 // steps of x (LDS stages) and codes (registers) in flight
 constexpr int kKRepl = 8;                                   // 2x8 codebook replicas in LDS
 constexpr int kKCbBytes = 2 * kCodewords2x8 * kKRepl * 16;   // 64 KB
 
@@ -63,13 +62,28 @@ __device__ __forceinline__ u32x4 lds16(uint32_t byte) {
     return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)byte);
 }
 
-template <int SCHEME, int BM, bool GATED>
-__global__ __launch_bounds__(kKThreads) __attribute__((amdgpu_waves_per_eu(4, 4))) void skinny_kernel(const SkinnyArgs a) {
+// How a row divides into slabs and 16-byte pieces of codes: whole slabs (in % 256 == 0), whole
+// pieces (in % 64 == 0), or neither.
+enum RowKind : int { kRowWhole = 0, kRowVec = 1, kRowAny = 2 };
+
+// Zeros that the direct-to-LDS loads of x read in the place of groups past the row.
+__device__ const u32x4 skinny_zero = {0u, 0u, 0u, 0u};
+
+// RT: row tiles of a wave (16 / RT waves a workgroup).  SUM: 2x8 adds its two codewords in
+// fp16 (one rounding) before one product, instead of multiplying both.
+template <int SCHEME, int BM, bool GATED, int ROW, int RT, bool SUM>
+__global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_eu(4 / RT, 4 / RT))) void skinny_kernel(
+    const SkinnyArgs a) {
     extern __shared__ u32x4 smem[];
+    constexpr int kThreads = 64 * kKTiles / RT;
     constexpr int kCT = BM / 16;                              // column tiles of tokens
     constexpr int kXStage = BM * kKSlab;                      // 16-byte slots of a stage
-    constexpr int kNX = kXStage / kKThreads;                  // x loads a wave issues a step
+    constexpr int kNX = kXStage / kThreads;                   // x loads a wave issues a step
+    constexpr int kR = kKStages;                              // steps of x and of codes in flight
+    constexpr bool kRagged = ROW != kRowWhole;                // the last slab may have groups past the row
     constexpr uint32_t kXOff = SCHEME == kScheme2x8 ? kKCbBytes : 0;
+    // vector loads that every step issues: the x tile, one of codes, the gathers
+    constexpr int kIssued = kNX + RT + (SCHEME == kScheme1x16 ? 8 * RT : 0);
     constexpr int kTileRows = GATED ? 8 : 16;
     constexpr int kN = GATED ? 2 : 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -84,69 +98,88 @@ __global__ __launch_bounds__(kKThreads) __attribute__((amdgpu_waves_per_eu(4, 4)
 
     // a unit is (token tile t, row block b, slab s), s fastest
     struct Unit { int t, b, s; };
-    auto unit_of = [&](int u) -> Unit {
-        const int blk = u / n_slab;
-        return Unit{blk / a.n_blk, blk % a.n_blk, u - blk * n_slab};
-    };
     auto next = [&](Unit& v) {
-        if (++v.s == n_slab) {
-            v.s = 0;
-            if (++v.b == a.n_blk) { v.b = 0; ++v.t; }
-        }
+        const bool row = v.s == n_slab - 1, col = row && v.b == a.n_blk - 1;
+        v.s = row ? 0 : v.s + 1;
+        v.b = col ? 0 : v.b + (row ? 1 : 0);
+        v.t += col ? 1 : 0;
+    };
+    // the unit of step `at`; past the last step it stays
+    struct Ahead { Unit v; int at; };
+    auto advance = [&](Ahead& p) {
+        Unit w = p.v;
+        next(w);
+        if (p.at < n - 1) { p.v = w; ++p.at; }
     };
     // the 8 codes of this lane in a unit: rows past the layer repeat its last row (their
     // outputs are not used), groups past the row its last 8 (masked when used)
-    auto load_codes = [&](const Unit& v) -> u32x4 {
-        const int row = min((v.b * kKWaves + wave) * kTileRows + trow, a.out - 1);
+    auto load_codes = [&](const Unit& v, int rt) -> u32x4 {
+        const int row = min((v.b * kKTiles + wave * RT + rt) * kTileRows + trow, a.out - 1);
         const uint16_t* r = codes + (size_t)row * G;
         const int g0 = v.s * kKSlab + 8 * kq;
-        if (G % 8 == 0) return load_nt16(r + min(g0, G - 8));
-        u32x4 c;
+        if constexpr (ROW != kRowAny) {
+            return load_nt16(r + min(g0, G - 8));
+        } else {
+            u32x4 c;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            c[q] = (uint32_t)r[min(g0 + 2 * q, G - 1)] | ((uint32_t)r[min(g0 + 2 * q + 1, G - 1)] << 16);
-        return c;
+            for (int q = 0; q < 4; ++q)
+                c[q] = (uint32_t)r[min(g0 + 2 * q, G - 1)] | ((uint32_t)r[min(g0 + 2 * q + 1, G - 1)] << 16);
+            return c;
+        }
     };
     // x of a unit into a stage: load i of a wave fills slots 64 (wave kNX + i) .. + 63, two tokens;
-    // tokens past the batch repeat its last one, groups past the row its last group
+    // tokens past the batch repeat its last one, groups past the row are zero
     auto load_x = [&](const Unit& v, int stage) {
         u32x4* dst = smem + kXOff / 16 + stage * kXStage;
 #pragma unroll
         for (int i = 0; i < kNX; ++i) {
             const int slot = 64 * (wave * kNX + i) + lane;
             const int b = slot / kKSlab, c = (slot % kKSlab) ^ (b & 15);
-            const int tok = min(v.t * BM + b, a.T - 1), grp = min(v.s * kKSlab + c, G - 1);
-            __builtin_amdgcn_global_load_lds((const void*)(a.x + ((size_t)tok * G + grp) * kGroup),
-                                             lds_ptr(dst + 64 * (wave * kNX + i)), 16, 0, 0);
+            const int tok = min(v.t * BM + b, a.T - 1), grp = v.s * kKSlab + c;
+            const f16* src = a.x + ((size_t)tok * G + grp) * kGroup;
+            if constexpr (kRagged) src = grp < G ? src : reinterpret_cast<const f16*>(&skinny_zero);
+            __builtin_amdgcn_global_load_lds((const void*)src, lds_ptr(dst + 64 * (wave * kNX + i)), 16, 0, 0);
         }
     };
-    auto gather = [&](const u32x4 cv, u32x4 (&e)[8]) {   // 1x16
+    // 1x16: the codewords of half h (four groups) of a unit's codes
+    auto gather = [&](const u32x4 (&cv)[RT], int h, u32x4 (&e)[RT][4]) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            e[q] = load16(codebooks + (size_t)((cv[q >> 1] >> (16 * (q & 1))) & 0xffffu) * kGroup);
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                e[rt][q] =
+                    load16(codebooks + (size_t)((cv[rt][2 * h + (q >> 1)] >> (16 * (q & 1))) & 0xffffu) * kGroup);
     };
 
-    Unit cur = unit_of(u0), pre = cur;   // the unit multiplied, and the next one to load
-    u32x4 c0 = load_codes(pre);          // codes of step k
-    load_x(pre, 0);
-    if (n > 1) next(pre);
-    u32x4 c1 = load_codes(pre);          // codes of step k + 1
-    load_x(pre, 1);
-    if (n > 2) next(pre);
-    int loaded = min(n - 1, 2);          // pre is step `loaded`: the last step is loaded again past the end
+    const int blk0 = u0 / n_slab;
+    Unit cur{blk0 / a.n_blk, blk0 % a.n_blk, u0 - blk0 * n_slab};   // the unit multiplied
+    Ahead px{cur, 0}, pc{cur, 0};                                   // the next x tile and codes to load
+    u32x4 ring[kR][RT];   // codes of step k in ring[k % kR]
+    auto load_ring = [&](u32x4 (&r)[RT]) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) r[rt] = load_codes(pc.v, rt);
+        advance(pc);
+    };
+#pragma unroll
+    for (int d = 0; d < kR; ++d) load_ring(ring[d]);
+#pragma unroll
+    for (int d = 0; d < kR - 1; ++d) {
+        load_x(px.v, d);
+        advance(px);
+    }
     if constexpr (SCHEME == kScheme2x8) {
         // slot (2 k + m) 8 + r: codeword k of codebook m (gated: the gate's for r < 4)
 #pragma unroll
-        for (int it = 0; it < kKCbBytes / 16 / kKThreads; ++it) {
-            const int km = (it * kKThreads + tid) / kKRepl;
+        for (int it = 0; it < kKCbBytes / 16 / kThreads; ++it) {
+            const int km = (it * kThreads + tid) / kKRepl;
             const f16* cbl = GATED && (tid & 4) != 0 ? a.codebooks[1] : a.codebooks[0];
             __builtin_amdgcn_global_load_lds(
                 (const void*)(cbl + (size_t)((km & 1) * kCodewords2x8 + (km >> 1)) * kGroup),
-                lds_ptr(smem + it * kKThreads + wave * kWave), 16, 0, 0);
+                lds_ptr(smem + it * kThreads + wave * kWave), 16, 0, 0);
         }
     }
-    u32x4 e[8] = {};
-    if constexpr (SCHEME == kScheme1x16) gather(c0, e);
+    u32x4 e[2][RT][4] = {};   // 1x16: codewords of the two halves of a step, gathered half a step ahead
+    if constexpr (SCHEME == kScheme1x16) gather(ring[0], 0, e[0]);
     __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
     __syncthreads();
 
@@ -154,96 +187,116 @@ __global__ __launch_bounds__(kKThreads) __attribute__((amdgpu_waves_per_eu(4, 4)
     const uint32_t r16 = (GATED ? (lane & 3u) + 4u * (uint32_t)up : lane & 7u) * 16u;
     const uint32_t base = (r16 + 128u * mA) | ((r16 + 128u * (mA ^ 1u)) << 8);
     const uint32_t xlane = kXOff + 16u * (uint32_t)(kKSlab * lrow + ((8 * kq) ^ lrow));
-    f32x4 acc[kCT];
+    f32x4 acc[RT][kCT];
+    auto clear = [&]() {
 #pragma unroll
-    for (int j = 0; j < kCT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int j = 0; j < kCT; ++j) acc[rt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    clear();
 
-    // the products of one unit; RAGGED: its last groups are past the row and count as zero
-    auto multiply = [&](const u32x4 cv, const u32x4 (&ev)[8], int s, int stage, auto ragged) {
-        constexpr bool RAGGED = decltype(ragged)::value;
-        const uint32_t xs = xlane + (uint32_t)(stage * kXStage * 16);
-        const int left = G - s * kKSlab - 8 * kq;   // groups of this lane inside the row
+    // the products of one unit; xs: this lane's place in the stage, left: its groups inside
+    // the row (those past it count as zero: x is zero there, W is made so).  The LDS reads of
+    // group q + 1 are spread between the products of group q, so that both units stay busy
+    // (all reads of a half first: the step took the sum of both, 7300 clocks for 64 tokens).
+    auto fetch = [&](const u32x4 (&cv)[RT], uint32_t xs, int q, f16x8 (&w)[RT], f16x8 (&w2)[RT], f16x8 (&xv)[kCT]) {
+        if constexpr (SCHEME == kScheme2x8) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f16x8 w[4], w2[4];
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t d = cv[rt][q >> 1], hw = 2u * (q & 1);
+                w[rt] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0004u | ((hw + mA) << 8))));
+                w2[rt] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0005u | ((hw + (mA ^ 1u)) << 8))));
+            }
+        }
+        const uint32_t xa = xs ^ (uint32_t)(q << 4);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (SCHEME == kScheme2x8) {
-                    const uint32_t d = cv[2 * h + (q >> 1)], hw = 2u * (q & 1);
-                    w[q] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0004u | ((hw + mA) << 8))));
-                    w2[q] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0005u | ((hw + (mA ^ 1u)) << 8))));
-                } else {
-                    w[q] = as_f16x8(ev[4 * h + q]);
+        for (int j = 0; j < kCT; ++j) xv[j] = as_f16x8(lds16(xa + (uint32_t)(j * 16 * kKSlab * 16)));
+    };
+    auto multiply = [&](const u32x4 (&cv)[RT], u32x4 (&e)[2][RT][4], const u32x4 (&ahead)[RT], uint32_t xs, int left) {
+        constexpr bool kTwo = SCHEME == kScheme2x8;
+        constexpr int kReads = kCT + (kTwo ? 2 * RT : 0), kProducts = RT * kCT * (kTwo && !SUM ? 2 : 1);
+        f16x8 w[2][RT], w2[2][RT], xv[2][kCT];
+        fetch(cv, xs, 0, w[0], w2[0], xv[0]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (q + 1 < 8) fetch(cv, xs, q + 1, w[(q + 1) & 1], w2[(q + 1) & 1], xv[(q + 1) & 1]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                f16x8 a0 = w[q & 1][rt], a1 = w2[q & 1][rt];
+                if constexpr (!kTwo) a0 = as_f16x8(e[q >> 2][rt][q & 3]);
+                if constexpr (kTwo && SUM) a0 = a0 + a1;
+                if constexpr (kRagged) {
+                    a0 = q < left ? a0 : f16x8{};
+                    if constexpr (kTwo && !SUM) a1 = q < left ? a1 : f16x8{};
                 }
-                if constexpr (RAGGED) {
-                    w[q] = 4 * h + q < left ? w[q] : f16x8{};
-                    if constexpr (SCHEME == kScheme2x8) w2[q] = 4 * h + q < left ? w2[q] : f16x8{};
+#pragma unroll
+                for (int j = 0; j < kCT; ++j) acc[rt][j] = mfma16x16x32(a0, xv[q & 1][j], acc[rt][j]);
+                if constexpr (kTwo && !SUM) {
+#pragma unroll
+                    for (int j = 0; j < kCT; ++j) acc[rt][j] = mfma16x16x32(a1, xv[q & 1][j], acc[rt][j]);
                 }
             }
+            if (q + 1 < 8) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t xa = xs ^ (uint32_t)((4 * h + q) << 4);
-                f16x8 xv[kCT];
-#pragma unroll
-                for (int j = 0; j < kCT; ++j) {
-                    xv[j] = as_f16x8(lds16(xa + (uint32_t)(j * 16 * kKSlab * 16)));
-                    if constexpr (RAGGED) xv[j] = 4 * h + q < left ? xv[j] : f16x8{};
+                for (int i = 0; i < (kReads < kProducts ? kReads : kProducts); ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one matrix product
+                    __builtin_amdgcn_sched_group_barrier(0x100, kReads <= kProducts ? 1 : (kReads + kProducts - 1) / kProducts, 0);   // LDS reads
                 }
-#pragma unroll
-                for (int j = 0; j < kCT; ++j) acc[j] = mfma16x16x32(w[q], xv[j], acc[j]);
-                if constexpr (SCHEME == kScheme2x8) {
-#pragma unroll
-                    for (int j = 0; j < kCT; ++j) acc[j] = mfma16x16x32(w2[q], xv[j], acc[j]);
-                }
+                if constexpr (kReads < kProducts) __builtin_amdgcn_sched_group_barrier(0x008, kProducts - kReads, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (!kTwo) {
+                if (q == 3) gather(ahead, 0, e[0]);   // the first half of the next step's codewords
             }
         }
     };
     // the run's part of a row block: lane holds rows 4 kq + r of token l % 16 of each column tile
     auto flush = [&](const Unit& v) {
         const int first = run_of((v.t * a.n_blk + v.b) * n_slab, W, a.units);
-        const int tile0 = (v.b * kKWaves + wave) * kTileRows;
-        const int l = GATED ? kq >> 1 : 0, r0 = tile0 + (GATED ? 4 * (kq & 1) : 4 * kq);
-        if (tile0 < a.op) {
+        const int l = GATED ? kq >> 1 : 0;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int tile0 = (v.b * kKTiles + wave * RT + rt) * kTileRows;
+            const int r0 = tile0 + (GATED ? 4 * (kq & 1) : 4 * kq);
+            if (tile0 >= a.op) break;
 #pragma unroll
             for (int j = 0; j < kCT; ++j) {
                 const int tok = v.t * BM + 16 * j + lrow;
                 if (tok < a.T)
                     *reinterpret_cast<f32x4*>(a.partial + (((size_t)(wid - first) * a.T + tok) * kN + l) * a.op + r0) =
-                        acc[j];
+                        acc[rt][j];
             }
         }
-#pragma unroll
-        for (int j = 0; j < kCT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        clear();
     };
 
-    for (int k = 0, stage = 0; k < n; ++k) {
-        // what later steps need, the x loads last: the wait at the end leaves only those in flight
-        u32x4 en[8];
-        if constexpr (SCHEME == kScheme1x16) gather(c1, en);
-        const u32x4 c2 = load_codes(pre);
-        __builtin_amdgcn_sched_barrier(0);
-        load_x(pre, stage == 0 ? 2 : stage - 1);   // stage (k + 2) % 3: read last in step k - 1
-        if (loaded < n - 1) { next(pre); ++loaded; }
-        __builtin_amdgcn_sched_barrier(0);
-        if ((cur.s + 1) * kKSlab <= G) multiply(c0, e, cur.s, stage, std::false_type{});
-        else multiply(c0, e, cur.s, stage, std::true_type{});
-        const Unit done = cur;
-        next(cur);
-        if (cur.s == 0 || k == n - 1) flush(done);
-        c0 = c1;
-        c1 = c2;
-        if constexpr (SCHEME == kScheme1x16) {
+    // Step k: stage and ring slot are fixed in the unrolled round, each register redefined
+    // after its last use, so no wait but for what is used next.
+    for (int k0 = 0; k0 < n; k0 += kR) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) e[q] = en[q];
+        for (int d = 0; d < kR; ++d) {
+            if (d > 0 && k0 + d >= n) break;
+            // the address arithmetic stays in the step (hoisted, it would hold 24 registers)
+            uint32_t xs = xlane + (uint32_t)(d * kXStage * 16);
+            asm volatile("" : "+v"(xs));
+            if constexpr (SCHEME == kScheme1x16) gather(ring[d], 1, e[1]);
+            load_x(px.v, (d + kR - 1) % kR);   // this stage was read last in step k - 1
+            advance(px);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(ring[d], e, ring[(d + 1) % kR], xs, G - cur.s * kKSlab - 8 * kq);
+            load_ring(ring[d]);
+            const Unit done = cur;
+            next(cur);
+            if (cur.s == 0 || k0 + d == n - 1) flush(done);
+            // x of step k + 1 has landed: this step issued kIssued loads after it
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kIssued < 16 ? kIssued : 15));
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
         }
-        stage = stage == 2 ? 0 : stage + 1;
-        // x of step k + 1 has landed (issued a step ago); at most this step's x loads are in flight
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kNX));
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));   // no LDS load in flight at exit
 }
@@ -274,13 +327,21 @@ __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) 
     for (int l = 0; l < N; ++l) sum[l] = f32x4{0.f, 0.f, 0.f, 0.f};
     const size_t step = (size_t)a.T * N * a.op;
     const float* p = a.partial + ((size_t)t * N) * a.op + r0;
-    for (int s = 0; s < parts; ++s, p += step)
+    constexpr int kAhead = 8;   // parts in flight
+    for (int s0 = 0; s0 < parts; s0 += kAhead, p += kAhead * step) {
+        f32x4 v[kAhead][N];
 #pragma unroll
-        for (int l = 0; l < N; ++l) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(p + (size_t)l * a.op);
+        for (int s = 0; s < kAhead; ++s)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sum[l][r] += v[r];
-        }
+            for (int l = 0; l < N; ++l)   // a part past the last repeats it and is not added
+                v[s][l] = *reinterpret_cast<const f32x4*>(p + (size_t)min(s, parts - 1 - s0) * step + (size_t)l * a.op);
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+            for (int l = 0; l < N; ++l)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum[l][r] += s0 + s < parts ? v[s][l][r] : 0.f;
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int row = r0 + r;
@@ -309,10 +370,10 @@ struct SkinnyPlan {
 SkinnyPlan skinny_plan(int n, int64_t out, int64_t in, int64_t batch) {
     SkinnyPlan p;
     const int64_t bm = batch <= 32 ? 32 : 64, tile = n == 2 ? 8 : 16;
-    const int64_t n_slab = (in / kGroup + kKSlab - 1) / kKSlab, n_blk = (out + kKWaves * tile - 1) / (kKWaves * tile);
+    const int64_t n_slab = (in / kGroup + kKSlab - 1) / kKSlab, n_blk = (out + kKTiles * tile - 1) / (kKTiles * tile);
     const int64_t units = (batch + bm - 1) / bm * n_blk * n_slab;
     p.bm = (int)bm;
-    p.blk_rows = (int)(kKWaves * tile);
+    p.blk_rows = (int)(kKTiles * tile);
     p.op = (int)((out + tile - 1) / tile * tile);
     p.n_slab = (int)n_slab;
     p.n_blk = (int)n_blk;
@@ -323,21 +384,31 @@ SkinnyPlan skinny_plan(int n, int64_t out, int64_t in, int64_t batch) {
     return p;
 }
 
-template <int SCHEME, int BM, bool GATED>
+template <int SCHEME, int BM, bool GATED, int RT, bool SUM>
 hipError_t launch_main(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t stream) {
-    auto kern = skinny_kernel<SCHEME, BM, GATED>;
-    const size_t lds = (SCHEME == kScheme2x8 ? kKCbBytes : 0) + (size_t)kKStages * BM * kKSlab * 16;
-    static_assert((SCHEME == kScheme2x8 ? kKCbBytes : 0) + kKStages * BM * kKSlab * 16 <= 163840, "LDS budget");
+    auto kern = a.G % kKSlab == 0 ? skinny_kernel<SCHEME, BM, GATED, kRowWhole, RT, SUM>
+                : a.G % 8 == 0    ? skinny_kernel<SCHEME, BM, GATED, kRowVec, RT, SUM>
+                                  : skinny_kernel<SCHEME, BM, GATED, kRowAny, RT, SUM>;
+    constexpr size_t lds = (SCHEME == kScheme2x8 ? kKCbBytes : 0) + (size_t)kKStages * BM * kKSlab * 16;
+    static_assert(lds <= 163840, "LDS budget");
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(p.W), dim3(kKThreads), lds, stream, a);
+    hipLaunchKernelGGL(kern, dim3(p.W), dim3(64 * kKTiles / RT), lds, stream, a);
     return hipGetLastError();
 }
 
-template <int SCHEME>
-hipError_t launch_scheme(int n, const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t stream) {
-    if (p.bm == 32) return n == 2 ? launch_main<SCHEME, 32, true>(p, a, stream) : launch_main<SCHEME, 32, false>(p, a, stream);
-    return n == 2 ? launch_main<SCHEME, 64, true>(p, a, stream) : launch_main<SCHEME, 64, false>(p, a, stream);
+// Up to 32 tokens: one row tile a wave.  Above, the matrix cores and the LDS reads of x weigh
+// more than the lookups: two row tiles a wave read x half as often (gated 8192x28672 at 512
+// tokens 825 -> 786 us).  Above 64 tokens 2x8 adds its codewords in fp16 and multiplies
+// once: half the products (606 us) for one rounding a weight, which decoded
+// weights have too; up to 64, where it would gain 4-20 %, both are multiplied and no weight is rounded.
+template <int SCHEME, bool GATED>
+hipError_t launch_scheme(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t stream) {
+    if (p.bm == 32) return launch_main<SCHEME, 32, GATED, 1, false>(p, a, stream);
+    if constexpr (SCHEME == kScheme2x8) {
+        if (a.T > 64) return launch_main<SCHEME, 64, GATED, 2, true>(p, a, stream);
+    }
+    return launch_main<SCHEME, 64, GATED, 2, false>(p, a, stream);
 }
 
 }  // namespace
@@ -382,8 +453,9 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
     f.bm = p.bm;
     f.blk_rows = p.blk_rows;
     f.W = p.W;
-    const hipError_t e = sc.B == 8 ? launch_scheme<kScheme2x8>(L.n, p, a, stream)
-                                   : launch_scheme<kScheme1x16>(L.n, p, a, stream);
+    const bool two = sc.B == 8, gated = L.n == 2;
+    const hipError_t e = two ? (gated ? launch_scheme<kScheme2x8, true>(p, a, stream) : launch_scheme<kScheme2x8, false>(p, a, stream))
+                             : (gated ? launch_scheme<kScheme1x16, true>(p, a, stream) : launch_scheme<kScheme1x16, false>(p, a, stream));
     if (e != hipSuccess) return e;
     const int64_t threads = batch * (p.op / 4);
     const dim3 grid((unsigned)((threads + 255) / 256));
