@@ -42,7 +42,7 @@ struct Parts {
 };
 
 struct ForwardPlan {
-    int64_t kp = 0, w[2] = {0, 0}, xp = 0, bytes = 0;
+    int64_t kp = 0, w[2] = {0, 0}, xp = 0, partial = 0, bytes = 0;
     bool pad = false, skinny = false;
 };
 
@@ -60,12 +60,13 @@ ForwardPlan forward_plan(int n, const GenericScheme& sc, int64_t out, int64_t in
     }
     for (int l = 0; l < n; ++l) p.w[l] = parts.add(out, p.kp, 2);
     if (p.pad) p.xp = parts.add(batch, p.kp, 2);
+    p.partial = parts.add(dense_partial_bytes(n, out, p.kp, batch), 1, 1);
     p.bytes = parts.total;
     return p;
 }
 
 struct BackwardPlan {
-    int64_t op = 0, wt = 0, dz = 0, partial = 0, bytes = 0;
+    int64_t op = 0, wt = 0, dz = 0, partial = 0, parts = 0, bytes = 0;
     bool grad = false;   // a pass over dy writes dz (else dy itself is the product's operand)
 };
 
@@ -77,6 +78,7 @@ BackwardPlan backward_plan(int n, int act, int64_t out, int64_t in, int64_t batc
     p.wt = parts.add(in, n * p.op, 2);
     p.dz = parts.add(batch, n * p.op, 2);
     p.partial = parts.add(grad_chunks(batch), n * out, 4);
+    p.parts = parts.add(dense_partial_bytes(1, in, n * p.op, batch), 1, 1);
     p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
     return p;
 }
@@ -84,7 +86,7 @@ BackwardPlan backward_plan(int n, int act, int64_t out, int64_t in, int64_t batc
 bool act_ok(int act) { return act >= AQLM_ACT_NONE && act <= AQLM_ACT_GELU_TANH; }
 
 // Scheme and sizes of the calls of this file, apart from any pointer.
-int check_sizes(int n, int act, int M, int B, int g, int64_t out, int64_t in, int64_t batch) {
+int check_sizes(int act, int M, int B, int g, int64_t out, int64_t in, int64_t batch) {
     if (!generic_scheme_ok(M, B, g)) return AQLM_ERR_SCHEME;
     if (!act_ok(act)) return AQLM_ERR_ACT;
     if (in < 1 || in > AQLM_MAX_IN || in % g != 0) return AQLM_ERR_SHAPE;
@@ -95,8 +97,6 @@ int check_sizes(int n, int act, int M, int B, int g, int64_t out, int64_t in, in
         return AQLM_ERR_SHAPE;
     const int64_t bt = (batch + 255) / 256, wide = op > kp ? op : kp;
     if ((wide / 64 + 8) * bt > INT32_MAX / 2 || grad_chunks(batch) * (op / 512 + 1) > INT32_MAX) return AQLM_ERR_SHAPE;
-    if (forward_plan(n, GenericScheme{M, B, g}, out, in, batch).bytes < 0 || backward_plan(n, act, out, in, batch).bytes < 0)
-        return AQLM_ERR_SHAPE;
     return AQLM_OK;
 }
 
@@ -109,6 +109,7 @@ int check_layers(const ActLayers& L) {
 }
 
 int check_workspace(const void* workspace, int64_t have, int64_t need) {
+    if (need < 0) return AQLM_ERR_SHAPE;   // more than int64 counts
     if (need == 0) return AQLM_OK;
     if (!workspace) return AQLM_ERR_NULL;
     if (!aligned(workspace, 16)) return AQLM_ERR_ALIGN;
@@ -121,7 +122,7 @@ T entry(T const* a, int l) { return a ? a[l] : nullptr; }
 
 int forward(const ActLayers& L, const void* x, const Epilogue& epi, void* workspace, int64_t workspace_bytes, int M,
             int B, int g, int64_t out, int64_t in, int64_t batch, void* stream) {
-    const int st = check_sizes(L.n, epi.act, M, B, g, out, in, batch);
+    const int st = check_sizes(epi.act, M, B, g, out, in, batch);
     if (st != AQLM_OK) return st;
     if (out == 0 || batch == 0) return AQLM_OK;
     const int lt = check_layers(L);
@@ -148,14 +149,14 @@ int forward(const ActLayers& L, const void* x, const Epilogue& epi, void* worksp
         if (r != AQLM_OK) return r;
         x = base + p.xp;
     }
-    return finish(launch_gemm_dense_act(x, w, ws == WeightScale::kNone ? L.scales : nullptr, L.n, epi, out, p.kp, batch,
-                                        s));
+    return finish(launch_gemm_dense_act(x, w, ws == WeightScale::kNone ? L.scales : nullptr, L.n, epi, base + p.partial, out,
+                                        p.kp, batch, s));
 }
 
 int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx, void* const* dbias, int act,
              void* workspace, int64_t workspace_bytes, int M, int B, int g, int64_t out, int64_t in, int64_t batch,
              void* stream) {
-    const int st = check_sizes(L.n, act, M, B, g, out, in, batch);
+    const int st = check_sizes(act, M, B, g, out, in, batch);
     if (st != AQLM_OK) return st;
     const bool want_bias = dbias[0] != nullptr;
     if (L.n > 1 && (dbias[1] != nullptr) != want_bias) return AQLM_ERR_NULL;   // both sums or none
@@ -194,7 +195,10 @@ int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx,
     }
     const int r = finish(launch_decode_transposed(GenericScheme{M, B, g}, L, ws, base + p.wt, out, in, p.op, s));
     if (r != AQLM_OK) return r;
-    return finish(launch_gemm_dense(p.grad ? base + p.dz : dy, base + p.wt, dx, in, L.n * p.op, batch, s));
+    const void* wt16 = base + p.wt;
+    const Epilogue plain = {{nullptr, nullptr}, nullptr, {nullptr, nullptr}, dx, kActNone};
+    return finish(launch_gemm_dense_act(p.grad ? base + p.dz : dy, &wt16, nullptr, 1, plain, base + p.parts, in,
+                                        L.n * p.op, batch, s));
 }
 
 // The slice-list product of n layers at batch 1.
@@ -233,9 +237,12 @@ int lists_forward(int n, const void* const* tables, const void* const* entries, 
 
 int workspace_bytes_of(int n, bool back, int M, int B, int g, int64_t out, int64_t in, int64_t batch, int64_t* bytes) {
     if (!bytes) return AQLM_ERR_NULL;
-    const int st = check_sizes(n, AQLM_ACT_RELU, M, B, g, out, in, batch);
+    const int st = check_sizes(AQLM_ACT_RELU, M, B, g, out, in, batch);
     if (st != AQLM_OK) return st;
-    *bytes = back ? backward_plan(n, AQLM_ACT_RELU, out, in, batch).bytes : forward_plan(n, GenericScheme{M, B, g}, out, in, batch).bytes;
+    const int64_t need = back ? backward_plan(n, AQLM_ACT_RELU, out, in, batch).bytes
+                              : forward_plan(n, GenericScheme{M, B, g}, out, in, batch).bytes;
+    if (need < 0) return AQLM_ERR_SHAPE;
+    *bytes = need;
     return AQLM_OK;
 }
 

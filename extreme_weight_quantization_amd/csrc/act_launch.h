@@ -45,9 +45,17 @@ hipError_t launch_pad_rows(const void* x, void* xp, int64_t batch, int64_t in, i
 hipError_t launch_zero16(void* p, int64_t n, hipStream_t stream);
 
 // The dense product of gemm_dense.hip on fp16 weights w[l] [out][kp] with an epilogue:
-// z_l = scales[l] (x w_l^T) + bias_l (scales NULL: 1).
+// z_l = scales[l] (x w_l^T) + bias_l (scales NULL: 1).  partial: dense_partial_bytes bytes,
+// for shapes whose k steps are split over workgroups (0: not used).
+int64_t dense_partial_bytes(int n, int64_t out, int64_t kp, int64_t batch);
 hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void* const* scales, int n,
-                                 const Epilogue& epi, int64_t out, int64_t kp, int64_t batch, hipStream_t stream);
+                                 const Epilogue& epi, void* partial, int64_t out, int64_t kp, int64_t batch,
+                                 hipStream_t stream);
+
+// y from fp32 parts of the products, [part][token][layer][op]: the parts added in order,
+// then scales (NULL: 1) and the epilogue.
+hipError_t launch_finish(int n, const float* partial, const void* const* scales, const Epilogue& epi, int64_t out,
+                         int64_t op, int64_t batch, int parts, hipStream_t stream);
 
 // Gradients of the pre-activations, fp16, as the dense product's x: dz[t][l * op + i] for
 // i < op (rows past `out` zero).  One layer: dy act'(z); two: dy zu act'(zg) and dy act(zg).

@@ -52,6 +52,12 @@
 //   gated        the 128 rows of a tile are 64 outputs of two layers, 16 rows of the gate
 //                and 16 of the up projection in turn, so one wave holds both products of
 //                an output: y = act(zg) zu.
+// MODE kDensePart / kDenseGatedPart: the k steps of a tile are split over `splits` workgroups,
+// where the tiles alone leave CUs idle; each writes its fp32 part of the product, and
+// skinny_finish_kernel (skinny.hip) adds the parts in order and runs the epilogue.  Work items
+// are ordered split by split, so the items of an XCD share one range of k of x and W.
+// BM: tokens of a tile, 256 next to 128 rows, or 128 next to 256 rows for batches that would
+// leave half of the first kind empty.
 // A wave passes its fp32 tile through LDS (64 rows of 64 + 4 floats: the writes of the four
 // lane quarters, 4 rows apart, then hit distinct banks) and finishes 8 outputs a lane,
 // with 16-byte accesses to y, z and the residual; everything up to the one rounding
@@ -65,16 +71,13 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kDenseBM = 256;                // tokens per tile
+constexpr int kDenseBM = 256;                // tokens per tile (BM = 256; or 128 x 256)
 constexpr int kDenseBN = 128;                // output rows per tile
 constexpr int kDenseWaves = 8;                // consumer waves: the products
 constexpr int kDenseLoaders = 4;              // loader waves: the global-to-LDS copies
 constexpr int kDenseThreads = 64 * (kDenseWaves + kDenseLoaders);
-constexpr int kDenseXStage = kDenseBM * 8;   // 16-byte slots of one X stage (a whole 64-input step)
-constexpr int kDenseWStage = kDenseBN * 8;   // 16-byte slots of one W stage
 constexpr int kDenseStages = 3;
-constexpr int kDenseWOff = kDenseStages * kDenseXStage;
-constexpr size_t kDenseLds = (size_t)(kDenseWOff + kDenseStages * kDenseWStage) * 16;
+constexpr size_t kDenseLds = (size_t)kDenseStages * (kDenseBM + kDenseBN) * 8 * 16;
 static_assert(kDenseLds <= 163840, "LDS budget");
 constexpr int kXcds = 8;                     // tile order only; any count gives correct results
 
@@ -93,7 +96,9 @@ __device__ __forceinline__ void step_barrier() {
     asm volatile("" ::: "memory");
 }
 
-enum DenseMode : int { kDensePlain = 0, kDenseAct = 1, kDenseGated = 2 };
+enum DenseMode : int { kDensePlain = 0, kDenseAct = 1, kDenseGated = 2, kDensePart = 3, kDenseGatedPart = 4 };
+constexpr bool dense_gated(int mode) { return mode == kDenseGated || mode == kDenseGatedPart; }
+constexpr bool dense_part(int mode) { return mode == kDensePart || mode == kDenseGatedPart; }
 
 // What the modes with an epilogue take next to the product's arguments.
 struct DenseEpi {
@@ -103,6 +108,8 @@ struct DenseEpi {
     const f16* residual;
     f16* z[2];
     int act;
+    float* partial;         // parts: [split][token][layer][op]
+    int splits, op;
 };
 constexpr int kEpiRow = 68;   // floats per row of a wave's fp32 tile in LDS
 static_assert((size_t)kDenseWaves * 64 * kEpiRow * sizeof(float) <= kDenseLds, "epilogue tiles");
@@ -136,7 +143,7 @@ __device__ __forceinline__ void epi_store8(f16* p, int left, bool vec, const flo
 // of its 64x64 piece.  tok0: its first token; col0: its first output.
 template <int MODE>
 __device__ __forceinline__ void dense_epilogue(const f32x4 (&acc)[4][4], float* tile, int lane, int tok0, int col0,
-                                               f16* y, int out, int T, const DenseEpi& e) {
+                                               f16* y, int out, int T, const DenseEpi& e, int split) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -148,12 +155,28 @@ __device__ __forceinline__ void dense_epilogue(const f32x4 (&acc)[4][4], float* 
     const bool vec = out % 8 == 0;
     // one layer: 8 lanes of 8 outputs a row; gated: 4 lanes of 8 outputs a row, the gate's in
     // columns 32 (c / 2) + 8 (c % 2) .. of the tile, the up projection's 16 further
-    constexpr int kLanes = MODE == kDenseGated ? 4 : 8;
+    constexpr bool kGated = dense_gated(MODE);
+    constexpr int kLanes = kGated ? 4 : 8;
     const int c = lane % kLanes;
-    const int at = MODE == kDenseGated ? 32 * (c >> 1) + 8 * (c & 1) : 8 * c;
+    const int at = kGated ? 32 * (c >> 1) + 8 * (c & 1) : 8 * c;
     const int col = col0 + 8 * c, left = out - col;
     if (left <= 0) return;
-    constexpr int kN = MODE == kDenseGated ? 2 : 1;
+    constexpr int kN = kGated ? 2 : 1;
+    if constexpr (dense_part(MODE)) {   // rows of op % 8 == 0 floats: whole chunks
+#pragma unroll
+        for (int it = 0; it < kLanes; ++it) {
+            const int rr = it * (64 / kLanes) + lane / kLanes, tok = tok0 + rr;
+            if (tok >= T) continue;
+#pragma unroll
+            for (int l = 0; l < kN; ++l) {
+                const f32x4* src = reinterpret_cast<const f32x4*>(tile + rr * kEpiRow + at + 16 * l);
+                f32x4* dst = reinterpret_cast<f32x4*>(e.partial + (((size_t)split * T + tok) * kN + l) * e.op + col);
+                dst[0] = src[0];
+                dst[1] = src[1];
+            }
+        }
+        return;
+    }
     float s[kN][8], b[kN][8];
 #pragma unroll
     for (int l = 0; l < kN; ++l)
@@ -193,34 +216,41 @@ __device__ __forceinline__ void dense_epilogue(const f32x4 (&acc)[4][4], float* 
 
 // y carries no __restrict__: the residual may be y itself, each element read by the lane
 // that then writes it.
-template <int MODE>
+template <int MODE, int BM>
 __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __restrict__ x,
                                                                    const f16* __restrict__ w, f16* y,
                                                                    int out, int in, int T, int n_tt, int n_tiles,
                                                                    int per_xcd, DenseEpi epi) {
-    constexpr int kCols = MODE == kDenseGated ? kDenseBN / 2 : kDenseBN;   // outputs per tile
+    constexpr int BN = kDenseBM + kDenseBN - BM;                 // W rows of a tile
+    constexpr int kCols = dense_gated(MODE) ? BN / 2 : BN;       // outputs per tile
+    constexpr int kXStage = BM * 8, kWStage = BN * 8;            // 16-byte slots of a stage (a whole 64-input step)
+    constexpr int kWOff = kDenseStages * kXStage;
     extern __shared__ u32x4 smem[];
-    u32x4* Xs = smem;                 // [stage 3][kDenseXStage]
-    u32x4* Ws = smem + kDenseWOff;    // [stage 3][kDenseWStage]
-    const int tile = (int)(blockIdx.x % kXcds) * per_xcd + (int)(blockIdx.x / kXcds);
-    if (tile >= n_tiles) return;      // the whole workgroup: the grid is rounded up to kXcds * per_xcd
+    u32x4* Xs = smem;            // [stage 3][kXStage]
+    u32x4* Ws = smem + kWOff;    // [stage 3][kWStage]
+    const int item = (int)(blockIdx.x % kXcds) * per_xcd + (int)(blockIdx.x / kXcds);
+    const int splits = dense_part(MODE) ? epi.splits : 1;
+    if (item >= n_tiles * splits) return;   // the whole workgroup: the grid is rounded up to kXcds * per_xcd
+    const int split = dense_part(MODE) ? item / n_tiles : 0, tile = dense_part(MODE) ? item % n_tiles : item;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int lw = wave - kDenseWaves;   // loader index (loader waves only)
     const int n0 = (tile / n_tt) * kCols;
-    const int t0 = (tile % n_tt) * kDenseBM;
-    const int n_k = in / 64;          // the launcher guarantees in % 64 == 0
+    const int t0 = (tile % n_tt) * BM;
+    const int n_all = in / 64;        // the launcher guarantees in % 64 == 0
+    const int k_at = dense_part(MODE) ? (int)((int64_t)split * n_all / splits) : 0;   // first step of this part
+    const int n_k = dense_part(MODE) ? (int)((int64_t)(split + 1) * n_all / splits) - k_at : n_all;
 
     // The tiles of step j into stage j % 3.  Load q writes slots 64 q .. 64 q + 63:
     // lane l fills slot 64 q + l, which holds chunk (l % 8) ^ ((r >> 1) & 7) of row
     // r = 8 q + l / 8, so the 8 lanes of a row read its whole 128-byte line.
     const int rsub = lane >> 3;
     auto load_step = [&](int j) {
-        const int jc = min(j, n_k - 1);
-        u32x4* dx = Xs + (j % kDenseStages) * kDenseXStage;
-        u32x4* dw = Ws + (j % kDenseStages) * kDenseWStage;
+        const int jc = k_at + min(j, n_k - 1);
+        u32x4* dx = Xs + (j % kDenseStages) * kXStage;
+        u32x4* dw = Ws + (j % kDenseStages) * kWStage;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int q = 8 * lw + i;
+        for (int i = 0; i < BM / 32; ++i) {
+            const int q = (BM / 32) * lw + i;
             const int r = 8 * q + rsub;
             const int c = (lane & 7) ^ ((r >> 1) & 7);
             const int tok = min(t0 + r, T - 1);
@@ -228,13 +258,13 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
                                              lds_ptr(dx + 64 * q), 16, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int q = 4 * lw + i;
+        for (int i = 0; i < BN / 32; ++i) {
+            const int q = (BN / 32) * lw + i;
             const int r = 8 * q + rsub;
             const int c = (lane & 7) ^ ((r >> 1) & 7);
             const f16* wl = w;
             int row = min(n0 + r, out - 1);
-            if constexpr (MODE == kDenseGated) {   // rows 32 m .. + 15: the gate's outputs 16 m ..; + 16: the up's
+            if constexpr (dense_gated(MODE)) {   // rows 32 m .. + 15: the gate's outputs 16 m ..; + 16: the up's
                 wl = ((r >> 4) & 1) ? epi.w1 : w;
                 row = min(n0 + 16 * (r >> 5) + (r & 15), out - 1);
             }
@@ -243,7 +273,8 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
         }
     };
 
-    const int wm = wave >> 1, wn = wave & 1;
+    constexpr int kWN = BN / 64;      // consumer waves across the rows
+    const int wm = wave / kWN, wn = wave % kWN;
     f32x4 acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -251,8 +282,8 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     // fragments of half h of step j: lane l holds A[l%16][8(l/16)..] and B[8(l/16)..][l%16]
     auto read_frags = [&](int j, int h, f16x8 (&a)[4], f16x8 (&b)[4]) {
-        const u32x4* xb = Xs + (j % kDenseStages) * kDenseXStage;
-        const u32x4* wb = Ws + (j % kDenseStages) * kDenseWStage;
+        const u32x4* xb = Xs + (j % kDenseStages) * kXStage;
+        const u32x4* wb = Ws + (j % kDenseStages) * kWStage;
         const int cc = 4 * h + (lane >> 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = as_f16x8(xb[stage_slot(wm * 64 + i * 16 + (lane & 15), cc)]);
@@ -323,7 +354,7 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         dense_epilogue<MODE>(acc, reinterpret_cast<float*>(smem) + wave * 64 * kEpiRow, lane, t0 + wm * 64,
-                             n0 + wn * (kCols / 2), y, out, T, epi);
+                             n0 + wn * (kCols / kWN), y, out, T, epi, split);
         return;
     }
     if (out % 8 == 0) {
@@ -376,35 +407,74 @@ __global__ __launch_bounds__(kDenseThreads) void gemm_dense_kernel(const f16* __
     }
 }
 
-// Tiles of `cols` outputs x kDenseBM tokens, dealt to the XCDs in contiguous runs.
-template <int MODE>
+// Tiles of BM tokens, dealt to the XCDs in contiguous runs.
+template <int MODE, int BM>
 hipError_t launch_dense(const void* x, const void* w16, void* y, int64_t out, int64_t in, int64_t batch,
                         const DenseEpi& epi, hipStream_t stream) {
     if (in % 64 != 0) return hipErrorInvalidValue;
     if (out == 0 || batch == 0) return hipSuccess;
-    const hipError_t e = hipFuncSetAttribute((const void*)gemm_dense_kernel<MODE>,
+    const hipError_t e = hipFuncSetAttribute((const void*)gemm_dense_kernel<MODE, BM>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)kDenseLds);
     if (e != hipSuccess) return e;
-    constexpr int kCols = MODE == kDenseGated ? kDenseBN / 2 : kDenseBN;
-    const int64_t n_tt = (batch + kDenseBM - 1) / kDenseBM;
+    constexpr int BN = kDenseBM + kDenseBN - BM, kCols = dense_gated(MODE) ? BN / 2 : BN;
+    const int64_t n_tt = (batch + BM - 1) / BM;
     const int64_t n_tiles = ((out + kCols - 1) / kCols) * n_tt;
-    const int64_t per = (n_tiles + kXcds - 1) / kXcds;
+    const int64_t per = (n_tiles * (dense_part(MODE) ? epi.splits : 1) + kXcds - 1) / kXcds;
     if (per * kXcds > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(gemm_dense_kernel<MODE>, dim3((unsigned)(per * kXcds)), dim3(kDenseThreads), kDenseLds, stream,
-                       (const f16*)x, (const f16*)w16, (f16*)y, (int)out, (int)in, (int)batch, (int)n_tt,
+    hipLaunchKernelGGL((gemm_dense_kernel<MODE, BM>), dim3((unsigned)(per * kXcds)), dim3(kDenseThreads), kDenseLds,
+                       stream, (const f16*)x, (const f16*)w16, (f16*)y, (int)out, (int)in, (int)batch, (int)n_tt,
                        (int)n_tiles, (int)per, epi);
     return hipGetLastError();
+}
+
+// How the product of n layers is tiled: tokens of a tile, and the workgroups that share a
+// tile's k steps.  A whole launch of tiles runs in rounds of kDenseCus workgroups, each as
+// long as its k steps; the split that takes the fewest microseconds by this count is
+// taken, with kStepUs for a step, kRoundUs to fill and drain a round's pipeline, and kPartBytesUs to write and
+// add the parts (a plain launch has none, and stores y itself).
+struct DensePlan {
+    int bm, splits;
+};
+constexpr int kDenseCus = 256;
+constexpr double kStepUs = 0.85, kRoundUs = 3.0, kFinishUs = 3.0, kPartBytesUs = 2.5e6;
+
+DensePlan dense_plan(int n, int64_t out, int64_t in, int64_t batch) {
+    DensePlan best = {kDenseBM, 1};
+    double best_us = 1e300;
+    const int64_t n_k = in / 64;
+    for (int bm = 128; bm <= 256; bm += 128) {
+        if (bm == 128 && batch > 1024) continue;
+        const int64_t cols = (kDenseBM + kDenseBN - bm) / n;
+        const int64_t tiles = (out + cols - 1) / cols * ((batch + bm - 1) / bm);
+        for (int s = 1; s <= 32 && s <= n_k; ++s) {
+            const int64_t rounds = (tiles * s + kDenseCus - 1) / kDenseCus, steps = (n_k + s - 1) / s;
+            double us = (double)rounds * ((double)steps * kStepUs + kRoundUs);
+            if (s > 1) us += kFinishUs + (double)s * batch * n * out * 8 / kPartBytesUs;
+            if (us < best_us) {
+                best_us = us;
+                best = {bm, s};
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
 hipError_t launch_gemm_dense(const void* x, const void* w16, void* y, int64_t out, int64_t in, int64_t batch,
                              hipStream_t stream) {
-    return launch_dense<kDensePlain>(x, w16, y, out, in, batch, DenseEpi{}, stream);
+    return launch_dense<kDensePlain, kDenseBM>(x, w16, y, out, in, batch, DenseEpi{}, stream);
+}
+
+int64_t dense_partial_bytes(int n, int64_t out, int64_t kp, int64_t batch) {
+    const DensePlan p = dense_plan(n, out, kp, batch);
+    return p.splits == 1 ? 0 : (int64_t)p.splits * batch * n * ((out + 7) / 8 * 8) * 4;
 }
 
 hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void* const* scales, int n,
-                                 const Epilogue& epi, int64_t out, int64_t kp, int64_t batch, hipStream_t stream) {
+                                 const Epilogue& epi, void* partial, int64_t out, int64_t kp, int64_t batch,
+                                 hipStream_t stream) {
+    const DensePlan p = dense_plan(n, out, kp, batch);
     DenseEpi e = {};
     for (int l = 0; l < n; ++l) {
         e.scales[l] = scales ? static_cast<const f16*>(scales[l]) : nullptr;
@@ -413,9 +483,26 @@ hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void
     }
     e.residual = static_cast<const f16*>(epi.residual);
     e.act = epi.act;
-    if (n == 1) return launch_dense<kDenseAct>(x, w[0], epi.y, out, kp, batch, e, stream);
-    e.w1 = static_cast<const f16*>(w[1]);
-    return launch_dense<kDenseGated>(x, w[0], epi.y, out, kp, batch, e, stream);
+    e.w1 = n == 2 ? static_cast<const f16*>(w[1]) : nullptr;
+    e.partial = static_cast<float*>(partial);
+    e.splits = p.splits;
+    e.op = (int)((out + 7) / 8 * 8);
+    if (p.splits == 1) {
+        if (n == 2)
+            return p.bm == 128 ? launch_dense<kDenseGated, 128>(x, w[0], epi.y, out, kp, batch, e, stream)
+                               : launch_dense<kDenseGated, 256>(x, w[0], epi.y, out, kp, batch, e, stream);
+        return p.bm == 128 ? launch_dense<kDenseAct, 128>(x, w[0], epi.y, out, kp, batch, e, stream)
+                           : launch_dense<kDenseAct, 256>(x, w[0], epi.y, out, kp, batch, e, stream);
+    }
+    hipError_t r;
+    if (n == 2)
+        r = p.bm == 128 ? launch_dense<kDenseGatedPart, 128>(x, w[0], nullptr, out, kp, batch, e, stream)
+                        : launch_dense<kDenseGatedPart, 256>(x, w[0], nullptr, out, kp, batch, e, stream);
+    else
+        r = p.bm == 128 ? launch_dense<kDensePart, 128>(x, w[0], nullptr, out, kp, batch, e, stream)
+                        : launch_dense<kDensePart, 256>(x, w[0], nullptr, out, kp, batch, e, stream);
+    if (r != hipSuccess) return r;
+    return launch_finish(n, e.partial, scales, epi, out, e.op, batch, p.splits, stream);
 }
 
 }  // namespace aqlm

@@ -309,7 +309,7 @@ struct FinishArgs {
     f16* z[2];
     f16* y;
     int out, op, T, act;
-    int bm, blk_rows, n_slab, n_blk, units, W;
+    int bm, blk_rows, n_slab, n_blk, units, W;   // units 0: W parts everywhere
 };
 
 // Thread: 4 outputs of a token.  The parts of its row block are the runs from the one that
@@ -320,8 +320,11 @@ __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) 
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)a.T * per) return;
     const int t = (int)(i / per), r0 = 4 * (int)(i - (int64_t)t * per);
-    const int blk = (t / a.bm) * a.n_blk + r0 / a.blk_rows;
-    const int parts = run_of((blk + 1) * a.n_slab - 1, a.W, a.units) - run_of(blk * a.n_slab, a.W, a.units) + 1;
+    int parts = a.W;
+    if (a.units > 0) {
+        const int blk = (t / a.bm) * a.n_blk + r0 / a.blk_rows;
+        parts = run_of((blk + 1) * a.n_slab - 1, a.W, a.units) - run_of(blk * a.n_slab, a.W, a.units) + 1;
+    }
     f32x4 sum[N];
 #pragma unroll
     for (int l = 0; l < N; ++l) sum[l] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -350,7 +353,7 @@ __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) 
         float v = 0.f;
 #pragma unroll
         for (int l = 0; l < N; ++l) {
-            float z = sum[l][r] * (float)a.scales[l][row];
+            float z = a.scales[l] != nullptr ? sum[l][r] * (float)a.scales[l][row] : sum[l][r];
             if (a.bias[l] != nullptr) z += (float)a.bias[l][row];
             if (a.z[l] != nullptr) a.z[l][at] = (f16)z;
             v = l == 0 ? act_value(a.act, z) : v * z;
@@ -358,6 +361,32 @@ __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) 
         if (a.residual != nullptr) v += (float)a.residual[at];
         a.y[at] = (f16)v;
     }
+}
+
+FinishArgs finish_args(int n, const float* partial, const void* const* scales, const Epilogue& epi, int64_t out,
+                       int64_t op, int64_t batch) {
+    FinishArgs f = {};
+    for (int l = 0; l < n; ++l) {
+        f.scales[l] = scales ? static_cast<const f16*>(scales[l]) : nullptr;
+        f.bias[l] = static_cast<const f16*>(epi.bias[l]);
+        f.z[l] = static_cast<f16*>(epi.z[l]);
+    }
+    f.partial = partial;
+    f.residual = static_cast<const f16*>(epi.residual);
+    f.y = static_cast<f16*>(epi.y);
+    f.out = (int)out;
+    f.op = (int)op;
+    f.T = (int)batch;
+    f.act = epi.act;
+    return f;
+}
+
+hipError_t launch_finish_args(int n, const FinishArgs& f, hipStream_t stream) {
+    const int64_t threads = (int64_t)f.T * (f.op / 4), blocks = (threads + 255) / 256;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (n == 2) hipLaunchKernelGGL(skinny_finish_kernel<2>, dim3((unsigned)blocks), dim3(256), 0, stream, f);
+    else hipLaunchKernelGGL(skinny_finish_kernel<1>, dim3((unsigned)blocks), dim3(256), 0, stream, f);
+    return hipGetLastError();
 }
 
 // Geometry of one call.
@@ -430,26 +459,20 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
                          int64_t out, int64_t in, int64_t batch, hipStream_t stream) {
     const SkinnyPlan p = skinny_plan(L.n, out, in, batch);
     SkinnyArgs a = {};
-    FinishArgs f = {};
     for (int l = 0; l < L.n; ++l) {
         a.codes[l] = static_cast<const uint8_t*>(L.codes[l]);
         a.codebooks[l] = static_cast<const f16*>(L.codebooks[l]);
-        f.scales[l] = static_cast<const f16*>(L.scales[l]);
-        f.bias[l] = static_cast<const f16*>(epi.bias[l]);
-        f.z[l] = static_cast<f16*>(epi.z[l]);
     }
     a.x = static_cast<const f16*>(x);
-    f.partial = a.partial = static_cast<float*>(partial);
-    f.out = a.out = (int)out;
-    f.op = a.op = p.op;
+    a.partial = static_cast<float*>(partial);
+    a.out = (int)out;
+    a.op = p.op;
     a.G = (int)(in / kGroup);
-    f.T = a.T = (int)batch;
+    a.T = (int)batch;
+    FinishArgs f = finish_args(L.n, a.partial, L.scales, epi, out, p.op, batch);
     f.n_slab = a.n_slab = p.n_slab;
     f.n_blk = a.n_blk = p.n_blk;
     f.units = a.units = p.units;
-    f.residual = static_cast<const f16*>(epi.residual);
-    f.y = static_cast<f16*>(epi.y);
-    f.act = epi.act;
     f.bm = p.bm;
     f.blk_rows = p.blk_rows;
     f.W = p.W;
@@ -457,11 +480,14 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
     const hipError_t e = two ? (gated ? launch_scheme<kScheme2x8, true>(p, a, stream) : launch_scheme<kScheme2x8, false>(p, a, stream))
                              : (gated ? launch_scheme<kScheme1x16, true>(p, a, stream) : launch_scheme<kScheme1x16, false>(p, a, stream));
     if (e != hipSuccess) return e;
-    const int64_t threads = batch * (p.op / 4);
-    const dim3 grid((unsigned)((threads + 255) / 256));
-    if (L.n == 2) hipLaunchKernelGGL(skinny_finish_kernel<2>, grid, dim3(256), 0, stream, f);
-    else hipLaunchKernelGGL(skinny_finish_kernel<1>, grid, dim3(256), 0, stream, f);
-    return hipGetLastError();
+    return launch_finish_args(L.n, f, stream);
+}
+
+hipError_t launch_finish(int n, const float* partial, const void* const* scales, const Epilogue& epi, int64_t out,
+                         int64_t op, int64_t batch, int parts, hipStream_t stream) {
+    FinishArgs f = finish_args(n, partial, scales, epi, out, op, batch);
+    f.W = parts;
+    return launch_finish_args(n, f, stream);
 }
 
 }  // namespace aqlm
