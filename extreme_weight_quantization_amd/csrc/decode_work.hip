@@ -30,41 +30,73 @@ struct DecodeArgs {
     f16* w[2];
 };
 
-// The fp32 weights of inputs 8p .. 8p+7 of a row before the scale, zero past `in`.
-// kScheme2x8 reads the codebooks' LDS copy (slot 256 m + k), 1x16 gathers its codeword, any
-// other scheme (g = G, code storage CB as in code_at) reads the codebooks through L2.
+// 16-byte LDS slots of a scheme's codebooks: 2x8 codeword k of codebook m at 256 m + k; 4x8 g16
+// half h of it at 1024 h + 256 m + k; 1x8 g4 codeword k in 8-byte slot k.  1x16 codewords
+// are gathered from L2, those of any other scheme (kSchemeGeneric) read through it.
+template <int SCHEME>
+constexpr int work_cb_slots() {
+    return SCHEME == kScheme2x8 ? 2 * kCodewords2x8 : SCHEME == kSchemeB8M4 ? 8 * kCodewords2x8
+         : SCHEME == kSchemeB8M1 ? kCodewords2x8 / 2 : 1;
+}
+
+template <int SCHEME>
+__device__ __forceinline__ void stage_codebooks(u32x4* lds, const f16* __restrict__ codebooks) {
+    if constexpr (SCHEME == kScheme2x8 || SCHEME == kSchemeB8M1) {
+        for (int i = threadIdx.x; i < work_cb_slots<SCHEME>(); i += blockDim.x) lds[i] = load16(codebooks + (size_t)i * 8);
+    } else if constexpr (SCHEME == kSchemeB8M4) {
+        for (int i = threadIdx.x; i < work_cb_slots<SCHEME>(); i += blockDim.x)
+            lds[i] = load16(codebooks + (size_t)(i & 1023) * 16 + (i >> 10) * 8);
+    }
+    __syncthreads();
+}
+
+// The codes of piece p (inputs 8p .. 8p+7) of a row of P whole pieces, p clamped into it; 4x8
+// g16: those of its group.  Nothing for kSchemeGeneric.
+template <int SCHEME>
+__device__ __forceinline__ uint32_t piece_codes(const uint8_t* __restrict__ codes, uint32_t row, uint32_t p, uint32_t P) {
+    if constexpr (SCHEME == kSchemeGeneric) return 0u;
+    p = min(p, P - 1);
+    if constexpr (SCHEME == kSchemeB8M4)
+        return reinterpret_cast<const uint32_t*>(codes)[(size_t)row * (P / 2) + (p >> 1)];
+    return reinterpret_cast<const uint16_t*>(codes)[(size_t)row * P + p];
+}
+
+// The fp32 weights of piece p of a row before the scale, zero past `in`, from its codes c
+// (kSchemeGeneric, g = G, code storage CB: read here).
 template <int SCHEME, int G, int CB>
-__device__ __forceinline__ void piece_weights(const uint8_t* __restrict__ codes, const f16* __restrict__ codebooks,
-                                              const u32x4* cb_lds, uint32_t row, uint32_t p, int in, int M, int B,
-                                              float (&v)[8]) {
-    if constexpr (SCHEME == kScheme2x8 || SCHEME == kScheme1x16) {
-        const uint32_t n_grp = (uint32_t)in / kGroup;
-        if (p >= n_grp) {
+__device__ __forceinline__ void piece_weights(uint32_t c, const uint8_t* __restrict__ codes,
+                                              const f16* __restrict__ codebooks, const u32x4* lds, uint32_t row,
+                                              uint32_t p, int in, int M, int B, float (&v)[8]) {
+    if constexpr (SCHEME == kScheme2x8) {
+        const f16x8 a = as_f16x8(lds[c & 0xff]), b = as_f16x8(lds[kCodewords2x8 + (c >> 8)]);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) v[t] = 0.f;
-            return;
-        }
-        const uint32_t c = reinterpret_cast<const uint16_t*>(codes)[(size_t)row * n_grp + p];
-        if constexpr (SCHEME == kScheme2x8) {
-            const f16x8 a = as_f16x8(cb_lds[c & 0xff]), b = as_f16x8(cb_lds[kCodewords2x8 + (c >> 8)]);
+        for (int t = 0; t < 8; ++t) v[t] = __fadd_rn((float)a[t], (float)b[t]);
+    } else if constexpr (SCHEME == kScheme1x16) {
+        const f16x8 a = as_f16x8(load16(codebooks + (size_t)c * kGroup));
 #pragma unroll
-            for (int t = 0; t < 8; ++t) v[t] = __fadd_rn((float)a[t], (float)b[t]);
-        } else {
-            const f16x8 a = as_f16x8(load16(codebooks + (size_t)c * kGroup));
+        for (int t = 0; t < 8; ++t) v[t] = (float)a[t];
+    } else if constexpr (SCHEME == kSchemeB8M1) {
+        const u32x2* lds8 = reinterpret_cast<const u32x2*>(lds);
+        const u32x2 lo = lds8[c & 0xff], hi = lds8[c >> 8];
+        const f16x8 a = as_f16x8(u32x4{lo[0], lo[1], hi[0], hi[1]});
 #pragma unroll
-            for (int t = 0; t < 8; ++t) v[t] = (float)a[t];
-        }
+        for (int t = 0; t < 8; ++t) v[t] = (float)a[t];
+    } else if constexpr (SCHEME == kSchemeB8M4) {
+        const u32x4* half = lds + 1024 * (p & 1);
+        f16x8 a[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) a[m] = as_f16x8(half[256 * m + ((c >> (8 * m)) & 0xff)]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            v[t] = __fadd_rn(__fadd_rn(__fadd_rn((float)a[0][t], (float)a[1][t]), (float)a[2][t]), (float)a[3][t]);
     } else {
         const uint32_t mask = (1u << B) - 1u;
         const int n_grp = in / G, k = (int)p * 8;
         const size_t rbase = (size_t)row * n_grp;
-        if constexpr (G >= 8) {
-            if (k < in) {
-                sum_codewords<G, 8, CB>(codes, (rbase + k / G) * M, codebooks, M, B, mask, k % G, v);
-            } else {
 #pragma unroll
-                for (int t = 0; t < 8; ++t) v[t] = 0.f;
-            }
+        for (int t = 0; t < 8; ++t) v[t] = 0.f;
+        if constexpr (G >= 8) {
+            if (k < in) sum_codewords<G, 8, CB>(codes, (rbase + k / G) * M, codebooks, M, B, mask, k % G, v);
         } else {
 #pragma unroll
             for (int q = 0; q < 8 / G; ++q) {
@@ -76,6 +108,12 @@ __device__ __forceinline__ void piece_weights(const uint8_t* __restrict__ codes,
 #pragma unroll
                 for (int t = 0; t < G; ++t) v[q * G + t] = part[t];
             }
+        }
+    }
+    if constexpr (SCHEME != kSchemeGeneric) {
+        if ((int)p * 8 >= in) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t) v[t] = 0.f;
         }
     }
 }
@@ -91,72 +129,115 @@ __device__ __forceinline__ float row_factor(const f16* __restrict__ scales, uint
     return ldexpf(1.f, e);
 }
 
-// Layer 2x8: its codebooks into LDS (512 slots of 16 bytes).
-template <int SCHEME>
-__device__ __forceinline__ void stage_2x8(u32x4* cb_lds, const f16* __restrict__ codebooks) {
-    if constexpr (SCHEME == kScheme2x8) {
-        for (int i = threadIdx.x; i < 2 * kCodewords2x8; i += blockDim.x) cb_lds[i] = load16(codebooks + (size_t)i * kGroup);
-        __syncthreads();
-    }
-}
+// Pieces a thread has in hand at once: their codes are loaded before any is decoded, and a
+// gather or lookup waits for the others' (one at a time the kernel ran at the latency of
+// code, codeword and store in turn: 4096x11008 2x8 29.6 us).
+constexpr int kAhead = 4;
+constexpr int kRowThreads = 512;
 
 template <int SCHEME, int G, int CB, WeightScale WS>
-__global__ __launch_bounds__(256) void decode_rows_kernel(DecodeArgs a, uint32_t n_pieces, uint32_t per_row, int in,
-                                                          int M, int B) {
-    __shared__ u32x4 cb_lds[SCHEME == kScheme2x8 ? 2 * kCodewords2x8 : 1];
+__global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(DecodeArgs a, uint32_t n_pieces, uint32_t per_row,
+                                                                  int in, int M, int B) {
+    __shared__ u32x4 cb_lds[work_cb_slots<SCHEME>()];
     const int l = blockIdx.y;
     const uint8_t* codes = l ? a.codes[1] : a.codes[0];
     const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
     const f16* scales = l ? a.scales[1] : a.scales[0];
     f16* w = l ? a.w[1] : a.w[0];
-    stage_2x8<SCHEME>(cb_lds, codebooks);
-    // 64-bit loop index: n_pieces may come within a stride of 2^32
-    const uint64_t stride = (uint64_t)gridDim.x * blockDim.x;
-    for (uint64_t i64 = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i64 < n_pieces; i64 += stride) {
-        const uint32_t i = (uint32_t)i64, row = i / per_row, p = i - row * per_row;
-        float v[8];
-        piece_weights<SCHEME, G, CB>(codes, codebooks, cb_lds, row, p, in, M, B, v);
-        const float s = row_factor<WS>(scales, row);
-        f16x8 o;
+    stage_codebooks<SCHEME>(cb_lds, codebooks);
+    const uint32_t P = (uint32_t)in / 8;   // whole pieces of a row (the schemes but kSchemeGeneric: in % 8 == 0)
+    // 64-bit piece index: n_pieces may come within a stride of 2^32
+    const uint64_t stride = (uint64_t)gridDim.x * kRowThreads * kAhead;
+    for (uint64_t i0 = (uint64_t)blockIdx.x * kRowThreads * kAhead + threadIdx.x; i0 < n_pieces; i0 += stride) {
+        uint32_t row[kAhead], p[kAhead], c[kAhead];
+        float s[kAhead];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) o[t] = (f16)__fmul_rn(v[t], s);
-        // non-temporal: the write stream must not evict the codebook or the codes from L2
-        __builtin_nontemporal_store(as_u32x4(o), reinterpret_cast<u32x4*>(w + (size_t)i * 8));
+        for (int k = 0; k < kAhead; ++k) {   // a piece past the end repeats the last one and is not stored
+            const uint32_t i = (uint32_t)min(i0 + (uint64_t)k * kRowThreads, (uint64_t)n_pieces - 1);
+            row[k] = i / per_row;
+            p[k] = i - row[k] * per_row;
+            c[k] = piece_codes<SCHEME>(codes, row[k], p[k], P);
+            s[k] = row_factor<WS>(scales, row[k]);
+        }
+        float v[kAhead][8];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            piece_weights<SCHEME, G, CB>(c[k], codes, codebooks, cb_lds, row[k], p[k], in, M, B, v[k]);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const uint64_t i = i0 + (uint64_t)k * kRowThreads;
+            if (i >= n_pieces) break;
+            f16x8 o;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) o[t] = (f16)__fmul_rn(v[k][t], s[k]);
+            // non-temporal: the write stream must not evict the codebook or the codes from L2
+            __builtin_nontemporal_store(as_u32x4(o), reinterpret_cast<u32x4*>(w + i * 8));
+        }
     }
 }
 
-// Tile of 64 rows x 32 pieces: thread (piece tid / 8, rows 8 (tid % 8) ..).
+// Tiles of 64 rows x 32 pieces: thread (piece tid / 8, rows 8 (tid % 8) ..).  A workgroup stages
+// the codebooks once and walks tiles; a tile's codes are loaded while the one before is decoded.
 template <int SCHEME, int G, int CB, WeightScale WS>
 __global__ __launch_bounds__(256) void decode_transposed_kernel(DecodeArgs a, int out, int in, int op, int ldt,
-                                                                int n_row_tiles, int M, int B) {
-    __shared__ u32x4 cb_lds[SCHEME == kScheme2x8 ? 2 * kCodewords2x8 : 1];
+                                                                int n_row_tiles, int n_tiles, int M, int B) {
+    __shared__ u32x4 cb_lds[work_cb_slots<SCHEME>()];
     const int l = blockIdx.y;
     const uint8_t* codes = l ? a.codes[1] : a.codes[0];
     const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
     const f16* scales = l ? a.scales[1] : a.scales[0];
-    stage_2x8<SCHEME>(cb_lds, codebooks);
-    const int rt = (int)(blockIdx.x % n_row_tiles), pt = (int)(blockIdx.x / n_row_tiles);
-    const int row0 = rt * 64 + 8 * (threadIdx.x & 7), p = pt * 32 + (threadIdx.x >> 3);
-    const int k0 = 8 * p;
-    if (k0 >= in) return;
-    f16 o[8][8];   // [row][input]
+    const uint32_t P = (uint32_t)in / 8;
+    const int oct = threadIdx.x & 7, piece = threadIdx.x >> 3;
+    auto row_of = [&](int tile) { return (tile % n_row_tiles) * 64 + 8 * oct; };
+    auto piece_of = [&](int tile) { return (tile / n_row_tiles) * 32 + piece; };
+    auto load = [&](int tile, uint32_t (&c)[8], f16 (&s)[8]) {
+        const int t = min(tile, n_tiles - 1);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const int row = min(row0 + r, out - 1);
-        float v[8];
-        piece_weights<SCHEME, G, CB>(codes, codebooks, cb_lds, row, p, in, M, B, v);
-        const float s = row_factor<WS>(scales, row);
+        for (int r = 0; r < 8; ++r) {
+            const int row = min(row_of(t) + r, out - 1);
+            c[r] = piece_codes<SCHEME>(codes, row, piece_of(t), P);
+            s[r] = scales[row];
+        }
+    };
+    uint32_t c[8];
+    f16 s[8];
+    load(blockIdx.x, c, s);
+    stage_codebooks<SCHEME>(cb_lds, codebooks);
+    for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
+        uint32_t cn[8];
+        f16 sn[8];
+        load(tile + gridDim.x, cn, sn);
+        const int row0 = row_of(tile), p = piece_of(tile), k0 = 8 * p;
+        if (k0 < in) {
+            f16 o[8][8];   // [row][input]
 #pragma unroll
-        for (int t = 0; t < 8; ++t) o[r][t] = row0 + r < out ? (f16)__fmul_rn(v[t], s) : (f16)0.f;
-    }
-    f16* w = a.w[0] + (size_t)l * op + row0;
+            for (int r = 0; r < 8; ++r) {
+                float v[8];
+                piece_weights<SCHEME, G, CB>(c[r], codes, codebooks, cb_lds, min(row0 + r, out - 1), p, in, M, B, v);
+                float f = (float)s[r];
+                if constexpr (WS == WeightScale::kPow2) {
+                    int e;
+                    scale_mantissa(f, &e);
+                    f = ldexpf(1.f, e);
+                }
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        if (k0 + t < in) {
-            f16x8 c;
+                for (int t = 0; t < 8; ++t) o[r][t] = row0 + r < out ? (f16)__fmul_rn(v[t], f) : (f16)0.f;
+            }
+            f16* w = a.w[0] + (size_t)l * op + row0;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) c[r] = o[r][t];
-            *reinterpret_cast<u32x4*>(w + (size_t)(k0 + t) * ldt) = as_u32x4(c);
+            for (int t = 0; t < 8; ++t) {
+                if (k0 + t < in) {
+                    f16x8 x;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) x[r] = o[r][t];
+                    *reinterpret_cast<u32x4*>(w + (size_t)(k0 + t) * ldt) = as_u32x4(x);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            c[r] = cn[r];
+            s[r] = sn[r];
         }
     }
 }
@@ -195,17 +276,18 @@ hipError_t launch_ws(const DecodeArgs& a, int n, int64_t out, int64_t in, int64_
                      hipStream_t stream) {
     if constexpr (T) {
         const int64_t n_rt = op / 64, n_pt = (in + 255) / 256;
-        if (n_rt * n_pt > INT32_MAX) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((decode_transposed_kernel<SCHEME, G, CB, WS>), dim3((unsigned)(n_rt * n_pt), n), dim3(256), 0,
-                           stream, a, (int)out, (int)in, (int)op, (int)ld, (int)n_rt, M, B);
+        const int64_t tiles = n_rt * n_pt, cap = (int64_t)device_cu_count() * 8 / n;
+        if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((decode_transposed_kernel<SCHEME, G, CB, WS>), dim3((unsigned)(tiles < cap ? tiles : cap), n),
+                           dim3(256), 0, stream, a, (int)out, (int)in, (int)op, (int)ld, (int)n_rt, (int)tiles, M, B);
     } else {
         const uint64_t per_row = (uint64_t)ld / 8, n_pieces = (uint64_t)out * per_row;
         if (n_pieces > UINT32_MAX) return hipErrorInvalidValue;
-        uint64_t blocks = (n_pieces + 255) / 256;
-        const uint64_t cap = (uint64_t)device_cu_count() * 16;
+        uint64_t blocks = (n_pieces + kRowThreads * kAhead - 1) / (kRowThreads * kAhead);
+        const uint64_t cap = (uint64_t)device_cu_count() * 4 / n;
         if (blocks > cap) blocks = cap;
-        hipLaunchKernelGGL((decode_rows_kernel<SCHEME, G, CB, WS>), dim3((unsigned)blocks, n), dim3(256), 0, stream, a,
-                           (uint32_t)n_pieces, (uint32_t)per_row, (int)in, M, B);
+        hipLaunchKernelGGL((decode_rows_kernel<SCHEME, G, CB, WS>), dim3((unsigned)blocks, n), dim3(kRowThreads), 0, stream,
+                           a, (uint32_t)n_pieces, (uint32_t)per_row, (int)in, M, B);
     }
     return hipGetLastError();
 }
@@ -227,6 +309,10 @@ hipError_t launch_any(const GenericScheme& sc, WeightScale ws, const DecodeArgs&
         return launch_scheme<T, kScheme2x8, 8, 1>(ws, a, n, out, in, ld, op, M, B, stream);
     if (M == 1 && B == 16 && sc.g == 8)
         return launch_scheme<T, kScheme1x16, 8, 2>(ws, a, n, out, in, ld, op, M, B, stream);
+    if (M == 4 && B == 8 && sc.g == 16)
+        return launch_scheme<T, kSchemeB8M4, 16, 1>(ws, a, n, out, in, ld, op, M, B, stream);
+    if (M == 1 && B == 8 && sc.g == 4 && in % 8 == 0)
+        return launch_scheme<T, kSchemeB8M1, 4, 1>(ws, a, n, out, in, ld, op, M, B, stream);
 #define AQLM_ROWS(G)                                                                                              \
     case G:                                                                                                       \
         return B <= 8 ? launch_scheme<T, kSchemeGeneric, G, 1>(ws, a, n, out, in, ld, op, M, B, stream)            \

@@ -186,7 +186,7 @@ __device__ __forceinline__ void dense_epilogue(const f32x4 (&acc)[4][4], float* 
             s[l][q] = e.scales[l] != nullptr ? (float)e.scales[l][k] : 1.f;
             b[l][q] = e.bias[l] != nullptr ? (float)e.bias[l][k] : 0.f;
         }
-#pragma unroll
+#pragma unroll 1
     for (int it = 0; it < kLanes; ++it) {
         const int rr = it * (64 / kLanes) + lane / kLanes, tok = tok0 + rr;
         if (tok >= T) continue;
@@ -200,7 +200,8 @@ __device__ __forceinline__ void dense_epilogue(const f32x4 (&acc)[4][4], float* 
             for (int q = 0; q < 8; ++q) z[q] = src[q] * s[l][q] + b[l][q];
             if (e.z[l] != nullptr) epi_store8(e.z[l] + o, left, vec, z);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = l == 0 ? act_value(e.act, z[q]) : v[q] * z[q];
+            for (int q = 0; q < 8; ++q) v[q] = l == 0 ? z[q] : v[q] * z[q];
+            if (l == 0) act_values(e.act, v);
         }
         if constexpr (MODE == kDenseAct) {
             if (e.residual != nullptr) {

@@ -45,7 +45,9 @@ __device__ __forceinline__ void gemv_finish(float p0, float p1, const f16* __res
     float z = p0 * (float)scales[row];
     if (e.bias[0] != nullptr) z += (float)e.bias[0][row];
     if (e.z[0] != nullptr) e.z[0][at] = (f16)z;
-    float v = act_value(e.act, z);
+    float va[1] = {z};
+    act_values(e.act, va);
+    float v = va[0];
     if constexpr (KIND == kGemvGated) {
         float u = p1 * (float)e.scales1[row];
         if (e.bias[1] != nullptr) u += (float)e.bias[1][row];

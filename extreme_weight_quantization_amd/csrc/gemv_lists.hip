@@ -443,16 +443,21 @@ __global__ __launch_bounds__(64 * kReduceParts * N) void lists_reduce_act_kernel
     red[l][part][rl] = lists_run_sum(e.partial[l], r, e.out, e.out_pad, e.slots, part);
     __syncthreads();
     if (wave != 0 || r >= e.out) return;
-    float v = 0.f;
+    float v[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         float z = lists_add_runs(red[k], rl) * (float)e.scales[k][r];
         if (e.bias[k] != nullptr) z += (float)e.bias[k][r];
         if (e.z[k] != nullptr) e.z[k][r] = (f16)z;
-        v = k == 0 ? act_value(e.act, z) : v * z;
+        if (k == 0) {
+            v[0] = z;
+            act_values(e.act, v);
+        } else {
+            v[0] *= z;
+        }
     }
-    if (e.residual != nullptr) v += (float)e.residual[r];
-    e.y[r] = (f16)v;
+    if (e.residual != nullptr) v[0] += (float)e.residual[r];
+    e.y[r] = (f16)v[0];
 }
 
 __global__ __launch_bounds__(64 * kReduceParts) void lists_reduce_kernel(const float* __restrict__ partial,

@@ -345,21 +345,28 @@ __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sum[l][r] += s0 + s < parts ? v[s][l][r] : 0.f;
     }
+    float z[N][4], v[4];
+#pragma unroll
+    for (int l = 0; l < N; ++l)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = min(r0 + r, a.out - 1);
+            z[l][r] = a.scales[l] != nullptr ? sum[l][r] * (float)a.scales[l][row] : sum[l][r];
+            if (a.bias[l] != nullptr) z[l][r] += (float)a.bias[l][row];
+        }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = z[0][r];
+    act_values(a.act, v);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const int row = r0 + r;
-        if (row >= a.out) break;
-        const size_t at = (size_t)t * a.out + row;
-        float v = 0.f;
+        if constexpr (N > 1) v[r] *= z[N - 1][r];
+        if (r0 + r >= a.out) break;
+        const size_t at = (size_t)t * a.out + r0 + r;
 #pragma unroll
-        for (int l = 0; l < N; ++l) {
-            float z = a.scales[l] != nullptr ? sum[l][r] * (float)a.scales[l][row] : sum[l][r];
-            if (a.bias[l] != nullptr) z += (float)a.bias[l][row];
-            if (a.z[l] != nullptr) a.z[l][at] = (f16)z;
-            v = l == 0 ? act_value(a.act, z) : v * z;
-        }
-        if (a.residual != nullptr) v += (float)a.residual[at];
-        a.y[at] = (f16)v;
+        for (int l = 0; l < N; ++l)
+            if (a.z[l] != nullptr) a.z[l][at] = (f16)z[l][r];
+        if (a.residual != nullptr) v[r] += (float)a.residual[at];
+        a.y[at] = (f16)v[r];
     }
 }
 
