@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include "../../include/aqlm.h"
+#include "act_bias.h"
 #include "act_launch.h"
 #include "act_math.h"
 #include "aqlm_validate.h"
@@ -53,9 +54,9 @@ ForwardPlan forward_plan(int n, const GenericScheme& sc, int64_t out, int64_t in
     p.kp = round_up(in, 64);
     p.pad = p.kp != in;
     if (out == 0 || batch <= AQLM_GEMV_MAX_BATCH) return p;   // one launch straight from the codes
-    if (skinny_serves(sc, out, in, batch)) {
+    if (skinny_serves(sc, n, out, in, batch)) {
         p.skinny = true;
-        p.bytes = skinny_partial_bytes(n, out, in, batch);
+        p.bytes = skinny_partial_bytes(sc, n, out, in, batch);
         return p;
     }
     for (int l = 0; l < n; ++l) p.w[l] = parts.add(out, p.kp, 2);
@@ -68,12 +69,22 @@ ForwardPlan forward_plan(int n, const GenericScheme& sc, int64_t out, int64_t in
 struct BackwardPlan {
     int64_t op = 0, wt = 0, dz = 0, partial = 0, parts = 0, bytes = 0;
     bool grad = false;   // a pass over dy writes dz (else dy itself is the product's operand)
+    bool skinny = false;
 };
 
-BackwardPlan backward_plan(int n, int act, int64_t out, int64_t in, int64_t batch) {
+BackwardPlan backward_plan(int n, int act, const GenericScheme& sc, int64_t out, int64_t in, int64_t batch) {
     BackwardPlan p;
     Parts parts;
     p.op = round_up(out, 64);
+    p.skinny = skinny_back_serves(sc, out, in, batch);
+    if (p.skinny) {
+        p.grad = true;
+        p.dz = parts.add(batch, n * p.op, 2);
+        p.partial = parts.add(grad_chunks(batch), n * out, 4);
+        p.parts = out == 0 || batch == 0 ? 0 : parts.add(skinny_back_partial_bytes(n, out, in, batch), 1, 1);
+        p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
+        return p;
+    }
     p.grad = n > 1 || act != kActNone || p.op != out;
     p.wt = parts.add(in, n * p.op, 2);
     p.dz = parts.add(batch, n * p.op, 2);
@@ -150,7 +161,7 @@ int forward(const ActLayers& L, const void* x, const Epilogue& epi, void* worksp
         x = base + p.xp;
     }
     return finish(launch_gemm_dense_act(x, w, ws == WeightScale::kNone ? L.scales : nullptr, L.n, epi, base + p.partial, out,
-                                        p.kp, batch, s));
+                                        p.kp, batch, BiasSum{}, s));
 }
 
 int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx, void* const* dbias, int act,
@@ -181,24 +192,31 @@ int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx,
         if ((L.n > 1 || act != kActNone) && !z[l]) return AQLM_ERR_NULL;
         if (!aligned(z[l], 16)) return AQLM_ERR_ALIGN;
     }
-    const BackwardPlan p = backward_plan(L.n, act, out, in, batch);
+    const BackwardPlan p = backward_plan(L.n, act, GenericScheme{M, B, g}, out, in, batch);
     const int wt = check_workspace(workspace, workspace_bytes, p.bytes);
     if (wt != AQLM_OK) return wt;
     char* base = static_cast<char*>(workspace);
-    const WeightScale ws = (M == 1 && p.grad) ? WeightScale::kPow2 : WeightScale::kFull;
+    const WeightScale ws = (p.skinny || (M == 1 && p.grad)) ? WeightScale::kPow2 : WeightScale::kFull;
     if (p.grad || want_bias) {
         const int r = finish(launch_act_grad(dy, z, ws == WeightScale::kPow2 ? L.scales : nullptr, L.n, act,
                                              p.grad ? base + p.dz : nullptr,
-                                             want_bias ? reinterpret_cast<float*>(base + p.partial) : nullptr, dbias,
-                                             out, p.op, batch, s));
+                                             want_bias ? reinterpret_cast<float*>(base + p.partial) : nullptr, out, p.op,
+                                             batch, s));
         if (r != AQLM_OK) return r;
     }
+    BiasSum bias = {};   // added by the launch that finishes dx, or by one of its own
+    if (want_bias)
+        bias = BiasSum{reinterpret_cast<const float*>(base + p.partial),
+                       {static_cast<f16*>(dbias[0]), static_cast<f16*>(dbias[1])}, L.n, (int)out, (int)grad_chunks(batch)};
+    if (p.skinny)
+        return finish(launch_skinny_back(GenericScheme{M, B, g}, L, base + p.dz, base + p.parts, dx, out, in, p.op, batch,
+                                         bias, s));
     const int r = finish(launch_decode_transposed(GenericScheme{M, B, g}, L, ws, base + p.wt, out, in, p.op, s));
     if (r != AQLM_OK) return r;
     const void* wt16 = base + p.wt;
     const Epilogue plain = {{nullptr, nullptr}, nullptr, {nullptr, nullptr}, dx, kActNone};
     return finish(launch_gemm_dense_act(p.grad ? base + p.dz : dy, &wt16, nullptr, 1, plain, base + p.parts, in,
-                                        L.n * p.op, batch, s));
+                                        L.n * p.op, batch, bias, s));
 }
 
 // The slice-list product of n layers at batch 1.
@@ -239,7 +257,7 @@ int workspace_bytes_of(int n, bool back, int M, int B, int g, int64_t out, int64
     if (!bytes) return AQLM_ERR_NULL;
     const int st = check_sizes(AQLM_ACT_RELU, M, B, g, out, in, batch);
     if (st != AQLM_OK) return st;
-    const int64_t need = back ? backward_plan(n, AQLM_ACT_RELU, out, in, batch).bytes
+    const int64_t need = back ? backward_plan(n, AQLM_ACT_RELU, GenericScheme{M, B, g}, out, in, batch).bytes
                               : forward_plan(n, GenericScheme{M, B, g}, out, in, batch).bytes;
     if (need < 0) return AQLM_ERR_SHAPE;
     *bytes = need;

@@ -6,11 +6,12 @@
 //
 // computed in fp32 from the fp16 inputs.  dz is rounded to fp16 once: it is the operand of
 // the fp16 matrix cores in dx = dz W.  The bias sums take the fp32 values, in a fixed
-// order: each wave adds its 4 tokens, a workgroup its four waves, and act_bias_kernel the
+// order: each wave adds its tokens, a workgroup its four waves, and act_bias_kernel the
 // workgroups' sums, four runs of them in order and then the runs.
 //
 // Elementwise, bound by HBM: 2 bytes read per input and element, 2 written.  A thread
 // takes 8 consecutive rows of W, 16 bytes of each operand.
+#include "act_bias.h"
 #include "act_launch.h"
 #include "act_math.h"
 #include "aqlm_device.h"
@@ -19,8 +20,9 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kGradWaveTokens = 4;                   // tokens per wave, all loaded before any is used
-constexpr int kGradChunk = 4 * kGradWaveTokens;      // tokens per workgroup
+// Tokens per wave, all loaded before any is used: 4, or 1 for batches too small to fill the CUs
+// (8 tokens of 4096 gated rows: 10.2 us with 4).
+constexpr int grad_wave_tokens(int64_t batch) { return batch <= 128 ? 1 : 4; }
 constexpr int kGradCols = 512;                       // columns per workgroup: 64 lanes of 8
 
 struct GradArgs {
@@ -40,23 +42,23 @@ __device__ __forceinline__ f16x8 load8(const f16* p, int left, bool vec) {
     return v;
 }
 
-template <int N, int ACT>
+template <int N, int ACT, int WT>
 __global__ __launch_bounds__(256) void act_grad_kernel(GradArgs a) {
     __shared__ float red[3][N][kGradCols];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int cb = (int)(blockIdx.x % a.n_cols), chunk = (int)(blockIdx.x / a.n_cols);
     const int c0 = cb * kGradCols + 8 * lane;
-    const int t0 = chunk * kGradChunk, t1 = min(a.T, t0 + kGradChunk);
+    const int t0 = chunk * 4 * WT, t1 = min(a.T, t0 + 4 * WT);
     const bool vec = a.out % 8 == 0;   // rows of 16-byte chunks
     const int left = a.out - c0;       // columns of this lane inside the matrix
     constexpr int kOps = N == 1 ? 2 : 3;   // dy, then z (gated: zg, zu)
-    const int tw = t0 + wave * kGradWaveTokens, n_tok = min(kGradWaveTokens, t1 - tw);   // may be <= 0
+    const int tw = t0 + wave * WT, n_tok = min(WT, t1 - tw);   // may be <= 0
     const bool in_row = left > 0;
     // every load of the wave's tokens first; a token past the batch repeats the last one
-    f16x8 v[kGradWaveTokens][kOps];
+    f16x8 v[WT][kOps];
     if (in_row && n_tok > 0) {
 #pragma unroll
-        for (int i = 0; i < kGradWaveTokens; ++i) {
+        for (int i = 0; i < WT; ++i) {
             const size_t at = (size_t)(tw + min(i, n_tok - 1)) * a.out + c0;
             v[i][0] = load8(a.dy + at, left, vec);
             if (N > 1 || ACT != kActNone) v[i][1] = load8(a.z[0] + at, left, vec);
@@ -68,13 +70,12 @@ __global__ __launch_bounds__(256) void act_grad_kernel(GradArgs a) {
     for (int l = 0; l < N; ++l)
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            int e;
-            m[l][q] = (a.mant[l] != nullptr && q < left) ? scale_mantissa((float)a.mant[l][c0 + q], &e) : 1.f;
+            m[l][q] = (a.mant[l] != nullptr && q < left) ? scale_rest(a.mant[l][c0 + q]) : 1.f;
             sum[l][q] = 0.f;
         }
     if (c0 < a.op) {
 #pragma unroll
-        for (int i = 0; i < kGradWaveTokens; ++i) {
+        for (int i = 0; i < WT; ++i) {
             if (i >= n_tok) break;
             float g[N][8];
 #pragma unroll
@@ -120,32 +121,31 @@ __global__ __launch_bounds__(256) void act_grad_kernel(GradArgs a) {
         }
 }
 
-// 64 sums a workgroup; wave w adds the w-th of four runs of the chunks, eight loads in flight.
-__global__ __launch_bounds__(256) void act_bias_kernel(const float* __restrict__ partial, f16* d0, f16* d1, int n,
-                                                       int out, int chunks) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t i = (int64_t)blockIdx.x * 64 + lane, per = (int64_t)n * out;
-    const int run = (chunks + 3) / 4, c1 = min(chunks, (wave + 1) * run);
-    float s = 0.f;
-    for (int c = wave * run; c < c1; c += 8) {
-        float v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = i < per && c + q < c1 ? partial[(size_t)(c + q) * per + i] : 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s += v[q];
-    }
-    red[wave][lane] = s;
-    __syncthreads();
-    if (wave > 0 || i >= per) return;
-    s = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
-    if (i < out) d0[i] = (f16)s;
-    else d1[i - out] = (f16)s;
-}
+__global__ __launch_bounds__(256) void act_bias_kernel(const BiasSum b) { bias_sum_block(b, blockIdx.x); }
 
 __global__ __launch_bounds__(256) void zero16_kernel(f16* p, int64_t n) {
     const int64_t stride = (int64_t)gridDim.x * 256;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) p[i] = (f16)0.f;
+}
+
+}  // namespace
+
+namespace {
+
+template <int N, int WT>
+auto grad_kernel_of(int act) {
+    switch (act) {
+        case kActRelu: return act_grad_kernel<N, kActRelu, WT>;
+        case kActSilu: return act_grad_kernel<N, kActSilu, WT>;
+        case kActGelu: return act_grad_kernel<N, kActGelu, WT>;
+        case kActGeluTanh: return act_grad_kernel<N, kActGeluTanh, WT>;
+        default: return act_grad_kernel<N, kActNone, WT>;
+    }
+}
+
+auto grad_kernel(int n, int act, int wave_tokens) {
+    if (wave_tokens == 1) return n == 1 ? grad_kernel_of<1, 1>(act) : grad_kernel_of<2, 1>(act);
+    return n == 1 ? grad_kernel_of<1, 4>(act) : grad_kernel_of<2, 4>(act);
 }
 
 }  // namespace
@@ -159,11 +159,13 @@ hipError_t launch_zero16(void* p, int64_t n, hipStream_t stream) {
     return hipGetLastError();
 }
 
-int64_t grad_chunks(int64_t batch) { return (batch + kGradChunk - 1) / kGradChunk; }
+int64_t grad_chunks(int64_t batch) {
+    const int64_t per = 4 * grad_wave_tokens(batch);
+    return (batch + per - 1) / per;
+}
 
 hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* mant, int n, int act, void* dz,
-                           float* partial, void* const* dbias, int64_t out, int64_t op, int64_t batch,
-                           hipStream_t stream) {
+                           float* partial, int64_t out, int64_t op, int64_t batch, hipStream_t stream) {
     GradArgs a = {};
     a.dy = static_cast<const f16*>(dy);
     for (int l = 0; l < n; ++l) {
@@ -179,21 +181,15 @@ hipError_t launch_act_grad(const void* dy, const void* const* z, const void* con
     if (chunks * n_cols > INT32_MAX) return hipErrorInvalidValue;
     a.n_cols = (int)n_cols;
     const dim3 grid((unsigned)(chunks * n_cols));
-    void (*kern)(GradArgs) = nullptr;
-    switch (act) {
-        case kActRelu: kern = n == 1 ? act_grad_kernel<1, kActRelu> : act_grad_kernel<2, kActRelu>; break;
-        case kActSilu: kern = n == 1 ? act_grad_kernel<1, kActSilu> : act_grad_kernel<2, kActSilu>; break;
-        case kActGelu: kern = n == 1 ? act_grad_kernel<1, kActGelu> : act_grad_kernel<2, kActGelu>; break;
-        case kActGeluTanh: kern = n == 1 ? act_grad_kernel<1, kActGeluTanh> : act_grad_kernel<2, kActGeluTanh>; break;
-        default: kern = n == 1 ? act_grad_kernel<1, kActNone> : act_grad_kernel<2, kActNone>; break;
-    }
+    auto kern = grad_kernel(n, act, grad_wave_tokens(batch));
     hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, a);
-    if (partial != nullptr) {
-        const int64_t per = (int64_t)n * out;
-        hipLaunchKernelGGL(act_bias_kernel, dim3((unsigned)((per + 63) / 64)), dim3(256), 0, stream, partial,
-                           static_cast<f16*>(dbias[0]), n > 1 ? static_cast<f16*>(dbias[1]) : nullptr, n, (int)out,
-                           (int)chunks);
-    }
+    return hipGetLastError();
+}
+
+hipError_t launch_bias_sum(const BiasSum& b, hipStream_t stream) {
+    const int64_t blocks = bias_sum_blocks(b);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(act_bias_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, b);
     return hipGetLastError();
 }
 

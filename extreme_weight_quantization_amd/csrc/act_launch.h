@@ -7,6 +7,8 @@
 
 namespace aqlm {
 
+struct BiasSum;   // act_bias.h
+
 // What follows the product of one or two layers that share x.  One layer:
 // z = W x + bias, y = act(z) + residual.  Two layers (gate, up): zg, zu likewise,
 // y = act(zg) zu.  Absent pointers are NULL.  residual may be y itself.
@@ -50,22 +52,23 @@ hipError_t launch_zero16(void* p, int64_t n, hipStream_t stream);
 int64_t dense_partial_bytes(int n, int64_t out, int64_t kp, int64_t batch);
 hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void* const* scales, int n,
                                  const Epilogue& epi, void* partial, int64_t out, int64_t kp, int64_t batch,
-                                 hipStream_t stream);
+                                 const BiasSum& bias, hipStream_t stream);
 
 // y from fp32 parts of the products, [part][token][layer][op]: the parts added in order,
-// then scales (NULL: 1) and the epilogue.
+// then scales (NULL: 1) and the epilogue.  bias: sums that further workgroups of the launch add.
 hipError_t launch_finish(int n, const float* partial, const void* const* scales, const Epilogue& epi, int64_t out,
-                         int64_t op, int64_t batch, int parts, hipStream_t stream);
+                         int64_t op, int64_t batch, int parts, const BiasSum& bias, hipStream_t stream);
 
 // Gradients of the pre-activations, fp16, as the dense product's x: dz[t][l * op + i] for
 // i < op (rows past `out` zero).  One layer: dy act'(z); two: dy zu act'(zg) and dy act(zg).
-// mant: scales whose mantissas (scale_mantissa) multiply the fp16 result (NULL: none).
-// partial: fp32 [grad_chunks(batch)][n][out], dbias[l] fp16 [out]: sums over the tokens of
-// the unscaled fp32 gradients (both NULL: not wanted).
+// mant: scales whose mantissas (scale_rest) multiply the fp16 result (NULL: none).
+// partial: fp32 [grad_chunks(batch)][n][out]: sums over chunks of tokens of the unscaled
+// fp32 gradients (NULL: not wanted); launch_bias_sum, or the launch that finishes a
+// product from parts, adds the chunks.
 int64_t grad_chunks(int64_t batch);
 hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* mant, int n, int act, void* dz,
-                           float* partial, void* const* dbias, int64_t out, int64_t op, int64_t batch,
-                           hipStream_t stream);
+                           float* partial, int64_t out, int64_t op, int64_t batch, hipStream_t stream);
+hipError_t launch_bias_sum(const BiasSum& b, hipStream_t stream);
 
 // The products of batch 1..16 (gemv_act.hip): any scheme, no workspace.
 hipError_t launch_gemv_act(const GenericScheme& sc, const ActLayers& L, const void* x, const Epilogue& epi, int64_t out,
@@ -80,12 +83,22 @@ bool launch_gemv_stream_act(const ActLayers& L, const GemvEpi& epi, const void* 
 // fp32 partial sums in the workspace.  The work is dealt to at most kSkinnyWorkgroups
 // workgroups, a fixed number so that the sums' order does not depend on the device.
 constexpr int kSkinnyWorkgroups = 256;
-constexpr int kSkinnyMaxBatch2x8 = 256;
-constexpr int kSkinnyMaxBatch1x16 = 64;
-bool skinny_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch);
-int64_t skinny_partial_bytes(int n, int64_t out, int64_t in, int64_t batch);
+constexpr int kSkinnyMaxBatch2x8 = 512;
+constexpr int kSkinnyMaxBatch1x16 = 256;
+bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
+int64_t skinny_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
 hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void* x, void* partial, const Epilogue& epi,
                          int64_t out, int64_t in, int64_t batch, hipStream_t stream);
+
+// dx of some tens of tokens (skinny_back.hip), 2x8 and 1x16: straight from the codes, dz as
+// launch_act_grad writes it with the scales' mantissas, fp32 parts in the workspace.
+constexpr int kSkinnyBackMaxBatch2x8 = 256;
+constexpr int kSkinnyBackMaxBatch1x16 = 128;
+bool skinny_back_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch);
+int64_t skinny_back_partial_bytes(int n, int64_t out, int64_t in, int64_t batch);
+hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, void* partial, void* dx,
+                              int64_t out, int64_t in, int64_t op, int64_t batch, const BiasSum& bias,
+                              hipStream_t stream);
 
 // The slice-list product of one layer, or of gate and up, batch 1, with the epilogue in its
 // reduction (gemv_lists.hip).  L as for launch_gemv_lists_fused; its y is not used.

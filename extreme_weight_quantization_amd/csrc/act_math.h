@@ -67,16 +67,15 @@ __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
     }
 }
 
-// A row scale s as m 2^e with 1 <= |m| < 2: the exact power of two can go into the fp16
-// weights and m into the other factor, so that only one of the two is rounded.  Zero and
-// values that are not finite keep e = 0.
-__device__ __forceinline__ float scale_mantissa(float s, int* e) {
-    *e = 0;
-    if (!(fabsf(s) > 0.f && fabsf(s) < 1e30f)) return s;
-    int k;
-    const float m = frexpf(s, &k);
-    *e = k - 1;
-    return 2.f * m;
+// A row scale s = m 2^e as an fp16 power of two, which goes into the fp16 weights exactly
+// (but for subnormals), and the rest, which goes into the other factor, so that only
+// one of the two is rounded: 1 <= |m| < 2 for normal s, m
+// below 1 for subnormal s (e = -14), m = s for zero, infinity and NaN (e = 0).
+__device__ __forceinline__ f16 scale_power(f16 s) {
+    const uint16_t b = __builtin_bit_cast(uint16_t, s), x = b & 0x7c00u;
+    const uint16_t p = (x == 0x7c00u || (b & 0x7fffu) == 0) ? 0x3c00u : x == 0 ? 0x0400u : x;
+    return __builtin_bit_cast(f16, p);
 }
+__device__ __forceinline__ float scale_rest(f16 s) { return (float)s / (float)scale_power(s); }
 
 }  // namespace aqlm

@@ -111,10 +111,9 @@ __device__ __forceinline__ void piece_weights(uint32_t c, const uint8_t* __restr
         }
     }
     if constexpr (SCHEME != kSchemeGeneric) {
-        if ((int)p * 8 >= in) {
+        const bool inside = (int)p * 8 < in;
 #pragma unroll
-            for (int t = 0; t < 8; ++t) v[t] = 0.f;
-        }
+        for (int t = 0; t < 8; ++t) v[t] = inside ? v[t] : 0.f;
     }
 }
 
@@ -122,56 +121,43 @@ __device__ __forceinline__ void piece_weights(uint32_t c, const uint8_t* __restr
 template <WeightScale WS>
 __device__ __forceinline__ float row_factor(const f16* __restrict__ scales, uint32_t row) {
     if constexpr (WS == WeightScale::kNone) return 1.f;
-    const float s = (float)scales[row];
-    if constexpr (WS == WeightScale::kFull) return s;
-    int e;
-    scale_mantissa(s, &e);
-    return ldexpf(1.f, e);
+    return (float)scales[row];
 }
 
-// Pieces a thread has in hand at once: their codes are loaded before any is decoded, and a
-// gather or lookup waits for the others' (one at a time the kernel ran at the latency of
-// code, codeword and store in turn: 4096x11008 2x8 29.6 us).
-constexpr int kAhead = 4;
-constexpr int kRowThreads = 512;
+// A workgroup's 256 threads take 256 >> shift rows of 1 << shift pieces each, so a piece's row
+// and place come from shifts and scalars.  The layers are decoded one after the other: one 1x16
+// codebook at a time in L2.  Two, four or eight pieces a thread in hand change the time by less than 10 %:
+// the write bounds it.  Between products that read the weights it takes 1.4-1.7 times what the same launch
+// takes when it only follows itself (28672x8192 2x8 125 against 88 us, 1x16 250 against 146): the weights the
+// product left in the last-level cache have to make room.
+constexpr int kRowThreads = 256;
 
 template <int SCHEME, int G, int CB, WeightScale WS>
-__global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(DecodeArgs a, uint32_t n_pieces, uint32_t per_row,
-                                                                  int in, int M, int B) {
+__global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(DecodeArgs a, int n, int out, int per_row, int shift,
+                                                                  int chunks, int n_items, int in, int M, int B) {
     __shared__ u32x4 cb_lds[work_cb_slots<SCHEME>()];
-    const int l = blockIdx.y;
-    const uint8_t* codes = l ? a.codes[1] : a.codes[0];
-    const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
-    const f16* scales = l ? a.scales[1] : a.scales[0];
-    f16* w = l ? a.w[1] : a.w[0];
-    stage_codebooks<SCHEME>(cb_lds, codebooks);
     const uint32_t P = (uint32_t)in / 8;   // whole pieces of a row (the schemes but kSchemeGeneric: in % 8 == 0)
-    // 64-bit piece index: n_pieces may come within a stride of 2^32
-    const uint64_t stride = (uint64_t)gridDim.x * kRowThreads * kAhead;
-    for (uint64_t i0 = (uint64_t)blockIdx.x * kRowThreads * kAhead + threadIdx.x; i0 < n_pieces; i0 += stride) {
-        uint32_t row[kAhead], p[kAhead], c[kAhead];
-        float s[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {   // a piece past the end repeats the last one and is not stored
-            const uint32_t i = (uint32_t)min(i0 + (uint64_t)k * kRowThreads, (uint64_t)n_pieces - 1);
-            row[k] = i / per_row;
-            p[k] = i - row[k] * per_row;
-            c[k] = piece_codes<SCHEME>(codes, row[k], p[k], P);
-            s[k] = row_factor<WS>(scales, row[k]);
-        }
-        float v[kAhead][8];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            piece_weights<SCHEME, G, CB>(c[k], codes, codebooks, cb_lds, row[k], p[k], in, M, B, v[k]);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const uint64_t i = i0 + (uint64_t)k * kRowThreads;
-            if (i >= n_pieces) break;
+    const int trow = threadIdx.x >> shift, tp = threadIdx.x & ((1 << shift) - 1);
+    for (int l = 0; l < n; ++l) {
+        const uint8_t* codes = l ? a.codes[1] : a.codes[0];
+        const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
+        const f16* scales = l ? a.scales[1] : a.scales[0];
+        f16* w = l ? a.w[1] : a.w[0];
+        if (l > 0) __syncthreads();   // the first layer's lookups are done
+        stage_codebooks<SCHEME>(cb_lds, codebooks);
+        for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+            const int rb = item / chunks, ch = item - rb * chunks;   // scalars: row block, chunk of the row
+            const int row = (rb << (8 - shift)) + trow, p = (ch << shift) + tp;
+            if (row >= out || p >= per_row) continue;
+            const uint32_t c = piece_codes<SCHEME>(codes, row, p, P);
+            float v[8];
+            piece_weights<SCHEME, G, CB>(c, codes, codebooks, cb_lds, row, p, in, M, B, v);
+            const float s = row_factor<WS>(scales, row);
             f16x8 o;
 #pragma unroll
-            for (int t = 0; t < 8; ++t) o[t] = (f16)__fmul_rn(v[k][t], s[k]);
+            for (int t = 0; t < 8; ++t) o[t] = (f16)__fmul_rn(v[t], s);
             // non-temporal: the write stream must not evict the codebook or the codes from L2
-            __builtin_nontemporal_store(as_u32x4(o), reinterpret_cast<u32x4*>(w + i * 8));
+            __builtin_nontemporal_store(as_u32x4(o), reinterpret_cast<u32x4*>(w + ((size_t)row * per_row + p) * 8));
         }
     }
 }
@@ -179,65 +165,62 @@ __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(DecodeArgs a, 
 // Tiles of 64 rows x 32 pieces: thread (piece tid / 8, rows 8 (tid % 8) ..).  A workgroup stages
 // the codebooks once and walks tiles; a tile's codes are loaded while the one before is decoded.
 template <int SCHEME, int G, int CB, WeightScale WS>
-__global__ __launch_bounds__(256) void decode_transposed_kernel(DecodeArgs a, int out, int in, int op, int ldt,
+__global__ __launch_bounds__(256) void decode_transposed_kernel(DecodeArgs a, int n, int out, int in, int op, int ldt,
                                                                 int n_row_tiles, int n_tiles, int M, int B) {
     __shared__ u32x4 cb_lds[work_cb_slots<SCHEME>()];
-    const int l = blockIdx.y;
-    const uint8_t* codes = l ? a.codes[1] : a.codes[0];
-    const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
-    const f16* scales = l ? a.scales[1] : a.scales[0];
     const uint32_t P = (uint32_t)in / 8;
     const int oct = threadIdx.x & 7, piece = threadIdx.x >> 3;
     auto row_of = [&](int tile) { return (tile % n_row_tiles) * 64 + 8 * oct; };
     auto piece_of = [&](int tile) { return (tile / n_row_tiles) * 32 + piece; };
-    auto load = [&](int tile, uint32_t (&c)[8], f16 (&s)[8]) {
-        const int t = min(tile, n_tiles - 1);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int row = min(row_of(t) + r, out - 1);
-            c[r] = piece_codes<SCHEME>(codes, row, piece_of(t), P);
-            s[r] = scales[row];
-        }
-    };
-    uint32_t c[8];
-    f16 s[8];
-    load(blockIdx.x, c, s);
-    stage_codebooks<SCHEME>(cb_lds, codebooks);
-    for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
-        uint32_t cn[8];
-        f16 sn[8];
-        load(tile + gridDim.x, cn, sn);
-        const int row0 = row_of(tile), p = piece_of(tile), k0 = 8 * p;
-        if (k0 < in) {
-            f16 o[8][8];   // [row][input]
+    for (int l = 0; l < n; ++l) {
+        const uint8_t* codes = l ? a.codes[1] : a.codes[0];
+        const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
+        const f16* scales = l ? a.scales[1] : a.scales[0];
+        auto load = [&](int tile, uint32_t (&c)[8], f16 (&s)[8]) {
+            const int t = min(tile, n_tiles - 1);
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                float v[8];
-                piece_weights<SCHEME, G, CB>(c[r], codes, codebooks, cb_lds, min(row0 + r, out - 1), p, in, M, B, v);
-                float f = (float)s[r];
-                if constexpr (WS == WeightScale::kPow2) {
-                    int e;
-                    scale_mantissa(f, &e);
-                    f = ldexpf(1.f, e);
-                }
-#pragma unroll
-                for (int t = 0; t < 8; ++t) o[r][t] = row0 + r < out ? (f16)__fmul_rn(v[t], f) : (f16)0.f;
+                const int row = min(row_of(t) + r, out - 1);
+                c[r] = piece_codes<SCHEME>(codes, row, piece_of(t), P);
+                s[r] = scales[row];
             }
-            f16* w = a.w[0] + (size_t)l * op + row0;
+        };
+        uint32_t c[8];
+        f16 s[8];
+        load(blockIdx.x, c, s);
+        if (l > 0) __syncthreads();   // the first layer's lookups are done
+        stage_codebooks<SCHEME>(cb_lds, codebooks);
+        for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
+            uint32_t cn[8];
+            f16 sn[8];
+            load(tile + gridDim.x, cn, sn);
+            const int row0 = row_of(tile), p = piece_of(tile), k0 = 8 * p;
+            if (k0 < in) {
+                f16 o[8][8];   // [row][input]
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                if (k0 + t < in) {
-                    f16x8 x;
+                for (int r = 0; r < 8; ++r) {
+                    float v[8];
+                    piece_weights<SCHEME, G, CB>(c[r], codes, codebooks, cb_lds, min(row0 + r, out - 1), p, in, M, B, v);
+                    const float f = (float)(WS == WeightScale::kPow2 ? scale_power(s[r]) : s[r]);
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) x[r] = o[r][t];
-                    *reinterpret_cast<u32x4*>(w + (size_t)(k0 + t) * ldt) = as_u32x4(x);
+                    for (int t = 0; t < 8; ++t) o[r][t] = row0 + r < out ? (f16)__fmul_rn(v[t], f) : (f16)0.f;
+                }
+                f16* w = a.w[0] + (size_t)l * op + row0;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    if (k0 + t < in) {
+                        f16x8 x;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) x[r] = o[r][t];
+                        *reinterpret_cast<u32x4*>(w + (size_t)(k0 + t) * ldt) = as_u32x4(x);
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            c[r] = cn[r];
-            s[r] = sn[r];
+            for (int r = 0; r < 8; ++r) {
+                c[r] = cn[r];
+                s[r] = sn[r];
+            }
         }
     }
 }
@@ -276,18 +259,20 @@ hipError_t launch_ws(const DecodeArgs& a, int n, int64_t out, int64_t in, int64_
                      hipStream_t stream) {
     if constexpr (T) {
         const int64_t n_rt = op / 64, n_pt = (in + 255) / 256;
-        const int64_t tiles = n_rt * n_pt, cap = (int64_t)device_cu_count() * 8 / n;
+        const int64_t tiles = n_rt * n_pt, cap = (int64_t)device_cu_count() * 8;
         if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((decode_transposed_kernel<SCHEME, G, CB, WS>), dim3((unsigned)(tiles < cap ? tiles : cap), n),
-                           dim3(256), 0, stream, a, (int)out, (int)in, (int)op, (int)ld, (int)n_rt, (int)tiles, M, B);
+        hipLaunchKernelGGL((decode_transposed_kernel<SCHEME, G, CB, WS>), dim3((unsigned)(tiles < cap ? tiles : cap)),
+                           dim3(256), 0, stream, a, n, (int)out, (int)in, (int)op, (int)ld, (int)n_rt, (int)tiles, M, B);
     } else {
-        const uint64_t per_row = (uint64_t)ld / 8, n_pieces = (uint64_t)out * per_row;
-        if (n_pieces > UINT32_MAX) return hipErrorInvalidValue;
-        uint64_t blocks = (n_pieces + kRowThreads * kAhead - 1) / (kRowThreads * kAhead);
-        const uint64_t cap = (uint64_t)device_cu_count() * 4 / n;
-        if (blocks > cap) blocks = cap;
-        hipLaunchKernelGGL((decode_rows_kernel<SCHEME, G, CB, WS>), dim3((unsigned)blocks, n), dim3(kRowThreads), 0, stream,
-                           a, (uint32_t)n_pieces, (uint32_t)per_row, (int)in, M, B);
+        const int64_t per_row = ld / 8;
+        int shift = 0;
+        while (shift < 8 && (1 << shift) < per_row) ++shift;
+        const int64_t rows = kRowThreads >> shift, chunks = (per_row + (1 << shift) - 1) >> shift;
+        const int64_t items = (out + rows - 1) / rows * chunks, cap = (int64_t)device_cu_count() * 16;
+        if (items > INT32_MAX / 2) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((decode_rows_kernel<SCHEME, G, CB, WS>), dim3((unsigned)(items < cap ? items : cap)),
+                           dim3(kRowThreads), 0, stream, a, n, (int)out, (int)per_row, shift, (int)chunks, (int)items,
+                           (int)in, M, B);
     }
     return hipGetLastError();
 }

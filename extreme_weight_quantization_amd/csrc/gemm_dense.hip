@@ -62,6 +62,7 @@
 // lane quarters, 4 rows apart, then hit distinct banks) and finishes 8 outputs a lane,
 // with 16-byte accesses to y, z and the residual; everything up to the one rounding
 // of y (and of z where it is kept) is fp32.
+#include "act_bias.h"
 #include "act_launch.h"
 #include "act_math.h"
 #include "aqlm_device.h"
@@ -474,7 +475,7 @@ int64_t dense_partial_bytes(int n, int64_t out, int64_t kp, int64_t batch) {
 
 hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void* const* scales, int n,
                                  const Epilogue& epi, void* partial, int64_t out, int64_t kp, int64_t batch,
-                                 hipStream_t stream) {
+                                 const BiasSum& bias, hipStream_t stream) {
     const DensePlan p = dense_plan(n, out, kp, batch);
     DenseEpi e = {};
     for (int l = 0; l < n; ++l) {
@@ -489,6 +490,8 @@ hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void
     e.splits = p.splits;
     e.op = (int)((out + 7) / 8 * 8);
     if (p.splits == 1) {
+        const hipError_t b = launch_bias_sum(bias, stream);
+        if (b != hipSuccess) return b;
         if (n == 2)
             return p.bm == 128 ? launch_dense<kDenseGated, 128>(x, w[0], epi.y, out, kp, batch, e, stream)
                                : launch_dense<kDenseGated, 256>(x, w[0], epi.y, out, kp, batch, e, stream);
@@ -503,7 +506,7 @@ hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void
         r = p.bm == 128 ? launch_dense<kDensePart, 128>(x, w[0], nullptr, out, kp, batch, e, stream)
                         : launch_dense<kDensePart, 256>(x, w[0], nullptr, out, kp, batch, e, stream);
     if (r != hipSuccess) return r;
-    return launch_finish(n, e.partial, scales, epi, out, e.op, batch, p.splits, stream);
+    return launch_finish(n, e.partial, scales, epi, out, e.op, batch, p.splits, bias, stream);
 }
 
 }  // namespace aqlm

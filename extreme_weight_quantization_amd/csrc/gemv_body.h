@@ -93,10 +93,14 @@ constexpr int kXStageSlots(int xm) {
 // packed two per 32-bit word.  The load is unconditional, with the row and
 // group indices clamped into the matrix, so that no branch forces an early
 // wait on it; groups outside the matrix are masked when they are decoded.
-template <bool VEC>
+template <bool VEC, int KIND>
 __device__ __forceinline__ u32x4 load_codes(const uint8_t* __restrict__ codes, int row, int out,
                                             int g0, int G) {
     const int r = min(row, out - 1);
+    if constexpr (!VEC && KIND != kGemvPlain) {
+        const size_t total = (size_t)out * G;
+        if (total >= 8) return load_codes_any(reinterpret_cast<const uint16_t*>(codes), (size_t)r * G + g0, total);
+    }
     const uint16_t* c16 = reinterpret_cast<const uint16_t*>(codes) + (size_t)r * G;
     if constexpr (VEC) {
         // G % 8 == 0: 16-byte aligned chunks; a chunk past the end is clamped to the last one.
@@ -307,7 +311,7 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
     for (int i = 0; i < RTP; ++i) {
         const int rt = rt0 + i * nwg;
         cnext[i] = (s0 < n_slab && rt < n_rt)
-                       ? load_codes<VEC>(codes, rt * kTileRows + trow, out, s0 * kSlabGroups + kq * 8, G)
+                       ? load_codes<VEC, KIND>(codes, rt * kTileRows + trow, out, s0 * kSlabGroups + kq * 8, G)
                        : u32x4{0u, 0u, 0u, 0u};
     }
     f16x8 bx[8];
@@ -471,7 +475,7 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
                 for (int i = 0; i < RTP; ++i) {
                     const int rt = rtn + i * nwg;
                     cnext[i] = (sn < n_slab && rt < n_rt)
-                                   ? load_codes<VEC>(codes, rt * kTileRows + trow, out, sn * kSlabGroups + kq * 8, G)
+                                   ? load_codes<VEC, KIND>(codes, rt * kTileRows + trow, out, sn * kSlabGroups + kq * 8, G)
                                    : u32x4{0u, 0u, 0u, 0u};
                 }
             }

@@ -27,6 +27,7 @@
 // 16 lanes that read one group of 16 tokens hit 16 distinct bank groups.
 #include <algorithm>
 
+#include "act_bias.h"
 #include "act_launch.h"
 #include "act_math.h"
 #include "aqlm_device.h"
@@ -37,7 +38,9 @@ namespace {
 
 constexpr int kKTiles = 16;                                  // matrix-core row tiles of a workgroup (256 rows)
 constexpr int kKSlab = 32;                                  // groups per step
-constexpr int kKStages = 3;                                 // steps of x (LDS stages) and codes (registers) in flight
+// Steps of x (LDS stages) and codes (registers) in flight: what 160 KB of LDS hold (1x16 at 128
+// tokens: two stages of 64 KB; its steps are long enough for one step ahead).
+constexpr int skinny_stages(int bm) { return bm == 128 ? 2 : 3; }
 constexpr int kKRepl = 8;                                   // 2x8 codebook replicas in LDS
 constexpr int kKCbBytes = 2 * kCodewords2x8 * kKRepl * 16;   // 64 KB
 
@@ -79,11 +82,13 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     constexpr int kCT = BM / 16;                              // column tiles of tokens
     constexpr int kXStage = BM * kKSlab;                      // 16-byte slots of a stage
     constexpr int kNX = kXStage / kThreads;                   // x loads a wave issues a step
-    constexpr int kR = kKStages;                              // steps of x and of codes in flight
+    constexpr int kR = skinny_stages(BM);                     // steps of x and of codes in flight
     constexpr bool kRagged = ROW != kRowWhole;                // the last slab may have groups past the row
     constexpr uint32_t kXOff = SCHEME == kScheme2x8 ? kKCbBytes : 0;
-    // vector loads that every step issues: the x tile, one of codes, the gathers
-    constexpr int kIssued = kNX + RT + (SCHEME == kScheme1x16 ? 8 * RT : 0);
+    // vector loads that every step issues after the x tile that its end waits for: with three
+    // stages (that tile: a step ago) all of its own, the x tile, the codes, the gathers; with two, the codes and half the gathers
+    constexpr int kGathers = SCHEME == kScheme1x16 ? 4 * RT : 0;   // of half a step
+    constexpr int kIssued = kR == 2 ? RT + kGathers : kNX + RT + 2 * kGathers;
     constexpr int kTileRows = GATED ? 8 : 16;
     constexpr int kN = GATED ? 2 : 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -115,16 +120,11 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     // outputs are not used), groups past the row its last 8 (masked when used)
     auto load_codes = [&](const Unit& v, int rt) -> u32x4 {
         const int row = min((v.b * kKTiles + wave * RT + rt) * kTileRows + trow, a.out - 1);
-        const uint16_t* r = codes + (size_t)row * G;
         const int g0 = v.s * kKSlab + 8 * kq;
         if constexpr (ROW != kRowAny) {
-            return load_nt16(r + min(g0, G - 8));
+            return load_nt16(codes + (size_t)row * G + min(g0, G - 8));
         } else {
-            u32x4 c;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                c[q] = (uint32_t)r[min(g0 + 2 * q, G - 1)] | ((uint32_t)r[min(g0 + 2 * q + 1, G - 1)] << 16);
-            return c;
+            return load_codes_any(codes, (size_t)row * G + g0, (size_t)a.out * G);
         }
     };
     // x of a unit into a stage: load i of a wave fills slots 64 (wave kNX + i) .. + 63, two tokens;
@@ -310,12 +310,18 @@ struct FinishArgs {
     f16* y;
     int out, op, T, act;
     int bm, blk_rows, n_slab, n_blk, units, W;   // units 0: W parts everywhere
+    int blocks;     // workgroups of the outputs; those after them add bias sums
+    BiasSum sums;
 };
 
 // Thread: 4 outputs of a token.  The parts of its row block are the runs from the one that
 // holds the block's first unit to the one that holds its last, added in that order.
 template <int N>
 __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) {
+    if ((int)blockIdx.x >= a.blocks) {
+        bias_sum_block(a.sums, (int)blockIdx.x - a.blocks);
+        return;
+    }
     const int per = a.op / 4;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)a.T * per) return;
@@ -388,11 +394,13 @@ FinishArgs finish_args(int n, const float* partial, const void* const* scales, c
     return f;
 }
 
-hipError_t launch_finish_args(int n, const FinishArgs& f, hipStream_t stream) {
+hipError_t launch_finish_args(int n, FinishArgs& f, hipStream_t stream) {
     const int64_t threads = (int64_t)f.T * (f.op / 4), blocks = (threads + 255) / 256;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    if (n == 2) hipLaunchKernelGGL(skinny_finish_kernel<2>, dim3((unsigned)blocks), dim3(256), 0, stream, f);
-    else hipLaunchKernelGGL(skinny_finish_kernel<1>, dim3((unsigned)blocks), dim3(256), 0, stream, f);
+    const int64_t all = blocks + bias_sum_blocks(f.sums);
+    if (all > INT32_MAX) return hipErrorInvalidValue;
+    f.blocks = (int)blocks;
+    if (n == 2) hipLaunchKernelGGL(skinny_finish_kernel<2>, dim3((unsigned)all), dim3(256), 0, stream, f);
+    else hipLaunchKernelGGL(skinny_finish_kernel<1>, dim3((unsigned)all), dim3(256), 0, stream, f);
     return hipGetLastError();
 }
 
@@ -402,10 +410,10 @@ struct SkinnyPlan {
 };
 
 // Token tiles of up to 64 tokens for 2x8 (its codebooks leave room for three x stages of
-// them); 1x16 is bound by its gathers, one per code and token tile.
-SkinnyPlan skinny_plan(int n, int64_t out, int64_t in, int64_t batch) {
+// them), up to 128 for 1x16, which is bound by its gathers, one per code and token tile.
+SkinnyPlan skinny_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     SkinnyPlan p;
-    const int64_t bm = batch <= 32 ? 32 : 64, tile = n == 2 ? 8 : 16;
+    const int64_t bm = batch <= 32 ? 32 : batch <= 64 || sc.M == 2 ? 64 : 128, tile = n == 2 ? 8 : 16;
     const int64_t n_slab = (in / kGroup + kKSlab - 1) / kKSlab, n_blk = (out + kKTiles * tile - 1) / (kKTiles * tile);
     const int64_t units = (batch + bm - 1) / bm * n_blk * n_slab;
     p.bm = (int)bm;
@@ -425,7 +433,7 @@ hipError_t launch_main(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t str
     auto kern = a.G % kKSlab == 0 ? skinny_kernel<SCHEME, BM, GATED, kRowWhole, RT, SUM>
                 : a.G % 8 == 0    ? skinny_kernel<SCHEME, BM, GATED, kRowVec, RT, SUM>
                                   : skinny_kernel<SCHEME, BM, GATED, kRowAny, RT, SUM>;
-    constexpr size_t lds = (SCHEME == kScheme2x8 ? kKCbBytes : 0) + (size_t)kKStages * BM * kKSlab * 16;
+    constexpr size_t lds = (SCHEME == kScheme2x8 ? kKCbBytes : 0) + (size_t)skinny_stages(BM) * BM * kKSlab * 16;
     static_assert(lds <= 163840, "LDS budget");
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
@@ -444,27 +452,39 @@ hipError_t launch_scheme(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t s
     if constexpr (SCHEME == kScheme2x8) {
         if (a.T > 64) return launch_main<SCHEME, 64, GATED, 2, true>(p, a, stream);
     }
+    if constexpr (SCHEME == kScheme1x16) {
+        if (p.bm == 128) return launch_main<SCHEME, 128, GATED, 2, false>(p, a, stream);
+    }
     return launch_main<SCHEME, 64, GATED, 2, false>(p, a, stream);
 }
 
 }  // namespace
 
-bool skinny_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch) {
+// 1x16: a unit is 131072 gathers, about 9 us of one CU, so few units leave the others idle and decoding the weights
+// first is faster (2048x1024 at 64 tokens: 22.2 us against 16.7; 160 units of 4000x2400:
+// 26.0 against 29.7), and above 128 tokens every code is gathered twice (4096^2 at 256 tokens, 256 units:
+// 46 against 41; 4096x11008, 688 units: 80 against 98; at 512 tokens 128 against 115).  2x8
+// wins from the smallest layers (10.9 against 16.4 us on 2048x1024 at 64 tokens) up to 512
+// tokens (11008x4096 68 against 91, at 1024 123 against 129 and gated 283 against 229).
+bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     const bool two = sc.M == 2 && sc.B == 8 && sc.g == 8, one = sc.M == 1 && sc.B == 16 && sc.g == 8;
     if (!two && !one) return false;
+    if (out * (in / kGroup) < 8) return false;   // 8 codes a load
     if (batch > (two ? kSkinnyMaxBatch2x8 : kSkinnyMaxBatch1x16)) return false;
-    // units are counted in 32 bits
-    return ((batch + 31) / 32) * ((out + 127) / 128) * (in / 256 + 1) < (1 << 30);
+    const int64_t rows = kKTiles * (n == 2 ? 8 : 16);
+    const int64_t units = (out + rows - 1) / rows * ((in / kGroup + kKSlab - 1) / kKSlab);
+    if (one && units < (batch <= 128 ? 128 : 512)) return false;
+    return (batch + 31) / 32 * units < (1 << 30);   // units are counted in 32 bits
 }
 
-int64_t skinny_partial_bytes(int n, int64_t out, int64_t in, int64_t batch) {
-    const SkinnyPlan p = skinny_plan(n, out, in, batch);
+int64_t skinny_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
+    const SkinnyPlan p = skinny_plan(sc, n, out, in, batch);
     return (int64_t)p.slots * batch * n * p.op * 4;
 }
 
 hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void* x, void* partial, const Epilogue& epi,
                          int64_t out, int64_t in, int64_t batch, hipStream_t stream) {
-    const SkinnyPlan p = skinny_plan(L.n, out, in, batch);
+    const SkinnyPlan p = skinny_plan(sc, L.n, out, in, batch);
     SkinnyArgs a = {};
     for (int l = 0; l < L.n; ++l) {
         a.codes[l] = static_cast<const uint8_t*>(L.codes[l]);
@@ -491,8 +511,9 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
 }
 
 hipError_t launch_finish(int n, const float* partial, const void* const* scales, const Epilogue& epi, int64_t out,
-                         int64_t op, int64_t batch, int parts, hipStream_t stream) {
+                         int64_t op, int64_t batch, int parts, const BiasSum& bias, hipStream_t stream) {
     FinishArgs f = finish_args(n, partial, scales, epi, out, op, batch);
+    f.sums = bias;
     f.W = parts;
     return launch_finish_args(n, f, stream);
 }

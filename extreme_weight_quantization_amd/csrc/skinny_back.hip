@@ -1,0 +1,287 @@
+// Gradients of a small batch with respect to the inputs, straight from the codes, 2x8 and 1x16:
+//   dx[t][k] = sum over layers and rows i of dz[t][i] s[i] Wc[i][k].
+//
+// "The AQLM Quantization Algorithm, Explained", Figure 2 of the MCQ section (a group's weights
+// are the sum of one codeword per codebook, times the row's scale).  The sum runs over the
+// rows of W, while a codeword holds 8 inputs of one row, and the matrix cores want 8
+// consecutive summed indices in a lane.  So a lane looks up the codewords of 8 consecutive
+// rows at one group and transposes the 8 x 8 block in registers (v_perm_b32 pairs two rows'
+// halves: 32 for 64 weights): operand t then holds input t of the group for the 8 rows.  A wave
+// covers 16 groups x 32 rows with 8 operands, each multiplied by the dz of up to 64 tokens,
+// and no weight is ever written to memory.
+//
+//  * The row scale is split into a power of two and a mantissa (act_math.h): the power of two
+//    multiplies the codewords in fp16, exactly but for subnormals, the mantissa is in dz (act_grad.hip), which is
+//    rounded to fp16 anyway.  2x8 multiplies its two codewords one by one, so no weight
+//    is rounded.
+//  * A workgroup of 8 waves owns 16 groups (128 inputs) of dx and a part of the rows of one
+//    layer; its waves take every eighth chunk of 32 rows, each with the next chunk's codes and dz
+//    in flight and no barrier, and add their sums in LDS in wave order.  Its fp32 part of dx goes to
+//    the workspace; skinny_finish_kernel adds the parts in order and rounds once.
+//  * 2x8 codebooks: LDS, 8 replicas, read without bank conflicts as in gemv.hip.  1x16
+//    codewords are gathered from L2.
+#include <algorithm>
+
+#include "act_bias.h"
+#include "act_launch.h"
+#include "act_math.h"
+#include "aqlm_device.h"
+
+namespace aqlm {
+
+namespace {
+
+constexpr int kBWaves = 8;
+constexpr int kBThreads = kBWaves * kWave;
+constexpr int kBGroups = 16;                                 // groups a workgroup
+constexpr int kBRows = 32;                                   // rows a chunk
+constexpr int kBCbBytes = 2 * kCodewords2x8 * 8 * 16;         // 64 KB: 8 replicas
+
+struct BackArgs {
+    const uint8_t* codes[2];
+    const f16* codebooks[2];
+    const f16* scales[2];
+    const f16* dz;      // [t][l * op + i], times the scales' mantissas; zero for i >= out
+    float* partial;     // [part][t][ip]
+    int out, op, G, T, n, ip, n_cb, splits;
+};
+
+__device__ __forceinline__ u32x4 lds16(uint32_t byte) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)byte);
+}
+
+template <int SCHEME, int CT>
+__global__ __launch_bounds__(kBThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void skinny_back_kernel(
+    const BackArgs a) {
+    extern __shared__ u32x4 smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lrow = lane & 15, kq = lane >> 4;
+    const int cb = (int)blockIdx.x % a.n_cb, rest = (int)blockIdx.x / a.n_cb;
+    const int split = rest % a.splits, l = (rest / a.splits) % a.n, tt = rest / (a.splits * a.n);
+    const uint16_t* codes = reinterpret_cast<const uint16_t*>(l ? a.codes[1] : a.codes[0]);
+    const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
+    const f16* scales = l ? a.scales[1] : a.scales[0];
+    const int n_chunks = a.op / kBRows;
+    const int c_end = (int)((int64_t)(split + 1) * n_chunks / a.splits);
+    const int c0 = (int)((int64_t)split * n_chunks / a.splits) + wave;
+    const int j = min(cb * kBGroups + lrow, a.G - 1);   // groups past the row repeat the last (not used)
+    const size_t ldz = (size_t)a.n * a.op;
+    const f16* dzl = a.dz + (size_t)l * a.op;
+
+    // What a chunk needs from memory: the codes and scales of the lane's 8 rows, dz of its
+    // tokens.  One set of registers: each part of the next chunk is loaded after its last use in this one.
+    uint16_t code[8];
+    f16 scale[8];
+    u32x4 dz[CT];
+    auto row0 = [&](int c) { return min(c, n_chunks - 1) * kBRows + 8 * kq; };
+    auto load_codes = [&](int c) {   // rows past the layer repeat its last one: their dz is zero
+#pragma unroll
+        for (int r = 0; r < 8; ++r) code[r] = codes[(size_t)min(row0(c) + r, a.out - 1) * a.G + j];
+    };
+    auto load_scales = [&](int c) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) scale[r] = scales[min(row0(c) + r, a.out - 1)];
+    };
+    auto load_dz = [&](int c) {   // tokens past the batch repeat the last (their sums are not used)
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+            dz[i] = load16(dzl + (size_t)min((tt * CT + i) * 16 + lrow, a.T - 1) * ldz + row0(c));
+    };
+    f32x4 acc[8][CT];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int i = 0; i < CT; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const uint32_t mA = (lane >> 3) & 1u, r16 = (lane & 7u) * 16u;
+    const uint32_t base = (r16 + 128u * mA) | ((r16 + 128u * (mA ^ 1u)) << 8);
+    // the products of one codeword per row (w: rows 0..7 of the lane, times the rows' powers of two)
+    auto multiply = [&](const u32x4 (&w)[8]) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            u32x4 lo, hi;   // inputs 2d and 2d + 1 of the 8 rows
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                lo[p] = __builtin_amdgcn_perm(w[2 * p + 1][d], w[2 * p][d], 0x05040100u);
+                hi[p] = __builtin_amdgcn_perm(w[2 * p + 1][d], w[2 * p][d], 0x07060302u);
+            }
+#pragma unroll
+            for (int i = 0; i < CT; ++i) acc[2 * d][i] = mfma16x16x32(as_f16x8(lo), as_f16x8(dz[i]), acc[2 * d][i]);
+#pragma unroll
+            for (int i = 0; i < CT; ++i)
+                acc[2 * d + 1][i] = mfma16x16x32(as_f16x8(hi), as_f16x8(dz[i]), acc[2 * d + 1][i]);
+        }
+    };
+    auto times_power = [&](u32x4 (&w)[8]) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const f16 q = scale_power(scale[r]);
+            const f16x8 p = {q, q, q, q, q, q, q, q};
+            w[r] = as_u32x4(as_f16x8(w[r]) * p);
+        }
+    };
+
+    load_codes(c0);
+    load_scales(c0);
+    load_dz(c0);
+    if constexpr (SCHEME == kScheme2x8) {   // slot (2 k + m) 8 + r: codeword k of codebook m
+#pragma unroll
+        for (int it = 0; it < kBCbBytes / 16 / kBThreads; ++it) {
+            const int km = (it * kBThreads + tid) / 8;
+            __builtin_amdgcn_global_load_lds(
+                (const void*)(codebooks + (size_t)((km & 1) * kCodewords2x8 + (km >> 1)) * kGroup),
+                lds_ptr(smem + it * kBThreads + wave * kWave), 16, 0, 0);
+        }
+        __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+        __syncthreads();
+    }
+    for (int c = c0; c < c_end; c += kBWaves) {
+        u32x4 w[8];
+        if constexpr (SCHEME == kScheme2x8) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const uint32_t sel = m == 0 ? 0x0c0c0004u | (mA << 8) : 0x0c0c0005u | ((mA ^ 1u) << 8);
+                    w[r] = lds16(__builtin_amdgcn_perm(base, (uint32_t)code[r], sel));
+                }
+                if (m == 1) load_codes(c + kBWaves);
+                times_power(w);
+                if (m == 1) load_scales(c + kBWaves);
+                multiply(w);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) w[r] = load16(codebooks + (size_t)code[r] * kGroup);
+            load_codes(c + kBWaves);
+            times_power(w);
+            load_scales(c + kBWaves);
+            multiply(w);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        load_dz(c + kBWaves);
+    }
+
+    // The waves' sums, in LDS [wave][t][i][r][lane], added in wave order; kH inputs t at a time.
+    // Thread (combination (i, r) of its wave, lane): group 4 kq + r, token 16 i + lane % 16.
+    constexpr int kH = CT == 4 ? 4 : 8;
+    float* red = reinterpret_cast<float*>(smem);
+    const size_t part = (size_t)((l * a.splits) + split);
+#pragma unroll
+    for (int h = 0; h < 8 / kH; ++h) {
+        __syncthreads();   // the codebooks, or the half before, are read
+#pragma unroll
+        for (int t = 0; t < kH; ++t)
+#pragma unroll
+            for (int i = 0; i < CT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    red[(((wave * kH + t) * CT + i) * 4 + r) * 64 + lane] = acc[h * kH + t][i][r];
+        __syncthreads();
+        for (int q = wave; q < 4 * CT; q += kBWaves) {
+            const int i = q >> 2, r = q & 3;
+            const int tok = (tt * CT + i) * 16 + lrow, grp = cb * kBGroups + 4 * kq + r;
+            float s[kH];
+#pragma unroll
+            for (int t = 0; t < kH; ++t) {
+                s[t] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kBWaves; ++w) s[t] += red[(((w * kH + t) * CT + i) * 4 + r) * 64 + lane];
+            }
+            if (tok < a.T) {
+                f32x4* dst = reinterpret_cast<f32x4*>(a.partial + (part * a.T + tok) * a.ip + 8 * (size_t)grp + h * kH);
+#pragma unroll
+                for (int k = 0; k < kH / 4; ++k) dst[k] = f32x4{s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]};
+            }
+        }
+    }
+}
+
+struct BackPlan {
+    int ct, n_tt, n_cb, splits;
+};
+
+// Token tiles of 16, 32 or 64 tokens; the rows are split until the workgroups, one a CU, run
+// in the fewest rounds of chunks (each part costs its write and its addition).
+BackPlan back_plan(int n, int64_t out, int64_t in, int64_t batch) {
+    BackPlan p;
+    p.ct = batch <= 16 ? 1 : batch <= 32 ? 2 : 4;
+    p.n_tt = (int)((batch + 16 * p.ct - 1) / (16 * p.ct));
+    p.n_cb = (int)((in / kGroup + kBGroups - 1) / kBGroups);
+    const int64_t n_chunks = (out + 63) / 64 * 2, wgs = (int64_t)p.n_cb * n * p.n_tt;
+    int64_t best = INT64_MAX;
+    p.splits = 1;
+    for (int s = 1; s <= 32 && s <= n_chunks; ++s) {
+        const int64_t rounds = (wgs * s + kSkinnyWorkgroups - 1) / kSkinnyWorkgroups;
+        // in chunks of a wave: the rounds' chunks, three for a round's start and end, the parts
+        const int64_t cost = 4 * rounds * ((n_chunks + 8 * s - 1) / (8 * s) + 3) + s * n * p.n_tt * p.ct / 2;
+        if (cost < best) {
+            best = cost;
+            p.splits = s;
+        }
+    }
+    return p;
+}
+
+template <int SCHEME, int CT>
+hipError_t launch_back(const BackArgs& a, int grid, hipStream_t stream) {
+    auto kern = skinny_back_kernel<SCHEME, CT>;
+    constexpr size_t sums = (size_t)kBWaves * (CT == 4 ? 4 : 8) * CT * 4 * 64 * 4;
+    constexpr size_t lds = SCHEME == kScheme2x8 && sums < kBCbBytes ? kBCbBytes : sums;
+    static_assert(lds <= 163840, "LDS budget");
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(kBThreads), lds, stream, a);
+    return hipGetLastError();
+}
+
+template <int SCHEME>
+hipError_t launch_ct(int ct, const BackArgs& a, int grid, hipStream_t stream) {
+    return ct == 1 ? launch_back<SCHEME, 1>(a, grid, stream)
+         : ct == 2 ? launch_back<SCHEME, 2>(a, grid, stream) : launch_back<SCHEME, 4>(a, grid, stream);
+}
+
+}  // namespace
+
+bool skinny_back_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch) {
+    const bool two = sc.M == 2 && sc.B == 8 && sc.g == 8, one = sc.M == 1 && sc.B == 16 && sc.g == 8;
+    if (!two && !one) return false;
+    return batch <= (two ? kSkinnyBackMaxBatch2x8 : kSkinnyBackMaxBatch1x16);
+}
+
+int64_t skinny_back_partial_bytes(int n, int64_t out, int64_t in, int64_t batch) {
+    const BackPlan p = back_plan(n, out, in, batch);
+    return (int64_t)p.splits * n * batch * p.n_cb * kBGroups * kGroup * 4;
+}
+
+hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, void* partial, void* dx,
+                              int64_t out, int64_t in, int64_t op, int64_t batch, const BiasSum& bias,
+                              hipStream_t stream) {
+    const BackPlan p = back_plan(L.n, out, in, batch);
+    BackArgs a = {};
+    for (int l = 0; l < L.n; ++l) {
+        a.codes[l] = static_cast<const uint8_t*>(L.codes[l]);
+        a.codebooks[l] = static_cast<const f16*>(L.codebooks[l]);
+        a.scales[l] = static_cast<const f16*>(L.scales[l]);
+    }
+    a.dz = static_cast<const f16*>(dz);
+    a.partial = static_cast<float*>(partial);
+    a.out = (int)out;
+    a.op = (int)op;
+    a.G = (int)(in / kGroup);
+    a.T = (int)batch;
+    a.n = L.n;
+    a.ip = p.n_cb * kBGroups * kGroup;
+    a.n_cb = p.n_cb;
+    a.splits = p.splits;
+    const int64_t grid = (int64_t)p.n_cb * L.n * p.splits * p.n_tt;
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    const hipError_t e = sc.B == 8 ? launch_ct<kScheme2x8>(p.ct, a, (int)grid, stream)
+                                   : launch_ct<kScheme1x16>(p.ct, a, (int)grid, stream);
+    if (e != hipSuccess) return e;
+    const Epilogue plain = {{nullptr, nullptr}, nullptr, {nullptr, nullptr}, dx, kActNone};
+    return launch_finish(1, a.partial, nullptr, plain, in, a.ip, batch, L.n * p.splits, bias, stream);
+}
+
+}  // namespace aqlm

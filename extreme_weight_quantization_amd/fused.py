@@ -16,6 +16,7 @@ import ctypes
 
 import torch
 
+from . import binding
 from .binding import SliceLists, _check, lists_fused_workspace_bytes, load_library
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # aqlm_act
@@ -31,7 +32,7 @@ def _act(act):
 
 def _tensor(name, t, dev, shape, dtype=_F16):
     """t is a contiguous `dtype` tensor of `shape` on dev; its address."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}")
     if t.device != dev:
         raise ValueError(f"tensors are on different devices: {name} on {t.device}, not {dev}")
@@ -47,15 +48,20 @@ def _layer(codes, codebooks, scales, dev):
     if codebooks.dim() != 3 or codes.dim() != 3:
         raise ValueError("codes must be [out][in/g][M] and codebooks [M][2^B][g]")
     M, K, g = codebooks.shape
+    out, G, m = codes.shape
     B = K.bit_length() - 1
     if K != 1 << B:
         raise ValueError("the codebook size must be a power of two")
-    out, G, m = codes.shape
     if m != M:
         raise ValueError(f"codes hold {m} codes per group but there are {M} codebooks")
-    return ((M, B, g), out, G * g,
-            (_tensor("codes", codes, dev, (out, G, M), _U8 if B <= 8 else _I16),
-             _tensor("codebooks", codebooks, dev, (M, K, g)), _tensor("scales", scales, dev, (out,))))
+    # one test for the usual case: these calls are made thousands of times a second
+    if (codes.dtype is not (_U8 if B <= 8 else _I16) or codebooks.dtype is not _F16 or scales.dtype is not _F16
+            or scales.shape != (out,) or codes.device != dev or codebooks.device != dev or scales.device != dev
+            or not codes.is_contiguous() or not codebooks.is_contiguous() or not scales.is_contiguous()):
+        _tensor("codes", codes, dev, (out, G, M), _U8 if B <= 8 else _I16)
+        _tensor("codebooks", codebooks, dev, (M, K, g))
+        _tensor("scales", scales, dev, (out,))
+    return (M, B, g), out, G * g, (codes.data_ptr(), codebooks.data_ptr(), scales.data_ptr())
 
 
 def _rows(name, x):
@@ -86,13 +92,24 @@ def _workspace(workspace, need, dev):
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
-def _call(fn, dev, *args):
-    """fn(..., stream) with `dev` current: kernels launch on the device of their tensors."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+# torch.cuda.current_stream builds a Stream object (1.9 us); the raw getter is what it asks
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
+def _call(name, dev, *args):
+    """The library's `name`(..., stream) with `dev` current: kernels launch on the device of their tensors."""
+    fn = getattr(binding._lib or load_library(), name)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _check(status)
 
 
 def _bytes(name, *shape) -> int:
@@ -147,7 +164,7 @@ def aqlm_linear_act(codes, codebooks, scales, x, act="none", bias=None, residual
     pz = _optional("z", z, dev, (batch, out))
     y, py = _output("y", y, dev, (batch, out))
     keep, ws, nws = _workspace(workspace, lambda: linear_act_workspace_bytes(*sch, out, n_in, batch), dev)
-    _call(load_library().aqlm_linear_act, dev, *layer, px, pb, pr, pz, py, ws, nws, a, *sch, out, n_in, batch)
+    _call("aqlm_linear_act", dev, *layer, px, pb, pr, pz, py, ws, nws, a, *sch, out, n_in, batch)
     return y
 
 
@@ -163,7 +180,7 @@ def aqlm_gated(gate, up, x, act="silu", gate_bias=None, up_bias=None, zg=None, z
     z = _pair(_optional("zg", zg, dev, (batch, out)), _optional("zu", zu, dev, (batch, out)))
     y, py = _output("y", y, dev, (batch, out))
     keep, ws, nws = _workspace(workspace, lambda: gated_workspace_bytes(*sch, out, n_in, batch), dev)
-    _call(load_library().aqlm_gated, dev, codes, codebooks, scales, px, bias, z, py, ws, nws, a, *sch, out, n_in, batch)
+    _call("aqlm_gated", dev, codes, codebooks, scales, px, bias, z, py, ws, nws, a, *sch, out, n_in, batch)
     return y
 
 
@@ -180,7 +197,7 @@ def aqlm_linear_act_backward(codes, codebooks, scales, dy, act="none", z=None, n
     dbias = torch.empty((out,), dtype=_F16, device=dev) if need_dbias else None
     dx, px = _output("dx", dx, dev, (batch, n_in))
     keep, ws, nws = _workspace(workspace, lambda: linear_act_backward_workspace_bytes(*sch, out, n_in, batch), dev)
-    _call(load_library().aqlm_linear_act_backward, dev, *layer, pd, pz, px, dbias.data_ptr() if need_dbias else None,
+    _call("aqlm_linear_act_backward", dev, *layer, pd, pz, px, dbias.data_ptr() if need_dbias else None,
           ws, nws, a, *sch, out, n_in, batch)
     return dx, dbias
 
@@ -196,11 +213,11 @@ def aqlm_gated_backward(gate, up, dy, zg, zu, act="silu", need_dbias=False, dx=N
     z = _pair(_tensor("zg", zg, dev, (batch, out)), _tensor("zu", zu, dev, (batch, out)))
     dbg = dbu = db = None
     if need_dbias:
-        dbg, dbu = (torch.empty((out,), dtype=_F16, device=dev) for _ in range(2))
+        dbg, dbu = torch.empty((2, out), dtype=_F16, device=dev).unbind(0)
         db = _pair(dbg.data_ptr(), dbu.data_ptr())
     dx, px = _output("dx", dx, dev, (batch, n_in))
     keep, ws, nws = _workspace(workspace, lambda: gated_backward_workspace_bytes(*sch, out, n_in, batch), dev)
-    _call(load_library().aqlm_gated_backward, dev, codes, codebooks, scales, pd, z, px, db, ws, nws, a, *sch, out, n_in,
+    _call("aqlm_gated_backward", dev, codes, codebooks, scales, pd, z, px, db, ws, nws, a, *sch, out, n_in,
           batch)
     return dx, dbg, dbu
 
@@ -234,7 +251,7 @@ def aqlm_linear_act_lists(lists, codebooks, scales, x, act="none", bias=None, re
     pz = _optional("z", z, dev, (batch, out))
     y, py = _output("y", y, dev, (batch, out))
     keep, ws, nws = _workspace(workspace, lambda: lists_fused_workspace_bytes([out], n_in), dev)
-    _call(load_library().aqlm_linear_act_lists, dev, table, entries, n_entries, cb, s, px, pb, pr, pz, py, ws, nws, a,
+    _call("aqlm_linear_act_lists", dev, table, entries, n_entries, cb, s, px, pb, pr, pz, py, ws, nws, a,
           1, 16, 8, out, n_in, batch)
     return y
 
@@ -252,7 +269,7 @@ def aqlm_gated_lists(gate, up, x, act="silu", gate_bias=None, up_bias=None, zg=N
     z = _pair(_optional("zg", zg, dev, (batch, out)), _optional("zu", zu, dev, (batch, out)))
     y, py = _output("y", y, dev, (batch, out))
     keep, ws, nws = _workspace(workspace, lambda: lists_fused_workspace_bytes([out, out], n_in), dev)
-    _call(load_library().aqlm_gated_lists, dev, _pair(g[0], u[0]), _pair(g[1], u[1]),
+    _call("aqlm_gated_lists", dev, _pair(g[0], u[0]), _pair(g[1], u[1]),
           (ctypes.c_int64 * 2)(g[2], u[2]), _pair(g[3], u[3]), _pair(g[4], u[4]), px, bias, z, py, ws, nws, a, 1, 16, 8,
           out, n_in, batch)
     return y
