@@ -80,15 +80,15 @@ BackwardPlan backward_plan(int n, int act, const GenericScheme& sc, int64_t out,
     if (p.skinny) {
         p.grad = true;
         p.dz = parts.add(batch, n * p.op, 2);
-        p.partial = parts.add(grad_chunks(batch), n * out, 4);
-        p.parts = out == 0 || batch == 0 ? 0 : parts.add(skinny_back_partial_bytes(n, out, in, batch), 1, 1);
+        p.partial = parts.add(grad_chunks(out, batch), n * out, 4);
+        p.parts = out == 0 || batch == 0 ? 0 : parts.add(skinny_back_partial_bytes(sc, n, out, in, batch), 1, 1);
         p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
         return p;
     }
     p.grad = n > 1 || act != kActNone || p.op != out;
     p.wt = parts.add(in, n * p.op, 2);
     p.dz = parts.add(batch, n * p.op, 2);
-    p.partial = parts.add(grad_chunks(batch), n * out, 4);
+    p.partial = parts.add(grad_chunks(out, batch), n * out, 4);
     p.parts = parts.add(dense_partial_bytes(1, in, n * p.op, batch), 1, 1);
     p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
     return p;
@@ -107,7 +107,7 @@ int check_sizes(int act, int M, int B, int g, int64_t out, int64_t in, int64_t b
     if ((uint64_t)op * (uint64_t)(kp / 8) > UINT32_MAX || (uint64_t)out * (uint64_t)(in / g) > UINT32_MAX)
         return AQLM_ERR_SHAPE;
     const int64_t bt = (batch + 255) / 256, wide = op > kp ? op : kp;
-    if ((wide / 64 + 8) * bt > INT32_MAX / 2 || grad_chunks(batch) * (op / 512 + 1) > INT32_MAX) return AQLM_ERR_SHAPE;
+    if ((wide / 64 + 8) * bt > INT32_MAX / 2 || grad_chunks(out, batch) * (op / 512 + 1) > INT32_MAX) return AQLM_ERR_SHAPE;
     return AQLM_OK;
 }
 
@@ -207,7 +207,7 @@ int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx,
     BiasSum bias = {};   // added by the launch that finishes dx, or by one of its own
     if (want_bias)
         bias = BiasSum{reinterpret_cast<const float*>(base + p.partial),
-                       {static_cast<f16*>(dbias[0]), static_cast<f16*>(dbias[1])}, L.n, (int)out, (int)grad_chunks(batch)};
+                       {static_cast<f16*>(dbias[0]), static_cast<f16*>(dbias[1])}, L.n, (int)out, (int)grad_chunks(out, batch)};
     if (p.skinny)
         return finish(launch_skinny_back(GenericScheme{M, B, g}, L, base + p.dz, base + p.parts, dx, out, in, p.op, batch,
                                          bias, s));

@@ -20,10 +20,13 @@ namespace aqlm {
 
 namespace {
 
-// Tokens per wave, all loaded before any is used: 4, or 1 for batches too small to fill the CUs
-// (8 tokens of 4096 gated rows: 10.2 us with 4).
-constexpr int grad_wave_tokens(int64_t batch) { return batch <= 128 ? 1 : 4; }
-constexpr int kGradCols = 512;                       // columns per workgroup: 64 lanes of 8
+constexpr int kGradCols = 512;   // columns per workgroup: 64 lanes of 8
+
+// Tokens per wave, all loaded before any is used: 4, or 1 where that leaves fewer than two
+// workgroups a CU (8 tokens of 4096 gated rows: 10.2 us with 4, 6.0 with 1).
+int grad_wave_tokens(int64_t out, int64_t batch) {
+    return (out + kGradCols - 1) / kGradCols * ((batch + 15) / 16) < 512 ? 1 : 4;
+}
 
 struct GradArgs {
     const f16* dy;
@@ -159,8 +162,8 @@ hipError_t launch_zero16(void* p, int64_t n, hipStream_t stream) {
     return hipGetLastError();
 }
 
-int64_t grad_chunks(int64_t batch) {
-    const int64_t per = 4 * grad_wave_tokens(batch);
+int64_t grad_chunks(int64_t out, int64_t batch) {
+    const int64_t per = 4 * grad_wave_tokens(out, batch);
     return (batch + per - 1) / per;
 }
 
@@ -177,11 +180,11 @@ hipError_t launch_act_grad(const void* dy, const void* const* z, const void* con
     a.out = (int)out;
     a.op = (int)op;
     a.T = (int)batch;
-    const int64_t chunks = grad_chunks(batch), n_cols = (op + kGradCols - 1) / kGradCols;
+    const int64_t chunks = grad_chunks(out, batch), n_cols = (op + kGradCols - 1) / kGradCols;
     if (chunks * n_cols > INT32_MAX) return hipErrorInvalidValue;
     a.n_cols = (int)n_cols;
     const dim3 grid((unsigned)(chunks * n_cols));
-    auto kern = grad_kernel(n, act, grad_wave_tokens(batch));
+    auto kern = grad_kernel(n, act, grad_wave_tokens(out, batch));
     hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }

@@ -62,10 +62,10 @@ hipError_t launch_finish(int n, const float* partial, const void* const* scales,
 // Gradients of the pre-activations, fp16, as the dense product's x: dz[t][l * op + i] for
 // i < op (rows past `out` zero).  One layer: dy act'(z); two: dy zu act'(zg) and dy act(zg).
 // mant: scales whose mantissas (scale_rest) multiply the fp16 result (NULL: none).
-// partial: fp32 [grad_chunks(batch)][n][out]: sums over chunks of tokens of the unscaled
+// partial: fp32 [grad_chunks(out, batch)][n][out]: sums over chunks of tokens of the unscaled
 // fp32 gradients (NULL: not wanted); launch_bias_sum, or the launch that finishes a
 // product from parts, adds the chunks.
-int64_t grad_chunks(int64_t batch);
+int64_t grad_chunks(int64_t out, int64_t batch);
 hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* mant, int n, int act, void* dz,
                            float* partial, int64_t out, int64_t op, int64_t batch, hipStream_t stream);
 hipError_t launch_bias_sum(const BiasSum& b, hipStream_t stream);
@@ -95,7 +95,7 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
 constexpr int kSkinnyBackMaxBatch2x8 = 256;
 constexpr int kSkinnyBackMaxBatch1x16 = 128;
 bool skinny_back_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch);
-int64_t skinny_back_partial_bytes(int n, int64_t out, int64_t in, int64_t batch);
+int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
 hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, void* partial, void* dx,
                               int64_t out, int64_t in, int64_t op, int64_t batch, const BiasSum& bias,
                               hipStream_t stream);

@@ -14,8 +14,8 @@
 //    multiplies the codewords in fp16, exactly but for subnormals, the mantissa is in dz (act_grad.hip), which is
 //    rounded to fp16 anyway.  2x8 multiplies its two codewords one by one, so no weight
 //    is rounded.
-//  * A workgroup of 8 waves owns 16 groups (128 inputs) of dx and a part of the rows of one
-//    layer; its waves take every eighth chunk of 32 rows, each with the next chunk's codes and dz
+//  * A workgroup of 8 waves (4 at 128 tokens) owns 16 groups (128 inputs) of dx and a part of the rows of one
+//    layer; its waves take the chunks of 32 rows in turn, each with the next chunk's codes and dz
 //    in flight and no barrier, and add their sums in LDS in wave order.  Its fp32 part of dx goes to
 //    the workspace; skinny_finish_kernel adds the parts in order and rounds once.
 //  * 2x8 codebooks: LDS, 8 replicas, read without bank conflicts as in gemv.hip.  1x16
@@ -31,11 +31,15 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kBWaves = 8;
-constexpr int kBThreads = kBWaves * kWave;
+// Waves of a workgroup by its column tiles of tokens: 8, or 4 with twice the registers a lane, which
+// hold the sums of 128 tokens (1x16: one gather of a code serves them all).
+constexpr int back_waves(int ct) { return ct == 8 ? 4 : 8; }
 constexpr int kBGroups = 16;                                 // groups a workgroup
 constexpr int kBRows = 32;                                   // rows a chunk
 constexpr int kBCbBytes = 2 * kCodewords2x8 * 8 * 16;         // 64 KB: 8 replicas
+
+// Inputs t of the groups whose sums share the LDS at a time (128 KB at most).
+constexpr int back_half(int ct) { return ct >= 4 ? 4 : 8; }
 
 struct BackArgs {
     const uint8_t* codes[2];
@@ -51,8 +55,9 @@ __device__ __forceinline__ u32x4 lds16(uint32_t byte) {
 }
 
 template <int SCHEME, int CT>
-__global__ __launch_bounds__(kBThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void skinny_back_kernel(
-    const BackArgs a) {
+__global__ __launch_bounds__(64 * back_waves(CT))
+    __attribute__((amdgpu_waves_per_eu(back_waves(CT) / 4, back_waves(CT) / 4))) void skinny_back_kernel(const BackArgs a) {
+    constexpr int kBWaves = back_waves(CT), kBThreads = 64 * kBWaves;
     extern __shared__ u32x4 smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lrow = lane & 15, kq = lane >> 4;
@@ -165,7 +170,7 @@ __global__ __launch_bounds__(kBThreads) __attribute__((amdgpu_waves_per_eu(2, 2)
 
     // The waves' sums, in LDS [wave][t][i][r][lane], added in wave order; kH inputs t at a time.
     // Thread (combination (i, r) of its wave, lane): group 4 kq + r, token 16 i + lane % 16.
-    constexpr int kH = CT == 4 ? 4 : 8;
+    constexpr int kH = back_half(CT);
     float* red = reinterpret_cast<float*>(smem);
     const size_t part = (size_t)((l * a.splits) + split);
 #pragma unroll
@@ -202,22 +207,26 @@ struct BackPlan {
     int ct, n_tt, n_cb, splits;
 };
 
-// Token tiles of 16, 32 or 64 tokens; the rows are split until the workgroups, one a CU, run
-// in the fewest rounds of chunks (each part costs its write and its addition).
-BackPlan back_plan(int n, int64_t out, int64_t in, int64_t batch) {
+// Token tiles of 16, 32 or 64 tokens, or 128 for 1x16.  The rows are split over as many workgroups as take the
+// fewest microseconds: rounds of one workgroup a CU, each some time to start and end and
+// kChunkUs per chunk of a wave (1x16: 4096 gathers of the workgroup's waves, at the rate a CU gets), then the parts,
+// written and added.
+BackPlan back_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
+    const bool two = sc.M == 2;
     BackPlan p;
-    p.ct = batch <= 16 ? 1 : batch <= 32 ? 2 : 4;
+    p.ct = batch <= 16 ? 1 : batch <= 32 ? 2 : batch <= 64 || two ? 4 : 8;
     p.n_tt = (int)((batch + 16 * p.ct - 1) / (16 * p.ct));
     p.n_cb = (int)((in / kGroup + kBGroups - 1) / kBGroups);
-    const int64_t n_chunks = (out + 63) / 64 * 2, wgs = (int64_t)p.n_cb * n * p.n_tt;
-    int64_t best = INT64_MAX;
+    const int64_t n_chunks = (out + 63) / 64 * 2, wgs = (int64_t)p.n_cb * n * p.n_tt, waves = back_waves(p.ct);
+    const double chunk_us = two ? (p.ct == 4 ? 1.8 : 1.2) : p.ct == 8 ? 3.0 : 4.5;
+    const double part_us = 0.15 * n + (double)n * batch * p.n_cb * kBGroups * kGroup * 8 / 3e6;
+    double best = 1e300;
     p.splits = 1;
     for (int s = 1; s <= 32 && s <= n_chunks; ++s) {
         const int64_t rounds = (wgs * s + kSkinnyWorkgroups - 1) / kSkinnyWorkgroups;
-        // in chunks of a wave: the rounds' chunks, three for a round's start and end, the parts
-        const int64_t cost = 4 * rounds * ((n_chunks + 8 * s - 1) / (8 * s) + 3) + s * n * p.n_tt * p.ct / 2;
-        if (cost < best) {
-            best = cost;
+        const double us = rounds * ((double)((n_chunks + waves * s - 1) / (waves * s)) * chunk_us + 4.0) + s * part_us;
+        if (us < best) {
+            best = us;
             p.splits = s;
         }
     }
@@ -227,17 +236,20 @@ BackPlan back_plan(int n, int64_t out, int64_t in, int64_t batch) {
 template <int SCHEME, int CT>
 hipError_t launch_back(const BackArgs& a, int grid, hipStream_t stream) {
     auto kern = skinny_back_kernel<SCHEME, CT>;
-    constexpr size_t sums = (size_t)kBWaves * (CT == 4 ? 4 : 8) * CT * 4 * 64 * 4;
+    constexpr size_t sums = (size_t)back_waves(CT) * back_half(CT) * CT * 4 * 64 * 4;
     constexpr size_t lds = SCHEME == kScheme2x8 && sums < kBCbBytes ? kBCbBytes : sums;
     static_assert(lds <= 163840, "LDS budget");
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(kBThreads), lds, stream, a);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * back_waves(CT)), lds, stream, a);
     return hipGetLastError();
 }
 
 template <int SCHEME>
 hipError_t launch_ct(int ct, const BackArgs& a, int grid, hipStream_t stream) {
+    if constexpr (SCHEME == kScheme1x16) {
+        if (ct == 8) return launch_back<SCHEME, 8>(a, grid, stream);
+    }
     return ct == 1 ? launch_back<SCHEME, 1>(a, grid, stream)
          : ct == 2 ? launch_back<SCHEME, 2>(a, grid, stream) : launch_back<SCHEME, 4>(a, grid, stream);
 }
@@ -250,15 +262,15 @@ bool skinny_back_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_
     return batch <= (two ? kSkinnyBackMaxBatch2x8 : kSkinnyBackMaxBatch1x16);
 }
 
-int64_t skinny_back_partial_bytes(int n, int64_t out, int64_t in, int64_t batch) {
-    const BackPlan p = back_plan(n, out, in, batch);
+int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
+    const BackPlan p = back_plan(sc, n, out, in, batch);
     return (int64_t)p.splits * n * batch * p.n_cb * kBGroups * kGroup * 4;
 }
 
 hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, void* partial, void* dx,
                               int64_t out, int64_t in, int64_t op, int64_t batch, const BiasSum& bias,
                               hipStream_t stream) {
-    const BackPlan p = back_plan(L.n, out, in, batch);
+    const BackPlan p = back_plan(sc, L.n, out, in, batch);
     BackArgs a = {};
     for (int l = 0; l < L.n; ++l) {
         a.codes[l] = static_cast<const uint8_t*>(L.codes[l]);
