@@ -50,14 +50,16 @@ __device__ __forceinline__ u32x4 load16(const void* p) {
 }
 
 // 8 two-byte codes from element `at` of an array of `total` >= 8, in one 16-byte load whatever
-// the alignment (global loads take any address).  Codes past the array read as zero or repeat;
-// the caller does not use them.
-__device__ __forceinline__ u32x4 load_codes_any(const uint16_t* __restrict__ codes, size_t at, size_t total) {
+// the alignment (global loads take any address).  Near the array's end the load is moved back
+// into it, and settle_codes moves the codes into place; codes past the end come out as zero or
+// repeated, and the caller does not use them.
+__device__ __forceinline__ u32x4 load_codes_raw(const uint16_t* __restrict__ codes, size_t at, size_t total) {
     typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-    const size_t p = min(at, total - 8);
-    const u32x4_any c = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(codes + p));
-    u32x4 v = {c[0], c[1], c[2], c[3]};
-    const uint32_t d = (uint32_t)min(at - p, (size_t)7);   // elements the load was moved back by
+    const u32x4_any c = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(codes + min(at, total - 8)));
+    return u32x4{c[0], c[1], c[2], c[3]};
+}
+__device__ __forceinline__ u32x4 settle_codes(u32x4 v, size_t at, size_t total) {
+    const uint32_t d = at <= total - 8 ? 0u : (uint32_t)min(at - (total - 8), (size_t)7);   // elements moved back by
     if (d & 1u)
         v = u32x4{(uint32_t)__builtin_amdgcn_alignbit(v[1], v[0], 16), (uint32_t)__builtin_amdgcn_alignbit(v[2], v[1], 16),
                   (uint32_t)__builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};

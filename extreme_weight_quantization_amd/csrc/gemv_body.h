@@ -99,7 +99,8 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* __restrict__ codes, i
     const int r = min(row, out - 1);
     if constexpr (!VEC && KIND != kGemvPlain) {
         const size_t total = (size_t)out * G;
-        if (total >= 8) return load_codes_any(reinterpret_cast<const uint16_t*>(codes), (size_t)r * G + g0, total);
+        const size_t at = (size_t)r * G + g0;
+        if (total >= 8) return settle_codes(load_codes_raw(reinterpret_cast<const uint16_t*>(codes), at, total), at, total);
     }
     const uint16_t* c16 = reinterpret_cast<const uint16_t*>(codes) + (size_t)r * G;
     if constexpr (VEC) {

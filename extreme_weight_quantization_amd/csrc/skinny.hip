@@ -44,6 +44,21 @@ constexpr int skinny_stages(int bm) { return bm == 128 ? 2 : 3; }
 constexpr int kKRepl = 8;                                   // 2x8 codebook replicas in LDS
 constexpr int kKCbBytes = 2 * kCodewords2x8 * kKRepl * 16;   // 64 KB
 
+// `units` dealt to W workgroups in contiguous runs of q or q + 1 (units = q W + r): workgroup w
+// begins at floor(w units / W) = w q + floor(w r / W).  W <= kSkinnyWorkgroups, so w r fits 32 bits.
+struct Runs {
+    int units, W, q, r;
+};
+__device__ __forceinline__ int run_begin(int w, const Runs& v) { return w * v.q + (int)((uint32_t)(w * v.r) / (uint32_t)v.W); }
+// The workgroup whose run holds unit u: an estimate within one (u < 2^30: a float quotient times
+// at most 256 is off by far less), then exact.
+__device__ __forceinline__ int run_of(int u, const Runs& v) {
+    int w = min((int)((float)u * ((float)v.W / (float)v.units)), v.W - 1);
+    if (run_begin(w, v) > u) --w;
+    if (w + 1 < v.W && run_begin(w + 1, v) <= u) ++w;
+    return w;
+}
+
 struct SkinnyArgs {
     const uint8_t* codes[2];
     const f16* codebooks[2];
@@ -51,14 +66,8 @@ struct SkinnyArgs {
     float* partial;   // [slot][t][l][op]
     int out, op, G, T;
     int n_slab, n_blk;   // slabs of a row; row blocks
-    int units;           // token tiles x row blocks x slabs
+    Runs runs;           // of token tiles x row blocks x slabs
 };
-
-// First unit of workgroup w, and the workgroup of unit u, of W equal contiguous runs.
-__host__ __device__ __forceinline__ int run_begin(int w, int W, int units) { return (int)((int64_t)w * units / W); }
-__host__ __device__ __forceinline__ int run_of(int u, int W, int units) {
-    return (int)((((int64_t)u + 1) * W - 1) / units);
-}
 
 // 16 bytes of the workgroup's LDS (dynamic only, so it starts at address 0).
 __device__ __forceinline__ u32x4 lds16(uint32_t byte) {
@@ -98,8 +107,8 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     const uint16_t* codes = reinterpret_cast<const uint16_t*>(up ? a.codes[1] : a.codes[0]);
     const f16* codebooks = up ? a.codebooks[1] : a.codebooks[0];
     const int G = a.G, n_slab = a.n_slab;
-    const int W = gridDim.x, wid = blockIdx.x;
-    const int u0 = run_begin(wid, W, a.units), n = run_begin(wid + 1, W, a.units) - u0;   // n >= 1: W <= units
+    const int wid = blockIdx.x;
+    const int u0 = run_begin(wid, a.runs), n = run_begin(wid + 1, a.runs) - u0;   // n >= 1: W <= units
 
     // a unit is (token tile t, row block b, slab s), s fastest
     struct Unit { int t, b, s; };
@@ -109,23 +118,28 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
         v.b = col ? 0 : v.b + (row ? 1 : 0);
         v.t += col ? 1 : 0;
     };
-    // the unit of step `at`; past the last step it stays
+    // the unit of step `at`
     struct Ahead { Unit v; int at; };
     auto advance = [&](Ahead& p) {
-        Unit w = p.v;
-        next(w);
-        if (p.at < n - 1) { p.v = w; ++p.at; }
+        next(p.v);
+        ++p.at;
     };
     // the 8 codes of this lane in a unit: rows past the layer repeat its last row (their
-    // outputs are not used), groups past the row its last 8 (masked when used)
-    auto load_codes = [&](const Unit& v, int rt) -> u32x4 {
+    // outputs are not used), groups past the row its last 8 (masked when used); kRowAny: as
+    // loaded, settle_codes puts them in place when they are used
+    auto codes_at = [&](const Unit& v, int rt) -> size_t {
         const int row = min((v.b * kKTiles + wave * RT + rt) * kTileRows + trow, a.out - 1);
         const int g0 = v.s * kKSlab + 8 * kq;
-        if constexpr (ROW != kRowAny) {
-            return load_nt16(codes + (size_t)row * G + min(g0, G - 8));
-        } else {
-            return load_codes_any(codes, (size_t)row * G + g0, (size_t)a.out * G);
-        }
+        return (size_t)row * G + (ROW != kRowAny ? min(g0, G - 8) : g0);
+    };
+    auto load_codes = [&](const Unit& v, int rt) -> u32x4 {
+        if constexpr (ROW != kRowAny) return load_nt16(codes + codes_at(v, rt));
+        return load_codes_raw(codes, codes_at(v, rt), (size_t)a.out * G);
+    };
+    auto settle = [&](const u32x4 (&c)[RT], const Unit& v, u32x4 (&o)[RT]) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+            o[rt] = ROW == kRowAny ? settle_codes(c[rt], codes_at(v, rt), (size_t)a.out * G) : c[rt];
     };
     // x of a unit into a stage: load i of a wave fills slots 64 (wave kNX + i) .. + 63, two tokens;
     // tokens past the batch repeat its last one, groups past the row are zero
@@ -151,22 +165,6 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
                     load16(codebooks + (size_t)((cv[rt][2 * h + (q >> 1)] >> (16 * (q & 1))) & 0xffffu) * kGroup);
     };
 
-    const int blk0 = u0 / n_slab;
-    Unit cur{blk0 / a.n_blk, blk0 % a.n_blk, u0 - blk0 * n_slab};   // the unit multiplied
-    Ahead px{cur, 0}, pc{cur, 0};                                   // the next x tile and codes to load
-    u32x4 ring[kR][RT];   // codes of step k in ring[k % kR]
-    auto load_ring = [&](u32x4 (&r)[RT]) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) r[rt] = load_codes(pc.v, rt);
-        advance(pc);
-    };
-#pragma unroll
-    for (int d = 0; d < kR; ++d) load_ring(ring[d]);
-#pragma unroll
-    for (int d = 0; d < kR - 1; ++d) {
-        load_x(px.v, d);
-        advance(px);
-    }
     if constexpr (SCHEME == kScheme2x8) {
         // slot (2 k + m) 8 + r: codeword k of codebook m (gated: the gate's for r < 4)
 #pragma unroll
@@ -178,8 +176,34 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
                 lds_ptr(smem + it * kThreads + wave * kWave), 16, 0, 0);
         }
     }
+    const int blk0 = (int)((uint32_t)u0 / (uint32_t)n_slab), tile0 = (int)((uint32_t)blk0 / (uint32_t)a.n_blk);
+    Unit cur{tile0, blk0 - tile0 * a.n_blk, u0 - blk0 * n_slab};   // the unit multiplied
+    Ahead px{cur, 0}, pc{cur, 0};                                  // the next x tile and codes to load
+    u32x4 ring[kR][RT];   // codes of step k in ring[k % kR]
+    auto load_ring = [&](u32x4 (&r)[RT]) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) r[rt] = load_codes(pc.v, rt);
+        advance(pc);
+    };
+#pragma unroll
+    for (int d = 0; d < kR; ++d) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) ring[d][rt] = u32x4{0u, 0u, 0u, 0u};
+        if (d < n) load_ring(ring[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < kR - 1; ++d) {
+        if (d < n) {
+            load_x(px.v, d);
+            advance(px);
+        }
+    }
     u32x4 e[2][RT][4] = {};   // 1x16: codewords of the two halves of a step, gathered half a step ahead
-    if constexpr (SCHEME == kScheme1x16) gather(ring[0], 0, e[0]);
+    if constexpr (SCHEME == kScheme1x16) {
+        u32x4 c[RT];
+        settle(ring[0], cur, c);
+        gather(c, 0, e[0]);
+    }
     __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
     __syncthreads();
 
@@ -213,7 +237,8 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
 #pragma unroll
         for (int j = 0; j < kCT; ++j) xv[j] = as_f16x8(lds16(xa + (uint32_t)(j * 16 * kKSlab * 16)));
     };
-    auto multiply = [&](const u32x4 (&cv)[RT], u32x4 (&e)[2][RT][4], const u32x4 (&ahead)[RT], uint32_t xs, int left) {
+    auto multiply = [&](const u32x4 (&cv)[RT], u32x4 (&e)[2][RT][4], const u32x4 (&ahead)[RT], bool more, uint32_t xs,
+                        int left) {
         constexpr bool kTwo = SCHEME == kScheme2x8;
         constexpr int kReads = kCT + (kTwo ? 2 * RT : 0), kProducts = RT * kCT * (kTwo && !SUM ? 2 : 1);
         f16x8 w[2][RT], w2[2][RT], xv[2][kCT];
@@ -247,13 +272,13 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
             }
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (!kTwo) {
-                if (q == 3) gather(ahead, 0, e[0]);   // the first half of the next step's codewords
+                if (q == 3 && more) gather(ahead, 0, e[0]);   // the first half of the next step's codewords
             }
         }
     };
     // the run's part of a row block: lane holds rows 4 kq + r of token l % 16 of each column tile
     auto flush = [&](const Unit& v) {
-        const int first = run_of((v.t * a.n_blk + v.b) * n_slab, W, a.units);
+        const int first = run_of((v.t * a.n_blk + v.b) * n_slab, a.runs);
         const int l = GATED ? kq >> 1 : 0;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -272,33 +297,45 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     };
 
     // Step k: stage and ring slot are fixed in the unrolled round, each register redefined
-    // after its last use, so no wait but for what is used next.
+    // after its last use, so no wait but for what is used next.  Nothing is loaded past the last unit.
     for (int k0 = 0; k0 < n; k0 += kR) {
 #pragma unroll
         for (int d = 0; d < kR; ++d) {
-            if (d > 0 && k0 + d >= n) break;
+            const int k = k0 + d;
+            if (d > 0 && k >= n) break;
             // the address arithmetic stays in the step (hoisted, it would hold 24 registers)
             uint32_t xs = xlane + (uint32_t)(d * kXStage * 16);
             asm volatile("" : "+v"(xs));
-            if constexpr (SCHEME == kScheme1x16) gather(ring[d], 1, e[1]);
-            load_x(px.v, (d + kR - 1) % kR);   // this stage was read last in step k - 1
-            advance(px);
+            u32x4 c[RT], ahead[RT];
+            settle(ring[d], cur, c);
+            Unit after = cur;
+            next(after);
+            if constexpr (SCHEME == kScheme1x16) {
+                settle(ring[(d + 1) % kR], after, ahead);
+                gather(c, 1, e[1]);
+            }
+            if (px.at < n) {
+                load_x(px.v, (d + kR - 1) % kR);   // this stage was read last in step k - 1
+                advance(px);
+            }
             __builtin_amdgcn_sched_barrier(0);
-            multiply(ring[d], e, ring[(d + 1) % kR], xs, G - cur.s * kKSlab - 8 * kq);
-            load_ring(ring[d]);
-            const Unit done = cur;
-            next(cur);
-            if (cur.s == 0 || k0 + d == n - 1) flush(done);
-            // x of step k + 1 has landed: this step issued kIssued loads after it
-            __builtin_amdgcn_sched_barrier(0);
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kIssued < 16 ? kIssued : 15));
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
+            multiply(c, e, ahead, k + 1 < n, xs, G - cur.s * kKSlab - 8 * kq);
+            if (pc.at < n) load_ring(ring[d]);
+            if (after.s == 0 || k == n - 1) flush(cur);
+            cur = after;
+            if (k + 1 < n) {
+                // x of step k + 1 has landed: the kIssued newest loads are later ones, where all
+                // of this step's were issued; near the end everything is waited for
+                __builtin_amdgcn_sched_barrier(0);
+                asm volatile("" ::: "memory");
+                if (k + kR < n) __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kIssued < 16 ? kIssued : 15));
+                else __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     }
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));   // no LDS load in flight at exit
 }
 
 struct FinishArgs {
@@ -309,7 +346,9 @@ struct FinishArgs {
     f16* z[2];
     f16* y;
     int out, op, T, act;
-    int bm, blk_rows, n_slab, n_blk, units, W;   // units 0: W parts everywhere
+    int parts;      // > 0: everywhere; else the runs that share the output's row block
+    int bm, blk_rows, n_slab, n_blk;
+    Runs runs;
     int blocks;     // workgroups of the outputs; those after them add bias sums
     BiasSum sums;
 };
@@ -325,11 +364,13 @@ __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) 
     const int per = a.op / 4;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)a.T * per) return;
-    const int t = (int)(i / per), r0 = 4 * (int)(i - (int64_t)t * per);
-    int parts = a.W;
-    if (a.units > 0) {
+    // the quotient of a product below 2^31 in 32 bits (a 64-bit one costs more than the rest of the thread)
+    const bool small = (int64_t)a.T * per < INT32_MAX;
+    const int t = small ? (int)((uint32_t)i / (uint32_t)per) : (int)(i / per), r0 = 4 * (int)(i - (int64_t)t * per);
+    int parts = a.parts;
+    if (parts == 0) {
         const int blk = (t / a.bm) * a.n_blk + r0 / a.blk_rows;
-        parts = run_of((blk + 1) * a.n_slab - 1, a.W, a.units) - run_of(blk * a.n_slab, a.W, a.units) + 1;
+        parts = run_of((blk + 1) * a.n_slab - 1, a.runs) - run_of(blk * a.n_slab, a.runs) + 1;
     }
     f32x4 sum[N];
 #pragma unroll
@@ -406,7 +447,8 @@ hipError_t launch_finish_args(int n, FinishArgs& f, hipStream_t stream) {
 
 // Geometry of one call.
 struct SkinnyPlan {
-    int bm = 0, blk_rows = 0, op = 0, n_slab = 0, n_blk = 0, units = 0, W = 0, slots = 0;
+    int bm = 0, blk_rows = 0, op = 0, n_slab = 0, n_blk = 0, slots = 0;
+    Runs runs = {};
 };
 
 // Token tiles of up to 64 tokens for 2x8 (its codebooks leave room for three x stages of
@@ -421,10 +463,10 @@ SkinnyPlan skinny_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, 
     p.op = (int)((out + tile - 1) / tile * tile);
     p.n_slab = (int)n_slab;
     p.n_blk = (int)n_blk;
-    p.units = (int)units;
-    p.W = (int)std::min<int64_t>(kSkinnyWorkgroups, units);
+    const int64_t W = std::min<int64_t>(kSkinnyWorkgroups, units);
+    p.runs = Runs{(int)units, (int)W, (int)(units / W), (int)(units % W)};
     // the runs that share a row block: those that its slabs fill, and one cut at each end
-    p.slots = (int)((n_slab * p.W + units - 1) / units + 1);
+    p.slots = (int)((n_slab * W + units - 1) / units + 1);
     return p;
 }
 
@@ -437,7 +479,7 @@ hipError_t launch_main(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t str
     static_assert(lds <= 163840, "LDS budget");
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(p.W), dim3(64 * kKTiles / RT), lds, stream, a);
+    hipLaunchKernelGGL(kern, dim3(p.runs.W), dim3(64 * kKTiles / RT), lds, stream, a);
     return hipGetLastError();
 }
 
@@ -499,10 +541,9 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
     FinishArgs f = finish_args(L.n, a.partial, L.scales, epi, out, p.op, batch);
     f.n_slab = a.n_slab = p.n_slab;
     f.n_blk = a.n_blk = p.n_blk;
-    f.units = a.units = p.units;
+    f.runs = a.runs = p.runs;
     f.bm = p.bm;
     f.blk_rows = p.blk_rows;
-    f.W = p.W;
     const bool two = sc.B == 8, gated = L.n == 2;
     const hipError_t e = two ? (gated ? launch_scheme<kScheme2x8, true>(p, a, stream) : launch_scheme<kScheme2x8, false>(p, a, stream))
                              : (gated ? launch_scheme<kScheme1x16, true>(p, a, stream) : launch_scheme<kScheme1x16, false>(p, a, stream));
@@ -514,7 +555,7 @@ hipError_t launch_finish(int n, const float* partial, const void* const* scales,
                          int64_t op, int64_t batch, int parts, const BiasSum& bias, hipStream_t stream) {
     FinishArgs f = finish_args(n, partial, scales, epi, out, op, batch);
     f.sums = bias;
-    f.W = parts;
+    f.parts = parts;
     return launch_finish_args(n, f, stream);
 }
 
