@@ -68,7 +68,7 @@ ForwardPlan forward_plan(int n, const GenericScheme& sc, int64_t out, int64_t in
 
 struct BackwardPlan {
     int64_t op = 0, wt = 0, dz = 0, partial = 0, parts = 0, bytes = 0;
-    bool grad = false;   // a pass over dy writes dz (else dy itself is the product's operand)
+    bool grad = false;   // a pass over dy writes dz (else the product takes dy itself)
     bool skinny = false;
 };
 
@@ -78,9 +78,11 @@ BackwardPlan backward_plan(int n, int act, const GenericScheme& sc, int64_t out,
     p.op = round_up(out, 64);
     p.skinny = skinny_back_serves(sc, out, in, batch);
     if (p.skinny) {
-        p.grad = true;
-        p.dz = parts.add(batch, n * p.op, 2);
-        p.partial = parts.add(grad_chunks(out, batch), n * out, 4);
+        p.grad = !skinny_back_grads(sc, n, out, in, batch);
+        if (p.grad) {
+            p.dz = parts.add(batch, n * p.op, 2);
+            p.partial = parts.add(grad_chunks(out, batch), n * out, 4);
+        }
         p.parts = out == 0 || batch == 0 ? 0 : parts.add(skinny_back_partial_bytes(sc, n, out, in, batch), 1, 1);
         p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
         return p;
@@ -196,6 +198,11 @@ int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx,
     const int wt = check_workspace(workspace, workspace_bytes, p.bytes);
     if (wt != AQLM_OK) return wt;
     char* base = static_cast<char*>(workspace);
+    if (p.skinny && !p.grad) {   // two launches
+        const BackGrads grads = {dy, {z[0], z[1]}, {dbias[0], dbias[1]}, act};
+        return finish(launch_skinny_back(GenericScheme{M, B, g}, L, nullptr, &grads, base + p.parts, dx, out, in, p.op,
+                                         batch, BiasSum{}, s));
+    }
     const WeightScale ws = (p.skinny || (M == 1 && p.grad)) ? WeightScale::kPow2 : WeightScale::kFull;
     if (p.grad || want_bias) {
         const int r = finish(launch_act_grad(dy, z, ws == WeightScale::kPow2 ? L.scales : nullptr, L.n, act,
@@ -209,7 +216,7 @@ int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx,
         bias = BiasSum{reinterpret_cast<const float*>(base + p.partial),
                        {static_cast<f16*>(dbias[0]), static_cast<f16*>(dbias[1])}, L.n, (int)out, (int)grad_chunks(out, batch)};
     if (p.skinny)
-        return finish(launch_skinny_back(GenericScheme{M, B, g}, L, base + p.dz, base + p.parts, dx, out, in, p.op, batch,
+        return finish(launch_skinny_back(GenericScheme{M, B, g}, L, base + p.dz, nullptr, base + p.parts, dx, out, in, p.op, batch,
                                          bias, s));
     const int r = finish(launch_decode_transposed(GenericScheme{M, B, g}, L, ws, base + p.wt, out, in, p.op, s));
     if (r != AQLM_OK) return r;

@@ -96,9 +96,18 @@ constexpr int kSkinnyBackMaxBatch2x8 = 256;
 constexpr int kSkinnyBackMaxBatch1x16 = 128;
 bool skinny_back_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch);
 int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
-hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, void* partial, void* dx,
-                              int64_t out, int64_t in, int64_t op, int64_t batch, const BiasSum& bias,
-                              hipStream_t stream);
+// skinny_back_grads: the shapes whose dz and bias sums the product computes itself, from grads
+// (then not NULL; dz and bias are not used).
+struct BackGrads {
+    const void* dy;
+    const void* z[2];
+    void* dbias[2];
+    int act;
+};
+bool skinny_back_grads(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
+hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, const BackGrads* grads,
+                              void* partial, void* dx, int64_t out, int64_t in, int64_t op, int64_t batch,
+                              const BiasSum& bias, hipStream_t stream);
 
 // The slice-list product of one layer, or of gate and up, batch 1, with the epilogue in its
 // reduction (gemv_lists.hip).  L as for launch_gemv_lists_fused; its y is not used.

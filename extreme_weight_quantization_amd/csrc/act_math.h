@@ -67,6 +67,24 @@ __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
     }
 }
 
+// v[i] = slope of act at v[i], one branch for all N.
+template <int ACT, int N>
+__device__ __forceinline__ void act_slopes_of(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_slope<ACT>(v[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void act_slopes(int act, float (&v)[N]) {
+    switch (act) {
+        case kActRelu: act_slopes_of<kActRelu>(v); break;
+        case kActSilu: act_slopes_of<kActSilu>(v); break;
+        case kActGelu: act_slopes_of<kActGelu>(v); break;
+        case kActGeluTanh: act_slopes_of<kActGeluTanh>(v); break;
+        default: act_slopes_of<kActNone>(v); break;
+    }
+}
+
 // A row scale s = m 2^e as an fp16 power of two, which goes into the fp16 weights exactly
 // (but for subnormals), and the rest, which goes into the other factor, so that only
 // one of the two is rounded: 1 <= |m| < 2 for normal s, m
@@ -76,6 +94,10 @@ __device__ __forceinline__ f16 scale_power(f16 s) {
     const uint16_t p = (x == 0x7c00u || (b & 0x7fffu) == 0) ? 0x3c00u : x == 0 ? 0x0400u : x;
     return __builtin_bit_cast(f16, p);
 }
-__device__ __forceinline__ float scale_rest(f16 s) { return (float)s / (float)scale_power(s); }
+// (The quotient by a power of two is the product with its reciprocal, exactly.)
+__device__ __forceinline__ float scale_rest(f16 s) {
+    const uint32_t e = (uint32_t)__builtin_bit_cast(uint16_t, scale_power(s)) >> 10;   // 1 .. 30
+    return (float)s * __builtin_bit_cast(float, (142u - e) << 23);
+}
 
 }  // namespace aqlm

@@ -18,6 +18,10 @@
 //    layer; its waves take the chunks of 32 rows in turn, each with the next chunk's codes and dz
 //    in flight and no barrier, and add their sums in LDS in wave order.  Its fp32 part of dx goes to
 //    the workspace; skinny_finish_kernel adds the parts in order and rounds once.
+//  * GRAD: where that is little work (skinny_back_grads) the kernel takes dy and the
+//    pre-activations themselves.  A lane computes the 8 gradients of its operand from 16 bytes of
+//    each, every workgroup anew, and the workgroups of the first 16 groups add them over the
+//    tokens for the bias.  That saves a launch and dz's way through memory.
 //  * 2x8 codebooks: LDS, 8 replicas, read without bank conflicts as in gemv.hip.  1x16
 //    codewords are gathered from L2.
 #include <algorithm>
@@ -48,13 +52,18 @@ struct BackArgs {
     const f16* dz;      // [t][l * op + i], times the scales' mantissas; zero for i >= out
     float* partial;     // [part][t][ip]
     int out, op, G, T, n, ip, n_cb, splits;
+    // GRAD: dz is computed here
+    const f16* dy;
+    const f16* z[2];
+    f16* dbias[2];      // NULL: not wanted
+    int act;
 };
 
 __device__ __forceinline__ u32x4 lds16(uint32_t byte) {
     return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)byte);
 }
 
-template <int SCHEME, int CT>
+template <int SCHEME, int CT, bool GRAD>
 __global__ __launch_bounds__(64 * back_waves(CT))
     __attribute__((amdgpu_waves_per_eu(back_waves(CT) / 4, back_waves(CT) / 4))) void skinny_back_kernel(const BackArgs a) {
     constexpr int kBWaves = back_waves(CT), kBThreads = 64 * kBWaves;
@@ -87,10 +96,47 @@ __global__ __launch_bounds__(64 * back_waves(CT))
 #pragma unroll
         for (int r = 0; r < 8; ++r) scale[r] = scales[min(row0(c) + r, a.out - 1)];
     };
+    u32x4 raw[3] = {};   // GRAD: dy, and the pre-activations, of the lane's rows (out % 8 == 0: all inside or all past)
     auto load_dz = [&](int c) {   // tokens past the batch repeat the last (their sums are not used)
+        if constexpr (GRAD) {
+            const size_t at = (size_t)min(lrow, a.T - 1) * a.out + min(row0(c), a.out - 8);
+            raw[0] = load16(a.dy + at);
+            if (a.n == 2 || a.act != kActNone) raw[1] = load16(a.z[0] + at);
+            if (a.n == 2 && l == 0) raw[2] = load16(a.z[1] + at);
+        } else {
 #pragma unroll
-        for (int i = 0; i < CT; ++i)
-            dz[i] = load16(dzl + (size_t)min((tt * CT + i) * 16 + lrow, a.T - 1) * ldz + row0(c));
+            for (int i = 0; i < CT; ++i)
+                dz[i] = load16(dzl + (size_t)min((tt * CT + i) * 16 + lrow, a.T - 1) * ldz + row0(c));
+        }
+    };
+    // GRAD: dz from raw, fp32 until its one rounding; the bias sums of a chunk's rows
+    auto make_dz = [&](int c) {
+        const f16x8 dy = as_f16x8(raw[0]), z0 = as_f16x8(raw[1]), z1 = as_f16x8(raw[2]);
+        float g[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) g[r] = (float)z0[r];
+        if (l == 0) act_slopes(a.act, g);   // none: ones
+        else act_values(a.act, g);
+        const bool inside = row0(c) < a.out && lrow < a.T;
+        f16x8 o;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            g[r] *= (float)dy[r];
+            if (a.n == 2 && l == 0) g[r] *= (float)z1[r];
+            g[r] = inside ? g[r] : 0.f;
+            o[r] = (f16)(inside ? g[r] * scale_rest(scale[r]) : 0.f);
+        }
+        dz[0] = as_u32x4(o);
+        if (cb == 0 && a.dbias[0] != nullptr) {   // the 16 lanes of a quarter hold the tokens of its 8 rows
+            f16* db = (l ? a.dbias[1] : a.dbias[0]) + row0(c);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float s = g[r];
+#pragma unroll
+                for (int o = 8; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+                if (lrow == 0 && row0(c) < a.out) db[r] = (f16)s;
+            }
+        }
     };
     f32x4 acc[8][CT];
 #pragma unroll
@@ -142,6 +188,7 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     }
     for (int c = c0; c < c_end; c += kBWaves) {
         u32x4 w[8];
+        if constexpr (GRAD) make_dz(c);
         if constexpr (SCHEME == kScheme2x8) {
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
@@ -233,9 +280,9 @@ BackPlan back_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, int6
     return p;
 }
 
-template <int SCHEME, int CT>
+template <int SCHEME, int CT, bool GRAD = false>
 hipError_t launch_back(const BackArgs& a, int grid, hipStream_t stream) {
-    auto kern = skinny_back_kernel<SCHEME, CT>;
+    auto kern = skinny_back_kernel<SCHEME, CT, GRAD>;
     constexpr size_t sums = (size_t)back_waves(CT) * back_half(CT) * CT * 4 * 64 * 4;
     constexpr size_t lds = SCHEME == kScheme2x8 && sums < kBCbBytes ? kBCbBytes : sums;
     static_assert(lds <= 163840, "LDS budget");
@@ -250,6 +297,7 @@ hipError_t launch_ct(int ct, const BackArgs& a, int grid, hipStream_t stream) {
     if constexpr (SCHEME == kScheme1x16) {
         if (ct == 8) return launch_back<SCHEME, 8>(a, grid, stream);
     }
+    if (a.dy != nullptr) return launch_back<SCHEME, 1, true>(a, grid, stream);
     return ct == 1 ? launch_back<SCHEME, 1>(a, grid, stream)
          : ct == 2 ? launch_back<SCHEME, 2>(a, grid, stream) : launch_back<SCHEME, 4>(a, grid, stream);
 }
@@ -267,9 +315,18 @@ int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, i
     return (int64_t)p.splits * n * batch * p.n_cb * kBGroups * kGroup * 4;
 }
 
-hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, void* partial, void* dx,
-                              int64_t out, int64_t in, int64_t op, int64_t batch, const BiasSum& bias,
-                              hipStream_t stream) {
+// Where a wave of a full chip has few chunks: a launch saved is 1.5 to 3.5 us, while every chunk's
+// gradients, computed in each of the in / 128 groups, cost a 2x8 wave 0.5 to 1 us.  Gated, 8 tokens, us with
+// and without: 2x8 4096x2048 (2 chunks a wave) 14.1 and 16.4, 4096^2 gelu (4) 22.5 and 19.5; 1x16 4096^2 (4)
+// 30.5 and 33.2, 4096x6144 gelu (6) 42.7 and 41.4.
+bool skinny_back_grads(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
+    const int64_t chunks = (out + kBRows - 1) / kBRows * n * ((in / kGroup + kBGroups - 1) / kBGroups);
+    return batch <= 16 && out % 8 == 0 && chunks <= (sc.M == 2 ? 2 : 4) * kSkinnyWorkgroups * back_waves(1);
+}
+
+hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, const BackGrads* grads,
+                              void* partial, void* dx, int64_t out, int64_t in, int64_t op, int64_t batch,
+                              const BiasSum& bias, hipStream_t stream) {
     const BackPlan p = back_plan(sc, L.n, out, in, batch);
     BackArgs a = {};
     for (int l = 0; l < L.n; ++l) {
@@ -278,6 +335,14 @@ hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const
         a.scales[l] = static_cast<const f16*>(L.scales[l]);
     }
     a.dz = static_cast<const f16*>(dz);
+    if (grads != nullptr) {
+        a.dy = static_cast<const f16*>(grads->dy);
+        for (int l = 0; l < L.n; ++l) {
+            a.z[l] = static_cast<const f16*>(grads->z[l]);
+            a.dbias[l] = static_cast<f16*>(grads->dbias[l]);
+        }
+        a.act = grads->act;
+    }
     a.partial = static_cast<float*>(partial);
     a.out = (int)out;
     a.op = (int)op;
