@@ -236,6 +236,7 @@ int lists_forward(int n, const void* const* tables, const void* const* entries, 
     if (!act_ok(epi.act)) return AQLM_ERR_ACT;
     if (batch < 0 || batch > 1 || workspace_bytes < 0) return AQLM_ERR_SHAPE;
     if (out == 0 || batch == 0) return AQLM_OK;
+    if (!x || !epi.y || !workspace) return AQLM_ERR_NULL;
     ListsLayers L{};
     L.n = n;
     const int64_t part = lists_workspace_bytes_aligned(out, in);
@@ -253,7 +254,6 @@ int lists_forward(int n, const void* const* tables, const void* const* entries, 
         L.out[l] = (int)out;
         L.partial[l] = reinterpret_cast<float*>(static_cast<char*>(workspace) + l * part);
     }
-    if (!x || !epi.y || !workspace) return AQLM_ERR_NULL;
     if (!aligned(x, 16) || !aligned(epi.y, 16) || !aligned(epi.residual, 16) || !aligned(workspace, 16))
         return AQLM_ERR_ALIGN;
     if (workspace_bytes < (n - 1) * part + lists_workspace_bytes(out, in)) return AQLM_ERR_SHAPE;

@@ -63,6 +63,8 @@ __device__ __forceinline__ u32x4 lds16(uint32_t byte) {
     return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>((uintptr_t)byte);
 }
 
+__device__ const u32x4 back_zero = {0u, 0u, 0u, 0u};
+
 template <int SCHEME, int CT, bool GRAD>
 __global__ __launch_bounds__(64 * back_waves(CT))
     __attribute__((amdgpu_waves_per_eu(back_waves(CT) / 4, back_waves(CT) / 4))) void skinny_back_kernel(const BackArgs a) {
@@ -88,7 +90,7 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     f16 scale[8];
     u32x4 dz[CT];
     auto row0 = [&](int c) { return min(c, n_chunks - 1) * kBRows + 8 * kq; };
-    auto load_codes = [&](int c) {   // rows past the layer repeat its last one: their dz is zero
+    auto load_codes = [&](int c) {   // rows past the layer repeat its last one (masked when used)
 #pragma unroll
         for (int r = 0; r < 8; ++r) code[r] = codes[(size_t)min(row0(c) + r, a.out - 1) * a.G + j];
     };
@@ -197,6 +199,10 @@ __global__ __launch_bounds__(64 * back_waves(CT))
                     const uint32_t sel = m == 0 ? 0x0c0c0004u | (mA << 8) : 0x0c0c0005u | ((mA ^ 1u) << 8);
                     w[r] = lds16(__builtin_amdgcn_perm(base, (uint32_t)code[r], sel));
                 }
+                if ((c + 1) * kBRows > a.out) {   // rows past the layer count as zero
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) w[r] = row0(c) + r < a.out ? w[r] : u32x4{0u, 0u, 0u, 0u};
+                }
                 if (m == 1) load_codes(c + kBWaves);
                 times_power(w);
                 if (m == 1) load_scales(c + kBWaves);
@@ -205,7 +211,10 @@ __global__ __launch_bounds__(64 * back_waves(CT))
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) w[r] = load16(codebooks + (size_t)code[r] * kGroup);
+            for (int r = 0; r < 8; ++r) {   // rows past the layer: zeros
+                const f16* src = codebooks + (size_t)code[r] * kGroup;
+                w[r] = load16(row0(c) + r < a.out ? src : reinterpret_cast<const f16*>(&back_zero));
+            }
             load_codes(c + kBWaves);
             times_power(w);
             load_scales(c + kBWaves);

@@ -222,9 +222,13 @@ def aqlm_gated_backward(gate, up, dy, zg, zu, act="silu", need_dbias=False, dx=N
     return dx, dbg, dbu
 
 
-def _lists_layer(lists, codebooks, scales, dev):
+def _lists_shape(lists):
     if not isinstance(lists, SliceLists):
         raise ValueError("a layer over slice lists is (SliceLists, codebooks, scales)")
+    return lists.out, lists.n_in
+
+
+def _lists_layer(lists, codebooks, scales, dev):
     for name, t in (("table", lists.table), ("entries", lists.entries)):
         if t.device != dev:
             raise ValueError(f"tensors are on different devices: {name} on {t.device}, not {dev}")
@@ -243,7 +247,7 @@ def aqlm_linear_act_lists(lists, codebooks, scales, x, act="none", bias=None, re
                           workspace=None):
     """aqlm_linear_act at batch 1 over slice lists (see aqlm.h); x is [1][in] (or [0][in])."""
     a = _act(act)
-    out, n_in = lists.out, lists.n_in
+    out, n_in = _lists_shape(lists)
     dev, batch, px = _lists_x(x, n_in)
     table, entries, n_entries, cb, s = _lists_layer(lists, codebooks, scales, dev)
     pb = _optional("bias", bias, dev, (out,))
@@ -260,8 +264,8 @@ def aqlm_gated_lists(gate, up, x, act="silu", gate_bias=None, up_bias=None, zg=N
                      workspace=None):
     """aqlm_gated at batch 1 for layers gate and up = (SliceLists, codebooks, scales) (see aqlm.h)."""
     a = _act(act)
-    out, n_in = gate[0].out, gate[0].n_in
-    if (up[0].out, up[0].n_in) != (out, n_in):
+    out, n_in = _lists_shape(gate[0])
+    if _lists_shape(up[0]) != (out, n_in):
         raise ValueError("gate and up must have the same out and in")
     dev, batch, px = _lists_x(x, n_in)
     g, u = _lists_layer(*gate, dev), _lists_layer(*up, dev)
