@@ -9,6 +9,14 @@ namespace aqlm {
 
 struct BiasSum;   // act_bias.h
 
+// Workgroups go to the 8 XCDs in turn: the place of workgroup b of n in an order in which each XCD
+// has a contiguous run, so that neighbours in it share an L2 (any count gives correct results).
+__device__ __forceinline__ int xcd_run(int b, int n) {
+    constexpr int kX = 8;
+    const int x = b % kX;
+    return x * (n / kX) + (x < n % kX ? x : n % kX) + b / kX;
+}
+
 // What follows the product of one or two layers that share x.  One layer:
 // z = W x + bias, y = act(z) + residual.  Two layers (gate, up): zg, zu likewise,
 // y = act(zg) zu.  Absent pointers are NULL.  residual may be y itself.

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     const uint16_t* codes = reinterpret_cast<const uint16_t*>(up ? a.codes[1] : a.codes[0]);
     const f16* codebooks = up ? a.codebooks[1] : a.codebooks[0];
     const int G = a.G, n_slab = a.n_slab;
-    const int wid = blockIdx.x;
+    const int wid = xcd_run((int)blockIdx.x, (int)gridDim.x);
     const int u0 = run_begin(wid, a.runs), n = run_begin(wid + 1, a.runs) - u0;   // n >= 1: W <= units
 
     // a unit is (token tile t, row block b, slab s), s fastest

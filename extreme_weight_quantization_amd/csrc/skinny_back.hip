@@ -72,7 +72,8 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     extern __shared__ u32x4 smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lrow = lane & 15, kq = lane >> 4;
-    const int cb = (int)blockIdx.x % a.n_cb, rest = (int)blockIdx.x / a.n_cb;
+    const int item = xcd_run((int)blockIdx.x, (int)gridDim.x);
+    const int cb = item % a.n_cb, rest = item / a.n_cb;
     const int split = rest % a.splits, l = (rest / a.splits) % a.n, tt = rest / (a.splits * a.n);
     const uint16_t* codes = reinterpret_cast<const uint16_t*>(l ? a.codes[1] : a.codes[0]);
     const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
@@ -188,10 +189,10 @@ __global__ __launch_bounds__(64 * back_waves(CT))
         __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
         __syncthreads();
     }
-    for (int c = c0; c < c_end; c += kBWaves) {
-        u32x4 w[8];
-        if constexpr (GRAD) make_dz(c);
-        if constexpr (SCHEME == kScheme2x8) {
+    if constexpr (SCHEME == kScheme2x8) {
+        for (int c = c0; c < c_end; c += kBWaves) {
+            u32x4 w[8];
+            if constexpr (GRAD) make_dz(c);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
 #pragma unroll
@@ -209,19 +210,40 @@ __global__ __launch_bounds__(64 * back_waves(CT))
                 multiply(w);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        } else {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {   // rows past the layer: zeros
-                const f16* src = codebooks + (size_t)code[r] * kGroup;
-                w[r] = load16(row0(c) + r < a.out ? src : reinterpret_cast<const f16*>(&back_zero));
-            }
-            load_codes(c + kBWaves);
-            times_power(w);
-            load_scales(c + kBWaves);
-            multiply(w);
-            __builtin_amdgcn_sched_barrier(0);
+            load_dz(c + kBWaves);
         }
-        load_dz(c + kBWaves);
+    }
+    if constexpr (SCHEME == kScheme1x16) {
+        // the gathers of the next chunk are in flight while this one is multiplied
+        u32x4 next[8];
+        auto gather = [&](int c) {   // rows past the layer: zeros
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const f16* src = codebooks + (size_t)code[r] * kGroup;
+                next[r] = load16(row0(c) + r < a.out ? src : reinterpret_cast<const f16*>(&back_zero));
+            }
+        };
+        if (c0 < c_end) {
+            gather(c0);
+            load_codes(c0 + kBWaves);
+            int c = c0;
+            for (; c + kBWaves < c_end; c += kBWaves) {
+                if constexpr (GRAD) make_dz(c);
+                u32x4 w[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) w[r] = next[r];
+                gather(c + kBWaves);
+                load_codes(c + 2 * kBWaves);
+                times_power(w);
+                load_scales(c + kBWaves);
+                multiply(w);
+                __builtin_amdgcn_sched_barrier(0);
+                load_dz(c + kBWaves);
+            }
+            if constexpr (GRAD) make_dz(c);
+            times_power(next);
+            multiply(next);
+        }
     }
 
     // The waves' sums, in LDS [wave][t][i][r][lane], added in wave order; kH inputs t at a time.
