@@ -93,6 +93,7 @@ bool launch_gemv_stream_act(const ActLayers& L, const GemvEpi& epi, const void* 
 constexpr int kSkinnyWorkgroups = 256;
 constexpr int kSkinnyMaxBatch2x8 = 512;
 constexpr int kSkinnyMaxBatch1x16 = 256;
+constexpr int kSkinnyMaxBatch4x8 = 320;
 bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
 int64_t skinny_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
 hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void* x, void* partial, const Epilogue& epi,

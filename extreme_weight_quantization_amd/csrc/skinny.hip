@@ -42,7 +42,8 @@ constexpr int kKSlab = 32;                                  // groups per step
 // tokens: two stages of 64 KB; its steps are long enough for one step ahead).
 constexpr int skinny_stages(int bm) { return bm == 128 ? 2 : 3; }
 constexpr int kKRepl = 8;                                   // 2x8 codebook replicas in LDS
-constexpr int kKCbBytes = 2 * kCodewords2x8 * kKRepl * 16;   // 64 KB
+constexpr int kKCbBytes = 2 * kCodewords2x8 * kKRepl * 16;   // 64 KB; 4x8 g16: two replicas
+constexpr bool lds_codebooks(int scheme) { return scheme != kScheme1x16; }
 
 // `units` dealt to W workgroups in contiguous runs of q or q + 1 (units = q W + r): workgroup w
 // begins at floor(w units / W) = w q + floor(w r / W).  W <= kSkinnyWorkgroups, so w r fits 32 bits.
@@ -93,7 +94,8 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     constexpr int kNX = kXStage / kThreads;                   // x loads a wave issues a step
     constexpr int kR = skinny_stages(BM);                     // steps of x and of codes in flight
     constexpr bool kRagged = ROW != kRowWhole;                // the last slab may have groups past the row
-    constexpr uint32_t kXOff = SCHEME == kScheme2x8 ? kKCbBytes : 0;
+    constexpr bool kCbLds = lds_codebooks(SCHEME), kFour = SCHEME == kSchemeB8M4;
+    constexpr uint32_t kXOff = kCbLds ? kKCbBytes : 0;
     // vector loads that every step issues after the x tile that its end waits for: with three
     // stages (that tile: a step ago) all of its own, the x tile, the codes, the gathers; with two, the codes and half the gathers
     constexpr int kGathers = SCHEME == kScheme1x16 ? 4 * RT : 0;   // of half a step
@@ -165,15 +167,16 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
                     load16(codebooks + (size_t)((cv[rt][2 * h + (q >> 1)] >> (16 * (q & 1))) & 0xffffu) * kGroup);
     };
 
-    if constexpr (SCHEME == kScheme2x8) {
-        // slot (2 k + m) 8 + r: codeword k of codebook m (gated: the gate's for r < 4)
+    if constexpr (kCbLds) {
+        // 2x8: slot (2 k + m) 8 + r, codeword k of codebook m (gated: the gate's for r < 4);
+        // 4x8 g16: slot 16 k + 8 h + 2 m + r, half h of it (gated: the gate's for r = 0)
 #pragma unroll
         for (int it = 0; it < kKCbBytes / 16 / kThreads; ++it) {
-            const int km = (it * kThreads + tid) / kKRepl;
-            const f16* cbl = GATED && (tid & 4) != 0 ? a.codebooks[1] : a.codebooks[0];
-            __builtin_amdgcn_global_load_lds(
-                (const void*)(cbl + (size_t)((km & 1) * kCodewords2x8 + (km >> 1)) * kGroup),
-                lds_ptr(smem + it * kThreads + wave * kWave), 16, 0, 0);
+            const int slot = it * kThreads + tid;
+            const f16* cbl = GATED && (tid & (kFour ? 1 : 4)) != 0 ? a.codebooks[1] : a.codebooks[0];
+            const f16* src = kFour ? cbl + (size_t)((slot >> 1 & 3) * kCodewords2x8 + (slot >> 4)) * 16 + (slot >> 3 & 1) * 8
+                                   : cbl + (size_t)((slot >> 3 & 1) * kCodewords2x8 + (slot >> 4)) * kGroup;
+            __builtin_amdgcn_global_load_lds((const void*)src, lds_ptr(smem + it * kThreads + wave * kWave), 16, 0, 0);
         }
     }
     const int blk0 = (int)((uint32_t)u0 / (uint32_t)n_slab), tile0 = (int)((uint32_t)blk0 / (uint32_t)a.n_blk);
@@ -210,6 +213,11 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     const uint32_t mA = GATED ? (lane >> 2) & 1u : (lane >> 3) & 1u;
     const uint32_t r16 = (GATED ? (lane & 3u) + 4u * (uint32_t)up : lane & 7u) * 16u;
     const uint32_t base = (r16 + 128u * mA) | ((r16 + 128u * (mA ^ 1u)) << 8);
+    // 4x8 g16: lane l looks up codebooks l, l + 1, .. (mod 4) in turn, so that 16 lanes hit 8 of
+    // the 16 bank groups twice; byte i: the slot of its i-th codebook in a codeword's 256 bytes
+    const uint32_t rot = lane & 3u, rep = 16u * (GATED ? (uint32_t)up : (lane >> 2) & 1u);
+    const uint32_t base4 = (32u * rot + rep) | ((32u * ((rot + 1u) & 3u) + rep) << 8) |
+                           ((32u * ((rot + 2u) & 3u) + rep) << 16) | ((32u * ((rot + 3u) & 3u) + rep) << 24);
     const uint32_t xlane = kXOff + 16u * (uint32_t)(kKSlab * lrow + ((8 * kq) ^ lrow));
     f32x4 acc[RT][kCT];
     auto clear = [&]() {
@@ -224,13 +232,22 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     // the row (those past it count as zero: x is zero there, W is made so).  The LDS reads of
     // group q + 1 are spread between the products of group q, so that both units stay busy
     // (all reads of a half first: the step took the sum of both, 7300 clocks for 64 tokens).
-    auto fetch = [&](const u32x4 (&cv)[RT], uint32_t xs, int q, f16x8 (&w)[RT], f16x8 (&w2)[RT], f16x8 (&xv)[kCT]) {
-        if constexpr (SCHEME == kScheme2x8) {
+    constexpr int kLook = kFour ? 4 : 2;   // codewords of a weight
+    auto fetch = [&](const u32x4 (&cv)[RT], uint32_t xs, int q, f16x8 (&w)[RT][kLook], f16x8 (&xv)[kCT]) {
+        if constexpr (kFour) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t d = __builtin_amdgcn_alignbit(cv[rt][q >> 1], cv[rt][q >> 1], 8u * rot);
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i)
+                    w[rt][i] = as_f16x8(lds16(__builtin_amdgcn_perm(base4, d, 0x0c0c0004u + i + (i << 8)) + 128u * (q & 1)));
+            }
+        } else if constexpr (SCHEME == kScheme2x8) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const uint32_t d = cv[rt][q >> 1], hw = 2u * (q & 1);
-                w[rt] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0004u | ((hw + mA) << 8))));
-                w2[rt] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0005u | ((hw + (mA ^ 1u)) << 8))));
+                w[rt][0] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0004u | ((hw + mA) << 8))));
+                w[rt][1] = as_f16x8(lds16(__builtin_amdgcn_perm(base, d, 0x0c0c0005u | ((hw + (mA ^ 1u)) << 8))));
             }
         }
         const uint32_t xa = xs ^ (uint32_t)(q << 4);
@@ -239,25 +256,28 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     };
     auto multiply = [&](const u32x4 (&cv)[RT], u32x4 (&e)[2][RT][4], const u32x4 (&ahead)[RT], bool more, uint32_t xs,
                         int left) {
-        constexpr bool kTwo = SCHEME == kScheme2x8;
-        constexpr int kReads = kCT + (kTwo ? 2 * RT : 0), kProducts = RT * kCT * (kTwo && !SUM ? 2 : 1);
-        f16x8 w[2][RT], w2[2][RT], xv[2][kCT];
-        fetch(cv, xs, 0, w[0], w2[0], xv[0]);
+        constexpr int kReads = kCT + (kCbLds ? kLook * RT : 0), kProducts = RT * kCT * (kCbLds && !SUM ? 2 : 1);
+        f16x8 w[2][RT][kLook], xv[2][kCT];
+        fetch(cv, xs, 0, w[0], xv[0]);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            if (q + 1 < 8) fetch(cv, xs, q + 1, w[(q + 1) & 1], w2[(q + 1) & 1], xv[(q + 1) & 1]);
+            if (q + 1 < 8) fetch(cv, xs, q + 1, w[(q + 1) & 1], xv[(q + 1) & 1]);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                f16x8 a0 = w[q & 1][rt], a1 = w2[q & 1][rt];
-                if constexpr (!kTwo) a0 = as_f16x8(e[q >> 2][rt][q & 3]);
-                if constexpr (kTwo && SUM) a0 = a0 + a1;
+                f16x8 a0 = w[q & 1][rt][0], a1 = w[q & 1][rt][1];
+                if constexpr (!kCbLds) a0 = as_f16x8(e[q >> 2][rt][q & 3]);
+                if constexpr (kFour) {
+                    a0 = a0 + a1;
+                    a1 = w[q & 1][rt][2] + w[q & 1][rt][3];
+                }
+                if constexpr (kCbLds && SUM) a0 = a0 + a1;
                 if constexpr (kRagged) {
                     a0 = q < left ? a0 : f16x8{};
-                    if constexpr (kTwo && !SUM) a1 = q < left ? a1 : f16x8{};
+                    if constexpr (kCbLds && !SUM) a1 = q < left ? a1 : f16x8{};
                 }
 #pragma unroll
                 for (int j = 0; j < kCT; ++j) acc[rt][j] = mfma16x16x32(a0, xv[q & 1][j], acc[rt][j]);
-                if constexpr (kTwo && !SUM) {
+                if constexpr (kCbLds && !SUM) {
 #pragma unroll
                     for (int j = 0; j < kCT; ++j) acc[rt][j] = mfma16x16x32(a1, xv[q & 1][j], acc[rt][j]);
                 }
@@ -271,7 +291,7 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
                 if constexpr (kReads < kProducts) __builtin_amdgcn_sched_group_barrier(0x008, kProducts - kReads, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (!kTwo) {
+            if constexpr (!kCbLds) {
                 if (q == 3 && more) gather(ahead, 0, e[0]);   // the first half of the next step's codewords
             }
         }
@@ -455,7 +475,7 @@ struct SkinnyPlan {
 // them), up to 128 for 1x16, which is bound by its gathers, one per code and token tile.
 SkinnyPlan skinny_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     SkinnyPlan p;
-    const int64_t bm = batch <= 32 ? 32 : batch <= 64 || sc.M == 2 ? 64 : 128, tile = n == 2 ? 8 : 16;
+    const int64_t bm = batch <= 32 ? 32 : batch <= 64 || sc.B == 8 ? 64 : 128, tile = n == 2 ? 8 : 16;
     const int64_t n_slab = (in / kGroup + kKSlab - 1) / kKSlab, n_blk = (out + kKTiles * tile - 1) / (kKTiles * tile);
     const int64_t units = (batch + bm - 1) / bm * n_blk * n_slab;
     p.bm = (int)bm;
@@ -475,7 +495,7 @@ hipError_t launch_main(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t str
     auto kern = a.G % kKSlab == 0 ? skinny_kernel<SCHEME, BM, GATED, kRowWhole, RT, SUM>
                 : a.G % 8 == 0    ? skinny_kernel<SCHEME, BM, GATED, kRowVec, RT, SUM>
                                   : skinny_kernel<SCHEME, BM, GATED, kRowAny, RT, SUM>;
-    constexpr size_t lds = (SCHEME == kScheme2x8 ? kKCbBytes : 0) + (size_t)skinny_stages(BM) * BM * kKSlab * 16;
+    constexpr size_t lds = (lds_codebooks(SCHEME) ? kKCbBytes : 0) + (size_t)skinny_stages(BM) * BM * kKSlab * 16;
     static_assert(lds <= 163840, "LDS budget");
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
@@ -510,9 +530,10 @@ hipError_t launch_scheme(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t s
 // tokens (11008x4096 68 against 91, at 1024 123 against 129 and gated 283 against 229).
 bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     const bool two = sc.M == 2 && sc.B == 8 && sc.g == 8, one = sc.M == 1 && sc.B == 16 && sc.g == 8;
-    if (!two && !one) return false;
-    if (out * (in / kGroup) < 8) return false;   // 8 codes a load
-    if (batch > (two ? kSkinnyMaxBatch2x8 : kSkinnyMaxBatch1x16)) return false;
+    const bool four = sc.M == 4 && sc.B == 8 && sc.g == 16;
+    if (!two && !one && !four) return false;
+    if (out * (in / kGroup) < 8) return false;   // 16 bytes of codes a load
+    if (batch > (two ? kSkinnyMaxBatch2x8 : one ? kSkinnyMaxBatch1x16 : kSkinnyMaxBatch4x8)) return false;
     const int64_t rows = kKTiles * (n == 2 ? 8 : 16);
     const int64_t units = (out + rows - 1) / rows * ((in / kGroup + kKSlab - 1) / kKSlab);
     if (one && units < (batch <= 128 ? 128 : 512)) return false;
@@ -544,9 +565,10 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
     f.runs = a.runs = p.runs;
     f.bm = p.bm;
     f.blk_rows = p.blk_rows;
-    const bool two = sc.B == 8, gated = L.n == 2;
-    const hipError_t e = two ? (gated ? launch_scheme<kScheme2x8, true>(p, a, stream) : launch_scheme<kScheme2x8, false>(p, a, stream))
-                             : (gated ? launch_scheme<kScheme1x16, true>(p, a, stream) : launch_scheme<kScheme1x16, false>(p, a, stream));
+    const bool gated = L.n == 2;
+    const hipError_t e = sc.M == 2   ? (gated ? launch_scheme<kScheme2x8, true>(p, a, stream) : launch_scheme<kScheme2x8, false>(p, a, stream))
+                         : sc.M == 1 ? (gated ? launch_scheme<kScheme1x16, true>(p, a, stream) : launch_scheme<kScheme1x16, false>(p, a, stream))
+                                     : (gated ? launch_scheme<kSchemeB8M4, true>(p, a, stream) : launch_scheme<kSchemeB8M4, false>(p, a, stream));
     if (e != hipSuccess) return e;
     return launch_finish_args(L.n, f, stream);
 }
