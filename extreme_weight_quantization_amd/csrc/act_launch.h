@@ -103,6 +103,7 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
 // launch_act_grad writes it with the scales' mantissas, fp32 parts in the workspace.
 constexpr int kSkinnyBackMaxBatch2x8 = 256;
 constexpr int kSkinnyBackMaxBatch1x16 = 128;
+constexpr int kSkinnyBackMaxBatch4x8 = 128;
 bool skinny_back_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch);
 int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
 // skinny_back_grads: the shapes whose dz and bias sums the product computes itself, from grads

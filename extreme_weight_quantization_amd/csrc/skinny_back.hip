@@ -25,6 +25,7 @@
 //  * 2x8 codebooks: LDS, 8 replicas, read without bank conflicts as in gemv.hip.  1x16
 //    codewords are gathered from L2.
 #include <algorithm>
+#include <type_traits>
 
 #include "act_bias.h"
 #include "act_launch.h"
@@ -75,7 +76,11 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     const int item = xcd_run((int)blockIdx.x, (int)gridDim.x);
     const int cb = item % a.n_cb, rest = item / a.n_cb;
     const int split = rest % a.splits, l = (rest / a.splits) % a.n, tt = rest / (a.splits * a.n);
-    const uint16_t* codes = reinterpret_cast<const uint16_t*>(l ? a.codes[1] : a.codes[0]);
+    constexpr bool kCbLds = SCHEME != kScheme1x16, kFour = SCHEME == kSchemeB8M4;
+    constexpr int kCodewords = kFour ? 4 : 2;   // of a weight, from LDS
+    // the codes of a group of 8 inputs are 2 bytes, those of a 4x8 g16 group (two of them) 4
+    using Code = std::conditional_t<kFour, uint32_t, uint16_t>;
+    const Code* codes = reinterpret_cast<const Code*>(l ? a.codes[1] : a.codes[0]);
     const f16* codebooks = l ? a.codebooks[1] : a.codebooks[0];
     const f16* scales = l ? a.scales[1] : a.scales[0];
     const int n_chunks = a.op / kBRows;
@@ -87,13 +92,13 @@ __global__ __launch_bounds__(64 * back_waves(CT))
 
     // What a chunk needs from memory: the codes and scales of the lane's 8 rows, dz of its
     // tokens.  One set of registers: each part of the next chunk is loaded after its last use in this one.
-    uint16_t code[8];
+    Code code[8];
     f16 scale[8];
     u32x4 dz[CT];
     auto row0 = [&](int c) { return min(c, n_chunks - 1) * kBRows + 8 * kq; };
     auto load_codes = [&](int c) {   // rows past the layer repeat its last one (masked when used)
 #pragma unroll
-        for (int r = 0; r < 8; ++r) code[r] = codes[(size_t)min(row0(c) + r, a.out - 1) * a.G + j];
+        for (int r = 0; r < 8; ++r) code[r] = codes[((size_t)min(row0(c) + r, a.out - 1) * a.G + j) / (kFour ? 2 : 1)];
     };
     auto load_scales = [&](int c) {
 #pragma unroll
@@ -149,6 +154,11 @@ __global__ __launch_bounds__(64 * back_waves(CT))
 
     const uint32_t mA = (lane >> 3) & 1u, r16 = (lane & 7u) * 16u;
     const uint32_t base = (r16 + 128u * mA) | ((r16 + 128u * (mA ^ 1u)) << 8);
+    // 4x8 g16: 16 lanes (halves h of a codeword, codebooks in rotation, replicas r) hit all 16 bank groups; byte
+    // i: the slot of the lane's i-th codebook in a codeword's 256 bytes
+    const uint32_t rot = (lane >> 1) & 3u, rep = 128u * (lane & 1u) + 16u * ((lane >> 3) & 1u);
+    const uint32_t base4 = (32u * rot + rep) | ((32u * ((rot + 1u) & 3u) + rep) << 8) |
+                           ((32u * ((rot + 2u) & 3u) + rep) << 16) | ((32u * ((rot + 3u) & 3u) + rep) << 24);
     // the products of one codeword per row (w: rows 0..7 of the lane, times the rows' powers of two)
     auto multiply = [&](const u32x4 (&w)[8]) {
 #pragma unroll
@@ -178,25 +188,31 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     load_codes(c0);
     load_scales(c0);
     load_dz(c0);
-    if constexpr (SCHEME == kScheme2x8) {   // slot (2 k + m) 8 + r: codeword k of codebook m
+    if constexpr (kCbLds) {
+        // 2x8: slot (2 k + m) 8 + r, codeword k of codebook m; 4x8 g16: slot 16 k + 8 h + 2 m + r, half h of it
 #pragma unroll
         for (int it = 0; it < kBCbBytes / 16 / kBThreads; ++it) {
-            const int km = (it * kBThreads + tid) / 8;
-            __builtin_amdgcn_global_load_lds(
-                (const void*)(codebooks + (size_t)((km & 1) * kCodewords2x8 + (km >> 1)) * kGroup),
-                lds_ptr(smem + it * kBThreads + wave * kWave), 16, 0, 0);
+            const int slot = it * kBThreads + tid;
+            const f16* src = kFour ? codebooks + (size_t)((slot >> 1 & 3) * kCodewords2x8 + (slot >> 4)) * 16 + (slot >> 3 & 1) * 8
+                                   : codebooks + (size_t)((slot >> 3 & 1) * kCodewords2x8 + (slot >> 4)) * kGroup;
+            __builtin_amdgcn_global_load_lds((const void*)src, lds_ptr(smem + it * kBThreads + wave * kWave), 16, 0, 0);
         }
         __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
         __syncthreads();
     }
-    if constexpr (SCHEME == kScheme2x8) {
+    if constexpr (kCbLds) {
         for (int c = c0; c < c_end; c += kBWaves) {
             u32x4 w[8];
             if constexpr (GRAD) make_dz(c);
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < kCodewords; ++m) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
+                    if constexpr (kFour) {
+                        const uint32_t d = __builtin_amdgcn_alignbit(code[r], code[r], 8u * rot);
+                        w[r] = lds16(__builtin_amdgcn_perm(base4, d, 0x0c0c0004u + 0x0101u * m));
+                        continue;
+                    }
                     const uint32_t sel = m == 0 ? 0x0c0c0004u | (mA << 8) : 0x0c0c0005u | ((mA ^ 1u) << 8);
                     w[r] = lds16(__builtin_amdgcn_perm(base, (uint32_t)code[r], sel));
                 }
@@ -204,9 +220,9 @@ __global__ __launch_bounds__(64 * back_waves(CT))
 #pragma unroll
                     for (int r = 0; r < 8; ++r) w[r] = row0(c) + r < a.out ? w[r] : u32x4{0u, 0u, 0u, 0u};
                 }
-                if (m == 1) load_codes(c + kBWaves);
+                if (m == kCodewords - 1) load_codes(c + kBWaves);
                 times_power(w);
-                if (m == 1) load_scales(c + kBWaves);
+                if (m == kCodewords - 1) load_scales(c + kBWaves);
                 multiply(w);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -290,7 +306,7 @@ struct BackPlan {
 // kChunkUs per chunk of a wave (1x16: 4096 gathers of the workgroup's waves, at the rate a CU gets), then the parts,
 // written and added.
 BackPlan back_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
-    const bool two = sc.M == 2;
+    const bool two = sc.B == 8;   // 2x8, 4x8 g16
     BackPlan p;
     p.ct = batch <= 16 ? 1 : batch <= 32 ? 2 : batch <= 64 || two ? 4 : 8;
     p.n_tt = (int)((batch + 16 * p.ct - 1) / (16 * p.ct));
@@ -315,7 +331,7 @@ template <int SCHEME, int CT, bool GRAD = false>
 hipError_t launch_back(const BackArgs& a, int grid, hipStream_t stream) {
     auto kern = skinny_back_kernel<SCHEME, CT, GRAD>;
     constexpr size_t sums = (size_t)back_waves(CT) * back_half(CT) * CT * 4 * 64 * 4;
-    constexpr size_t lds = SCHEME == kScheme2x8 && sums < kBCbBytes ? kBCbBytes : sums;
+    constexpr size_t lds = SCHEME != kScheme1x16 && sums < kBCbBytes ? kBCbBytes : sums;
     static_assert(lds <= 163840, "LDS budget");
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
@@ -337,8 +353,8 @@ hipError_t launch_ct(int ct, const BackArgs& a, int grid, hipStream_t stream) {
 
 bool skinny_back_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_t batch) {
     const bool two = sc.M == 2 && sc.B == 8 && sc.g == 8, one = sc.M == 1 && sc.B == 16 && sc.g == 8;
-    if (!two && !one) return false;
-    return batch <= (two ? kSkinnyBackMaxBatch2x8 : kSkinnyBackMaxBatch1x16);
+    const bool four = sc.M == 4 && sc.B == 8 && sc.g == 16;
+    return (two || one || four) && batch <= (two ? kSkinnyBackMaxBatch2x8 : one ? kSkinnyBackMaxBatch1x16 : kSkinnyBackMaxBatch4x8);
 }
 
 int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
@@ -352,7 +368,7 @@ int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, i
 // 30.5 and 33.2, 4096x6144 gelu (6) 42.7 and 41.4.
 bool skinny_back_grads(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     const int64_t chunks = (out + kBRows - 1) / kBRows * n * ((in / kGroup + kBGroups - 1) / kBGroups);
-    return batch <= 16 && out % 8 == 0 && chunks <= (sc.M == 2 ? 2 : 4) * kSkinnyWorkgroups * back_waves(1);
+    return batch <= 16 && out % 8 == 0 && chunks <= (sc.B == 8 ? 2 : 4) * kSkinnyWorkgroups * back_waves(1);
 }
 
 hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const void* dz, const BackGrads* grads,
@@ -385,8 +401,9 @@ hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const
     a.splits = p.splits;
     const int64_t grid = (int64_t)p.n_cb * L.n * p.splits * p.n_tt;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
-    const hipError_t e = sc.B == 8 ? launch_ct<kScheme2x8>(p.ct, a, (int)grid, stream)
-                                   : launch_ct<kScheme1x16>(p.ct, a, (int)grid, stream);
+    const hipError_t e = sc.M == 2   ? launch_ct<kScheme2x8>(p.ct, a, (int)grid, stream)
+                         : sc.M == 1 ? launch_ct<kScheme1x16>(p.ct, a, (int)grid, stream)
+                                     : launch_ct<kSchemeB8M4>(p.ct, a, (int)grid, stream);
     if (e != hipSuccess) return e;
     const Epilogue plain = {{nullptr, nullptr}, nullptr, {nullptr, nullptr}, dx, kActNone};
     return launch_finish(1, a.partial, nullptr, plain, in, a.ip, batch, L.n * p.splits, bias, stream);

@@ -22,14 +22,15 @@ def _gpu():
 
 
 # forward: 2x8 adds its codewords in fp16 above 64 tokens and is decoded first above 512; 1x16 needs 128 units of 256
-# rows x 256 inputs (512 above 128 tokens) and is decoded first above 256 tokens
+# rows x 256 inputs (512 above 128 tokens) and is decoded first above 256 tokens, 4x8 g16 above 320
 @pytest.mark.parametrize("scheme,out,n_in,T", [
     *[("2x8", 1100, 520, T) for T in (32, 33, 64, 65, 128, 130, 511, 512, 513)],
     *[("2x8", 8, 8, T) for T in (17, 512, 513)],
     *[("1x16", 4096, 2048, T) for T in (17, 32, 33, 64, 65, 127, 128, 129)],   # 128 units
     ("1x16", 4096, 2040, 128), ("1x16", 4094, 1800, 128), ("1x16", 3840, 2048, 128),   # 128, 128, 120 units
     ("1x16", 8192, 4096, 129), ("1x16", 8188, 4080, 256), ("1x16", 8192, 4096, 257), ("1x16", 8192, 3840, 256),
-    *[("4x8g16", 300, 528, T) for T in (17, 128, 129, 1024, 1025)],
+    *[("4x8g16", 300, 528, T) for T in (17, 33, 64, 65, 128, 320, 321, 1024, 1025)],
+    ("4x8g16", 1100, 1024, 40), ("4x8g16", 1100, 1152, 200), ("4x8g16", 9, 16, 64),
 ])
 def test_forward_paths(scheme, out, n_in, T):
     run_linear(scheme, out, n_in, T, "silu", True, True, True, seed=T)
@@ -38,14 +39,15 @@ def test_forward_paths(scheme, out, n_in, T):
 
 
 # backward: the gradients inside the product up to 16 tokens of few chunks and rows of whole 16 bytes; the codes direct
-# up to 256 tokens (2x8) and 128 (1x16)
+# up to 256 tokens (2x8) and 128 (1x16, 4x8 g16)
 @pytest.mark.parametrize("scheme,out,n_in,T", [
     *[("2x8", 1100, 520, T) for T in (1, 16, 17, 32, 33, 64, 65, 128, 129, 255, 256, 257)],
     *[("1x16", 1100, 520, T) for T in (1, 16, 17, 32, 33, 64, 65, 127, 128, 129)],
     *[("2x8", out, 264, 16) for out in (8, 40, 96, 104, 100, 101)],
     *[("1x16", out, 264, 15) for out in (8, 40, 96, 104, 100, 101)],
     ("2x8", 4096, 4096, 16), ("2x8", 4104, 4224, 16), ("1x16", 4096, 8192, 3), ("1x16", 4224, 8192, 16),   # both sides of the chunks
-    *[("4x8g16", 520, 272, T) for T in (17, 256, 257, 1030)],
+    *[("4x8g16", 520, 272, T) for T in (1, 16, 17, 33, 64, 127, 128, 129, 1030)],
+    *[("4x8g16", out, 272, 16) for out in (8, 40, 104, 101)],
     ("1x8g4", 136, 72, 5003),
 ])
 def test_backward_paths(scheme, out, n_in, T):
@@ -57,17 +59,18 @@ def test_backward_paths(scheme, out, n_in, T):
 # few tiles of a dense product: its steps are split over workgroups, 128 or 256 tokens to a tile
 @pytest.mark.parametrize("out,n_in", [(130, 8192), (64, 4112), (1000, 2000), (2064, 320)])
 @pytest.mark.parametrize("T", [40, 128, 200, 256, 700])
-def test_dense_splits(out, n_in, T):
-    run_linear("4x8g16", out, n_in, T, "gelu", True, True, True)
-    run_gated("4x8g16", out, n_in, T, "silu", False, True)
-    run_linear_back("4x8g16", n_in, out - out % 16, T, "relu", True)   # the summed axis is the rows
+@pytest.mark.parametrize("scheme", ["1x8g4", "4x8g16"])
+def test_dense_splits(scheme, out, n_in, T):
+    run_linear(scheme, out, n_in, T, "gelu", True, True, True)
+    run_gated(scheme, out, n_in, T, "silu", False, True)
+    run_linear_back(scheme, n_in, out - out % 16, T, "relu", True)   # the summed axis is the rows
 
 
 def test_infinite_codewords():
     """An infinite weight reaches the outputs that it takes part in, and nothing beside them."""
     rng = np.random.default_rng(9)
     for scheme, (out, n_in), T in itertools.product(("2x8", "1x16", "4x8g16"), ((131, 208), (257, 528), (72, 1104)),
-                                                    (1, 4, 16, 17, 40, 130, 260, 600)):
+                                                    (1, 4, 16, 17, 40, 100, 130, 260, 600)):
         M, B, g = SCHEMES[scheme]
         (codes, cb, s), _, _ = layer(scheme, out, n_in, 21)
         codes[codes == 7] = 8
@@ -119,7 +122,7 @@ def rows_of(codes, cb, s, rows):
     return R.weights(L)
 
 
-@pytest.mark.parametrize("scheme", ["2x8", "1x16"])
+@pytest.mark.parametrize("scheme", ["2x8", "1x16", "4x8g16"])
 def test_a_layer_beyond_4_gb(scheme):
     """Codes beyond 4 GB, and at 600 tokens a workspace and outputs beyond it, at rows on both sides of every power."""
     out, n_in, M, B, g = 2_200_003, 8192, *SCHEMES[scheme]
@@ -131,7 +134,7 @@ def test_a_layer_beyond_4_gb(scheme):
         codes = torch.randint(-(1 << 15), 1 << 15, (out, n_in // g, M), dtype=torch.int16, device="cuda", generator=gen)
     s = torch.rand((out,), device="cuda", generator=gen).half() * 0.25 + 0.125
     rows = sorted({0, 1, 255, 256, out - 1, out - 2, out - 257, *(int(2 ** 31 // n_in) + k for k in (-1, 0, 1)),
-                   *(int(2 ** 32 // (n_in // g * 2)) + k for k in (-1, 0, 1)), 1 << 20, (1 << 21) - 1, 1 << 21})
+                   *(int(2 ** 32 // (n_in // 4)) + k for k in (-1, 0, 1)), 1 << 20, (1 << 21) - 1, 1 << 21})
     w = rows_of(codes, cb, s, rows)
     rng = np.random.default_rng(11)
     for T in (1, 16, 40, 600):
