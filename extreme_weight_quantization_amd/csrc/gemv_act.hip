@@ -60,8 +60,10 @@ hipError_t launch_v(const ActCall& c) {
 }
 
 // How x reaches the registers and how many codebook replicas fit next to it: as the plain
-// launches choose (gemv.hip).  Gated 4x8 g16 keeps two replicas a layer and direct x loads at
-// every batch (the 8-row stage would leave it one).
+// launches choose (gemv.hip), but for 4x8 g16: four replicas, read without conflicts, and direct
+// x loads at batch 1 and 2 (gated: to 8), else two replicas, read with 2-way conflicts, and staged x:
+// 4096^2 at batch 8 7.1 us (direct 7.9), at 16 7.6 (12.2); gated 4096x11008 at 4 21.7 (direct
+// 19.8), at 16 22.7 (25.1).
 template <int KIND>
 hipError_t launch_tuned(int scheme, const ActCall& c) {
     const bool one = c.T <= 2, eight = c.T <= 8;
@@ -75,8 +77,9 @@ hipError_t launch_tuned(int scheme, const ActCall& c) {
             if (one) return launch_v<kSchemeB8M1, 8, kXDirect, KIND>(c);
             return eight ? launch_v<kSchemeB8M1, 8, kXStaged8, KIND>(c) : launch_v<kSchemeB8M1, 8, kXStaged16, KIND>(c);
         default:
+            if (!eight) return launch_v<kSchemeB8M4, 2, kXStaged16in8, KIND>(c);
             if constexpr (KIND == kGemvAct) {
-                if (!one && eight) return launch_v<kSchemeB8M4, 3, kXStaged8, KIND>(c);
+                if (!one) return launch_v<kSchemeB8M4, 2, kXStaged8, KIND>(c);
             }
             return launch_v<kSchemeB8M4, 4, kXDirect, KIND>(c);
     }

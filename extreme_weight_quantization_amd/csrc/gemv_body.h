@@ -121,7 +121,8 @@ __device__ __forceinline__ int slab_group(int kq, int q) { return 8 * kq + q; }
 // 16-byte LDS slots of the codebooks of a 2-bit B = 8 scheme with REPL
 // replicas: codeword k of codebook m, 8-entry piece h (of H = g / 8) sits in
 // slot ((k M + m) H + h) REPL + r (2x8: (2k + m) REPL + r).  1x8 g4 keeps its
-// 4-entry codewords in 8-byte slots k REPL + r (half as many 16-byte slots).
+// 4-entry codewords in 8-byte slots k REPL + r (half as many 16-byte slots).  4x8 g16 with an
+// epilogue: slot ((k H + h) M + m) REPL + r.
 // 0 for 1x16.
 template <int SCHEME, int REPL>
 constexpr int cb_slots() {
@@ -172,21 +173,38 @@ __device__ __forceinline__ f32x4 chunk_mfma(const u32x4 cv, const u32x4* __restr
             }
         }
         return acc;
+    } else if constexpr (M == 4 && EXACT) {
+        // 4x8 g16 with an epilogue: lanes take the four codebooks in rotation (which the sum does not
+        // feel but in the order of its fp32 additions), so that the 16 lanes served together read 16 distinct bank
+        // groups of the half h of a codeword, 4 codebooks x 4 replicas of 16 bytes (in the same
+        // order in all lanes: 4-way conflicts, gated 4096x11008 at batch 1 31.4 us).
+        const uint32_t lane = threadIdx.x & (kWave - 1);
+        const uint32_t rot = lane / (KIND == kGemvGated ? REPL / 2 : REPL) & 3u;
+        uint32_t low[4];   // slot of the i-th codebook's piece 0, codeword 0
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) low[i] = ((rot + i) & 3u) * REPL + rrep;
+#pragma unroll
+        for (int gi = 0; gi < 4; ++gi) {
+            const uint32_t d = __builtin_amdgcn_alignbit(cv[gi], cv[gi], 8u * rot);
+            f16x8 c[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const u32x4* at = cb_lds + ((d >> (8 * i)) & 0xffu) * (8 * REPL) + low[i];
+                c[0][i] = as_f16x8(at[0]);
+                c[1][i] = as_f16x8(at[4 * REPL]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc = mfma16x16x32(keep(2 * gi + h) ? c[h][i] : f16x8{}, bx[2 * gi + h], acc);
+        }
+        return acc;
     } else if constexpr (M >= 4) {
         constexpr int H = M / 2;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const int gi = q / H, h = q % H;
-            if constexpr (EXACT) {
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const uint32_t k = code_byte(cv, gi * M + m);
-                    f16x8 c = as_f16x8(cb_lds[((k * M + m) * H + h) * REPL + rrep]);
-                    c = keep(q) ? c : f16x8{};
-                    acc = mfma16x16x32(c, bx[q], acc);
-                }
-                continue;
-            }
             float sum[8];
 #pragma unroll
             for (int m = 0; m < M; ++m) {
@@ -442,10 +460,12 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
 #pragma unroll
         for (int it = 0; it < kCbSlots / kGemvThreads; ++it) {
             const int j = it * kGemvThreads + tid;
-            const int kmh = j / REPL, km = kmh / kH;
+            const int kmh = j / REPL;
+            const int km = kM == 4 && KIND != kGemvPlain ? kmh / 8 * 4 + kmh % 4 : kmh / kH;
+            const int h = kM == 4 && KIND != kGemvPlain ? kmh / 4 % 2 : kmh % kH;
             const f16* cbl = GATED && j % REPL >= REPL / 2 ? epi.codebooks1 : codebooks0;
             __builtin_amdgcn_global_load_lds(
-                (const void*)(cbl + (size_t)((km % kM) * kCodewords2x8 + km / kM) * kG + (kmh % kH) * 8),
+                (const void*)(cbl + (size_t)((km % kM) * kCodewords2x8 + km / kM) * kG + h * 8),
                 lds_ptr(smem + it * kGemvThreads + wave * 64), 16, 0, 0);
         }
         __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
