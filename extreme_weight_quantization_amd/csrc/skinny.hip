@@ -23,8 +23,11 @@
 //    a row block is written as fp32 partial sums, and skinny_finish_kernel adds a
 //    block's parts in order, applies the row scale and the epilogue, and rounds once.
 //
-// LDS layout of an x stage: token b, group c in 16-byte slot 32 b + (c ^ (b % 16)), so the
-// 16 lanes that read one group of 16 tokens hit 16 distinct bank groups.
+// LDS layout of an x stage: token b, group c in 16-byte slot 32 b + (x_place(c) ^ (b % 16)).
+// A 16-byte LDS read serves 16 lanes at a time: 0-3, 12-15 and 20-27; 4-11, 16-19 and 28-31;
+// likewise above 32.  Lanes 0-15 read group q and lanes 16-31 group 8 + q of 16 tokens, and
+// x_place makes those two differ in bits 2 and 3 of the slot, so that the 16 bank groups are distinct
+// (with c itself there, bit 3 alone, every read was a 2-way conflict).
 #include <algorithm>
 
 #include "act_bias.h"
@@ -59,6 +62,9 @@ __device__ __forceinline__ int run_of(int u, const Runs& v) {
     if (w + 1 < v.W && run_begin(w + 1, v) <= u) ++w;
     return w;
 }
+
+// Place of group c in a row of the x stage (its own inverse): bit 2 flipped by bit 3.
+__device__ __forceinline__ int x_place(int c) { return c ^ (c >> 1 & 4); }
 
 struct SkinnyArgs {
     const uint8_t* codes[2];
@@ -150,7 +156,7 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
 #pragma unroll
         for (int i = 0; i < kNX; ++i) {
             const int slot = 64 * (wave * kNX + i) + lane;
-            const int b = slot / kKSlab, c = (slot % kKSlab) ^ (b & 15);
+            const int b = slot / kKSlab, c = x_place(slot % kKSlab ^ (b & 15));
             const int tok = min(v.t * BM + b, a.T - 1), grp = v.s * kKSlab + c;
             const f16* src = a.x + ((size_t)tok * G + grp) * kGroup;
             if constexpr (kRagged) src = grp < G ? src : reinterpret_cast<const f16*>(&skinny_zero);
@@ -218,7 +224,7 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     const uint32_t rot = lane & 3u, rep = 16u * (GATED ? (uint32_t)up : (lane >> 2) & 1u);
     const uint32_t base4 = (32u * rot + rep) | ((32u * ((rot + 1u) & 3u) + rep) << 8) |
                            ((32u * ((rot + 2u) & 3u) + rep) << 16) | ((32u * ((rot + 3u) & 3u) + rep) << 24);
-    const uint32_t xlane = kXOff + 16u * (uint32_t)(kKSlab * lrow + ((8 * kq) ^ lrow));
+    const uint32_t xlane = kXOff + 16u * (uint32_t)(kKSlab * lrow + (x_place(8 * kq) ^ lrow));
     f32x4 acc[RT][kCT];
     auto clear = [&]() {
 #pragma unroll
