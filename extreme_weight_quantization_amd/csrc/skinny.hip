@@ -379,6 +379,26 @@ struct FinishArgs {
     BiasSum sums;
 };
 
+// Adds `parts` parts of 4 outputs of N layers in order, kAhead of them in flight; one past the last
+// repeats it and is not added.
+template <int N, int kAhead>
+__device__ __forceinline__ void add_parts(const float* p, size_t step, int op, int parts, f32x4 (&sum)[N]) {
+    for (int s0 = 0; s0 < parts; s0 += kAhead, p += kAhead * step) {
+        f32x4 v[kAhead][N];
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+            for (int l = 0; l < N; ++l)
+                v[s][l] = *reinterpret_cast<const f32x4*>(p + (size_t)min(s, parts - 1 - s0) * step + (size_t)l * op);
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+            for (int l = 0; l < N; ++l)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum[l][r] += s0 + s < parts ? v[s][l][r] : 0.f;
+    }
+}
+
 // Thread: 4 outputs of a token.  The parts of its row block are the runs from the one that
 // holds the block's first unit to the one that holds its last, added in that order.
 template <int N>
@@ -403,21 +423,9 @@ __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) 
     for (int l = 0; l < N; ++l) sum[l] = f32x4{0.f, 0.f, 0.f, 0.f};
     const size_t step = (size_t)a.T * N * a.op;
     const float* p = a.partial + ((size_t)t * N) * a.op + r0;
-    constexpr int kAhead = 8;   // parts in flight
-    for (int s0 = 0; s0 < parts; s0 += kAhead, p += kAhead * step) {
-        f32x4 v[kAhead][N];
-#pragma unroll
-        for (int s = 0; s < kAhead; ++s)
-#pragma unroll
-            for (int l = 0; l < N; ++l)   // a part past the last repeats it and is not added
-                v[s][l] = *reinterpret_cast<const f32x4*>(p + (size_t)min(s, parts - 1 - s0) * step + (size_t)l * a.op);
-#pragma unroll
-        for (int s = 0; s < kAhead; ++s)
-#pragma unroll
-            for (int l = 0; l < N; ++l)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) sum[l][r] += s0 + s < parts ? v[s][l][r] : 0.f;
-    }
+    if (parts <= 2) add_parts<N, 2>(p, step, a.op, parts, sum);
+    else if (parts <= 4) add_parts<N, 4>(p, step, a.op, parts, sum);
+    else add_parts<N, 8>(p, step, a.op, parts, sum);
     float z[N][4], v[4];
 #pragma unroll
     for (int l = 0; l < N; ++l)
