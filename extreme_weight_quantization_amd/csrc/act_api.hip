@@ -1,9 +1,9 @@
 // C ABI of the fused products and their backward passes (declared in include/aqlm.h):
 // argument checks on the host, then the launches on the caller's stream.
 //
-// Forward at batch 1..16 the codes are multiplied as they are decoded, in one launch; 2x8 and
-// 1x16 at some tens of tokens likewise, with partial sums in the workspace (skinny.hip).
-// Otherwise the products run in passes: the weights decoded once into the workspace as fp16, then a
+// Forward at batch 1..16 the codes are multiplied as they are decoded, in one launch; 2x8, 1x16
+// and 4x8 g16 at up to some hundreds of tokens likewise, with partial sums in the workspace
+// (skinny.hip), and so are their gradients (skinny_back.hip).  Otherwise the products run in passes: the weights decoded once into the workspace as fp16, then a
 // dense matrix-core product over them.  Forward, the decoded rows are padded to whole
 // steps of 64 inputs; backward, they are written transposed (dx = dz W sums over the rows
 // of W).  With one codebook (M = 1) a codeword is exactly an fp16 weight: forward, the row

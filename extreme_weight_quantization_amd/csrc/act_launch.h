@@ -87,7 +87,7 @@ struct GemvEpi;
 bool launch_gemv_stream_act(const ActLayers& L, const GemvEpi& epi, const void* x, void* y, int64_t out, int64_t in,
                             int64_t batch, hipStream_t stream, hipError_t* result);
 
-// The products of tens of tokens (skinny.hip), 2x8 and 1x16: straight from the codes, with
+// The products of tens to hundreds of tokens (skinny.hip), 2x8, 1x16 and 4x8 g16: straight from the codes, with
 // fp32 partial sums in the workspace.  The work is dealt to at most kSkinnyWorkgroups
 // workgroups, a fixed number so that the sums' order does not depend on the device.
 constexpr int kSkinnyWorkgroups = 256;
@@ -99,7 +99,7 @@ int64_t skinny_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_
 hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void* x, void* partial, const Epilogue& epi,
                          int64_t out, int64_t in, int64_t batch, hipStream_t stream);
 
-// dx of some tens of tokens (skinny_back.hip), 2x8 and 1x16: straight from the codes, dz as
+// dx of some tens of tokens (skinny_back.hip), 2x8, 1x16 and 4x8 g16: straight from the codes, dz as
 // launch_act_grad writes it with the scales' mantissas, fp32 parts in the workspace.
 constexpr int kSkinnyBackMaxBatch2x8 = 256;
 constexpr int kSkinnyBackMaxBatch1x16 = 128;

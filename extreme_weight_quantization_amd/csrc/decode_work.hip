@@ -128,8 +128,8 @@ __device__ __forceinline__ float row_factor(const f16* __restrict__ scales, uint
 // and place come from shifts and scalars.  The layers are decoded one after the other: one 1x16
 // codebook at a time in L2.  Two, four or eight pieces a thread in hand change the time by less than 10 %:
 // the write bounds it.  Between products that read the weights it takes 1.4-1.7 times what the same launch
-// takes when it only follows itself (28672x8192 2x8 125 against 88 us, 1x16 250 against 146): the weights the
-// product left in the last-level cache have to make room.
+// takes when it only follows itself (28672x8192 2x8 125 against 88 us, 1x16 250 against 146): a
+// product keeps the clock near 1.5 GHz and leaves its weights in the last-level cache.
 constexpr int kRowThreads = 256;
 
 template <int SCHEME, int G, int CB, WeightScale WS>

@@ -1,10 +1,11 @@
-// Products of a small batch (tens of tokens) straight from the codes, 2x8 and 1x16:
+// Products of a small batch (tens to hundreds of tokens) straight from the codes, 2x8, 1x16 and
+// 4x8 g16:
 //   P_l[t][i] = sum_k Wc_l[i][k] x[t][k]  for one layer, or the gate and up projections,
 // then the epilogue of act_launch.h.
 //
 // "The AQLM Quantization Algorithm, Explained", Figure 2 of the MCQ section (a group's
 // weights are the sum of one codeword per codebook, times the row's scale) and section
-// "Key AQLM quantization parameters" (2x8 and 1x16 at g = 8).
+// "Key AQLM quantization parameters" (2x8 and 1x16 at g = 8, 4x8 at g = 16).
 //
 // Between the decode-phase product (one 16-column matrix-core tile of tokens) and prefill (where decoding
 // the weights once into memory pays) a call is bound by its codeword lookups, the matrix
@@ -13,8 +14,11 @@
 //  * the matrix-core operand of W wants lane l to hold 8 consecutive inputs of row l % 16,
 //    which is one group of 8: a lane looks its groups up (2x8: two codewords from the LDS
 //    copy of the codebooks, 8 replicas, conflict-free as in gemv.hip; 1x16: one 16-byte
-//    gather from L2, half a step ahead) and multiplies them at once.  2x8 multiplies its two
-//    codewords one by one, so their sum is never rounded to fp16;
+//    gather from L2, half a step ahead; 4x8 g16: the halves of four codewords from 2 replicas,
+//    2-way conflicts) and multiplies them at once.  Up to 64 tokens 2x8 multiplies its two
+//    codewords one by one, so no weight is rounded; above, it adds them in fp16
+//    (launch_scheme).  4x8 g16 adds its four in two pairs, whose roundings are together about
+//    as large as one rounding of the weight, and multiplies the pairs;
 //  * a workgroup of 16 waves covers 256 rows (gated: 8 gate and 8 up rows a wave) and
 //    walks slabs of 32 groups (256 inputs); the x tile of a slab, BM tokens, sits in LDS
 //    for all waves, three stages of direct-to-LDS loads, one barrier a slab;
@@ -22,6 +26,13 @@
 //    contiguous runs, so every CU has the same work whatever the shape; each run's part of
 //    a row block is written as fp32 partial sums, and skinny_finish_kernel adds a
 //    block's parts in order, applies the row scale and the epilogue, and rounds once.
+//
+// What bounds it.  1x16: the gathers, one L2 request each; 4096x11008 at 48 tokens, main kernel
+// 32.7 us by the profiler for 5.6 M of them, 172 G/s of the 264 G/s that a kernel of nothing
+// else reaches (runs of 3 units where 2.7 would be even, and about 8 us to start and end).
+// 2x8 and 4x8 g16: LDS reads (gated 4096x11008 2x8 at 256 tokens: 2.8 M, at 8 clocks each 58 %
+// of the kernel's 67.7 us, matrix cores 29 %), at small sizes the start, two dependent loads
+// and the end of a run.
 //
 // LDS layout of an x stage: token b, group c in 16-byte slot 32 b + (x_place(c) ^ (b % 16)).
 // A 16-byte LDS read serves 16 lanes at a time: 0-3, 12-15 and 20-27; 4-11, 16-19 and 28-31;
@@ -522,6 +533,7 @@ hipError_t launch_main(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t str
 // tokens 825 -> 786 us).  Above 64 tokens 2x8 adds its codewords in fp16 and multiplies
 // once: half the products (606 us) for one rounding a weight, which decoded
 // weights have too; up to 64, where it would gain 4-20 %, both are multiplied and no weight is rounded.
+// Gated 4096x11008 at 128 tokens 48.2 us against 56.6, 4096^2 linear at 128 18.6 against 19.6.
 template <int SCHEME, bool GATED>
 hipError_t launch_scheme(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t stream) {
     if (p.bm == 32) return launch_main<SCHEME, 32, GATED, 1, false>(p, a, stream);
@@ -541,7 +553,9 @@ hipError_t launch_scheme(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t s
 // 26.0 against 29.7), and above 128 tokens every code is gathered twice (4096^2 at 256 tokens, 256 units:
 // 46 against 41; 4096x11008, 688 units: 80 against 98; at 512 tokens 128 against 115).  2x8
 // wins from the smallest layers (10.9 against 16.4 us on 2048x1024 at 64 tokens) up to 512
-// tokens (11008x4096 68 against 91, at 1024 123 against 129 and gated 283 against 229).
+// tokens (11008x4096 68 against 91, at 1024 123 against 129 and gated 283 against 229).  4x8 g16
+// wins likewise (1024^2 at 17 tokens 9.8 us against 13.3, gated 4096x11008 at 64 40.5 against
+// 138) up to about 320: 4096x11008 at 256 66.6 against 89.4, at 512 121 against 101.
 bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     const bool two = sc.M == 2 && sc.B == 8 && sc.g == 8, one = sc.M == 1 && sc.B == 16 && sc.g == 8;
     const bool four = sc.M == 4 && sc.B == 8 && sc.g == 16;

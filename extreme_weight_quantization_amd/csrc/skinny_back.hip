@@ -1,4 +1,5 @@
-// Gradients of a small batch with respect to the inputs, straight from the codes, 2x8 and 1x16:
+// Gradients of a small batch with respect to the inputs, straight from the codes, 2x8, 1x16 and
+// 4x8 g16:
 //   dx[t][k] = sum over layers and rows i of dz[t][i] s[i] Wc[i][k].
 //
 // "The AQLM Quantization Algorithm, Explained", Figure 2 of the MCQ section (a group's weights
@@ -7,13 +8,14 @@
 // consecutive summed indices in a lane.  So a lane looks up the codewords of 8 consecutive
 // rows at one group and transposes the 8 x 8 block in registers (v_perm_b32 pairs two rows'
 // halves: 32 for 64 weights): operand t then holds input t of the group for the 8 rows.  A wave
-// covers 16 groups x 32 rows with 8 operands, each multiplied by the dz of up to 64 tokens,
-// and no weight is ever written to memory.
+// covers 16 groups x 32 rows with 8 operands, each multiplied by the dz of up to 64 tokens (1x16:
+// 128), and no weight is ever written to memory.
 //
 //  * The row scale is split into a power of two and a mantissa (act_math.h): the power of two
 //    multiplies the codewords in fp16, exactly but for subnormals, the mantissa is in dz (act_grad.hip), which is
-//    rounded to fp16 anyway.  2x8 multiplies its two codewords one by one, so no weight
-//    is rounded.
+//    rounded to fp16 anyway.  2x8 and 4x8 g16 multiply their codewords one by one, so no
+//    weight is rounded (pairs of 4x8 g16 added in fp16, as forward, are too coarse next to the
+//    rounding of dz).
 //  * A workgroup of 8 waves (4 at 128 tokens) owns 16 groups (128 inputs) of dx and a part of the rows of one
 //    layer; its waves take the chunks of 32 rows in turn, each with the next chunk's codes and dz
 //    in flight and no barrier, and add their sums in LDS in wave order.  Its fp32 part of dx goes to
@@ -22,8 +24,21 @@
 //    pre-activations themselves.  A lane computes the 8 gradients of its operand from 16 bytes of
 //    each, every workgroup anew, and the workgroups of the first 16 groups add them over the
 //    tokens for the bias.  That saves a launch and dz's way through memory.
-//  * 2x8 codebooks: LDS, 8 replicas, read without bank conflicts as in gemv.hip.  1x16
-//    codewords are gathered from L2.
+//  * 2x8 codebooks: LDS, 8 replicas, read without bank conflicts as in gemv.hip; 4x8 g16: 2
+//    replicas of the four, no conflicts either, since neighbouring groups read different
+//    halves.  1x16 codewords are gathered from L2, a chunk ahead.
+//  * Neighbouring 16-group columns share lines of codes (128 bytes hold 64 groups), so they run
+//    on one XCD (xcd_run): 4096x11008 1x16 at 20 tokens 38.3 -> 36.5 us.
+//
+// What bounds it.  1x16: the gathers (4096x11008 at 77 tokens, main kernel 42.6 us by the
+// profiler: 5.6 M gathers, 21 us at the 264 G/s of a kernel of nothing else; without gathers it
+// took 18 us less, without reloading dz 6; three chunks of codes, scales and dz in flight
+// changed nothing).  2x8: transposes, products and latencies; gated 4096x11008 at 64 tokens
+// 36.2 us.
+//
+// Against decoding the transposed weights first (decode_work.hip), us in a graph: 4x8 g16 4096^2
+// at 16 tokens 14.5 and 32.3, 4096x11008 at 128 61.8 and 76.5, at 256 104 and 85: to 128 tokens.
+// 2x8 to 256 and 1x16 to 128 tokens by the same measure.
 #include <algorithm>
 #include <type_traits>
 

@@ -2,7 +2,10 @@
 
     python3 -m extreme_weight_quantization_amd.profile_op OP SCHEME OUT IN [BATCH] [--reps N]
 
-OP is gemv, gemm, gemm_dequant, decode or gemv_lists; SCHEME is 2x8, 1x16 or
+OP is gemv, gemm, gemm_dequant, decode, gemv_lists, linear_act, gated,
+linear_act_backward or gated_backward (the last four with silu and, backward,
+bias gradients; linear_act and gated at batch 1 also as linear_act_lists and
+gated_lists); SCHEME is 2x8, 1x16 or
 an (M, B, g) triple written MxBgG (4x8g16).  OP copy runs a plain 64 MiB
 device-to-device copy instead (the reference for scaling byte counters; the
 other arguments are ignored).  Inputs follow the distributions of
@@ -33,7 +36,8 @@ def parse_scheme(name: str):
 
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
-    ap.add_argument("op", choices=("gemv", "gemm", "gemm_dequant", "decode", "gemv_lists", "copy"))
+    ap.add_argument("op", choices=("gemv", "gemm", "gemm_dequant", "decode", "gemv_lists", "copy", "linear_act", "gated",
+                                   "linear_act_lists", "gated_lists", "linear_act_backward", "gated_backward"))
     ap.add_argument("scheme")
     ap.add_argument("out", type=int)
     ap.add_argument("n_in", type=int)
@@ -79,6 +83,31 @@ def main(argv=None):
     elif args.op == "decode":
         w = torch.empty((args.out, args.n_in), dtype=torch.float16, device="cuda")
         call = lambda: E.aqlm_linear_decode(codes, cb, s, w)
+    elif args.op in ("linear_act", "gated", "linear_act_backward", "gated_backward"):
+        op = args.op
+        layer = (codes, cb, s)
+        # the second layer of a pair has codes of its own, so that both are read
+        up = (codes.flip(0).contiguous(), cb, s)
+        need = getattr(E, op + "_workspace_bytes")(M, B, g, args.out, args.n_in, args.batch)
+        ws = torch.empty((max(need, 16),), dtype=torch.uint8, device="cuda")
+        y, z, zu = (torch.randn((args.batch, args.out), generator=gen, device="cuda").half() for _ in range(3))
+        dx = torch.empty_like(x)
+        call = {
+            "linear_act": lambda: E.aqlm_linear_act(*layer, x, act="silu", y=y, workspace=ws),
+            "gated": lambda: E.aqlm_gated(layer, up, x, y=y, workspace=ws),
+            "linear_act_backward": lambda: E.aqlm_linear_act_backward(*layer, y, act="silu", z=z, need_dbias=True,
+                                                                      dx=dx, workspace=ws),
+            "gated_backward": lambda: E.aqlm_gated_backward(layer, up, y, z, zu, need_dbias=True, dx=dx, workspace=ws),
+        }[op]
+    elif args.op in ("linear_act_lists", "gated_lists"):
+        if (M, B, g) != (1, 16, 8) or args.batch != 1:
+            raise SystemExit(f"{args.op} serves 1x16 at batch 1")
+        layer = (E.aqlm_lists_pack(codes), cb, s)
+        if args.op == "linear_act_lists":
+            call = lambda: E.aqlm_linear_act_lists(*layer, x, act="silu")
+        else:
+            up = (E.aqlm_lists_pack(codes.flip(0).contiguous()), cb, s)
+            call = lambda: E.aqlm_gated_lists(layer, up, x)
     else:
         if (M, B, g) != (1, 16, 8) or args.batch != 1:
             raise SystemExit("gemv_lists serves 1x16 at batch 1")

@@ -374,10 +374,21 @@ int aqlm_linear_gemv_lists_noalloc(const void* table, const void* entries, int64
  *
  * Numerics: products are accumulated in fp32; bias, activation, gate and
  * residual are applied in fp32; y, and z where it is kept, are rounded to fp16
- * once, y from the unrounded z.  The products run on fp16 weights: exact
- * codewords for M = 1 (the row scale applied in fp32), otherwise the decoded
- * weights that aqlm_linear_decode gives.  Backward, dz is rounded to fp16
- * before dx = dz W; dbias sums the fp32 values in a fixed order.  Results are
+ * once, y from the unrounded z.  With M = 1 the codewords are multiplied as
+ * they are and the row scale is applied in fp32.  With M > 1 a weight is
+ * rounded to fp16 once at most:
+ *   - batch 1..16, and 2x8 up to 64 tokens: not at all (codewords multiplied
+ *     one by one; the general schemes decode in fp32);
+ *   - 2x8 from 65 to 512 tokens: the sum of its two codewords; 4x8 g16 from 17
+ *     to 320: the sums of two pairs of codewords;
+ *   - else the decoded weight that aqlm_linear_decode gives.
+ * Backward, dz is rounded to fp16 before dx = dz W.  Small batches (2x8 to 256
+ * tokens, 1x16 and 4x8 g16 to 128) multiply the codewords, times the power of
+ * two of the row's scale, by dz times the rest of it; larger ones do so for
+ * M = 1 and take the decoded weights for M > 1.  dbias sums the fp32 values in
+ * a fixed order.  Codewords times that power of two, sums of codewords and
+ * decoded weights beyond fp16's range are infinite; non-finite values reach
+ * the outputs that they take part in and no others.  Results are
  * deterministic.
  */
 typedef enum {
