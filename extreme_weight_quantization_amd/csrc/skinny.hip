@@ -40,6 +40,7 @@
 // x_place makes those two differ in bits 2 and 3 of the slot, so that the 16 bank groups are distinct
 // (with c itself there, bit 3 alone, every read was a 2-way conflict).
 #include <algorithm>
+#include <type_traits>
 
 #include "act_bias.h"
 #include "act_launch.h"
@@ -58,19 +59,34 @@ constexpr int skinny_stages(int bm) { return bm == 128 ? 2 : 3; }
 constexpr int kKRepl = 8;                                   // 2x8 codebook replicas in LDS
 constexpr int kKCbBytes = 2 * kCodewords2x8 * kKRepl * 16;   // 64 KB; 4x8 g16: two replicas
 constexpr bool lds_codebooks(int scheme) { return scheme != kScheme1x16; }
+// The kernels that have a short form for a last token tile that is at most half full.  Not 1x16: its
+// gathers, which bound it, stay the same.
+constexpr bool skinny_halves(int scheme, int bm, bool sum) { return bm == 64 && (scheme == kSchemeB8M4 || sum); }
 
-// `units` dealt to W workgroups in contiguous runs of q or q + 1 (units = q W + r): workgroup w
-// begins at floor(w units / W) = w q + floor(w r / W).  W <= kSkinnyWorkgroups, so w r fits 32 bits.
+// Units dealt to W workgroups in contiguous runs.  A unit takes one place; or (`full` >= 0, for a
+// last token tile at most half full) the units of the other tiles, the first `full`, take two,
+// and those of the last tile, which multiply half the columns, one.  The
+// `places` go to the workgroups in intervals of q or q + 1 (places = q W + r): that of w begins at
+// floor(w places / W) = w q + floor(w r / W), and a unit belongs to the interval that its first
+// place is in.  W <= kSkinnyWorkgroups, so w r fits 32 bits; q >= 2 with `full`, so that no run is
+// empty.
 struct Runs {
-    int units, W, q, r;
+    int places, W, q, r, full;
 };
-__device__ __forceinline__ int run_begin(int w, const Runs& v) { return w * v.q + (int)((uint32_t)(w * v.r) / (uint32_t)v.W); }
-// The workgroup whose run holds unit u: an estimate within one (u < 2^30: a float quotient times
-// at most 256 is off by far less), then exact.
+__device__ __forceinline__ int run_place(int w, const Runs& v) { return w * v.q + (int)((uint32_t)(w * v.r) / (uint32_t)v.W); }
+// The first unit of run w: the first whose place is at or after the interval's begin.
+__device__ __forceinline__ int run_begin(int w, const Runs& v) {
+    const int p = run_place(w, v);
+    if (v.full < 0) return p;
+    return p <= 2 * v.full ? (p + 1) >> 1 : p - v.full;
+}
+// The workgroup whose run holds unit u: an estimate within one (fewer than 2^30 places: a float
+// quotient times at most 256 is off by far less), then exact.
 __device__ __forceinline__ int run_of(int u, const Runs& v) {
-    int w = min((int)((float)u * ((float)v.W / (float)v.units)), v.W - 1);
-    if (run_begin(w, v) > u) --w;
-    if (w + 1 < v.W && run_begin(w + 1, v) <= u) ++w;
+    const int p = v.full < 0 ? u : u + min(u, v.full);
+    int w = min((int)((float)p * ((float)v.W / (float)v.places)), v.W - 1);
+    if (run_place(w, v) > p) --w;
+    if (w + 1 < v.W && run_place(w + 1, v) <= p) ++w;
     return w;
 }
 
@@ -84,6 +100,7 @@ struct SkinnyArgs {
     float* partial;   // [slot][t][l][op]
     int out, op, G, T;
     int n_slab, n_blk;   // slabs of a row; row blocks
+    int half_tile;       // the token tile that is at most half full, or -1
     Runs runs;           // of token tiles x row blocks x slabs
 };
 
@@ -119,6 +136,7 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     constexpr int kIssued = kR == 2 ? RT + kGathers : kNX + RT + 2 * kGathers;
     constexpr int kTileRows = GATED ? 8 : 16;
     constexpr int kN = GATED ? 2 : 1;
+    constexpr bool kHalves = skinny_halves(SCHEME, BM, SUM);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lrow = lane & 15, kq = lane >> 4;
     const bool up = GATED && lrow >= 8;
@@ -127,7 +145,7 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     const f16* codebooks = up ? a.codebooks[1] : a.codebooks[0];
     const int G = a.G, n_slab = a.n_slab;
     const int wid = xcd_run((int)blockIdx.x, (int)gridDim.x);
-    const int u0 = run_begin(wid, a.runs), n = run_begin(wid + 1, a.runs) - u0;   // n >= 1: W <= units
+    const int u0 = run_begin(wid, a.runs), n = run_begin(wid + 1, a.runs) - u0;   // n >= 1
 
     // a unit is (token tile t, row block b, slab s), s fastest
     struct Unit { int t, b, s; };
@@ -250,7 +268,8 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     // group q + 1 are spread between the products of group q, so that both units stay busy
     // (all reads of a half first: the step took the sum of both, 7300 clocks for 64 tokens).
     constexpr int kLook = kFour ? 4 : 2;   // codewords of a weight
-    auto fetch = [&](const u32x4 (&cv)[RT], uint32_t xs, int q, f16x8 (&w)[RT][kLook], f16x8 (&xv)[kCT]) {
+    auto fetch = [&](const u32x4 (&cv)[RT], uint32_t xs, int q, f16x8 (&w)[RT][kLook], auto& xv) {
+        constexpr int kC = std::extent_v<std::remove_reference_t<decltype(xv)>>;
         if constexpr (kFour) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -269,12 +288,13 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
         }
         const uint32_t xa = xs ^ (uint32_t)(q << 4);
 #pragma unroll
-        for (int j = 0; j < kCT; ++j) xv[j] = as_f16x8(lds16(xa + (uint32_t)(j * 16 * kKSlab * 16)));
+        for (int j = 0; j < kC; ++j) xv[j] = as_f16x8(lds16(xa + (uint32_t)(j * 16 * kKSlab * 16)));
     };
-    auto multiply = [&](const u32x4 (&cv)[RT], u32x4 (&e)[2][RT][4], const u32x4 (&ahead)[RT], bool more, uint32_t xs,
-                        int left) {
-        constexpr int kReads = kCT + (kCbLds ? kLook * RT : 0), kProducts = RT * kCT * (kCbLds && !SUM ? 2 : 1);
-        f16x8 w[2][RT][kLook], xv[2][kCT];
+    auto multiply = [&](auto columns, const u32x4 (&cv)[RT], u32x4 (&e)[2][RT][4], const u32x4 (&ahead)[RT], bool more,
+                        uint32_t xs, int left) {
+        constexpr int kC = decltype(columns)::value;   // column tiles multiplied
+        constexpr int kReads = kC + (kCbLds ? kLook * RT : 0), kProducts = RT * kC * (kCbLds && !SUM ? 2 : 1);
+        f16x8 w[2][RT][kLook], xv[2][kC];
         fetch(cv, xs, 0, w[0], xv[0]);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -293,10 +313,10 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
                     if constexpr (kCbLds && !SUM) a1 = q < left ? a1 : f16x8{};
                 }
 #pragma unroll
-                for (int j = 0; j < kCT; ++j) acc[rt][j] = mfma16x16x32(a0, xv[q & 1][j], acc[rt][j]);
+                for (int j = 0; j < kC; ++j) acc[rt][j] = mfma16x16x32(a0, xv[q & 1][j], acc[rt][j]);
                 if constexpr (kCbLds && !SUM) {
 #pragma unroll
-                    for (int j = 0; j < kCT; ++j) acc[rt][j] = mfma16x16x32(a1, xv[q & 1][j], acc[rt][j]);
+                    for (int j = 0; j < kC; ++j) acc[rt][j] = mfma16x16x32(a1, xv[q & 1][j], acc[rt][j]);
                 }
             }
             if (q + 1 < 8) {
@@ -356,7 +376,15 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
                 advance(px);
             }
             __builtin_amdgcn_sched_barrier(0);
-            multiply(c, e, ahead, k + 1 < n, xs, G - cur.s * kKSlab - 8 * kq);
+            const int left = G - cur.s * kKSlab - 8 * kq;
+            using All = std::integral_constant<int, kCT>;
+            if constexpr (kHalves) {
+                using Half = std::integral_constant<int, kCT / 2>;
+                if (cur.t == a.half_tile) multiply(Half{}, c, e, ahead, k + 1 < n, xs, left);
+                else multiply(All{}, c, e, ahead, k + 1 < n, xs, left);
+            } else {
+                multiply(All{}, c, e, ahead, k + 1 < n, xs, left);
+            }
             if (pc.at < n) load_ring(ring[d]);
             if (after.s == 0 || k == n - 1) flush(cur);
             cur = after;
@@ -492,7 +520,7 @@ hipError_t launch_finish_args(int n, FinishArgs& f, hipStream_t stream) {
 
 // Geometry of one call.
 struct SkinnyPlan {
-    int bm = 0, blk_rows = 0, op = 0, n_slab = 0, n_blk = 0, slots = 0;
+    int bm = 0, blk_rows = 0, op = 0, n_slab = 0, n_blk = 0, slots = 0, half_tile = -1;
     Runs runs = {};
 };
 
@@ -508,10 +536,26 @@ SkinnyPlan skinny_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, 
     p.op = (int)((out + tile - 1) / tile * tile);
     p.n_slab = (int)n_slab;
     p.n_blk = (int)n_blk;
-    const int64_t W = std::min<int64_t>(kSkinnyWorkgroups, units);
-    p.runs = Runs{(int)units, (int)W, (int)(units / W), (int)(units % W)};
+    const int64_t n_tt = (batch + bm - 1) / bm;
+    const bool half = sc.B == 8 && n_tt > 1 && batch - (n_tt - 1) * bm <= bm / 2;
+    if (half) p.half_tile = (int)n_tt - 1;
+    const int64_t full = (n_tt - 1) * n_blk * n_slab;
+    // Two places for a whole unit and one for a half one where that shortens the longest run, a half
+    // unit counted as 0.8 (its lookups are whole): 264 units of gated 1000x2733 at 130 tokens, two
+    // in some runs, 21.8 -> 17.6 us; 16 a run (4096x11008 at 160) would take 68.3 instead of 61.5.
+    int64_t places = units, each = 1;
+    if (half) {
+        const int64_t q = (full + units + kSkinnyWorkgroups - 1) / kSkinnyWorkgroups;   // places of the longest
+        const double weighted = std::max<double>((double)((q + 1) / 2), 0.8 * (double)q);
+        if (weighted < (double)((units + kSkinnyWorkgroups - 1) / kSkinnyWorkgroups)) {
+            places = full + units;
+            each = 2;
+        }
+    }
+    const int64_t W = std::min<int64_t>(kSkinnyWorkgroups, places / each);
+    p.runs = Runs{(int)places, (int)W, (int)(places / W), (int)(places % W), each == 2 ? (int)full : -1};
     // the runs that share a row block: those that its slabs fill, and one cut at each end
-    p.slots = (int)((n_slab * W + units - 1) / units + 1);
+    p.slots = (int)((each * n_slab * W + places - 1) / places + 1);
     return p;
 }
 
@@ -591,6 +635,7 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
     f.n_slab = a.n_slab = p.n_slab;
     f.n_blk = a.n_blk = p.n_blk;
     f.runs = a.runs = p.runs;
+    a.half_tile = p.half_tile;
     f.bm = p.bm;
     f.blk_rows = p.blk_rows;
     const bool gated = L.n == 2;

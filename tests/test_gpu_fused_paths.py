@@ -24,12 +24,13 @@ def _gpu():
 # forward: 2x8 adds its codewords in fp16 above 64 tokens and is decoded first above 512; 1x16 needs 128 units of 256
 # rows x 256 inputs (512 above 128 tokens) and is decoded first above 256 tokens, 4x8 g16 above 320
 @pytest.mark.parametrize("scheme,out,n_in,T", [
-    *[("2x8", 1100, 520, T) for T in (32, 33, 64, 65, 128, 130, 511, 512, 513)],
+    *[("2x8", 1100, 520, T) for T in (32, 33, 64, 65, 96, 97, 128, 130, 160, 161, 511, 512, 513)],
+    *[("2x8", 700, 5000, T) for T in (66, 130)], *[("2x8", 300, 256, T) for T in (65, 90)], ("2x8", 5000, 696, 80),
     *[("2x8", 8, 8, T) for T in (17, 512, 513)],
     *[("1x16", 4096, 2048, T) for T in (17, 32, 33, 64, 65, 127, 128, 129)],   # 128 units
     ("1x16", 4096, 2040, 128), ("1x16", 4094, 1800, 128), ("1x16", 3840, 2048, 128),   # 128, 128, 120 units
     ("1x16", 8192, 4096, 129), ("1x16", 8188, 4080, 256), ("1x16", 8192, 4096, 257), ("1x16", 8192, 3840, 256),
-    *[("4x8g16", 300, 528, T) for T in (17, 33, 64, 65, 128, 320, 321, 1024, 1025)],
+    *[("4x8g16", 300, 528, T) for T in (17, 33, 64, 65, 96, 97, 128, 160, 320, 321, 1024, 1025)],
     ("4x8g16", 1100, 1024, 40), ("4x8g16", 1100, 1152, 200), ("4x8g16", 9, 16, 64),
 ])
 def test_forward_paths(scheme, out, n_in, T):
@@ -246,3 +247,24 @@ def test_two_streams_at_once(T):
         for i in range(2):
             for g in got[i]:
                 assert all(torch.equal(a, b) for a, b in zip(g, want[i])), (scheme, T)
+
+
+@pytest.mark.parametrize("T", [17, 64, 65, 96, 97, 130, 160, 257, 300])
+def test_the_workspace_is_enough(T):
+    """With exactly the bytes asked for, the results are those of a larger one and nothing behind them changes."""
+    rng = np.random.default_rng(14)
+    for scheme, (out, n_in) in itertools.product(("2x8", "1x16", "4x8g16"), ((72, 272), (700, 1040), (3000, 256), (96, 4096))):
+        M, B, g = SCHEMES[scheme]
+        gate, _, _ = layer(scheme, out, n_in, 50)
+        up, _, _ = layer(scheme, out, n_in, 51)
+        x, dy, z = half(rng, T, n_in).cuda(), half(rng, T, out).cuda(), half(rng, T, out).cuda()
+        for name, f in (("linear_act", lambda **k: [E.aqlm_linear_act(*gate, x, act="silu", **k)]),
+                        ("gated", lambda **k: [E.aqlm_gated(gate, up, x, **k)]),
+                        ("linear_act_backward", lambda **k: E.aqlm_linear_act_backward(*gate, dy, act="silu", z=z,
+                                                                                       need_dbias=True, **k)),
+                        ("gated_backward", lambda **k: E.aqlm_gated_backward(gate, up, dy, z, z, need_dbias=True, **k))):
+            need = getattr(E, name + "_workspace_bytes")(M, B, g, out, n_in, T)
+            buf = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")   # parts unwritten would be NaN
+            got, want = f(workspace=buf[:need]), f(workspace=torch.zeros(2 * need + 4096, dtype=torch.uint8, device="cuda"))
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (name, scheme, out, n_in)
+            assert bool((buf[need:] == 0xFF).all()), (name, scheme, out, n_in)
