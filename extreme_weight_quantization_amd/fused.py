@@ -73,9 +73,9 @@ def _rows(name, x):
     return x.device, x.shape[0]
 
 
-def _output(name, y, dev, shape):
+def _output(name, y, like, dev, shape):
     if y is None:
-        y = torch.empty(shape, dtype=_F16, device=dev)
+        y = like.new_empty(shape)   # like: the fp16 input (0.2 us less than torch.empty)
         return y, y.data_ptr()
     return y, _tensor(name, y, dev, shape)
 
@@ -97,13 +97,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 if _raw_stream is None:
     def _raw_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name, dev, *args):
     """The library's `name`(..., stream) with `dev` current: kernels launch on the device of their tensors."""
     fn = getattr(binding._lib or load_library(), name)
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
@@ -162,7 +163,7 @@ def aqlm_linear_act(codes, codebooks, scales, x, act="none", bias=None, residual
     pb = _optional("bias", bias, dev, (out,))
     pr = _optional("residual", residual, dev, (batch, out))
     pz = _optional("z", z, dev, (batch, out))
-    y, py = _output("y", y, dev, (batch, out))
+    y, py = _output("y", y, x, dev, (batch, out))
     keep, ws, nws = _workspace(workspace, lambda: linear_act_workspace_bytes(*sch, out, n_in, batch), dev)
     _call("aqlm_linear_act", dev, *layer, px, pb, pr, pz, py, ws, nws, a, *sch, out, n_in, batch)
     return y
@@ -178,7 +179,7 @@ def aqlm_gated(gate, up, x, act="silu", gate_bias=None, up_bias=None, zg=None, z
     px = _tensor("x", x, dev, (batch, n_in))
     bias = _pair(_optional("gate_bias", gate_bias, dev, (out,)), _optional("up_bias", up_bias, dev, (out,)))
     z = _pair(_optional("zg", zg, dev, (batch, out)), _optional("zu", zu, dev, (batch, out)))
-    y, py = _output("y", y, dev, (batch, out))
+    y, py = _output("y", y, x, dev, (batch, out))
     keep, ws, nws = _workspace(workspace, lambda: gated_workspace_bytes(*sch, out, n_in, batch), dev)
     _call("aqlm_gated", dev, codes, codebooks, scales, px, bias, z, py, ws, nws, a, *sch, out, n_in, batch)
     return y
@@ -195,7 +196,7 @@ def aqlm_linear_act_backward(codes, codebooks, scales, dy, act="none", z=None, n
     pd = _tensor("dy", dy, dev, (batch, out))
     pz = _optional("z", z, dev, (batch, out))
     dbias = torch.empty((out,), dtype=_F16, device=dev) if need_dbias else None
-    dx, px = _output("dx", dx, dev, (batch, n_in))
+    dx, px = _output("dx", dx, dy, dev, (batch, n_in))
     keep, ws, nws = _workspace(workspace, lambda: linear_act_backward_workspace_bytes(*sch, out, n_in, batch), dev)
     _call("aqlm_linear_act_backward", dev, *layer, pd, pz, px, dbias.data_ptr() if need_dbias else None,
           ws, nws, a, *sch, out, n_in, batch)
@@ -215,7 +216,7 @@ def aqlm_gated_backward(gate, up, dy, zg, zu, act="silu", need_dbias=False, dx=N
     if need_dbias:
         dbg, dbu = torch.empty((2, out), dtype=_F16, device=dev).unbind(0)
         db = _pair(dbg.data_ptr(), dbu.data_ptr())
-    dx, px = _output("dx", dx, dev, (batch, n_in))
+    dx, px = _output("dx", dx, dy, dev, (batch, n_in))
     keep, ws, nws = _workspace(workspace, lambda: gated_backward_workspace_bytes(*sch, out, n_in, batch), dev)
     _call("aqlm_gated_backward", dev, codes, codebooks, scales, pd, z, px, db, ws, nws, a, *sch, out, n_in,
           batch)
@@ -253,7 +254,7 @@ def aqlm_linear_act_lists(lists, codebooks, scales, x, act="none", bias=None, re
     pb = _optional("bias", bias, dev, (out,))
     pr = _optional("residual", residual, dev, (batch, out))
     pz = _optional("z", z, dev, (batch, out))
-    y, py = _output("y", y, dev, (batch, out))
+    y, py = _output("y", y, x, dev, (batch, out))
     keep, ws, nws = _workspace(workspace, lambda: lists_fused_workspace_bytes([out], n_in), dev)
     _call("aqlm_linear_act_lists", dev, table, entries, n_entries, cb, s, px, pb, pr, pz, py, ws, nws, a,
           1, 16, 8, out, n_in, batch)
@@ -271,7 +272,7 @@ def aqlm_gated_lists(gate, up, x, act="silu", gate_bias=None, up_bias=None, zg=N
     g, u = _lists_layer(*gate, dev), _lists_layer(*up, dev)
     bias = _pair(_optional("gate_bias", gate_bias, dev, (out,)), _optional("up_bias", up_bias, dev, (out,)))
     z = _pair(_optional("zg", zg, dev, (batch, out)), _optional("zu", zu, dev, (batch, out)))
-    y, py = _output("y", y, dev, (batch, out))
+    y, py = _output("y", y, x, dev, (batch, out))
     keep, ws, nws = _workspace(workspace, lambda: lists_fused_workspace_bytes([out, out], n_in), dev)
     _call("aqlm_gated_lists", dev, _pair(g[0], u[0]), _pair(g[1], u[1]),
           (ctypes.c_int64 * 2)(g[2], u[2]), _pair(g[3], u[3]), _pair(g[4], u[4]), px, bias, z, py, ws, nws, a, 1, 16, 8,
