@@ -61,16 +61,25 @@ __device__ __forceinline__ uint32_t piece_codes(const uint8_t* __restrict__ code
     return reinterpret_cast<const uint16_t*>(codes)[(size_t)row * P + p];
 }
 
+// a + b in fp32 as fma(a, 1, b): one instruction on the fp16 values (v_fma_mix_f32) instead of
+// two conversions and an addition.  The 1 is hidden from the compiler, which would fold it.
+__device__ __forceinline__ float hidden_one() {
+    float one = 1.f;
+    asm("" : "+v"(one));
+    return one;
+}
+
 // The fp32 weights of piece p of a row before the scale, zero past `in`, from its codes c
 // (kSchemeGeneric, g = G, code storage CB: read here).
 template <int SCHEME, int G, int CB>
 __device__ __forceinline__ void piece_weights(uint32_t c, const uint8_t* __restrict__ codes,
                                               const f16* __restrict__ codebooks, const u32x4* lds, uint32_t row,
                                               uint32_t p, int in, int M, int B, float (&v)[8]) {
+    [[maybe_unused]] const float one = hidden_one();
     if constexpr (SCHEME == kScheme2x8) {
         const f16x8 a = as_f16x8(lds[c & 0xff]), b = as_f16x8(lds[kCodewords2x8 + (c >> 8)]);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = __fadd_rn((float)a[t], (float)b[t]);
+        for (int t = 0; t < 8; ++t) v[t] = __builtin_fmaf((float)a[t], one, (float)b[t]);
     } else if constexpr (SCHEME == kScheme1x16) {
         const f16x8 a = as_f16x8(load16(codebooks + (size_t)c * kGroup));
 #pragma unroll
@@ -88,7 +97,8 @@ __device__ __forceinline__ void piece_weights(uint32_t c, const uint8_t* __restr
         for (int m = 0; m < 4; ++m) a[m] = as_f16x8(half[256 * m + ((c >> (8 * m)) & 0xff)]);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
-            v[t] = __fadd_rn(__fadd_rn(__fadd_rn((float)a[0][t], (float)a[1][t]), (float)a[2][t]), (float)a[3][t]);
+            v[t] = __builtin_fmaf((float)a[3][t], one,
+                                  __builtin_fmaf((float)a[2][t], one, __builtin_fmaf((float)a[0][t], one, (float)a[1][t])));
     } else {
         const uint32_t mask = (1u << B) - 1u;
         const int n_grp = in / G, k = (int)p * 8;
@@ -203,7 +213,13 @@ __global__ __launch_bounds__(256) void decode_transposed_kernel(DecodeArgs a, in
                     piece_weights<SCHEME, G, CB>(c[r], codes, codebooks, cb_lds, min(row0 + r, out - 1), p, in, M, B, v);
                     const float f = (float)(WS == WeightScale::kPow2 ? scale_power(s[r]) : s[r]);
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) o[r][t] = row0 + r < out ? (f16)__fmul_rn(v[t], f) : (f16)0.f;
+                    for (int t = 0; t < 8; ++t) o[r][t] = (f16)__fmul_rn(v[t], f);
+                }
+                if ((tile % n_row_tiles) * 64 + 64 > out) {   // rows past the layer: zeros
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) o[r][t] = row0 + r < out ? o[r][t] : (f16)0.f;
                 }
                 f16* w = a.w[0] + (size_t)l * op + row0;
 #pragma unroll
