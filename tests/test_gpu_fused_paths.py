@@ -9,7 +9,7 @@ import torch
 import extreme_weight_quantization_amd as E
 import fused_reference as R
 from extreme_weight_quantization_amd import synth
-from test_gpu_fused import SCHEMES, d, half, layer, opt, run_gated, run_gated_back, run_linear, run_linear_back
+from test_gpu_fused import SCHEMES, half, layer, run_gated, run_gated_back, run_linear, run_linear_back
 
 pytestmark = pytest.mark.gpu
 
