@@ -8,8 +8,8 @@
 // steps of 64 inputs; backward, they are written transposed (dx = dz W sums over the rows
 // of W).  With one codebook (M = 1) a codeword is exactly an fp16 weight: forward, the row
 // scale then goes into the fp32 epilogue and the weights are not rounded at all; backward,
-// its power of two goes into the weights (exact) and its mantissa into dz, which is
-// rounded to fp16 anyway.  With several codebooks a weight is the fp32 sum times the scale, rounded once.
+// it goes into dz, which is rounded to fp16 anyway.  With several codebooks a weight is the fp32 sum times
+// the scale, rounded once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -76,11 +76,16 @@ BackwardPlan backward_plan(int n, int act, const GenericScheme& sc, int64_t out,
     BackwardPlan p;
     Parts parts;
     p.op = round_up(out, 64);
+    auto add_dz = [&]() {   // with its levels and units behind it (act_launch.h)
+        p.dz = parts.add(batch, n * p.op, 2);
+        parts.add(batch, n * grad_level_cols(p.op), 1);
+        parts.add(batch, 4, 1);
+    };
     p.skinny = skinny_back_serves(sc, out, in, batch);
     if (p.skinny) {
         p.grad = !skinny_back_grads(sc, n, out, in, batch);
         if (p.grad) {
-            p.dz = parts.add(batch, n * p.op, 2);
+            add_dz();
             p.partial = parts.add(grad_chunks(out, batch), n * out, 4);
         }
         p.parts = out == 0 || batch == 0 ? 0 : parts.add(skinny_back_partial_bytes(sc, n, out, in, batch), 1, 1);
@@ -89,7 +94,7 @@ BackwardPlan backward_plan(int n, int act, const GenericScheme& sc, int64_t out,
     }
     p.grad = n > 1 || act != kActNone || p.op != out;
     p.wt = parts.add(in, n * p.op, 2);
-    p.dz = parts.add(batch, n * p.op, 2);
+    add_dz();
     p.partial = parts.add(grad_chunks(out, batch), n * out, 4);
     p.parts = parts.add(dense_partial_bytes(1, in, n * p.op, batch), 1, 1);
     p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
@@ -203,9 +208,10 @@ int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx,
         return finish(launch_skinny_back(GenericScheme{M, B, g}, L, nullptr, &grads, base + p.parts, dx, out, in, p.op,
                                          batch, BiasSum{}, s));
     }
-    const WeightScale ws = (p.skinny || (M == 1 && p.grad)) ? WeightScale::kPow2 : WeightScale::kFull;
+    // the scale goes into dz where the codewords are multiplied as they are
+    const WeightScale ws = (p.skinny || (M == 1 && p.grad)) ? WeightScale::kNone : WeightScale::kFull;
     if (p.grad || want_bias) {
-        const int r = finish(launch_act_grad(dy, z, ws == WeightScale::kPow2 ? L.scales : nullptr, L.n, act,
+        const int r = finish(launch_act_grad(dy, z, ws == WeightScale::kNone ? L.scales : nullptr, L.n, act,
                                              p.grad ? base + p.dz : nullptr,
                                              want_bias ? reinterpret_cast<float*>(base + p.partial) : nullptr, out, p.op,
                                              batch, s));
@@ -218,10 +224,13 @@ int backward(const ActLayers& L, const void* dy, const void* const* z, void* dx,
     if (p.skinny)
         return finish(launch_skinny_back(GenericScheme{M, B, g}, L, base + p.dz, nullptr, base + p.parts, dx, out, in, p.op, batch,
                                          bias, s));
-    const int r = finish(launch_decode_transposed(GenericScheme{M, B, g}, L, ws, base + p.wt, out, in, p.op, s));
+    ActLayers decoded = L;
+    if (p.grad) decoded.grads = {base + p.dz, batch};
+    const int r = finish(launch_decode_transposed(GenericScheme{M, B, g}, decoded, ws, base + p.wt, out, in, p.op, s));
     if (r != AQLM_OK) return r;
     const void* wt16 = base + p.wt;
-    const Epilogue plain = {{nullptr, nullptr}, nullptr, {nullptr, nullptr}, dx, kActNone};
+    Epilogue plain = {{nullptr, nullptr}, nullptr, {nullptr, nullptr}, dx, kActNone};
+    if (p.grad) plain.units = grad_units(base + p.dz, L.n, p.op, batch);
     return finish(launch_gemm_dense_act(p.grad ? base + p.dz : dy, &wt16, nullptr, 1, plain, base + p.parts, in,
                                         L.n * p.op, batch, bias, s));
 }

@@ -4,8 +4,10 @@
 //   gated        dzg = dy zu act'(zg),  dzu = dy act(zg)
 //   bias         dbias[i] = sum over tokens t of dz[t][i]
 //
-// computed in fp32 from the fp16 inputs.  dz is rounded to fp16 once: it is the operand of
-// the fp16 matrix cores in dx = dz W.  The bias sums take the fp32 values, in a fixed
+// computed in fp32 from the fp16 inputs.  dz, times the row's scale where the codewords are
+// multiplied as they are, is rounded to fp16 once, in units of a power of two that a token's 512
+// columns of a workgroup share (act_math.h): it is the operand of the fp16 matrix cores in dx = dz W.
+// The bias sums take the fp32 values, in a fixed
 // order: each wave adds its tokens, a workgroup its four waves, and act_bias_kernel the
 // workgroups' sums, four runs of them in order and then the runs.
 //
@@ -20,7 +22,7 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kGradCols = 512;   // columns per workgroup: 64 lanes of 8
+constexpr int kGradCols = kLevelCols;   // columns per workgroup: 64 lanes of 8
 
 // Tokens per wave, all loaded before any is used: 4, or 1 where that leaves fewer than two
 // workgroups a CU (8 tokens of 4096 gated rows: 10.2 us with 4, 6.0 with 1).
@@ -31,8 +33,9 @@ int grad_wave_tokens(int64_t out, int64_t batch) {
 struct GradArgs {
     const f16* dy;
     const f16* z[2];
-    const f16* mant[2];
+    const f16* scales[2];
     f16* dz;
+    int8_t* levels;
     float* partial;
     int out, op, T, n_cols;   // n_cols: workgroups across the columns
 };
@@ -43,6 +46,22 @@ __device__ __forceinline__ f16x8 load8(const f16* p, int left, bool vec) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = q < left ? p[q] : (f16)0.f;
     return v;
+}
+
+// The largest of the wave's non-negative values, in a scalar: prefix maxima inside rows of 16 lanes, then
+// across them; lane 63 ends up with all.
+template <int CTRL>
+__device__ __forceinline__ float max_from(float v) {
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = max_from<0x111>(v);   // row_shr 1, 2, 4, 8
+    v = max_from<0x112>(v);
+    v = max_from<0x114>(v);
+    v = max_from<0x118>(v);
+    v = max_from<0x142>(v);   // row_bcast 15, 31
+    v = max_from<0x143>(v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 template <int N, int ACT, int WT>
@@ -73,36 +92,42 @@ __global__ __launch_bounds__(256) void act_grad_kernel(GradArgs a) {
     for (int l = 0; l < N; ++l)
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            m[l][q] = (a.mant[l] != nullptr && q < left) ? scale_rest(a.mant[l][c0 + q]) : 1.f;
+            m[l][q] = (a.scales[l] != nullptr && q < left) ? (float)a.scales[l][c0 + q] : 1.f;
             sum[l][q] = 0.f;
         }
-    if (c0 < a.op) {
 #pragma unroll
-        for (int i = 0; i < WT; ++i) {
-            if (i >= n_tok) break;
-            float g[N][8];
+    for (int i = 0; i < WT; ++i) {
+        if (i >= n_tok) break;
+        float g[N][8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float dy = (float)v[i][0][q], z = (float)v[i][1][q];
+            if constexpr (N == 1) {
+                g[0][q] = ACT == kActNone ? dy : dy * act_slope<ACT>(z);
+            } else {
+                g[0][q] = dy * (float)v[i][kOps - 1][q] * act_slope<ACT>(z);
+                g[N - 1][q] = dy * act_value<ACT>(z);
+            }
+        }
+#pragma unroll
+        for (int l = 0; l < N; ++l) {
+            float largest = 0.f;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float dy = (float)v[i][0][q], z = (float)v[i][1][q];
-                if constexpr (N == 1) {
-                    g[0][q] = ACT == kActNone ? dy : dy * act_slope<ACT>(z);
-                } else {
-                    g[0][q] = dy * (float)v[i][kOps - 1][q] * act_slope<ACT>(z);
-                    g[N - 1][q] = dy * act_value<ACT>(z);
-                }
+                g[l][q] = q < left ? g[l][q] : 0.f;
+                sum[l][q] += g[l][q];
+                g[l][q] = q < left ? g[l][q] * m[l][q] : 0.f;
+                largest = fmaxf(largest, finite_magnitude(g[l][q]));
             }
+            if (a.dz == nullptr) continue;
+            const int level = grad_level(wave_max(largest));
+            const float unit = level_unit(-level);
+            f16x8 o;
 #pragma unroll
-            for (int l = 0; l < N; ++l) {
-                f16x8 o;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float w = q < left ? g[l][q] : 0.f;
-                    sum[l][q] += w;
-                    o[q] = (f16)(q < left ? w * m[l][q] : 0.f);
-                }
-                if (a.dz != nullptr)
-                    *reinterpret_cast<u32x4*>(a.dz + (size_t)(tw + i) * (N * a.op) + (size_t)l * a.op + c0) = as_u32x4(o);
-            }
+            for (int q = 0; q < 8; ++q) o[q] = (f16)(g[l][q] * unit);
+            if (c0 < a.op)
+                *reinterpret_cast<u32x4*>(a.dz + (size_t)(tw + i) * (N * a.op) + (size_t)l * a.op + c0) = as_u32x4(o);
+            if (lane == 0) a.levels[((size_t)(tw + i) * N + l) * a.n_cols + cb] = (int8_t)level;
         }
     }
     if (a.partial == nullptr) return;
@@ -167,20 +192,21 @@ int64_t grad_chunks(int64_t out, int64_t batch) {
     return (batch + per - 1) / per;
 }
 
-hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* mant, int n, int act, void* dz,
+hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* scales, int n, int act, void* dz,
                            float* partial, int64_t out, int64_t op, int64_t batch, hipStream_t stream) {
     GradArgs a = {};
     a.dy = static_cast<const f16*>(dy);
     for (int l = 0; l < n; ++l) {
         a.z[l] = z ? static_cast<const f16*>(z[l]) : nullptr;
-        a.mant[l] = mant ? static_cast<const f16*>(mant[l]) : nullptr;
+        a.scales[l] = scales ? static_cast<const f16*>(scales[l]) : nullptr;
     }
     a.dz = static_cast<f16*>(dz);
+    a.levels = dz ? grad_levels(dz, n, op, batch) : nullptr;
     a.partial = partial;
     a.out = (int)out;
     a.op = (int)op;
     a.T = (int)batch;
-    const int64_t chunks = grad_chunks(out, batch), n_cols = (op + kGradCols - 1) / kGradCols;
+    const int64_t chunks = grad_chunks(out, batch), n_cols = grad_level_cols(op);
     if (chunks * n_cols > INT32_MAX) return hipErrorInvalidValue;
     a.n_cols = (int)n_cols;
     const dim3 grid((unsigned)(chunks * n_cols));

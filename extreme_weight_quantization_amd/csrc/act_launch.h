@@ -26,6 +26,13 @@ struct Epilogue {
     void* z[2];                // fp16 [batch][out]: where the pre-activations are kept
     void* y;                   // fp16 [batch][out]
     int act;
+    const float* units = nullptr;   // [batch]: factors of the tokens' products, powers of two (NULL: ones)
+};
+
+// Gradients dz of `batch` tokens as launch_act_grad writes them (dz NULL: none).
+struct GradRows {
+    void* dz = nullptr;
+    int64_t batch = 0;
 };
 
 // One or two layers (n) of the same scheme, out and in.
@@ -34,18 +41,19 @@ struct ActLayers {
     const void* codebooks[2];
     const void* scales[2];
     int n;
+    GradRows grads = {};   // launch_decode_transposed: the rows that it brings to one unit beside its own work
 };
 
 // How a decoded weight enters the fp16 workspace: the codewords' fp32 sum times the row
-// scale; the sum alone (M = 1: exact, the scale then goes into the epilogue); the sum
-// times the scale's power of two (M = 1: exact but for subnormals).
-enum class WeightScale : int { kFull = 0, kNone = 1, kPow2 = 2 };
+// scale; or the sum alone (M = 1: exact; the scale then goes into the epilogue, or into dz).
+enum class WeightScale : int { kFull = 0, kNone = 1 };
 
 // w[l][row][0 .. kp) for l < n: the layers' fp16 weights, inputs past `in` zero (kp % 8 == 0).
 hipError_t launch_decode_rows(const GenericScheme& sc, const ActLayers& L, WeightScale ws, void* const* w,
                               int64_t out, int64_t in, int64_t kp, hipStream_t stream);
 // wt[k][l * op + row] for k < in, l < n, row < op: the transposed weights, rows past `out`
-// zero (op % 64 == 0).
+// zero (op % 64 == 0).  L.grads: every row of dz is brought to the unit of its largest level
+// before the product sums over it, and the units are written to grad_units.
 hipError_t launch_decode_transposed(const GenericScheme& sc, const ActLayers& L, WeightScale ws, void* wt,
                                     int64_t out, int64_t in, int64_t op, hipStream_t stream);
 // xp[t][0 .. kp): x [batch][in], inputs past `in` zero.
@@ -69,12 +77,22 @@ hipError_t launch_finish(int n, const float* partial, const void* const* scales,
 
 // Gradients of the pre-activations, fp16, as the dense product's x: dz[t][l * op + i] for
 // i < op (rows past `out` zero).  One layer: dy act'(z); two: dy zu act'(zg) and dy act(zg).
-// mant: scales whose mantissas (scale_rest) multiply the fp16 result (NULL: none).
+// scales: row scales that multiply them in fp32 (NULL: none).
+// dz is in units of 2^(12 level) (act_math.h); behind it, each 256-byte aligned, lie the levels
+// [batch][n][grad_level_cols(op)] of the blocks of 512 rows, and room for one unit a token.
 // partial: fp32 [grad_chunks(out, batch)][n][out]: sums over chunks of tokens of the unscaled
 // fp32 gradients (NULL: not wanted); launch_bias_sum, or the launch that finishes a
 // product from parts, adds the chunks.
+inline int64_t grad_level_cols(int64_t op) { return (op + 511) / 512; }
+inline int64_t grad_align(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+inline int8_t* grad_levels(void* dz, int n, int64_t op, int64_t batch) {
+    return static_cast<int8_t*>(dz) + grad_align(batch * n * op * 2);
+}
+inline float* grad_units(void* dz, int n, int64_t op, int64_t batch) {
+    return reinterpret_cast<float*>(grad_levels(dz, n, op, batch) + grad_align(batch * n * grad_level_cols(op)));
+}
 int64_t grad_chunks(int64_t out, int64_t batch);
-hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* mant, int n, int act, void* dz,
+hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* scales, int n, int act, void* dz,
                            float* partial, int64_t out, int64_t op, int64_t batch, hipStream_t stream);
 hipError_t launch_bias_sum(const BiasSum& b, hipStream_t stream);
 
@@ -100,7 +118,7 @@ hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void
                          int64_t out, int64_t in, int64_t batch, hipStream_t stream);
 
 // dx of some tens of tokens (skinny_back.hip), 2x8, 1x16 and 4x8 g16: straight from the codes, dz as
-// launch_act_grad writes it with the scales' mantissas, fp32 parts in the workspace.
+// launch_act_grad writes it with the scales, fp32 parts in the workspace.
 constexpr int kSkinnyBackMaxBatch2x8 = 256;
 constexpr int kSkinnyBackMaxBatch1x16 = 128;
 constexpr int kSkinnyBackMaxBatch4x8 = 128;

@@ -85,19 +85,35 @@ __device__ __forceinline__ void act_slopes(int act, float (&v)[N]) {
     }
 }
 
-// A row scale s = m 2^e as an fp16 power of two, which goes into the fp16 weights exactly
-// (but for subnormals), and the rest, which goes into the other factor, so that only
-// one of the two is rounded: 1 <= |m| < 2 for normal s, m
-// below 1 for subnormal s (e = -14), m = s for zero, infinity and NaN (e = 0).
-__device__ __forceinline__ f16 scale_power(f16 s) {
-    const uint16_t b = __builtin_bit_cast(uint16_t, s), x = b & 0x7c00u;
-    const uint16_t p = (x == 0x7c00u || (b & 0x7fffu) == 0) ? 0x3c00u : x == 0 ? 0x0400u : x;
-    return __builtin_bit_cast(f16, p);
+// The matrix cores' operand d of dx = d W is fp16, while its values (dy zu act'(zg), times a row scale) span far
+// more than fp16's range.  So d is stored in units of 2^(12 L), the level L chosen per token and
+// block of rows from the block's largest finite magnitude m:  2^(12 L + 3) <= m < 2^(12 L + 15).  Nothing
+// overflows, and an element that becomes subnormal is off by 2^-25 units, at most 2^-28 m.  Levels this
+// coarse are nearly always the same along a row, which the products that join blocks make use of.
+// Bounds: m < 65504^3 1.13 < 2^49, and m = 0 takes the lowest level (2^-72 keeps every product of three fp16
+// numbers that could move a sum).
+constexpr int kLevelBits = 12, kLevelMin = -6, kLevelMax = 3;
+constexpr int kLevelCols = 512;   // rows of W that share a level
+
+__device__ __forceinline__ int grad_level(float m) {
+    const int e = (int)(__builtin_bit_cast(uint32_t, m) >> 23) - 127;   // floor(log2 m); m >= 0
+    const int l = (e - 3 + 16 * kLevelBits) / kLevelBits - 16;          // floor of the quotient: e >= -127
+    return min(max(l, kLevelMin), kLevelMax);
 }
-// (The quotient by a power of two is the product with its reciprocal, exactly.)
-__device__ __forceinline__ float scale_rest(f16 s) {
-    const uint32_t e = (uint32_t)__builtin_bit_cast(uint16_t, scale_power(s)) >> 10;   // 1 .. 30
-    return (float)s * __builtin_bit_cast(float, (142u - e) << 23);
+// 2^(12 l), for levels and their differences.
+__device__ __forceinline__ float level_unit(int l) { return __builtin_bit_cast(float, (uint32_t)(127 + kLevelBits * l) << 23); }
+// |v|, or 0 where v is not finite: infinities and NaN stay what they are at any level.
+__device__ __forceinline__ float finite_magnitude(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;
+    return __builtin_bit_cast(float, b < 0x7f800000u ? b : 0u);
+}
+// Eight fp16 values from units of one level to those of one `by` >= 0 levels higher, rounded once more where
+// they become subnormal.  In two factors, each an fp16 number (2^-24 is the smallest): finite values vanish
+// from four levels on, infinities stay.
+__device__ __forceinline__ u32x4 raise_level(u32x4 v, int by) {
+    const int a = min(by, 2), b = min(by - a, 2);
+    const f16 p = (f16)level_unit(-a), q = (f16)level_unit(-b);
+    return as_u32x4(as_f16x8(v) * f16x8{p, p, p, p, p, p, p, p} * f16x8{q, q, q, q, q, q, q, q});
 }
 
 }  // namespace aqlm

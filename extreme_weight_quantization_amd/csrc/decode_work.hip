@@ -172,12 +172,51 @@ __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(DecodeArgs a, 
     }
 }
 
+// The levels of dz's blocks and the one unit that each of its rows gets.
+struct GradAlign {
+    f16* dz;
+    const int8_t* levels;
+    float* units;
+    int T, cols;   // tokens (0: nothing to do), level columns of a layer
+};
+
+// Brings every row of dz to the unit of its largest level, since the dense product sums over whole rows, and
+// writes the units.  A wave a row; blocks at a lower level are rewritten.  Done here because this launch lies between
+// the one that writes dz and the product anyway; levels are 12 bits apart, so few rows have two.
+__device__ __forceinline__ void align_gradients(const GradAlign& g, int n, int op) {
+    const int lane = threadIdx.x & 63, n_blk = n * g.cols;
+    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < g.T; t += (int64_t)gridDim.x * 4) {
+        const int8_t* lv = g.levels + t * n_blk;
+        int top = kLevelMin, low = kLevelMax;
+        for (int b = lane; b < n_blk; b += 64) {
+            const int v = lv[b];
+            top = max(top, v);
+            low = min(low, v);
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            top = max(top, __shfl_xor(top, o, 64));
+            low = min(low, __shfl_xor(low, o, 64));
+        }
+        if (lane == 0) g.units[t] = level_unit(top);
+        if (low == top) continue;
+        for (int b = 0; b < n_blk; ++b) {
+            const int d = top - lv[b];
+            const int l = b / g.cols, c = (b - l * g.cols) * kLevelCols + 8 * lane;   // its 512 rows, 8 a lane
+            if (d == 0 || c >= op) continue;
+            u32x4* p = reinterpret_cast<u32x4*>(g.dz + t * n * op + (int64_t)l * op + c);
+            *p = raise_level(*p, d);
+        }
+    }
+}
+
 // Tiles of 64 rows x 32 pieces: thread (piece tid / 8, rows 8 (tid % 8) ..).  A workgroup stages
 // the codebooks once and walks tiles; a tile's codes are loaded while the one before is decoded.
 template <int SCHEME, int G, int CB, WeightScale WS>
 __global__ __launch_bounds__(256) void decode_transposed_kernel(DecodeArgs a, int n, int out, int in, int op, int ldt,
-                                                                int n_row_tiles, int n_tiles, int M, int B) {
+                                                                int n_row_tiles, int n_tiles, int M, int B, GradAlign grads) {
     __shared__ u32x4 cb_lds[work_cb_slots<SCHEME>()];
+    align_gradients(grads, n, op);
     const uint32_t P = (uint32_t)in / 8;
     const int oct = threadIdx.x & 7, piece = threadIdx.x >> 3;
     auto row_of = [&](int tile) { return (tile % n_row_tiles) * 64 + 8 * oct; };
@@ -211,7 +250,7 @@ __global__ __launch_bounds__(256) void decode_transposed_kernel(DecodeArgs a, in
                 for (int r = 0; r < 8; ++r) {
                     float v[8];
                     piece_weights<SCHEME, G, CB>(c[r], codes, codebooks, cb_lds, min(row0 + r, out - 1), p, in, M, B, v);
-                    const float f = (float)(WS == WeightScale::kPow2 ? scale_power(s[r]) : s[r]);
+                    const float f = WS == WeightScale::kNone ? 1.f : (float)s[r];
 #pragma unroll
                     for (int t = 0; t < 8; ++t) o[r][t] = (f16)__fmul_rn(v[t], f);
                 }
@@ -272,13 +311,13 @@ DecodeArgs decode_args(const ActLayers& L) {
 // One launch of decode_rows (T = false) or decode_transposed (T = true).
 template <bool T, int SCHEME, int G, int CB, WeightScale WS>
 hipError_t launch_ws(const DecodeArgs& a, int n, int64_t out, int64_t in, int64_t ld, int64_t op, int M, int B,
-                     hipStream_t stream) {
+                     const GradAlign& grads, hipStream_t stream) {
     if constexpr (T) {
         const int64_t n_rt = op / 64, n_pt = (in + 255) / 256;
         const int64_t tiles = n_rt * n_pt, cap = (int64_t)device_cu_count() * 8;
         if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
         hipLaunchKernelGGL((decode_transposed_kernel<SCHEME, G, CB, WS>), dim3((unsigned)(tiles < cap ? tiles : cap)),
-                           dim3(256), 0, stream, a, n, (int)out, (int)in, (int)op, (int)ld, (int)n_rt, (int)tiles, M, B);
+                           dim3(256), 0, stream, a, n, (int)out, (int)in, (int)op, (int)ld, (int)n_rt, (int)tiles, M, B, grads);
     } else {
         const int64_t per_row = ld / 8;
         int shift = 0;
@@ -295,29 +334,28 @@ hipError_t launch_ws(const DecodeArgs& a, int n, int64_t out, int64_t in, int64_
 
 template <bool T, int SCHEME, int G, int CB>
 hipError_t launch_scheme(WeightScale ws, const DecodeArgs& a, int n, int64_t out, int64_t in, int64_t ld, int64_t op,
-                         int M, int B, hipStream_t stream) {
+                         int M, int B, const GradAlign& grads, hipStream_t stream) {
     if (ws == WeightScale::kFull)
-        return launch_ws<T, SCHEME, G, CB, WeightScale::kFull>(a, n, out, in, ld, op, M, B, stream);
-    if constexpr (T) return launch_ws<T, SCHEME, G, CB, WeightScale::kPow2>(a, n, out, in, ld, op, M, B, stream);
-    else return launch_ws<T, SCHEME, G, CB, WeightScale::kNone>(a, n, out, in, ld, op, M, B, stream);
+        return launch_ws<T, SCHEME, G, CB, WeightScale::kFull>(a, n, out, in, ld, op, M, B, grads, stream);
+    return launch_ws<T, SCHEME, G, CB, WeightScale::kNone>(a, n, out, in, ld, op, M, B, grads, stream);
 }
 
 template <bool T>
 hipError_t launch_any(const GenericScheme& sc, WeightScale ws, const DecodeArgs& a, int n, int64_t out, int64_t in,
-                      int64_t ld, int64_t op, hipStream_t stream) {
+                      int64_t ld, int64_t op, const GradAlign& grads, hipStream_t stream) {
     const int M = sc.M, B = sc.B;
     if (M == 2 && B == 8 && sc.g == 8)
-        return launch_scheme<T, kScheme2x8, 8, 1>(ws, a, n, out, in, ld, op, M, B, stream);
+        return launch_scheme<T, kScheme2x8, 8, 1>(ws, a, n, out, in, ld, op, M, B, grads, stream);
     if (M == 1 && B == 16 && sc.g == 8)
-        return launch_scheme<T, kScheme1x16, 8, 2>(ws, a, n, out, in, ld, op, M, B, stream);
+        return launch_scheme<T, kScheme1x16, 8, 2>(ws, a, n, out, in, ld, op, M, B, grads, stream);
     if (M == 4 && B == 8 && sc.g == 16)
-        return launch_scheme<T, kSchemeB8M4, 16, 1>(ws, a, n, out, in, ld, op, M, B, stream);
+        return launch_scheme<T, kSchemeB8M4, 16, 1>(ws, a, n, out, in, ld, op, M, B, grads, stream);
     if (M == 1 && B == 8 && sc.g == 4 && in % 8 == 0)
-        return launch_scheme<T, kSchemeB8M1, 4, 1>(ws, a, n, out, in, ld, op, M, B, stream);
+        return launch_scheme<T, kSchemeB8M1, 4, 1>(ws, a, n, out, in, ld, op, M, B, grads, stream);
 #define AQLM_ROWS(G)                                                                                              \
     case G:                                                                                                       \
-        return B <= 8 ? launch_scheme<T, kSchemeGeneric, G, 1>(ws, a, n, out, in, ld, op, M, B, stream)            \
-                      : launch_scheme<T, kSchemeGeneric, G, 2>(ws, a, n, out, in, ld, op, M, B, stream);
+        return B <= 8 ? launch_scheme<T, kSchemeGeneric, G, 1>(ws, a, n, out, in, ld, op, M, B, grads, stream)            \
+                      : launch_scheme<T, kSchemeGeneric, G, 2>(ws, a, n, out, in, ld, op, M, B, grads, stream);
     switch (sc.g) {
         AQLM_ROWS(1)
         AQLM_ROWS(2)
@@ -336,14 +374,18 @@ hipError_t launch_decode_rows(const GenericScheme& sc, const ActLayers& L, Weigh
                               int64_t out, int64_t in, int64_t kp, hipStream_t stream) {
     DecodeArgs a = decode_args(L);
     for (int l = 0; l < L.n; ++l) a.w[l] = static_cast<f16*>(w[l]);
-    return launch_any<false>(sc, ws, a, L.n, out, in, kp, 0, stream);
+    return launch_any<false>(sc, ws, a, L.n, out, in, kp, 0, GradAlign{}, stream);
 }
 
 hipError_t launch_decode_transposed(const GenericScheme& sc, const ActLayers& L, WeightScale ws, void* wt,
                                     int64_t out, int64_t in, int64_t op, hipStream_t stream) {
     DecodeArgs a = decode_args(L);
     a.w[0] = static_cast<f16*>(wt);
-    return launch_any<true>(sc, ws, a, L.n, out, in, L.n * op, op, stream);
+    GradAlign g = {};
+    if (L.grads.dz != nullptr)
+        g = GradAlign{static_cast<f16*>(L.grads.dz), grad_levels(L.grads.dz, L.n, op, L.grads.batch),
+                      grad_units(L.grads.dz, L.n, op, L.grads.batch), (int)L.grads.batch, (int)grad_level_cols(op)};
+    return launch_any<true>(sc, ws, a, L.n, out, in, L.n * op, op, g, stream);
 }
 
 hipError_t launch_pad_rows(const void* x, void* xp, int64_t batch, int64_t in, int64_t kp, hipStream_t stream) {

@@ -109,6 +109,7 @@ struct DenseEpi {
     const f16* residual;
     f16* z[2];
     int act;
+    const float* units;     // one layer: factors of the tokens' products, or NULL
     float* partial;         // parts: [split][token][layer][op]
     int splits, op;
 };
@@ -193,12 +194,13 @@ __device__ __forceinline__ void dense_epilogue(const f32x4 (&acc)[4][4], float* 
         if (tok >= T) continue;
         const size_t o = (size_t)tok * out + col;
         float v[8];
+        const float unit = MODE == kDenseAct && e.units != nullptr ? e.units[tok] : 1.f;
 #pragma unroll
         for (int l = 0; l < kN; ++l) {
             const float* src = tile + rr * kEpiRow + at + 16 * l;
             float z[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) z[q] = src[q] * s[l][q] + b[l][q];
+            for (int q = 0; q < 8; ++q) z[q] = src[q] * unit * s[l][q] + b[l][q];
             if (e.z[l] != nullptr) epi_store8(e.z[l] + o, left, vec, z);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = l == 0 ? z[q] : v[q] * z[q];
@@ -485,6 +487,7 @@ hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void
     }
     e.residual = static_cast<const f16*>(epi.residual);
     e.act = epi.act;
+    e.units = epi.units;
     e.w1 = n == 2 ? static_cast<const f16*>(w[1]) : nullptr;
     e.partial = static_cast<float*>(partial);
     e.splits = p.splits;

@@ -410,6 +410,7 @@ struct FinishArgs {
     const f16* residual;   // may be y
     f16* z[2];
     f16* y;
+    const float* units;    // factors of the tokens' sums, or NULL
     int out, op, T, act;
     int parts;      // > 0: everywhere; else the runs that share the output's row block
     int bm, blk_rows, n_slab, n_blk;
@@ -465,6 +466,13 @@ __global__ __launch_bounds__(256) void skinny_finish_kernel(const FinishArgs a) 
     if (parts <= 2) add_parts<N, 2>(p, step, a.op, parts, sum);
     else if (parts <= 4) add_parts<N, 4>(p, step, a.op, parts, sum);
     else add_parts<N, 8>(p, step, a.op, parts, sum);
+    if (a.units != nullptr) {
+        const float unit = a.units[t];
+#pragma unroll
+        for (int l = 0; l < N; ++l)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[l][r] *= unit;
+    }
     float z[N][4], v[4];
 #pragma unroll
     for (int l = 0; l < N; ++l)
@@ -501,6 +509,7 @@ FinishArgs finish_args(int n, const float* partial, const void* const* scales, c
     f.partial = partial;
     f.residual = static_cast<const f16*>(epi.residual);
     f.y = static_cast<f16*>(epi.y);
+    f.units = epi.units;
     f.out = (int)out;
     f.op = (int)op;
     f.T = (int)batch;

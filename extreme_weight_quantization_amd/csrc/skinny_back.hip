@@ -11,11 +11,12 @@
 // covers 16 groups x 32 rows with 8 operands, each multiplied by the dz of up to 64 tokens (1x16:
 // 128), and no weight is ever written to memory.
 //
-//  * The row scale is split into a power of two and a mantissa (act_math.h): the power of two
-//    multiplies the codewords in fp16, exactly but for subnormals, the mantissa is in dz (act_grad.hip), which is
-//    rounded to fp16 anyway.  2x8 and 4x8 g16 multiply their codewords one by one, so no
-//    weight is rounded (pairs of 4x8 g16 added in fp16, as forward, are too coarse next to the
-//    rounding of dz).
+//  * The row scale is in dz (act_grad.hip), which is rounded to fp16 anyway, and the codewords are
+//    multiplied as they are, one by one for 2x8 and 4x8 g16, so no weight is rounded (pairs of
+//    4x8 g16 added in fp16, as forward, are too coarse next to the rounding of dz).
+//  * dz of a token comes in units of 2^(12 level), one level per 512 rows (act_math.h).  The sums of
+//    a token are kept at its highest level in the workgroup's rows (a lane has one token per column tile),
+//    blocks at a lower one are brought to it as they are used, and the sums leave in units of one.
 //  * A workgroup of 8 waves (4 at 128 tokens) owns 16 groups (128 inputs) of dx and a part of the rows of one
 //    layer; its waves take the chunks of 32 rows in turn, each with the next chunk's codes and dz
 //    in flight and no barrier, and add their sums in LDS in wave order.  Its fp32 part of dx goes to
@@ -23,7 +24,8 @@
 //  * GRAD: where that is little work (skinny_back_grads) the kernel takes dy and the
 //    pre-activations themselves.  A lane computes the 8 gradients of its operand from 16 bytes of
 //    each, every workgroup anew, and the workgroups of the first 16 groups add them over the
-//    tokens for the bias.  That saves a launch and dz's way through memory.
+//    tokens for the bias.  That saves a launch and dz's way through memory.  Levels are then found chunk by
+//    chunk, and a higher one brings the sums to its unit.
 //  * 2x8 codebooks: LDS, 8 replicas, read without bank conflicts as in gemv.hip; 4x8 g16: 2
 //    replicas of the four, no conflicts either, since neighbouring groups read different
 //    halves.  1x16 codewords are gathered from L2, a chunk ahead.
@@ -65,7 +67,9 @@ struct BackArgs {
     const uint8_t* codes[2];
     const f16* codebooks[2];
     const f16* scales[2];
-    const f16* dz;      // [t][l * op + i], times the scales' mantissas; zero for i >= out
+    const f16* dz;      // [t][l * op + i], times the scales; zero for i >= out
+    const int8_t* levels;   // [t][l][level_cols]
+    int level_cols;
     float* partial;     // [part][t][ip]
     int out, op, G, T, n, ip, n_cb, splits;
     // GRAD: dz is computed here
@@ -108,8 +112,11 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     // What a chunk needs from memory: the codes and scales of the lane's 8 rows, dz of its
     // tokens.  One set of registers: each part of the next chunk is loaded after its last use in this one.
     Code code[8];
-    f16 scale[8];
+    f16 scale[8];   // GRAD
     u32x4 dz[CT];
+    int level[CT], top[CT];   // of the tokens: of dz, and of their sums
+#pragma unroll
+    for (int i = 0; i < CT; ++i) level[i] = top[i] = kLevelMin;
     auto row0 = [&](int c) { return min(c, n_chunks - 1) * kBRows + 8 * kq; };
     auto load_codes = [&](int c) {   // rows past the layer repeat its last one (masked when used)
 #pragma unroll
@@ -118,6 +125,9 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     auto load_scales = [&](int c) {
 #pragma unroll
         for (int r = 0; r < 8; ++r) scale[r] = scales[min(row0(c) + r, a.out - 1)];
+    };
+    auto level_at = [&](int i) -> size_t {   // tokens past the batch repeat the last (their sums are not used)
+        return ((size_t)min((tt * CT + i) * 16 + lrow, a.T - 1) * a.n + l) * a.level_cols;
     };
     u32x4 raw[3] = {};   // GRAD: dy, and the pre-activations, of the lane's rows (out % 8 == 0: all inside or all past)
     auto load_dz = [&](int c) {   // tokens past the batch repeat the last (their sums are not used)
@@ -128,11 +138,44 @@ __global__ __launch_bounds__(64 * back_waves(CT))
             if (a.n == 2 && l == 0) raw[2] = load16(a.z[1] + at);
         } else {
 #pragma unroll
-            for (int i = 0; i < CT; ++i)
+            for (int i = 0; i < CT; ++i) {
                 dz[i] = load16(dzl + (size_t)min((tt * CT + i) * 16 + lrow, a.T - 1) * ldz + row0(c));
+                level[i] = a.levels[level_at(i) + min(c, n_chunks - 1) / (kLevelCols / kBRows)];
+            }
         }
     };
-    // GRAD: dz from raw, fp32 until its one rounding; the bias sums of a chunk's rows
+    f32x4 acc[8][CT];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int i = 0; i < CT; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // The highest level of each token in the rows of this part; the quarters take the blocks in turn.
+    auto load_tops = [&]() {
+        if constexpr (!GRAD) {
+            const int b1 = (c_end - 1) / (kLevelCols / kBRows);
+            for (int b = (int)((int64_t)split * n_chunks / a.splits) / (kLevelCols / kBRows) + kq; b <= b1; b += 4)
+#pragma unroll
+                for (int i = 0; i < CT; ++i) top[i] = max(top[i], (int)a.levels[level_at(i) + b]);
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                top[i] = max(top[i], __shfl_xor(top[i], 16, 64));
+                top[i] = max(top[i], __shfl_xor(top[i], 32, 64));
+            }
+        }
+    };
+    // Brings dz to the level of the sums.
+    auto settle_dz = [&]() {
+        if constexpr (!GRAD) {
+            bool differ = false;
+#pragma unroll
+            for (int i = 0; i < CT; ++i) differ |= level[i] != top[i];
+            if (__any(differ)) {
+#pragma unroll
+                for (int i = 0; i < CT; ++i) dz[i] = raise_level(dz[i], top[i] - level[i]);
+            }
+        }
+    };
+    // GRAD: dz from raw, fp32 until its one rounding, at the sums' level; the bias sums of a chunk's rows
     auto make_dz = [&](int c) {
         const f16x8 dy = as_f16x8(raw[0]), z0 = as_f16x8(raw[1]), z1 = as_f16x8(raw[2]);
         float g[8];
@@ -141,14 +184,31 @@ __global__ __launch_bounds__(64 * back_waves(CT))
         if (l == 0) act_slopes(a.act, g);   // none: ones
         else act_values(a.act, g);
         const bool inside = row0(c) < a.out && lrow < a.T;
-        f16x8 o;
+        float scaled[8], largest = 0.f;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             g[r] *= (float)dy[r];
             if (a.n == 2 && l == 0) g[r] *= (float)z1[r];
             g[r] = inside ? g[r] : 0.f;
-            o[r] = (f16)(inside ? g[r] * scale_rest(scale[r]) : 0.f);
+            scaled[r] = inside ? g[r] * (float)scale[r] : 0.f;
+            largest = fmaxf(largest, finite_magnitude(scaled[r]));
         }
+        // the four quarters hold the token's other rows
+        largest = fmaxf(largest, __shfl_xor(largest, 16, 64));
+        largest = fmaxf(largest, __shfl_xor(largest, 32, 64));
+        const int now = max(top[0], grad_level(largest));
+        if (__any(now != top[0])) {   // the sums to the unit of a higher level
+            const float unit = level_unit(top[0] - now);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[t][0][q] *= unit;
+        }
+        top[0] = now;
+        const float unit = level_unit(-now);
+        f16x8 o;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) o[r] = (f16)(scaled[r] * unit);
         dz[0] = as_u32x4(o);
         if (cb == 0 && a.dbias[0] != nullptr) {   // the 16 lanes of a quarter hold the tokens of its 8 rows
             f16* db = (l ? a.dbias[1] : a.dbias[0]) + row0(c);
@@ -161,12 +221,6 @@ __global__ __launch_bounds__(64 * back_waves(CT))
             }
         }
     };
-    f32x4 acc[8][CT];
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int i = 0; i < CT; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-
     const uint32_t mA = (lane >> 3) & 1u, r16 = (lane & 7u) * 16u;
     const uint32_t base = (r16 + 128u * mA) | ((r16 + 128u * (mA ^ 1u)) << 8);
     // 4x8 g16: 16 lanes (halves h of a codeword, codebooks in rotation, replicas r) hit all 16 bank groups; byte
@@ -174,7 +228,7 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     const uint32_t rot = (lane >> 1) & 3u, rep = 128u * (lane & 1u) + 16u * ((lane >> 3) & 1u);
     const uint32_t base4 = (32u * rot + rep) | ((32u * ((rot + 1u) & 3u) + rep) << 8) |
                            ((32u * ((rot + 2u) & 3u) + rep) << 16) | ((32u * ((rot + 3u) & 3u) + rep) << 24);
-    // the products of one codeword per row (w: rows 0..7 of the lane, times the rows' powers of two)
+    // the products of one codeword per row (w: rows 0..7 of the lane)
     auto multiply = [&](const u32x4 (&w)[8]) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -191,18 +245,11 @@ __global__ __launch_bounds__(64 * back_waves(CT))
                 acc[2 * d + 1][i] = mfma16x16x32(as_f16x8(hi), as_f16x8(dz[i]), acc[2 * d + 1][i]);
         }
     };
-    auto times_power = [&](u32x4 (&w)[8]) {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const f16 q = scale_power(scale[r]);
-            const f16x8 p = {q, q, q, q, q, q, q, q};
-            w[r] = as_u32x4(as_f16x8(w[r]) * p);
-        }
-    };
 
     load_codes(c0);
-    load_scales(c0);
+    if constexpr (GRAD) load_scales(c0);
     load_dz(c0);
+    if constexpr (!kCbLds) load_tops();   // next to the loads before it; LDS codebooks: to theirs
     if constexpr (kCbLds) {
         // 2x8: slot (2 k + m) 8 + r, codeword k of codebook m; 4x8 g16: slot 16 k + 8 h + 2 m + r, half h of it
 #pragma unroll
@@ -212,13 +259,13 @@ __global__ __launch_bounds__(64 * back_waves(CT))
                                    : codebooks + (size_t)((slot >> 3 & 1) * kCodewords2x8 + (slot >> 4)) * kGroup;
             __builtin_amdgcn_global_load_lds((const void*)src, lds_ptr(smem + it * kBThreads + wave * kWave), 16, 0, 0);
         }
+        load_tops();
         __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
         __syncthreads();
-    }
-    if constexpr (kCbLds) {
         for (int c = c0; c < c_end; c += kBWaves) {
             u32x4 w[8];
             if constexpr (GRAD) make_dz(c);
+            settle_dz();
 #pragma unroll
             for (int m = 0; m < kCodewords; ++m) {
 #pragma unroll
@@ -235,9 +282,10 @@ __global__ __launch_bounds__(64 * back_waves(CT))
 #pragma unroll
                     for (int r = 0; r < 8; ++r) w[r] = row0(c) + r < a.out ? w[r] : u32x4{0u, 0u, 0u, 0u};
                 }
-                if (m == kCodewords - 1) load_codes(c + kBWaves);
-                times_power(w);
-                if (m == kCodewords - 1) load_scales(c + kBWaves);
+                if (m == kCodewords - 1) {
+                    load_codes(c + kBWaves);
+                    if constexpr (GRAD) load_scales(c + kBWaves);
+                }
                 multiply(w);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -260,19 +308,19 @@ __global__ __launch_bounds__(64 * back_waves(CT))
             int c = c0;
             for (; c + kBWaves < c_end; c += kBWaves) {
                 if constexpr (GRAD) make_dz(c);
+                settle_dz();
                 u32x4 w[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) w[r] = next[r];
                 gather(c + kBWaves);
                 load_codes(c + 2 * kBWaves);
-                times_power(w);
-                load_scales(c + kBWaves);
+                if constexpr (GRAD) load_scales(c + kBWaves);
                 multiply(w);
                 __builtin_amdgcn_sched_barrier(0);
                 load_dz(c + kBWaves);
             }
             if constexpr (GRAD) make_dz(c);
-            times_power(next);
+            settle_dz();
             multiply(next);
         }
     }
@@ -280,7 +328,13 @@ __global__ __launch_bounds__(64 * back_waves(CT))
     // The waves' sums, in LDS [wave][t][i][r][lane], added in wave order; kH inputs t at a time.
     // Thread (combination (i, r) of its wave, lane): group 4 kq + r, token 16 i + lane % 16.
     constexpr int kH = back_half(CT);
+    // The sums' units: GRAD, of the wave, applied as it writes them; else the workgroup's, behind the sums.
     float* red = reinterpret_cast<float*>(smem);
+    float* units = red + kBWaves * kH * CT * 4 * 64;
+    if (!GRAD && wave == 0 && kq == 0) {
+#pragma unroll
+        for (int i = 0; i < CT; ++i) units[16 * i + lrow] = level_unit(top[i]);
+    }
     const size_t part = (size_t)((l * a.splits) + split);
 #pragma unroll
     for (int h = 0; h < 8 / kH; ++h) {
@@ -291,7 +345,8 @@ __global__ __launch_bounds__(64 * back_waves(CT))
             for (int i = 0; i < CT; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    red[(((wave * kH + t) * CT + i) * 4 + r) * 64 + lane] = acc[h * kH + t][i][r];
+                    red[(((wave * kH + t) * CT + i) * 4 + r) * 64 + lane] =
+                        GRAD ? acc[h * kH + t][i][r] * level_unit(top[i]) : acc[h * kH + t][i][r];
         __syncthreads();
         for (int q = wave; q < 4 * CT; q += kBWaves) {
             const int i = q >> 2, r = q & 3;
@@ -302,6 +357,7 @@ __global__ __launch_bounds__(64 * back_waves(CT))
                 s[t] = 0.f;
 #pragma unroll
                 for (int w = 0; w < kBWaves; ++w) s[t] += red[(((w * kH + t) * CT + i) * 4 + r) * 64 + lane];
+                if (!GRAD) s[t] *= units[16 * i + lrow];
             }
             if (tok < a.T) {
                 f32x4* dst = reinterpret_cast<f32x4*>(a.partial + (part * a.T + tok) * a.ip + 8 * (size_t)grp + h * kH);
@@ -346,7 +402,8 @@ template <int SCHEME, int CT, bool GRAD = false>
 hipError_t launch_back(const BackArgs& a, int grid, hipStream_t stream) {
     auto kern = skinny_back_kernel<SCHEME, CT, GRAD>;
     constexpr size_t sums = (size_t)back_waves(CT) * back_half(CT) * CT * 4 * 64 * 4;
-    constexpr size_t lds = SCHEME != kScheme1x16 && sums < kBCbBytes ? kBCbBytes : sums;
+    constexpr size_t lds = sums + 16 * CT * 4;   // and a unit a token
+    static_assert(SCHEME == kScheme1x16 || sums >= kBCbBytes, "the units lie behind the codebooks");
     static_assert(lds <= 163840, "LDS budget");
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
@@ -397,6 +454,10 @@ hipError_t launch_skinny_back(const GenericScheme& sc, const ActLayers& L, const
         a.scales[l] = static_cast<const f16*>(L.scales[l]);
     }
     a.dz = static_cast<const f16*>(dz);
+    if (dz != nullptr) {
+        a.levels = grad_levels(const_cast<void*>(dz), L.n, op, batch);
+        a.level_cols = (int)grad_level_cols(op);
+    }
     if (grads != nullptr) {
         a.dy = static_cast<const f16*>(grads->dy);
         for (int l = 0; l < L.n; ++l) {

@@ -382,14 +382,18 @@ int aqlm_linear_gemv_lists_noalloc(const void* table, const void* entries, int64
  *   - 2x8 from 65 to 512 tokens: the sum of its two codewords; 4x8 g16 from 17
  *     to 320: the sums of two pairs of codewords;
  *   - else the decoded weight that aqlm_linear_decode gives.
- * Backward, dz is rounded to fp16 before dx = dz W.  Small batches (2x8 to 256
- * tokens, 1x16 and 4x8 g16 to 128) multiply the codewords, times the power of
- * two of the row's scale, by dz times the rest of it; larger ones do so for
- * M = 1 and take the decoded weights for M > 1.  dbias sums the fp32 values in
- * a fixed order.  Codewords times that power of two, sums of codewords and
- * decoded weights beyond fp16's range are infinite; non-finite values reach
- * the outputs that they take part in and no others.  Results are
- * deterministic.
+ * Backward, small batches (2x8 to 256 tokens, 1x16 and 4x8 g16 to 128) multiply
+ * the codewords as they are, one by one, by dz times the row's scale.  Larger
+ * ones do so for M = 1 and multiply the decoded weights by dz for M > 1; with
+ * AQLM_ACT_NONE, one layer and out % 64 == 0 they multiply the decoded weights
+ * by dy as it is, for every M.  dz, times the scale where it takes it, is
+ * rounded to fp16 once, in units of a power of two per token and 512 rows that
+ * its largest finite value in them fixes, so that it does not leave fp16's
+ * range: elements down to 2^-17 of the token's largest keep all their bits,
+ * smaller ones are off by at most 2^-27 of it.  dbias sums the fp32 values in
+ * a fixed order.  Sums of codewords and decoded weights beyond fp16's range are
+ * infinite, decoded weights below 2^-14 lose bits; non-finite values reach the
+ * outputs that they take part in and no others.  Results are deterministic.
  */
 typedef enum {
     AQLM_ACT_NONE = 0,
