@@ -13,6 +13,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/aqlm.h"
 #include "act_bias.h"
 #include "act_launch.h"
@@ -63,6 +65,10 @@ ForwardPlan forward_plan(int n, const GenericScheme& sc, int64_t out, int64_t in
     if (p.pad) p.xp = parts.add(batch, p.kp, 2);
     p.partial = parts.add(dense_partial_bytes(n, out, p.kp, batch), 1, 1);
     p.bytes = parts.total;
+    // not less than the batches below need that are served straight from the codes
+    for (int64_t t : {kSkinnyMaxBatch1x16Few, sc.M == 1 ? kSkinnyMaxBatch1x16 : sc.M == 2 ? kSkinnyMaxBatch2x8 : kSkinnyMaxBatch4x8})
+        if (p.bytes >= 0 && t < batch && skinny_serves(sc, n, out, in, t))
+            p.bytes = std::max(p.bytes, skinny_partial_bytes(sc, n, out, in, t));
     return p;
 }
 
@@ -86,7 +92,7 @@ BackwardPlan backward_plan(int n, int act, const GenericScheme& sc, int64_t out,
         p.grad = !skinny_back_grads(sc, n, out, in, batch);
         if (p.grad) {
             add_dz();
-            p.partial = parts.add(grad_chunks(out, batch), n * out, 4);
+            p.partial = parts.add(grad_chunks_room(out, batch), n * out, 4);
         }
         p.parts = out == 0 || batch == 0 ? 0 : parts.add(skinny_back_partial_bytes(sc, n, out, in, batch), 1, 1);
         p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
@@ -95,9 +101,12 @@ BackwardPlan backward_plan(int n, int act, const GenericScheme& sc, int64_t out,
     p.grad = n > 1 || act != kActNone || p.op != out;
     p.wt = parts.add(in, n * p.op, 2);
     add_dz();
-    p.partial = parts.add(grad_chunks(out, batch), n * out, 4);
+    p.partial = parts.add(grad_chunks_room(out, batch), n * out, 4);
     p.parts = parts.add(dense_partial_bytes(1, in, n * p.op, batch), 1, 1);
     p.bytes = (out == 0 || batch == 0) ? 0 : parts.total;
+    const int64_t direct = sc.M == 1 ? kSkinnyBackMaxBatch1x16 : sc.M == 2 ? kSkinnyBackMaxBatch2x8 : kSkinnyBackMaxBatch4x8;
+    if (p.bytes > 0 && direct < batch && skinny_back_serves(sc, out, in, direct))
+        p.bytes = std::max(p.bytes, backward_plan(n, act, sc, out, in, direct).bytes);
     return p;
 }
 

@@ -22,13 +22,7 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kGradCols = kLevelCols;   // columns per workgroup: 64 lanes of 8
-
-// Tokens per wave, all loaded before any is used: 4, or 1 where that leaves fewer than two
-// workgroups a CU (8 tokens of 4096 gated rows: 10.2 us with 4, 6.0 with 1).
-int grad_wave_tokens(int64_t out, int64_t batch) {
-    return (out + kGradCols - 1) / kGradCols * ((batch + 15) / 16) < 512 ? 1 : 4;
-}
+static_assert(kGradCols == 64 * 8 && kGradCols == kLevelCols, "columns per workgroup: 64 lanes of 8");
 
 struct GradArgs {
     const f16* dy;

@@ -9,6 +9,14 @@ namespace aqlm {
 
 struct BiasSum;   // act_bias.h
 
+// Workspaces never shrink as the batch grows, so that one sized for the largest batch serves all: the
+// *_bytes functions below give room for any batch up to theirs, in closed form or as the largest over its steps.
+// Where a product's sum is split into fp32 parts, at most kPartsRoom bytes of them are written (or one
+// part, if that is more and the product always writes one): a limit that only products larger than a full chip's
+// tiles feel (over a grid of layers and batches the planned times rise by 0.02 % on average, 7 % at most).
+constexpr int kMaxSplits = 32;
+constexpr int64_t kPartsRoom = (int64_t)128 << 20;
+
 // Workgroups go to the 8 XCDs in turn: the place of workgroup b of n in an order in which each XCD
 // has a contiguous run, so that neighbours in it share an L2 (any count gives correct results).
 __device__ __forceinline__ int xcd_run(int b, int n) {
@@ -64,7 +72,7 @@ hipError_t launch_zero16(void* p, int64_t n, hipStream_t stream);
 
 // The dense product of gemm_dense.hip on fp16 weights w[l] [out][kp] with an epilogue:
 // z_l = scales[l] (x w_l^T) + bias_l (scales NULL: 1).  partial: dense_partial_bytes bytes,
-// for shapes whose k steps are split over workgroups (0: not used).
+// for shapes whose k steps are split over workgroups.
 int64_t dense_partial_bytes(int n, int64_t out, int64_t kp, int64_t batch);
 hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void* const* scales, int n,
                                  const Epilogue& epi, void* partial, int64_t out, int64_t kp, int64_t batch,
@@ -92,6 +100,19 @@ inline float* grad_units(void* dz, int n, int64_t op, int64_t batch) {
     return reinterpret_cast<float*>(grad_levels(dz, n, op, batch) + grad_align(batch * n * grad_level_cols(op)));
 }
 int64_t grad_chunks(int64_t out, int64_t batch);
+// Tokens per wave: 4, or 1 where that leaves fewer than two workgroups a CU (8 tokens of 4096 gated rows: 10.2 us
+// with 4, 6.0 with 1).
+constexpr int kGradCols = 512, kGradFew = 512;
+inline int grad_wave_tokens(int64_t out, int64_t batch) {
+    return (out + kGradCols - 1) / kGradCols * ((batch + 15) / 16) < kGradFew ? 1 : 4;
+}
+// The most chunks of any batch up to this one: of it, or of the last with one token a wave.
+inline int64_t grad_chunks_room(int64_t out, int64_t batch) {
+    if (out < 1) return 0;
+    const int64_t one = (kGradFew - 1) / ((out + kGradCols - 1) / kGradCols) * 16;
+    const int64_t few = ((batch < one ? batch : one) + 3) / 4, many = (batch + 15) / 16;
+    return few > many ? few : many;
+}
 hipError_t launch_act_grad(const void* dy, const void* const* z, const void* const* scales, int n, int act, void* dz,
                            float* partial, int64_t out, int64_t op, int64_t batch, hipStream_t stream);
 hipError_t launch_bias_sum(const BiasSum& b, hipStream_t stream);
@@ -110,7 +131,7 @@ bool launch_gemv_stream_act(const ActLayers& L, const GemvEpi& epi, const void* 
 // workgroups, a fixed number so that the sums' order does not depend on the device.
 constexpr int kSkinnyWorkgroups = 256;
 constexpr int kSkinnyMaxBatch2x8 = 512;
-constexpr int kSkinnyMaxBatch1x16 = 256;
+constexpr int kSkinnyMaxBatch1x16 = 256, kSkinnyMaxBatch1x16Few = 128;   // Few: of layers with few units
 constexpr int kSkinnyMaxBatch4x8 = 320;
 bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
 int64_t skinny_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);

@@ -62,6 +62,8 @@
 // lane quarters, 4 rows apart, then hit distinct banks) and finishes 8 outputs a lane,
 // with 16-byte accesses to y, z and the residual; everything up to the one rounding
 // of y (and of z where it is kept) is fp32.
+#include <algorithm>
+
 #include "act_bias.h"
 #include "act_launch.h"
 #include "act_math.h"
@@ -442,15 +444,19 @@ struct DensePlan {
 constexpr int kDenseCus = 256;
 constexpr double kStepUs = 0.85, kRoundUs = 3.0, kFinishUs = 3.0, kPartBytesUs = 2.5e6;
 
+// Bytes of one part of the product of n layers.
+int64_t part_bytes(int n, int64_t out, int64_t batch) { return batch * n * ((out + 7) / 8 * 8) * 4; }
+
 DensePlan dense_plan(int n, int64_t out, int64_t in, int64_t batch) {
     DensePlan best = {kDenseBM, 1};
     double best_us = 1e300;
-    const int64_t n_k = in / 64;
+    const int64_t n_k = in / 64, part = part_bytes(n, out, batch);
     for (int bm = 128; bm <= 256; bm += 128) {
         if (bm == 128 && batch > 1024) continue;
         const int64_t cols = (kDenseBM + kDenseBN - bm) / n;
         const int64_t tiles = (out + cols - 1) / cols * ((batch + bm - 1) / bm);
-        for (int s = 1; s <= 32 && s <= n_k; ++s) {
+        for (int s = 1; s <= kMaxSplits && s <= n_k; ++s) {
+            if (s > 1 && s * part > kPartsRoom) break;
             const int64_t rounds = (tiles * s + kDenseCus - 1) / kDenseCus, steps = (n_k + s - 1) / s;
             double us = (double)rounds * ((double)steps * kStepUs + kRoundUs);
             if (s > 1) us += kFinishUs + (double)s * batch * n * out * 8 / kPartBytesUs;
@@ -471,8 +477,8 @@ hipError_t launch_gemm_dense(const void* x, const void* w16, void* y, int64_t ou
 }
 
 int64_t dense_partial_bytes(int n, int64_t out, int64_t kp, int64_t batch) {
-    const DensePlan p = dense_plan(n, out, kp, batch);
-    return p.splits == 1 ? 0 : (int64_t)p.splits * batch * n * ((out + 7) / 8 * 8) * 4;
+    const int64_t splits = std::min<int64_t>(kMaxSplits, kp / 64);
+    return splits < 2 ? 0 : std::min(splits * part_bytes(n, out, batch), kPartsRoom);
 }
 
 hipError_t launch_gemm_dense_act(const void* x, const void* const* w, const void* const* scales, int n,

@@ -617,13 +617,18 @@ bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int6
     if (batch > (two ? kSkinnyMaxBatch2x8 : one ? kSkinnyMaxBatch1x16 : kSkinnyMaxBatch4x8)) return false;
     const int64_t rows = kKTiles * (n == 2 ? 8 : 16);
     const int64_t units = (out + rows - 1) / rows * ((in / kGroup + kKSlab - 1) / kKSlab);
-    if (one && units < (batch <= 128 ? 128 : 512)) return false;
+    if (one && units < (batch <= kSkinnyMaxBatch1x16Few ? 128 : 512)) return false;
     return (batch + 31) / 32 * units < (1 << 30);   // units are counted in 32 bits
 }
 
 int64_t skinny_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
-    const SkinnyPlan p = skinny_plan(sc, n, out, in, batch);
-    return (int64_t)p.slots * batch * n * p.op * 4;
+    // the plan changes at multiples of 32 tokens and is linear in the batch in between
+    int64_t room = 0;
+    for (int64_t t = std::min<int64_t>(32, batch);; t = std::min(t + 32, batch)) {
+        const SkinnyPlan p = skinny_plan(sc, n, out, in, t);
+        room = std::max(room, (int64_t)p.slots * t * n * p.op * 4);
+        if (t == batch) return room;
+    }
 }
 
 hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void* x, void* partial, const Epilogue& epi,

@@ -376,6 +376,9 @@ struct BackPlan {
 // fewest microseconds: rounds of one workgroup a CU, each some time to start and end and
 // kChunkUs per chunk of a wave (1x16: 4096 gathers of the workgroup's waves, at the rate a CU gets), then the parts,
 // written and added.
+// Bytes of one part of dx of n layers (their parts lie side by side).
+int64_t part_bytes(int n, int64_t n_cb, int64_t batch) { return n * batch * n_cb * kBGroups * kGroup * 4; }
+
 BackPlan back_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     const bool two = sc.B == 8;   // 2x8, 4x8 g16
     BackPlan p;
@@ -387,7 +390,9 @@ BackPlan back_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, int6
     const double part_us = 0.15 * n + (double)n * batch * p.n_cb * kBGroups * kGroup * 8 / 3e6;
     double best = 1e300;
     p.splits = 1;
-    for (int s = 1; s <= 32 && s <= n_chunks; ++s) {
+    const int64_t part = part_bytes(n, p.n_cb, batch);
+    for (int s = 1; s <= kMaxSplits && s <= n_chunks; ++s) {
+        if (s > 1 && s * part > kPartsRoom) break;
         const int64_t rounds = (wgs * s + kSkinnyWorkgroups - 1) / kSkinnyWorkgroups;
         const double us = rounds * ((double)((n_chunks + waves * s - 1) / (waves * s)) * chunk_us + 4.0) + s * part_us;
         if (us < best) {
@@ -430,8 +435,8 @@ bool skinny_back_serves(const GenericScheme& sc, int64_t out, int64_t in, int64_
 }
 
 int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
-    const BackPlan p = back_plan(sc, n, out, in, batch);
-    return (int64_t)p.splits * n * batch * p.n_cb * kBGroups * kGroup * 4;
+    const int64_t part = part_bytes(n, (in / kGroup + kBGroups - 1) / kBGroups, batch);
+    return std::max(part, std::min(std::min<int64_t>(kMaxSplits, (out + 63) / 64 * 2) * part, kPartsRoom));
 }
 
 // Where a wave of a full chip has few chunks: a launch saved is 1.5 to 3.5 us, while every chunk's

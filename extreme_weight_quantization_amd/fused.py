@@ -120,22 +120,22 @@ def _bytes(name, *shape) -> int:
 
 
 def linear_act_workspace_bytes(M: int, B: int, g: int, out: int, n_in: int, batch: int) -> int:
-    """Bytes of workspace aqlm_linear_act needs for the shape."""
+    """Bytes of workspace aqlm_linear_act needs for the shape and any smaller batch of it."""
     return _bytes("aqlm_linear_act_workspace_bytes", M, B, g, out, n_in, batch)
 
 
 def gated_workspace_bytes(M: int, B: int, g: int, out: int, n_in: int, batch: int) -> int:
-    """Bytes of workspace aqlm_gated needs for the shape (out: rows of the gate and of the up projection)."""
+    """Bytes of workspace aqlm_gated needs for the shape and any smaller batch of it (out: rows of either layer)."""
     return _bytes("aqlm_gated_workspace_bytes", M, B, g, out, n_in, batch)
 
 
 def linear_act_backward_workspace_bytes(M: int, B: int, g: int, out: int, n_in: int, batch: int) -> int:
-    """Bytes of workspace aqlm_linear_act_backward needs for the shape."""
+    """Bytes of workspace aqlm_linear_act_backward needs for the shape and any smaller batch of it."""
     return _bytes("aqlm_linear_act_backward_workspace_bytes", M, B, g, out, n_in, batch)
 
 
 def gated_backward_workspace_bytes(M: int, B: int, g: int, out: int, n_in: int, batch: int) -> int:
-    """Bytes of workspace aqlm_gated_backward needs for the shape."""
+    """Bytes of workspace aqlm_gated_backward needs for the shape and any smaller batch of it."""
     return _bytes("aqlm_gated_backward_workspace_bytes", M, B, g, out, n_in, batch)
 
 

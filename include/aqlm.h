@@ -368,7 +368,9 @@ int aqlm_linear_gemv_lists_noalloc(const void* table, const void* entries, int64
  *
  * Workspace: caller-owned device memory, 16-byte aligned, of at least the
  * bytes that the _workspace_bytes call of the same shape gives (0 for some
- * shapes: NULL is then accepted; an undersized one gives AQLM_ERR_SHAPE).  Its
+ * shapes: NULL is then accepted; an undersized one gives AQLM_ERR_SHAPE).  The
+ * bytes of a larger batch of the same call, scheme, out and in are never
+ * fewer, so a workspace for the largest batch serves every smaller one.  Its
  * contents on entry do not matter; calls that share it, captured graphs
  * included, must not run concurrently.
  *
