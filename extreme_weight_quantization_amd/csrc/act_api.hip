@@ -66,7 +66,7 @@ ForwardPlan forward_plan(int n, const GenericScheme& sc, int64_t out, int64_t in
     p.partial = parts.add(dense_partial_bytes(n, out, p.kp, batch), 1, 1);
     p.bytes = parts.total;
     // not less than the batches below need that are served straight from the codes
-    for (int64_t t : {kSkinnyMaxBatch1x16Few, sc.M == 1 ? kSkinnyMaxBatch1x16 : sc.M == 2 ? kSkinnyMaxBatch2x8 : kSkinnyMaxBatch4x8})
+    for (int64_t t : {kSkinnyMaxBatch1x16Few, skinny_max_batch(sc, n)})
         if (p.bytes >= 0 && t < batch && skinny_serves(sc, n, out, in, t))
             p.bytes = std::max(p.bytes, skinny_partial_bytes(sc, n, out, in, t));
     return p;

@@ -130,9 +130,15 @@ bool launch_gemv_stream_act(const ActLayers& L, const GemvEpi& epi, const void* 
 // fp32 partial sums in the workspace.  The work is dealt to at most kSkinnyWorkgroups
 // workgroups, a fixed number so that the sums' order does not depend on the device.
 constexpr int kSkinnyWorkgroups = 256;
-constexpr int kSkinnyMaxBatch2x8 = 512;
+constexpr int kSkinnyMaxBatch2x8 = 512, kSkinnyMaxBatch2x8Gated = 384;
 constexpr int kSkinnyMaxBatch1x16 = 256, kSkinnyMaxBatch1x16Few = 128;   // Few: of layers with few units
-constexpr int kSkinnyMaxBatch4x8 = 320;
+constexpr int kSkinnyMaxBatch4x8 = 320, kSkinnyMaxBatch4x8Gated = 256;
+// The largest batch of n layers, by scheme (one of the three).
+inline int skinny_max_batch(const GenericScheme& sc, int n) {
+    if (sc.M == 1) return kSkinnyMaxBatch1x16;
+    if (sc.M == 2) return n == 2 ? kSkinnyMaxBatch2x8Gated : kSkinnyMaxBatch2x8;
+    return n == 2 ? kSkinnyMaxBatch4x8Gated : kSkinnyMaxBatch4x8;
+}
 bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
 int64_t skinny_partial_bytes(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch);
 hipError_t launch_skinny(const GenericScheme& sc, const ActLayers& L, const void* x, void* partial, const Epilogue& epi,

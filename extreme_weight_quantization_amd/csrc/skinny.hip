@@ -15,10 +15,9 @@
 //    which is one group of 8: a lane looks its groups up (2x8: two codewords from the LDS
 //    copy of the codebooks, 8 replicas, conflict-free as in gemv.hip; 1x16: one 16-byte
 //    gather from L2, half a step ahead; 4x8 g16: the halves of four codewords from 2 replicas,
-//    2-way conflicts) and multiplies them at once.  Up to 64 tokens 2x8 multiplies its two
-//    codewords one by one, so no weight is rounded; above, it adds them in fp16
-//    (launch_scheme).  4x8 g16 adds its four in two pairs, whose roundings are together about
-//    as large as one rounding of the weight, and multiplies the pairs;
+//    2-way conflicts) and multiplies each codeword on its own, so no weight is rounded.  Their sums
+//    in fp16 would halve the products, for one rounding of every weight (2x8; two of 4x8 g16's pairs): gated
+//    4096x11008 at 256 tokens 97 -> 81 us, at 1000x2733 and 130 16.9 -> 16.3, 4x8 g16 at 40 46 -> 38;
 //  * a workgroup of 16 waves covers 256 rows (gated: 8 gate and 8 up rows a wave) and
 //    walks slabs of 32 groups (256 inputs); the x tile of a slab, BM tokens, sits in LDS
 //    for all waves, three stages of direct-to-LDS loads, one barrier a slab;
@@ -61,7 +60,7 @@ constexpr int kKCbBytes = 2 * kCodewords2x8 * kKRepl * 16;   // 64 KB; 4x8 g16: 
 constexpr bool lds_codebooks(int scheme) { return scheme != kScheme1x16; }
 // The kernels that have a short form for a last token tile that is at most half full.  Not 1x16: its
 // gathers, which bound it, stay the same.
-constexpr bool skinny_halves(int scheme, int bm, bool sum) { return bm == 64 && (scheme == kSchemeB8M4 || sum); }
+constexpr bool skinny_halves(int scheme, int bm) { return bm == 64 && lds_codebooks(scheme); }
 
 // Units dealt to W workgroups in contiguous runs.  A unit takes one place; or (`full` >= 0, for a
 // last token tile at most half full) the units of the other tiles, the first `full`, take two,
@@ -116,9 +115,8 @@ enum RowKind : int { kRowWhole = 0, kRowVec = 1, kRowAny = 2 };
 // Zeros that the direct-to-LDS loads of x read in the place of groups past the row.
 __device__ const u32x4 skinny_zero = {0u, 0u, 0u, 0u};
 
-// RT: row tiles of a wave (16 / RT waves a workgroup).  SUM: 2x8 adds its two codewords in
-// fp16 (one rounding) before one product, instead of multiplying both.
-template <int SCHEME, int BM, bool GATED, int ROW, int RT, bool SUM>
+// RT: row tiles of a wave (16 / RT waves a workgroup).
+template <int SCHEME, int BM, bool GATED, int ROW, int RT>
 __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_eu(4 / RT, 4 / RT))) void skinny_kernel(
     const SkinnyArgs a) {
     extern __shared__ u32x4 smem[];
@@ -136,7 +134,7 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     constexpr int kIssued = kR == 2 ? RT + kGathers : kNX + RT + 2 * kGathers;
     constexpr int kTileRows = GATED ? 8 : 16;
     constexpr int kN = GATED ? 2 : 1;
-    constexpr bool kHalves = skinny_halves(SCHEME, BM, SUM);
+    constexpr bool kHalves = skinny_halves(SCHEME, BM);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lrow = lane & 15, kq = lane >> 4;
     const bool up = GATED && lrow >= 8;
@@ -293,7 +291,7 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
     auto multiply = [&](auto columns, const u32x4 (&cv)[RT], u32x4 (&e)[2][RT][4], const u32x4 (&ahead)[RT], bool more,
                         uint32_t xs, int left) {
         constexpr int kC = decltype(columns)::value;   // column tiles multiplied
-        constexpr int kReads = kC + (kCbLds ? kLook * RT : 0), kProducts = RT * kC * (kCbLds && !SUM ? 2 : 1);
+        constexpr int kReads = kC + (kCbLds ? kLook * RT : 0), kProducts = RT * kC * (kCbLds ? kLook : 1);
         f16x8 w[2][RT][kLook], xv[2][kC];
         fetch(cv, xs, 0, w[0], xv[0]);
 #pragma unroll
@@ -301,22 +299,15 @@ __global__ __launch_bounds__(64 * kKTiles / RT) __attribute__((amdgpu_waves_per_
             if (q + 1 < 8) fetch(cv, xs, q + 1, w[(q + 1) & 1], xv[(q + 1) & 1]);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                f16x8 a0 = w[q & 1][rt][0], a1 = w[q & 1][rt][1];
-                if constexpr (!kCbLds) a0 = as_f16x8(e[q >> 2][rt][q & 3]);
-                if constexpr (kFour) {
-                    a0 = a0 + a1;
-                    a1 = w[q & 1][rt][2] + w[q & 1][rt][3];
-                }
-                if constexpr (kCbLds && SUM) a0 = a0 + a1;
-                if constexpr (kRagged) {
-                    a0 = q < left ? a0 : f16x8{};
-                    if constexpr (kCbLds && !SUM) a1 = q < left ? a1 : f16x8{};
-                }
+                // every codeword on its own: no sum of them is rounded
+                constexpr int kEach = kCbLds ? kLook : 1;
 #pragma unroll
-                for (int j = 0; j < kC; ++j) acc[rt][j] = mfma16x16x32(a0, xv[q & 1][j], acc[rt][j]);
-                if constexpr (kCbLds && !SUM) {
+                for (int m = 0; m < kEach; ++m) {
+                    f16x8 c = w[q & 1][rt][m];
+                    if constexpr (!kCbLds) c = as_f16x8(e[q >> 2][rt][q & 3]);
+                    if constexpr (kRagged) c = q < left ? c : f16x8{};
 #pragma unroll
-                    for (int j = 0; j < kC; ++j) acc[rt][j] = mfma16x16x32(a1, xv[q & 1][j], acc[rt][j]);
+                    for (int j = 0; j < kC; ++j) acc[rt][j] = mfma16x16x32(c, xv[q & 1][j], acc[rt][j]);
                 }
             }
             if (q + 1 < 8) {
@@ -551,7 +542,7 @@ SkinnyPlan skinny_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, 
     const int64_t full = (n_tt - 1) * n_blk * n_slab;
     // Two places for a whole unit and one for a half one where that shortens the longest run, a half
     // unit counted as 0.8 (its lookups are whole): 264 units of gated 1000x2733 at 130 tokens, two
-    // in some runs, 21.8 -> 17.6 us; 16 a run (4096x11008 at 160) would take 68.3 instead of 61.5.
+    // in some runs, 21.6 -> 16.9 us; 16 a run (4096x11008 at 160) would take 75.1 instead of 71.0.
     int64_t places = units, each = 1;
     if (half) {
         const int64_t q = (full + units + kSkinnyWorkgroups - 1) / kSkinnyWorkgroups;   // places of the longest
@@ -568,11 +559,11 @@ SkinnyPlan skinny_plan(const GenericScheme& sc, int n, int64_t out, int64_t in, 
     return p;
 }
 
-template <int SCHEME, int BM, bool GATED, int RT, bool SUM>
+template <int SCHEME, int BM, bool GATED, int RT>
 hipError_t launch_main(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t stream) {
-    auto kern = a.G % kKSlab == 0 ? skinny_kernel<SCHEME, BM, GATED, kRowWhole, RT, SUM>
-                : a.G % 8 == 0    ? skinny_kernel<SCHEME, BM, GATED, kRowVec, RT, SUM>
-                                  : skinny_kernel<SCHEME, BM, GATED, kRowAny, RT, SUM>;
+    auto kern = a.G % kKSlab == 0 ? skinny_kernel<SCHEME, BM, GATED, kRowWhole, RT>
+                : a.G % 8 == 0    ? skinny_kernel<SCHEME, BM, GATED, kRowVec, RT>
+                                  : skinny_kernel<SCHEME, BM, GATED, kRowAny, RT>;
     constexpr size_t lds = (lds_codebooks(SCHEME) ? kKCbBytes : 0) + (size_t)skinny_stages(BM) * BM * kKSlab * 16;
     static_assert(lds <= 163840, "LDS budget");
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -583,20 +574,14 @@ hipError_t launch_main(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t str
 
 // Up to 32 tokens: one row tile a wave.  Above, the matrix cores and the LDS reads of x weigh
 // more than the lookups: two row tiles a wave read x half as often (gated 8192x28672 at 512
-// tokens 825 -> 786 us).  Above 64 tokens 2x8 adds its codewords in fp16 and multiplies
-// once: half the products (606 us) for one rounding a weight, which decoded
-// weights have too; up to 64, where it would gain 4-20 %, both are multiplied and no weight is rounded.
-// Gated 4096x11008 at 128 tokens 48.2 us against 56.6, 4096^2 linear at 128 18.6 against 19.6.
+// tokens 825 -> 786 us).
 template <int SCHEME, bool GATED>
 hipError_t launch_scheme(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t stream) {
-    if (p.bm == 32) return launch_main<SCHEME, 32, GATED, 1, false>(p, a, stream);
-    if constexpr (SCHEME == kScheme2x8) {
-        if (a.T > 64) return launch_main<SCHEME, 64, GATED, 2, true>(p, a, stream);
-    }
+    if (p.bm == 32) return launch_main<SCHEME, 32, GATED, 1>(p, a, stream);
     if constexpr (SCHEME == kScheme1x16) {
-        if (p.bm == 128) return launch_main<SCHEME, 128, GATED, 2, false>(p, a, stream);
+        if (p.bm == 128) return launch_main<SCHEME, 128, GATED, 2>(p, a, stream);
     }
-    return launch_main<SCHEME, 64, GATED, 2, false>(p, a, stream);
+    return launch_main<SCHEME, 64, GATED, 2>(p, a, stream);
 }
 
 }  // namespace
@@ -606,15 +591,16 @@ hipError_t launch_scheme(const SkinnyPlan& p, const SkinnyArgs& a, hipStream_t s
 // 26.0 against 29.7), and above 128 tokens every code is gathered twice (4096^2 at 256 tokens, 256 units:
 // 46 against 41; 4096x11008, 688 units: 80 against 98; at 512 tokens 128 against 115).  2x8
 // wins from the smallest layers (10.9 against 16.4 us on 2048x1024 at 64 tokens) up to 512
-// tokens (11008x4096 68 against 91, at 1024 123 against 129 and gated 283 against 229).  4x8 g16
-// wins likewise (1024^2 at 17 tokens 9.8 us against 13.3, gated 4096x11008 at 64 40.5 against
-// 138) up to about 320: 4096x11008 at 256 66.6 against 89.4, at 512 121 against 101.
+// tokens (4096^2 41.7 against 43.5, 11008x4096 87 against 90), gated, whose decoding is spread over twice the
+// products, up to about 384 (4096x11008 136 against 152, 8192x28672 608 against 580; at 512 178 against 169 and
+// 805 against 676).  4x8 g16 wins likewise (1024^2 at 17 tokens 9.8 us against 13.3, gated 4096x11008 at 64 49
+// against 140) up to about 320 (11008x4096 92.7 against 96.8), gated 256 (4096x11008 150 against 148, at 320 both 181).
 bool skinny_serves(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     const bool two = sc.M == 2 && sc.B == 8 && sc.g == 8, one = sc.M == 1 && sc.B == 16 && sc.g == 8;
     const bool four = sc.M == 4 && sc.B == 8 && sc.g == 16;
     if (!two && !one && !four) return false;
     if (out * (in / kGroup) < 8) return false;   // 16 bytes of codes a load
-    if (batch > (two ? kSkinnyMaxBatch2x8 : one ? kSkinnyMaxBatch1x16 : kSkinnyMaxBatch4x8)) return false;
+    if (batch > skinny_max_batch(sc, n)) return false;
     const int64_t rows = kKTiles * (n == 2 ? 8 : 16);
     const int64_t units = (out + rows - 1) / rows * ((in / kGroup + kKSlab - 1) / kKSlab);
     if (one && units < (batch <= kSkinnyMaxBatch1x16Few ? 128 : 512)) return false;

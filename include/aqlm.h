@@ -379,10 +379,9 @@ int aqlm_linear_gemv_lists_noalloc(const void* table, const void* entries, int64
  * once, y from the unrounded z.  With M = 1 the codewords are multiplied as
  * they are and the row scale is applied in fp32.  With M > 1 a weight is
  * rounded to fp16 once at most:
- *   - batch 1..16, and 2x8 up to 64 tokens: not at all (codewords multiplied
- *     one by one; the general schemes decode in fp32);
- *   - 2x8 from 65 to 512 tokens: the sum of its two codewords; 4x8 g16 from 17
- *     to 320: the sums of two pairs of codewords;
+ *   - batch 1..16, 2x8 up to 512 tokens (gated: 384) and 4x8 g16 up to 320
+ *     (gated: 256): not at all (codewords multiplied one by one; the general
+ *     schemes decode in fp32);
  *   - else the decoded weight that aqlm_linear_decode gives.
  * Backward, small batches (2x8 to 256 tokens, 1x16 and 4x8 g16 to 128) multiply
  * the codewords as they are, one by one, by dz times the row's scale.  Larger
@@ -393,9 +392,9 @@ int aqlm_linear_gemv_lists_noalloc(const void* table, const void* entries, int64
  * its largest finite value in them fixes, so that it does not leave fp16's
  * range: elements down to 2^-17 of the token's largest keep all their bits,
  * smaller ones are off by at most 2^-27 of it.  dbias sums the fp32 values in
- * a fixed order.  Sums of codewords and decoded weights beyond fp16's range are
- * infinite, decoded weights below 2^-14 lose bits; non-finite values reach the
- * outputs that they take part in and no others.  Results are deterministic.
+ * a fixed order.  Decoded weights beyond fp16's range are infinite, and those
+ * below 2^-14 lose bits; non-finite values reach the outputs that they take
+ * part in and no others.  Results are deterministic.
  */
 typedef enum {
     AQLM_ACT_NONE = 0,

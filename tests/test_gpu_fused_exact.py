@@ -39,6 +39,14 @@ def layer(scheme, out, n_in, seed, rows):
     return tuple(torch.from_numpy(a).cuda() for a in (L.codes, L.codebooks, L.scales)), R.weights(L)
 
 
+def plain_layer(scheme, out, n_in, seed):
+    """Independent codes and like codebooks; a product with x has about unit variance."""
+    M, B, g = SCHEMES[scheme]
+    L = synth.make_layer_mbg(M, B, g, out, n_in, 1, seed, 0.05)
+    L.scales = (L.scales.astype(np.float64) / (0.05 * np.sqrt(M * n_in))).astype(np.float16)
+    return tuple(torch.from_numpy(a).cuda() for a in (L.codes, L.codebooks, L.scales)), R.weights(L)
+
+
 def inputs(rng, T, n, step):
     """Normal fp16 numbers, each run of `step` the negative of the one before it."""
     v = rng.normal(0, 1, (T, n // (2 * step), 1, step))
@@ -47,6 +55,8 @@ def inputs(rng, T, n, step):
 
 FORWARD = [*[("2x8", out, n, T) for out, n in ((272, 512), (131, 528)) for T in (1, 2, 3, 4, 5, 8, 9, 16, 17, 32, 33, 64)],
            *[("2x8", 4112, 8192, T) for T in (1, 2, 3, 4)], ("2x8", 1040, 2048, 40),
+           *[("2x8", out, n, T) for out, n in ((272, 512), (131, 528)) for T in (65, 80, 97, 128, 130, 257, 320, 384)],
+           *[("4x8g16", out, n, T) for out, n in ((272, 512), (131, 544)) for T in (17, 33, 64, 65, 80, 97, 130, 256)],
            *[(s, 72, 512, T) for s in ("4x8g16", "8x8g32", "3x5g2", "2x10g4") for T in (1, 2, 5, 8, 9, 16)]]
 
 
@@ -64,6 +74,36 @@ def test_forward(scheme, out, n_in, T):
     y = E.aqlm_gated(gate, up, x.cuda(), act="none")
     want, tol, _ = R.gated(wg, wu, x.double(), "none", None, None, False)
     R.assert_within(y, want, tol, "gated y")
+
+
+# beyond the batches of the gated product
+LINEAR = [*[("2x8", out, n, T) for out, n in ((272, 512), (131, 528)) for T in (385, 500, 512)],
+          *[("4x8g16", out, n, T) for out, n in ((272, 512), (131, 544)) for T in (257, 300, 320)]]
+
+
+@pytest.mark.parametrize("scheme,out,n_in,T", LINEAR)
+def test_linear(scheme, out, n_in, T):
+    rng = np.random.default_rng(T)
+    gpu, w = layer(scheme, out, n_in, 1, False)
+    x = inputs(rng, T, n_in, SCHEMES[scheme][2])
+    y = E.aqlm_linear_act(*gpu, x.cuda())
+    want, tol, _, _ = R.linear(w, x.double(), "none", None, None, False)
+    R.assert_within(y, want, tol, "y")
+
+
+# both sides of the gated product's last batch straight from the codes
+@pytest.mark.parametrize("scheme,T", [("2x8", 384), ("2x8", 385), ("4x8g16", 256), ("4x8g16", 257)])
+def test_gated_limits(scheme, T):
+    rng = np.random.default_rng(T)
+    for out, n_in in ((272, 512), (131, 544)):
+        (gate, wg), (up, wu) = (plain_layer(scheme, out, n_in, seed) for seed in (1, 2))
+        x = torch.from_numpy(rng.normal(0, 1, (T, n_in)).astype(np.float16))
+        zg, zu = (torch.empty((T, out), dtype=torch.float16, device="cuda") for _ in range(2))
+        y = E.aqlm_gated(gate, up, x.cuda(), zg=zg, zu=zu)
+        want, tol, zs = R.gated(wg, wu, x.double(), "silu", None, None, T in (385, 257))
+        R.assert_within(y, want, tol, "y")
+        for got, (z, tz) in zip((zg, zu), zs):
+            R.assert_within(got, z, tz, "z")
 
 
 BACKWARD = [*[("2x8", out, T) for out in (512, 520, 1036) for T in (1, 8, 16, 17, 33, 64, 65, 200, 256)],
