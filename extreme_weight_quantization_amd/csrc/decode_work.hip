@@ -180,32 +180,45 @@ struct GradAlign {
     int T, cols;   // tokens (0: nothing to do), level columns of a layer
 };
 
+// Lanes that share a row of dz: a power of two, one a block or 64.
+__host__ __device__ inline int align_lanes(int n_blk) {
+    int lanes = 1;
+    while (lanes < 64 && lanes < n_blk) lanes *= 2;
+    return lanes;
+}
+
 // Brings every row of dz to the unit of its largest level, since the dense product sums over whole rows, and
-// writes the units.  A wave a row; blocks at a lower level are rewritten.  Done here because this launch lies between
+// writes the units; blocks at a lower level are rewritten.  Done here because this launch lies between
 // the one that writes dz and the product anyway; levels are 12 bits apart, so few rows have two.
 __device__ __forceinline__ void align_gradients(const GradAlign& g, int n, int op) {
-    const int lane = threadIdx.x & 63, n_blk = n * g.cols;
-    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < g.T; t += (int64_t)gridDim.x * 4) {
-        const int8_t* lv = g.levels + t * n_blk;
+    const int lane = threadIdx.x & 63, n_blk = n * g.cols, lanes = align_lanes(n_blk), rows = 64 / lanes;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    for (int64_t t0 = wave * rows; t0 < g.T; t0 += (int64_t)gridDim.x * 4 * rows) {
+        const int64_t t = t0 + lane / lanes;
         int top = kLevelMin, low = kLevelMax;
-        for (int b = lane; b < n_blk; b += 64) {
-            const int v = lv[b];
-            top = max(top, v);
-            low = min(low, v);
+        if (t < g.T) {
+            for (int b = lane % lanes; b < n_blk; b += lanes) {
+                const int v = g.levels[t * n_blk + b];
+                top = max(top, v);
+                low = min(low, v);
+            }
         }
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
+        for (int o = lanes / 2; o >= 1; o /= 2) {
             top = max(top, __shfl_xor(top, o, 64));
             low = min(low, __shfl_xor(low, o, 64));
         }
-        if (lane == 0) g.units[t] = level_unit(top);
-        if (low == top) continue;
-        for (int b = 0; b < n_blk; ++b) {
-            const int d = top - lv[b];
-            const int l = b / g.cols, c = (b - l * g.cols) * kLevelCols + 8 * lane;   // its 512 rows, 8 a lane
-            if (d == 0 || c >= op) continue;
-            u32x4* p = reinterpret_cast<u32x4*>(g.dz + t * n * op + (int64_t)l * op + c);
-            *p = raise_level(*p, d);
+        const bool first = lane % lanes == 0 && t < g.T;
+        if (first) g.units[t] = level_unit(top);
+        for (uint64_t mixed = __ballot(first && low != top); mixed != 0; mixed &= mixed - 1) {   // the wave a row
+            const int src = __ffsll((unsigned long long)mixed) - 1, highest = __shfl(top, src, 64);
+            const int64_t row = t0 + src / lanes;
+            for (int b = 0; b < n_blk; ++b) {
+                const int d = highest - g.levels[row * n_blk + b];
+                const int l = b / g.cols, c = (b - l * g.cols) * kLevelCols + 8 * lane;   // its 512 rows of W, 8 a lane
+                if (d == 0 || c >= op) continue;
+                u32x4* p = reinterpret_cast<u32x4*>(g.dz + row * n * op + (int64_t)l * op + c);
+                *p = raise_level(*p, d);
+            }
         }
     }
 }
@@ -217,6 +230,7 @@ __global__ __launch_bounds__(256) void decode_transposed_kernel(DecodeArgs a, in
                                                                 int n_row_tiles, int n_tiles, int M, int B, GradAlign grads) {
     __shared__ u32x4 cb_lds[work_cb_slots<SCHEME>()];
     align_gradients(grads, n, op);
+    if ((int)blockIdx.x >= n_tiles) return;   // the whole workgroup: few tiles, many rows of dz
     const uint32_t P = (uint32_t)in / 8;
     const int oct = threadIdx.x & 7, piece = threadIdx.x >> 3;
     auto row_of = [&](int tile) { return (tile % n_row_tiles) * 64 + 8 * oct; };
@@ -316,7 +330,9 @@ hipError_t launch_ws(const DecodeArgs& a, int n, int64_t out, int64_t in, int64_
         const int64_t n_rt = op / 64, n_pt = (in + 255) / 256;
         const int64_t tiles = n_rt * n_pt, cap = (int64_t)device_cu_count() * 8;
         if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((decode_transposed_kernel<SCHEME, G, CB, WS>), dim3((unsigned)(tiles < cap ? tiles : cap)),
+        const int64_t per = 4 * 64 / align_lanes(n * grads.cols);   // rows of dz a workgroup aligns at a time
+        const int64_t rows = (grads.T + per - 1) / per, work = rows > tiles ? rows : tiles;
+        hipLaunchKernelGGL((decode_transposed_kernel<SCHEME, G, CB, WS>), dim3((unsigned)(work < cap ? work : cap)),
                            dim3(256), 0, stream, a, n, (int)out, (int)in, (int)op, (int)ld, (int)n_rt, (int)tiles, M, B, grads);
     } else {
         const int64_t per_row = ld / 8;

@@ -165,3 +165,13 @@ def test_an_infinite_gradient_next_to_large_and_small_ones():
         keep = [t for t in range(T) if t not in (1, 3)]
         assert torch.isfinite(a).all() and torch.equal(a[keep], b[keep]), (scheme, T)
         assert not torch.isfinite(b[1]).any() and torch.isnan(b[3]).all(), (scheme, T)
+
+
+@pytest.mark.parametrize("scheme", list(SCHEMES))
+@pytest.mark.parametrize("out,n_in,T", [(264, 272, 1100), (264, 272, 100), (264, 272, 7), (20000, 64, 300), (64, 64, 5003)])
+def test_the_two_layers_of_a_token_at_different_levels(scheme, out, n_in, T):
+    """dzg far above dzu in most tokens, below it in some: few and many blocks a token, more tokens than weights."""
+    rng = np.random.default_rng(8)
+    zu = normal(rng, T, out, scale=2.0 ** np.where(np.arange(T) % 5 == 2, -9.0, 10.0)[:, None])
+    zg = normal(rng, T, out, scale=2.0 ** np.where(np.arange(T) % 5 == 2, 3.0, -8.0)[:, None])
+    check_gated(scheme, out, n_in, T, normal(rng, T, out, scale=8), zg, zu, size=2.0 ** -5)
