@@ -1,6 +1,6 @@
 // Activations of the fused products and their slopes, in fp32 (device helpers).
 //
-//   relu       max(z, 0)                             slope 1 for z > 0, else 0
+//   relu       max(z, 0)                             slope 1 for z > 0, 0 for z <= 0
 //   silu       z p,           p = 1 / (1 + e^-z)     slope p (1 + z (1 - p))
 //   gelu       z erfc(-z / sqrt 2) / 2               slope erfc(-z / sqrt 2) / 2 + z e^(-z^2 / 2) / sqrt(2 pi)
 //   gelu_tanh  z (1 + tanh v) / 2 = z p(2v),         slope p + z p (1 - p) 2 v',
@@ -34,7 +34,7 @@ __device__ __forceinline__ float act_value(float z) {
 
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-    if constexpr (ACT == kActRelu) return z <= 0.f ? 0.f : 1.f;
+    if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;   // NaN: neither
     if constexpr (ACT == kActSilu) {
         const float p = logistic(z);
         return p * (1.f + z * (1.f - p));

@@ -175,3 +175,21 @@ def test_the_two_layers_of_a_token_at_different_levels(scheme, out, n_in, T):
     zu = normal(rng, T, out, scale=2.0 ** np.where(np.arange(T) % 5 == 2, -9.0, 10.0)[:, None])
     zg = normal(rng, T, out, scale=2.0 ** np.where(np.arange(T) % 5 == 2, 3.0, -8.0)[:, None])
     check_gated(scheme, out, n_in, T, normal(rng, T, out, scale=8), zg, zu, size=2.0 ** -5)
+
+
+@pytest.mark.parametrize("T", [5, 40, 300])
+def test_nan_pre_activations_give_nan(T):
+    """For every activation that looks at them."""
+    rng = np.random.default_rng(9)
+    for name in ("relu", "silu", "gelu", "gelu_tanh"):
+        gate, _, _ = layer("2x8", 264, 272, 0)
+        up, _, _ = layer("2x8", 264, 272, 1)
+        dy, zg, zu = normal(rng, T, 264) + 2, normal(rng, T, 264), normal(rng, T, 264)
+        bad = zg.clone()
+        bad[2, 100] = float("nan")
+        a, b = (E.aqlm_linear_act_backward(*gate, dy.cuda(), act=name, z=z.cuda(), need_dbias=True) for z in (zg, bad))
+        keep = [t for t in range(T) if t != 2]
+        assert torch.equal(a[0][keep], b[0][keep]) and torch.isnan(b[0][2]).all(), (name, T)
+        assert torch.isnan(b[1][100]) and int(torch.isnan(b[1]).sum()) == 1, (name, T)
+        a, b = (E.aqlm_gated_backward(gate, up, dy.cuda(), z.cuda(), zu.cuda(), act=name)[0] for z in (zg, bad))
+        assert torch.equal(a[keep], b[keep]) and torch.isnan(b[2]).all(), (name, T)
