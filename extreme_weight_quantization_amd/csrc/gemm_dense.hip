@@ -436,8 +436,11 @@ hipError_t launch_dense(const void* x, const void* w16, void* y, int64_t out, in
 // How the product of n layers is tiled: tokens of a tile, and the workgroups that share a
 // tile's k steps.  A whole launch of tiles runs in rounds of kDenseCus workgroups, each as
 // long as its k steps; the split that takes the fewest microseconds by this count is
-// taken, with kStepUs for a step, kRoundUs to fill and drain a round's pipeline, and kPartBytesUs to write and
-// add the parts (a plain launch has none, and stores y itself).
+// taken, with kStepUs for a step, kRoundUs to fill and drain a round's pipeline, kFinishUs for the finishing
+// launch and kPartBytesUs to write and add the parts (a plain launch has none, and stores y itself).
+// Measured on 256 CUs, kernel times by the profiler: 32768 rows at 256 tokens, one round of 128 x 256 tiles, take 28,
+// 47, 77 and 161 us for 16, 32, 64 and 128 steps (0.9 to 1.3 a step), 4096 rows at 200 tokens with split steps 21.6 and
+// 28.2 for 64 and 128 (0.8 to 0.9 a step, start and end 3 to 9), their finishing launch 4.8 and 5.8.
 struct DensePlan {
     int bm, splits;
 };

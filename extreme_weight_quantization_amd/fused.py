@@ -7,7 +7,8 @@
 
 As in ``binding``: tensors are checked for device, dtype, shape and contiguity, then handed to the C ABI with
 torch's current HIP stream of their device; every step of the computation runs in the library's kernels.  The
-quantized weights are frozen.  A layer is (codes, codebooks, scales), or (SliceLists, codebooks, scales) for the
+quantized weights are frozen.  No call records an autograd graph: an input that requires a gradient gives a result
+without one, and the backward calls are what a ``torch.autograd.Function`` around a layer runs.  A layer is (codes, codebooks, scales), or (SliceLists, codebooks, scales) for the
 batch-1 calls over slice lists.
 """
 from __future__ import annotations
