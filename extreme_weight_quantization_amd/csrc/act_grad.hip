@@ -105,16 +105,14 @@ __global__ __launch_bounds__(256) void act_grad_kernel(GradArgs a) {
         }
 #pragma unroll
         for (int l = 0; l < N; ++l) {
-            float largest = 0.f;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 g[l][q] = q < left ? g[l][q] : 0.f;
                 sum[l][q] += g[l][q];
                 g[l][q] = q < left ? g[l][q] * m[l][q] : 0.f;
-                largest = fmaxf(largest, finite_magnitude(g[l][q]));
             }
             if (a.dz == nullptr) continue;
-            const int level = grad_level(wave_max(largest));
+            const int level = grad_level(wave_max(largest_finite(g[l])));
             const float unit = level_unit(-level);
             f16x8 o;
 #pragma unroll

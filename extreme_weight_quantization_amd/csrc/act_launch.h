@@ -86,7 +86,7 @@ hipError_t launch_finish(int n, const float* partial, const void* const* scales,
 // Gradients of the pre-activations, fp16, as the dense product's x: dz[t][l * op + i] for
 // i < op (rows past `out` zero).  One layer: dy act'(z); two: dy zu act'(zg) and dy act(zg).
 // scales: row scales that multiply them in fp32 (NULL: none).
-// dz is in units of 2^(12 level) (act_math.h); behind it, each 256-byte aligned, lie the levels
+// dz is in units of 2^(20 level) (act_math.h); behind it, each 256-byte aligned, lie the levels
 // [batch][n][grad_level_cols(op)] of the blocks of 512 rows, and room for one unit a token.
 // partial: fp32 [grad_chunks(out, batch)][n][out]: sums over chunks of tokens of the unscaled
 // fp32 gradients (NULL: not wanted); launch_bias_sum, or the launch that finishes a

@@ -189,7 +189,7 @@ __host__ __device__ inline int align_lanes(int n_blk) {
 
 // Brings every row of dz to the unit of its largest level, since the dense product sums over whole rows, and
 // writes the units; blocks at a lower level are rewritten.  Done here because this launch lies between
-// the one that writes dz and the product anyway; levels are 12 bits apart, so few rows have two.
+// the one that writes dz and the product anyway; levels are 20 bits apart, so few rows have two.
 __device__ __forceinline__ void align_gradients(const GradAlign& g, int n, int op) {
     const int lane = threadIdx.x & 63, n_blk = n * g.cols, lanes = align_lanes(n_blk), rows = 64 / lanes;
     const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);

@@ -14,7 +14,7 @@
 //  * The row scale is in dz (act_grad.hip), which is rounded to fp16 anyway, and the codewords are
 //    multiplied as they are, one by one for 2x8 and 4x8 g16, so no weight is rounded (pairs of
 //    4x8 g16 added in fp16, as forward, are too coarse next to the rounding of dz).
-//  * dz of a token comes in units of 2^(12 level), one level per 512 rows (act_math.h).  The sums of
+//  * dz of a token comes in units of 2^(20 level), one level per 512 rows (act_math.h).  The sums of
 //    a token are kept at its highest level in the workgroup's rows (a lane has one token per column tile),
 //    blocks at a lower one are brought to it as they are used, and the sums leave in units of one.
 //  * A workgroup of 8 waves (4 at 128 tokens) owns 16 groups (128 inputs) of dx and a part of the rows of one
@@ -184,16 +184,16 @@ __global__ __launch_bounds__(64 * back_waves(CT))
         if (l == 0) act_slopes(a.act, g);   // none: ones
         else act_values(a.act, g);
         const bool inside = row0(c) < a.out && lrow < a.T;
-        float scaled[8], largest = 0.f;
+        float scaled[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             g[r] *= (float)dy[r];
             if (a.n == 2 && l == 0) g[r] *= (float)z1[r];
             g[r] = inside ? g[r] : 0.f;
             scaled[r] = inside ? g[r] * (float)scale[r] : 0.f;
-            largest = fmaxf(largest, finite_magnitude(scaled[r]));
         }
         // the four quarters hold the token's other rows
+        float largest = largest_finite(scaled);
         largest = fmaxf(largest, __shfl_xor(largest, 16, 64));
         largest = fmaxf(largest, __shfl_xor(largest, 32, 64));
         const int now = max(top[0], grad_level(largest));

@@ -390,8 +390,8 @@ int aqlm_linear_gemv_lists_noalloc(const void* table, const void* entries, int64
  * by dy as it is, for every M.  dz, times the scale where it takes it, is
  * rounded to fp16 once, in units of a power of two per token and 512 rows that
  * its largest finite value in them fixes, so that it does not leave fp16's
- * range: elements down to 2^-17 of the token's largest keep all their bits,
- * smaller ones are off by at most 2^-27 of it.  dbias sums the fp32 values in
+ * range: elements down to 2^-9 of the token's largest keep all their bits,
+ * smaller ones are off by at most 2^-19 of it.  dbias sums the fp32 values in
  * a fixed order.  Decoded weights beyond fp16's range are infinite, and those
  * below 2^-14 lose bits; non-finite values reach the outputs that they take
  * part in and no others.  Results are deterministic.
