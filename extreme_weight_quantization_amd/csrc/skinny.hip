@@ -27,11 +27,11 @@
 //    block's parts in order, applies the row scale and the epilogue, and rounds once.
 //
 // What bounds it.  1x16: the gathers, one L2 request each; 4096x11008 at 48 tokens, main kernel
-// 32.7 us by the profiler for 5.6 M of them, 172 G/s of the 264 G/s that a kernel of nothing
+// 34 us by the profiler for 5.6 M of them, 170 G/s of the 264 G/s that a kernel of nothing
 // else reaches (runs of 3 units where 2.7 would be even, and about 8 us to start and end).
-// 2x8 and 4x8 g16: LDS reads (gated 4096x11008 2x8 at 256 tokens: 2.8 M, at 8 clocks each 58 %
-// of the kernel's 67.7 us, matrix cores 29 %), at small sizes the start, two dependent loads
-// and the end of a run.
+// 2x8 and 4x8 g16: matrix cores and LDS reads alike (gated 4096x11008 2x8 at 256 tokens: 5.6 M products of 16
+// cycles and 2.8 M reads at 8 clocks each are 50 % each of the kernel's 85 us at 2.1 GHz), at small sizes the
+// start, two dependent loads and the end of a run.
 //
 // LDS layout of an x stage: token b, group c in 16-byte slot 32 b + (x_place(c) ^ (b % 16)).
 // A 16-byte LDS read serves 16 lanes at a time: 0-3, 12-15 and 20-27; 4-11, 16-19 and 28-31;

@@ -32,15 +32,16 @@
 //  * Neighbouring 16-group columns share lines of codes (128 bytes hold 64 groups), so they run
 //    on one XCD (xcd_run): 4096x11008 1x16 at 20 tokens 38.3 -> 36.5 us.
 //
-// What bounds it.  1x16: the gathers (4096x11008 at 77 tokens, main kernel 42.6 us by the
+// What bounds it.  1x16: the gathers (4096x11008 at 77 tokens, main kernel 44 us by the
 // profiler: 5.6 M gathers, 21 us at the 264 G/s of a kernel of nothing else; without gathers it
-// took 18 us less, without reloading dz 6; three chunks of codes, scales and dz in flight
+// took 18 us less, without reloading dz 6; three chunks of codes and dz in flight
 // changed nothing).  2x8: transposes, products and latencies; gated 4096x11008 at 64 tokens
-// 36.2 us.
+// 34.3 us.
 //
 // Against decoding the transposed weights first (decode_work.hip), us in a graph: 4x8 g16 4096^2
-// at 16 tokens 14.5 and 32.3, 4096x11008 at 128 61.8 and 76.5, at 256 104 and 85: to 128 tokens.
-// 2x8 to 256 and 1x16 to 128 tokens by the same measure.
+// at 16 tokens 14.2 and 29.5, 4096x11008 at 128 64.7 and 72.3, at 256 108 and 80: to 128 tokens.
+// 2x8 4096x11008 at 256 60 and 78, at 512 101 and 93, gated at 256 108 and 146, at 320 158 and 156: to 256.  1x16 at 128
+// 54 and 79, at 192 85 and 83: to 128.
 #include <algorithm>
 #include <type_traits>
 
@@ -443,8 +444,8 @@ int64_t skinny_back_partial_bytes(const GenericScheme& sc, int n, int64_t out, i
 
 // Where a wave of a full chip has few chunks: a launch saved is 1.5 to 3.5 us, while every chunk's
 // gradients, computed in each of the in / 128 groups, cost a 2x8 wave 0.5 to 1 us.  Gated, 8 tokens, us with
-// and without: 2x8 4096x2048 (2 chunks a wave) 14.1 and 16.4, 4096^2 gelu (4) 22.5 and 19.5; 1x16 4096^2 (4)
-// 30.5 and 33.2, 4096x6144 gelu (6) 42.7 and 41.4.
+// and without: 2x8 4096x2048 (2 chunks a wave) 12.7 and 14.5, 4096^2 (4) silu 16.7 and 17.0, gelu 20.9 and 17.7; 1x16
+// 4096^2 (4) 27.0 and 30.4, 4096x6144 (6) silu 39.5 and 41.1, gelu 43.1 and 41.5.
 bool skinny_back_grads(const GenericScheme& sc, int n, int64_t out, int64_t in, int64_t batch) {
     const int64_t chunks = (out + kBRows - 1) / kBRows * n * ((in / kGroup + kBGroups - 1) / kBGroups);
     return batch <= 16 && out % 8 == 0 && chunks <= (sc.B == 8 ? 2 : 4) * kSkinnyWorkgroups * back_waves(1);
