@@ -381,7 +381,7 @@ int aqlm_linear_gemv_lists_noalloc(const void* table, const void* entries, int64
  * rounded to fp16 once at most:
  *   - batch 1..16, 2x8 up to 512 tokens (gated: 384) and 4x8 g16 up to 320
  *     (gated: 256): not at all (codewords multiplied one by one; the general
- *     schemes decode in fp32);
+ *     schemes decode in fp32; layers of fewer than 64 weights: batch 1..16 only);
  *   - else the decoded weight that aqlm_linear_decode gives.
  * Backward, small batches (2x8 to 256 tokens, 1x16 and 4x8 g16 to 128) multiply
  * the codewords as they are, one by one, by dz times the row's scale.  Larger
