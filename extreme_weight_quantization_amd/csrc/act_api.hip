@@ -3,13 +3,13 @@
 //
 // Forward at batch 1..16 the codes are multiplied as they are decoded, in one launch; 2x8, 1x16
 // and 4x8 g16 at up to some hundreds of tokens likewise, with partial sums in the workspace
-// (skinny.hip), and so are their gradients (skinny_back.hip).  Otherwise the products run in passes: the weights decoded once into the workspace as fp16, then a
-// dense matrix-core product over them.  Forward, the decoded rows are padded to whole
+// (skinny.hip), and so are their gradients (skinny_back.hip).  Otherwise the products run in passes:
+// the weights decoded once into the workspace as fp16, then a dense matrix-core product over them.  Forward, the decoded rows are padded to whole
 // steps of 64 inputs; backward, they are written transposed (dx = dz W sums over the rows
 // of W).  With one codebook (M = 1) a codeword is exactly an fp16 weight: forward, the row
 // scale then goes into the fp32 epilogue and the weights are not rounded at all; backward,
-// it goes into dz, which is rounded to fp16 anyway.  With several codebooks a weight is the fp32 sum times
-// the scale, rounded once.
+// it goes into dz, which is rounded to fp16 anyway (where dz is dy as it is, it stays with the
+// weights).  With several codebooks a weight is the fp32 sum times the scale, rounded once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -12,8 +12,7 @@
 // 128), and no weight is ever written to memory.
 //
 //  * The row scale is in dz (act_grad.hip), which is rounded to fp16 anyway, and the codewords are
-//    multiplied as they are, one by one for 2x8 and 4x8 g16, so no weight is rounded (pairs of
-//    4x8 g16 added in fp16, as forward, are too coarse next to the rounding of dz).
+//    multiplied as they are, one by one for 2x8 and 4x8 g16, so no weight is rounded.
 //  * dz of a token comes in units of 2^(20 level), one level per 512 rows (act_math.h).  The sums of
 //    a token are kept at its highest level in the workgroup's rows (a lane has one token per column tile),
 //    blocks at a lower one are brought to it as they are used, and the sums leave in units of one.
