@@ -46,3 +46,9 @@ from .fused import (  # noqa: F401
     linear_act_backward_workspace_bytes,
     linear_act_workspace_bytes,
 )
+from .mx4 import (  # noqa: F401
+    aqlm_mx4_decode,
+    aqlm_mx4_linear,
+    aqlm_mx4_quantize,
+    mx4_linear_workspace_bytes,
+)

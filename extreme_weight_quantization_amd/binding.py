@@ -28,6 +28,7 @@ EXPORTED = ("aqlm_linear_gemv", "aqlm_linear_gemv_fused", "aqlm_linear_gemm", "a
             "aqlm_linear_act", "aqlm_linear_act_workspace_bytes", "aqlm_gated", "aqlm_gated_workspace_bytes",
             "aqlm_linear_act_backward", "aqlm_linear_act_backward_workspace_bytes", "aqlm_gated_backward",
             "aqlm_gated_backward_workspace_bytes", "aqlm_linear_act_lists", "aqlm_gated_lists",
+            "aqlm_mx4_quantize", "aqlm_mx4_decode", "aqlm_mx4_linear", "aqlm_mx4_linear_workspace_bytes",
             "aqlm_status_str", "aqlm_last_hip_error", "aqlm_version")
 FUSED_MAX_LAYERS = 8   # AQLM_FUSED_MAX_LAYERS
 
@@ -105,6 +106,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.aqlm_gated_lists.argtypes = [pp, pp, ctypes.POINTER(i64), pp, pp, vp, pp, pp, vp] + tail
         for name in ("aqlm_linear_act", "aqlm_gated", "aqlm_linear_act_backward", "aqlm_gated_backward",
                      "aqlm_linear_act_lists", "aqlm_gated_lists"):
+            getattr(lib, name).restype = ci
+        lib.aqlm_mx4_quantize.argtypes = lib.aqlm_mx4_decode.argtypes = [vp, vp, vp, i64, i64, vp]
+        lib.aqlm_mx4_linear_workspace_bytes.argtypes = [ci, i64, i64, i64, ctypes.POINTER(i64)]
+        lib.aqlm_mx4_linear.argtypes = [vp] * 8 + [i64, ci, i64, i64, i64, vp]
+        for name in ("aqlm_mx4_quantize", "aqlm_mx4_decode", "aqlm_mx4_linear_workspace_bytes", "aqlm_mx4_linear"):
             getattr(lib, name).restype = ci
         lib.aqlm_status_str.argtypes = [ci]
         lib.aqlm_status_str.restype = ctypes.c_char_p

@@ -1,0 +1,162 @@
+// A workgroup's part of a product of MX4 rows with up to 64 columns of activations: mx4_linear.hip describes the kernel
+// that it carries; the mixture-of-experts layer (moe_mx4.hip) runs it on experts.
+//
+// The workgroup walks tiles of 16 matrix-core rows (tile t, t + nwg, ...) in groups of kMxTiles.  Its 8 waves share the
+// inputs: wave w takes `nk` <= NK steps of 128 inputs out of every chunk of 8 nk, keeps their activations in registers
+// for all tiles of the group, and streams the codes of its steps, kMxTiles tiles ahead.  The waves' partial tiles are
+// added in LDS in the order of the waves.
+#pragma once
+#include "mx4.h"
+
+namespace aqlm {
+
+constexpr int kMxWaves = 8;
+constexpr int kMxThreads = kMxWaves * kWave;
+constexpr int kMxTiles = 4;       // tiles of a group: the codes of this many are in flight
+constexpr int kMxRows = 16;       // matrix-core rows of a tile
+
+// LDS floats of the partial tiles of a group, CT column tiles.
+constexpr int mx4_red_floats(int ct) { return kMxTiles * kMxWaves * ct * 256; }
+
+// How the inputs are dealt to the waves.
+struct MxSteps {
+    int nb;        // blocks of a row
+    int nk;        // steps a wave takes of a chunk
+    int chunks;
+};
+inline MxSteps mx4_steps(int64_t in, int nk_max) {
+    MxSteps s;
+    s.nb = (int)(in / kMxBlock);
+    const int steps = (s.nb + 3) / 4;
+    s.chunks = (steps + kMxWaves * nk_max - 1) / (kMxWaves * nk_max);
+    s.nk = (steps + kMxWaves * s.chunks - 1) / (kMxWaves * s.chunks);
+    return s;
+}
+
+// Activations of one lane: for column tile c the blocks of token row xrow[c].
+//   FMT kFmt6: split blocks (mx4.h), xq [..][nb][24] dwords, xs [..][nb] scale words
+//   FMT kFmt4: MX4, xq [..][nb][4] dwords, xs [..][nb] scale bytes
+template <int FMT>
+struct MxOperand {
+    static constexpr int kDwords = FMT == kFmt6 ? kSplitDwords : 4;
+    uint32_t q[kDwords];
+    uint32_t s;
+    __device__ __forceinline__ void load(const uint32_t* xq, const void* xs, size_t block, bool in_row) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(xq + block * kDwords);
+#pragma unroll
+        for (int i = 0; i < kDwords / 4; ++i) {
+            const u32x4 v = p[i];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) q[4 * i + t] = in_row ? v[t] : 0u;
+        }
+        const uint32_t sv = FMT == kFmt6 ? static_cast<const uint32_t*>(xs)[block] : static_cast<const uint8_t*>(xs)[block];
+        s = in_row ? sv : 0x7f7f7f7fu;
+    }
+    __device__ __forceinline__ f32x4 product(u32x4 a, uint32_t sa, f32x4 acc) const {
+        const i32x8 av = operand4(a);
+        if constexpr (FMT == kFmt4) {
+            return mfma_mx<kFmt4, 0>(av, operand4(u32x4{q[0], q[1], q[2], q[3]}), acc, sa, s);
+        } else {
+            auto piece = [&](int p) { return operand6(u32x6{q[6 * p], q[6 * p + 1], q[6 * p + 2], q[6 * p + 3], q[6 * p + 4], q[6 * p + 5]}); };
+            acc = mfma_mx<kFmt6, 3>(av, piece(3), acc, sa, s);   // small terms first
+            acc = mfma_mx<kFmt6, 2>(av, piece(2), acc, sa, s);
+            acc = mfma_mx<kFmt6, 1>(av, piece(1), acc, sa, s);
+            return mfma_mx<kFmt6, 0>(av, piece(0), acc, sa, s);
+        }
+    }
+};
+
+// row_of(tile): this lane's row of the tile inside wq / ws, which are the lane's own layer (clamped into it).
+// fin(tile, sum): called by all threads of the workgroup once per tile, after a barrier; sum(col, r) adds the waves'
+// partial products of matrix-core row r and column col.
+// With `grouped`, fin also gets the place of the tile in its group and is called for a whole group at once (fin_group).
+template <int CT, int NK, int FMT, class RowOf, class Fin>
+__device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws,
+                                         const uint32_t* xq, const void* xs, const int (&xrow)[CT], const MxSteps st,
+                                         const int bid, const int nwg, const int n_tiles, float* red, RowOf row_of,
+                                         Fin fin) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int q = lane >> 4;
+    const int nb = st.nb;
+
+    u32x4 cw[kMxTiles][NK];
+    uint32_t cs[kMxTiles][NK];
+    auto first = [&](int c) { return (c * kMxWaves + wave) * st.nk; };   // this wave's first step of chunk c
+    auto load_tile = [&](int i, int tile, int c) {
+        const size_t row = (size_t)row_of(min(tile, n_tiles - 1));
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            if (j < st.nk) {
+                const size_t at = row * nb + min(4 * (first(c) + j) + q, nb - 1);
+                cw[i][j] = load_nt16(wq + at * kMxBlockBytes);
+                cs[i][j] = ws[at];
+            }
+        }
+    };
+    MxOperand<FMT> x[CT][NK];
+    auto load_x = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            if (j < st.nk) {
+                const int b = 4 * (first(c) + j) + q;
+#pragma unroll
+                for (int t = 0; t < CT; ++t) x[t][j].load(xq, xs, (size_t)xrow[t] * nb + min(b, nb - 1), b < nb);
+            }
+        }
+    };
+
+#pragma unroll
+    for (int i = 0; i < kMxTiles; ++i)
+        if (bid + i * nwg < n_tiles) load_tile(i, bid + i * nwg, 0);
+    load_x(0);
+
+    for (int t0 = bid; t0 < n_tiles; t0 += nwg * kMxTiles) {
+        f32x4 acc[kMxTiles][CT];
+#pragma unroll
+        for (int i = 0; i < kMxTiles; ++i)
+#pragma unroll
+            for (int t = 0; t < CT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < st.chunks; ++c) {
+            const int cn = c + 1 < st.chunks ? c + 1 : 0;                      // what comes next
+            const int tn = cn != 0 ? t0 : t0 + nwg * kMxTiles;
+#pragma unroll
+            for (int i = 0; i < kMxTiles; ++i) {
+                if (t0 + i * nwg < n_tiles) {
+#pragma unroll
+                    for (int j = 0; j < NK; ++j) {
+                        if (j < st.nk) {
+                            // past the row: codes 0 with a scale of 1, whatever was loaded
+                            const bool in_row = 4 * (first(c) + j) + q < nb;
+                            u32x4 a = cw[i][j];
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) a[d] = in_row ? a[d] : 0u;
+                            const uint32_t sa = in_row ? cs[i][j] : 127u;
+#pragma unroll
+                            for (int t = 0; t < CT; ++t) acc[i][t] = x[t][j].product(a, sa, acc[i][t]);
+                        }
+                    }
+                    if (tn + i * nwg < n_tiles) load_tile(i, tn + i * nwg, cn);
+                }
+            }
+            if (st.chunks > 1) load_x(cn);
+        }
+#pragma unroll
+        for (int i = 0; i < kMxTiles; ++i)
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                pin(acc[i][t]);
+                *reinterpret_cast<f32x4*>(red + ((i * kMxWaves + wave) * CT + t) * 256 + (lane & 15) * kMxRows + 4 * q) = acc[i][t];
+            }
+        __syncthreads();
+        fin(t0, [&](int i, int col, int r) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kMxWaves; ++w) s += red[(i * kMxWaves + w) * CT * 256 + col * kMxRows + r];
+            return s;
+        });
+        __syncthreads();
+    }
+}
+
+}  // namespace aqlm

@@ -1,0 +1,139 @@
+// Products of MX4 weights: y = act(W x + bias) + residual.
+//
+// z[t][i] = sum over blocks b of 2^(s_ib - 127) sum_k q_ibk x[t][32 b + k].  The scaled matrix instruction takes the codes
+// and their scales as they lie in memory; x is in MX4 too, or in fp16 as four 6-bit pieces (mx4.h), so a weight costs no
+// vector instruction.
+//
+// Few tokens (mx4_rows_kernel): the codes are read once, 17/32 of a byte a weight, and that bounds the time.  Matrix-core
+// rows are output rows, columns are tokens; a workgroup keeps the activations of all inputs in the registers of its 8 waves
+// (100 bytes a block and token: 12 KB of a wave's 64 KB for each step of 128 inputs and 16 tokens) and streams the rows
+// past them (mx4_body.h).
+#include <algorithm>
+
+#include "act_math.h"
+#include "mx4_body.h"
+#include "mx4_launch.h"
+
+namespace aqlm {
+
+namespace {
+
+struct MxEpilogue {
+    const f16* bias;
+    const f16* residual;   // may be y
+    f16* y;
+    int act;
+};
+
+// Activations that are split inside the product: at most this many blocks of 32, 1.2 KB of LDS for every 12.  A launch
+// of its own for the split costs more from there down.
+constexpr int kInlineBlocks = 1024;
+
+template <int CT, int NK, int FMT, bool INLINE>
+__global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __restrict__ codes,
+                                                              const uint8_t* __restrict__ scales, const void* xq,
+                                                              const void* xs, MxSteps st, int out, int T, MxEpilogue e) {
+    extern __shared__ u32x4 smem[];
+    float* red = reinterpret_cast<float*>(smem);
+    const int lane = threadIdx.x & (kWave - 1);
+    const int col0 = (int)blockIdx.y * CT * 16, cols = min(T - col0, CT * 16);
+    int xrow[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t) xrow[t] = min(col0 + t * 16 + (lane & 15), T - 1);
+    const int n_tiles = (out + kMxRows - 1) / kMxRows;
+    const uint32_t* pieces = static_cast<const uint32_t*>(xq);
+    if constexpr (INLINE) {
+        uint32_t* lq = reinterpret_cast<uint32_t*>(red + mx4_red_floats(CT));
+        uint32_t* lsc = lq + (size_t)T * st.nb * kSplitDwords;
+        for (int b = threadIdx.x; b < T * st.nb; b += kMxThreads) {
+            uint32_t o[kSplitDwords], s;
+            split_block(load_block16(static_cast<const f16*>(xq) + (size_t)b * kMxBlock), o, s);
+            u32x4* to = reinterpret_cast<u32x4*>(lq + (size_t)b * kSplitDwords);
+#pragma unroll
+            for (int i = 0; i < kSplitDwords / 4; ++i) to[i] = u32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+            lsc[b] = s;
+        }
+        __syncthreads();
+        pieces = lq;
+        xs = lsc;
+    }
+    const int nwg = (int)gridDim.x;
+    mx4_body<CT, NK, FMT>(
+        codes, scales, pieces, xs, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
+        [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); },
+        [&](int t0, auto sum) {
+            for (int idx = threadIdx.x; idx < kMxTiles * cols * kMxRows; idx += kMxThreads) {
+                const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, col = ic % cols;
+                const int row = (t0 + i * nwg) * kMxRows + r;
+                if (t0 + i * nwg >= n_tiles || row >= out) continue;
+                float v[1] = {sum(i, col, r)};
+                if (e.bias != nullptr) v[0] += (float)e.bias[row];
+                act_values(e.act, v);
+                const size_t at = (size_t)(col0 + col) * out + row;
+                if (e.residual != nullptr) v[0] += (float)e.residual[at];
+                e.y[at] = (f16)v[0];
+            }
+        });
+}
+
+struct RowsCall {
+    const void *codes, *scales, *xq, *xs;
+    MxEpilogue e;
+    int64_t out, in;
+    int T;
+    hipStream_t stream;
+};
+
+template <int CT, int NK, int FMT, bool INLINE>
+hipError_t launch_rows_v(const RowsCall& c) {
+    auto kern = mx4_rows_kernel<CT, NK, FMT, INLINE>;
+    const MxSteps st = mx4_steps(c.in, NK);
+    const size_t lds = mx4_red_floats(CT) * sizeof(float) +
+                       (INLINE ? (size_t)c.T * st.nb * (kSplitBytes + kSplitScaleBytes) : 0);
+    if (lds > 65536) {
+        const hipError_t r = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (r != hipSuccess) return r;
+    }
+    const int tiles = (int)((c.out + kMxRows - 1) / kMxRows), groups = (c.T + CT * 16 - 1) / (CT * 16);
+    hipLaunchKernelGGL(kern, dim3(std::min(tiles, device_cu_count()), groups), dim3(kMxThreads), lds, c.stream,
+                       static_cast<const uint8_t*>(c.codes), static_cast<const uint8_t*>(c.scales), c.xq, c.xs, st,
+                       (int)c.out, c.T, c.e);
+    return hipGetLastError();
+}
+
+template <int FMT, bool INLINE>
+hipError_t launch_rows(const RowsCall& c) {
+    if constexpr (!INLINE) {
+        if (c.T > 32) return launch_rows_v<4, 1, FMT, INLINE>(c);
+        if (c.T > 16) return launch_rows_v<2, 2, FMT, INLINE>(c);
+    }
+    return launch_rows_v<1, 4, FMT, INLINE>(c);
+}
+
+bool split_inline(int64_t in, int64_t batch) { return batch <= 16 && batch * (in / kMxBlock) <= kInlineBlocks; }
+
+}  // namespace
+
+int64_t mx4_linear_workspace(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
+    if (x_mx4 || out == 0 || batch == 0 || split_inline(in, batch)) return 0;
+    return batch * (in / kMxBlock) * (kSplitBytes + kSplitScaleBytes);
+}
+
+hipError_t launch_mx4_linear(const void* codes, const void* scales, MxInput x, const Epilogue& e, void* workspace,
+                             int64_t out, int64_t in, int64_t batch, hipStream_t stream) {
+    RowsCall c = {codes, scales, x.x, x.scales,
+                  MxEpilogue{static_cast<const f16*>(e.bias[0]), static_cast<const f16*>(e.residual),
+                             static_cast<f16*>(e.y), e.act},
+                  out, in, (int)batch, stream};
+    if (x.scales != nullptr) return launch_rows<kFmt4, false>(c);
+    if (split_inline(in, batch)) return launch_rows<kFmt6, true>(c);
+    const int64_t blocks = batch * (in / kMxBlock);
+    char* xs = static_cast<char*>(workspace) + blocks * kSplitBytes;
+    const hipError_t r = launch_mx4_split(x.x, workspace, xs, blocks, stream);
+    if (r != hipSuccess) return r;
+    c.xq = workspace;
+    c.xs = xs;
+    return launch_rows<kFmt6, false>(c);
+}
+
+}  // namespace aqlm

@@ -445,6 +445,58 @@ int aqlm_gated_lists(const void* const* tables, const void* const* entries, cons
                      void* const* z, void* y, void* workspace, int64_t workspace_bytes, int act, int M, int B, int g,
                      int64_t out, int64_t in, int64_t batch, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * MX4: layers in microscaled 4-bit floating point (4.25 bits per weight), the
+ * format that the matrix cores multiply as it is stored.  For the layers that
+ * a 2-bit model keeps at more bits, and for products with 4-bit activations.
+ *
+ *   aqlm_mx4_quantize  fp16 rows [rows][in] to codes and scales
+ *   aqlm_mx4_decode    and back: W16 [rows][in]
+ *   aqlm_mx4_linear    y = act(W x + bias) + residual, x in fp16 or in MX4
+ *
+ * A row is cut into blocks of 32 consecutive values.  Value i of block b is
+ * q 2^(s[b] - 127): q, one of +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}, is a 4-bit float
+ * (sign, two exponent bits of bias 1, one mantissa bit), s the block's scale
+ * byte (255: the block is NaN).
+ *   codes   [rows][in / 2]   uint8, value 2i in the low half of byte i
+ *   scales  [rows][in / 32]  uint8
+ * in % 32 == 0, 32 <= in <= AQLM_MAX_IN.  codes, fp16 arrays: 16-byte aligned,
+ * bias 2-byte, scales at any address.
+ *
+ * Quantization: 2^(s - 127) = 2^(floor(log2 max |v|) - 2) over the block;
+ * v / 2^(s - 127) is rounded to nearest (ties to even) and is 6 at most.  A
+ * block of zeros has s = 0, one that holds an infinity or NaN s = 255 and
+ * codes 0.  Decoding rounds q 2^(s - 127) to fp16 once (nearest even, 0 and
+ * infinity where it leaves fp16's range); what aqlm_mx4_quantize wrote is
+ * decoded without rounding.  rows == 0 enqueues nothing.
+ *
+ * aqlm_mx4_linear: x_scales NULL: x is fp16 [batch][in]; else x holds MX4
+ * codes [batch][in / 2] and x_scales their scales [batch][in / 32].  bias [out]
+ * and residual [batch][out] fp16 may be NULL; residual may be y itself; no
+ * other arrays may overlap.  act is one of aqlm_act.  0 <= out <=
+ * AQLM_ACT_MAX_OUT, 0 <= batch <= AQLM_MX4_MAX_BATCH (else AQLM_ERR_SHAPE).
+ * out == 0 or batch == 0 enqueues nothing.  Workspace: as for the fused
+ * products above, of aqlm_mx4_linear_workspace_bytes bytes (x_mx4: whether x
+ * is in MX4); a larger batch never needs fewer.
+ *
+ * Numerics: no weight is rounded.  fp16 activations enter as a sum of four
+ * 6-bit floats a value, per block of 32: values down to 2^-8 of the block's
+ * largest exactly, smaller ones off by at most 2^-19 of it.  Products are
+ * accumulated in fp32; bias, activation and residual are applied in fp32 and y
+ * is rounded to fp16 once.  A block of x with an infinity or NaN makes its
+ * token's outputs NaN, a weight block of scale 255 its row's; non-finite bias and
+ * residual values reach the outputs that they take part in.  Results are
+ * deterministic.
+ */
+#define AQLM_MX4_MAX_BATCH (1 << 30)
+
+int aqlm_mx4_quantize(const void* w, void* codes, void* scales, int64_t rows, int64_t in, void* stream);
+int aqlm_mx4_decode(const void* codes, const void* scales, void* w, int64_t rows, int64_t in, void* stream);
+int aqlm_mx4_linear_workspace_bytes(int x_mx4, int64_t out, int64_t in, int64_t batch, int64_t* bytes);
+int aqlm_mx4_linear(const void* codes, const void* scales, const void* x, const void* x_scales, const void* bias,
+                    const void* residual, void* y, void* workspace, int64_t workspace_bytes, int act, int64_t out,
+                    int64_t in, int64_t batch, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* aqlm_status_str(int status);
 
