@@ -46,6 +46,15 @@ from .fused import (  # noqa: F401
     linear_act_backward_workspace_bytes,
     linear_act_workspace_bytes,
 )
+from .moe import (  # noqa: F401
+    SCORES,
+    aqlm_moe,
+    aqlm_moe_mx4,
+    aqlm_moe_route,
+    moe_mx4_workspace_bytes,
+    moe_route_workspace_bytes,
+    moe_workspace_bytes,
+)
 from .mx4 import (  # noqa: F401
     aqlm_mx4_decode,
     aqlm_mx4_linear,

@@ -29,6 +29,8 @@ EXPORTED = ("aqlm_linear_gemv", "aqlm_linear_gemv_fused", "aqlm_linear_gemm", "a
             "aqlm_linear_act_backward", "aqlm_linear_act_backward_workspace_bytes", "aqlm_gated_backward",
             "aqlm_gated_backward_workspace_bytes", "aqlm_linear_act_lists", "aqlm_gated_lists",
             "aqlm_mx4_quantize", "aqlm_mx4_decode", "aqlm_mx4_linear", "aqlm_mx4_linear_workspace_bytes",
+            "aqlm_moe_route", "aqlm_moe_route_workspace_bytes", "aqlm_moe", "aqlm_moe_workspace_bytes", "aqlm_moe_mx4",
+            "aqlm_moe_mx4_workspace_bytes",
             "aqlm_status_str", "aqlm_last_hip_error", "aqlm_version")
 FUSED_MAX_LAYERS = 8   # AQLM_FUSED_MAX_LAYERS
 
@@ -110,7 +112,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.aqlm_mx4_quantize.argtypes = lib.aqlm_mx4_decode.argtypes = [vp, vp, vp, i64, i64, vp]
         lib.aqlm_mx4_linear_workspace_bytes.argtypes = [ci, i64, i64, i64, ctypes.POINTER(i64)]
         lib.aqlm_mx4_linear.argtypes = [vp] * 8 + [i64, ci, i64, i64, i64, vp]
-        for name in ("aqlm_mx4_quantize", "aqlm_mx4_decode", "aqlm_mx4_linear_workspace_bytes", "aqlm_mx4_linear"):
+        moe = [ctypes.c_int64] * 5   # experts, in, inner, k, tokens
+        lib.aqlm_moe_route_workspace_bytes.argtypes = [i64] * 4 + [ctypes.POINTER(i64)]
+        lib.aqlm_moe_route.argtypes = [vp] * 6 + [i64, ci, ci, ctypes.c_float] + [i64] * 4 + [vp]
+        lib.aqlm_moe_workspace_bytes.argtypes = [ci, ci, ci, *moe, ctypes.POINTER(i64)]
+        lib.aqlm_moe.argtypes = [pp, pp, pp, vp, vp, vp, vp, vp, vp, i64, ci, ci, ci, ci, *moe, vp]
+        lib.aqlm_moe_mx4_workspace_bytes.argtypes = [*moe, ctypes.POINTER(i64)]
+        lib.aqlm_moe_mx4.argtypes = [pp, pp, vp, vp, vp, vp, vp, vp, i64, ci, *moe, vp]
+        for name in ("aqlm_mx4_quantize", "aqlm_mx4_decode", "aqlm_mx4_linear_workspace_bytes", "aqlm_mx4_linear",
+                     "aqlm_moe_route_workspace_bytes", "aqlm_moe_route", "aqlm_moe_workspace_bytes", "aqlm_moe",
+                     "aqlm_moe_mx4_workspace_bytes", "aqlm_moe_mx4"):
             getattr(lib, name).restype = ci
         lib.aqlm_status_str.argtypes = [ci]
         lib.aqlm_status_str.restype = ctypes.c_char_p

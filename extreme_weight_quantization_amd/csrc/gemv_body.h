@@ -22,7 +22,20 @@
 
 namespace aqlm {
 
-enum GemvKind : int { kGemvPlain = 0, kGemvAct = 1, kGemvGated = 2 };
+// KIND kGemvGatedAt, kGemvPartAt: an expert's products in a mixture-of-experts layer (moe.hip).  Column b of x is row
+//   rows.x[b], and results go to row rows.y[b] (GemvRows).  GatedAt writes act(zg) zu as the sum of two fp16 numbers, PartAt
+//   takes such pairs as columns 2b and 2b + 1 and writes their product, weighted, in fp32.
+enum GemvKind : int { kGemvPlain = 0, kGemvAct = 1, kGemvGated = 2, kGemvGatedAt = 3, kGemvPartAt = 4 };
+constexpr bool gemv_gated(int kind) { return kind == kGemvGated || kind == kGemvGatedAt; }
+constexpr bool gemv_at(int kind) { return kind == kGemvGatedAt || kind == kGemvPartAt; }
+
+// Rows of the kinds that gather; x, y and w are in LDS.
+struct GemvRows {
+    const uint16_t* x;   // rows of x of the columns
+    const uint16_t* y;   // rows of the result
+    const float* w;      // [columns / 2] weights (kGemvPartAt)
+    float* part;         // fp32 [..][out] (kGemvPartAt)
+};
 
 // What the kinds with an epilogue take next to the first layer's arguments (l = 1: the up
 // projection).  residual may be y: each element is read by the thread that then writes it.
@@ -57,6 +70,19 @@ __device__ __forceinline__ void gemv_finish(float p0, float p1, const f16* __res
         if (e.residual != nullptr) v += (float)e.residual[at];
     }
     y[at] = (f16)v;
+}
+
+// kGemvGatedAt: h = act(zg) zu of (row `at`, `row`) as the sum of two fp16 numbers, rows 2 at and 2 at + 1 of y.  One
+// rounding to fp16 would add its error to that of the layer's own result; the second number costs a column that the matrix cores
+// multiply anyway.
+__device__ __forceinline__ void gemv_finish_pair(float p0, float p1, const f16* __restrict__ scales, f16* y, int at, int row,
+                                                 int out, const GemvEpi& e) {
+    float va[1] = {p0 * (float)scales[row]};
+    act_values(e.act, va);
+    const float h = va[0] * (p1 * (float)e.scales1[row]);
+    const f16 hi = (f16)h;
+    y[(size_t)(2 * at) * out + row] = hi;
+    y[(size_t)(2 * at + 1) * out + row] = fabsf((float)hi) < __builtin_inff() ? (f16)(h - (float)hi) : (f16)0.f;
 }
 
 constexpr int kGemvWaves = 16;
@@ -179,7 +205,7 @@ __device__ __forceinline__ f32x4 chunk_mfma(const u32x4 cv, const u32x4* __restr
         // groups of the half h of a codeword, 4 codebooks x 4 replicas of 16 bytes (in the same
         // order in all lanes: 4-way conflicts, gated 4096x11008 at batch 1 31.4 us).
         const uint32_t lane = threadIdx.x & (kWave - 1);
-        const uint32_t rot = lane / (KIND == kGemvGated ? REPL / 2 : REPL) & 3u;
+        const uint32_t rot = lane / (gemv_gated(KIND) ? REPL / 2 : REPL) & 3u;
         uint32_t low[4];   // slot of the i-th codebook's piece 0, codeword 0
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) low[i] = ((rot + i) & 3u) * REPL + rrep;
@@ -234,8 +260,8 @@ __device__ __forceinline__ f32x4 chunk_mfma(const u32x4 cv, const u32x4* __restr
             // fp16 sum of the two codewords does not depend on the order of its operands.
             const uint32_t lane = threadIdx.x & (kWave - 1);
             // gated: bit 3 of the lane is the layer, whose replicas are 4 .. 7
-            const uint32_t mA = KIND == kGemvGated ? (lane >> 2) & 1u : (lane >> 3) & 1u;
-            const uint32_t r16 = (KIND == kGemvGated ? (lane & 3u) + 4u * ((lane >> 3) & 1u) : lane & 7u) * 16u;
+            const uint32_t mA = gemv_gated(KIND) ? (lane >> 2) & 1u : (lane >> 3) & 1u;
+            const uint32_t r16 = (gemv_gated(KIND) ? (lane & 3u) + 4u * ((lane >> 3) & 1u) : lane & 7u) * 16u;
             const uint32_t base = (r16 + 128u * mA) | ((r16 + 128u * (mA ^ 1u)) << 8);
             const char* cbb = reinterpret_cast<const char*>(cb_lds);
             f16x8 c1[4];
@@ -291,8 +317,8 @@ template <int SCHEME, int REPL, bool VEC, int RTP, int XM, int KIND = kGemvPlain
 __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, const f16* __restrict__ codebooks0,
                                           const f16* __restrict__ scales, f16* y, const int out,
                                           const int bid, const int nwg, const f16* __restrict__ x, int in, int T,
-                                          const GemvEpi epi = {}) {
-    constexpr bool GATED = KIND == kGemvGated;
+                                          const GemvEpi epi = {}, const GemvRows rows = {}) {
+    constexpr bool GATED = gemv_gated(KIND), AT = gemv_at(KIND);
     constexpr int kTileRows = GATED ? kRowTile / 2 : kRowTile;   // output rows of a tile
     constexpr bool XS = XM == kXStaged8 || XM == kXStaged16 || XM == kXStaged16in8;
     constexpr int kStage = kXStageSlots(XM);    // 16-byte slots of one wave's x stage
@@ -339,7 +365,7 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
         for (int q = 0; q < 8; ++q) {
             const int grp = s * kSlabGroups + slab_group(kq, q);
             bx[q] = (lrow < T && grp < G)
-                        ? as_f16x8(load16(x + (size_t)lrow * in + (size_t)grp * kGroup))
+                        ? as_f16x8(load16(x + (size_t)(AT ? (int)rows.x[lrow] : lrow) * in + (size_t)grp * kGroup))
                         : f16x8{};
         }
     };
@@ -365,8 +391,9 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
             if (r0 + 2 * i >= T) break;   // rows past the batch only feed discarded columns
             const int b = 2 * i + (l >> 5);
             const int grp = min(s * kSlabGroups + ((l & 31) ^ b), G - 1);
+            const int row = AT ? (int)rows.x[min(r0 + b, T - 1)] : min(r0 + b, T - 1);
             __builtin_amdgcn_global_load_lds(
-                (const void*)(x + (size_t)min(r0 + b, T - 1) * in + (size_t)grp * kGroup),
+                (const void*)(x + (size_t)row * in + (size_t)grp * kGroup),
                 lds_ptr(xst + 64 * i), 16, 0, 0);
         }
     };
@@ -533,7 +560,15 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
             if (tid < kTileRows * 16) {
                 const int b = tid / kTileRows, rr = tid % kTileRows;
                 const int row = rt * kTileRows + rr;
-                if (b < T && row < out) {
+                if constexpr (KIND == kGemvPartAt) {
+                    if (2 * b < T && row < out) {   // T is even
+                        float sum = 0.f;
+#pragma unroll
+                        for (int w = 0; w < kGemvWaves; ++w)
+                            sum += red[w * kRedStride + rr * kRedRow + 2 * b] + red[w * kRedStride + rr * kRedRow + 2 * b + 1];
+                        rows.part[(size_t)rows.y[b] * out + row] = sum * (float)scales[row] * rows.w[b];
+                    }
+                } else if (b < T && row < out) {
                     float sum = 0.f;
 #pragma unroll
                     for (int w = 0; w < kGemvWaves; ++w) sum += red[w * kRedStride + rr * kRedRow + b];
@@ -545,7 +580,8 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
 #pragma unroll
                             for (int w = 0; w < kGemvWaves; ++w) sum1 += red[w * kRedStride + (8 + rr) * kRedRow + b];
                         }
-                        gemv_finish<KIND>(sum, sum1, scales, y, b, row, out, epi);
+                        if constexpr (AT) gemv_finish_pair(sum, sum1, scales, y, rows.y[b], row, out, epi);
+                        else gemv_finish<KIND>(sum, sum1, scales, y, b, row, out, epi);
                     }
                 }
             }

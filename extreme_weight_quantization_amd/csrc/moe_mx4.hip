@@ -1,0 +1,152 @@
+// A mixture-of-experts layer for few tokens, experts in MX4: as moe.hip, with the products of mx4_body.h.
+//
+// A tile of 16 matrix-core rows is 8 rows of gate and the same 8 of up (lanes with l % 16 < 8: gate), so that one
+// workgroup has both halves of h = act(zg) zu; four neighbouring tiles are one block of 32 hidden values, which goes
+// to the down product in the four-piece form of mx4.h, from fp32: it is rounded by 2^-19 of the block's largest only.
+#include <algorithm>
+
+#include "act_math.h"
+#include "moe_plan.h"
+#include "mx4_body.h"
+#include "mx4_launch.h"
+
+namespace aqlm {
+
+namespace {
+
+constexpr int kMxMoeNk = 4, kCols = 16, kHalf = kMxRows / 2;
+
+struct MoeMxProduct {
+    const uint8_t* codes[2];
+    const uint8_t* scales[2];
+    const uint32_t* xq;      // split rows of the input and their scale words
+    const uint32_t* xs;
+    uint32_t* hq;            // gate and up: [pairs][rows / 32] split blocks
+    uint32_t* hs;
+    float* part;             // down: [pairs][rows]
+    const int32_t* ids;
+    const float* weights;
+    MxSteps st;
+    int experts, pairs, k, rows, act;
+    float fixed;
+};
+
+template <bool GATED>
+__global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
+    __shared__ MoeLds m;
+    __shared__ float red[mx4_red_floats(1)];
+    __shared__ float hb[kCols][kMxBlock + 1];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int n = moe_items<kCols>(p.ids, p.pairs, p.experts, m);
+    const int tiles = GATED ? (p.rows + kHalf - 1) / kHalf : (p.rows + kMxRows - 1) / kMxRows;
+    const int parts = moe_parts(n, (int)gridDim.x, GATED ? (tiles + kMxTiles - 1) / kMxTiles : tiles, p.fixed);
+    for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
+        const int cols = moe_item<kCols, false>(u / parts, p.k, p.weights, m);
+        const size_t row0 = (size_t)p.rows * __builtin_amdgcn_readfirstlane(m.expert) * p.st.nb;   // the expert's first block
+        const int r16 = lane & 15, layer = GATED && r16 >= kHalf;
+        const uint8_t* wq = (layer ? p.codes[1] : p.codes[0]) + row0 * kMxBlockBytes;
+        const uint8_t* ws = (layer ? p.scales[1] : p.scales[0]) + row0;
+        const int col = min(r16, cols - 1);
+        const int xrow[1] = {GATED ? (int)m.x[col] : (int)m.y[col]};
+        const int part = u % parts;
+        mx4_body<1, kMxMoeNk, kFmt6, GATED>(
+            wq, ws, p.xq, p.xs, xrow, p.st, part, parts, tiles, red,
+            [&](int tile) { return min(GATED ? tile * kHalf + (r16 & (kHalf - 1)) : tile * kMxRows + r16, p.rows - 1); },
+            [&](int t0, auto sum) {
+                if constexpr (GATED) {
+                    for (int idx = tid; idx < cols * kMxBlock; idx += kMxThreads) {   // rows is a multiple of 32: whole blocks
+                        const int c = idx / kMxBlock, i = idx % kMxBlock;
+                        float v[1] = {sum(i / kHalf, c, i % kHalf)};
+                        act_values(p.act, v);
+                        hb[c][i] = v[0] * sum(i / kHalf, c, i % kHalf + kHalf);
+                    }
+                    __syncthreads();
+                    if (tid < cols) {
+                        f32x16 even, odd;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            even[i] = hb[tid][2 * i];
+                            odd[i] = hb[tid][2 * i + 1];
+                        }
+                        uint32_t o[kSplitDwords], s;
+                        split_block32(even, odd, o, s);
+                        const size_t b = (size_t)m.y[tid] * (p.rows / kMxBlock) + t0 / kMxTiles;
+                        store_split(p.hq + b * kSplitDwords, o);
+                        p.hs[b] = s;
+                    }
+                } else {
+                    for (int idx = tid; idx < kMxTiles * cols * kMxRows; idx += kMxThreads) {
+                        const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, c = ic % cols;
+                        const int tile = t0 + i * parts, row = tile * kMxRows + r;
+                        if (tile < tiles && row < p.rows)
+                            p.part[(size_t)m.y[c] * p.rows + row] = sum(i, c, r) * m.w[c];
+                    }
+                }
+            });
+    }
+}
+
+int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
+int64_t split_bytes(int64_t rows, int64_t in) { return round256(rows * (in / kMxBlock) * kSplitBytes); }
+int64_t split_scale_bytes(int64_t rows, int64_t in) { return round256(rows * (in / kMxBlock) * kSplitScaleBytes); }
+
+// As moe.hip's, with 17/32 of a byte a weight and 1 us.
+float start_cost(int layers, int64_t rows, int64_t in) {
+    return 1.f / ((float)layers * (float)rows * (float)in * 0.53f / 20e3f);
+}
+
+}  // namespace
+
+int64_t moe_mx4_workspace(int64_t in, int64_t inner, int64_t tokens, int64_t k) {
+    const int64_t pairs = tokens * k;
+    return split_bytes(tokens, in) + split_scale_bytes(tokens, in) + split_bytes(pairs, inner) + split_scale_bytes(pairs, inner) +
+           round256(pairs * in * 4);
+}
+
+hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspace, hipStream_t stream) {
+    char* at = static_cast<char*>(workspace);
+    auto take = [&](int64_t bytes) {
+        char* p = at;
+        at += bytes;
+        return p;
+    };
+    uint32_t* xq = reinterpret_cast<uint32_t*>(take(split_bytes(c.tokens, c.in)));
+    uint32_t* xs = reinterpret_cast<uint32_t*>(take(split_scale_bytes(c.tokens, c.in)));
+    MoeMxProduct p = {};
+    p.hq = reinterpret_cast<uint32_t*>(take(split_bytes(c.pairs(), c.inner)));
+    p.hs = reinterpret_cast<uint32_t*>(take(split_scale_bytes(c.pairs(), c.inner)));
+    p.part = reinterpret_cast<float*>(at);
+    hipError_t r = launch_mx4_split(c.x, xq, xs, c.tokens * (c.in / kMxBlock), stream);
+    if (r != hipSuccess) return r;
+    for (int l = 0; l < 2; ++l) {
+        p.codes[l] = static_cast<const uint8_t*>(L.codes[l]);
+        p.scales[l] = static_cast<const uint8_t*>(L.scales[l]);
+    }
+    p.xq = xq;
+    p.xs = xs;
+    p.ids = c.ids;
+    p.weights = c.weights;
+    p.st = mx4_steps(c.in, kMxMoeNk);
+    p.experts = c.experts;
+    p.pairs = c.pairs();
+    p.k = c.k;
+    p.rows = (int)c.inner;
+    p.act = c.act;
+    p.fixed = start_cost(2, c.inner, c.in);
+    hipLaunchKernelGGL(moe_mx4_kernel<true>, dim3(device_cu_count()), dim3(kMxThreads), 0, stream, p);
+    r = hipGetLastError();
+    if (r != hipSuccess) return r;
+    p.codes[0] = static_cast<const uint8_t*>(L.codes[2]);
+    p.scales[0] = static_cast<const uint8_t*>(L.scales[2]);
+    p.xq = p.hq;
+    p.xs = p.hs;
+    p.st = mx4_steps(c.inner, kMxMoeNk);
+    p.rows = (int)c.in;
+    p.fixed = start_cost(1, c.inner, c.in);
+    hipLaunchKernelGGL(moe_mx4_kernel<false>, dim3(device_cu_count()), dim3(kMxThreads), 0, stream, p);
+    r = hipGetLastError();
+    if (r != hipSuccess) return r;
+    return launch_moe_combine(p.part, c, stream);
+}
+
+}  // namespace aqlm

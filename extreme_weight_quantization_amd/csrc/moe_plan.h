@@ -1,0 +1,138 @@
+// How a mixture-of-experts launch finds its work (device helpers).
+//
+// Which experts are asked for, and by whom, is known on the device only.  Every workgroup sorts the layer's pairs (token,
+// choice) by expert in its LDS: at most 1024 of them, below a microsecond, where a launch of its own would take
+// two.  Up to CHUNK pairs of one expert are an item: its weights are read once for them.  Items are cut
+// into `parts` so that parts x items fill the launch's workgroups evenly.
+#pragma once
+#include "aqlm_device.h"
+#include "moe_launch.h"
+
+namespace aqlm {
+
+constexpr uint32_t kMoeNone = 0xffff;   // an id that is no expert
+constexpr int kMoeIdBits = 9;
+static_assert(kMoeMaxExperts <= 1 << kMoeIdBits, "bits of an id");
+
+struct MoeLds {
+    int count[kMoeMaxExperts];
+    int start[kMoeMaxExperts + 1];   // first place of an expert in pair[]
+    int item0[kMoeMaxExperts + 1];   // first item of an expert
+    uint16_t id[kMoeMaxPairs];       // the expert of a pair, or kMoeNone
+    uint16_t rank[kMoeMaxPairs];     // place of a pair among its expert's
+    uint16_t pair[kMoeMaxPairs];     // pairs by expert
+    int expert;                      // of the item at hand
+    uint16_t x[16], y[16];           // its columns: rows of the input, pairs
+    float w[16];                     // weights of the pairs
+};
+
+// Sorts the pairs; the number of items.  All threads of the workgroup (at least 512) call it.  A pair whose id is no
+// expert is left out.  An expert's pairs stay in their order: workgroups that take parts of one item must agree on its pairs.
+template <int CHUNK>
+__device__ __forceinline__ int moe_items(const int32_t* __restrict__ ids, int pairs, int experts, MoeLds& m) {
+    const int tid = threadIdx.x, n = blockDim.x;
+    if (tid < kMoeMaxExperts) m.count[tid] = 0;
+    for (int p = tid; p < pairs; p += n) {
+        const int e = ids[p];
+        m.id[p] = (uint16_t)(e >= 0 && e < experts ? e : kMoeNone);
+    }
+    __syncthreads();
+    if (tid < kWave) {
+        // One wave ranks 64 pairs after another: the lanes of equal ids by a vote on each bit of them.
+        for (int p0 = 0; p0 < pairs; p0 += kWave) {
+            const int p = p0 + tid;
+            const uint32_t e = p < pairs ? m.id[p] : kMoeNone;
+            uint64_t same = __ballot(e != kMoeNone);
+#pragma unroll
+            for (int b = 0; b < kMoeIdBits; ++b) {
+                const uint64_t set = __ballot((e >> b) & 1u);
+                same &= (e >> b) & 1u ? set : ~set;
+            }
+            if (e != kMoeNone) {
+                const int before = m.count[e];
+                m.rank[p] = (uint16_t)(before + __popcll(same & ((1ull << tid) - 1ull)));
+                if ((same >> tid) == 1ull) m.count[e] = before + __popcll(same);   // the last of them
+            }
+        }
+        constexpr int kPer = kMoeMaxExperts / kWave;
+        int c[kPer], sum = 0, items = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            c[i] = m.count[tid * kPer + i];
+            sum += c[i];
+            items += (c[i] + CHUNK - 1) / CHUNK;
+        }
+        int s = sum, t = items;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int so = __shfl_up(s, o, kWave), to = __shfl_up(t, o, kWave);
+            s += tid >= o ? so : 0;
+            t += tid >= o ? to : 0;
+        }
+        if (tid == kWave - 1) {
+            m.start[kMoeMaxExperts] = s;
+            m.item0[kMoeMaxExperts] = t;
+        }
+        s -= sum;
+        t -= items;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            m.start[tid * kPer + i] = s;
+            m.item0[tid * kPer + i] = t;
+            s += c[i];
+            t += (c[i] + CHUNK - 1) / CHUNK;
+        }
+    }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += n) {
+        const uint32_t e = m.id[p];
+        if (e != kMoeNone) m.pair[m.start[e] + m.rank[p]] = (uint16_t)p;
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(m.item0[kMoeMaxExperts]);
+}
+
+// Parts an item is cut into: `rounds` rounds of `wgs` workgroups take n * parts <= rounds * wgs units, each 1 / parts of an
+// item and the fixed cost `fixed` (in items) of starting on one.
+__device__ __forceinline__ int moe_parts(int n, int wgs, int most, float fixed) {
+    int best = 1;
+    float cost = (float)((n + wgs - 1) / wgs) * (1.f + fixed);
+    for (int r = 1; r <= 4; ++r) {
+        const int p = min(r * wgs / max(n, 1), most);
+        if (p < 1) continue;
+        const float c = (float)((n * p + wgs - 1) / wgs) * (1.f / (float)p + fixed);
+        if (c < cost) {
+            cost = c;
+            best = p;
+        }
+    }
+    return best;
+}
+
+// Makes item v the one at hand: m.expert, and m.x (rows of the input), m.y (pairs), m.w (weights) for its pairs; returns how many there are.  PAIRED: the
+// input has two rows for a pair (2 pair, 2 pair + 1), else one for its token.  Ends with a barrier.
+template <int CHUNK, bool PAIRED>
+__device__ __forceinline__ int moe_item(int v, int k, const float* __restrict__ weights, MoeLds& m) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid < kMoeMaxExperts && m.item0[tid] <= v && v < m.item0[tid + 1]) m.expert = tid;
+    __syncthreads();
+    const int e = __builtin_amdgcn_readfirstlane(m.expert);
+    const int at = m.start[e] + (v - m.item0[e]) * CHUNK;
+    const int n = min(CHUNK, m.start[e + 1] - at);
+    if (tid < n) {
+        const int p = m.pair[at + tid];
+        m.y[tid] = (uint16_t)p;
+        m.w[tid] = weights[p];
+        if constexpr (PAIRED) {
+            m.x[2 * tid] = (uint16_t)(2 * p);
+            m.x[2 * tid + 1] = (uint16_t)(2 * p + 1);
+        } else {
+            m.x[tid] = (uint16_t)(p / k);
+        }
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+}  // namespace aqlm

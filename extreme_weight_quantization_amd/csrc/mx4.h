@@ -106,4 +106,41 @@ __device__ __forceinline__ void split_block(f16x32 v, uint32_t (&out)[kSplitDwor
     }
 }
 
+// The same for the fp32 values 2i (even[i]) and 2i + 1 (odd[i]) of a block, for results that go on into another product.  Below 2^-110 a block counts as zero, from 2^126 on
+// as infinite.
+__device__ __forceinline__ void split_block32(f32x16 even, f32x16 odd, uint32_t (&out)[kSplitDwords], uint32_t& scales) {
+    uint32_t top = 0;   // magnitudes order as their bits do
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float a = even[i], b = odd[i];
+        top = max(top, max(__builtin_bit_cast(uint32_t, a) & 0x7fffffffu, __builtin_bit_cast(uint32_t, b) & 0x7fffffffu));
+    }
+    int e = (int)(top >> 23) - 127;
+    const bool none = e < -110, bad = e >= 126;
+    if (none || bad) e = 0;
+    scales = 0;
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+        const float unit = pow2(e - 1 - 5 * p);
+        const u32x6 c = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, unit);
+        if (p + 1 < kPieces) {
+            const auto back = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(c, unit);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {   // exact
+                even[i] -= back[2 * i];
+                odd[i] -= back[2 * i + 1];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPieceDwords; ++i) out[p * kPieceDwords + i] = none || bad ? 0u : c[i];
+        scales |= (bad ? kScaleNaN : (uint32_t)(127 + e - 1 - 5 * p)) << (8 * p);
+    }
+}
+
+__device__ __forceinline__ void store_split(uint32_t* to, const uint32_t (&o)[kSplitDwords]) {   // 16-byte aligned
+#pragma unroll
+    for (int i = 0; i < kSplitDwords / 4; ++i)
+        reinterpret_cast<u32x4*>(to)[i] = u32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+}
+
 }  // namespace aqlm

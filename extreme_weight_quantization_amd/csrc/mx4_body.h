@@ -1,7 +1,8 @@
 // A workgroup's part of a product of MX4 rows with up to 64 columns of activations: mx4_linear.hip describes the kernel
 // that it carries; the mixture-of-experts layer (moe_mx4.hip) runs it on experts.
 //
-// The workgroup walks tiles of 16 matrix-core rows (tile t, t + nwg, ...) in groups of kMxTiles.  Its 8 waves share the
+// The workgroup walks tiles of 16 matrix-core rows in groups of kMxTiles: tiles bid + i nwg, or, RUN, 4 neighbours
+// each (kMxTiles (bid + i nwg) + 0 .. 3).  Its 8 waves share the
 // inputs: wave w takes `nk` <= NK steps of 128 inputs out of every chunk of 8 nk, keeps their activations in registers
 // for all tiles of the group, and streams the codes of its steps, kMxTiles tiles ahead.  The waves' partial tiles are
 // added in LDS in the order of the waves.
@@ -67,10 +68,9 @@ struct MxOperand {
 };
 
 // row_of(tile): this lane's row of the tile inside wq / ws, which are the lane's own layer (clamped into it).
-// fin(tile, sum): called by all threads of the workgroup once per tile, after a barrier; sum(col, r) adds the waves'
-// partial products of matrix-core row r and column col.
-// With `grouped`, fin also gets the place of the tile in its group and is called for a whole group at once (fin_group).
-template <int CT, int NK, int FMT, class RowOf, class Fin>
+// fin(t0, sum): called by all threads of the workgroup once per group, after a barrier: tiles t0 + i step, step 1 with RUN, else
+// nwg; sum(i, col, r) adds the waves' partial products of matrix-core row r and column col of the i-th.
+template <int CT, int NK, int FMT, bool RUN, class RowOf, class Fin>
 __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws,
                                          const uint32_t* xq, const void* xs, const int (&xrow)[CT], const MxSteps st,
                                          const int bid, const int nwg, const int n_tiles, float* red, RowOf row_of,
@@ -106,12 +106,13 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
         }
     };
 
+    const int step = RUN ? 1 : nwg, begin = RUN ? bid * kMxTiles : bid;
 #pragma unroll
     for (int i = 0; i < kMxTiles; ++i)
-        if (bid + i * nwg < n_tiles) load_tile(i, bid + i * nwg, 0);
+        if (begin + i * step < n_tiles) load_tile(i, begin + i * step, 0);
     load_x(0);
 
-    for (int t0 = bid; t0 < n_tiles; t0 += nwg * kMxTiles) {
+    for (int t0 = begin; t0 < n_tiles; t0 += nwg * kMxTiles) {
         f32x4 acc[kMxTiles][CT];
 #pragma unroll
         for (int i = 0; i < kMxTiles; ++i)
@@ -122,7 +123,7 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
             const int tn = cn != 0 ? t0 : t0 + nwg * kMxTiles;
 #pragma unroll
             for (int i = 0; i < kMxTiles; ++i) {
-                if (t0 + i * nwg < n_tiles) {
+                if (t0 + i * step < n_tiles) {
 #pragma unroll
                     for (int j = 0; j < NK; ++j) {
                         if (j < st.nk) {
@@ -136,7 +137,7 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
                             for (int t = 0; t < CT; ++t) acc[i][t] = x[t][j].product(a, sa, acc[i][t]);
                         }
                     }
-                    if (tn + i * nwg < n_tiles) load_tile(i, tn + i * nwg, cn);
+                    if (tn + i * step < n_tiles) load_tile(i, tn + i * step, cn);
                 }
             }
             if (st.chunks > 1) load_x(cn);

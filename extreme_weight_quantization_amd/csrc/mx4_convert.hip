@@ -72,9 +72,7 @@ __global__ __launch_bounds__(kThreads) void mx4_split_kernel(const f16* __restri
     for (int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x; b < blocks; b += (int64_t)gridDim.x * kThreads) {
         uint32_t out[kSplitDwords], s;
         split_block(load_block16(x + b * kMxBlock), out, s);
-        u32x4* to = reinterpret_cast<u32x4*>(pieces + b * kSplitDwords);
-#pragma unroll
-        for (int i = 0; i < kSplitDwords / 4; ++i) to[i] = u32x4{out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]};
+        store_split(pieces + b * kSplitDwords, out);
         scales[b] = s;
     }
 }

@@ -48,9 +48,7 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
         for (int b = threadIdx.x; b < T * st.nb; b += kMxThreads) {
             uint32_t o[kSplitDwords], s;
             split_block(load_block16(static_cast<const f16*>(xq) + (size_t)b * kMxBlock), o, s);
-            u32x4* to = reinterpret_cast<u32x4*>(lq + (size_t)b * kSplitDwords);
-#pragma unroll
-            for (int i = 0; i < kSplitDwords / 4; ++i) to[i] = u32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+            store_split(lq + (size_t)b * kSplitDwords, o);
             lsc[b] = s;
         }
         __syncthreads();
@@ -58,7 +56,7 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
         xs = lsc;
     }
     const int nwg = (int)gridDim.x;
-    mx4_body<CT, NK, FMT>(
+    mx4_body<CT, NK, FMT, false>(
         codes, scales, pieces, xs, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
         [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); },
         [&](int t0, auto sum) {

@@ -497,6 +497,78 @@ int aqlm_mx4_linear(const void* codes, const void* scales, const void* x, const 
                     const void* residual, void* y, void* workspace, int64_t workspace_bytes, int act, int64_t out,
                     int64_t in, int64_t batch, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Mixture of experts, for serving: the router, and a whole layer for few
+ * tokens.
+ *
+ *   aqlm_moe_route    l = x R^T;  scores, the k experts of every token and
+ *                     their weights
+ *   aqlm_moe          y_t = residual_t
+ *   aqlm_moe_mx4            + sum_{j<k} w_tj Wd_e (act(Wg_e x_t) * (Wu_e x_t)),
+ *                     e = ids_tj
+ *
+ * aqlm_moe_route: x [tokens][in], router R [experts][in] fp16; ids
+ * [tokens][k] int32 and weights [tokens][k] fp32 are written, best expert
+ * first.  Scores: softmax of a token's logits, or 1 / (1 + exp(-l)) of each.
+ * The experts are those of the k largest scores, plus bias [experts] (fp32,
+ * or NULL) where it is given; equal ones: the lowest index first.  weights are
+ * the scores without the bias, divided by their sum over the k when renorm is
+ * not 0, times scale.  in % 8 == 0, k <= experts, 0 <= tokens <=
+ * AQLM_ROUTE_MAX_TOKENS.  Logits and scores are computed in 64 bits, so the
+ * choice does not depend on the batch.  A NaN score ranks below all others; a
+ * token with a NaN logit has NaN weights under softmax.
+ *
+ * aqlm_moe: the experts' layers in one AQLM scheme, three host arrays of three
+ * entries (gate, up, down), each stacked over the experts: codes
+ * [experts][rows][n/g][M], codebooks [experts][M][2^B][g], scales
+ * [experts][rows], for gate and up rows = inner, n = in, for down rows = in,
+ * n = inner.  aqlm_moe_mx4: the same in MX4, codes [experts][rows][n / 2],
+ * scales [experts][rows][n / 32].  x, y, residual [tokens][in] fp16 (residual
+ * may be NULL, or y itself; no other arrays may overlap), ids, weights as
+ * aqlm_moe_route writes them.  A token may name an expert twice, and an id
+ * that is no expert (-1, say) adds nothing.  in and inner are multiples of g
+ * (MX4: 32), 0 <= tokens, tokens * k <= AQLM_MOE_MAX_PAIRS.  Larger batches:
+ * sort the tokens by expert and use the products above.
+ *
+ * Codes, codebooks, x, y, residual and workspace need 16-byte alignment, AQLM
+ * scales 2, ids, weights and bias 4, MX4 scales none.  Workspaces as for the
+ * fused products above.
+ *
+ * Numerics: aqlm_moe multiplies every codeword on its own (no weight is
+ * rounded), aqlm_moe_mx4 as aqlm_mx4_linear.  The hidden vector
+ * act(.) * (.) is kept to 2^-22 of each element or 2^-25, whichever is larger
+ * (infinite beyond fp16's range), for aqlm_moe_mx4 to 2^-19 of the largest in
+ * its block of 32.  Sums are fp32, over a token's choices in their order; y is rounded to fp16
+ * once.  Results are deterministic.
+ */
+#define AQLM_MOE_MAX_EXPERTS 512
+#define AQLM_MOE_MAX_K 16
+#define AQLM_MOE_MAX_PAIRS 1024
+#define AQLM_ROUTE_MAX_TOKENS (1 << 24)
+
+typedef enum {
+    AQLM_SCORE_SOFTMAX = 0,
+    AQLM_SCORE_SIGMOID = 1
+} aqlm_score;
+
+int aqlm_moe_route_workspace_bytes(int64_t experts, int64_t in, int64_t k, int64_t tokens, int64_t* bytes);
+/* score: one of aqlm_score (else AQLM_ERR_ACT). */
+int aqlm_moe_route(const void* x, const void* router, const float* bias, int32_t* ids, float* weights, void* workspace,
+                   int64_t workspace_bytes, int score, int renorm, float scale, int64_t experts, int64_t in, int64_t k,
+                   int64_t tokens, void* stream);
+
+int aqlm_moe_workspace_bytes(int M, int B, int g, int64_t experts, int64_t in, int64_t inner, int64_t k, int64_t tokens,
+                             int64_t* bytes);
+int aqlm_moe(const void* const* codes, const void* const* codebooks, const void* const* scales, const void* x,
+             const int32_t* ids, const float* weights, const void* residual, void* y, void* workspace,
+             int64_t workspace_bytes, int act, int M, int B, int g, int64_t experts, int64_t in, int64_t inner, int64_t k,
+             int64_t tokens, void* stream);
+
+int aqlm_moe_mx4_workspace_bytes(int64_t experts, int64_t in, int64_t inner, int64_t k, int64_t tokens, int64_t* bytes);
+int aqlm_moe_mx4(const void* const* codes, const void* const* scales, const void* x, const int32_t* ids,
+                 const float* weights, const void* residual, void* y, void* workspace, int64_t workspace_bytes, int act,
+                 int64_t experts, int64_t in, int64_t inner, int64_t k, int64_t tokens, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* aqlm_status_str(int status);
 
