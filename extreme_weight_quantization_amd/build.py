@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libaqlm.so")
 OBJ_DIR = os.path.join(os.path.dirname(PKG_DIR), "_build")
 SOURCES = ["aqlm_api.hip", "decode.hip", "gemv.hip", "gemm.hip", "gemm_pipe.hip", "generic.hip", "encode.hip",
            "gemv_lists.hip", "gemm_dense.hip", "gemv_stream.hip", "act_api.hip", "gemv_act.hip", "skinny.hip", "skinny_back.hip", "decode_work.hip", "act_grad.hip",
-           "mx4_api.hip", "mx4_convert.hip", "mx4_linear.hip",
+           "mx4_api.hip", "mx4_convert.hip", "mx4_linear.hip", "mx4_gemm.hip",
            "moe_api.hip", "moe_route.hip", "moe.hip", "moe_mx4.hip"]
 ARCH = "gfx950"
 

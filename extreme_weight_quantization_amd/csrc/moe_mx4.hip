@@ -19,10 +19,8 @@ constexpr int kMxMoeNk = 4, kCols = 16, kHalf = kMxRows / 2;
 struct MoeMxProduct {
     const uint8_t* codes[2];
     const uint8_t* scales[2];
-    const uint32_t* xq;      // split rows of the input and their scale words
-    const uint32_t* xs;
-    uint32_t* hq;            // gate and up: [pairs][rows / 32] split blocks
-    uint32_t* hs;
+    char* x;                 // split records of the input
+    char* h;                 // gate and up: of the hidden vectors of the pairs
     float* part;             // down: [pairs][rows]
     const int32_t* ids;
     const float* weights;
@@ -49,8 +47,9 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
         const int col = min(r16, cols - 1);
         const int xrow[1] = {GATED ? (int)m.x[col] : (int)m.y[col]};
         const int part = u % parts;
+        const MxInputRows<kFmt6> xin = {SplitRows{p.x, kSplitTokens, p.st.nb}};
         mx4_body<1, kMxMoeNk, kFmt6, GATED>(
-            wq, ws, p.xq, p.xs, xrow, p.st, part, parts, tiles, red,
+            wq, ws, xin, xrow, p.st, part, parts, tiles, red,
             [&](int tile) { return min(GATED ? tile * kHalf + (r16 & (kHalf - 1)) : tile * kMxRows + r16, p.rows - 1); },
             [&](int t0, auto sum) {
                 if constexpr (GATED) {
@@ -70,9 +69,7 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
                         }
                         uint32_t o[kSplitDwords], s;
                         split_block32(even, odd, o, s);
-                        const size_t b = (size_t)m.y[tid] * (p.rows / kMxBlock) + t0 / kMxTiles;
-                        store_split(p.hq + b * kSplitDwords, o);
-                        p.hs[b] = s;
+                        store_split(SplitRows{p.h, kSplitTokens, p.rows / kMxBlock}, m.y[tid], t0 / kMxTiles, o, s);
                     }
                 } else {
                     for (int idx = tid; idx < kMxTiles * cols * kMxRows; idx += kMxThreads) {
@@ -87,8 +84,6 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
 }
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
-int64_t split_bytes(int64_t rows, int64_t in) { return round256(rows * (in / kMxBlock) * kSplitBytes); }
-int64_t split_scale_bytes(int64_t rows, int64_t in) { return round256(rows * (in / kMxBlock) * kSplitScaleBytes); }
 
 // As moe.hip's, with 17/32 of a byte a weight and 1 us.
 float start_cost(int layers, int64_t rows, int64_t in) {
@@ -99,8 +94,7 @@ float start_cost(int layers, int64_t rows, int64_t in) {
 
 int64_t moe_mx4_workspace(int64_t in, int64_t inner, int64_t tokens, int64_t k) {
     const int64_t pairs = tokens * k;
-    return split_bytes(tokens, in) + split_scale_bytes(tokens, in) + split_bytes(pairs, inner) + split_scale_bytes(pairs, inner) +
-           round256(pairs * in * 4);
+    return round256(mx4_split_bytes(tokens, in)) + round256(mx4_split_bytes(pairs, inner)) + round256(pairs * in * 4);
 }
 
 hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspace, hipStream_t stream) {
@@ -110,20 +104,16 @@ hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspa
         at += bytes;
         return p;
     };
-    uint32_t* xq = reinterpret_cast<uint32_t*>(take(split_bytes(c.tokens, c.in)));
-    uint32_t* xs = reinterpret_cast<uint32_t*>(take(split_scale_bytes(c.tokens, c.in)));
     MoeMxProduct p = {};
-    p.hq = reinterpret_cast<uint32_t*>(take(split_bytes(c.pairs(), c.inner)));
-    p.hs = reinterpret_cast<uint32_t*>(take(split_scale_bytes(c.pairs(), c.inner)));
+    p.x = take(round256(mx4_split_bytes(c.tokens, c.in)));
+    p.h = take(round256(mx4_split_bytes(c.pairs(), c.inner)));
     p.part = reinterpret_cast<float*>(at);
-    hipError_t r = launch_mx4_split(c.x, xq, xs, c.tokens * (c.in / kMxBlock), stream);
+    hipError_t r = launch_mx4_split(c.x, p.x, c.in, c.tokens, stream);
     if (r != hipSuccess) return r;
     for (int l = 0; l < 2; ++l) {
         p.codes[l] = static_cast<const uint8_t*>(L.codes[l]);
         p.scales[l] = static_cast<const uint8_t*>(L.scales[l]);
     }
-    p.xq = xq;
-    p.xs = xs;
     p.ids = c.ids;
     p.weights = c.weights;
     p.st = mx4_steps(c.in, kMxMoeNk);
@@ -138,8 +128,7 @@ hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspa
     if (r != hipSuccess) return r;
     p.codes[0] = static_cast<const uint8_t*>(L.codes[2]);
     p.scales[0] = static_cast<const uint8_t*>(L.scales[2]);
-    p.xq = p.hq;
-    p.xs = p.hs;
+    p.x = p.h;
     p.st = mx4_steps(c.inner, kMxMoeNk);
     p.rows = (int)c.in;
     p.fixed = start_cost(1, c.inner, c.in);

@@ -23,6 +23,11 @@
 
 namespace aqlm {
 
+typedef _Float16 f16x32 __attribute__((ext_vector_type(32)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
 constexpr int kMxBlock = 32;          // values that share a scale
 constexpr int kMxBlockBytes = 16;     // codes of a block
 constexpr int kMxStep = 128;          // values a scaled matrix instruction multiplies per row
@@ -31,10 +36,29 @@ constexpr int kPieceDwords = 6;       // 32 of them
 constexpr int kSplitDwords = kPieces * kPieceDwords;   // a block in four pieces: 96 bytes
 constexpr uint32_t kScaleNaN = 255;
 
-typedef _Float16 f16x32 __attribute__((ext_vector_type(32)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
+// Split activations lie in records, one for every tile of w tokens (w = 32 in a workspace) and block of 32 inputs: for each
+// piece the first 16 bytes of the tokens' 24, then for each piece the other 8, then the tokens' scale words.  So an
+// operand is one 16-byte and one 8-byte access, and neighbouring tokens are neighbours in memory.
+constexpr int kSplitTokens = 32;
+constexpr int kSplitTokenBytes = kPieces * kPieceDwords * 4 + 4;          // 100
+constexpr int kSplitRecord = kSplitTokens * kSplitTokenBytes;             // 3200
+struct SplitRows {
+    char* base;
+    int w, nb;   // tokens of a tile, blocks of a row
+    __device__ __forceinline__ char* record(int token, int block) const {
+        return base + ((size_t)(token / w) * nb + block) * (size_t)(w * kSplitTokenBytes);
+    }
+    __device__ __forceinline__ u32x4* first(char* rec, int token, int p) const {
+        return reinterpret_cast<u32x4*>(rec + 16 * (p * w + token % w));
+    }
+    __device__ __forceinline__ u32x2* rest(char* rec, int token, int p) const {
+        return reinterpret_cast<u32x2*>(rec + 64 * w + 8 * (p * w + token % w));
+    }
+    __device__ __forceinline__ uint32_t* scales(char* rec, int token) const {
+        return reinterpret_cast<uint32_t*>(rec + 96 * w) + token % w;
+    }
+};
+
 
 __device__ __forceinline__ i32x8 operand4(u32x4 v) { return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0}; }
 __device__ __forceinline__ i32x8 operand6(u32x6 v) {
@@ -43,6 +67,10 @@ __device__ __forceinline__ i32x8 operand6(u32x6 v) {
 
 // acc + A B for MX4 A (16 rows) and B (16 columns) of 4- or 6-bit floats; the scale of B is byte SEL of sb.
 constexpr int kFmt6 = 2, kFmt4 = 4;   // the instruction's format numbers (6 bits: two exponent, three mantissa)
+template <int FMT_B, int SEL_A, int SEL_B>
+__device__ __forceinline__ f32x16 mfma_mx32(i32x8 a, i32x8 b, f32x16 acc, uint32_t sa, uint32_t sb) {   // 32 rows and columns, 64 values
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, kFmt4, FMT_B, SEL_A, (int)sa, SEL_B, (int)sb);
+}
 template <int FMT_B, int SEL>
 __device__ __forceinline__ f32x4 mfma_mx(i32x8 a, i32x8 b, f32x4 acc, uint32_t sa, uint32_t sb) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, kFmt4, FMT_B, 0, (int)sa, SEL, (int)sb);
@@ -137,10 +165,16 @@ __device__ __forceinline__ void split_block32(f32x16 even, f32x16 odd, uint32_t 
     }
 }
 
-__device__ __forceinline__ void store_split(uint32_t* to, const uint32_t (&o)[kSplitDwords]) {   // 16-byte aligned
+__device__ __forceinline__ void store_split(const SplitRows& to, int token, int block, const uint32_t (&o)[kSplitDwords],
+                                            uint32_t scales) {
+    char* rec = to.record(token, block);
 #pragma unroll
-    for (int i = 0; i < kSplitDwords / 4; ++i)
-        reinterpret_cast<u32x4*>(to)[i] = u32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+    for (int p = 0; p < kPieces; ++p) {
+        const uint32_t* q = o + p * kPieceDwords;
+        *to.first(rec, token, p) = u32x4{q[0], q[1], q[2], q[3]};
+        *to.rest(rec, token, p) = u32x2{q[4], q[5]};
+    }
+    *to.scales(rec, token) = scales;
 }
 
 }  // namespace aqlm

@@ -18,6 +18,8 @@ bool in_ok(int64_t in) { return in >= 32 && in <= AQLM_MAX_IN && in % 32 == 0; }
 int check_linear(int act, int64_t out, int64_t in, int64_t batch) {
     if (act < AQLM_ACT_NONE || act > AQLM_ACT_GELU_TANH) return AQLM_ERR_ACT;
     if (!in_ok(in) || out < 0 || out > AQLM_ACT_MAX_OUT || batch < 0 || batch > AQLM_MX4_MAX_BATCH) return AQLM_ERR_SHAPE;
+    // output tiles are counted in 32 bits
+    if (((out + 127) / 128 + 1) * ((batch + 127) / 128 + 1) > INT32_MAX) return AQLM_ERR_SHAPE;
     return AQLM_OK;
 }
 

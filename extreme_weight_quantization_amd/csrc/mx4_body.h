@@ -7,6 +7,8 @@
 // for all tiles of the group, and streams the codes of its steps, kMxTiles tiles ahead.  The waves' partial tiles are
 // added in LDS in the order of the waves.
 #pragma once
+#include <type_traits>
+
 #include "mx4.h"
 
 namespace aqlm {
@@ -34,35 +36,58 @@ inline MxSteps mx4_steps(int64_t in, int nk_max) {
     return s;
 }
 
-// Activations of one lane: for column tile c the blocks of token row xrow[c].
-//   FMT kFmt6: split blocks (mx4.h), xq [..][nb][24] dwords, xs [..][nb] scale words
-//   FMT kFmt4: MX4, xq [..][nb][4] dwords, xs [..][nb] scale bytes
+// Activations of one lane, the block `block` of token `row`.
+//   FMT kFmt6: split records (mx4.h)
+//   FMT kFmt4: MX4 rows, codes [..][nb][16 bytes] and scale bytes [..][nb]
+template <int FMT>
+struct MxInputRows;
+template <>
+struct MxInputRows<kFmt6> {
+    SplitRows rows;
+};
+template <>
+struct MxInputRows<kFmt4> {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int nb;
+};
+
 template <int FMT>
 struct MxOperand {
-    static constexpr int kDwords = FMT == kFmt6 ? kSplitDwords : 4;
-    uint32_t q[kDwords];
+    static constexpr int kParts = FMT == kFmt6 ? kPieces : 1;
+    using Part = std::conditional_t<FMT == kFmt6, u32x6, u32x4>;
+    Part q[kParts];
     uint32_t s;
-    __device__ __forceinline__ void load(const uint32_t* xq, const void* xs, size_t block, bool in_row) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(xq + block * kDwords);
+    __device__ __forceinline__ void load(const MxInputRows<FMT>& x, int row, int block, bool in_row) {
+        if constexpr (FMT == kFmt6) {
+            char* rec = x.rows.record(row, block);
 #pragma unroll
-        for (int i = 0; i < kDwords / 4; ++i) {
-            const u32x4 v = p[i];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) q[4 * i + t] = in_row ? v[t] : 0u;
+            for (int p = 0; p < kPieces; ++p) {
+                const u32x4 a = *x.rows.first(rec, row, p);
+                const u32x2 b = *x.rows.rest(rec, row, p);
+                q[p] = u32x6{a[0], a[1], a[2], a[3], b[0], b[1]};
+            }
+            s = *x.rows.scales(rec, row);
+        } else {
+            const size_t at = (size_t)row * x.nb + block;
+            q[0] = load16(x.codes + at * kMxBlockBytes);
+            s = x.scales[at];
         }
-        const uint32_t sv = FMT == kFmt6 ? static_cast<const uint32_t*>(xs)[block] : static_cast<const uint8_t*>(xs)[block];
-        s = in_row ? sv : 0x7f7f7f7fu;
+        if (!in_row) {
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) q[p] = Part{};
+            s = 0x7f7f7f7fu;
+        }
     }
     __device__ __forceinline__ f32x4 product(u32x4 a, uint32_t sa, f32x4 acc) const {
         const i32x8 av = operand4(a);
         if constexpr (FMT == kFmt4) {
-            return mfma_mx<kFmt4, 0>(av, operand4(u32x4{q[0], q[1], q[2], q[3]}), acc, sa, s);
+            return mfma_mx<kFmt4, 0>(av, operand4(q[0]), acc, sa, s);
         } else {
-            auto piece = [&](int p) { return operand6(u32x6{q[6 * p], q[6 * p + 1], q[6 * p + 2], q[6 * p + 3], q[6 * p + 4], q[6 * p + 5]}); };
-            acc = mfma_mx<kFmt6, 3>(av, piece(3), acc, sa, s);   // small terms first
-            acc = mfma_mx<kFmt6, 2>(av, piece(2), acc, sa, s);
-            acc = mfma_mx<kFmt6, 1>(av, piece(1), acc, sa, s);
-            return mfma_mx<kFmt6, 0>(av, piece(0), acc, sa, s);
+            acc = mfma_mx<kFmt6, 3>(av, operand6(q[3]), acc, sa, s);   // small terms first
+            acc = mfma_mx<kFmt6, 2>(av, operand6(q[2]), acc, sa, s);
+            acc = mfma_mx<kFmt6, 1>(av, operand6(q[1]), acc, sa, s);
+            return mfma_mx<kFmt6, 0>(av, operand6(q[0]), acc, sa, s);
         }
     }
 };
@@ -72,7 +97,7 @@ struct MxOperand {
 // nwg; sum(i, col, r) adds the waves' partial products of matrix-core row r and column col of the i-th.
 template <int CT, int NK, int FMT, bool RUN, class RowOf, class Fin>
 __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws,
-                                         const uint32_t* xq, const void* xs, const int (&xrow)[CT], const MxSteps st,
+                                         const MxInputRows<FMT>& xin, const int (&xrow)[CT], const MxSteps st,
                                          const int bid, const int nwg, const int n_tiles, float* red, RowOf row_of,
                                          Fin fin) {
     const int lane = threadIdx.x & (kWave - 1);
@@ -101,7 +126,7 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
             if (j < st.nk) {
                 const int b = 4 * (first(c) + j) + q;
 #pragma unroll
-                for (int t = 0; t < CT; ++t) x[t][j].load(xq, xs, (size_t)xrow[t] * nb + min(b, nb - 1), b < nb);
+                for (int t = 0; t < CT; ++t) x[t][j].load(xin, xrow[t], min(b, nb - 1), b < nb);
             }
         }
     };

@@ -67,13 +67,15 @@ __global__ __launch_bounds__(kThreads) void mx4_decode_kernel(const uint32_t* __
     }
 }
 
-__global__ __launch_bounds__(kThreads) void mx4_split_kernel(const f16* __restrict__ x, uint32_t* __restrict__ pieces,
-                                                             uint32_t* __restrict__ scales, int64_t blocks) {
-    for (int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x; b < blocks; b += (int64_t)gridDim.x * kThreads) {
-        uint32_t out[kSplitDwords], s;
-        split_block(load_block16(x + b * kMxBlock), out, s);
-        store_split(pieces + b * kSplitDwords, out);
-        scales[b] = s;
+// A lane splits one block: neighbouring lanes, neighbouring tokens of a tile.
+__global__ __launch_bounds__(kThreads) void mx4_split_kernel(const f16* __restrict__ x, SplitRows to, int T, int64_t lanes) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < lanes; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t tb = i / kSplitTokens;
+        const int token = (int)(tb / to.nb) * kSplitTokens + (int)(i % kSplitTokens), block = (int)(tb % to.nb);
+        if (token >= T) continue;
+        uint32_t o[kSplitDwords], s;
+        split_block(load_block16(x + ((size_t)token * to.nb + block) * kMxBlock), o, s);
+        store_split(to, token, block, o, s);
     }
 }
 
@@ -96,9 +98,15 @@ hipError_t launch_mx4_decode(const void* codes, const void* scales, void* w, int
     return hipGetLastError();
 }
 
-hipError_t launch_mx4_split(const void* x, void* pieces, void* scales, int64_t blocks, hipStream_t stream) {
-    hipLaunchKernelGGL(mx4_split_kernel, flat_grid(blocks, 8), dim3(kThreads), 0, stream, static_cast<const f16*>(x),
-                       static_cast<uint32_t*>(pieces), static_cast<uint32_t*>(scales), blocks);
+int64_t mx4_split_bytes(int64_t batch, int64_t in) {
+    return (batch + kSplitTokens - 1) / kSplitTokens * (in / kMxBlock) * kSplitRecord;
+}
+
+hipError_t launch_mx4_split(const void* x, void* records, int64_t in, int64_t batch, hipStream_t stream) {
+    const int nb = (int)(in / kMxBlock);
+    const int64_t lanes = (batch + kSplitTokens - 1) / kSplitTokens * kSplitTokens * nb;
+    hipLaunchKernelGGL(mx4_split_kernel, flat_grid(lanes, 8), dim3(kThreads), 0, stream, static_cast<const f16*>(x),
+                       SplitRows{static_cast<char*>(records), kSplitTokens, nb}, (int)batch, lanes);
     return hipGetLastError();
 }
 

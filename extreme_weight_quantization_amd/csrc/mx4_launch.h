@@ -10,9 +10,9 @@ namespace aqlm {
 // fp16 [blocks][32] to codes [blocks][16] and scales [blocks], and back (mx4_convert.hip).
 hipError_t launch_mx4_quantize(const void* w, void* codes, void* scales, int64_t blocks, hipStream_t stream);
 hipError_t launch_mx4_decode(const void* codes, const void* scales, void* w, int64_t blocks, hipStream_t stream);
-// fp16 [blocks][32] to the four-piece form of mx4.h: pieces [blocks][96 bytes], scale words [blocks].
-hipError_t launch_mx4_split(const void* x, void* pieces, void* scales, int64_t blocks, hipStream_t stream);
-constexpr int64_t kSplitBytes = 96, kSplitScaleBytes = 4;
+// fp16 rows [batch][in] to split records of 32 tokens (mx4.h), which take mx4_split_bytes.
+int64_t mx4_split_bytes(int64_t batch, int64_t in);
+hipError_t launch_mx4_split(const void* x, void* records, int64_t in, int64_t batch, hipStream_t stream);
 
 // Activations of an MX4 product: fp16 rows (scales NULL), or MX4 codes and scales.
 struct MxInput {

@@ -12,6 +12,7 @@
 
 #include "act_math.h"
 #include "mx4_body.h"
+#include "mx4_gemm.h"
 #include "mx4_launch.h"
 
 namespace aqlm {
@@ -31,7 +32,7 @@ constexpr int kInlineBlocks = 1024;
 
 template <int CT, int NK, int FMT, bool INLINE>
 __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __restrict__ codes,
-                                                              const uint8_t* __restrict__ scales, const void* xq,
+                                                              const uint8_t* __restrict__ scales, const void* x,
                                                               const void* xs, MxSteps st, int out, int T, MxEpilogue e) {
     extern __shared__ u32x4 smem[];
     float* red = reinterpret_cast<float*>(smem);
@@ -41,23 +42,23 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
 #pragma unroll
     for (int t = 0; t < CT; ++t) xrow[t] = min(col0 + t * 16 + (lane & 15), T - 1);
     const int n_tiles = (out + kMxRows - 1) / kMxRows;
-    const uint32_t* pieces = static_cast<const uint32_t*>(xq);
-    if constexpr (INLINE) {
-        uint32_t* lq = reinterpret_cast<uint32_t*>(red + mx4_red_floats(CT));
-        uint32_t* lsc = lq + (size_t)T * st.nb * kSplitDwords;
-        for (int b = threadIdx.x; b < T * st.nb; b += kMxThreads) {
+    MxInputRows<FMT> xin;
+    if constexpr (FMT == kFmt4) {
+        xin = {static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(xs), st.nb};
+    } else if constexpr (INLINE) {
+        xin.rows = SplitRows{reinterpret_cast<char*>(red + mx4_red_floats(CT)), T, st.nb};
+        for (int i = threadIdx.x; i < T * st.nb; i += kMxThreads) {
             uint32_t o[kSplitDwords], s;
-            split_block(load_block16(static_cast<const f16*>(xq) + (size_t)b * kMxBlock), o, s);
-            store_split(lq + (size_t)b * kSplitDwords, o);
-            lsc[b] = s;
+            split_block(load_block16(static_cast<const f16*>(x) + (size_t)i * kMxBlock), o, s);
+            store_split(xin.rows, i / st.nb, i % st.nb, o, s);
         }
         __syncthreads();
-        pieces = lq;
-        xs = lsc;
+    } else {
+        xin.rows = SplitRows{static_cast<char*>(const_cast<void*>(x)), kSplitTokens, st.nb};
     }
     const int nwg = (int)gridDim.x;
     mx4_body<CT, NK, FMT, false>(
-        codes, scales, pieces, xs, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
+        codes, scales, xin, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
         [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); },
         [&](int t0, auto sum) {
             for (int idx = threadIdx.x; idx < kMxTiles * cols * kMxRows; idx += kMxThreads) {
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
 }
 
 struct RowsCall {
-    const void *codes, *scales, *xq, *xs;
+    const void *codes, *scales, *x, *xs;
     MxEpilogue e;
     int64_t out, in;
     int T;
@@ -87,14 +88,14 @@ hipError_t launch_rows_v(const RowsCall& c) {
     auto kern = mx4_rows_kernel<CT, NK, FMT, INLINE>;
     const MxSteps st = mx4_steps(c.in, NK);
     const size_t lds = mx4_red_floats(CT) * sizeof(float) +
-                       (INLINE ? (size_t)c.T * st.nb * (kSplitBytes + kSplitScaleBytes) : 0);
+                       (INLINE ? (size_t)c.T * st.nb * kSplitTokenBytes : 0);
     if (lds > 65536) {
         const hipError_t r = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (r != hipSuccess) return r;
     }
     const int tiles = (int)((c.out + kMxRows - 1) / kMxRows), groups = (c.T + CT * 16 - 1) / (CT * 16);
     hipLaunchKernelGGL(kern, dim3(std::min(tiles, device_cu_count()), groups), dim3(kMxThreads), lds, c.stream,
-                       static_cast<const uint8_t*>(c.codes), static_cast<const uint8_t*>(c.scales), c.xq, c.xs, st,
+                       static_cast<const uint8_t*>(c.codes), static_cast<const uint8_t*>(c.scales), c.x, c.xs, st,
                        (int)c.out, c.T, c.e);
     return hipGetLastError();
 }
@@ -113,25 +114,28 @@ bool split_inline(int64_t in, int64_t batch) { return batch <= 16 && batch * (in
 }  // namespace
 
 int64_t mx4_linear_workspace(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
-    if (x_mx4 || out == 0 || batch == 0 || split_inline(in, batch)) return 0;
-    return batch * (in / kMxBlock) * (kSplitBytes + kSplitScaleBytes);
+    if (out == 0 || batch == 0) return 0;
+    const int64_t split = x_mx4 || split_inline(in, batch) ? 0 : mx4_split_bytes(batch, in);
+    return split + (mx4_gemm_serves(out, in, batch) ? mx4_gemm_part_bytes(out, in, batch) : 0);
 }
 
 hipError_t launch_mx4_linear(const void* codes, const void* scales, MxInput x, const Epilogue& e, void* workspace,
                              int64_t out, int64_t in, int64_t batch, hipStream_t stream) {
-    RowsCall c = {codes, scales, x.x, x.scales,
-                  MxEpilogue{static_cast<const f16*>(e.bias[0]), static_cast<const f16*>(e.residual),
-                             static_cast<f16*>(e.y), e.act},
-                  out, in, (int)batch, stream};
-    if (x.scales != nullptr) return launch_rows<kFmt4, false>(c);
-    if (split_inline(in, batch)) return launch_rows<kFmt6, true>(c);
-    const int64_t blocks = batch * (in / kMxBlock);
-    char* xs = static_cast<char*>(workspace) + blocks * kSplitBytes;
-    const hipError_t r = launch_mx4_split(x.x, workspace, xs, blocks, stream);
-    if (r != hipSuccess) return r;
-    c.xq = workspace;
-    c.xs = xs;
-    return launch_rows<kFmt6, false>(c);
+    const bool four = x.scales != nullptr, inlined = !four && split_inline(in, batch);
+    char* part = static_cast<char*>(workspace);
+    if (!four && !inlined) {
+        const hipError_t r = launch_mx4_split(x.x, workspace, in, batch, stream);
+        if (r != hipSuccess) return r;
+        x.x = workspace;
+        part += mx4_split_bytes(batch, in);
+    }
+    if (mx4_gemm_serves(out, in, batch)) return launch_mx4_gemm(codes, scales, x, e, part, out, in, batch, stream);
+    const RowsCall c = {codes, scales, x.x, x.scales,
+                        MxEpilogue{static_cast<const f16*>(e.bias[0]), static_cast<const f16*>(e.residual),
+                                   static_cast<f16*>(e.y), e.act},
+                        out, in, (int)batch, stream};
+    if (four) return launch_rows<kFmt4, false>(c);
+    return inlined ? launch_rows<kFmt6, true>(c) : launch_rows<kFmt6, false>(c);
 }
 
 }  // namespace aqlm

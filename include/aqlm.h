@@ -474,7 +474,8 @@ int aqlm_gated_lists(const void* const* tables, const void* const* entries, cons
  * codes [batch][in / 2] and x_scales their scales [batch][in / 32].  bias [out]
  * and residual [batch][out] fp16 may be NULL; residual may be y itself; no
  * other arrays may overlap.  act is one of aqlm_act.  0 <= out <=
- * AQLM_ACT_MAX_OUT, 0 <= batch <= AQLM_MX4_MAX_BATCH (else AQLM_ERR_SHAPE).
+ * AQLM_ACT_MAX_OUT, 0 <= batch <= AQLM_MX4_MAX_BATCH, fewer than 2^31 tiles
+ * of 128 outputs x 128 tokens (else AQLM_ERR_SHAPE).
  * out == 0 or batch == 0 enqueues nothing.  Workspace: as for the fused
  * products above, of aqlm_mx4_linear_workspace_bytes bytes (x_mx4: whether x
  * is in MX4); a larger batch never needs fewer.
