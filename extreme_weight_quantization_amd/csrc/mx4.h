@@ -67,8 +67,10 @@ __device__ __forceinline__ i32x8 operand6(u32x6 v) {
 
 // acc + A B for MX4 A (16 rows) and B (16 columns) of 4- or 6-bit floats; the scale of B is byte SEL of sb.
 constexpr int kFmt6 = 2, kFmt4 = 4;   // the instruction's format numbers (6 bits: two exponent, three mantissa)
+// The same over 64 values for 32 rows and columns, A in MX4: lane l supplies the 32 values of block l / 32 for row (column) l % 32
+// and holds D[8 (r / 4) + 4 (l / 32) + r % 4][l % 32] for r = 0 .. 15.
 template <int FMT_B, int SEL_A, int SEL_B>
-__device__ __forceinline__ f32x16 mfma_mx32(i32x8 a, i32x8 b, f32x16 acc, uint32_t sa, uint32_t sb) {   // 32 rows and columns, 64 values
+__device__ __forceinline__ f32x16 mfma_mx32(i32x8 a, i32x8 b, f32x16 acc, uint32_t sa, uint32_t sb) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, kFmt4, FMT_B, SEL_A, (int)sa, SEL_B, (int)sb);
 }
 template <int FMT_B, int SEL>

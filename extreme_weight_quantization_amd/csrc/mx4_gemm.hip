@@ -1,22 +1,24 @@
 // Products of MX4 weights with many tokens: z[t][i] = sum_k W[i][k] x[t][k], then mx4_linear.hip's epilogue.
 //
-// The scaled matrix instructions take codes and scales as they are, so the work is to bring them on time.  A workgroup of 8
-// waves owns a tile of TM rows of W x TN tokens; wave (m, n) of WM x WN a part of MT x NT squares of 32 x 32, which
-// each take one instruction a step of 64 inputs (four with x split in pieces).  Inputs pass through LDS in stages of 128, loaded
-// straight from memory, with one barrier a stage; the two waves of a SIMD read and multiply in turn.
+// The scaled matrix instructions take codes and scales as they are, so the work is to bring them on time.  A workgroup of
+// WM x WN waves owns a tile of TM rows of W x TN tokens; a wave a part of MT x NT squares of 32 x 32, which each take one
+// instruction a step of 64 inputs (four with x split in pieces).  Inputs pass through LDS in stages of 32 KB blocks, loaded straight
+// from memory, with one barrier a stage.  Between two matrix instructions of a step a wave reads a piece of the
+// next step's operands, or issues a load of a later stage.
 //
 // LDS of a stage:
-//   rows of MX4 (W, and x where it is MX4): 64 bytes a row; block b of row r lies in slot b ^ (r / 4 % 4), so that the 16 lanes
-//     that one clock of a 16-byte read serves (0-3, 12-15, 20-27; 4-11, 16-19, 28-31; likewise above 32) find 16 distinct
-//     banks, and four neighbouring lanes of a load still read 64 contiguous bytes;
+//   rows of MX4 (W, and x where it is MX4): KB blocks of 16 bytes a row; block b of row r lies in slot b ^ fold(r), so that the
+//     16 lanes that one clock of a 16-byte read serves (0-3, 12-15, 20-27; 4-11, 16-19, 28-31; likewise above 32) find 16
+//     distinct banks, and KB neighbouring lanes of a load still read 16 KB contiguous bytes;
 //   split x: the records of mx4.h as they are.
-// Scale bytes of MX4 rows: 16 bytes a row at a time, four stages' worth, from any address, through registers into LDS of their
-// own (two buffers).  A lane reads the four bytes of its row and stage and moves its half of the wave's to where the
-// instruction's byte selection finds it.
+// Scale bytes of MX4 rows: 16 bytes a row at a time, 16 blocks' worth, into LDS of their own (two buffers): straight where
+// rows and array are 16-byte aligned (in % 512 == 0), else through registers from any address.  A lane reads the bytes of
+// its row and stage and moves its half of the wave's to where the instruction's byte selection finds it.
 //
-// LDS reads are inline assembly with their wait, because the compiler would make every LDS read wait for the
-// loads into LDS that are still in flight.
+// At the end a wave turns its squares in LDS, so that a lane has 8 neighbouring outputs of a token, and finishes them in a
+// loop that is not unrolled: with a copy of the activations' code for every square the epilogue took 70 us of 360.
 #include <algorithm>
+#include <type_traits>
 
 #include "act_bias.h"
 #include "act_math.h"
@@ -26,9 +28,7 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kThreads = 512, kWaves = 8;
-constexpr int kStageBlocks = 4;        // blocks of a stage: 128 inputs
-constexpr int kScaleStages = 4;        // stages that a load of scales serves
+constexpr int kChunkBlocks = 16;       // blocks that a load of scales serves
 
 struct GemmArgs {
     const uint8_t* w;        // codes, scales of W
@@ -40,23 +40,26 @@ struct GemmArgs {
     f16* y;
     float* part;             // [split][token][op], for splits > 1
     int act, out, T, nb, op;
-    int tiles_m, tiles_n, splits, stages;   // stages of the whole row; of a split: a multiple of kScaleStages
+    int tiles_m, tiles_n, splits, chunks;   // chunks of kChunkBlocks of the whole row
 };
 
-template <int FMT, int WM, int WN, int MT, int NT, int STAGES>
+template <int FMT, int WM, int WN, int MT, int NT, int KB, int STAGES>
 struct Tile {
+    static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     static constexpr int kM = WM * MT * 32, kN = WN * NT * 32;
-    static constexpr int kABytes = kM * 64;
-    static constexpr int kBBytes = FMT == kFmt4 ? kN * 64 : kN / 32 * kStageBlocks * kSplitRecord;
+    static constexpr int kABytes = kM * KB * 16;
+    static constexpr int kBBytes = FMT == kFmt4 ? kN * KB * 16 : kN / 32 * KB * kSplitRecord;
     static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kScaleRows = kM + (FMT == kFmt4 ? kN : 0);
+    static constexpr int kScaleLoads = (kM + (FMT == kFmt4 ? kN : 0) + kThreads - 1) / kThreads;   // rows a thread
+    static constexpr int kScaleRows = kScaleLoads * kThreads;              // the last may repeat
     static constexpr int kScales = STAGES * kStage;                        // their place in LDS
     static constexpr int kPipe = kScales + 2 * kScaleRows * 16;
-    static constexpr int kEpiRow = MT * 32 * 4 + 16;                       // bytes of a token's row of a wave's epilogue tile
+    static constexpr int kEpiRow = MT * 32 * 4 + 16;                       // bytes of a token in a wave's LDS of the epilogue
     static constexpr int kLds = kPipe > kWaves * 32 * kEpiRow ? kPipe : kWaves * 32 * kEpiRow;
-    static constexpr int kLoads = (kStage / 1024 + (kStage % 1024 != 0) + kWaves - 1) / kWaves;   // a wave, a stage
-    static_assert(WM * WN == kWaves && kLds <= 163840 && kScaleRows <= kThreads);
-    static_assert(kStage % 1024 == 0, "whole loads of a wave");
+    static constexpr int kLoads = (kStage / 1024 + kWaves - 1) / kWaves;   // a wave, a stage
+    static constexpr int kSteps = KB / 2;
+    static constexpr int kChunkStages = kChunkBlocks / KB;
+    static_assert(kLds <= 163840 && kStage % 1024 == 0 && kM % 64 == 0 && kN % 64 == 0);
 };
 
 // 16 bytes of an array of `total` >= 16 from any offset; bytes past its end are zero.
@@ -76,73 +79,35 @@ __device__ __forceinline__ u32x4 load_bytes16(const uint8_t* __restrict__ p, int
     return r;
 }
 
+// 64 x 16 bytes from base + off (a lane's) to LDS address `to` (uniform) on.  Inline assembly, because the compiler
+// makes every later LDS read wait for a load into LDS that it knows of; the stage's barrier waits for all of them instead.  There
+// is no result to wait for, and the address register is read when the load is issued.  M0 has no other user in this kernel.
+__device__ __forceinline__ void load_to_lds(uint32_t to, const void* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
+}
+
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)lds_ptr(const_cast<void*>(p)); }
 
-// One step of 64 inputs: the operands of MT row squares, from `a` + 2048 i.
-template <int MT>
-struct AOperand {
-    u32x4 v[MT];
+template <int KB>
+__device__ __forceinline__ int fold(int r) { return KB == 8 ? r & 7 : (r >> 2) & 3; }
+
+// The operands of a step of 64 inputs.
+template <int FMT, int MT, int NT>
+struct StepOperands {
+    u32x4 a[MT];
+    std::conditional_t<FMT == kFmt4, u32x4, u32x6> b[NT][FMT == kFmt4 ? 1 : kPieces];
+    uint32_t sb[NT];   // split x: scale words of the pieces
 };
 
+// The scales of MX4 rows of a stage: KB / 4 words a square.
+template <int FMT, int MT, int NT, int KB>
+struct StageScales {
+    uint32_t a[MT][KB / 4], b[FMT == kFmt4 ? NT : 1][KB / 4];
+};
 
-// Reads of a wave's operands, all waited for.  a: LDS address of the lane's block of the first row square; b: of x.
-__device__ __forceinline__ void read_4(AOperand<4>& a, u32x4 (&b)[2], uint32_t pa, uint32_t pb) {
-    asm volatile("ds_read_b128 %0, %6\n\tds_read_b128 %1, %6 offset:2048\n\tds_read_b128 %2, %6 offset:4096\n\t"
-                 "ds_read_b128 %3, %6 offset:6144\n\tds_read_b128 %4, %7\n\tds_read_b128 %5, %7 offset:2048\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(a.v[0]), "=&v"(a.v[1]), "=&v"(a.v[2]), "=&v"(a.v[3]), "=&v"(b[0]), "=&v"(b[1])
-                 : "v"(pa), "v"(pb)
-                 : "memory");
-}
-__device__ __forceinline__ void read_4(AOperand<2>& a, u32x4 (&b)[1], uint32_t pa, uint32_t pb) {
-    asm volatile("ds_read_b128 %0, %3\n\tds_read_b128 %1, %3 offset:2048\n\tds_read_b128 %2, %4\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(a.v[0]), "=&v"(a.v[1]), "=&v"(b[0])
-                 : "v"(pa), "v"(pb)
-                 : "memory");
-}
-// x in pieces: the first 16 bytes of piece p at pb + 512 p, the other 8 at pr + 256 p, the scale word at ps.
-__device__ __forceinline__ void read_6(AOperand<4>& a, u32x4 (&b)[4], u32x2 (&r)[4], uint32_t& s, uint32_t pa, uint32_t pb,
-                                       uint32_t pr, uint32_t ps) {
-    asm volatile("ds_read_b128 %0, %13\n\tds_read_b128 %1, %13 offset:2048\n\tds_read_b128 %2, %13 offset:4096\n\t"
-                 "ds_read_b128 %3, %13 offset:6144\n\t"
-                 "ds_read_b128 %4, %14\n\tds_read_b128 %5, %14 offset:512\n\tds_read_b128 %6, %14 offset:1024\n\t"
-                 "ds_read_b128 %7, %14 offset:1536\n\t"
-                 "ds_read_b64 %8, %15\n\tds_read_b64 %9, %15 offset:256\n\tds_read_b64 %10, %15 offset:512\n\t"
-                 "ds_read_b64 %11, %15 offset:768\n\tds_read_b32 %12, %16\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(a.v[0]), "=&v"(a.v[1]), "=&v"(a.v[2]), "=&v"(a.v[3]), "=&v"(b[0]), "=&v"(b[1]), "=&v"(b[2]), "=&v"(b[3]),
-                   "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(s)
-                 : "v"(pa), "v"(pb), "v"(pr), "v"(ps)
-                 : "memory");
-}
-__device__ __forceinline__ void read_6(AOperand<2>& a, u32x4 (&b)[4], u32x2 (&r)[4], uint32_t& s, uint32_t pa, uint32_t pb,
-                                       uint32_t pr, uint32_t ps) {
-    asm volatile("ds_read_b128 %0, %11\n\tds_read_b128 %1, %11 offset:2048\n\t"
-                 "ds_read_b128 %2, %12\n\tds_read_b128 %3, %12 offset:512\n\tds_read_b128 %4, %12 offset:1024\n\t"
-                 "ds_read_b128 %5, %12 offset:1536\n\t"
-                 "ds_read_b64 %6, %13\n\tds_read_b64 %7, %13 offset:256\n\tds_read_b64 %8, %13 offset:512\n\t"
-                 "ds_read_b64 %9, %13 offset:768\n\tds_read_b32 %10, %14\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(a.v[0]), "=&v"(a.v[1]), "=&v"(b[0]), "=&v"(b[1]), "=&v"(b[2]), "=&v"(b[3]), "=&v"(r[0]), "=&v"(r[1]),
-                   "=&v"(r[2]), "=&v"(r[3]), "=&v"(s)
-                 : "v"(pa), "v"(pb), "v"(pr), "v"(ps)
-                 : "memory");
-}
-// N scale words, 512 bytes (32 rows) apart.
-__device__ __forceinline__ void read_scales(uint32_t (&s)[4], uint32_t p) {
-    asm volatile("ds_read_b32 %0, %4\n\tds_read_b32 %1, %4 offset:512\n\tds_read_b32 %2, %4 offset:1024\n\t"
-                 "ds_read_b32 %3, %4 offset:1536\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(s[0]), "=&v"(s[1]), "=&v"(s[2]), "=&v"(s[3])
-                 : "v"(p)
-                 : "memory");
-}
-__device__ __forceinline__ void read_scales(uint32_t (&s)[2], uint32_t p) {
-    asm volatile("ds_read_b32 %0, %2\n\tds_read_b32 %1, %2 offset:512\n\ts_waitcnt lgkmcnt(0)" : "=&v"(s[0]), "=&v"(s[1]) : "v"(p) : "memory");
-}
-__device__ __forceinline__ void read_scales(uint32_t (&s)[1], uint32_t p) {
-    asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(s[0]) : "v"(p) : "memory");
-}
-
-template <int FMT, int WM, int WN, int MT, int NT, int STAGES, bool PART>
-__global__ __launch_bounds__(kThreads) void mx4_gemm_kernel(GemmArgs g) {
-    using L = Tile<FMT, WM, WN, MT, NT, STAGES>;
+template <int FMT, int WM, int WN, int MT, int NT, int KB, int STAGES, bool PART, bool STRAIGHT>
+__global__ __launch_bounds__(WM* WN * 64) void mx4_gemm_kernel(GemmArgs g) {
+    using L = Tile<FMT, WM, WN, MT, NT, KB, STAGES>;
     extern __shared__ u32x4 smem[];
     char* lds = reinterpret_cast<char*>(smem);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -150,51 +115,74 @@ __global__ __launch_bounds__(kThreads) void mx4_gemm_kernel(GemmArgs g) {
     // tokens fastest: an XCD's workgroups share rows of W
     const int u = xcd_run((int)blockIdx.x, (int)gridDim.x);
     const int n0 = u % g.tiles_n * L::kN, m0 = u / g.tiles_n % g.tiles_m * L::kM, split = u / g.tiles_n / g.tiles_m;
-    const int per = ((g.stages + g.splits - 1) / g.splits + kScaleStages - 1) / kScaleStages * kScaleStages;
-    const int first = split * per, n_stage = min(per, g.stages - first);
     const int nb = g.nb;
+    const int per = (g.chunks + g.splits - 1) / g.splits;               // chunks of a part
+    const int block0 = split * per * kChunkBlocks, blocks = min(per * kChunkBlocks, nb - block0);
+    const int n_stage = (blocks + KB - 1) / KB;
     const int wm = wave / WN, wn = wave % WN;
+    const uint32_t lds0 = lds_address(lds);
 
-    // Load j of this wave in a stage: 64 chunks of 16 bytes, from `chunk` on.  Loads past the stage repeat the last.
-    auto load_stage = [&](int s) {
-        char* to = lds + s % STAGES * L::kStage;
-        const int b0 = (first + s) * kStageBlocks;
+    // Load j of this wave in a stage: 64 chunks of 16 bytes, from chunk 64 (wave + kWaves j) on (past the stage: the last 64
+    // again).  The lane's chunk of stage 0 lies row_off from the operand's base.  Blocks past the row are whatever follows it, and
+    // the array's last 16 bytes where nothing does: the products leave them out.
+    const uint8_t* const wbase = g.w + (size_t)m0 * nb * kMxBlockBytes;
+    const uint8_t* const xbase = g.x + (FMT == kFmt4 ? (size_t)n0 * nb * kMxBlockBytes : (size_t)(n0 / kSplitTokens) * nb * kSplitRecord);
+    auto last16 = [](int64_t bytes) { return (uint32_t)(bytes - 16 < (int64_t)0xfffffff0 ? bytes - 16 : (int64_t)0xfffffff0); };
+    const uint32_t wlast = last16((int64_t)(g.out - m0) * nb * kMxBlockBytes);
+    const uint32_t xlast = last16(FMT == kFmt4 ? (int64_t)(g.T - n0) * nb * kMxBlockBytes
+                                               : (int64_t)((g.T - n0 + kSplitTokens - 1) / kSplitTokens) * nb * kSplitRecord);
+    uint32_t row_off[L::kLoads];
 #pragma unroll
-        for (int j = 0; j < L::kLoads; ++j) {
-            const int i = min(wave + j * kWaves, L::kStage / 1024 - 1);   // uniform
-            const int c = i * 64 + lane;
-            const void* from;
-            if (i < L::kABytes / 1024) {
-                const int r = c / 4, b = b0 + ((c & 3) ^ ((r >> 2) & 3));
-                from = g.w + ((size_t)min(m0 + r, g.out - 1) * nb + min(b, nb - 1)) * kMxBlockBytes;
-            } else if constexpr (FMT == kFmt4) {
-                const int cb = c - L::kABytes / 16, r = cb / 4, b = b0 + ((cb & 3) ^ ((r >> 2) & 3));
-                from = g.x + ((size_t)min(n0 + r, g.T - 1) * nb + min(b, nb - 1)) * kMxBlockBytes;
-            } else {
-                constexpr int kPer = kSplitRecord / 16;   // chunks of a record
-                const int cb = c - L::kABytes / 16, rec = cb / kPer, tile = rec / kStageBlocks;
-                const int tt = min(n0 / kSplitTokens + tile, (g.T - 1) / kSplitTokens);
-                from = g.x + ((size_t)tt * nb + min(b0 + rec % kStageBlocks, nb - 1)) * kSplitRecord + (cb % kPer) * 16;
-            }
-            __builtin_amdgcn_global_load_lds(from, lds_ptr(to + i * 1024), 16, 0, 0);
+    for (int j = 0; j < L::kLoads; ++j) {
+        const int i = min(wave + j * L::kWaves, L::kStage / 1024 - 1), c = i * 64 + lane;
+        if (i < L::kABytes / 1024) {
+            const int r = c / KB;
+            row_off[j] = (uint32_t)((min(r, g.out - 1 - m0) * nb + block0 + ((c & (KB - 1)) ^ fold<KB>(r))) * kMxBlockBytes);
+        } else if constexpr (FMT == kFmt4) {
+            const int cb = c - L::kABytes / 16, r = cb / KB;
+            row_off[j] = (uint32_t)((min(r, g.T - 1 - n0) * nb + block0 + ((cb & (KB - 1)) ^ fold<KB>(r))) * kMxBlockBytes);
+        } else {
+            constexpr int kPer = kSplitRecord / 16;   // chunks of a record
+            const int cb = c - L::kABytes / 16, rec = cb / kPer;
+            row_off[j] = (uint32_t)(min(rec / KB, (g.T - 1 - n0) / kSplitTokens) * nb + block0 + rec % KB) * kSplitRecord + (cb % kPer) * 16;
         }
+    }
+    static_assert(L::kABytes / 1024 % L::kWaves == 0, "a load is of W or x for all waves");
+    auto load = [&](int s, int j) {
+        const int i = min(wave + j * L::kWaves, L::kStage / 1024 - 1);   // uniform
+        const bool of_w = j * L::kWaves < L::kABytes / 1024;
+        const uint32_t off = row_off[j] + (uint32_t)(s * KB * (FMT == kFmt4 || of_w ? kMxBlockBytes : kSplitRecord));
+        load_to_lds(lds0 + s % STAGES * L::kStage + i * 1024, of_w ? wbase : xbase, min(off, of_w ? wlast : xlast));
     };
-    // Scales of four stages: thread r has row r of W, then of x.
-    const bool has_scales = tid < L::kScaleRows;
-    auto load_scales = [&](int c) {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (has_scales) {
-            const bool of_w = tid < L::kM;
-            const int row = of_w ? min(m0 + tid, g.out - 1) : min(n0 + tid - L::kM, g.T - 1);
-            v = load_bytes16(of_w ? g.ws : g.xs, (int64_t)row * nb + (int64_t)(first + c * kScaleStages) * kStageBlocks,
-                             (int64_t)(of_w ? g.out : g.T) * nb);
-        }
-        return v;
+
+    // Scales of a chunk: a thread has rows tid, tid + kThreads, ... of W, then, where x is MX4, of x (then the last again).
+    auto scales_of_w = [&](int q) { return FMT != kFmt4 || wave * 64 + q * L::kThreads < L::kM; };   // all of a wave's 64
+    const uint8_t* sbase[L::kScaleLoads];
+    int64_t srow[L::kScaleLoads], sbytes[L::kScaleLoads];
+#pragma unroll
+    for (int q = 0; q < L::kScaleLoads; ++q) {
+        const bool of_w = scales_of_w(q);
+        const int r = tid + q * L::kThreads, rows = of_w ? g.out : g.T;
+        sbase[q] = of_w ? g.ws : g.xs;
+        srow[q] = (int64_t)min(of_w ? m0 + r : n0 + r - L::kM, rows - 1) * nb;
+        sbytes[q] = (int64_t)rows * nb;
+    }
+    auto load_scales = [&](int c, u32x4 (&v)[L::kScaleLoads]) {   // into registers
+#pragma unroll
+        for (int q = 0; q < L::kScaleLoads; ++q) v[q] = load_bytes16(sbase[q], srow[q] + block0 + c * kChunkBlocks, sbytes[q]);
     };
-    auto keep_scales = [&](u32x4 v, int c) {
-        if (has_scales) {
-            const uint32_t at = lds_address(lds + L::kScales + (c & 1) * L::kScaleRows * 16 + tid * 16);
-            asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
+    auto keep_scales = [&](const u32x4 (&v)[L::kScaleLoads], int c) {
+#pragma unroll
+        for (int q = 0; q < L::kScaleLoads; ++q)
+            *reinterpret_cast<u32x4*>(lds + L::kScales + ((c & 1) * L::kScaleRows + tid + q * L::kThreads) * 16) = v[q];
+    };
+    auto send_scales = [&](int c) {   // straight into LDS
+        const int b = min(block0 + c * kChunkBlocks, nb - kChunkBlocks);
+#pragma unroll
+        for (int q = 0; q < L::kScaleLoads; ++q) {
+            const int64_t row0 = (int64_t)(scales_of_w(q) ? m0 : n0) * nb;
+            load_to_lds(lds0 + L::kScales + ((c & 1) * L::kScaleRows + wave * 64 + q * L::kThreads) * 16, sbase[q] + row0,
+                        (uint32_t)(srow[q] - row0) + b);
         }
     };
 
@@ -204,112 +192,163 @@ __global__ __launch_bounds__(kThreads) void mx4_gemm_kernel(GemmArgs g) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = f32x16{};
 
-    u32x4 sc = load_scales(0);
-    keep_scales(sc, 0);
-    sc = load_scales(1);
+    u32x4 sc[L::kScaleLoads] = {};
+    if constexpr (STRAIGHT) {
+        send_scales(0);
+    } else {
+        load_scales(0, sc);
+        keep_scales(sc, 0);
+        load_scales(1, sc);
+    }
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
-        if (s < n_stage) load_stage(s);
-
-    // LDS addresses of the lane's operands in a stage
-    const uint32_t lds0 = lds_address(lds);
-    const uint32_t fold = (lane >> 2) & 3;
-    const uint32_t pa = (uint32_t)(wm * MT * 32 + l32) * 64 + ((half ^ fold) * 16);   // second step: bit 5 flipped
-    const uint32_t pb4 = L::kABytes + (uint32_t)(wn * NT * 32 + l32) * 64 + ((half ^ fold) * 16);
-    const uint32_t pb6 = L::kABytes + (uint32_t)(wn * NT * kStageBlocks + half) * kSplitRecord;
-    const uint32_t sa0 = lds0 + L::kScales + (uint32_t)(wm * MT * 32 + l32) * 16;
-    const uint32_t sb0 = lds0 + L::kScales + (uint32_t)(L::kM + wn * NT * 32 + l32) * 16;
-
-    for (int s = 0; s < n_stage; ++s) {
-        // this wave's loads of stage s have landed (those of the STAGES - 2 behind it may be in flight), and the barrier says
-        // so for all; every wave has read stage s - 1, whose place is loaded next
-        if (s + STAGES - 1 <= n_stage)
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(L::kLoads * (STAGES - 2)) : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (s + STAGES - 1 < n_stage) load_stage(s + STAGES - 1);
-        const int c = s / kScaleStages;
-        if (s % kScaleStages == kScaleStages - 1) {
-            keep_scales(sc, c + 1);
-            sc = load_scales(c + 2);
-        }
-        const uint32_t base = lds0 + s % STAGES * L::kStage;
-        const uint32_t soff = (c & 1) * L::kScaleRows * 16 + s % kScaleStages * 4;
-        uint32_t sa[MT], sb[NT];
-        read_scales(sa, sa0 + soff);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sa[i] >>= 8 * half;
+        for (int j = 0; j < L::kLoads; ++j) load(s, j);
+
+    // Places of the lane's operands in a stage, at block b ^ its row's fold.
+    const int fd = fold<KB>(l32);
+    const uint32_t pa = (uint32_t)(wm * MT * 32 + l32) * (KB * 16);
+    const uint32_t pb4 = L::kABytes + (uint32_t)(wn * NT * 32 + l32) * (KB * 16);
+    const uint32_t pb6 = L::kABytes + (uint32_t)(wn * NT * KB + half) * kSplitRecord;
+    const uint32_t psa = L::kScales + (uint32_t)(wm * MT * 32 + l32) * 16;
+    const uint32_t psb = L::kScales + (uint32_t)(L::kM + wn * NT * 32 + l32) * 16;
+
+    using Operands = StepOperands<FMT, MT, NT>;
+    using Scales = StageScales<FMT, MT, NT, KB>;
+    // Reads of step k of the stage at `st`, one of kReads.
+    constexpr int kReads = MT + NT * (FMT == kFmt4 ? 1 : kPieces + 1);
+    auto read = [&](Operands& o, const char* st, int k, int q) {
+        const int slot = ((2 * k + half) ^ fd) * 16;
+        if (q < MT) {
+            o.a[q] = *reinterpret_cast<const u32x4*>(st + pa + slot + q * 32 * KB * 16);
+        } else if constexpr (FMT == kFmt4) {
+            o.b[q - MT][0] = *reinterpret_cast<const u32x4*>(st + pb4 + slot + (q - MT) * 32 * KB * 16);
+        } else {
+            const int j = (q - MT) / (kPieces + 1), p = (q - MT) % (kPieces + 1);
+            const char* rec = st + pb6 + (j * KB + 2 * k) * kSplitRecord;
+            if (p < kPieces) {
+                const u32x4 f = *reinterpret_cast<const u32x4*>(rec + p * 512 + l32 * 16);
+                const u32x2 r = *reinterpret_cast<const u32x2*>(rec + 2048 + p * 256 + l32 * 8);
+                o.b[j][p] = u32x6{f[0], f[1], f[2], f[3], r[0], r[1]};
+            } else {
+                o.sb[j] = *reinterpret_cast<const uint32_t*>(rec + 3072 + l32 * 4);
+            }
+        }
+    };
+    auto read_scales = [&](Scales& sc, int s) {
+        const char* at = lds + (s / L::kChunkStages & 1) * L::kScaleRows * 16 + s % L::kChunkStages * KB;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int d = 0; d < KB / 4; ++d) sc.a[i][d] = *reinterpret_cast<const uint32_t*>(at + psa + i * 512 + d * 4);
         if constexpr (FMT == kFmt4) {
-            read_scales(sb, sb0 + soff);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) sb[j] >>= 8 * half;
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int d = 0; d < KB / 4; ++d) sc.b[j][d] = *reinterpret_cast<const uint32_t*>(at + psb + j * 512 + d * 4);
         }
-        const int b0 = (first + s) * kStageBlocks + half;
-        const bool whole = (first + s + 1) * kStageBlocks <= nb;   // uniform
-        auto step = [&](auto ks_const) {
-            constexpr int KS = decltype(ks_const)::value;
-            AOperand<MT> a;
-            u32x4 b4[NT], b[4];
-            u32x2 r[4];
-            uint32_t s6;
-            const uint32_t flip = KS * 32;
-            if constexpr (FMT == kFmt4) {
-                read_4(a, b4, (base + pa) ^ flip, (base + pb4) ^ flip);
-            } else {
-                const uint32_t q = base + pb6 + KS * 2 * kSplitRecord;
-                read_6(a, b, r, s6, (base + pa) ^ flip, q + l32 * 16, q + 2048 + l32 * 8, q + 3072 + l32 * 4);
-            }
-            if (!whole) {   // blocks past the row: codes 0 and scales of 1, whatever was loaded
-                const bool in_row = b0 + 2 * KS < nb;
+    };
+    auto half_scales = [&](Scales& sc) {   // byte 2 k + half to byte 2 k of word k / 2
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    a.v[i] = in_row ? a.v[i] : u32x4{0u, 0u, 0u, 0u};
-                    sa[i] = in_row ? sa[i] : 0x7f7f7f7fu;
-                }
-                if constexpr (FMT == kFmt4) {
+        for (int d = 0; d < KB / 4; ++d) {
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) sb[j] = in_row ? sb[j] : 0x7f7f7f7fu;
-                }
-            }
+            for (int i = 0; i < MT; ++i) sc.a[i][d] >>= 8 * half;
             if constexpr (FMT == kFmt4) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        acc[i][j] = mfma_mx32<kFmt4, 2 * KS, 2 * KS>(operand4(a.v[i]), operand4(b4[j]), acc[i][j], sa[i], sb[j]);
-            } else {
-                auto piece = [&](int p) { return operand6(u32x6{b[p][0], b[p][1], b[p][2], b[p][3], r[p][0], r[p][1]}); };
-#pragma unroll
-                for (int i = 0; i < MT; ++i) acc[i][0] = mfma_mx32<kFmt6, 2 * KS, 3>(operand4(a.v[i]), piece(3), acc[i][0], sa[i], s6);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) acc[i][0] = mfma_mx32<kFmt6, 2 * KS, 2>(operand4(a.v[i]), piece(2), acc[i][0], sa[i], s6);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) acc[i][0] = mfma_mx32<kFmt6, 2 * KS, 1>(operand4(a.v[i]), piece(1), acc[i][0], sa[i], s6);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) acc[i][0] = mfma_mx32<kFmt6, 2 * KS, 0>(operand4(a.v[i]), piece(0), acc[i][0], sa[i], s6);
+                for (int j = 0; j < NT; ++j) sc.b[j][d] >>= 8 * half;
             }
-        };
-        step(std::integral_constant<int, 0>{});
-        step(std::integral_constant<int, 1>{});
-    }
+        }
+    };
 
-    // Epilogue: a wave turns its squares in LDS of its own (token rows of MT * 32 floats, 16 bytes apart), and a lane finishes
-    // four neighbouring outputs of a token.
+    // acc += the products of step K, and between them what between(n) does.  Blocks past the row, whatever was loaded for them,
+    // count with scales of 2^-127 and 1: below 2^-118, which no fp16 result feels.
+    constexpr int kProducts = MT * NT * (FMT == kFmt4 ? 1 : kPieces);
+    auto multiply = [&](const Operands& o, const Scales& sc, int s, auto k_const, auto between) {
+        constexpr int K = decltype(k_const)::value;
+        const bool in_row = block0 + s * KB + half + 2 * K < nb;
+        uint32_t sa[MT], sb[NT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i) sa[i] = in_row ? sc.a[i][K / 2] : 0u;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) pin(acc[i][j]);
-    __syncthreads();
-    char* turn = lds + wave * 32 * L::kEpiRow;
-    constexpr int kQuads = MT * 8;   // lanes a token
-    const int row = m0 + wm * MT * 32 + 4 * (lane % kQuads);
-    const bool vec = g.out % 4 == 0;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (!PART && g.bias != nullptr) {
+        for (int j = 0; j < NT; ++j) sb[j] = in_row ? (FMT == kFmt4 ? sc.b[FMT == kFmt4 ? j : 0][K / 2] : o.sb[j]) : 0x7f7f7f7fu;
+        constexpr int SA = 2 * (K % 2);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (row + q < g.out) bias[q] = (float)g.bias[row + q];
+        for (int n = 0; n < kProducts; ++n) {
+            const int i = n % MT, j = n / MT % NT, p = kPieces - 1 - n / (MT * NT);   // small pieces first
+            f32x16& c = acc[i][j];
+            const i32x8 a = operand4(o.a[i]);
+            if constexpr (FMT == kFmt4) {
+                c = mfma_mx32<kFmt4, SA, SA>(a, operand4(o.b[j][0]), c, sa[i], sb[j]);
+            } else {
+                if (p == 3) c = mfma_mx32<kFmt6, SA, 3>(a, operand6(o.b[j][3]), c, sa[i], sb[j]);
+                if (p == 2) c = mfma_mx32<kFmt6, SA, 2>(a, operand6(o.b[j][2]), c, sa[i], sb[j]);
+                if (p == 1) c = mfma_mx32<kFmt6, SA, 1>(a, operand6(o.b[j][1]), c, sa[i], sb[j]);
+                if (p == 0) c = mfma_mx32<kFmt6, SA, 0>(a, operand6(o.b[j][0]), c, sa[i], sb[j]);
+            }
+            between(n);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    // This wave's loads of a stage have landed (those of the STAGES - 2 behind it may be in flight), and the barrier says so for
+    // all; every wave has read the stage before it, whose place is loaded next.  Loads go on past the last stage, unused.
+    auto arrive = [&]() { asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(L::kLoads * (STAGES - 2)) : "memory"); };
+    auto place = [&](int s) { return lds + s % STAGES * L::kStage; };
+
+    Operands o[2];
+    Scales cur, nxt;
+    arrive();
+#pragma unroll
+    for (int q = 0; q < kReads; ++q) read(o[0], place(0), 0, q);
+    read_scales(cur, 0);
+#pragma unroll
+    for (int j = 0; j < L::kLoads; ++j) load(STAGES - 1, j);
+    half_scales(cur);
+    static_assert(L::kSteps == 2 || L::kSteps == 4);
+    auto read_next = [&](Operands& to, const char* from, int k, int n) {
+#pragma unroll
+        for (int q = n * kReads / kProducts; q < (n + 1) * kReads / kProducts; ++q) read(to, from, k, q);
+    };
+    auto stage = [&](int s) {
+        using std::integral_constant;
+        multiply(o[0], cur, s, integral_constant<int, 0>{}, [&](int n) { read_next(o[1], place(s), 1, n); });
+        if constexpr (L::kSteps == 4) {
+            multiply(o[1], cur, s, integral_constant<int, 1>{}, [&](int n) { read_next(o[0], place(s), 2, n); });
+            multiply(o[0], cur, s, integral_constant<int, 2>{}, [&](int n) { read_next(o[1], place(s), 3, n); });
+        }
+        arrive();   // stage s + 1
+        read_scales(nxt, s + 1);
+        multiply(o[1], cur, s, integral_constant<int, L::kSteps - 1>{}, [&](int n) {
+            read_next(o[0], place(s + 1), 0, n);
+#pragma unroll
+            for (int j = n * L::kLoads / kProducts; j < (n + 1) * L::kLoads / kProducts; ++j) load(s + STAGES, j);
+        });
+        cur = nxt;
+        half_scales(cur);
+    };
+    for (int c = 0; c * L::kChunkStages < n_stage; ++c) {
+        // the scales of the chunk after this one: their place was last read in the chunk before it
+        if constexpr (STRAIGHT) {
+            send_scales(c + 1);
+        } else {
+            keep_scales(sc, c + 1);
+            load_scales(c + 2, sc);
+        }
+#pragma unroll
+        for (int t = 0; t < L::kChunkStages; ++t) {
+            if (t > 0 && c * L::kChunkStages + t >= n_stage) break;
+            stage(c * L::kChunkStages + t);
+        }
     }
+    // nothing is on its way into LDS, and nobody reads the stages
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    char* const turn = lds + wave * 32 * L::kEpiRow;
+    constexpr int kLanes = MT * 4;   // a token
+    const int row = m0 + wm * MT * 32 + 8 * (lane % kLanes), left = g.out - row;
+    const bool vec = g.out % 8 == 0;
+    float bias[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) bias[q] = !PART && g.bias != nullptr && q < left ? (float)g.bias[row + q] : 0.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -319,32 +358,36 @@ __global__ __launch_bounds__(kThreads) void mx4_gemm_kernel(GemmArgs g) {
                 *reinterpret_cast<f32x4*>(turn + l32 * L::kEpiRow + (i * 32 + 8 * q + 4 * half) * 4) =
                     f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int t0 = 0; t0 < 32; t0 += 64 / kQuads) {
-            const int t = t0 + lane / kQuads, token = n0 + (wn * NT + j) * 32 + t;
-            const f32x4 z = *reinterpret_cast<const f32x4*>(turn + t * L::kEpiRow + (lane % kQuads) * 16);
-            if (token >= g.T) continue;
+        const char* from = turn + lane / kLanes * L::kEpiRow + (lane % kLanes) * 32;
+        int token = n0 + (wn * NT + j) * 32 + lane / kLanes;
+#pragma unroll 1
+        for (int t = 0; t < 32; t += 64 / kLanes, token += 64 / kLanes, from += 64 / kLanes * L::kEpiRow) {
+            const f32x4 z0 = *reinterpret_cast<const f32x4*>(from), z1 = *reinterpret_cast<const f32x4*>(from + 16);
+            if (token >= g.T || left <= 0) continue;
             if constexpr (PART) {
-                if (row < g.op) *reinterpret_cast<f32x4*>(g.part + ((size_t)split * g.T + token) * g.op + row) = z;
+                float* to = g.part + ((size_t)split * g.T + token) * g.op + row;
+                *reinterpret_cast<f32x4*>(to) = z0;
+                if (left > 4) *reinterpret_cast<f32x4*>(to + 4) = z1;
             } else {
-                if (row >= g.out) continue;
-                float v[4];
+                float v[8];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = z[q] + bias[q];
+                for (int q = 0; q < 8; ++q) v[q] = (q < 4 ? z0[q & 3] : z1[q & 3]) + bias[q];
                 act_values(g.act, v);
                 const size_t at = (size_t)token * g.out + row;
-                typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
                 if (vec) {
                     if (g.residual != nullptr) {
-                        const f16x4 res = *reinterpret_cast<const f16x4*>(g.residual + at);
+                        const f16x8 res = as_f16x8(load16(g.residual + at));
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] += (float)res[q];
+                        for (int q = 0; q < 8; ++q) v[q] += (float)res[q];
                     }
-                    *reinterpret_cast<f16x4*>(g.y + at) = f16x4{(f16)v[0], (f16)v[1], (f16)v[2], (f16)v[3]};
+                    f16x8 y;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) y[q] = (f16)v[q];
+                    *reinterpret_cast<u32x4*>(g.y + at) = as_u32x4(y);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (row + q < g.out) {
+                    for (int q = 0; q < 8; ++q) {
+                        if (q < left) {
                             if (g.residual != nullptr) v[q] += (float)g.residual[at + q];
                             g.y[at + q] = (f16)v[q];
                         }
@@ -361,23 +404,44 @@ struct GemmPlan {
     int tiles_m, tiles_n, splits;
 };
 
-template <int FMT, int WM, int WN, int MT, int NT, int STAGES>
-hipError_t launch_tile(GemmArgs& g, hipStream_t stream) {
-    using L = Tile<FMT, WM, WN, MT, NT, STAGES>;
+template <int FMT, int WM, int WN, int MT, int NT, int KB, int STAGES, bool PART>
+hipError_t launch_tile(GemmArgs& g, bool straight, hipStream_t stream) {
+    using L = Tile<FMT, WM, WN, MT, NT, KB, STAGES>;
     g.tiles_m = (g.out + L::kM - 1) / L::kM;
     g.tiles_n = (g.T + L::kN - 1) / L::kN;
-    auto kern = g.splits > 1 ? mx4_gemm_kernel<FMT, WM, WN, MT, NT, STAGES, true> : mx4_gemm_kernel<FMT, WM, WN, MT, NT, STAGES, false>;
+    auto kern = straight ? mx4_gemm_kernel<FMT, WM, WN, MT, NT, KB, STAGES, PART, true>
+                         : mx4_gemm_kernel<FMT, WM, WN, MT, NT, KB, STAGES, PART, false>;
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n * g.splits)), dim3(kThreads), L::kLds, stream, g);
+    hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n * g.splits)), dim3(L::kThreads), L::kLds, stream, g);
     return hipGetLastError();
+}
+
+#ifndef BIG4
+#define BIG4 2, 4, 4, 2, 8, 2
+#endif
+#ifndef BIG6
+#define BIG6 2, 2, 4, 2, 4, 2
+#endif
+
+template <int FMT>
+hipError_t launch_plan(const GemmPlan& p, GemmArgs& g, hipStream_t stream) {
+    // scales in 16-byte pieces that start on 16 bytes
+    const bool straight = g.nb % kChunkBlocks == 0 && (uintptr_t)g.ws % 16 == 0 && (uintptr_t)g.xs % 16 == 0;
+    if (p.big) {
+        if constexpr (FMT == kFmt4) return launch_tile<FMT, BIG4, false>(g, straight, stream);
+        else return launch_tile<FMT, BIG6, false>(g, straight, stream);
+    }
+    constexpr int kStages = FMT == kFmt4 ? 4 : 2;
+    return p.splits > 1 ? launch_tile<FMT, 2, 4, 2, 1, 4, kStages, true>(g, straight, stream)
+                        : launch_tile<FMT, 2, 4, 2, 1, 4, kStages, false>(g, straight, stream);
 }
 
 int64_t round4(int64_t v) { return (v + 3) / 4 * 4; }
 
 // The small tile (128 x 128) and how many parts of the sum fill the chip with it.
 constexpr int kSmall = 128, kWant = 512;
-int max_splits(int64_t in) { return (int)std::max<int64_t>(1, in / (2 * kScaleStages * kStageBlocks * kMxBlock)); }
+int max_splits(int64_t in) { return (int)std::max<int64_t>(1, in / (2 * kChunkBlocks * kMxBlock)); }
 
 GemmPlan gemm_plan(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
     const int64_t big_n = x_mx4 ? 256 : 128;
@@ -389,12 +453,8 @@ GemmPlan gemm_plan(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     p.splits = p.big ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(max_splits(in), 256 / tiles));
     // no empty part
-    const int64_t stages = (in / kMxBlock + kStageBlocks - 1) / kStageBlocks;
-    while (p.splits > 1) {
-        const int64_t per = ((stages + p.splits - 1) / p.splits + kScaleStages - 1) / kScaleStages * kScaleStages;
-        if (per * (p.splits - 1) < stages) break;
-        --p.splits;
-    }
+    const int64_t chunks = (in / kMxBlock + kChunkBlocks - 1) / kChunkBlocks;
+    while (p.splits > 1 && (chunks + p.splits - 1) / p.splits * (p.splits - 1) >= chunks) --p.splits;
     return p;
 }
 
@@ -428,10 +488,8 @@ hipError_t launch_mx4_gemm(const void* codes, const void* scales, MxInput x, con
     g.nb = (int)(in / kMxBlock);
     g.op = (int)round4(out);
     g.splits = p.splits;
-    g.stages = (g.nb + kStageBlocks - 1) / kStageBlocks;
-    hipError_t r;
-    if (x.scales != nullptr) r = p.big ? launch_tile<kFmt4, 2, 4, 4, 2, 4>(g, stream) : launch_tile<kFmt4, 2, 4, 2, 1, 4>(g, stream);
-    else r = p.big ? launch_tile<kFmt6, 2, 4, 4, 1, 2>(g, stream) : launch_tile<kFmt6, 2, 4, 2, 1, 2>(g, stream);
+    g.chunks = (g.nb + kChunkBlocks - 1) / kChunkBlocks;
+    const hipError_t r = x.scales != nullptr ? launch_plan<kFmt4>(p, g, stream) : launch_plan<kFmt6>(p, g, stream);
     if (r != hipSuccess || p.splits == 1) return r;
     return launch_finish(1, g.part, nullptr, e, out, g.op, batch, p.splits, BiasSum{}, stream);
 }
