@@ -112,9 +112,14 @@ __global__ __launch_bounds__(WM* WN * 64) void mx4_gemm_kernel(GemmArgs g) {
     char* lds = reinterpret_cast<char*>(smem);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int l32 = lane & 31, half = lane >> 5;
-    // tokens fastest: an XCD's workgroups share rows of W
-    const int u = xcd_run((int)blockIdx.x, (int)gridDim.x);
-    const int n0 = u % g.tiles_n * L::kN, m0 = u / g.tiles_n % g.tiles_m * L::kM, split = u / g.tiles_n / g.tiles_m;
+    // An XCD's workgroups are neighbours in an order of kBand token tiles next to each other, row tile after row tile: what
+    // 32 of them read in a stage is then about as little as it can be (x in pieces: 4 x 51 KB and 8 x 16 KB, where all
+    // 16 token tiles of 2048 tokens would make 850 KB), and comes out of the XCD's L2 when it is shared.
+    constexpr int kBand = FMT == kFmt4 ? 8 : 4;
+    const int tiles = g.tiles_m * g.tiles_n, u = xcd_run((int)blockIdx.x, (int)gridDim.x), split = u / tiles;
+    const int band = u % tiles / (kBand * g.tiles_m), in_band = u % tiles - band * kBand * g.tiles_m;
+    const int width = min(kBand, g.tiles_n - band * kBand);
+    const int n0 = (band * kBand + in_band % width) * L::kN, m0 = in_band / width * L::kM;
     const int nb = g.nb;
     const int per = (g.chunks + g.splits - 1) / g.splits;               // chunks of a part
     const int block0 = split * per * kChunkBlocks, blocks = min(per * kChunkBlocks, nb - block0);
