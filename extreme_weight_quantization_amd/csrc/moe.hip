@@ -55,12 +55,13 @@ __global__ __launch_bounds__(kGemvThreads) void moe_gemv_kernel(MoeProduct p) {
     __shared__ MoeLds m;
     constexpr int kChunk = moe_chunk(KIND);
     constexpr int kTile = gemv_gated(KIND) ? kRowTile / 2 : kRowTile;
-    const int n = moe_items<kChunk>(p.ids, p.pairs, p.experts, m);
+    const MoeItems items = moe_items<kChunk>(p.ids, p.pairs, p.experts, m);
+    const int n = items.n;
     const int tiles = (p.rows + kTile - 1) / kTile;
     const int parts = moe_parts(n, (int)gridDim.x, tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
-        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(u / parts, p.k, p.weights, m);
-        const int e = __builtin_amdgcn_readfirstlane(m.expert);
+        int e;
+        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, p.weights, m, e);
         gemv_body<SCHEME, REPL, VEC, kRtp, XM, KIND>(
             p.codes[0] + p.codes_stride * e, p.codebooks[0] + p.codebooks_stride * e, p.scales[0] + (size_t)p.rows * e, p.h, p.rows,
             u % parts, parts, p.x, p.in, KIND == kGemvPartAt ? 2 * cols : cols, expert_epi<KIND>(p, e),
@@ -114,11 +115,12 @@ __global__ __launch_bounds__(kGemvThreads) void moe_generic_kernel(MoeProduct p,
     const uint32_t mask = (1u << B) - 1u;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n_grp = p.in / G;
-    const int n = moe_items<kChunk>(p.ids, p.pairs, p.experts, m);
+    const MoeItems items = moe_items<kChunk>(p.ids, p.pairs, p.experts, m);
+    const int n = items.n;
     const int parts = moe_parts(n, (int)gridDim.x, (p.rows + 15) / 16, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
-        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(u / parts, p.k, p.weights, m);
-        const int e = __builtin_amdgcn_readfirstlane(m.expert);
+        int e;
+        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, p.weights, m, e);
         const GemvEpi epi = expert_epi<KIND>(p, e);
         const f16* scales = p.scales[0] + (size_t)p.rows * e;
         for (int row = u % parts * 16 + wave; row < p.rows; row += parts * 16) {
@@ -214,11 +216,21 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
                                                           const f16* residual, f16* y, int n, int in, int k, int experts) {
     const int at = (int)blockIdx.x * 256 + (int)threadIdx.x;
     if (at >= n) return;
+    constexpr int kStep = 8;
     const int t = at / in, i = at % in;
     float s = 0.f;
-    for (int j = 0; j < k; ++j) {
-        const int e = ids[t * k + j];
-        if (e >= 0 && e < experts) s += part[(size_t)(t * k + j) * in + i];
+    for (int j0 = 0; j0 < k; j0 += kStep) {   // kStep loads in flight
+        int e[kStep];
+        float v[kStep];
+#pragma unroll
+        for (int q = 0; q < kStep; ++q) {
+            const size_t pair = (size_t)t * k + min(j0 + q, k - 1);
+            e[q] = ids[pair];
+            v[q] = part[pair * in + i];
+        }
+#pragma unroll
+        for (int q = 0; q < kStep; ++q)   // a pair without an expert has no part: whatever is there is left out
+            if (j0 + q < k && e[q] >= 0 && e[q] < experts) s += v[q];
     }
     if (residual != nullptr) s += (float)residual[at];
     y[at] = (f16)s;

@@ -2,7 +2,8 @@
 //
 // A tile of 16 matrix-core rows is 8 rows of gate and the same 8 of up (lanes with l % 16 < 8: gate), so that one
 // workgroup has both halves of h = act(zg) zu; four neighbouring tiles are one block of 32 hidden values, which goes
-// to the down product in the four-piece form of mx4.h, from fp32: it is rounded by 2^-19 of the block's largest only.
+// to the down product in the four-piece form of mx4.h, from fp32: it is rounded by 2^-19 of the block's largest only.  The
+// splitting takes a thread some 2000 clocks a block, so up to 8 blocks wait for it in LDS.
 #include <algorithm>
 
 #include "act_math.h"
@@ -15,6 +16,7 @@ namespace aqlm {
 namespace {
 
 constexpr int kMxMoeNk = 4, kCols = 16, kHalf = kMxRows / 2;
+constexpr int kHold = 8;   // blocks of hidden values that wait to be split together, a thread a column
 
 struct MoeMxProduct {
     const uint8_t* codes[2];
@@ -33,14 +35,16 @@ template <bool GATED>
 __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
     __shared__ MoeLds m;
     __shared__ float red[mx4_red_floats(1)];
-    __shared__ float hb[kCols][kMxBlock + 1];
+    __shared__ float hb[kHold][kCols][kMxBlock + 1];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
-    const int n = moe_items<kCols>(p.ids, p.pairs, p.experts, m);
+    const MoeItems items = moe_items<kCols>(p.ids, p.pairs, p.experts, m);
+    const int n = items.n;
     const int tiles = GATED ? (p.rows + kHalf - 1) / kHalf : (p.rows + kMxRows - 1) / kMxRows;
     const int parts = moe_parts(n, (int)gridDim.x, GATED ? (tiles + kMxTiles - 1) / kMxTiles : tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
-        const int cols = moe_item<kCols, false>(u / parts, p.k, p.weights, m);
-        const size_t row0 = (size_t)p.rows * __builtin_amdgcn_readfirstlane(m.expert) * p.st.nb;   // the expert's first block
+        int e;
+        const int cols = moe_item<kCols, false>(items, u / parts, p.k, p.weights, m, e);
+        const size_t row0 = (size_t)p.rows * e * p.st.nb;   // the expert's first block
         const int r16 = lane & 15, layer = GATED && r16 >= kHalf;
         const uint8_t* wq = (layer ? p.codes[1] : p.codes[0]) + row0 * kMxBlockBytes;
         const uint8_t* ws = (layer ? p.scales[1] : p.scales[0]) + row0;
@@ -51,31 +55,35 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
         mx4_body<1, kMxMoeNk, kFmt6, GATED>(
             wq, ws, xin, xrow, p.st, part, parts, tiles, red,
             [&](int tile) { return min(GATED ? tile * kHalf + (r16 & (kHalf - 1)) : tile * kMxRows + r16, p.rows - 1); },
-            [&](int t0, auto sum) {
+            [&]() {},
+            [&](int t0, int nt, auto sum) {
                 if constexpr (GATED) {
+                    const int slot = (t0 / kMxTiles - part) / parts % kHold;   // blocks part, part + parts, ...
                     for (int idx = tid; idx < cols * kMxBlock; idx += kMxThreads) {   // rows is a multiple of 32: whole blocks
                         const int c = idx / kMxBlock, i = idx % kMxBlock;
                         float v[1] = {sum(i / kHalf, c, i % kHalf)};
                         act_values(p.act, v);
-                        hb[c][i] = v[0] * sum(i / kHalf, c, i % kHalf + kHalf);
+                        hb[slot][c][i] = v[0] * sum(i / kHalf, c, i % kHalf + kHalf);
                     }
+                    if (slot + 1 < kHold && t0 + parts * kMxTiles < tiles) return;
                     __syncthreads();
-                    if (tid < cols) {
+                    if (tid < (slot + 1) * cols) {
+                        const int q = tid / cols, c = tid - q * cols;
                         f32x16 even, odd;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            even[i] = hb[tid][2 * i];
-                            odd[i] = hb[tid][2 * i + 1];
+                            even[i] = hb[q][c][2 * i];
+                            odd[i] = hb[q][c][2 * i + 1];
                         }
                         uint32_t o[kSplitDwords], s;
                         split_block32(even, odd, o, s);
-                        store_split(SplitRows{p.h, kSplitTokens, p.rows / kMxBlock}, m.y[tid], t0 / kMxTiles, o, s);
+                        store_split(SplitRows{p.h, kSplitTokens, p.rows / kMxBlock}, m.y[c], t0 / kMxTiles - (slot - q) * parts, o, s);
                     }
                 } else {
-                    for (int idx = tid; idx < kMxTiles * cols * kMxRows; idx += kMxThreads) {
-                        const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, c = ic % cols;
-                        const int tile = t0 + i * parts, row = tile * kMxRows + r;
-                        if (tile < tiles && row < p.rows)
+                    for (int idx = tid; idx < nt * cols * kMxRows; idx += kMxThreads) {
+                        const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, c = ic - i * cols;
+                        const int row = (t0 + i * parts) * kMxRows + r;
+                        if (row < p.rows)
                             p.part[(size_t)m.y[c] * p.rows + row] = sum(i, c, r) * m.w[c];
                     }
                 }

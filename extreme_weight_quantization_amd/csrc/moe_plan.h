@@ -26,10 +26,38 @@ struct MoeLds {
     float w[16];                     // weights of the pairs
 };
 
-// Sorts the pairs; the number of items.  All threads of the workgroup (at least 512) call it.  A pair whose id is no
+// What a workgroup knows about the items.  few: no more pairs than an item takes, so every expert that is asked for is one item;
+// lane p of each wave then holds pair p: its expert, the pairs of the same expert, and (all lanes) the first pair of each expert.
+struct MoeItems {
+    int n;
+    bool few;
+    uint32_t expert;
+    uint64_t same, firsts;
+};
+
+// The lanes whose e equals this lane's, by a vote on each of its bits, among those with an expert.
+__device__ __forceinline__ uint64_t same_expert(uint32_t e) {
+    uint64_t same = __ballot(e != kMoeNone);
+#pragma unroll
+    for (int b = 0; b < kMoeIdBits; ++b) {
+        const uint64_t set = __ballot((e >> b) & 1u);
+        same &= (e >> b) & 1u ? set : ~set;
+    }
+    return same;
+}
+
+// Sorts the pairs.  All threads of the workgroup (at least 512) call it.  A pair whose id is no
 // expert is left out.  An expert's pairs stay in their order: workgroups that take parts of one item must agree on its pairs.
 template <int CHUNK>
-__device__ __forceinline__ int moe_items(const int32_t* __restrict__ ids, int pairs, int experts, MoeLds& m) {
+__device__ __forceinline__ MoeItems moe_items(const int32_t* __restrict__ ids, int pairs, int experts, MoeLds& m) {
+    if (pairs <= CHUNK) {
+        const int lane = threadIdx.x & (kWave - 1);
+        const int id = ids[min(lane, pairs - 1)];
+        const uint32_t e = lane < pairs && id >= 0 && id < experts ? (uint32_t)id : kMoeNone;
+        const uint64_t same = same_expert(e);
+        const uint64_t firsts = __ballot(e != kMoeNone && __builtin_ctzll(same | 1ull << 63) == lane);
+        return MoeItems{(int)__popcll(firsts), true, e, same, firsts};
+    }
     const int tid = threadIdx.x, n = blockDim.x;
     if (tid < kMoeMaxExperts) m.count[tid] = 0;
     for (int p = tid; p < pairs; p += n) {
@@ -42,12 +70,7 @@ __device__ __forceinline__ int moe_items(const int32_t* __restrict__ ids, int pa
         for (int p0 = 0; p0 < pairs; p0 += kWave) {
             const int p = p0 + tid;
             const uint32_t e = p < pairs ? m.id[p] : kMoeNone;
-            uint64_t same = __ballot(e != kMoeNone);
-#pragma unroll
-            for (int b = 0; b < kMoeIdBits; ++b) {
-                const uint64_t set = __ballot((e >> b) & 1u);
-                same &= (e >> b) & 1u ? set : ~set;
-            }
+            const uint64_t same = same_expert(e);
             if (e != kMoeNone) {
                 const int before = m.count[e];
                 m.rank[p] = (uint16_t)(before + __popcll(same & ((1ull << tid) - 1ull)));
@@ -89,7 +112,7 @@ __device__ __forceinline__ int moe_items(const int32_t* __restrict__ ids, int pa
         if (e != kMoeNone) m.pair[m.start[e] + m.rank[p]] = (uint16_t)p;
     }
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane(m.item0[kMoeMaxExperts]);
+    return MoeItems{__builtin_amdgcn_readfirstlane(m.item0[kMoeMaxExperts]), false, 0u, 0ull, 0ull};
 }
 
 // Parts an item is cut into: `rounds` rounds of `wgs` workgroups take n * parts <= rounds * wgs units, each 1 / parts of an
@@ -109,26 +132,41 @@ __device__ __forceinline__ int moe_parts(int n, int wgs, int most, float fixed) 
     return best;
 }
 
-// Makes item v the one at hand: m.expert, and m.x (rows of the input), m.y (pairs), m.w (weights) for its pairs; returns how many there are.  PAIRED: the
-// input has two rows for a pair (2 pair, 2 pair + 1), else one for its token.  Ends with a barrier.
+// Makes item v the one at hand: its expert e, and m.x (rows of the input), m.y (pairs), m.w (weights) for its pairs; returns how
+// many there are.  PAIRED: the input has two rows for a pair (2 pair, 2 pair + 1), else one for its token.  Ends with a barrier.
 template <int CHUNK, bool PAIRED>
-__device__ __forceinline__ int moe_item(int v, int k, const float* __restrict__ weights, MoeLds& m) {
+__device__ __forceinline__ int moe_item(const MoeItems& items, int v, int k, const float* __restrict__ weights, MoeLds& m, int& e) {
     const int tid = threadIdx.x;
+    int n, place = 0, p = 0;   // this thread's pair, if place < n
     __syncthreads();
-    if (tid < kMoeMaxExperts && m.item0[tid] <= v && v < m.item0[tid + 1]) m.expert = tid;
-    __syncthreads();
-    const int e = __builtin_amdgcn_readfirstlane(m.expert);
-    const int at = m.start[e] + (v - m.item0[e]) * CHUNK;
-    const int n = min(CHUNK, m.start[e + 1] - at);
-    if (tid < n) {
-        const int p = m.pair[at + tid];
-        m.y[tid] = (uint16_t)p;
-        m.w[tid] = weights[p];
+    if (items.few) {
+        const int lane = tid & (kWave - 1);
+        const uint64_t below = (1ull << lane) - 1ull;
+        const uint64_t first = __ballot((items.firsts >> lane & 1ull) && __popcll(items.firsts & below) == v);
+        const int l = __builtin_ctzll(first);
+        e = __builtin_amdgcn_readlane((int)items.expert, l);
+        const uint64_t same = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(items.same >> 32), l) << 32 |
+                              (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)items.same, l);
+        n = __popcll(same);
+        p = lane;
+        place = tid < kWave && (same >> lane & 1ull) ? __popcll(same & below) : n;
+    } else {
+        if (tid < kMoeMaxExperts && m.item0[tid] <= v && v < m.item0[tid + 1]) m.expert = tid;
+        __syncthreads();
+        e = __builtin_amdgcn_readfirstlane(m.expert);
+        const int at = m.start[e] + (v - m.item0[e]) * CHUNK;
+        n = min(CHUNK, m.start[e + 1] - at);
+        place = tid;
+        if (tid < n) p = m.pair[at + tid];
+    }
+    if (place < n) {
+        m.y[place] = (uint16_t)p;
+        m.w[place] = weights[p];
         if constexpr (PAIRED) {
-            m.x[2 * tid] = (uint16_t)(2 * p);
-            m.x[2 * tid + 1] = (uint16_t)(2 * p + 1);
+            m.x[2 * place] = (uint16_t)(2 * p);
+            m.x[2 * place + 1] = (uint16_t)(2 * p + 1);
         } else {
-            m.x[tid] = (uint16_t)(p / k);
+            m.x[place] = (uint16_t)(p / k);
         }
     }
     __syncthreads();

@@ -19,7 +19,7 @@ namespace {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kTile = 16, kWaves = 4, kStep = 32;
+constexpr int kTile = 16, kWaves = 4, kStep = 32, kAhead = 4;
 
 __global__ __launch_bounds__(kWaves* kWave) void route_logits_kernel(const f16* __restrict__ x, const f16* __restrict__ r,
                                                                      double* __restrict__ part, int in, int T, int E,
@@ -33,14 +33,26 @@ __global__ __launch_bounds__(kWaves* kWave) void route_logits_kernel(const f16* 
     const f16* rr = r + (size_t)min(e0 + (lane & 15), E - 1) * in;
     const f16* xr = x + (size_t)min(t0 + (lane & 15), T - 1) * in;
     f64x4 acc = {0., 0., 0., 0.};
-    for (int s = split * kWaves + wave; s < steps; s += splits * kWaves) {
-        const int k = s * kStep + 8 * (lane >> 4);
-        const int at = min(k, in - 8);   // in % 8 == 0: a lane's 8 inputs are inside or outside together
-        f16x8 a = as_f16x8(load16(rr + at)), b = as_f16x8(load16(xr + at));
-        a = k < in ? a : f16x8{};
-        b = k < in ? b : f16x8{};
+    const int stride = splits * kWaves;
+    for (int s0 = split * kWaves + wave; s0 < steps; s0 += kAhead * stride) {   // kAhead steps' loads in flight
+        f16x8 a[kAhead], b[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)a[i], (double)b[i], acc, 0, 0, 0);
+        for (int q = 0; q < kAhead; ++q) {
+            const int at = min((s0 + q * stride) * kStep + 8 * (lane >> 4), in - 8);
+            a[q] = as_f16x8(load16(rr + at));
+            b[q] = as_f16x8(load16(xr + at));
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            // in % 8 == 0: a lane's 8 inputs are inside or outside together
+            const bool in_row = (s0 + q * stride) * kStep + 8 * (lane >> 4) < in;
+            a[q] = in_row ? a[q] : f16x8{};
+            b[q] = in_row ? b[q] : f16x8{};
+            if (s0 + q * stride >= steps) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)a[q][i], (double)b[q][i], acc, 0, 0, 0);
+        }
     }
     // lane l holds rows l / 16 + 4 i of column l % 16
 #pragma unroll
@@ -100,12 +112,21 @@ __global__ __launch_bounds__(kWaves* kWave) void route_pick_kernel(const double*
     double v[N];
     uint64_t key[N];
     const double kInf = __builtin_inf();
+    constexpr int kParts = N == 1 ? 8 : 4;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const int e = lane + 64 * j;
         v[j] = e < E ? 0. : -kInf;
-        if (e < E)
-            for (int s = 0; s < splits; ++s) v[j] += part[((size_t)s * T + t) * E + e];
+        if (e < E) {
+            for (int s0 = 0; s0 < splits; s0 += kParts) {   // kParts loads in flight
+                double d[kParts];
+#pragma unroll
+                for (int s = 0; s < kParts; ++s) d[s] = part[((size_t)min(s0 + s, splits - 1) * T + t) * E + e];
+#pragma unroll
+                for (int s = 0; s < kParts; ++s)
+                    if (s0 + s < splits) v[j] += d[s];
+            }
+        }
         key[j] = e < E ? rank_key(v[j]) : 0ull;
     }
     if (score == kScoreSoftmax) {
@@ -169,11 +190,12 @@ __global__ __launch_bounds__(kWaves* kWave) void route_pick_kernel(const double*
 }
 
 // Workgroups that fill the chip, by splitting the sums of small batches.
-constexpr int kWantTiles = 512;
+constexpr int kWantTiles = 128;
 struct RoutePlan {
     int tiles_e, tiles_t, splits;
 };
-int max_splits(int64_t in) { return (int)std::max<int64_t>(1, in / (kStep * kWaves)); }
+constexpr int kMaxSplits = 8;   // each a load more for the pick
+int max_splits(int64_t in) { return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, in / (kStep * kWaves))); }
 RoutePlan route_plan(int64_t experts, int64_t in, int64_t tokens) {
     RoutePlan p;
     p.tiles_e = (int)((experts + kTile - 1) / kTile);

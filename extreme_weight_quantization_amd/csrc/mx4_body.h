@@ -93,13 +93,14 @@ struct MxOperand {
 };
 
 // row_of(tile): this lane's row of the tile inside wq / ws, which are the lane's own layer (clamped into it).
-// fin(t0, sum): called by all threads of the workgroup once per group, after a barrier: tiles t0 + i step, step 1 with RUN, else
-// nwg; sum(i, col, r) adds the waves' partial products of matrix-core row r and column col of the i-th.
-template <int CT, int NK, int FMT, bool RUN, class RowOf, class Fin>
+// prepare(): called once the first codes are on their way; what the activations wait for.
+// fin(t0, n, sum): called by all threads of the workgroup once per group, after a barrier: tiles t0 + i step for i < n, step 1
+// with RUN, else nwg; sum(i, col, r) adds the waves' partial products of matrix-core row r and column col of the i-th.
+template <int CT, int NK, int FMT, bool RUN, class RowOf, class Prepare, class Fin>
 __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws,
                                          const MxInputRows<FMT>& xin, const int (&xrow)[CT], const MxSteps st,
                                          const int bid, const int nwg, const int n_tiles, float* red, RowOf row_of,
-                                         Fin fin) {
+                                         Prepare prepare, Fin fin) {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int q = lane >> 4;
@@ -135,6 +136,7 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
 #pragma unroll
     for (int i = 0; i < kMxTiles; ++i)
         if (begin + i * step < n_tiles) load_tile(i, begin + i * step, 0);
+    prepare();
     load_x(0);
 
     for (int t0 = begin; t0 < n_tiles; t0 += nwg * kMxTiles) {
@@ -170,12 +172,17 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
 #pragma unroll
         for (int i = 0; i < kMxTiles; ++i)
 #pragma unroll
+            for (int t = 0; t < CT; ++t) pin(acc[i][t]);
+        const int left = (n_tiles - t0 + step - 1) / step;   // tiles of this group
+#pragma unroll
+        for (int i = 0; i < kMxTiles; ++i)
+#pragma unroll
             for (int t = 0; t < CT; ++t) {
-                pin(acc[i][t]);
+                if (i >= left) continue;
                 *reinterpret_cast<f32x4*>(red + ((i * kMxWaves + wave) * CT + t) * 256 + (lane & 15) * kMxRows + 4 * q) = acc[i][t];
             }
         __syncthreads();
-        fin(t0, [&](int i, int col, int r) {
+        fin(t0, min(left, kMxTiles), [&](int i, int col, int r) {
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < kMxWaves; ++w) s += red[(i * kMxWaves + w) * CT * 256 + col * kMxRows + r];

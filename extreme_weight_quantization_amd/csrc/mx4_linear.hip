@@ -47,24 +47,39 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
         xin = {static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(xs), st.nb};
     } else if constexpr (INLINE) {
         xin.rows = SplitRows{reinterpret_cast<char*>(red + mx4_red_floats(CT)), T, st.nb};
-        for (int i = threadIdx.x; i < T * st.nb; i += kMxThreads) {
-            uint32_t o[kSplitDwords], s;
-            split_block(load_block16(static_cast<const f16*>(x) + (size_t)i * kMxBlock), o, s);
-            store_split(xin.rows, i / st.nb, i % st.nb, o, s);
-        }
-        __syncthreads();
     } else {
         xin.rows = SplitRows{static_cast<char*>(const_cast<void*>(x)), kSplitTokens, st.nb};
+    }
+    // Blocks that this thread splits, asked for in front of the first codes: loads come back in order.
+    constexpr int kMine = INLINE ? kInlineBlocks / kMxThreads : 1;
+    f16x32 mine[kMine];
+    if constexpr (INLINE) {
+#pragma unroll
+        for (int q = 0; q < kMine; ++q)
+            mine[q] = load_block16(static_cast<const f16*>(x) + (size_t)min((int)threadIdx.x + q * kMxThreads, T * st.nb - 1) * kMxBlock);
     }
     const int nwg = (int)gridDim.x;
     mx4_body<CT, NK, FMT, false>(
         codes, scales, xin, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
         [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); },
-        [&](int t0, auto sum) {
-            for (int idx = threadIdx.x; idx < kMxTiles * cols * kMxRows; idx += kMxThreads) {
-                const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, col = ic % cols;
+        [&]() {
+            if constexpr (INLINE) {
+#pragma unroll
+                for (int q = 0; q < kMine; ++q) {
+                    const int i = threadIdx.x + q * kMxThreads;
+                    if (i >= T * st.nb) break;
+                    uint32_t o[kSplitDwords], s;
+                    split_block(mine[q], o, s);
+                    store_split(xin.rows, i / st.nb, i % st.nb, o, s);
+                }
+                __syncthreads();
+            }
+        },
+        [&](int t0, int n, auto sum) {
+            for (int idx = threadIdx.x; idx < n * cols * kMxRows; idx += kMxThreads) {
+                const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, col = ic - i * cols;
                 const int row = (t0 + i * nwg) * kMxRows + r;
-                if (t0 + i * nwg >= n_tiles || row >= out) continue;
+                if (row >= out) continue;
                 float v[1] = {sum(i, col, r)};
                 if (e.bias != nullptr) v[0] += (float)e.bias[row];
                 act_values(e.act, v);
