@@ -167,7 +167,7 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
                     if (tn + i * step < n_tiles) load_tile(i, tn + i * step, cn);
                 }
             }
-            if (st.chunks > 1) load_x(cn);
+            if (st.chunks > 1 && tn < n_tiles) load_x(cn);
         }
 #pragma unroll
         for (int i = 0; i < kMxTiles; ++i)

@@ -103,7 +103,7 @@ hipError_t launch_rows_v(const RowsCall& c) {
     auto kern = mx4_rows_kernel<CT, NK, FMT, INLINE>;
     const MxSteps st = mx4_steps(c.in, NK);
     const size_t lds = mx4_red_floats(CT) * sizeof(float) +
-                       (INLINE ? (size_t)c.T * st.nb * kSplitTokenBytes : 0);
+                       (INLINE ? (size_t)SplitRows::record_bytes(c.T) * st.nb : 0);
     if (lds > 65536) {
         const hipError_t r = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (r != hipSuccess) return r;
