@@ -16,6 +16,7 @@ namespace aqlm {
 namespace {
 
 constexpr int kMxMoeNk = 4, kCols = 16, kHalf = kMxRows / 2;
+constexpr int kDownTiles = 3;   // a fourth would not fit the registers
 constexpr int kHold = 8;   // blocks of hidden values that wait to be split together, a thread a column
 
 struct MoeMxProduct {
@@ -40,7 +41,7 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
     const MoeItems items = moe_items<kCols>(p.ids, p.pairs, p.experts, m);
     const int n = items.n;
     const int tiles = GATED ? (p.rows + kHalf - 1) / kHalf : (p.rows + kMxRows - 1) / kMxRows;
-    const int parts = moe_parts(n, (int)gridDim.x, GATED ? (tiles + kMxTiles - 1) / kMxTiles : tiles, p.fixed);
+    const int parts = moe_parts(n, (int)gridDim.x, GATED ? (tiles + 3) / 4 : tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
         const int cols = moe_item<kCols, false>(items, u / parts, p.k, p.weights, m, e);
@@ -52,42 +53,50 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
         const int xrow[1] = {GATED ? (int)m.x[col] : (int)m.y[col]};
         const int part = u % parts;
         const MxInputRows<kFmt6> xin = {SplitRows{p.x, kSplitTokens, p.st.nb}};
-        mx4_body<1, kMxMoeNk, kFmt6, GATED>(
-            wq, ws, xin, xrow, p.st, part, parts, tiles, red,
-            [&](int tile) { return min(GATED ? tile * kHalf + (r16 & (kHalf - 1)) : tile * kMxRows + r16, p.rows - 1); },
-            [&]() {},
-            [&](int t0, int nt, auto sum) {
-                if constexpr (GATED) {
-                    const int slot = (t0 / kMxTiles - part) / parts % kHold;   // blocks part, part + parts, ...
-                    for (int idx = tid; idx < cols * kMxBlock; idx += kMxThreads) {   // rows is a multiple of 32: whole blocks
-                        const int c = idx / kMxBlock, i = idx % kMxBlock;
-                        float v[1] = {sum(i / kHalf, c, i % kHalf)};
-                        act_values(p.act, v);
-                        hb[slot][c][i] = v[0] * sum(i / kHalf, c, i % kHalf + kHalf);
-                    }
-                    if (slot + 1 < kHold && t0 + parts * kMxTiles < tiles) return;
-                    __syncthreads();
-                    if (tid < (slot + 1) * cols) {
-                        const int q = tid / cols, c = tid - q * cols;
-                        f32x16 even, odd;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            even[i] = hb[q][c][2 * i];
-                            odd[i] = hb[q][c][2 * i + 1];
+        const auto row_of = [&](int tile) { return min(GATED ? tile * kHalf + (r16 & (kHalf - 1)) : tile * kMxRows + r16, p.rows - 1); };
+        if constexpr (GATED) {
+            // blocks part, part + parts, ... of the hidden vectors, kHold at a time; the products' registers are free when the
+            // blocks are split
+            for (int b0 = part; b0 * 4 < tiles; b0 += kHold * parts) {
+                const int end = min(tiles, 4 * (b0 + kHold * parts));
+                mx4_body<1, kMxMoeNk, kFmt6, true, 4>(
+                    wq, ws, xin, xrow, p.st, b0, parts, end, red, row_of, [&]() {},
+                    [&](int t0, int, auto sum) {
+                        const int slot = (t0 / 4 - b0) / parts;
+                        for (int idx = tid; idx < cols * kMxBlock; idx += kMxThreads) {   // rows is a multiple of 32: whole blocks
+                            const int c = idx / kMxBlock, i = idx % kMxBlock;
+                            float v[1] = {sum(i / kHalf, c, i % kHalf)};
+                            act_values(p.act, v);
+                            hb[slot][c][i] = v[0] * sum(i / kHalf, c, i % kHalf + kHalf);
                         }
-                        uint32_t o[kSplitDwords], s;
-                        split_block32(even, odd, o, s);
-                        store_split(SplitRows{p.h, kSplitTokens, p.rows / kMxBlock}, m.y[c], t0 / kMxTiles - (slot - q) * parts, o, s);
+                    });
+                const int held = ((end + 3) / 4 - b0 + parts - 1) / parts;
+                if (tid < held * cols) {
+                    const int q = tid / cols, c = tid - q * cols;
+                    f32x16 even, odd;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        even[i] = hb[q][c][2 * i];
+                        odd[i] = hb[q][c][2 * i + 1];
                     }
-                } else {
+                    uint32_t o[kSplitDwords], s;
+                    split_block32(even, odd, o, s);
+                    store_split(SplitRows{p.h, kSplitTokens, p.rows / kMxBlock}, m.y[c], b0 + q * parts, o, s);
+                }
+                __syncthreads();
+            }
+        } else {
+            mx4_body<1, kMxMoeNk, kFmt6, false, kDownTiles>(
+                wq, ws, xin, xrow, p.st, part, parts, tiles, red, row_of, [&]() {},
+                [&](int t0, int nt, auto sum) {
                     for (int idx = tid; idx < nt * cols * kMxRows; idx += kMxThreads) {
                         const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, c = ic - i * cols;
                         const int row = (t0 + i * parts) * kMxRows + r;
                         if (row < p.rows)
                             p.part[(size_t)m.y[c] * p.rows + row] = sum(i, c, r) * m.w[c];
                     }
-                }
-            });
+                });
+        }
     }
 }
 

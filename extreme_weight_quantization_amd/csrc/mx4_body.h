@@ -1,10 +1,10 @@
 // A workgroup's part of a product of MX4 rows with up to 64 columns of activations: mx4_linear.hip describes the kernel
 // that it carries; the mixture-of-experts layer (moe_mx4.hip) runs it on experts.
 //
-// The workgroup walks tiles of 16 matrix-core rows in groups of kMxTiles: tiles bid + i nwg, or, RUN, 4 neighbours
-// each (kMxTiles (bid + i nwg) + 0 .. 3).  Its 8 waves share the
+// The workgroup walks tiles of 16 matrix-core rows in groups of mx4_tiles: tiles bid + i nwg, or, RUN, 4 neighbours
+// each (4 (bid + i nwg) + 0 .. 3).  Its 8 waves share the
 // inputs: wave w takes `nk` <= NK steps of 128 inputs out of every chunk of 8 nk, keeps their activations in registers
-// for all tiles of the group, and streams the codes of its steps, kMxTiles tiles ahead.  The waves' partial tiles are
+// for all tiles of the group, and streams the codes of its steps, a group ahead.  The waves' partial tiles are
 // added in LDS in the order of the waves.
 #pragma once
 #include <type_traits>
@@ -15,11 +15,12 @@ namespace aqlm {
 
 constexpr int kMxWaves = 8;
 constexpr int kMxThreads = kMxWaves * kWave;
-constexpr int kMxTiles = 4;       // tiles of a group: the codes of this many are in flight
+// Tiles of a group: the codes of this many are in flight.  Four column tiles leave registers for two.
+constexpr int mx4_tiles(int ct) { return ct == 4 ? 2 : 4; }
 constexpr int kMxRows = 16;       // matrix-core rows of a tile
 
 // LDS floats of the partial tiles of a group, CT column tiles.
-constexpr int mx4_red_floats(int ct) { return kMxTiles * kMxWaves * ct * 256; }
+constexpr int mx4_red_floats(int ct) { return mx4_tiles(ct) * kMxWaves * ct * 256; }
 
 // How the inputs are dealt to the waves.
 struct MxSteps {
@@ -96,7 +97,7 @@ struct MxOperand {
 // prepare(): called once the first codes are on their way; what the activations wait for.
 // fin(t0, n, sum): called by all threads of the workgroup once per group, after a barrier: tiles t0 + i step for i < n, step 1
 // with RUN, else nwg; sum(i, col, r) adds the waves' partial products of matrix-core row r and column col of the i-th.
-template <int CT, int NK, int FMT, bool RUN, class RowOf, class Prepare, class Fin>
+template <int CT, int NK, int FMT, bool RUN, int TILES, class RowOf, class Prepare, class Fin>
 __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws,
                                          const MxInputRows<FMT>& xin, const int (&xrow)[CT], const MxSteps st,
                                          const int bid, const int nwg, const int n_tiles, float* red, RowOf row_of,
@@ -105,6 +106,7 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int q = lane >> 4;
     const int nb = st.nb;
+    constexpr int kMxTiles = TILES;
 
     u32x4 cw[kMxTiles][NK];
     uint32_t cs[kMxTiles][NK];

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
             mine[q] = load_block16(static_cast<const f16*>(x) + (size_t)min((int)threadIdx.x + q * kMxThreads, T * st.nb - 1) * kMxBlock);
     }
     const int nwg = (int)gridDim.x;
-    mx4_body<CT, NK, FMT, false>(
+    mx4_body<CT, NK, FMT, false, mx4_tiles(CT)>(
         codes, scales, xin, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
         [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); },
         [&]() {
