@@ -24,16 +24,15 @@ namespace aqlm {
 
 // KIND kGemvGatedAt, kGemvPartAt: an expert's products in a mixture-of-experts layer (moe.hip).  Column b of x is row
 //   rows.x[b], and results go to row rows.y[b] (GemvRows).  GatedAt writes act(zg) zu as the sum of two fp16 numbers, PartAt
-//   takes such pairs as columns 2b and 2b + 1 and writes their product, weighted, in fp32.
+//   takes such pairs as columns 2b and 2b + 1 and writes their product in fp32.
 enum GemvKind : int { kGemvPlain = 0, kGemvAct = 1, kGemvGated = 2, kGemvGatedAt = 3, kGemvPartAt = 4 };
 constexpr bool gemv_gated(int kind) { return kind == kGemvGated || kind == kGemvGatedAt; }
 constexpr bool gemv_at(int kind) { return kind == kGemvGatedAt || kind == kGemvPartAt; }
 
-// Rows of the kinds that gather; x, y and w are in LDS.
+// Rows of the kinds that gather; x and y are in LDS.
 struct GemvRows {
     const uint16_t* x;   // rows of x of the columns
     const uint16_t* y;   // rows of the result
-    const float* w;      // [columns / 2] weights (kGemvPartAt)
     float* part;         // fp32 [..][out] (kGemvPartAt)
 };
 
@@ -566,7 +565,7 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
 #pragma unroll
                         for (int w = 0; w < kGemvWaves; ++w)
                             sum += red[w * kRedStride + rr * kRedRow + 2 * b] + red[w * kRedStride + rr * kRedRow + 2 * b + 1];
-                        rows.part[(size_t)rows.y[b] * out + row] = sum * (float)scales[row] * rows.w[b];
+                        rows.part[(size_t)rows.y[b] * out + row] = sum * (float)scales[row];
                     }
                 } else if (b < T && row < out) {
                     float sum = 0.f;

@@ -7,7 +7,7 @@
 // The products are those of gemv_act.hip: workgroups of 16 waves that hold the expert's codebooks in LDS (2x8, 1x8 g4,
 // 4x8 g16) or gather codewords from L2 (1x16), on the columns that moe_plan.h finds.  An expert's workgroups are neighbours on
 // one XCD, whose L2 then holds its codebook.  The hidden vector h of a pair (token, choice) is kept as the sum of two fp16 numbers; the down
-// product takes both as columns.  Its results stay apart per pair, weighted, in fp32, and the last launch adds a
+// product takes both as columns.  Its results stay apart per pair, in fp32, and the last launch weights and adds a
 // token's pairs in the order of its choices: no atomics, the same result every time.
 #include <algorithm>
 
@@ -29,9 +29,8 @@ struct MoeProduct {
     size_t codes_stride, codebooks_stride;   // bytes, entries
     const f16* x;
     f16* h;          // GatedAt: [pairs][2][rows]
-    float* part;     // PartAt: [pairs][rows]
+    float* part;     // PartAt: [pairs][rows], before the weights
     const int32_t* ids;
-    const float* weights;
     int experts, pairs, k, rows, in, act;
     float fixed;     // cost of starting on an item, in items
 };
@@ -61,11 +60,11 @@ __global__ __launch_bounds__(kGemvThreads) void moe_gemv_kernel(MoeProduct p) {
     const int parts = moe_parts(n, (int)gridDim.x, tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, p.weights, m, e);
+        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, m, e);
         gemv_body<SCHEME, REPL, VEC, kRtp, XM, KIND>(
             p.codes[0] + p.codes_stride * e, p.codebooks[0] + p.codebooks_stride * e, p.scales[0] + (size_t)p.rows * e, p.h, p.rows,
             u % parts, parts, p.x, p.in, KIND == kGemvPartAt ? 2 * cols : cols, expert_epi<KIND>(p, e),
-            GemvRows{m.x, m.y, m.w, p.part});
+            GemvRows{m.x, m.y, p.part});
     }
 }
 
@@ -120,7 +119,7 @@ __global__ __launch_bounds__(kGemvThreads) void moe_generic_kernel(MoeProduct p,
     const int parts = moe_parts(n, (int)gridDim.x, (p.rows + 15) / 16, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, p.weights, m, e);
+        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, m, e);
         const GemvEpi epi = expert_epi<KIND>(p, e);
         const f16* scales = p.scales[0] + (size_t)p.rows * e;
         for (int row = u % parts * 16 + wave; row < p.rows; row += parts * 16) {
@@ -170,7 +169,7 @@ __global__ __launch_bounds__(kGemvThreads) void moe_generic_kernel(MoeProduct p,
             for (int b = 0; b < kChunk; ++b) {   // lane b finishes column b
                 if (b < cols && lane == b) {
                     if constexpr (KIND == kGemvPartAt)
-                        p.part[(size_t)m.y[b] * p.rows + row] = acc[0][b] * (float)scales[row] * m.w[b];
+                        p.part[(size_t)m.y[b] * p.rows + row] = acc[0][b] * (float)scales[row];
                     else
                         gemv_finish_pair(acc[0][b], acc[kN - 1][b], scales, p.h, m.y[b], row, p.rows, epi);
                 }
@@ -213,7 +212,7 @@ hipError_t launch_product(const GenericScheme& sc, const MoeProduct& p, int cols
 }
 
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ part, const int32_t* __restrict__ ids,
-                                                          const f16* residual, f16* y, int n, int in, int k, int experts) {
+                                                          const float* __restrict__ weights, const f16* residual, f16* y, int n, int in, int k, int experts) {
     const int at = (int)blockIdx.x * 256 + (int)threadIdx.x;
     if (at >= n) return;
     constexpr int kStep = 8;
@@ -221,16 +220,17 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
     float s = 0.f;
     for (int j0 = 0; j0 < k; j0 += kStep) {   // kStep loads in flight
         int e[kStep];
-        float v[kStep];
+        float v[kStep], w[kStep];
 #pragma unroll
         for (int q = 0; q < kStep; ++q) {
             const size_t pair = (size_t)t * k + min(j0 + q, k - 1);
             e[q] = ids[pair];
+            w[q] = weights[pair];
             v[q] = part[pair * in + i];
         }
 #pragma unroll
         for (int q = 0; q < kStep; ++q)   // a pair without an expert has no part: whatever is there is left out
-            if (j0 + q < k && e[q] >= 0 && e[q] < experts) s += v[q];
+            if (j0 + q < k && e[q] >= 0 && e[q] < experts) s += w[q] * v[q];
     }
     if (residual != nullptr) s += (float)residual[at];
     y[at] = (f16)s;
@@ -250,7 +250,7 @@ int64_t moe_workspace(int64_t in, int64_t inner, int64_t tokens, int64_t k) {
 
 hipError_t launch_moe_combine(const float* part, const MoeCall& c, hipStream_t stream) {
     const int n = (int)(c.tokens * c.in);
-    hipLaunchKernelGGL(moe_combine_kernel, dim3((n + 255) / 256), dim3(256), 0, stream, part, c.ids,
+    hipLaunchKernelGGL(moe_combine_kernel, dim3((n + 255) / 256), dim3(256), 0, stream, part, c.ids, c.weights,
                        static_cast<const f16*>(c.residual), static_cast<f16*>(c.y), n, (int)c.in, c.k, c.experts);
     return hipGetLastError();
 }
@@ -271,7 +271,6 @@ hipError_t launch_moe(const GenericScheme& sc, const MoeLayers& L, const MoeCall
     p.h = h;
     p.part = part;
     p.ids = c.ids;
-    p.weights = c.weights;
     p.experts = c.experts;
     p.pairs = c.pairs();
     p.k = c.k;

@@ -52,7 +52,7 @@ struct MoeMx4Layers {
 int64_t moe_mx4_workspace(int64_t in, int64_t inner, int64_t tokens, int64_t k);
 hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspace, hipStream_t stream);
 
-// y_t = residual_t + sum over choices j with an expert of part[t k + j], in the order of j (moe.hip).
+// y_t = residual_t + sum over choices j with an expert of w_tj part[t k + j], in the order of j (moe.hip).
 hipError_t launch_moe_combine(const float* part, const MoeCall& c, hipStream_t stream);
 
 }  // namespace aqlm

@@ -15,25 +15,29 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kMxMoeNk = 4, kCols = 16, kHalf = kMxRows / 2;
+constexpr int kMxMoeNk = 3, kCols = 16, kHalf = kMxRows / 2;
 constexpr int kDownTiles = 3;   // a fourth would not fit the registers
-constexpr int kHold = 8;   // blocks of hidden values that wait to be split together, a thread a column
+constexpr int kHold = 4;   // blocks of hidden values that wait to be split together, a thread a column
+// Activations that are split inside the product (100 KB of LDS): a launch of its own for the split costs 5 us.
+constexpr int kInlineBlocks = 1024;
+bool split_inline(int64_t tokens, int64_t in) { return std::min<int64_t>(tokens, kCols) * (in / kMxBlock) <= kInlineBlocks; }
 
 struct MoeMxProduct {
     const uint8_t* codes[2];
     const uint8_t* scales[2];
     char* x;                 // split records of the input
     char* h;                 // gate and up: of the hidden vectors of the pairs
-    float* part;             // down: [pairs][rows]
+    float* part;             // down: [pairs][rows], before the weights
     const int32_t* ids;
-    const float* weights;
     MxSteps st;
     int experts, pairs, k, rows, act;
     float fixed;
 };
 
-template <bool GATED>
+// INLINE (gate and up): p.x is fp16 rows, and each workgroup splits those of its item into LDS, at most kInlineBlocks blocks.
+template <bool GATED, bool INLINE>
 __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
+    extern __shared__ u32x4 smem[];
     __shared__ MoeLds m;
     __shared__ float red[mx4_red_floats(1)];
     __shared__ float hb[kHold][kCols][kMxBlock + 1];
@@ -44,15 +48,25 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
     const int parts = moe_parts(n, (int)gridDim.x, GATED ? (tiles + 3) / 4 : tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kCols, false>(items, u / parts, p.k, p.weights, m, e);
+        const int cols = moe_item<kCols, false>(items, u / parts, p.k, m, e);
         const size_t row0 = (size_t)p.rows * e * p.st.nb;   // the expert's first block
         const int r16 = lane & 15, layer = GATED && r16 >= kHalf;
         const uint8_t* wq = (layer ? p.codes[1] : p.codes[0]) + row0 * kMxBlockBytes;
         const uint8_t* ws = (layer ? p.scales[1] : p.scales[0]) + row0;
         const int col = min(r16, cols - 1);
-        const int xrow[1] = {GATED ? (int)m.x[col] : (int)m.y[col]};
-        const int part = u % parts;
-        const MxInputRows<kFmt6> xin = {SplitRows{p.x, kSplitTokens, p.st.nb}};
+        const int xrow[1] = {INLINE ? col : GATED ? (int)m.x[col] : (int)m.y[col]};
+        const int part = u % parts, nb = p.st.nb;
+        const MxInputRows<kFmt6> xin = {INLINE ? SplitRows{reinterpret_cast<char*>(smem), cols, nb} : SplitRows{p.x, kSplitTokens, nb}};
+        if constexpr (INLINE) {
+            for (int i = tid; i < cols * nb; i += kMxThreads) {
+                const int c = i / nb;
+                uint32_t o[kSplitDwords], s;
+                split_block(load_block16(reinterpret_cast<const f16*>(p.x) + ((size_t)m.x[c] * nb + (i - c * nb)) * kMxBlock), o, s);
+                store_split(xin.rows, c, i - c * nb, o, s);
+            }
+            __syncthreads();
+        }
+        const auto prepare = []() {};
         const auto row_of = [&](int tile) { return min(GATED ? tile * kHalf + (r16 & (kHalf - 1)) : tile * kMxRows + r16, p.rows - 1); };
         if constexpr (GATED) {
             // blocks part, part + parts, ... of the hidden vectors, kHold at a time; the products' registers are free when the
@@ -60,7 +74,7 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
             for (int b0 = part; b0 * 4 < tiles; b0 += kHold * parts) {
                 const int end = min(tiles, 4 * (b0 + kHold * parts));
                 mx4_body<1, kMxMoeNk, kFmt6, true, 4>(
-                    wq, ws, xin, xrow, p.st, b0, parts, end, red, row_of, [&]() {},
+                    wq, ws, xin, xrow, p.st, b0, parts, end, red, row_of, prepare,
                     [&](int t0, int, auto sum) {
                         const int slot = (t0 / 4 - b0) / parts;
                         for (int idx = tid; idx < cols * kMxBlock; idx += kMxThreads) {   // rows is a multiple of 32: whole blocks
@@ -87,13 +101,13 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
             }
         } else {
             mx4_body<1, kMxMoeNk, kFmt6, false, kDownTiles>(
-                wq, ws, xin, xrow, p.st, part, parts, tiles, red, row_of, [&]() {},
+                wq, ws, xin, xrow, p.st, part, parts, tiles, red, row_of, prepare,
                 [&](int t0, int nt, auto sum) {
                     for (int idx = tid; idx < nt * cols * kMxRows; idx += kMxThreads) {
                         const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, c = ic - i * cols;
                         const int row = (t0 + i * parts) * kMxRows + r;
                         if (row < p.rows)
-                            p.part[(size_t)m.y[c] * p.rows + row] = sum(i, c, r) * m.w[c];
+                            p.part[(size_t)m.y[c] * p.rows + row] = sum(i, c, r);
                     }
                 });
         }
@@ -122,17 +136,19 @@ hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspa
         return p;
     };
     MoeMxProduct p = {};
-    p.x = take(round256(mx4_split_bytes(c.tokens, c.in)));
+    const bool inlined = split_inline(c.tokens, c.in);
+    if (!inlined) p.x = take(round256(mx4_split_bytes(c.tokens, c.in)));
     p.h = take(round256(mx4_split_bytes(c.pairs(), c.inner)));
     p.part = reinterpret_cast<float*>(at);
-    hipError_t r = launch_mx4_split(c.x, p.x, c.in, c.tokens, stream);
+    hipError_t r = hipSuccess;
+    if (inlined) p.x = const_cast<char*>(static_cast<const char*>(c.x));
+    else r = launch_mx4_split(c.x, p.x, c.in, c.tokens, stream);
     if (r != hipSuccess) return r;
     for (int l = 0; l < 2; ++l) {
         p.codes[l] = static_cast<const uint8_t*>(L.codes[l]);
         p.scales[l] = static_cast<const uint8_t*>(L.scales[l]);
     }
     p.ids = c.ids;
-    p.weights = c.weights;
     p.st = mx4_steps(c.in, kMxMoeNk);
     p.experts = c.experts;
     p.pairs = c.pairs();
@@ -140,7 +156,15 @@ hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspa
     p.rows = (int)c.inner;
     p.act = c.act;
     p.fixed = start_cost(2, c.inner, c.in);
-    hipLaunchKernelGGL(moe_mx4_kernel<true>, dim3(device_cu_count()), dim3(kMxThreads), 0, stream, p);
+    const dim3 grid(device_cu_count());
+    if (inlined) {
+        const int lds = SplitRows::record_bytes(std::min(c.tokens, kCols)) * (int)(c.in / kMxBlock);
+        r = hipFuncSetAttribute((const void*)moe_mx4_kernel<true, true>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (r != hipSuccess) return r;
+        hipLaunchKernelGGL((moe_mx4_kernel<true, true>), grid, dim3(kMxThreads), lds, stream, p);
+    } else {
+        hipLaunchKernelGGL((moe_mx4_kernel<true, false>), grid, dim3(kMxThreads), 0, stream, p);
+    }
     r = hipGetLastError();
     if (r != hipSuccess) return r;
     p.codes[0] = static_cast<const uint8_t*>(L.codes[2]);
@@ -149,7 +173,7 @@ hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspa
     p.st = mx4_steps(c.inner, kMxMoeNk);
     p.rows = (int)c.in;
     p.fixed = start_cost(1, c.inner, c.in);
-    hipLaunchKernelGGL(moe_mx4_kernel<false>, dim3(device_cu_count()), dim3(kMxThreads), 0, stream, p);
+    hipLaunchKernelGGL((moe_mx4_kernel<false, false>), grid, dim3(kMxThreads), 0, stream, p);
     r = hipGetLastError();
     if (r != hipSuccess) return r;
     return launch_moe_combine(p.part, c, stream);

@@ -23,7 +23,6 @@ struct MoeLds {
     uint16_t pair[kMoeMaxPairs];     // pairs by expert
     int expert;                      // of the item at hand
     uint16_t x[16], y[16];           // its columns: rows of the input, pairs
-    float w[16];                     // weights of the pairs
 };
 
 // What a workgroup knows about the items.  few: no more pairs than an item takes, so every expert that is asked for is one item;
@@ -132,10 +131,10 @@ __device__ __forceinline__ int moe_parts(int n, int wgs, int most, float fixed) 
     return best;
 }
 
-// Makes item v the one at hand: its expert e, and m.x (rows of the input), m.y (pairs), m.w (weights) for its pairs; returns how
+// Makes item v the one at hand: its expert e, and m.x (rows of the input) and m.y (pairs) for its pairs; returns how
 // many there are.  PAIRED: the input has two rows for a pair (2 pair, 2 pair + 1), else one for its token.  Ends with a barrier.
 template <int CHUNK, bool PAIRED>
-__device__ __forceinline__ int moe_item(const MoeItems& items, int v, int k, const float* __restrict__ weights, MoeLds& m, int& e) {
+__device__ __forceinline__ int moe_item(const MoeItems& items, int v, int k, MoeLds& m, int& e) {
     const int tid = threadIdx.x;
     int n, place = 0, p = 0;   // this thread's pair, if place < n
     __syncthreads();
@@ -161,7 +160,6 @@ __device__ __forceinline__ int moe_item(const MoeItems& items, int v, int k, con
     }
     if (place < n) {
         m.y[place] = (uint16_t)p;
-        m.w[place] = weights[p];
         if constexpr (PAIRED) {
             m.x[2 * place] = (uint16_t)(2 * p);
             m.x[2 * place + 1] = (uint16_t)(2 * p + 1);
