@@ -16,7 +16,7 @@ namespace aqlm {
 namespace {
 
 constexpr int kMxMoeNk = 3, kCols = 16, kHalf = kMxRows / 2;
-constexpr int kDownTiles = 3;   // a fourth would not fit the registers
+constexpr int kDownTiles = 4;
 constexpr int kHold = 4;   // blocks of hidden values that wait to be split together, a thread a column
 // Activations that are split inside the product (100 KB of LDS): a launch of its own for the split costs 5 us.
 constexpr int kInlineBlocks = 1024;

@@ -117,7 +117,7 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
         for (int j = 0; j < NK; ++j) {
             if (j < st.nk) {
                 const size_t at = row * nb + min(4 * (first(c) + j) + q, nb - 1);
-                cw[i][j] = load_nt16(wq + at * kMxBlockBytes);
+                cw[i][j] = load16(wq + at * kMxBlockBytes);
                 cs[i][j] = ws[at];
             }
         }
