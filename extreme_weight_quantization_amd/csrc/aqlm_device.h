@@ -74,6 +74,15 @@ __device__ __forceinline__ __attribute__((address_space(3))) void* lds_ptr(void*
     return (__attribute__((address_space(3))) void*)p;
 }
 
+// 64 x 16 bytes from base + off (a lane's) to LDS address `to` (uniform) on.  Inline assembly, because the compiler
+// makes every later LDS read wait for a load into LDS that it knows of; the stage's barrier waits for all of them instead.  There
+// is no result to wait for, and the address register is read when the load is issued.  M0 has no other user in these kernels.
+__device__ __forceinline__ void load_to_lds(uint32_t to, const void* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)lds_ptr(const_cast<void*>(p)); }
+
 // s_waitcnt immediates for __builtin_amdgcn_s_waitcnt, which, unlike a wait in
 // inline assembly, the compiler's own wait placement sees.  vmcnt sits in bits
 // 0-3 and 14-15, expcnt in 4-6, lgkmcnt in 8-11.

@@ -79,15 +79,6 @@ __device__ __forceinline__ u32x4 load_bytes16(const uint8_t* __restrict__ p, int
     return r;
 }
 
-// 64 x 16 bytes from base + off (a lane's) to LDS address `to` (uniform) on.  Inline assembly, because the compiler
-// makes every later LDS read wait for a load into LDS that it knows of; the stage's barrier waits for all of them instead.  There
-// is no result to wait for, and the address register is read when the load is issued.  M0 has no other user in this kernel.
-__device__ __forceinline__ void load_to_lds(uint32_t to, const void* base, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)lds_ptr(const_cast<void*>(p)); }
-
 template <int KB>
 __device__ __forceinline__ int fold(int r) { return KB == 8 ? r & 7 : (r >> 2) & 3; }
 

@@ -515,9 +515,12 @@ int aqlm_mx4_linear(const void* codes, const void* scales, const void* x, const 
  * or NULL) where it is given; equal ones: the lowest index first.  weights are
  * the scores without the bias, divided by their sum over the k when renorm is
  * not 0, times scale.  in % 8 == 0, k <= experts, 0 <= tokens <=
- * AQLM_ROUTE_MAX_TOKENS.  Logits and scores are computed in 64 bits, so the
- * choice does not depend on the batch.  A NaN score ranks below all others; a
- * token with a NaN logit has NaN weights under softmax.
+ * AQLM_ROUTE_MAX_TOKENS.  The choice is the one of logits and scores in 64
+ * bits and does not depend on the batch.  So are the weights, except where
+ * tokens * experts * in >= 2^29 (and no softmax with a bias): there they come
+ * from logits with sums of 64 products in fp32, added in 64 bits, off by at
+ * most 2^-17 |x| |R_e| and usually by about 2^-22.  A NaN score ranks below all
+ * others; a token with a NaN logit has NaN weights under softmax.
  *
  * aqlm_moe: the experts' layers in one AQLM scheme, three host arrays of three
  * entries (gate, up, down), each stacked over the experts: codes

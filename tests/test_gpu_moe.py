@@ -102,6 +102,91 @@ def test_route_non_finite_logits():
     assert E.aqlm_moe_route(x[:0].cuda(), router.cuda(), 3)[0].shape == (0, 3)
 
 
+def many_tokens(experts, n_in):
+    """Tokens from which on logits are summed in 32 bits first."""
+    return -(-2 ** 29 // (experts * n_in))
+
+
+@pytest.mark.parametrize("score,biased,renorm", [("softmax", False, True), ("sigmoid", False, False), ("sigmoid", True, True),
+                                                 ("softmax", True, False)])
+@pytest.mark.parametrize("experts,n_in,k,more", [(1, 8192, 1, 1), (40, 1000, 3, 5), (64, 4096, 8, 0), (130, 264, 16, 63), (256, 4096, 8, 1),
+                                                 (512, 2056, 16, 31)])
+def test_route_of_many_tokens(experts, n_in, k, more, score, biased, renorm):
+    tokens = many_tokens(experts, n_in) + more
+    g = gen(experts + n_in)
+    x = torch.randn((tokens, n_in), generator=g).half()
+    router = (torch.randn((experts, n_in), generator=g) / math.sqrt(n_in)).half()
+    bias = torch.randn(experts, generator=g) * 0.1 if biased else None
+    ids, w = E.aqlm_moe_route(x.cuda(), router.cuda(), k, score=score, bias=None if bias is None else bias.cuda(), renorm=renorm)
+    want_i, want_w = route_reference(x, router, k, score, bias, renorm, 1.0)
+    assert torch.equal(ids.cpu(), want_i)
+    # A logit is off by at most d = 2^-17 |x| |r|: a score by a factor e^d, against a sum of scores by e^2d.
+    d = 2.0 ** -17 * (x.double().norm(dim=1, keepdim=True) * router.double().norm(dim=1).max())
+    assert bool(((w.cpu().double() - want_w).abs() <= (torch.expm1(2 * d) + 2.0 ** -23) * want_w).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_of_many_tokens_with_exact_sums(score):
+    """Small whole numbers: sums of 32 bits are exact, so that weights are as for few tokens; many logits tie."""
+    experts, n_in, k = 96, 2048, 8
+    g = gen(3)
+    x = torch.randint(-2, 3, (many_tokens(experts, n_in) + 3, n_in), generator=g).half()
+    router = (torch.randint(-2, 3, (experts, n_in), generator=g) / 64).half()
+    ids, w = E.aqlm_moe_route(x.cuda(), router.cuda(), k, score=score)
+    want_i, want_w = route_reference(x, router, k, score, None, True, 1.0)
+    assert torch.equal(ids.cpu(), want_i)
+    assert bool(((w.cpu().double() - want_w).abs() <= 2.0 ** -23 * want_w).all())
+    few_i, few_w = E.aqlm_moe_route(x[:100].cuda(), router.cuda(), k, score=score)
+    assert torch.equal(few_i, ids[:100]) and torch.equal(few_w, w[:100])
+
+
+def test_route_of_many_tokens_close_and_equal_logits():
+    n_in, experts = 2048, 40
+    tokens = many_tokens(experts, n_in)
+    x = torch.ones((tokens, n_in), dtype=F16)
+    x[:, 1] = 2.0 ** -14
+    router = torch.ones((experts, n_in), dtype=F16)
+    router[:, 1] = torch.arange(experts).half() * 2.0 ** -8    # logits 2047 + i 2^-22
+    assert E.aqlm_moe_route(x.cuda(), router.cuda(), 4)[0].cpu().tolist() == [[39, 38, 37, 36]] * tokens
+    router[:, 1] = 1
+    bias = torch.zeros(experts)
+    bias[7] = -math.inf
+    bias[0] = -1.0
+    for score in ("softmax", "sigmoid"):
+        assert E.aqlm_moe_route(x.cuda(), router.cuda(), 3, score=score)[0].cpu().tolist() == [[0, 1, 2]] * tokens
+        got = E.aqlm_moe_route(x.cuda(), router.cuda(), experts // 8 + 3, score=score, bias=bias.cuda())[0].cpu()
+        assert got.tolist() == [[1, 2, 3, 4, 5, 6, 8, 9]] * tokens
+    zero = E.aqlm_moe_route(torch.zeros_like(x).cuda(), router.cuda(), 5)[0].cpu()
+    assert zero.tolist() == [[0, 1, 2, 3, 4]] * tokens
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_of_many_tokens_non_finite_logits(score):
+    g = gen(4)
+    experts, n_in = 20, 4096
+    tokens = many_tokens(experts, n_in)
+    x = torch.randn((tokens, n_in), generator=g).half()
+    router = (torch.randn((experts, n_in), generator=g) / 64).half()
+    router[11, 4090] = math.nan
+    x[1, 7] = math.nan
+    router[6] = 0
+    x[2] = 0
+    router[6, 0], x[2, 0] = math.inf, 1.0
+    x[:, 0] = x[:, 0].abs() + 1   # logit 6 is infinite
+    x[5, 0] = -1.0                # minus infinity
+    ids, w = (v.cpu() for v in E.aqlm_moe_route(x.cuda(), router.cuda(), 16, score=score, renorm=False))
+    logits = x.double() @ router.double().t()
+    logits[:, 11], logits[1] = math.nan, math.nan
+    logits[:, 6] = torch.where(x[:, 0] > 0, math.inf, -math.inf)
+    logits[1] = math.nan
+    order = torch.sort(torch.nan_to_num(logits, nan=-1e300, posinf=1e300, neginf=-1e299), dim=1, descending=True, stable=True)
+    assert torch.equal(ids, order.indices[:, :16].int())
+    if score == "sigmoid":
+        rows = torch.tensor([t for t in range(tokens) if t != 1])
+        assert bool((w[rows][ids[rows] == 6] == torch.where(x[rows, 0] > 0, 1.0, 0.0)[(ids[rows] == 6).any(1)]).all())
+    assert bool(w[1].isnan().all())
+
+
 # ------------------------------------------------------------------------------------------------ layers
 
 
