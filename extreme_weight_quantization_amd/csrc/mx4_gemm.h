@@ -6,7 +6,7 @@
 namespace aqlm {
 
 // Whether it takes this call.
-bool mx4_gemm_serves(int64_t out, int64_t in, int64_t batch);
+bool mx4_gemm_serves(bool x_mx4, int64_t out, int64_t in, int64_t batch);
 // Bytes of fp32 parts it may write for any batch up to this one.
 int64_t mx4_gemm_part_bytes(int64_t out, int64_t in, int64_t batch);
 // x: MX4, or split records (scales NULL).

@@ -1,15 +1,15 @@
 // Products of MX4 weights with many tokens: z[t][i] = sum_k W[i][k] x[t][k], then mx4_linear.hip's epilogue.
 //
 // The scaled matrix instructions take codes and scales as they are, so the work is to bring them on time.  A workgroup of
-// WM x WN waves owns a tile of TM rows of W x TN tokens; a wave a part of MT x NT squares of 32 x 32, which each take one
-// instruction a step of 64 inputs (four with x split in pieces).  Inputs pass through LDS in stages of 32 KB blocks, loaded straight
-// from memory, with one barrier a stage.  Between two matrix instructions of a step a wave reads a piece of the
+// WM x WN waves owns a tile of rows of W x tokens; a wave a part of MT x NT squares of 32 x 32, which each take one
+// instruction a step of 64 inputs (four with x split in pieces).  Inputs pass through LDS in stages of KB blocks of 32, loaded
+// straight from memory, with one barrier a stage.  Between two matrix instructions of a step a wave reads a piece of the
 // next step's operands, or issues a load of a later stage.
 //
 // LDS of a stage:
 //   rows of MX4 (W, and x where it is MX4): KB blocks of 16 bytes a row; block b of row r lies in slot b ^ fold(r), so that the
 //     16 lanes that one clock of a 16-byte read serves (0-3, 12-15, 20-27; 4-11, 16-19, 28-31; likewise above 32) find 16
-//     distinct banks, and KB neighbouring lanes of a load still read 16 KB contiguous bytes;
+//     distinct banks, and KB neighbouring lanes of a load still read 16 * KB contiguous bytes;
 //   split x: the records of mx4.h as they are.
 // Scale bytes of MX4 rows: 16 bytes a row at a time, 16 blocks' worth, into LDS of their own (two buffers): straight where
 // rows and array are 16-byte aligned (in % 512 == 0), else through registers from any address.  A lane reads the bytes of
@@ -395,9 +395,12 @@ __global__ __launch_bounds__(WM* WN * 64) void mx4_gemm_kernel(GemmArgs g) {
     }
 }
 
+// Tiles of W's rows x tokens: 256 x 256 (split x: 256 x 128), 128 x 128, 128 x 64.
+enum TileKind { kBig, kSmall, kNarrowTile };
+constexpr int64_t kNarrow = 64;
 struct GemmPlan {
-    bool big;
-    int tiles_m, tiles_n, splits;
+    TileKind kind;
+    int splits;
 };
 
 template <int FMT, int WM, int WN, int MT, int NT, int KB, int STAGES, bool PART>
@@ -413,41 +416,39 @@ hipError_t launch_tile(GemmArgs& g, bool straight, hipStream_t stream) {
     return hipGetLastError();
 }
 
-#ifndef BIG4
-#define BIG4 2, 4, 4, 2, 8, 2
-#endif
-#ifndef BIG6
-#define BIG6 2, 2, 4, 2, 4, 2
-#endif
-
 template <int FMT>
 hipError_t launch_plan(const GemmPlan& p, GemmArgs& g, hipStream_t stream) {
     // scales in 16-byte pieces that start on 16 bytes
     const bool straight = g.nb % kChunkBlocks == 0 && (uintptr_t)g.ws % 16 == 0 && (uintptr_t)g.xs % 16 == 0;
-    if (p.big) {
-        if constexpr (FMT == kFmt4) return launch_tile<FMT, BIG4, false>(g, straight, stream);
-        else return launch_tile<FMT, BIG6, false>(g, straight, stream);
+    constexpr bool kX4 = FMT == kFmt4;
+    if (p.kind == kBig) {   // 8 waves of 128 x 64, stages of 256 inputs; split x: 4 waves of 128 x 64, stages of 128
+        if constexpr (kX4) return launch_tile<FMT, 2, 4, 4, 2, 8, 2, false>(g, straight, stream);
+        else return launch_tile<FMT, 2, 2, 4, 2, 4, 2, false>(g, straight, stream);
     }
-    constexpr int kStages = FMT == kFmt4 ? 4 : 2;
-    return p.splits > 1 ? launch_tile<FMT, 2, 4, 2, 1, 4, kStages, true>(g, straight, stream)
-                        : launch_tile<FMT, 2, 4, 2, 1, 4, kStages, false>(g, straight, stream);
+    if (p.kind == kSmall) {   // 8 waves of 64 x 32
+        constexpr int kStages = kX4 ? 4 : 2;
+        return p.splits > 1 ? launch_tile<FMT, 2, 4, 2, 1, 4, kStages, true>(g, straight, stream)
+                            : launch_tile<FMT, 2, 4, 2, 1, 4, kStages, false>(g, straight, stream);
+    }
+    constexpr int kStages = kX4 ? 5 : 4;   // 8 waves of 32 x 32
+    return p.splits > 1 ? launch_tile<FMT, 4, 2, 1, 1, 4, kStages, true>(g, straight, stream)
+                        : launch_tile<FMT, 4, 2, 1, 1, 4, kStages, false>(g, straight, stream);
 }
 
 int64_t round4(int64_t v) { return (v + 3) / 4 * 4; }
 
-// The small tile (128 x 128) and how many parts of the sum fill the chip with it.
-constexpr int kSmall = 128, kWant = 512;
+constexpr int kSmallRows = 128;   // of W, in both small tiles
+constexpr int kFill = 256;        // workgroups that fill the chip: a tile's sum is split as long as there are no more
 int max_splits(int64_t in) { return (int)std::max<int64_t>(1, in / (2 * kChunkBlocks * kMxBlock)); }
 
+// Up to 64 tokens the narrow tile (128 x 128 at 64 tokens, 8192 -> 28672: 81 us against 53, x in MX4 28 against 26).  The big tile
+// from three quarters of the chip on: fewer leave CUs without work for a whole tile's time.
 GemmPlan gemm_plan(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
     const int64_t big_n = x_mx4 ? 256 : 128;
     GemmPlan p;
-    const int64_t big = (out + 255) / 256 * ((batch + big_n - 1) / big_n);
-    p.big = big >= 192;
-    p.tiles_m = (int)((out + kSmall - 1) / kSmall);
-    p.tiles_n = (int)((batch + kSmall - 1) / kSmall);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    p.splits = p.big ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(max_splits(in), 256 / tiles));
+    p.kind = batch <= kNarrow ? kNarrowTile : (out + 255) / 256 * ((batch + big_n - 1) / big_n) >= kFill * 3 / 4 ? kBig : kSmall;
+    const int64_t tiles = (out + kSmallRows - 1) / kSmallRows * ((batch + 127) / 128);
+    p.splits = p.kind == kBig ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(max_splits(in), kFill / tiles));
     // no empty part
     const int64_t chunks = (in / kMxBlock + kChunkBlocks - 1) / kChunkBlocks;
     while (p.splits > 1 && (chunks + p.splits - 1) / p.splits * (p.splits - 1) >= chunks) --p.splits;
@@ -456,13 +457,17 @@ GemmPlan gemm_plan(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
 
 }  // namespace
 
-bool mx4_gemm_serves(int64_t out, int64_t in, int64_t batch) {
-    return batch > 64 && out * (in / kMxBlock) >= 16;   // load_bytes16's least array
+// Against mx4_linear.hip's kernel, which walks a row from end to end in one workgroup (x fp16 | x MX4, us, its time first):
+//   33 tokens   8192 -> 1024: 26 15 | 15 9    4096 -> 2048: 17 15 | 9 9    2048 -> 4096: 12 14 | 6 8
+//   8192 -> 28672, 17 tokens: 53 53 | 39 24    1 token, x MX4: 33 23;    4096 -> 28672: 18 14    8192 -> 8192: 12 13
+bool mx4_gemm_serves(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
+    if (out * (in / kMxBlock) < 16) return false;   // load_bytes16's least array
+    return batch > kNarrow || (batch > 32 && (in >= 4096 || out * in >= (int64_t)1 << 25)) || (x_mx4 && out * in > (int64_t)1 << 26);
 }
 
 int64_t mx4_gemm_part_bytes(int64_t out, int64_t in, int64_t batch) {
-    // splits <= max_splits and splits * tiles_n <= kWant / tiles_m: the most of any batch up to this one
-    const int64_t tiles_m = (out + kSmall - 1) / kSmall, cap = std::max<int64_t>(1, kWant / tiles_m) * kSmall;
+    // splits <= max_splits and splits * token tiles <= kFill / tiles_m: the most of any batch up to this one
+    const int64_t tiles_m = (out + kSmallRows - 1) / kSmallRows, cap = std::max<int64_t>(1, kFill / tiles_m) * 128;
     return max_splits(in) < 2 ? 0 : std::min(max_splits(in) * batch, cap) * round4(out) * (int64_t)sizeof(float);
 }
 

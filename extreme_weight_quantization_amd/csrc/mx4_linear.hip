@@ -131,7 +131,7 @@ bool split_inline(int64_t in, int64_t batch) { return batch <= 16 && batch * (in
 int64_t mx4_linear_workspace(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
     if (out == 0 || batch == 0) return 0;
     const int64_t split = x_mx4 || split_inline(in, batch) ? 0 : mx4_split_bytes(batch, in);
-    return split + (mx4_gemm_serves(out, in, batch) ? mx4_gemm_part_bytes(out, in, batch) : 0);
+    return split + (mx4_gemm_serves(x_mx4, out, in, batch) ? mx4_gemm_part_bytes(out, in, batch) : 0);
 }
 
 hipError_t launch_mx4_linear(const void* codes, const void* scales, MxInput x, const Epilogue& e, void* workspace,
@@ -144,7 +144,7 @@ hipError_t launch_mx4_linear(const void* codes, const void* scales, MxInput x, c
         x.x = workspace;
         part += mx4_split_bytes(batch, in);
     }
-    if (mx4_gemm_serves(out, in, batch)) return launch_mx4_gemm(codes, scales, x, e, part, out, in, batch, stream);
+    if (mx4_gemm_serves(four, out, in, batch)) return launch_mx4_gemm(codes, scales, x, e, part, out, in, batch, stream);
     const RowsCall c = {codes, scales, x.x, x.scales,
                         MxEpilogue{static_cast<const f16*>(e.bias[0]), static_cast<const f16*>(e.residual),
                                    static_cast<f16*>(e.y), e.act},

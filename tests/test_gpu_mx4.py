@@ -139,6 +139,27 @@ def test_linear(n_in, out, t, four):
     assert torch.equal(again, y)
 
 
+@pytest.mark.parametrize("four", [False, True], ids=["fp16", "mx4"])
+@pytest.mark.parametrize("n_in,out,t", [(4096, 5, 33), (4128, 300, 40), (8192, 129, 64), (11008, 64, 63), (4640, 1, 34)])
+def test_linear_of_33_to_64_tokens_and_long_rows(n_in, out, t, four):
+    test_linear(n_in, out, t, four)
+
+
+@pytest.mark.parametrize("t", [1, 6, 33, 65])
+@pytest.mark.parametrize("four", [False, True], ids=["fp16", "mx4"])
+@pytest.mark.parametrize("n_in,out", [(1024, 65800), (8192, 8320)])
+def test_linear_of_large_layers(n_in, out, t, four):
+    codes, scales = weights(out, n_in, t)
+    x = activations(t, n_in, t + 1)
+    xin = E.aqlm_mx4_quantize(x.cuda()) if four else x.cuda()
+    y = E.aqlm_mx4_linear(codes.cuda(), scales.cuda(), xin)
+    xv = R.mx4_values(*R.mx4_quantize(x)) if four else x.double()
+    rows = torch.cat([torch.arange(0, 300), torch.arange(out // 2, out // 2 + 300), torch.arange(out - 300, out)])
+    z, ez = R.mx4_product(R.mx4_values(codes[rows], scales[rows]), xv, not four)
+    want, tol = R.linear(z, ez, "none", None, None)
+    check(y.cpu()[:, rows], want, tol)
+
+
 @pytest.mark.parametrize("t", [1, 20, 300])
 def test_activations_of_unlike_sizes_in_a_block(t):
     """Values 2^-8 of their block's largest and more are multiplied exactly, smaller ones to 2^-19 of it."""
