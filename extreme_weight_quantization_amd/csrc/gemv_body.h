@@ -312,7 +312,7 @@ __device__ __forceinline__ f32x4 chunk_mfma(const u32x4 cv, const u32x4* __restr
 
 // The product for one layer, run by workgroup bid of the nwg that serve it.
 // XM: how x reaches the registers (XMode).
-template <int SCHEME, int REPL, bool VEC, int RTP, int XM, int KIND = kGemvPlain>
+template <int SCHEME, int REPL, bool VEC, int RTP, int XM, int KIND = kGemvPlain, int TEAM = kGemvWaves>
 __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, const f16* __restrict__ codebooks0,
                                           const f16* __restrict__ scales, f16* y, const int out,
                                           const int bid, const int nwg, const f16* __restrict__ x, int in, int T,
@@ -346,14 +346,19 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
     const int rrep = GATED ? (REPL / 2) * (int)up + lane % (REPL > 1 ? REPL / 2 : 1) : lane % REPL;
     static_assert(!GATED || SCHEME == kScheme1x16 || REPL % 2 == 0, "replicas of two layers");
 
+    // A team of TEAM waves takes a tile, its waves the tile's slabs in turn.
+    constexpr int kTeams = kGemvWaves / TEAM;
+    const int team = kTeams == 1 ? 0 : wave / TEAM;
+    const int stride = nwg * kTeams;   // between the tiles of a pass
+
     // First codes and activations of this wave, issued before the codebook is
     // staged so that their memory latency overlaps the LDS fill.
-    int rt0 = bid;
-    int s0 = wave;
+    int rt0 = bid + team * nwg;
+    const int s0 = kTeams == 1 ? wave : wave % TEAM;
     u32x4 cnext[RTP];
 #pragma unroll
     for (int i = 0; i < RTP; ++i) {
-        const int rt = rt0 + i * nwg;
+        const int rt = rt0 + i * stride;
         cnext[i] = (s0 < n_slab && rt < n_rt)
                        ? load_codes<VEC, KIND>(codes, rt * kTileRows + trow, out, s0 * kSlabGroups + kq * 8, G)
                        : u32x4{0u, 0u, 0u, 0u};
@@ -498,12 +503,12 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
     }
     __syncthreads();
 
-    for (; rt0 < n_rt; rt0 += nwg * RTP) {
+    for (; rt0 - team * nwg < n_rt; rt0 += stride * RTP) {
         f32x4 acc[RTP];
 #pragma unroll
         for (int i = 0; i < RTP; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-        for (int s = s0; s < n_slab; s += kGemvWaves) {
+        for (int s = s0; s < n_slab; s += TEAM) {
             u32x4 ccur[RTP];
 #pragma unroll
             for (int i = 0; i < RTP; ++i) ccur[i] = cnext[i];
@@ -516,11 +521,11 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
             }
             // Prefetch the codes of this wave's next slab (or of the next pass).
             {
-                int sn = s + kGemvWaves, rtn = rt0;
-                if (sn >= n_slab) { sn = wave; rtn = rt0 + nwg * RTP; }
+                int sn = s + TEAM, rtn = rt0;
+                if (sn >= n_slab) { sn = s0; rtn = rt0 + stride * RTP; }
 #pragma unroll
                 for (int i = 0; i < RTP; ++i) {
-                    const int rt = rtn + i * nwg;
+                    const int rt = rtn + i * stride;
                     cnext[i] = (sn < n_slab && rt < n_rt)
                                    ? load_codes<VEC, KIND>(codes, rt * kTileRows + trow, out, sn * kSlabGroups + kq * 8, G)
                                    : u32x4{0u, 0u, 0u, 0u};
@@ -536,7 +541,7 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
             const bool whole_slab = (s + 1) * kSlabGroups <= G;   // uniform over the wave
 #pragma unroll
             for (int i = 0; i < RTP; ++i) {
-                const int rt = rt0 + i * nwg;
+                const int rt = rt0 + i * stride;
                 if (rt >= n_rt) break;
                 if (whole_slab && (rt + 1) * kTileRows <= out) {
                     acc[i] = chunk_mfma<SCHEME, REPL, false, KIND>(ccur[i], smem, codebooks, rrep, 0u, bx, acc[i]);
@@ -550,34 +555,36 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
         // Sum the per-wave partial tiles, scale, round to fp16.
 #pragma unroll
         for (int i = 0; i < RTP; ++i) {
-            const int rt = rt0 + i * nwg;
-            if (rt >= n_rt) break;
+            if (rt0 - team * nwg + i * stride >= n_rt) break;   // no team has a tile
             __syncthreads();
 #pragma unroll
             for (int r = 0; r < 4; ++r) red[wave * kRedStride + (4 * kq + r) * kRedRow + lrow] = acc[i][r];
             __syncthreads();
-            if (tid < kTileRows * 16) {
-                const int b = tid / kTileRows, rr = tid % kTileRows;
+            static_assert(kTeams * kTileRows * 16 <= kGemvThreads, "a thread an element of the teams' tiles");
+            if (tid < kTeams * kTileRows * 16) {
+                const int tm = kTeams == 1 ? 0 : tid / (kTileRows * 16), w0 = tm * TEAM;   // the element's team and its first wave
+                const int rt = rt0 + (tm - team) * nwg + i * stride;
+                const int b = kTeams == 1 ? tid / kTileRows : tid / kTileRows % 16, rr = tid % kTileRows;
                 const int row = rt * kTileRows + rr;
                 if constexpr (KIND == kGemvPartAt) {
                     if (2 * b < T && row < out) {   // T is even
                         float sum = 0.f;
 #pragma unroll
-                        for (int w = 0; w < kGemvWaves; ++w)
+                        for (int w = w0; w < w0 + TEAM; ++w)
                             sum += red[w * kRedStride + rr * kRedRow + 2 * b] + red[w * kRedStride + rr * kRedRow + 2 * b + 1];
                         rows.part[(size_t)rows.y[b] * out + row] = sum * (float)scales[row];
                     }
                 } else if (b < T && row < out) {
                     float sum = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kGemvWaves; ++w) sum += red[w * kRedStride + rr * kRedRow + b];
+                    for (int w = w0; w < w0 + TEAM; ++w) sum += red[w * kRedStride + rr * kRedRow + b];
                     if constexpr (KIND == kGemvPlain) {
                         y[(size_t)b * out + row] = (f16)(sum * (float)scales[row]);
                     } else {
                         float sum1 = 0.f;
                         if constexpr (GATED) {
 #pragma unroll
-                            for (int w = 0; w < kGemvWaves; ++w) sum1 += red[w * kRedStride + (8 + rr) * kRedRow + b];
+                            for (int w = w0; w < w0 + TEAM; ++w) sum1 += red[w * kRedStride + (8 + rr) * kRedRow + b];
                         }
                         if constexpr (AT) gemv_finish_pair(sum, sum1, scales, y, rows.y[b], row, out, epi);
                         else gemv_finish<KIND>(sum, sum1, scales, y, b, row, out, epi);
@@ -588,7 +595,7 @@ __device__ __forceinline__ void gemv_body(const uint8_t* __restrict__ codes0, co
         // Staged x, several slabs per wave: the next pass stages its first slab
         // over the tiles just summed.
         if constexpr (XS) {
-            if (n_slab > kGemvWaves) __syncthreads();
+            if (n_slab > TEAM) __syncthreads();
         }
     }
     // Keeps the L2 warm-up loads alive; the condition never holds (tid < 1024).

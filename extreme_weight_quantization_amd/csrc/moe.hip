@@ -19,7 +19,11 @@ namespace aqlm {
 
 namespace {
 
-constexpr int kRtp = 2;   // row tiles a pass, as the plain launches
+// Rows of up to 8 slabs of 256 inputs would leave half of a workgroup's 16 waves without work: there two teams of 8 waves take a
+// tile each, and a pass is one tile; else 16 waves a tile and two tiles a pass, as the plain launches.  In teams | not, us:
+//   2x8, 64 experts 2048x1408: 1 token 24 | 28, 16 tokens 65 | 79; 8 experts 4096x11008: 1 token 52 | 47
+constexpr int kTeam = 8;
+constexpr int rtp(int team) { return team == kGemvWaves ? 2 : 1; }
 
 // One launch's layers: rows x in of each expert, the second layer for the gated kind only.
 struct MoeProduct {
@@ -49,7 +53,7 @@ __device__ __forceinline__ GemvEpi expert_epi(const MoeProduct& p, int e) {
     return epi;
 }
 
-template <int SCHEME, int REPL, bool VEC, int XM, int KIND>
+template <int SCHEME, int REPL, bool VEC, int XM, int KIND, int TEAM>
 __global__ __launch_bounds__(kGemvThreads) void moe_gemv_kernel(MoeProduct p) {
     __shared__ MoeLds m;
     constexpr int kChunk = moe_chunk(KIND);
@@ -61,16 +65,17 @@ __global__ __launch_bounds__(kGemvThreads) void moe_gemv_kernel(MoeProduct p) {
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
         const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, m, e);
-        gemv_body<SCHEME, REPL, VEC, kRtp, XM, KIND>(
+        gemv_body<SCHEME, REPL, VEC, rtp(TEAM), XM, KIND, TEAM>(
             p.codes[0] + p.codes_stride * e, p.codebooks[0] + p.codebooks_stride * e, p.scales[0] + (size_t)p.rows * e, p.h, p.rows,
             u % parts, parts, p.x, p.in, KIND == kGemvPartAt ? 2 * cols : cols, expert_epi<KIND>(p, e),
             GemvRows{m.x, m.y, p.part});
     }
 }
 
-template <int SCHEME, int REPL, int XM, int KIND>
-hipError_t launch_v(const MoeProduct& p, hipStream_t stream) {
-    auto kern = p.in % 64 == 0 ? moe_gemv_kernel<SCHEME, REPL, true, XM, KIND> : moe_gemv_kernel<SCHEME, REPL, false, XM, KIND>;
+template <int SCHEME, int REPL, int XM, int KIND, int TEAM>
+hipError_t launch_team(const MoeProduct& p, hipStream_t stream) {
+    auto kern = p.in % 64 == 0 ? moe_gemv_kernel<SCHEME, REPL, true, XM, KIND, TEAM>
+                               : moe_gemv_kernel<SCHEME, REPL, false, XM, KIND, TEAM>;
     const size_t lds = (size_t)cb_slots<SCHEME, REPL>() * 16 +
                        std::max((size_t)kGemvWaves * kRedStride * sizeof(float),
                                 (size_t)kGemvWaves * kXStageSlots(XM) * 16);
@@ -78,6 +83,12 @@ hipError_t launch_v(const MoeProduct& p, hipStream_t stream) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(device_cu_count()), dim3(kGemvThreads), lds, stream, p);
     return hipGetLastError();
+}
+
+template <int SCHEME, int REPL, int XM, int KIND>
+hipError_t launch_v(const MoeProduct& p, hipStream_t stream) {
+    return p.in <= kTeam * kSlabGroups * kGroup ? launch_team<SCHEME, REPL, XM, KIND, kTeam>(p, stream)
+                                                : launch_team<SCHEME, REPL, XM, KIND, kGemvWaves>(p, stream);
 }
 
 // How x reaches the registers, by the most columns an item can have: as gemv_act.hip chooses.
