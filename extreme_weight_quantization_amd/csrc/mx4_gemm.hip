@@ -441,13 +441,17 @@ constexpr int kSmallRows = 128;   // of W, in both small tiles
 constexpr int kFill = 256;        // workgroups that fill the chip: a tile's sum is split as long as there are no more
 int max_splits(int64_t in) { return (int)std::max<int64_t>(1, in / (2 * kChunkBlocks * kMxBlock)); }
 
-// Up to 64 tokens the narrow tile (128 x 128 at 64 tokens, 8192 -> 28672: 81 us against 53, x in MX4 28 against 26).  The big tile
-// from three quarters of the chip on: fewer leave CUs without work for a whole tile's time.
+// Up to 64 tokens the narrow tile (128 x 128 at 64 tokens, 8192 -> 28672: 81 us against 53, x in MX4 28 against 26); also where
+// narrow tiles of whole, short rows fit the chip at once, which then needs fewer parts.  Narrow | 128 x 128, us, x fp16, x in MX4:
+//   4096 -> 4096: 128 tokens 22 | 24, 15 | 15, 400 tokens 31 | 37, 13 | 18    4096 -> 11008: 128 tokens 28 | 33, 13 | 17
+//   past the chip, 130 tokens: 47 | 41, 17 | 13    long rows, 11008 -> 4096, 300 tokens: 68 | 64, 37 | 27
+// The big tile from three quarters of the chip on: fewer leave CUs without work for a whole tile's time.
 GemmPlan gemm_plan(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
-    const int64_t big_n = x_mx4 ? 256 : 128;
+    const int64_t rows = (out + kSmallRows - 1) / kSmallRows, narrow = rows * ((batch + kNarrow - 1) / kNarrow);
+    const int64_t big = (out + 255) / 256 * (x_mx4 ? (batch + 255) / 256 : (batch + 127) / 128);
     GemmPlan p;
-    p.kind = batch <= kNarrow ? kNarrowTile : (out + 255) / 256 * ((batch + big_n - 1) / big_n) >= kFill * 3 / 4 ? kBig : kSmall;
-    const int64_t tiles = (out + kSmallRows - 1) / kSmallRows * ((batch + 127) / 128);
+    p.kind = batch <= kNarrow || (in <= 4096 && narrow <= kFill) ? kNarrowTile : big >= kFill * 3 / 4 ? kBig : kSmall;
+    const int64_t tiles = p.kind == kNarrowTile ? narrow : rows * ((batch + 127) / 128);
     p.splits = p.kind == kBig ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(max_splits(in), kFill / tiles));
     // no empty part
     const int64_t chunks = (in / kMxBlock + kChunkBlocks - 1) / kChunkBlocks;
