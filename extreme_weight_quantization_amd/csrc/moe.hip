@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kGemvThreads) void moe_gemv_kernel(MoeProduct p) {
     const int parts = moe_parts(n, (int)gridDim.x, tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, m, e);
+        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.pairs, p.k, m, e);
         gemv_body<SCHEME, REPL, VEC, rtp(TEAM), XM, KIND, TEAM>(
             p.codes[0] + p.codes_stride * e, p.codebooks[0] + p.codebooks_stride * e, p.scales[0] + (size_t)p.rows * e, p.h, p.rows,
             u % parts, parts, p.x, p.in, KIND == kGemvPartAt ? 2 * cols : cols, expert_epi<KIND>(p, e),
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kGemvThreads) void moe_generic_kernel(MoeProduct p,
     const int parts = moe_parts(n, (int)gridDim.x, (p.rows + 15) / 16, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.k, m, e);
+        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.pairs, p.k, m, e);
         const GemvEpi epi = expert_epi<KIND>(p, e);
         const f16* scales = p.scales[0] + (size_t)p.rows * e;
         for (int row = u % parts * 16 + wave; row < p.rows; row += parts * 16) {

@@ -35,12 +35,13 @@ struct MoeMxProduct {
 };
 
 // INLINE (gate and up): p.x is fp16 rows, and each workgroup splits those of its item into LDS, at most kInlineBlocks blocks.
-template <bool GATED, bool INLINE>
+template <bool GATED, bool INLINE, bool WIDE>
 __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
     extern __shared__ u32x4 smem[];
     __shared__ MoeLds m;
     __shared__ float red[mx4_red_floats(1)];
     __shared__ float hb[kHold][kCols][kMxBlock + 1];
+    constexpr int kNk = WIDE ? kMxMoeNk : 1;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const MoeItems items = moe_items<kCols>(p.ids, p.pairs, p.experts, m);
     const int n = items.n;
@@ -48,7 +49,7 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
     const int parts = moe_parts(n, (int)gridDim.x, GATED ? (tiles + 3) / 4 : tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kCols, false>(items, u / parts, p.k, m, e);
+        const int cols = moe_item<kCols, false>(items, u / parts, p.pairs, p.k, m, e);
         const size_t row0 = (size_t)p.rows * e * p.st.nb;   // the expert's first block
         const int r16 = lane & 15, layer = GATED && r16 >= kHalf;
         const uint8_t* wq = (layer ? p.codes[1] : p.codes[0]) + row0 * kMxBlockBytes;
@@ -73,7 +74,7 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
             // blocks are split
             for (int b0 = part; b0 * 4 < tiles; b0 += kHold * parts) {
                 const int end = min(tiles, 4 * (b0 + kHold * parts));
-                mx4_body<1, kMxMoeNk, kFmt6, true, 4>(
+                mx4_body<1, kNk, kFmt6, true, 4, WIDE>(
                     wq, ws, xin, xrow, p.st, b0, parts, end, red, row_of, prepare,
                     [&](int t0, int, auto sum) {
                         const int slot = (t0 / 4 - b0) / parts;
@@ -100,7 +101,7 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
                 __syncthreads();
             }
         } else {
-            mx4_body<1, kMxMoeNk, kFmt6, false, kDownTiles>(
+            mx4_body<1, kNk, kFmt6, false, kDownTiles, WIDE>(
                 wq, ws, xin, xrow, p.st, part, parts, tiles, red, row_of, prepare,
                 [&](int t0, int nt, auto sum) {
                     for (int idx = tid; idx < nt * cols * kMxRows; idx += kMxThreads) {
@@ -112,6 +113,22 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
                 });
         }
     }
+}
+
+template <bool GATED, bool INLINE, bool WIDE>
+hipError_t launch_v(const MoeMxProduct& p, int lds, hipStream_t stream) {
+    auto kern = moe_mx4_kernel<GATED, INLINE, WIDE>;
+    if (INLINE) {
+        const hipError_t r = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (r != hipSuccess) return r;
+    }
+    hipLaunchKernelGGL(kern, dim3(device_cu_count()), dim3(kMxThreads), lds, stream, p);
+    return hipGetLastError();
+}
+
+template <bool GATED, bool INLINE>
+hipError_t launch_product(const MoeMxProduct& p, int lds, hipStream_t stream) {
+    return p.st.nb >= kMxWideBlocks ? launch_v<GATED, INLINE, true>(p, lds, stream) : launch_v<GATED, INLINE, false>(p, lds, stream);
 }
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -156,16 +173,8 @@ hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspa
     p.rows = (int)c.inner;
     p.act = c.act;
     p.fixed = start_cost(2, c.inner, c.in);
-    const dim3 grid(device_cu_count());
-    if (inlined) {
-        const int lds = SplitRows::record_bytes(std::min(c.tokens, kCols)) * (int)(c.in / kMxBlock);
-        r = hipFuncSetAttribute((const void*)moe_mx4_kernel<true, true>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (r != hipSuccess) return r;
-        hipLaunchKernelGGL((moe_mx4_kernel<true, true>), grid, dim3(kMxThreads), lds, stream, p);
-    } else {
-        hipLaunchKernelGGL((moe_mx4_kernel<true, false>), grid, dim3(kMxThreads), 0, stream, p);
-    }
-    r = hipGetLastError();
+    const int lds = inlined ? SplitRows::record_bytes(std::min(c.tokens, kCols)) * (int)(c.in / kMxBlock) : 0;
+    r = inlined ? launch_product<true, true>(p, lds, stream) : launch_product<true, false>(p, lds, stream);
     if (r != hipSuccess) return r;
     p.codes[0] = static_cast<const uint8_t*>(L.codes[2]);
     p.scales[0] = static_cast<const uint8_t*>(L.scales[2]);
@@ -173,8 +182,7 @@ hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspa
     p.st = mx4_steps(c.inner, kMxMoeNk);
     p.rows = (int)c.in;
     p.fixed = start_cost(1, c.inner, c.in);
-    hipLaunchKernelGGL((moe_mx4_kernel<false, false>), grid, dim3(kMxThreads), 0, stream, p);
-    r = hipGetLastError();
+    r = launch_product<false, false>(p, 0, stream);
     if (r != hipSuccess) return r;
     return launch_moe_combine(p.part, c, stream);
 }

@@ -1,8 +1,8 @@
 // How a mixture-of-experts launch finds its work (device helpers).
 //
 // Which experts are asked for, and by whom, is known on the device only.  Every workgroup sorts the layer's pairs (token,
-// choice) by expert in its LDS: at most 1024 of them, below a microsecond, where a launch of its own would take
-// two.  Up to CHUNK pairs of one expert are an item: its weights are read once for them.  Items are cut
+// choice) by expert in its LDS, at most 1024 of them: it counts each expert's, and finds the pairs of the items that it takes by a
+// vote of 64 lanes at a time.  A launch of its own would take two microseconds.  Up to CHUNK pairs of one expert are an item: its weights are read once for them.  Items are cut
 // into `parts` so that parts x items fill the launch's workgroups evenly.
 #pragma once
 #include "aqlm_device.h"
@@ -16,11 +16,8 @@ static_assert(kMoeMaxExperts <= 1 << kMoeIdBits, "bits of an id");
 
 struct MoeLds {
     int count[kMoeMaxExperts];
-    int start[kMoeMaxExperts + 1];   // first place of an expert in pair[]
     int item0[kMoeMaxExperts + 1];   // first item of an expert
     uint16_t id[kMoeMaxPairs];       // the expert of a pair, or kMoeNone
-    uint16_t rank[kMoeMaxPairs];     // place of a pair among its expert's
-    uint16_t pair[kMoeMaxPairs];     // pairs by expert
     int expert;                      // of the item at hand
     uint16_t x[16], y[16];           // its columns: rows of the input, pairs
 };
@@ -45,8 +42,7 @@ __device__ __forceinline__ uint64_t same_expert(uint32_t e) {
     return same;
 }
 
-// Sorts the pairs.  All threads of the workgroup (at least 512) call it.  A pair whose id is no
-// expert is left out.  An expert's pairs stay in their order: workgroups that take parts of one item must agree on its pairs.
+// Counts the pairs.  All threads of the workgroup (at least 512) call it.  A pair whose id is no expert is left out.
 template <int CHUNK>
 __device__ __forceinline__ MoeItems moe_items(const int32_t* __restrict__ ids, int pairs, int experts, MoeLds& m) {
     if (pairs <= CHUNK) {
@@ -59,56 +55,35 @@ __device__ __forceinline__ MoeItems moe_items(const int32_t* __restrict__ ids, i
     }
     const int tid = threadIdx.x, n = blockDim.x;
     if (tid < kMoeMaxExperts) m.count[tid] = 0;
+    __syncthreads();
     for (int p = tid; p < pairs; p += n) {
         const int e = ids[p];
-        m.id[p] = (uint16_t)(e >= 0 && e < experts ? e : kMoeNone);
+        const bool some = e >= 0 && e < experts;
+        m.id[p] = (uint16_t)(some ? e : kMoeNone);
+        if (some) atomicAdd(&m.count[e], 1);   // whole numbers: in any order the same
     }
     __syncthreads();
     if (tid < kWave) {
-        // One wave ranks 64 pairs after another: the lanes of equal ids by a vote on each bit of them.
-        for (int p0 = 0; p0 < pairs; p0 += kWave) {
-            const int p = p0 + tid;
-            const uint32_t e = p < pairs ? m.id[p] : kMoeNone;
-            const uint64_t same = same_expert(e);
-            if (e != kMoeNone) {
-                const int before = m.count[e];
-                m.rank[p] = (uint16_t)(before + __popcll(same & ((1ull << tid) - 1ull)));
-                if ((same >> tid) == 1ull) m.count[e] = before + __popcll(same);   // the last of them
-            }
-        }
         constexpr int kPer = kMoeMaxExperts / kWave;
-        int c[kPer], sum = 0, items = 0;
+        int c[kPer], items = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            c[i] = m.count[tid * kPer + i];
-            sum += c[i];
-            items += (c[i] + CHUNK - 1) / CHUNK;
+            c[i] = (m.count[tid * kPer + i] + CHUNK - 1) / CHUNK;
+            items += c[i];
         }
-        int s = sum, t = items;
+        int t = items;
 #pragma unroll
         for (int o = 1; o < kWave; o <<= 1) {
-            const int so = __shfl_up(s, o, kWave), to = __shfl_up(t, o, kWave);
-            s += tid >= o ? so : 0;
+            const int to = __shfl_up(t, o, kWave);
             t += tid >= o ? to : 0;
         }
-        if (tid == kWave - 1) {
-            m.start[kMoeMaxExperts] = s;
-            m.item0[kMoeMaxExperts] = t;
-        }
-        s -= sum;
+        if (tid == kWave - 1) m.item0[kMoeMaxExperts] = t;
         t -= items;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            m.start[tid * kPer + i] = s;
             m.item0[tid * kPer + i] = t;
-            s += c[i];
-            t += (c[i] + CHUNK - 1) / CHUNK;
+            t += c[i];
         }
-    }
-    __syncthreads();
-    for (int p = tid; p < pairs; p += n) {
-        const uint32_t e = m.id[p];
-        if (e != kMoeNone) m.pair[m.start[e] + m.rank[p]] = (uint16_t)p;
     }
     __syncthreads();
     return MoeItems{__builtin_amdgcn_readfirstlane(m.item0[kMoeMaxExperts]), false, 0u, 0ull, 0ull};
@@ -132,39 +107,46 @@ __device__ __forceinline__ int moe_parts(int n, int wgs, int most, float fixed) 
 }
 
 // Makes item v the one at hand: its expert e, and m.x (rows of the input) and m.y (pairs) for its pairs; returns how
-// many there are.  PAIRED: the input has two rows for a pair (2 pair, 2 pair + 1), else one for its token.  Ends with a barrier.
+// many there are.  An expert's pairs keep their order: workgroups that take parts of one item must agree on its pairs.  PAIRED: the input has two rows for a pair (2 pair, 2 pair + 1), else one for its token.  Ends with a barrier.
 template <int CHUNK, bool PAIRED>
-__device__ __forceinline__ int moe_item(const MoeItems& items, int v, int k, MoeLds& m, int& e) {
+__device__ __forceinline__ int moe_item(const MoeItems& items, int v, int pairs, int k, MoeLds& m, int& e) {
     const int tid = threadIdx.x;
-    int n, place = 0, p = 0;   // this thread's pair, if place < n
-    __syncthreads();
-    if (items.few) {
-        const int lane = tid & (kWave - 1);
-        const uint64_t below = (1ull << lane) - 1ull;
-        const uint64_t first = __ballot((items.firsts >> lane & 1ull) && __popcll(items.firsts & below) == v);
-        const int l = __builtin_ctzll(first);
-        e = __builtin_amdgcn_readlane((int)items.expert, l);
-        const uint64_t same = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(items.same >> 32), l) << 32 |
-                              (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)items.same, l);
-        n = __popcll(same);
-        p = lane;
-        place = tid < kWave && (same >> lane & 1ull) ? __popcll(same & below) : n;
-    } else {
-        if (tid < kMoeMaxExperts && m.item0[tid] <= v && v < m.item0[tid + 1]) m.expert = tid;
-        __syncthreads();
-        e = __builtin_amdgcn_readfirstlane(m.expert);
-        const int at = m.start[e] + (v - m.item0[e]) * CHUNK;
-        n = min(CHUNK, m.start[e + 1] - at);
-        place = tid;
-        if (tid < n) p = m.pair[at + tid];
-    }
-    if (place < n) {
+    int n;
+    auto keep = [&](int place, int p) {
         m.y[place] = (uint16_t)p;
         if constexpr (PAIRED) {
             m.x[2 * place] = (uint16_t)(2 * p);
             m.x[2 * place + 1] = (uint16_t)(2 * p + 1);
         } else {
             m.x[place] = (uint16_t)(p / k);
+        }
+    };
+    const int lane = tid & (kWave - 1);
+    const uint64_t below = (1ull << lane) - 1ull;
+    __syncthreads();
+    if (items.few) {
+        const uint64_t first = __ballot((items.firsts >> lane & 1ull) && __popcll(items.firsts & below) == v);
+        const int l = __builtin_ctzll(first);
+        e = __builtin_amdgcn_readlane((int)items.expert, l);
+        const uint64_t same = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(items.same >> 32), l) << 32 |
+                              (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)items.same, l);
+        n = __popcll(same);
+        if (tid < kWave && (same >> lane & 1ull)) keep(__popcll(same & below), lane);
+    } else {
+        if (tid < kMoeMaxExperts && m.item0[tid] <= v && v < m.item0[tid + 1]) m.expert = tid;
+        __syncthreads();
+        e = __builtin_amdgcn_readfirstlane(m.expert);
+        const int from = __builtin_amdgcn_readfirstlane((v - m.item0[e]) * CHUNK);   // the item's first pair among the expert's
+        n = min(CHUNK, m.count[e] - from);
+        if (tid < kWave) {
+            int before = 0;   // of the expert's pairs
+            for (int p0 = 0; p0 < pairs && before < from + n; p0 += kWave) {
+                const bool mine = p0 + lane < pairs && m.id[p0 + lane] == e;
+                const uint64_t same = __ballot(mine);
+                const int place = before + __popcll(same & below) - from;
+                if (mine && place >= 0 && place < n) keep(place, p0 + lane);
+                before += __popcll(same);
+            }
         }
     }
     __syncthreads();

@@ -191,4 +191,16 @@ __device__ __forceinline__ void store_split(const SplitRows& to, int token, int 
     *to.scales(rec, token) = scales;
 }
 
+// Bytes d, d + 1, ... of r (0 <= d <= 16), then zeros.
+__device__ __forceinline__ u32x4 move_bytes(u32x4 r, int d) {
+    if (d & 1) r = u32x4{(uint32_t)__builtin_amdgcn_alignbyte(r[1], r[0], 1), (uint32_t)__builtin_amdgcn_alignbyte(r[2], r[1], 1),
+                         (uint32_t)__builtin_amdgcn_alignbyte(r[3], r[2], 1), r[3] >> 8};
+    if (d & 2) r = u32x4{(uint32_t)__builtin_amdgcn_alignbyte(r[1], r[0], 2), (uint32_t)__builtin_amdgcn_alignbyte(r[2], r[1], 2),
+                         (uint32_t)__builtin_amdgcn_alignbyte(r[3], r[2], 2), r[3] >> 16};
+    if (d & 4) r = u32x4{r[1], r[2], r[3], 0u};
+    if (d & 8) r = u32x4{r[2], r[3], 0u, 0u};
+    if (d & 16) r = u32x4{0u, 0u, 0u, 0u};
+    return r;
+}
+
 }  // namespace aqlm

@@ -67,16 +67,7 @@ __device__ __forceinline__ u32x4 load_bytes16(const uint8_t* __restrict__ p, int
     typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
     const int64_t from = at < total - 16 ? at : total - 16;
     const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p + from);
-    u32x4 r = {v[0], v[1], v[2], v[3]};
-    const int d = (int)(at - from < 16 ? at - from : 16);
-    if (d & 1) r = u32x4{(uint32_t)__builtin_amdgcn_alignbyte(r[1], r[0], 1), (uint32_t)__builtin_amdgcn_alignbyte(r[2], r[1], 1),
-                         (uint32_t)__builtin_amdgcn_alignbyte(r[3], r[2], 1), r[3] >> 8};
-    if (d & 2) r = u32x4{(uint32_t)__builtin_amdgcn_alignbyte(r[1], r[0], 2), (uint32_t)__builtin_amdgcn_alignbyte(r[2], r[1], 2),
-                         (uint32_t)__builtin_amdgcn_alignbyte(r[3], r[2], 2), r[3] >> 16};
-    if (d & 4) r = u32x4{r[1], r[2], r[3], 0u};
-    if (d & 8) r = u32x4{r[2], r[3], 0u, 0u};
-    if (d & 16) r = u32x4{0u, 0u, 0u, 0u};
-    return r;
+    return move_bytes(u32x4{v[0], v[1], v[2], v[3]}, (int)(at - from < 16 ? at - from : 16));
 }
 
 template <int KB>

@@ -30,7 +30,7 @@ struct MxEpilogue {
 // of its own for the split costs more from there down.
 constexpr int kInlineBlocks = 1024;
 
-template <int CT, int NK, int FMT, bool INLINE>
+template <int CT, int NK, int FMT, bool INLINE, bool WIDE = false>
 __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales, const void* x,
                                                               const void* xs, MxSteps st, int out, int T, MxEpilogue e) {
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
             mine[q] = load_block16(static_cast<const f16*>(x) + (size_t)min((int)threadIdx.x + q * kMxThreads, T * st.nb - 1) * kMxBlock);
     }
     const int nwg = (int)gridDim.x;
-    mx4_body<CT, NK, FMT, false, mx4_tiles(CT)>(
+    mx4_body<CT, NK, FMT, false, mx4_tiles(CT), WIDE>(
         codes, scales, xin, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
         [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); },
         [&]() {
@@ -98,9 +98,9 @@ struct RowsCall {
     hipStream_t stream;
 };
 
-template <int CT, int NK, int FMT, bool INLINE>
+template <int CT, int NK, int FMT, bool INLINE, bool WIDE = false>
 hipError_t launch_rows_v(const RowsCall& c) {
-    auto kern = mx4_rows_kernel<CT, NK, FMT, INLINE>;
+    auto kern = mx4_rows_kernel<CT, NK, FMT, INLINE, WIDE>;
     const MxSteps st = mx4_steps(c.in, NK);
     const size_t lds = mx4_red_floats(CT) * sizeof(float) +
                        (INLINE ? (size_t)SplitRows::record_bytes(c.T) * st.nb : 0);
@@ -121,7 +121,7 @@ hipError_t launch_rows(const RowsCall& c) {
         if (c.T > 32) return launch_rows_v<4, 1, FMT, INLINE>(c);
         if (c.T > 16) return launch_rows_v<2, 2, FMT, INLINE>(c);
     }
-    return launch_rows_v<1, 4, FMT, INLINE>(c);
+    return c.in >= kMxWideBlocks * kMxBlock ? launch_rows_v<1, 4, FMT, INLINE, true>(c) : launch_rows_v<1, 1, FMT, INLINE>(c);
 }
 
 bool split_inline(int64_t in, int64_t batch) { return batch <= 16 && batch * (in / kMxBlock) <= kInlineBlocks; }
