@@ -187,6 +187,33 @@ def test_route_of_many_tokens_non_finite_logits(score):
     assert bool(w[1].isnan().all())
 
 
+
+def test_captured_route_of_many_tokens_follows_its_input():
+    experts, n_in, k = 64, 4096, 8
+    tokens = many_tokens(experts, n_in)
+    g = gen(5)
+    router = (torch.randn((experts, n_in), generator=g) / 64).half().cuda()
+    x = torch.randn((tokens, n_in), generator=g).half().cuda()
+    ws = torch.empty(E.moe_route_workspace_bytes(experts, n_in, k, tokens), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        E.aqlm_moe_route(x, router, k, workspace=ws)
+        with torch.cuda.graph(graph, stream=side):
+            ids, w = E.aqlm_moe_route(x, router, k, workspace=ws)
+    torch.cuda.synchronize()
+    for seed in (6, 7, 8):
+        x.copy_(torch.randn((tokens, n_in), generator=gen(seed)).half())
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = ids.clone(), w.clone()
+        want = E.aqlm_moe_route(x, router, k)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(got[0].cpu(), route_reference(x.cpu(), router.cpu(), k, "softmax", None, True, 1.0)[0])
+
+
 # ------------------------------------------------------------------------------------------------ layers
 
 

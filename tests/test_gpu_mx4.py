@@ -341,3 +341,66 @@ def test_refusals():
         n = E.mx4_linear_workspace_bytes(8, 64, 300)
         E.aqlm_mx4_linear(codes, scales, torch.zeros((300, 64), dtype=F16, device="cuda"),
                           workspace=torch.empty(n - 1, dtype=U8, device="cuda"))
+
+
+@pytest.mark.parametrize("four", [False, True], ids=["fp16", "mx4"])
+@pytest.mark.parametrize("n_in,t", [(4128, 1), (4128, 40), (4128, 130), (8192, 64), (512, 3), (544, 7)])
+def test_long_rows_with_odd_scales_and_non_finite_blocks(n_in, t, four):
+    out = 150
+    codes, scales = weights(out, n_in, n_in + t)
+    scales[9, n_in // 32 - 1] = 255
+    x = activations(t, n_in, t)
+    if t > 2:
+        x[2, n_in - 1] = math.inf
+    odd = torch.empty(scales.numel() + 1, dtype=U8, device="cuda")[1:].view(out, -1)
+    odd.copy_(scales)
+    xin = E.aqlm_mx4_quantize(x.cuda()) if four else x.cuda()
+    y = E.aqlm_mx4_linear(codes.cuda(), odd, xin).cpu()
+    rows = [t0 for t0 in range(t) if t0 != 2]
+    keep = [r for r in range(out) if r != 9]
+    assert bool(y[:, 9].isnan().all()) and (t <= 2 or bool(y[2].isnan().all()))
+    xv = (R.mx4_values(*R.mx4_quantize(x[rows])) if four else x[rows].double())
+    z, ez = R.mx4_product(R.mx4_values(codes[keep], scales[keep]), xv, not four)
+    want, tol = R.linear(z, ez, "none", None, None)
+    check(y[rows][:, keep], want, tol)
+
+
+@pytest.mark.parametrize("t", [1, 40, 70])
+def test_longest_rows(t):
+    n_in, out = 1 << 20, 18
+    codes, scales = weights(out, n_in, t)
+    x = activations(t, n_in, t)
+    for four in (False, True):
+        xin = E.aqlm_mx4_quantize(x.cuda()) if four else x.cuda()
+        y = E.aqlm_mx4_linear(codes.cuda(), scales.cuda(), xin)
+        xv = R.mx4_values(*R.mx4_quantize(x)) if four else x.double()
+        z, ez = R.mx4_product(R.mx4_values(codes, scales), xv, not four)
+        want, tol = R.linear(z, ez, "none", None, None)
+        check(y, want, tol)
+
+
+@pytest.mark.parametrize("four", [False, True], ids=["fp16", "mx4"])
+def test_captured_products_of_40_tokens_follow_their_inputs(four):
+    n_in, out, t = 4096, 200, 40
+    codes, scales = (v.cuda() for v in weights(out, n_in, 31))
+    x = activations(t, n_in, 32).cuda()
+    ws = torch.empty(max(16, E.mx4_linear_workspace_bytes(out, n_in, t, x_mx4=four)), dtype=U8, device="cuda")
+    y = torch.empty((t, out), dtype=F16, device="cuda")
+
+    def call():
+        return E.aqlm_mx4_linear(codes, scales, E.aqlm_mx4_quantize(x) if four else x, act="silu", y=y, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        call()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    torch.cuda.synchronize()
+    for seed in (33, 34, 35):
+        x.copy_(activations(t, n_in, seed))
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, call())
