@@ -215,10 +215,10 @@ __global__ __launch_bounds__(WM* WN * 64) void mx4_gemm_kernel(GemmArgs g) {
             const char* rec = st + pb6 + (j * KB + 2 * k) * kSplitRecord;
             if (p < kPieces) {
                 const u32x4 f = *reinterpret_cast<const u32x4*>(rec + p * 512 + l32 * 16);
-                const u32x2 r = *reinterpret_cast<const u32x2*>(rec + 2048 + p * 256 + l32 * 8);
+                const u32x2 r = *reinterpret_cast<const u32x2*>(rec + kPieces * 512 + p * 256 + l32 * 8);
                 o.b[j][p] = u32x6{f[0], f[1], f[2], f[3], r[0], r[1]};
             } else {
-                o.sb[j] = *reinterpret_cast<const uint32_t*>(rec + 3072 + l32 * 4);
+                o.sb[j] = *reinterpret_cast<const uint32_t*>(rec + kPieces * 768 + l32 * 4);
             }
         }
     };
@@ -454,10 +454,12 @@ GemmPlan gemm_plan(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
 
 // Against mx4_linear.hip's kernel, which walks a row from end to end in one workgroup (x fp16 | x MX4, us, its time first):
 //   33 tokens   8192 -> 1024: 26 15 | 15 9    4096 -> 2048: 17 15 | 9 9    2048 -> 4096: 12 14 | 6 8
-//   8192 -> 28672, 17 tokens: 53 53 | 39 24    1 token, x MX4: 33 23;    4096 -> 28672: 18 14    8192 -> 8192: 12 13
+//   17 tokens   8192 -> 28672: 53 53 | 39 24; x in MX4, 32 tokens   8192 -> 11008: 22 17    4096 -> 11008: 12 13
+//   x in MX4, 1 token   8192 -> 28672: 28 22    8192 -> 16384: 17 18    4096 -> 28672: 15 14
 bool mx4_gemm_serves(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
     if (out * (in / kMxBlock) < 16) return false;   // load_bytes16's least array
-    return batch > kNarrow || (batch > 32 && (in >= 4096 || out * in >= (int64_t)1 << 25)) || (x_mx4 && out * in > (int64_t)1 << 26);
+    return batch > kNarrow || (batch > 32 && (in >= 4096 || out * in >= (int64_t)1 << 25)) ||
+           (x_mx4 && out * in > (int64_t)1 << (batch > 16 ? 26 : 27));
 }
 
 int64_t mx4_gemm_part_bytes(int64_t out, int64_t in, int64_t batch) {

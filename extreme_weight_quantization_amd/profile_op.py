@@ -6,7 +6,11 @@ OP is gemv, gemm, gemm_dequant, decode, gemv_lists, linear_act, gated,
 linear_act_backward or gated_backward (the last four with silu and, backward,
 bias gradients; linear_act and gated at batch 1 also as linear_act_lists and
 gated_lists); SCHEME is 2x8, 1x16 or
-an (M, B, g) triple written MxBgG (4x8g16).  OP copy runs a plain 64 MiB
+an (M, B, g) triple written MxBgG (4x8g16).  With SCHEME mx4 OP is
+mx4_quantize, mx4_decode, mx4_linear or mx4_linear_x4 (x in MX4).  moe_route and
+moe take --experts (default 32) and --k (4): route's SCHEME is softmax or
+sigmoid, its OUT the experts; moe's SCHEME is mx4 or an AQLM scheme, its OUT the
+inner size.  OP copy runs a plain 64 MiB
 device-to-device copy instead (the reference for scaling byte counters; the
 other arguments are ignored).  Inputs follow the distributions of
 the benchmark layers: codebooks N(0, 0.05) (2x8, other B = 8 schemes) or
@@ -34,15 +38,70 @@ def parse_scheme(name: str):
     return M, B, g, 0.05
 
 
+def repeat(call, reps, torch):
+    call()
+    torch.cuda.synchronize()
+    for _ in range(reps):
+        call()
+    torch.cuda.synchronize()
+    print("done", flush=True)
+
+
+def serving_call(args, torch, E):
+    """A call of the MX4 or mixture-of-experts operators; weights N(0, 1 / sqrt(in)) in MX4, AQLM as above."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(0)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device="cuda")
+
+    def mx4(rows, n_in, lead=()):
+        codes, scales = E.aqlm_mx4_quantize((normal(rows, n_in) / n_in ** 0.5).half())
+        return codes.repeat(*lead, 1, 1) if lead else codes, scales.repeat(*lead, 1, 1) if lead else scales
+
+    x = normal(args.batch, args.n_in).half()
+    if args.op == "moe_route":
+        router = (normal(args.out, args.n_in) / args.n_in ** 0.5).half()
+        return lambda: E.aqlm_moe_route(x, router, args.k, score=args.scheme)
+    if args.op == "moe":
+        ids = torch.stack([torch.randperm(args.experts, generator=gen, device="cuda")[: args.k] for _ in range(args.batch)]).int()
+        weights = torch.full(ids.shape, 1.0 / args.k, device="cuda")
+        shapes = ((args.out, args.n_in), (args.out, args.n_in), (args.n_in, args.out))
+        if args.scheme == "mx4":
+            layers = [mx4(rows, n, (args.experts,)) for rows, n in shapes]
+            return lambda: E.aqlm_moe_mx4(*layers, x, ids, weights)
+        M, B, g, sd = parse_scheme(args.scheme)
+        lo, hi = (-(1 << 15), 1 << 15) if B == 16 else (0, 1 << B)
+        layers = [(torch.randint(lo, hi, (args.experts, rows, n // g, M), generator=gen, device="cuda",
+                                 dtype=torch.uint8 if B <= 8 else torch.int16),
+                   (normal(args.experts, M, 1 << B, g) * sd).half(),
+                   (torch.rand((args.experts, rows), generator=gen, device="cuda") + 0.5).half()) for rows, n in shapes]
+        return lambda: E.aqlm_moe(*layers, x, ids, weights)
+    if args.scheme != "mx4":
+        raise SystemExit(f"{args.op} takes scheme mx4")
+    if args.op == "mx4_quantize":
+        w = normal(args.out, args.n_in).half()
+        return lambda: E.aqlm_mx4_quantize(w)
+    codes, scales = mx4(args.out, args.n_in)
+    if args.op == "mx4_decode":
+        return lambda: E.aqlm_mx4_decode(codes, scales)
+    if args.op == "mx4_linear_x4":
+        x = E.aqlm_mx4_quantize(x)
+    return lambda: E.aqlm_mx4_linear(codes, scales, x)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("op", choices=("gemv", "gemm", "gemm_dequant", "decode", "gemv_lists", "copy", "linear_act", "gated",
-                                   "linear_act_lists", "gated_lists", "linear_act_backward", "gated_backward"))
+                                   "linear_act_lists", "gated_lists", "linear_act_backward", "gated_backward",
+                                   "mx4_quantize", "mx4_decode", "mx4_linear", "mx4_linear_x4", "moe_route", "moe"))
     ap.add_argument("scheme")
     ap.add_argument("out", type=int)
     ap.add_argument("n_in", type=int)
     ap.add_argument("batch", type=int, nargs="?", default=1)
     ap.add_argument("--reps", type=int, default=5)
+    ap.add_argument("--experts", type=int, default=32)
+    ap.add_argument("--k", type=int, default=4)
     args = ap.parse_args(argv)
 
     import torch
@@ -58,6 +117,9 @@ def main(argv=None):
             dst.copy_(src)
         torch.cuda.synchronize()
         print("done", flush=True)
+        return
+    if args.op.startswith(("mx4", "moe")):
+        repeat(serving_call(args, torch, E), args.reps, torch)
         return
     M, B, g, sd = parse_scheme(args.scheme)
     gen = torch.Generator(device="cuda")
@@ -115,12 +177,7 @@ def main(argv=None):
         y = torch.empty((1, args.out), dtype=torch.float16, device="cuda")
         ws = torch.empty(E.lists_workspace_bytes(args.out, args.n_in), dtype=torch.uint8, device="cuda")
         call = lambda: E.aqlm_linear_gemv_lists(lists, cb, s, x, y, ws)
-    call()
-    torch.cuda.synchronize()
-    for _ in range(args.reps):
-        call()
-    torch.cuda.synchronize()
-    print("done", flush=True)
+    repeat(call, args.reps, torch)
 
 
 if __name__ == "__main__":

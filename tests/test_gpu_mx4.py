@@ -145,9 +145,9 @@ def test_linear_of_33_to_64_tokens_and_long_rows(n_in, out, t, four):
     test_linear(n_in, out, t, four)
 
 
-@pytest.mark.parametrize("t", [1, 6, 33, 65])
+@pytest.mark.parametrize("t", [1, 6, 20, 33, 65])
 @pytest.mark.parametrize("four", [False, True], ids=["fp16", "mx4"])
-@pytest.mark.parametrize("n_in,out", [(1024, 65800), (8192, 8320)])
+@pytest.mark.parametrize("n_in,out", [(1024, 65800), (8192, 8320), (8192, 16500)])
 def test_linear_of_large_layers(n_in, out, t, four):
     codes, scales = weights(out, n_in, t)
     x = activations(t, n_in, t + 1)
