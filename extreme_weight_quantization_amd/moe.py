@@ -40,8 +40,10 @@ def aqlm_moe_route(x, router, k, score="softmax", bias=None, renorm=True, scale=
     """(ids int32 [tokens][k], weights fp32 [tokens][k]) of fp16 x [tokens][in] and router [experts][in] (see aqlm.h).
 
     bias: fp32 [experts], added to the scores for the choice only."""
-    if score not in SCORES:
-        raise ValueError(f"score must be one of {', '.join(SCORES)}")
+    try:
+        how = SCORES[score]
+    except (KeyError, TypeError):
+        raise ValueError(f"score must be one of {', '.join(SCORES)}") from None
     dev, tokens = _rows("x", x)
     if router.dim() != 2:
         raise ValueError("router must be [experts][in]")
@@ -53,7 +55,7 @@ def aqlm_moe_route(x, router, k, score="softmax", bias=None, renorm=True, scale=
         raise ValueError("k must be between 1 and the number of experts")
     keep, ws, nws = _workspace(workspace, lambda: moe_route_workspace_bytes(experts, n_in, k, tokens), dev)
     ids, weights = x.new_empty((tokens, k), dtype=_I32), x.new_empty((tokens, k), dtype=_F32)
-    _call("aqlm_moe_route", dev, px, pr, pb, ids.data_ptr(), weights.data_ptr(), ws, nws, SCORES[score], int(bool(renorm)),
+    _call("aqlm_moe_route", dev, px, pr, pb, ids.data_ptr(), weights.data_ptr(), ws, nws, how, int(bool(renorm)),
           float(scale), experts, n_in, k, tokens)
     return ids, weights
 

@@ -29,16 +29,21 @@ def _pair(name, codes, scales, dev):
             _tensor(f"{name} scales", scales, dev, (rows, n_in // _BLOCK), _U8))
 
 
+def _bytes_of(name, t, like, dev, shape):
+    """A uint8 result, a new one if none is given, and its address."""
+    if t is None:
+        t = like.new_empty(shape, dtype=_U8)
+        return t, t.data_ptr()
+    return t, _tensor(name, t, dev, shape, _U8)
+
+
 def aqlm_mx4_quantize(w, codes=None, scales=None):
     """(codes, scales) of fp16 rows w [rows][in] (see aqlm.h)."""
     dev, rows = _rows("w", w)
     n_in = w.shape[1]
     pw = _tensor("w", w, dev, (rows, n_in))
-    if codes is None:
-        codes = w.new_empty((rows, n_in // 2), dtype=_U8)
-    if scales is None:
-        scales = w.new_empty((rows, n_in // _BLOCK), dtype=_U8)
-    pc, ps = _tensor("codes", codes, dev, (rows, n_in // 2), _U8), _tensor("scales", scales, dev, (rows, n_in // _BLOCK), _U8)
+    codes, pc = _bytes_of("codes", codes, w, dev, (rows, n_in // 2))
+    scales, ps = _bytes_of("scales", scales, w, dev, (rows, n_in // _BLOCK))
     _call("aqlm_mx4_quantize", dev, pw, pc, ps, rows, n_in)
     return codes, scales
 
@@ -49,7 +54,10 @@ def aqlm_mx4_decode(codes, scales, w=None):
     rows, n_in, pc, ps = _pair("the", codes, scales, dev)
     if w is None:
         w = codes.new_empty((rows, n_in), dtype=_F16)
-    _call("aqlm_mx4_decode", dev, pc, ps, _tensor("w", w, dev, (rows, n_in)), rows, n_in)
+        pw = w.data_ptr()
+    else:
+        pw = _tensor("w", w, dev, (rows, n_in))
+    _call("aqlm_mx4_decode", dev, pc, ps, pw, rows, n_in)
     return w
 
 

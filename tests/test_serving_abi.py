@@ -158,6 +158,8 @@ def test_the_binding_refuses(lib):
             call()
     with pytest.raises(ValueError, match="score must be"):
         E.aqlm_moe_route(f16(1, 64), f16(4, 64), 2, score="top")
+    with pytest.raises(ValueError, match="score must be"):
+        E.aqlm_moe_route(f16(1, 64), f16(4, 64), 2, score=["softmax"])
     with pytest.raises(ValueError, match="act must be one of"):
         E.aqlm_mx4_linear(u8(2, 32), u8(2, 2), f16(1, 64), act="swish")
     with pytest.raises(ValueError, match="pair"):
