@@ -219,4 +219,113 @@ __device__ __forceinline__ void mx4_body(const uint8_t* __restrict__ wq, const u
     }
 }
 
+// The same for up to 16 columns of split activations in LDS, rows of at least kMxWideBlocks blocks, and workgroups of few tiles.  A
+// step's activations are read when its turn comes, for all tiles of the group; that leaves registers to write the loads without
+// branches.  The compiler counts the loads in flight and waits for the oldest; where paths with and without a load meet it waits for all
+// of them, so the last round, which loads nothing, is code of its own.  Past a workgroup's last tile its loads repeat that tile.
+template <int NK, int TILES, class RowOf, class Prepare, class Fin>
+__device__ __forceinline__ void mx4_body_lds(const uint8_t* __restrict__ wq, const uint8_t* __restrict__ ws, const SplitRows xs,
+                                             const int xrow, const MxSteps st, const int bid, const int nwg, const int n_tiles,
+                                             float* red, RowOf row_of, Prepare prepare, Fin fin) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int q = lane >> 4;
+    const int nb = st.nb;
+    if (bid >= n_tiles) return;   // uniform
+    const int last = bid + (n_tiles - 1 - bid) / nwg * nwg;
+    auto first = [&](int c) { return (c * kMxWaves + wave) * NK; };   // this wave's first step of chunk c
+    auto base = [&](int tile) { return (size_t)row_of(min(tile, last)) * nb; };
+
+    u32x4 cw[TILES][NK];
+    uint32_t cs[TILES][4], next[TILES][4];
+    auto load_codes = [&](int i, int j, size_t row, int c) {
+        cw[i][j] = load16(wq + (row + min(4 * (first(c) + j) + q, nb - 1)) * kMxBlockBytes);
+    };
+    auto load_scales = [&](uint32_t (&to)[4], size_t row, int c) {
+        typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+        const u32x4_any v = *reinterpret_cast<const u32x4_any*>(ws + row + min(4 * first(c), nb - kMxWideBlocks));
+#pragma unroll
+        for (int d = 0; d < 4; ++d) to[d] = v[d];
+    };
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) load_scales(cs[i], base(bid + i * nwg), 0);
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) load_codes(i, j, base(bid + i * nwg), 0);
+    prepare();
+
+    f32x4 acc[TILES];
+    auto run = [&](auto more, int c, int tn, int cn) {
+        const int d = min(max(4 * first(c) - (nb - kMxWideBlocks), 0), kMxWideBlocks);   // uniform
+        if (d != 0) {
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                const u32x4 v = move_bytes(u32x4{cs[i][0], cs[i][1], cs[i][2], cs[i][3]}, d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cs[i][j] = v[j];
+            }
+        }
+        size_t row[TILES];
+        if constexpr (decltype(more)::value) {
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                row[i] = base(tn + i * nwg);
+                load_scales(next[i], row[i], cn);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+            const int b = 4 * (first(c) + j) + q;
+            const bool in_row = b < nb;
+            MxOperand<kFmt6> x;
+            x.load(MxInputRows<kFmt6>{xs}, xrow, min(b, nb - 1), in_row);
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                // past the row: codes 0 with a scale of 1, whatever was loaded
+                u32x4 a = cw[i][j];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) a[w] = in_row ? a[w] : 0u;
+                acc[i] = x.product(a, in_row ? cs[i][j] >> 8 * q : 127u, acc[i]);
+                if constexpr (decltype(more)::value) load_codes(i, j, row[i], cn);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if constexpr (decltype(more)::value) {
+#pragma unroll
+            for (int i = 0; i < TILES; ++i)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) cs[i][w] = next[i][w];
+        }
+    };
+    for (int t0 = bid; t0 < n_tiles; t0 += nwg * TILES) {
+        const int after = t0 + nwg * TILES;
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const bool end = after >= n_tiles;
+        for (int c = 0; c < st.chunks - (int)end; ++c) {
+            const bool same = c + 1 < st.chunks;
+            run(std::true_type{}, c, same ? t0 : after, same ? c + 1 : 0);
+        }
+        if (end) run(std::false_type{}, st.chunks - 1, 0, 0);
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) pin(acc[i]);
+        const int left = (n_tiles - t0 + nwg - 1) / nwg;   // tiles of this group
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+            if (i >= left) continue;
+            *reinterpret_cast<f32x4*>(red + (i * kMxWaves + wave) * 256 + (lane & 15) * kMxRows + 4 * q) = acc[i];
+        }
+        __syncthreads();
+        fin(t0, min(left, TILES), [&](int i, int col, int r) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kMxWaves; ++w) s += red[(i * kMxWaves + w) * 256 + col * kMxRows + r];
+            return s;
+        });
+        __syncthreads();
+    }
+}
+
 }  // namespace aqlm

@@ -30,7 +30,7 @@ struct MxEpilogue {
 // of its own for the split costs more from there down.
 constexpr int kInlineBlocks = 1024;
 
-template <int CT, int NK, int FMT, bool INLINE, bool WIDE = false>
+template <int CT, int NK, int FMT, bool INLINE, bool WIDE = false, int TILES = mx4_tiles(CT)>
 __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales, const void* x,
                                                               const void* xs, MxSteps st, int out, int T, MxEpilogue e) {
@@ -59,35 +59,39 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
             mine[q] = load_block16(static_cast<const f16*>(x) + (size_t)min((int)threadIdx.x + q * kMxThreads, T * st.nb - 1) * kMxBlock);
     }
     const int nwg = (int)gridDim.x;
-    mx4_body<CT, NK, FMT, false, mx4_tiles(CT), WIDE>(
-        codes, scales, xin, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
-        [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); },
-        [&]() {
-            if constexpr (INLINE) {
+    const auto row_of = [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); };
+    const auto prepare = [&]() {
+        if constexpr (INLINE) {
 #pragma unroll
-                for (int q = 0; q < kMine; ++q) {
-                    const int i = threadIdx.x + q * kMxThreads;
-                    if (i >= T * st.nb) break;
-                    uint32_t o[kSplitDwords], s;
-                    split_block(mine[q], o, s);
-                    store_split(xin.rows, i / st.nb, i % st.nb, o, s);
-                }
-                __syncthreads();
+            for (int q = 0; q < kMine; ++q) {
+                const int i = threadIdx.x + q * kMxThreads;
+                if (i >= T * st.nb) break;
+                uint32_t o[kSplitDwords], s;
+                split_block(mine[q], o, s);
+                store_split(xin.rows, i / st.nb, i % st.nb, o, s);
             }
-        },
-        [&](int t0, int n, auto sum) {
-            for (int idx = threadIdx.x; idx < n * cols * kMxRows; idx += kMxThreads) {
-                const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, col = ic - i * cols;
-                const int row = (t0 + i * nwg) * kMxRows + r;
-                if (row >= out) continue;
-                float v[1] = {sum(i, col, r)};
-                if (e.bias != nullptr) v[0] += (float)e.bias[row];
-                act_values(e.act, v);
-                const size_t at = (size_t)(col0 + col) * out + row;
-                if (e.residual != nullptr) v[0] += (float)e.residual[at];
-                e.y[at] = (f16)v[0];
-            }
-        });
+            __syncthreads();
+        }
+    };
+    const auto fin = [&](int t0, int n, auto sum) {
+        for (int idx = threadIdx.x; idx < n * cols * kMxRows; idx += kMxThreads) {
+            const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, col = ic - i * cols;
+            const int row = (t0 + i * nwg) * kMxRows + r;
+            if (row >= out) continue;
+            float v[1] = {sum(i, col, r)};
+            if (e.bias != nullptr) v[0] += (float)e.bias[row];
+            act_values(e.act, v);
+            const size_t at = (size_t)(col0 + col) * out + row;
+            if (e.residual != nullptr) v[0] += (float)e.residual[at];
+            e.y[at] = (f16)v[0];
+        }
+    };
+    if constexpr (INLINE && WIDE && TILES <= 2) {
+        mx4_body_lds<NK, TILES>(codes, scales, xin.rows, xrow[0], st, (int)blockIdx.x, nwg, n_tiles, red, row_of, prepare, fin);
+    } else {
+        mx4_body<CT, NK, FMT, false, TILES, WIDE>(codes, scales, xin, xrow, st, (int)blockIdx.x, nwg, n_tiles, red, row_of, prepare,
+                                                  fin);
+    }
 }
 
 struct RowsCall {
@@ -98,9 +102,9 @@ struct RowsCall {
     hipStream_t stream;
 };
 
-template <int CT, int NK, int FMT, bool INLINE, bool WIDE = false>
+template <int CT, int NK, int FMT, bool INLINE, bool WIDE = false, int TILES = mx4_tiles(CT)>
 hipError_t launch_rows_v(const RowsCall& c) {
-    auto kern = mx4_rows_kernel<CT, NK, FMT, INLINE, WIDE>;
+    auto kern = mx4_rows_kernel<CT, NK, FMT, INLINE, WIDE, TILES>;
     const MxSteps st = mx4_steps(c.in, NK);
     const size_t lds = mx4_red_floats(CT) * sizeof(float) +
                        (INLINE ? (size_t)SplitRows::record_bytes(c.T) * st.nb : 0);
@@ -115,13 +119,32 @@ hipError_t launch_rows_v(const RowsCall& c) {
     return hipGetLastError();
 }
 
+// x split in LDS: one or two tiles a workgroup by mx4_body_lds, more by mx4_body, which keeps x in registers (4096 -> 4096 at 1 token
+// 5.7 us against 6.4, 4096 -> 8192 6.4 against 7.3; four tiles and more: 4096 -> 28672 17.6 against 16.3).
+template <int NK>
+hipError_t launch_inline(const RowsCall& c) {
+    return (c.out + kMxRows - 1) / kMxRows <= device_cu_count() ? launch_rows_v<1, NK, kFmt6, true, true, 1>(c)
+                                                                : launch_rows_v<1, NK, kFmt6, true, true, 2>(c);
+}
+
 template <int FMT, bool INLINE>
 hipError_t launch_rows(const RowsCall& c) {
     if constexpr (!INLINE) {
         if (c.T > 32) return launch_rows_v<4, 1, FMT, INLINE>(c);
         if (c.T > 16) return launch_rows_v<2, 2, FMT, INLINE>(c);
     }
-    return c.in >= kMxWideBlocks * kMxBlock ? launch_rows_v<1, 4, FMT, INLINE, true>(c) : launch_rows_v<1, 1, FMT, INLINE>(c);
+    if (c.in < kMxWideBlocks * kMxBlock) return launch_rows_v<1, 1, FMT, INLINE>(c);
+    if constexpr (INLINE) {
+        if ((c.out + kMxRows - 1) / kMxRows <= 2 * device_cu_count()) {
+            switch (mx4_steps(c.in, 4).nk) {
+                case 1: return launch_inline<1>(c);
+                case 2: return launch_inline<2>(c);
+                case 3: return launch_inline<3>(c);
+                default: return launch_inline<4>(c);
+            }
+        }
+    }
+    return launch_rows_v<1, 4, FMT, INLINE, true>(c);
 }
 
 bool split_inline(int64_t in, int64_t batch) { return batch <= 16 && batch * (in / kMxBlock) <= kInlineBlocks; }

@@ -145,6 +145,12 @@ def test_linear_of_33_to_64_tokens_and_long_rows(n_in, out, t, four):
     test_linear(n_in, out, t, four)
 
 
+@pytest.mark.parametrize("n_in,out,t", [(512, 4100, 1), (2080, 4096, 5), (4096, 4113, 8), (3104, 8192, 1), (12000, 4200, 2), (32768, 40, 1),
+                                        (24576, 4100, 1), (512, 8193, 16)])
+def test_linear_of_one_and_two_tiles_a_workgroup(n_in, out, t):
+    test_linear(n_in, out, t, False)
+
+
 @pytest.mark.parametrize("t", [1, 6, 20, 33, 65])
 @pytest.mark.parametrize("four", [False, True], ids=["fp16", "mx4"])
 @pytest.mark.parametrize("n_in,out", [(1024, 65800), (8192, 8320), (8192, 16500)])
