@@ -2,7 +2,9 @@
 // product, weighted sum, in three launches.
 //
 // Bounds: the codes of the experts that are asked for, read once per 16 tokens (down: 8) of an expert; then the lookups, and for a
-// single token the fixed latencies of the launches.
+// single token the fixed latencies of the launches.  2x8, 64 experts of 2048 x 1408, 1 token of 8: 24 us in a graph (gate and up 11.6,
+// down 9.0, combining 2); 1x16, 8 experts of 4096 x 11008, 16 tokens of 2: 583 us, 231 G gathers a second of the 264 that a kernel of
+// nothing else reaches.
 //
 // The products are those of gemv_act.hip: workgroups of 16 waves that hold the expert's codebooks in LDS (2x8, 1x8 g4,
 // 4x8 g16) or gather codewords from L2 (1x16), on the columns that moe_plan.h finds.  An expert's workgroups are neighbours on
