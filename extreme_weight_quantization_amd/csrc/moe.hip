@@ -41,7 +41,8 @@ struct MoeProduct {
     float fixed;     // cost of starting on an item, in items
 };
 
-constexpr int moe_chunk(int kind) { return kind == kGemvPartAt ? 8 : 16; }
+// Pairs of an item: as many as a way for x to reach the registers has columns for (two a pair in the down product).
+constexpr int moe_chunk(int kind, int xm = kXDirect) { return (xm == kXStaged8 ? 8 : 16) / (kind == kGemvPartAt ? 2 : 1); }
 
 template <int KIND>
 __device__ __forceinline__ GemvEpi expert_epi(const MoeProduct& p, int e) {
@@ -58,15 +59,15 @@ __device__ __forceinline__ GemvEpi expert_epi(const MoeProduct& p, int e) {
 template <int SCHEME, int REPL, bool VEC, int XM, int KIND, int TEAM>
 __global__ __launch_bounds__(kGemvThreads) void moe_gemv_kernel(MoeProduct p) {
     __shared__ MoeLds m;
-    constexpr int kChunk = moe_chunk(KIND);
+    constexpr int kChunk = moe_chunk(KIND, XM);
     constexpr int kTile = gemv_gated(KIND) ? kRowTile / 2 : kRowTile;
-    const MoeItems items = moe_items<kChunk>(p.ids, p.pairs, p.experts, m);
+    const MoeItems items = moe_items<moe_chunk(KIND)>(p.ids, p.pairs, p.experts, kChunk, m);
     const int n = items.n;
     const int tiles = (p.rows + kTile - 1) / kTile;
     const int parts = moe_parts(n, (int)gridDim.x, tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.pairs, p.k, m, e);
+        const int cols = moe_item<KIND == kGemvPartAt>(items, u / parts, p.pairs, p.k, kChunk, m, e);
         gemv_body<SCHEME, REPL, VEC, rtp(TEAM), XM, KIND, TEAM>(
             p.codes[0] + p.codes_stride * e, p.codebooks[0] + p.codebooks_stride * e, p.scales[0] + (size_t)p.rows * e, p.h, p.rows,
             u % parts, parts, p.x, p.in, KIND == kGemvPartAt ? 2 * cols : cols, expert_epi<KIND>(p, e),
@@ -93,7 +94,8 @@ hipError_t launch_v(const MoeProduct& p, hipStream_t stream) {
                                                 : launch_team<SCHEME, REPL, XM, KIND, kGemvWaves>(p, stream);
 }
 
-// How x reaches the registers, by the most columns an item can have: as gemv_act.hip chooses.
+// How x reaches the registers, by the most columns of an expert whose pairs belong to different tokens: as gemv_act.hip chooses.
+// Where tokens name an expert twice it may have more; they are an item of their own then (moe_chunk).
 template <int KIND>
 hipError_t launch_tuned(int scheme, const MoeProduct& p, int cols, hipStream_t stream) {
     const bool one = cols <= 2, eight = cols <= 8;
@@ -127,12 +129,12 @@ __global__ __launch_bounds__(kGemvThreads) void moe_generic_kernel(MoeProduct p,
     const uint32_t mask = (1u << B) - 1u;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n_grp = p.in / G;
-    const MoeItems items = moe_items<kChunk>(p.ids, p.pairs, p.experts, m);
+    const MoeItems items = moe_items<moe_chunk(KIND)>(p.ids, p.pairs, p.experts, kChunk, m);
     const int n = items.n;
     const int parts = moe_parts(n, (int)gridDim.x, (p.rows + 15) / 16, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kChunk, KIND == kGemvPartAt>(items, u / parts, p.pairs, p.k, m, e);
+        const int cols = moe_item<KIND == kGemvPartAt>(items, u / parts, p.pairs, p.k, kChunk, m, e);
         const GemvEpi epi = expert_epi<KIND>(p, e);
         const f16* scales = p.scales[0] + (size_t)p.rows * e;
         for (int row = u % parts * 16 + wave; row < p.rows; row += parts * 16) {

@@ -48,13 +48,13 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
     __shared__ float hb[kHold][kCols][kMxBlock + 1];
     constexpr int kNk = WIDE ? kMxMoeNk : 1;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
-    const MoeItems items = moe_items<kCols>(p.ids, p.pairs, p.experts, m);
+    const MoeItems items = moe_items<kCols>(p.ids, p.pairs, p.experts, kCols, m);
     const int n = items.n;
     const int tiles = GATED ? (p.rows + kHalf - 1) / kHalf : (p.rows + kMxRows - 1) / kMxRows;
     const int parts = moe_parts(n, (int)gridDim.x, GATED ? (tiles + 3) / 4 : tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<kCols, false>(items, u / parts, p.pairs, p.k, m, e);
+        const int cols = moe_item<false>(items, u / parts, p.pairs, p.k, kCols, m, e);
         const size_t row0 = (size_t)p.rows * e * p.st.nb;   // the expert's first block
         const int r16 = lane & 15, layer = GATED && r16 >= kHalf;
         const uint8_t* wq = (layer ? p.codes[1] : p.codes[0]) + row0 * kMxBlockBytes;

@@ -2,8 +2,10 @@
 //
 // Which experts are asked for, and by whom, is known on the device only.  Every workgroup sorts the layer's pairs (token,
 // choice) by expert in its LDS, at most 1024 of them: it counts each expert's, and finds the pairs of the items that it takes by a
-// vote of 64 lanes at a time.  A launch of its own would take two microseconds.  Up to CHUNK pairs of one expert are an item: its weights are read once for them.  Items are cut
-// into `parts` so that parts x items fill the launch's workgroups evenly.
+// vote of 64 lanes at a time.  A launch of its own would take two microseconds.  Up to `chunk` pairs of one expert are an item: its
+// weights are read once for them.  chunk is what the kernel has columns for, whatever tokens they belong to: a token may name an
+// expert more than once, so an expert can have more pairs than there are tokens.  Items are cut into `parts` so that parts x items
+// fill the launch's workgroups evenly.
 #pragma once
 #include "aqlm_device.h"
 #include "moe_launch.h"
@@ -22,8 +24,8 @@ struct MoeLds {
     uint16_t x[16], y[16];           // its columns: rows of the input, pairs
 };
 
-// What a workgroup knows about the items.  few: no more pairs than an item takes, so every expert that is asked for is one item;
-// lane p of each wave then holds pair p: its expert, the pairs of the same expert, and (all lanes) the first pair of each expert.
+// What a workgroup knows about the items.  few: at most FEW pairs, and no expert has more than an item takes, so every expert that is
+// asked for is one item; lane p of each wave then holds pair p: its expert, the pairs of the same expert, and (all lanes) the first pair of each expert.
 struct MoeItems {
     int n;
     bool few;
@@ -43,15 +45,18 @@ __device__ __forceinline__ uint64_t same_expert(uint32_t e) {
 }
 
 // Counts the pairs.  All threads of the workgroup (at least 512) call it.  A pair whose id is no expert is left out.
-template <int CHUNK>
-__device__ __forceinline__ MoeItems moe_items(const int32_t* __restrict__ ids, int pairs, int experts, MoeLds& m) {
-    if (pairs <= CHUNK) {
+template <int FEW>
+__device__ __forceinline__ MoeItems moe_items(const int32_t* __restrict__ ids, int pairs, int experts, int chunk, MoeLds& m) {
+    static_assert(FEW <= kWave, "a lane a pair");
+    if (pairs <= FEW) {
         const int lane = threadIdx.x & (kWave - 1);
         const int id = ids[min(lane, pairs - 1)];
         const uint32_t e = lane < pairs && id >= 0 && id < experts ? (uint32_t)id : kMoeNone;
         const uint64_t same = same_expert(e);
         const uint64_t firsts = __ballot(e != kMoeNone && __builtin_ctzll(same | 1ull << 63) == lane);
-        return MoeItems{(int)__popcll(firsts), true, e, same, firsts};
+        // all waves read the same ids: the workgroup goes one way
+        if (pairs <= chunk || __ballot(e != kMoeNone && __popcll(same) > chunk) == 0)
+            return MoeItems{(int)__popcll(firsts), true, e, same, firsts};
     }
     const int tid = threadIdx.x, n = blockDim.x;
     if (tid < kMoeMaxExperts) m.count[tid] = 0;
@@ -68,7 +73,7 @@ __device__ __forceinline__ MoeItems moe_items(const int32_t* __restrict__ ids, i
         int c[kPer], items = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            c[i] = (m.count[tid * kPer + i] + CHUNK - 1) / CHUNK;
+            c[i] = (m.count[tid * kPer + i] + chunk - 1) / chunk;
             items += c[i];
         }
         int t = items;
@@ -107,9 +112,10 @@ __device__ __forceinline__ int moe_parts(int n, int wgs, int most, float fixed) 
 }
 
 // Makes item v the one at hand: its expert e, and m.x (rows of the input) and m.y (pairs) for its pairs; returns how
-// many there are.  An expert's pairs keep their order: workgroups that take parts of one item must agree on its pairs.  PAIRED: the input has two rows for a pair (2 pair, 2 pair + 1), else one for its token.  Ends with a barrier.
-template <int CHUNK, bool PAIRED>
-__device__ __forceinline__ int moe_item(const MoeItems& items, int v, int pairs, int k, MoeLds& m, int& e) {
+// many there are.  An expert's pairs keep their order: workgroups that take parts of one item must agree on its pairs.  PAIRED: the
+// input has two rows for a pair (2 pair, 2 pair + 1), else one for its token.  chunk: as for moe_items.  Ends with a barrier.
+template <bool PAIRED>
+__device__ __forceinline__ int moe_item(const MoeItems& items, int v, int pairs, int k, int chunk, MoeLds& m, int& e) {
     const int tid = threadIdx.x;
     int n;
     auto keep = [&](int place, int p) {
@@ -136,8 +142,8 @@ __device__ __forceinline__ int moe_item(const MoeItems& items, int v, int pairs,
         if (tid < kMoeMaxExperts && m.item0[tid] <= v && v < m.item0[tid + 1]) m.expert = tid;
         __syncthreads();
         e = __builtin_amdgcn_readfirstlane(m.expert);
-        const int from = __builtin_amdgcn_readfirstlane((v - m.item0[e]) * CHUNK);   // the item's first pair among the expert's
-        n = min(CHUNK, m.count[e] - from);
+        const int from = __builtin_amdgcn_readfirstlane((v - m.item0[e]) * chunk);   // the item's first pair among the expert's
+        n = min(chunk, m.count[e] - from);
         if (tid < kWave) {
             int before = 0;   // of the expert's pairs
             for (int p0 = 0; p0 < pairs && before < from + n; p0 += kWave) {
