@@ -36,10 +36,12 @@ struct MoeMxProduct {
     const int32_t* ids;
     MxSteps st;
     int experts, pairs, k, rows, act;
+    int cols;                // INLINE: columns that LDS has room for
     float fixed;
 };
 
-// INLINE (gate and up): p.x is fp16 rows, and each workgroup splits those of its item into LDS, at most kInlineBlocks blocks.
+// INLINE (gate and up): p.x is fp16 rows, and each workgroup splits those of its item into LDS, at most kInlineBlocks blocks.  An item
+// has no more pairs than there are tokens then; an expert that a token names twice may have more, which are an item of their own.
 template <bool GATED, bool INLINE, bool WIDE>
 __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
     extern __shared__ u32x4 smem[];
@@ -48,13 +50,14 @@ __global__ __launch_bounds__(kMxThreads) void moe_mx4_kernel(MoeMxProduct p) {
     __shared__ float hb[kHold][kCols][kMxBlock + 1];
     constexpr int kNk = WIDE ? kMxMoeNk : 1;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
-    const MoeItems items = moe_items<kCols>(p.ids, p.pairs, p.experts, kCols, m);
+    const int most = INLINE ? p.cols : kCols;   // pairs of an item
+    const MoeItems items = moe_items<kCols>(p.ids, p.pairs, p.experts, most, m);
     const int n = items.n;
     const int tiles = GATED ? (p.rows + kHalf - 1) / kHalf : (p.rows + kMxRows - 1) / kMxRows;
     const int parts = moe_parts(n, (int)gridDim.x, GATED ? (tiles + 3) / 4 : tiles, p.fixed);
     for (int u = xcd_run((int)blockIdx.x, (int)gridDim.x); u < n * parts; u += (int)gridDim.x) {
         int e;
-        const int cols = moe_item<false>(items, u / parts, p.pairs, p.k, kCols, m, e);
+        const int cols = moe_item<false>(items, u / parts, p.pairs, p.k, most, m, e);
         const size_t row0 = (size_t)p.rows * e * p.st.nb;   // the expert's first block
         const int r16 = lane & 15, layer = GATED && r16 >= kHalf;
         const uint8_t* wq = (layer ? p.codes[1] : p.codes[0]) + row0 * kMxBlockBytes;
@@ -178,7 +181,8 @@ hipError_t launch_moe_mx4(const MoeMx4Layers& L, const MoeCall& c, void* workspa
     p.rows = (int)c.inner;
     p.act = c.act;
     p.fixed = start_cost(2, c.inner, c.in);
-    const int lds = inlined ? SplitRows::record_bytes(std::min(c.tokens, kCols)) * (int)(c.in / kMxBlock) : 0;
+    p.cols = std::min(c.tokens, kCols);
+    const int lds = inlined ? SplitRows::record_bytes(p.cols) * (int)(c.in / kMxBlock) : 0;
     r = inlined ? launch_product<true, true>(p, lds, stream) : launch_product<true, false>(p, lds, stream);
     if (r != hipSuccess) return r;
     p.codes[0] = static_cast<const uint8_t*>(L.codes[2]);

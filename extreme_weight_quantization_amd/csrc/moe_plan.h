@@ -70,10 +70,11 @@ __device__ __forceinline__ MoeItems moe_items(const int32_t* __restrict__ ids, i
     __syncthreads();
     if (tid < kWave) {
         constexpr int kPer = kMoeMaxExperts / kWave;
+        const uint32_t inverse = 65536u / (uint32_t)chunk + 1u;   // n inverse >> 16 is n / chunk for n < 1040, chunk <= 16
         int c[kPer], items = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            c[i] = (m.count[tid * kPer + i] + chunk - 1) / chunk;
+            c[i] = (int)((uint32_t)(m.count[tid * kPer + i] + chunk - 1) * inverse >> 16);
             items += c[i];
         }
         int t = items;

@@ -49,3 +49,28 @@ def test_aqlm_experts(scheme, tokens, k, how):
 def test_aqlm_experts_with_long_rows(scheme, tokens, k):
     """Rows of more than 2048 inputs: 16 waves a tile instead of two teams."""
     run(scheme, 2080, 2112, tokens, k, "partly")
+
+
+@pytest.mark.parametrize("how", ["all", "partly"])
+@pytest.mark.parametrize("tokens,k", TOKENS_K)
+def test_mx4_experts(tokens, k, how):
+    run("mx4", 96, 64, tokens, k, how)
+
+
+@pytest.mark.parametrize("n_in,inner,tokens,k", [(4096, 96, 1, 4), (4096, 96, 7, 2), (4096, 64, 8, 8), (2048, 1056, 15, 4),
+                                                 (32768, 32, 1, 2), (16384, 32, 2, 8), (16384, 32, 3, 8), (1056, 4128, 5, 4)])
+def test_mx4_experts_with_long_rows(n_in, inner, tokens, k):
+    """Activations split in LDS, up to the most that fit, and split before."""
+    run("mx4", n_in, inner, tokens, k, "partly")
+
+
+@pytest.mark.parametrize("scheme", [(2, 8, 8), (1, 16, 8), "mx4"], ids=["2x8", "1x16", "mx4"])
+def test_padding_rows_of_a_batch_leave_the_others_alone(scheme):
+    """Rows behind the last token that all name expert 0, as a captured batch has them: the tokens' results are those of the
+    batch without them."""
+    L = Layer(scheme, 4, 160, 96, seed=5)
+    x, ids, w, residual = L.inputs(8, 2, seed=6)
+    x[5:], ids[5:], w[5:], residual[5:] = 0, 0, 0, 0
+    y = L.check(x, ids, w, "silu", residual).cpu()
+    assert float(y[5:].abs().max()) == 0
+    assert torch.equal(y[:5], L.run(x[:5], ids[:5], w[:5], residual=residual[:5]).cpu())
