@@ -461,7 +461,8 @@ GemmPlan gemm_plan(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
 //   17 tokens   8192 -> 28672: 53 53 | 39 24; x in MX4, 32 tokens   8192 -> 11008: 22 17    4096 -> 11008: 12 13
 //   x in MX4, 1 token   8192 -> 28672: 28 22    8192 -> 16384: 17 18    4096 -> 28672: 15 14
 bool mx4_gemm_serves(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
-    if (out * (in / kMxBlock) < 16) return false;   // load_bytes16's least array
+    // load_bytes16's least array: the scales of W, and of x where they are read
+    if ((x_mx4 ? std::min(out, batch) : out) * (in / kMxBlock) < 16) return false;
     return batch > kNarrow || (batch > 32 && (in >= 4096 || out * in >= (int64_t)1 << 25)) ||
            (x_mx4 && out * in > (int64_t)1 << (batch > 16 ? 26 : 27));
 }
