@@ -453,9 +453,11 @@ int max_splits(int64_t in) { return (int)std::max<int64_t>(1, std::min<int64_t>(
 // 24 in 64 bits, 2048 tokens 30 against 36; 256 experts: 512 tokens 38 against 40, 1024 tokens 43 against 61.
 constexpr int64_t kFastFrom = (int64_t)1 << 29;
 constexpr int kFastMaxSplits = 4;
-RoutePlan route_plan(int64_t experts, int64_t in, int64_t tokens, bool fast_ok) {
+// Tokens of a launch: a grid has fewer than 2^32 threads, and 512 experts take 512 threads a token in 64 bits.
+constexpr int64_t kLaunchTokens = (int64_t)1 << 22;
+RoutePlan route_plan(int64_t experts, int64_t in, int64_t tokens, bool fast) {
     RoutePlan p;
-    p.fast = fast_ok && tokens * experts >= kFastFrom / in;
+    p.fast = fast;
     const int tile = p.fast ? kFastTile : kTile;
     p.tiles_e = (int)((experts + tile - 1) / tile);
     p.tiles_t = (int)((tokens + tile - 1) / tile);
@@ -474,6 +476,7 @@ RoutePlan route_plan(int64_t experts, int64_t in, int64_t tokens, bool fast_ok) 
 
 int64_t route_workspace(int64_t experts, int64_t in, int64_t tokens) {
     if (tokens == 0) return 0;
+    tokens = std::min(tokens, kLaunchTokens);   // parts of a larger batch take turns
     // Sums: splits * tokens * experts.  splits * tiles grows with the batch up to its cap and then with the batch alone, so
     // the larger of both bounds covers this batch and every smaller one.  Norms behind them.
     const int64_t te = (experts + kTile - 1) / kTile, tt = (tokens + kTile - 1) / kTile;
@@ -483,9 +486,10 @@ int64_t route_workspace(int64_t experts, int64_t in, int64_t tokens) {
     return std::max(rows, fast_rows) * experts * (int64_t)sizeof(double) + kFastMaxSplits * (tokens + experts) * (int64_t)sizeof(float);
 }
 
-hipError_t launch_route(const RouteCall& c, void* workspace, hipStream_t stream) {
-    // softmax scores with a bias compare sums over all logits
-    const RoutePlan p = route_plan(c.experts, c.in, c.tokens, c.score == kScoreSigmoid || c.bias == nullptr);
+namespace {
+
+// The tokens of c, at most kLaunchTokens, by plan p.
+hipError_t launch_part(const RouteCall& c, const RoutePlan& p, void* workspace, hipStream_t stream) {
     double* part = static_cast<double*>(workspace);
     const f16 *x = static_cast<const f16*>(c.x), *r = static_cast<const f16*>(c.router);
     const dim3 tiles((unsigned)((int64_t)p.tiles_e * p.tiles_t * p.splits));
@@ -513,6 +517,23 @@ hipError_t launch_route(const RouteCall& c, void* workspace, hipStream_t stream)
     else AQLM_PICK(8);
 #undef AQLM_PICK
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteCall& c, void* workspace, hipStream_t stream) {
+    // for all parts of the batch alike; softmax scores with a bias compare sums over all logits
+    const bool fast = (c.score == kScoreSigmoid || c.bias == nullptr) && c.tokens * c.experts * c.in >= kFastFrom;
+    for (int64_t t = 0; t < c.tokens; t += kLaunchTokens) {
+        RouteCall part = c;
+        part.tokens = std::min(kLaunchTokens, c.tokens - t);
+        part.x = static_cast<const f16*>(c.x) + t * c.in;
+        part.ids = c.ids + t * c.k;
+        part.weights = c.weights + t * c.k;
+        const hipError_t e = launch_part(part, route_plan(c.experts, c.in, part.tokens, fast), workspace, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace aqlm

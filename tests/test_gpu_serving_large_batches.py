@@ -1,6 +1,4 @@
 """The largest batches: more workgroups than one launch takes, which are launched in parts of the batch."""
-import math
-
 import pytest
 import torch
 
@@ -39,3 +37,27 @@ def test_linear_of_tiny_layers_and_many_tokens(n_in, out, t, four):
     # equal tokens have equal results but for the residual: all of them, on the GPU
     plain = E.aqlm_mx4_linear(codes.cuda(), scales.cuda(), xin, act="silu", bias=bias.cuda())
     assert torch.equal(plain, plain[:1000].repeat(-(-t // 1000), 1)[:t])
+
+
+@pytest.mark.parametrize("score,biased", [("softmax", True), ("sigmoid", False)])
+@pytest.mark.parametrize("tokens", [(1 << 22) + 1, (1 << 23) + 19])
+def test_route_of_the_most_tokens(score, biased, tokens):
+    """512 experts, in 64 bits (softmax with a bias) and with sums of 32: more than 2^32 threads in all."""
+    experts, n_in, k = 512, 8, 3
+    some = torch.randn((4096, n_in), generator=gen(5)).half()
+    router = torch.randn((experts, n_in), generator=gen(6)).half()
+    bias = torch.randn(experts, generator=gen(7)) * 0.1 if biased else None
+    x = some.cuda().repeat(-(-tokens // 4096), 1)[:tokens].contiguous()
+    ids, w = E.aqlm_moe_route(x, router.cuda(), k, score=score, bias=None if bias is None else bias.cuda())
+    want_i, want_w = route_reference(some, router, k, score, bias, True, 1.0)
+    assert torch.equal(ids[:4096].cpu(), want_i)
+    # sums of 8 products in fp32: d = 8 2^-23 |x| |r| at most
+    d = 2.0 ** -20 * some.double().norm(dim=1, keepdim=True) * router.double().norm(dim=1).max()
+    assert bool(((w[:4096].cpu().double() - want_w).abs() <= (torch.expm1(2 * d) + 2.0 ** -23) * want_w).all())
+    for got in (ids, w):   # equal tokens, equal results: all of them
+        assert torch.equal(got, got[:4096].repeat(-(-tokens // 4096), 1)[:tokens])
+
+
+def test_route_workspace_of_the_most_tokens():
+    sizes = [E.moe_route_workspace_bytes(512, 8, 3, t) for t in (1, 1000, 1 << 21, 1 << 22, (1 << 22) + 1, 1 << 24)]
+    assert sizes == sorted(sizes)
