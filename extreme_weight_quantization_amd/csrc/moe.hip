@@ -8,7 +8,7 @@
 //
 // The products are those of gemv_act.hip: workgroups of 16 waves that hold the expert's codebooks in LDS (2x8, 1x8 g4,
 // 4x8 g16) or gather codewords from L2 (1x16), on the columns that moe_plan.h finds.  An expert's workgroups are neighbours on
-// one XCD, whose L2 then holds its codebook.  The hidden vector h of a pair (token, choice) is kept as the sum of two fp16 numbers; the down
+// one XCD, whose L2 then holds its codebook.  The hidden vector h of a pair (token, choice) is kept as two fp16 numbers (gemv_finish_pair); the down
 // product takes both as columns.  Its results stay apart per pair, in fp32, and the last launch weights and adds a
 // token's pairs in the order of its choices: no atomics, the same result every time.
 #include <algorithm>
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(kGemvThreads) void moe_generic_kernel(MoeProduct p,
                                     float lo[N];
                                     load_f16<N>(p.x + (size_t)m.x[2 * b + 1] * p.in + (size_t)j * G + q * N, lo);
 #pragma unroll
-                                    for (int t = 0; t < N; ++t) xv[t] += lo[t];
+                                    for (int t = 0; t < N; ++t) xv[t] += lo[t] * (1.f / kPairFine);
                                 }
 #pragma unroll
                                 for (int t = 0; t < N; ++t) d += v[q * N + t] * xv[t];
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(kGemvThreads) void moe_generic_kernel(MoeProduct p,
             for (int b = 0; b < kChunk; ++b) {   // lane b finishes column b
                 if (b < cols && lane == b) {
                     if constexpr (KIND == kGemvPartAt)
-                        p.part[(size_t)m.y[b] * p.rows + row] = acc[0][b] * (float)scales[row];
+                        p.part[(size_t)m.y[b] * p.rows + row] = acc[0][b] * kPairUnit * (float)scales[row];
                     else
                         gemv_finish_pair(acc[0][b], acc[kN - 1][b], scales, p.h, m.y[b], row, p.rows, epi);
                 }

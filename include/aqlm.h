@@ -540,8 +540,8 @@ int aqlm_mx4_linear(const void* codes, const void* scales, const void* x, const 
  *
  * Numerics: aqlm_moe multiplies every codeword on its own (no weight is
  * rounded), aqlm_moe_mx4 as aqlm_mx4_linear.  The hidden vector
- * act(.) * (.) is kept to 2^-22 of each element or 2^-25, whichever is larger
- * (infinite beyond fp16's range), for aqlm_moe_mx4 to 2^-19 of the largest in
+ * act(.) * (.) is kept to 2^-22 of each element or 2^-28, whichever is larger
+ * (infinite beyond 2^8 * 65504), for aqlm_moe_mx4 to 2^-19 of the largest in
  * its block of 32.  Sums are fp32, over a token's choices in their order; y is rounded to fp16
  * once.  Results are deterministic.
  */
