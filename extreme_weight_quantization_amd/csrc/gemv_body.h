@@ -19,11 +19,12 @@
 #include "act_math.h"
 #include "aqlm_device.h"
 #include "aqlm_launch.h"
+#include "hidden_pair.h"
 
 namespace aqlm {
 
 // KIND kGemvGatedAt, kGemvPartAt: an expert's products in a mixture-of-experts layer (moe.hip).  Column b of x is row
-//   rows.x[b], and results go to row rows.y[b] (GemvRows).  GatedAt writes act(zg) zu as two fp16 numbers (gemv_finish_pair), PartAt
+//   rows.x[b], and results go to row rows.y[b] (GemvRows).  GatedAt writes act(zg) zu as two fp16 numbers (hidden_pair.h), PartAt
 //   takes such pairs as columns 2b and 2b + 1 and writes their product in fp32.
 enum GemvKind : int { kGemvPlain = 0, kGemvAct = 1, kGemvGated = 2, kGemvGatedAt = 3, kGemvPartAt = 4 };
 constexpr bool gemv_gated(int kind) { return kind == kGemvGated || kind == kGemvGatedAt; }
@@ -71,20 +72,12 @@ __device__ __forceinline__ void gemv_finish(float p0, float p1, const f16* __res
     y[at] = (f16)v;
 }
 
-// kGemvGatedAt: h = act(zg) zu of (row `at`, `row`) as two fp16 numbers, rows 2 at and 2 at + 1 of y:
-//     h = kPairUnit (hi + lo / kPairFine),   hi = nearest(h / kPairUnit),   lo = nearest(kPairFine (h / kPairUnit - hi)).
-// One rounding to fp16 would add its error to that of the layer's own result; the second number costs a column that the matrix cores
-// multiply anyway.  hi is off by 2^-11 of itself or 2^-25, lo again: together 2^-22 |h| or 2^-36 kPairUnit = 2^-28.  The unit of 2^8
-// moves the range up, to |h| = 2^8 * 65504; kPairFine keeps lo out of fp16's subnormals and is the most that |lo| <= 2^-11 2^16 allows.
-constexpr float kPairUnit = 256.f, kPairFine = 2048.f;
+// kGemvGatedAt: h = act(zg) zu of (row `at`, `row`), kept as hidden_pair.h says.
 __device__ __forceinline__ void gemv_finish_pair(float p0, float p1, const f16* __restrict__ scales, f16* y, int at, int row,
                                                  int out, const GemvEpi& e) {
     float va[1] = {p0 * (float)scales[row]};
     act_values(e.act, va);
-    const float h = va[0] * (p1 * (float)e.scales1[row]) * (1.f / kPairUnit);
-    const f16 hi = (f16)h;
-    y[(size_t)(2 * at) * out + row] = hi;
-    y[(size_t)(2 * at + 1) * out + row] = fabsf((float)hi) < __builtin_inff() ? (f16)((h - (float)hi) * kPairFine) : (f16)0.f;
+    store_pair(va[0] * (p1 * (float)e.scales1[row]), y, at, row, out);
 }
 
 constexpr int kGemvWaves = 16;

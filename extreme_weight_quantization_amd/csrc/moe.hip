@@ -8,7 +8,7 @@
 //
 // The products are those of gemv_act.hip: workgroups of 16 waves that hold the expert's codebooks in LDS (2x8, 1x8 g4,
 // 4x8 g16) or gather codewords from L2 (1x16), on the columns that moe_plan.h finds.  An expert's workgroups are neighbours on
-// one XCD, whose L2 then holds its codebook.  The hidden vector h of a pair (token, choice) is kept as two fp16 numbers (gemv_finish_pair); the down
+// one XCD, whose L2 then holds its codebook.  The hidden vector h of a pair (token, choice) is kept as two fp16 numbers (hidden_pair.h); the down
 // product takes both as columns.  Its results stay apart per pair, in fp32, and the last launch weights and adds a
 // token's pairs in the order of its choices: no atomics, the same result every time.
 #include <algorithm>

@@ -1,4 +1,4 @@
-// Conversions between fp16 and MX4 (mx4.h), and of fp16 activations into the matrix cores' four-piece form.
+// Conversions between fp16 and MX4 (mx4.h).
 //
 // quantize: the scale of a block is 2^(floor(log2 max |v|) - 2), so that the largest value lies in [4, 8) of the 4-bit
 // floats' range; values are rounded to nearest even and at most 6.  A block of zeros takes scale byte 0, one with an
@@ -67,18 +67,6 @@ __global__ __launch_bounds__(kThreads) void mx4_decode_kernel(const uint32_t* __
     }
 }
 
-// A lane splits one block: neighbouring lanes, neighbouring tokens of a tile.
-__global__ __launch_bounds__(kThreads) void mx4_split_kernel(const f16* __restrict__ x, SplitRows to, int T, int64_t lanes) {
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < lanes; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t tb = i / kSplitTokens;
-        const int token = (int)(tb / to.nb) * kSplitTokens + (int)(i % kSplitTokens), block = (int)(tb % to.nb);
-        if (token >= T) continue;
-        uint32_t o[kSplitDwords], s;
-        split_block(load_block16(x + ((size_t)token * to.nb + block) * kMxBlock), o, s);
-        store_split(to, token, block, o, s);
-    }
-}
-
 dim3 flat_grid(int64_t threads, int per_cu) {
     return dim3((unsigned)std::min<int64_t>((threads + kThreads - 1) / kThreads, (int64_t)device_cu_count() * per_cu));
 }
@@ -95,18 +83,6 @@ hipError_t launch_mx4_decode(const void* codes, const void* scales, void* w, int
     hipLaunchKernelGGL(mx4_decode_kernel, flat_grid(blocks * 4, 32), dim3(kThreads), 0, stream,
                        static_cast<const uint32_t*>(codes), static_cast<const uint8_t*>(scales), static_cast<f16*>(w),
                        blocks * 4);
-    return hipGetLastError();
-}
-
-int64_t mx4_split_bytes(int64_t batch, int64_t in) {
-    return (batch + kSplitTokens - 1) / kSplitTokens * (in / kMxBlock) * kSplitRecord;
-}
-
-hipError_t launch_mx4_split(const void* x, void* records, int64_t in, int64_t batch, hipStream_t stream) {
-    const int nb = (int)(in / kMxBlock);
-    const int64_t lanes = (batch + kSplitTokens - 1) / kSplitTokens * kSplitTokens * nb;
-    hipLaunchKernelGGL(mx4_split_kernel, flat_grid(lanes, 8), dim3(kThreads), 0, stream, static_cast<const f16*>(x),
-                       SplitRows{static_cast<char*>(records), kSplitTokens, nb}, (int)batch, lanes);
     return hipGetLastError();
 }
 

@@ -9,7 +9,7 @@ namespace aqlm {
 bool mx4_gemm_serves(bool x_mx4, int64_t out, int64_t in, int64_t batch);
 // Bytes of fp32 parts it may write for any batch up to this one.
 int64_t mx4_gemm_part_bytes(int64_t out, int64_t in, int64_t batch);
-// x: MX4, or split records (scales NULL).
+// x: MX4, or fp16 rows (scales NULL).
 hipError_t launch_mx4_gemm(const void* codes, const void* scales, MxInput x, const Epilogue& e, void* part, int64_t out, int64_t in,
                            int64_t batch, hipStream_t stream);
 

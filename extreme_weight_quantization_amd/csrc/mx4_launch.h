@@ -10,9 +10,6 @@ namespace aqlm {
 // fp16 [blocks][32] to codes [blocks][16] and scales [blocks], and back (mx4_convert.hip).
 hipError_t launch_mx4_quantize(const void* w, void* codes, void* scales, int64_t blocks, hipStream_t stream);
 hipError_t launch_mx4_decode(const void* codes, const void* scales, void* w, int64_t blocks, hipStream_t stream);
-// fp16 rows [batch][in] to split records of 32 tokens (mx4.h), which take mx4_split_bytes.
-int64_t mx4_split_bytes(int64_t batch, int64_t in);
-hipError_t launch_mx4_split(const void* x, void* records, int64_t in, int64_t batch, hipStream_t stream);
 
 // Activations of an MX4 product: fp16 rows (scales NULL), or MX4 codes and scales.
 struct MxInput {
@@ -20,7 +17,7 @@ struct MxInput {
     const void* scales;
 };
 
-// Bytes of workspace launch_mx4_linear needs (the split activations), for any batch up to `batch`.
+// Bytes of workspace launch_mx4_linear needs (fp32 parts), for any batch up to `batch`.
 int64_t mx4_linear_workspace(bool x_mx4, int64_t out, int64_t in, int64_t batch);
 // y = act(W x + bias) + residual (Epilogue's first entries).
 hipError_t launch_mx4_linear(const void* codes, const void* scales, MxInput x, const Epilogue& e, void* workspace,

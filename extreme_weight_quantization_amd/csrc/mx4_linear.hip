@@ -1,14 +1,12 @@
 // Products of MX4 weights: y = act(W x + bias) + residual.
 //
-// z[t][i] = sum over blocks b of 2^(s_ib - 127) sum_k q_ibk x[t][32 b + k].  The scaled matrix instruction takes the codes
-// and their scales as they lie in memory; x is in MX4 too, or in fp16 as four 6-bit pieces (mx4.h), so a weight costs no
-// vector instruction.
+// z[t][i] = sum over blocks b of 2^(s_ib - 127) sum_k q_ibk x[t][32 b + k].  With x in MX4 the scaled matrix instruction takes
+// codes and scales of both as they lie in memory; with x in fp16 the codes are converted to fp16, which is exact (mx4.h).
 //
 // Few tokens (mx4_rows_kernel): the codes are read once, 17/32 of a byte a weight, and that bounds the time.  Matrix-core
-// rows are output rows, columns are tokens; a workgroup keeps the activations of all inputs in the registers of its 8 waves
-// (100 bytes a block and token: 12 KB of a wave's 64 KB for each step of 128 inputs and 16 tokens) and streams the rows
-// past them (mx4_body.h); with one or two tiles a workgroup it reads them from LDS.  1 token: 8192 -> 28672 29 us (4.3 TB/s),
-// 4096 -> 4096 5.7 in a graph (1.6 TB/s: latencies); 16 tokens 8192 -> 28672 38 us.
+// rows are output rows, columns are tokens; a workgroup keeps the activations of all inputs in LDS or in the registers of its 8
+// waves and streams the rows past them (mx4_body.h).  1 token: 8192 -> 28672 27.6 us in a graph (4.5 TB/s), 4096 -> 4096 5.2 (1.7 TB/s:
+// latencies); 16 tokens 8192 -> 28672 34 us.
 #include <algorithm>
 
 #include "act_math.h"
@@ -27,55 +25,24 @@ struct MxEpilogue {
     int act;
 };
 
-// Activations that are split inside the product: at most this many blocks of 32, 1.2 KB of LDS for every 12.  A launch
-// of its own for the split costs more from there down.
-// Blocks of x that a workgroup splits itself, into 100 KB of LDS; a launch of its own for the split costs 3 us (4096 -> 4096: 8 tokens
-// 8.5 us without, 16 tokens 9.1 with it).
-constexpr int kInlineBlocks = 1024;
-
-template <int CT, int NK, int FMT, bool INLINE, bool WIDE = false, int TILES = mx4_tiles(CT)>
+// How fp16 activations come: STAGED, up to 16 rows in LDS, where they fit; else, to 16 rows, in records of them, made by
+// mx4_records_kernel in a launch before, which 16 lanes read next to each other where rows would be 16 lines; else as they lie in memory.
+// us, 16 tokens, as they lie | so: 4096 -> 28672 in LDS 27 | 19.5, 8192 -> 11008 in records 21.6 | 17.7.
+template <int CT, int NK, int FMT, bool WIDE, int TILES, bool STAGED>
 __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __restrict__ codes,
-                                                              const uint8_t* __restrict__ scales, const void* x,
-                                                              const void* xs, MxSteps st, int out, int T, MxEpilogue e) {
+                                                              const uint8_t* __restrict__ scales, MxInputRows<FMT> xin,
+                                                              MxSteps st, int out, int T, MxEpilogue e) {
     extern __shared__ u32x4 smem[];
-    float* red = reinterpret_cast<float*>(smem);
+    __shared__ float red[TILES * kMxWaves * CT * 256];
     const int lane = threadIdx.x & (kWave - 1);
     const int col0 = (int)blockIdx.y * CT * 16, cols = min(T - col0, CT * 16);
     int xrow[CT];
 #pragma unroll
     for (int t = 0; t < CT; ++t) xrow[t] = min(col0 + t * 16 + (lane & 15), T - 1);
     const int n_tiles = (out + kMxRows - 1) / kMxRows;
-    MxInputRows<FMT> xin;
-    if constexpr (FMT == kFmt4) {
-        xin = {static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(xs), st.nb};
-    } else if constexpr (INLINE) {
-        xin.rows = SplitRows{reinterpret_cast<char*>(red + mx4_red_floats(CT)), T, st.nb};
-    } else {
-        xin.rows = SplitRows{static_cast<char*>(const_cast<void*>(x)), kSplitTokens, st.nb};
-    }
-    // Blocks that this thread splits, asked for in front of the first codes: loads come back in order.
-    constexpr int kMine = INLINE ? kInlineBlocks / kMxThreads : 1;
-    f16x32 mine[kMine];
-    if constexpr (INLINE) {
-#pragma unroll
-        for (int q = 0; q < kMine; ++q)
-            mine[q] = load_block16(static_cast<const f16*>(x) + (size_t)min((int)threadIdx.x + q * kMxThreads, T * st.nb - 1) * kMxBlock);
-    }
     const int nwg = (int)gridDim.x;
-    const auto row_of = [&](int tile) { return min(tile * kMxRows + (lane & 15), out - 1); };
-    const auto prepare = [&]() {
-        if constexpr (INLINE) {
-#pragma unroll
-            for (int q = 0; q < kMine; ++q) {
-                const int i = threadIdx.x + q * kMxThreads;
-                if (i >= T * st.nb) break;
-                uint32_t o[kSplitDwords], s;
-                split_block(mine[q], o, s);
-                store_split(xin.rows, i / st.nb, i % st.nb, o, s);
-            }
-            __syncthreads();
-        }
-    };
+    const MxStaged staged = {smem, lds_address(smem), MxStaged::row_steps(st.nb)};
+    if constexpr (STAGED) staged.send(xin.x, T, st.nb);
     const auto fin = [&](int t0, int n, auto sum) {
         for (int idx = threadIdx.x; idx < n * cols * kMxRows; idx += kMxThreads) {
             const int r = idx % kMxRows, ic = idx / kMxRows, i = ic / cols, col = ic - i * cols;
@@ -89,13 +56,17 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
             e.y[at] = (f16)v[0];
         }
     };
-    if constexpr (INLINE && WIDE && TILES <= 2) {
-        mx4_body_lds<NK, TILES>(codes, scales, xin.rows, xrow[0], st, (int)blockIdx.x, nwg, n_tiles, red, row_of, prepare, fin);
-    } else {
-        mx4_body<CT, NK, FMT, false, TILES, WIDE>(codes, scales, xin, xrow, st, (int)blockIdx.x, nwg, n_tiles, red, row_of, prepare,
-                                                  fin);
-    }
+    mx4_body<CT, NK, FMT, TILES, WIDE, kMxRows, false, STAGED>(codes, scales, xin, xrow, st, (int)blockIdx.x, nwg, n_tiles, red,
+                                                               MxTileRows{lane & 15, out}, fin, staged);
 }
+
+// Up to 16 rows of x to records: piece e of 8 values of block b of row r at (4 b + e) * 16 + r; rows past the last repeat it.
+__global__ __launch_bounds__(256) void mx4_records_kernel(const f16* __restrict__ x, u32x4* __restrict__ to, int T, int in) {
+    const int i = (int)blockIdx.x * 256 + (int)threadIdx.x;   // 16 consecutive pieces of a row are read by 16 lanes each
+    const int piece = i % 16 + i / 256 * 16, r = i / 16 % 16;
+    if (piece < in / 8) to[(size_t)piece * 16 + r] = load16(x + (size_t)min(r, T - 1) * in + piece * 8);
+}
+constexpr int kRecordRows = 16;
 
 struct RowsCall {
     const void *codes, *scales, *x, *xs;
@@ -103,80 +74,104 @@ struct RowsCall {
     int64_t out, in;
     int T;
     hipStream_t stream;
+    bool records;   // x is in records
 };
 
-template <int CT, int NK, int FMT, bool INLINE, bool WIDE = false, int TILES = mx4_tiles(CT)>
-hipError_t launch_rows_v(const RowsCall& c) {
-    auto kern = mx4_rows_kernel<CT, NK, FMT, INLINE, WIDE, TILES>;
-    const MxSteps st = mx4_steps(c.in, NK);
-    const size_t lds = mx4_red_floats(CT) * sizeof(float) +
-                       (INLINE ? (size_t)SplitRows::record_bytes(c.T) * st.nb : 0);
-    if (lds > 65536) {
+template <int CT, int NK, int FMT, bool WIDE, int TILES, bool STAGED>
+hipError_t launch_rows_v(const RowsCall& c, const MxSteps& st) {
+    auto kern = mx4_rows_kernel<CT, NK, FMT, WIDE, TILES, STAGED>;
+    MxInputRows<FMT> x;
+    if constexpr (FMT == kFmt4) x = {static_cast<const uint8_t*>(c.x), static_cast<const uint8_t*>(c.xs), st.nb};
+    else if (c.records) x = {static_cast<const f16*>(c.x), 8, kRecordRows * kMxBlock, kRecordRows * 8};
+    else x = mx4_rows16(static_cast<const f16*>(c.x), st.nb);
+    const size_t lds = STAGED ? (size_t)c.T * MxStaged::row_steps(st.nb) * 256 : 0;
+    if (lds > 0) {
         const hipError_t r = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (r != hipSuccess) return r;
     }
     const int tiles = (int)((c.out + kMxRows - 1) / kMxRows), groups = (c.T + CT * 16 - 1) / (CT * 16);
     hipLaunchKernelGGL(kern, dim3(std::min(tiles, device_cu_count()), groups), dim3(kMxThreads), lds, c.stream,
-                       static_cast<const uint8_t*>(c.codes), static_cast<const uint8_t*>(c.scales), c.x, c.xs, st,
-                       (int)c.out, c.T, c.e);
+                       static_cast<const uint8_t*>(c.codes), static_cast<const uint8_t*>(c.scales), x, st, (int)c.out, c.T, c.e);
     return hipGetLastError();
 }
 
-// x split in LDS: one or two tiles a workgroup by mx4_body_lds, more by mx4_body, which keeps x in registers (4096 -> 4096 at 1 token
-// 5.7 us against 6.4, 4096 -> 8192 6.4 against 7.3; four tiles and more: 4096 -> 28672 17.6 against 16.3).
-template <int NK>
-hipError_t launch_inline(const RowsCall& c) {
-    return (c.out + kMxRows - 1) / kMxRows <= device_cu_count() ? launch_rows_v<1, NK, kFmt6, true, true, 1>(c)
-                                                                : launch_rows_v<1, NK, kFmt6, true, true, 2>(c);
+// Steps a wave holds: four, where registers allow.
+template <int CT, int FMT, bool WIDE, int TILES, bool STAGED>
+hipError_t launch_rows_t(const RowsCall& c) {
+    constexpr int kNk = CT == 4 ? 1 : CT == 2 ? 2 : !WIDE ? 1 : FMT == kFmt16 && TILES > (STAGED ? 3 : 2) ? 2 : 4;
+    int nk;
+    const MxSteps st = mx4_steps(c.in, kNk, &nk);
+    if constexpr (kNk == 4) {
+        if (nk == 4) return launch_rows_v<CT, 4, FMT, WIDE, TILES, STAGED>(c, st);
+    }
+    if constexpr (kNk >= 3) {
+        if (nk == 3) return launch_rows_v<CT, 3, FMT, WIDE, TILES, STAGED>(c, st);
+    }
+    if constexpr (kNk >= 2) {
+        if (nk == 2) return launch_rows_v<CT, 2, FMT, WIDE, TILES, STAGED>(c, st);
+    }
+    return launch_rows_v<CT, 1, FMT, WIDE, TILES, STAGED>(c, st);
 }
 
-template <int FMT, bool INLINE>
+// No more tiles in a group than a workgroup has: fewer leave registers for more steps in flight (4096 -> 11008, 3 tiles a workgroup, 1 and
+// 16 tokens: groups of 3 tiles and 4 steps 8.3 and 10.6 us, of 4 and 2 8.9 and 11.4).
+template <int CT, int FMT, bool WIDE, bool STAGED = false>
+hipError_t launch_rows_ct(const RowsCall& c) {
+    const int tiles = (int)((c.out + kMxRows - 1) / kMxRows), cus = device_cu_count();
+    if (tiles <= cus) return launch_rows_t<CT, FMT, WIDE, 1, STAGED>(c);
+    if (tiles <= 2 * cus || mx4_tiles(CT) == 2) return launch_rows_t<CT, FMT, WIDE, 2, STAGED>(c);
+    if constexpr (STAGED) {
+        if (tiles <= 3 * cus) return launch_rows_t<CT, FMT, WIDE, 3, STAGED>(c);
+    }
+    return launch_rows_t<CT, FMT, WIDE, mx4_tiles(CT), STAGED>(c);
+}
+
+bool wide(int64_t in) { return in >= kMxWideBlocks * kMxBlock; }
+bool fits_lds(int64_t in, int64_t batch) { return batch * ((in + 127) / 128) <= MxStaged::kSteps; }
+bool in_records(int64_t in, int64_t batch) { return wide(in) && batch <= 16 && !fits_lds(in, batch); }
+
+template <int FMT>
 hipError_t launch_rows(const RowsCall& c) {
-    if constexpr (!INLINE) {
-        if (c.T > 32) return launch_rows_v<4, 1, FMT, INLINE>(c);
-        if (c.T > 16) return launch_rows_v<2, 2, FMT, INLINE>(c);
+    if (c.T > 32) return launch_rows_ct<4, FMT, false>(c);
+    if (c.T > 16) return launch_rows_ct<2, FMT, false>(c);
+    if (!wide(c.in)) return launch_rows_ct<1, FMT, false>(c);
+    if constexpr (FMT == kFmt16) {
+        // few short rows are read as they lie: no wait for LDS in front of few tiles (512 -> 8192, 1 token: 3.9 us, staged 4.9)
+        const bool few = c.T <= 4 && c.in <= 4096 && c.out <= (int64_t)2 * kMxRows * device_cu_count();
+        if (!c.records && !few) return launch_rows_ct<1, FMT, true, true>(c);
     }
-    if (c.in < kMxWideBlocks * kMxBlock) return launch_rows_v<1, 1, FMT, INLINE>(c);
-    if constexpr (INLINE) {
-        if ((c.out + kMxRows - 1) / kMxRows <= 2 * device_cu_count()) {
-            switch (mx4_steps(c.in, 4).nk) {
-                case 1: return launch_inline<1>(c);
-                case 2: return launch_inline<2>(c);
-                case 3: return launch_inline<3>(c);
-                default: return launch_inline<4>(c);
-            }
-        }
-    }
-    return launch_rows_v<1, 4, FMT, INLINE, true>(c);
+    return launch_rows_ct<1, FMT, true>(c);
 }
 
-bool split_inline(int64_t in, int64_t batch) { return batch <= 16 && batch * (in / kMxBlock) <= kInlineBlocks; }
+// Room for records: what any batch up to this one may need.
+int64_t records_bytes(bool x_mx4, int64_t in, int64_t batch) {
+    return !x_mx4 && wide(in) && !fits_lds(in, std::min<int64_t>(batch, 16)) ? kRecordRows * in * 2 : 0;
+}
 
 }  // namespace
 
 int64_t mx4_linear_workspace(bool x_mx4, int64_t out, int64_t in, int64_t batch) {
     if (out == 0 || batch == 0) return 0;
-    const int64_t split = x_mx4 || split_inline(in, batch) ? 0 : mx4_split_bytes(batch, in);
-    return split + (mx4_gemm_serves(x_mx4, out, in, batch) ? mx4_gemm_part_bytes(out, in, batch) : 0);
+    const int64_t parts = mx4_gemm_serves(x_mx4, out, in, batch) ? mx4_gemm_part_bytes(out, in, batch) : 0;
+    return std::max(parts, records_bytes(x_mx4, in, batch));
 }
 
 hipError_t launch_mx4_linear(const void* codes, const void* scales, MxInput x, const Epilogue& e, void* workspace,
                              int64_t out, int64_t in, int64_t batch, hipStream_t stream) {
-    const bool four = x.scales != nullptr, inlined = !four && split_inline(in, batch);
-    char* part = static_cast<char*>(workspace);
-    if (!four && !inlined) {
-        const hipError_t r = launch_mx4_split(x.x, workspace, in, batch, stream);
+    const bool four = x.scales != nullptr;
+    if (mx4_gemm_serves(four, out, in, batch)) return launch_mx4_gemm(codes, scales, x, e, workspace, out, in, batch, stream);
+    RowsCall c = {codes, scales, x.x, x.scales,
+                  MxEpilogue{static_cast<const f16*>(e.bias[0]), static_cast<const f16*>(e.residual),
+                             static_cast<f16*>(e.y), e.act},
+                  out, in, (int)batch, stream, !four && in_records(in, batch)};
+    if (c.records) {
+        hipLaunchKernelGGL(mx4_records_kernel, dim3((unsigned)((in / 8 + 15) / 16)), dim3(256), 0, stream, static_cast<const f16*>(x.x),
+                           static_cast<u32x4*>(workspace), (int)batch, (int)in);
+        const hipError_t r = hipGetLastError();
         if (r != hipSuccess) return r;
-        x.x = workspace;
-        part += mx4_split_bytes(batch, in);
+        c.x = workspace;
     }
-    if (mx4_gemm_serves(four, out, in, batch)) return launch_mx4_gemm(codes, scales, x, e, part, out, in, batch, stream);
-    const RowsCall c = {codes, scales, x.x, x.scales,
-                        MxEpilogue{static_cast<const f16*>(e.bias[0]), static_cast<const f16*>(e.residual),
-                                   static_cast<f16*>(e.y), e.act},
-                        out, in, (int)batch, stream};
-    if (four) return launch_rows<kFmt4, false>(c);
-    return inlined ? launch_rows<kFmt6, true>(c) : launch_rows<kFmt6, false>(c);
+    return four ? launch_rows<kFmt4>(c) : launch_rows<kFmt16>(c);
 }
 
 }  // namespace aqlm

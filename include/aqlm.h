@@ -480,11 +480,12 @@ int aqlm_gated_lists(const void* const* tables, const void* const* entries, cons
  * products above, of aqlm_mx4_linear_workspace_bytes bytes (x_mx4: whether x
  * is in MX4); a larger batch never needs fewer.
  *
- * Numerics: no weight is rounded.  fp16 activations enter as a sum of four
- * 6-bit floats a value, per block of 32: values down to 2^-8 of the block's
- * largest exactly, smaller ones off by at most 2^-19 of it.  Products are
+ * Numerics: neither weights nor activations are rounded.  Products are
  * accumulated in fp32; bias, activation and residual are applied in fp32 and y
- * is rounded to fp16 once.  A block of x with an infinity or NaN makes its
+ * is rounded to fp16 once.  Next to fp16 activations a weight block of scale 0
+ * counts as zero, and blocks of scales outside 104..140 (0.5 2^-23 to 6 2^13:
+ * quantized blocks whose largest value is below 2^-21, or foreign ones) cost
+ * up to ten times the time of others.  A block of x with an infinity or NaN makes its
  * token's outputs NaN, a weight block of scale 255 its row's; non-finite bias and
  * residual values reach the outputs that they take part in.  Results are
  * deterministic.
@@ -541,9 +542,8 @@ int aqlm_mx4_linear(const void* codes, const void* scales, const void* x, const 
  * Numerics: aqlm_moe multiplies every codeword on its own (no weight is
  * rounded), aqlm_moe_mx4 as aqlm_mx4_linear.  The hidden vector
  * act(.) * (.) is kept to 2^-22 of each element or 2^-28, whichever is larger
- * (infinite beyond 2^8 * 65504), for aqlm_moe_mx4 to 2^-19 of the largest in
- * its block of 32.  Sums are fp32, over a token's choices in their order; y is rounded to fp16
- * once.  Results are deterministic.
+ * (infinite beyond 2^8 * 65504).  Sums are fp32, over a token's choices in their
+ * order; y is rounded to fp16 once.  Results are deterministic.
  */
 #define AQLM_MOE_MAX_EXPERTS 512
 #define AQLM_MOE_MAX_K 16
