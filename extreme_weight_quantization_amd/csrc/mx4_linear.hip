@@ -34,6 +34,7 @@ __global__ __launch_bounds__(kMxThreads) void mx4_rows_kernel(const uint8_t* __r
                                                               MxSteps st, int out, int T, MxEpilogue e) {
     extern __shared__ u32x4 smem[];
     __shared__ float red[TILES * kMxWaves * CT * 256];
+    static_assert(sizeof(red) + (STAGED ? MxStaged::kSteps * 256 : 0) <= 163840, "the LDS of a CU");
     const int lane = threadIdx.x & (kWave - 1);
     const int col0 = (int)blockIdx.y * CT * 16, cols = min(T - col0, CT * 16);
     int xrow[CT];
@@ -114,14 +115,16 @@ hipError_t launch_rows_t(const RowsCall& c) {
 }
 
 // No more tiles in a group than a workgroup has: fewer leave registers for more steps in flight (4096 -> 11008, 3 tiles a workgroup, 1 and
-// 16 tokens: groups of 3 tiles and 4 steps 8.3 and 10.6 us, of 4 and 2 8.9 and 11.4).
+// 16 tokens: groups of 3 tiles and 4 steps 8.3 and 10.6 us, of 4 and 2 8.9 and 11.4; 8192 -> 22016, 6 tiles, 1 token: 22.3 and 25.2).  More
+// groups than of 4 tiles cost more than that (8192 -> 28672, 7 tiles, 1 token: 30.6 and 27.6).
 template <int CT, int FMT, bool WIDE, bool STAGED = false>
 hipError_t launch_rows_ct(const RowsCall& c) {
     const int tiles = (int)((c.out + kMxRows - 1) / kMxRows), cus = device_cu_count();
     if (tiles <= cus) return launch_rows_t<CT, FMT, WIDE, 1, STAGED>(c);
     if (tiles <= 2 * cus || mx4_tiles(CT) == 2) return launch_rows_t<CT, FMT, WIDE, 2, STAGED>(c);
     if constexpr (STAGED) {
-        if (tiles <= 3 * cus) return launch_rows_t<CT, FMT, WIDE, 3, STAGED>(c);
+        const int n = (tiles + cus - 1) / cus;   // of a workgroup
+        if ((n + 2) / 3 == (n + 3) / 4) return launch_rows_t<CT, FMT, WIDE, 3, STAGED>(c);
     }
     return launch_rows_t<CT, FMT, WIDE, mx4_tiles(CT), STAGED>(c);
 }
