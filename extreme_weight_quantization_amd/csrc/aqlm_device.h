@@ -76,10 +76,14 @@ __device__ __forceinline__ __attribute__((address_space(3))) void* lds_ptr(void*
 
 // 64 x 16 bytes from base + off (a lane's) to LDS address `to` (uniform) on.  Inline assembly, because the compiler
 // makes every later LDS read wait for a load into LDS that it knows of; the stage's barrier waits for all of them instead.  There
-// is no result to wait for, and the address register is read when the load is issued.  M0 has no other user in these kernels.
+// is no result to wait for, and the address register is read when the load is issued.  M0 is named as written: the compiler's own loads
+// into LDS set it too.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // that M0 is reserved
 __device__ __forceinline__ void load_to_lds(uint32_t to, const void* base, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)lds_ptr(const_cast<void*>(p)); }
 
