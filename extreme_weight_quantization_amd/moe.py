@@ -89,12 +89,13 @@ def _experts_mx4(name, codes, scales, dev):
 def _layers(make, gate, up, down, dev):
     """Scheme, experts, in, inner, and the host arrays of gate, up and down."""
     sch, E, inner, n_in, g = make("gate", *gate, dev)
-    if make("up", *up, dev)[:4] != (sch, E, inner, n_in):
+    *like_gate, u = make("up", *up, dev)
+    if like_gate != [sch, E, inner, n_in]:
         raise ValueError("gate and up must have the same scheme, experts, rows and in")
-    if make("down", *down, dev)[:4] != (sch, E, n_in, inner):
+    *turned, d = make("down", *down, dev)
+    if turned != [sch, E, n_in, inner]:
         raise ValueError("down must have gate's scheme and experts, and its rows and in exchanged")
-    parts = [g, make("up", *up, dev)[4], make("down", *down, dev)[4]]
-    return sch, E, n_in, inner, [_three(a) for a in zip(*parts)]
+    return sch, E, n_in, inner, [_three(a) for a in zip(g, u, d)]
 
 
 def _moe(name, make, need, gate, up, down, x, ids, weights, act, residual, y, workspace):
