@@ -517,7 +517,8 @@ int aqlm_mx4_linear(const void* codes, const void* scales, const void* x, const 
  * the scores without the bias, divided by their sum over the k when renorm is
  * not 0, times scale.  in % 8 == 0, k <= experts, 0 <= tokens <=
  * AQLM_ROUTE_MAX_TOKENS.  The choice is the one of logits and scores in 64
- * bits and does not depend on the batch.  So are the weights, except where
+ * bits (softmax scores without a bias: of the logits) and does not depend on
+ * the batch.  So are the weights, except where
  * tokens * experts * in >= 2^29 (and no softmax with a bias): there they come
  * from logits with sums of 64 products in fp32, added in 64 bits, off by at
  * most 2^-17 |x| |R_e| and usually by about 2^-22.  A NaN score ranks below all
