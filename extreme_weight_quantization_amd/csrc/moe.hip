@@ -3,8 +3,8 @@
 //
 // Bounds: the codes of the experts that are asked for, read once per 16 tokens (down: 8) of an expert; then the lookups, and for a
 // single token the fixed latencies of the launches.  2x8, 64 experts of 2048 x 1408, 1 token of 8: 24 us in a graph (gate and up 11.6,
-// down 9.0, combining 2); 1x16, 8 experts of 4096 x 11008, 16 tokens of 2: 583 us, 231 G gathers a second of the 264 that a kernel of
-// nothing else reaches.
+// down 9.0, combining 2); 1x16, 8 experts of 4096 x 11008, 16 tokens of 2: 560 to 620 us (by card), 217 to 241 G gathers a
+// second of the 264 that a kernel of nothing else reaches.
 //
 // The products are those of gemv_act.hip: workgroups of 16 waves that hold the expert's codebooks in LDS (2x8, 1x8 g4,
 // 4x8 g16) or gather codewords from L2 (1x16), on the columns that moe_plan.h finds.  An expert's workgroups are neighbours on
@@ -23,7 +23,7 @@ namespace {
 
 // Rows of up to 8 slabs of 256 inputs would leave half of a workgroup's 16 waves without work: there two teams of 8 waves take a
 // tile each, and a pass is one tile; else 16 waves a tile and two tiles a pass, as the plain launches.  In teams | not, us:
-//   2x8, 64 experts 2048x1408: 1 token 24 | 28, 16 tokens 65 | 79; 8 experts 4096x11008: 1 token 52 | 47
+//   2x8, 64 experts 2048x1408: 1 token 24 | 28, 16 tokens 79 | 119; 8 experts 4096x11008: 1 token 52 | 47
 constexpr int kTeam = 8;
 constexpr int rtp(int team) { return team == kGemvWaves ? 2 : 1; }
 

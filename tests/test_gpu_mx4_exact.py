@@ -127,6 +127,19 @@ def test_odd_blocks_in_captured_calls(t):
         scales.copy_(now)
 
 
+@pytest.mark.parametrize("n_in,out,t", [(4096, 16384, 16), (8192, 14000, 8), (65536, 100, 1), (32768, 300, 2), (4128, 14000, 16), (65568, 40, 1),
+                                        (5120, 12300, 12), (4096, 28000, 16), (8192, 9000, 16), (1024, 21000, 3)])
+def test_the_most_rows_that_lds_holds(n_in, out, t):
+    """Activations of 128 KB and a step more, for workgroups of one to eight tiles."""
+    codes, scales = weights(out, n_in, t)
+    x = activations(t, n_in, t + 1)
+    y = E.aqlm_mx4_linear(codes.cuda(), scales.cuda(), x.cuda())
+    rows = torch.unique(torch.cat([torch.arange(0, min(out, 100)), torch.arange(out // 2, min(out, out // 2 + 100)), torch.arange(max(0, out - 300), out)]))
+    z, ez = R.mx4_product(R.mx4_values(codes[rows], scales[rows]), x.double(), False)
+    want, tol = R.linear(z, ez, "none", None, None)
+    check(y.cpu()[:, rows], want, tol)
+
+
 # ------------------------------------------------------------------------------------------------ experts
 
 
