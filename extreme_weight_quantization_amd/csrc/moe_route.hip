@@ -13,7 +13,9 @@
 // route_fast_kernel multiplies on the fp16 instruction and adds its fp32 sums in 64 bits every 64 inputs.  A sum of 64 products
 // p in fp32 is off by at most 64 2^-23 sum |p|, so a logit by at most eb = 2^-17 |x| |r|.  The pick then knows which of its
 // comparisons eb could turn, and computes those logits again in 64 bits (one token in ten, two or three logits): the choice is
-// the same.  Weights come from the faster sums, off by some 2^-22.  Not for softmax scores with a bias, whose
+// the same.  Weights come from the faster sums: their error against 64 bits is within 4 % of that of an fp32 number's rounding
+// (2.9e-8 against 2.8e-8, relative, 2048 tokens), at most 2^-22.  All chosen logits in 64 bits too took 62 us instead of 47
+// (2048 tokens, k 8), 132 instead of 72 (3000, 512 experts of 2048 inputs, k 16), 148 instead of 111 (8192).  Not for softmax scores with a bias, whose
 // comparisons need every logit of a token.  Together 48 us: the product 20 (134 MB through LDS), the pick 26, of which the
 // last token's exact logits are 10.
 #include <algorithm>
